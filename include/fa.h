@@ -247,6 +247,165 @@ fa_status fa_step_host(const void* q, const void* k, const void* v,
                        int chunk_heads, void* stream);
 
 /*
+ * ---- Before and behind the attention: norms with rotation, a 4-bit cache
+ *
+ * Norms of query and key heads with the rotation of positions, in one pass
+ * from a projection's output to the attention's inputs.  With x a head's row
+ * of qkv, p the token's position, w the norm's weight and R(p) the rotation:
+ *   y = x * (mean(x^2) + eps)^(-1/2) * w,   out = R(p) y
+ * for query heads (q_weight) and key heads (k_weight); value heads are only
+ * moved.  Computed in fp32 and rounded once.
+ *   qkv       : in, bf16 [B, N, H + 2 Hkv, d]: the H query heads of a token,
+ *               then its Hkv key heads, then its Hkv value heads, contiguous;
+ *               stride_b, stride_n: elements from one batch entry and from
+ *               one token to the next (multiples of 8)
+ *   rope      : in, fp32 [rope_rows, rot]: for each position rot/2 cosines,
+ *               then rot/2 sines, the caller's; 16-byte aligned.  The first
+ *               rot dims of a head are rotated (rot a multiple of 16, at
+ *               most d), the others pass.  interleaved = 0 pairs dims
+ *               (i, i + rot/2), 1 pairs dims (2i, 2i + 1); pair i turns by
+ *               angle i: (u, v) -> (u cos - v sin, v cos + u sin).
+ *   positions : in, int32 [B, N], or NULL for 0 .. N-1 in each entry;
+ *               clamped to [0, rope_rows)
+ *   q_weight, k_weight : in, [d], bf16 (weight_bf16 = 1) or fp32 (0); both
+ *               NULL: no norm, only the rotation
+ *   q, k, v   : out, bf16 [B,H,N,d], [B,Hkv,N,d], [B,Hkv,N,d]
+ * eps >= 0.  An H of 0, or an Hkv of 0, is a call for the other heads alone.
+ */
+fa_status fa_qk_norm_rope(const void* qkv, long long stride_b,
+                          long long stride_n, const float* rope, int rope_rows,
+                          int rot, const int* positions, const void* q_weight,
+                          const void* k_weight, int weight_bf16, float eps,
+                          int interleaved, void* q, void* k, void* v, int B,
+                          int N, int H, int Hkv, int d, void* stream);
+
+/*
+ * Its backward: from dq, dk, dv (as fa_bwd, fa_bwd_ext, fa_bwd_varlen write
+ * them) and the forward's qkv to dqkv (bf16, laid out like qkv, with strides
+ * of its own) and, with weights, dq_weight and dk_weight (fp32 [d], summed
+ * over all tokens and heads in an order that does not change from call to
+ * call; zero without tokens).  dqkv may be qkv itself.  With weights it needs
+ * fa_qk_norm_rope_bwd_workspace_size(d) bytes of device workspace, 16-byte
+ * aligned, whose contents do not matter.
+ */
+size_t fa_qk_norm_rope_bwd_workspace_size(int d);
+fa_status fa_qk_norm_rope_bwd(const void* qkv, long long stride_b,
+                              long long stride_n, const float* rope,
+                              int rope_rows, int rot, const int* positions,
+                              const void* q_weight, const void* k_weight,
+                              int weight_bf16, float eps, int interleaved,
+                              const void* dq, const void* dk, const void* dv,
+                              void* dqkv, long long dstride_b,
+                              long long dstride_n, float* dq_weight,
+                              float* dk_weight, void* workspace,
+                              size_t workspace_bytes, int B, int N, int H,
+                              int Hkv, int d, void* stream);
+
+/*
+ * A paged key/value cache held in 4 bits.  `cache` is pages *
+ * fa_cache4_page_bytes(Hkv, page_size, d) bytes of device memory, 16-byte
+ * aligned, owned by the caller; page_size is 16, 32, 64, 128 or 256 tokens.
+ * A token's slot is page * page_size + its place in the page, and
+ * pages * page_size fits an int.
+ *
+ * Every 16 neighbouring dims of a token's key (or value) row of one head
+ * share a scale: with g the call's k_scale (or v_scale), a power of two
+ * within 2^-60 .. 2^60 that a user fixes once per cache,
+ *   scale = E4M3(amax / (6 g)), code = E2M1(x / (scale g)),
+ * both to nearest, ties to even, saturating (at 448 and 6); the value held
+ * is code * scale * g, which bf16 represents exactly.  A block with a NaN
+ * reads as NaN in all 16 dims; an infinity saturates.
+ *
+ * Layout: [pages][Hkv][page_size / 16] groups of 16 tokens, 18 d bytes each:
+ *   K codes  [16][d/2]           two dims a byte, the even one in the low half
+ *   K scales [16][d/16]
+ *   V codes  [2][8][4][2][d/16]  axes: token / 8, the dims in eighths,
+ *                                token % 8 / 2, token % 2, bytes
+ *   V scales [2][d/16][4][2]     token / 8, block, token % 8 / 2, token % 2
+ * fa_cache4_page_bytes returns 0 for sizes that are not supported.
+ */
+size_t fa_cache4_page_bytes(int Hkv, int page_size, int d);
+
+/*
+ * Block tables and slot maps of R requests, kept on the device and updated
+ * by one call per step:
+ *   new_tokens  : in, int32 [R].  n > 0: the request grows by n tokens;
+ *                 n < 0: its last -n tokens (at most all) are dropped, e.g.
+ *                 rejected drafts, or -INT_MAX for a request that ended;
+ *                 0: it stays as it is.
+ *   lens        : in/out, int32 [R]  tokens in the cache
+ *   block_table : in/out, int32 [R, max_blocks]  page ids in order; entries
+ *                 past a request's pages are left as they were
+ *   free_list   : in/out, int32 [pages]  stack of free page ids
+ *   free_count  : in/out, int32 [1]      entries in use of that stack
+ *   slots       : out, int32 [R, T]  slot of new token t of request r; -1 at
+ *                 t >= granted[r]
+ *   positions   : out, int32 [R, T]  its position in the request; 0 there
+ *   granted     : out, int32 [R]     tokens added: n, or 0
+ * Dropped tokens' pages return to the stack first, the last request's last
+ * page deepest; then requests take pages in order, each the ones it needs
+ * from the top.  A request grows only if the pages wanted up to and
+ * including it are there (or it needs none), if n <= T, and if it fits
+ * max_blocks pages; otherwise it is left as it was, granted 0.  Dropping what
+ * one call granted restores the stack.  Values out of range in lens and
+ * free_count are clamped.  The results feed fa_qk_norm_rope (positions),
+ * fa_cache4_append (slots) and fa_cache4_attn (lens, granted, block_table).
+ */
+fa_status fa_cache4_plan(const int* new_tokens, int* lens, int* block_table,
+                         int* free_list, int* free_count, int* slots,
+                         int* positions, int* granted, int R, int max_blocks,
+                         int pages, int page_size, int T, void* stream);
+
+/*
+ * Writes keys and values to their slots of the cache.
+ *   k, v         : in, bf16 [B,Hkv,N,d] (keys already rotated)
+ *   slots        : in, int32 [B,N]; tokens whose slot is outside
+ *                  [0, pages * page_size) are skipped: not read, not written
+ *   k_out, v_out : out, bf16 [B,Hkv,N,d], or both NULL: the values that the
+ *                  cache now holds for these tokens, so that a prompt's
+ *                  attention (fa_fwd_varlen) can use what later steps will
+ *                  read.  They may be k and v themselves.  Rows of skipped
+ *                  tokens are left as they were.
+ * A slot that occurs twice in a call holds an unspecified mix of the two.
+ */
+fa_status fa_cache4_append(const void* k, const void* v, void* cache,
+                           const int* slots, float k_scale, float v_scale,
+                           void* k_out, void* v_out, int B, int Hkv, int N,
+                           int d, int pages, int page_size, void* stream);
+
+/*
+ * Causal attention of each request's newest tokens over its cache.
+ *   q           : in,  bf16 [B,H,T,d]; heads share key/value heads as in
+ *                 fa_fwd_ext (head h reads h / (H / Hkv))
+ *   block_table : in,  int32 [B, max_blocks]
+ *   seq_lens    : in,  int32 [B]  tokens in the cache, the new ones included;
+ *                 clamped to [0, max_blocks * page_size]
+ *   q_lens      : in,  int32 [B], or NULL for T: new tokens of each request,
+ *                 clamped to [0, T].  Row t < q_lens[b] is at position
+ *                 i = seq_lens[b] - q_lens[b] + t and sees keys j <= i, with
+ *                 window >= 0 only those with j >= i - window.
+ *   o, lse      : out, bf16 [B,H,T,d], fp32 [B,H,T]; rows t >= q_lens[b] are
+ *                 left as they were.  A row that sees no key gets o = 0 and
+ *                 lse = -infinity.
+ *   workspace   : fa_cache4_attn_workspace_size(B, H, Hkv, T, d) bytes,
+ *                 256-byte aligned; contents do not matter.  Calls that
+ *                 share a workspace must not overlap in time.
+ * Table entries outside [0, pages) hide their tokens.  Cached values that no
+ * row of the request sees are never used, whatever they hold; a NaN that
+ * some row sees may reach every row of the request and key/value head.
+ * The result does not depend on the order in which blocks run.  The kernel's
+ * waits have the time limit of fa_set_wait_timeout_ns, where-code 0x511.
+ */
+size_t fa_cache4_attn_workspace_size(int B, int H, int Hkv, int T, int d);
+fa_status fa_cache4_attn(const void* q, const void* cache,
+                         const int* block_table, const int* seq_lens,
+                         const int* q_lens, void* o, float* lse,
+                         void* workspace, size_t workspace_bytes, int B, int H,
+                         int Hkv, int T, int d, int max_blocks, int pages,
+                         int page_size, int window, float scale, float k_scale,
+                         float v_scale, void* stream);
+
+/*
  * Synchronises `stream`, then reports (and clears) the device status record
  * of the current GPU: FA_ERR_DEVICE_TIMEOUT if any kernel of this library
  * gave up on a pipeline wait since the last check, FA_ERR_CUDA if the stream

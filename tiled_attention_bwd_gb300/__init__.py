@@ -4,7 +4,10 @@ The compute path is libfa.so (hand-written tcgen05/TMA kernels behind the C
 ABI of include/fa.h); this package only builds it, marshals arguments to it,
 and describes the synthetic workloads.
 """
-from .fa import (FAError, fa_bwd, fa_bwd_ext, fa_bwd_ext_workspace_size,
+from .fa import (FAError, fa_cache4_append, fa_cache4_attn,
+                 fa_cache4_attn_workspace_size, fa_cache4_page_bytes,
+                 fa_cache4_plan, fa_qk_norm_rope, fa_qk_norm_rope_bwd,
+                 fa_qk_norm_rope_bwd_workspace_size, fa_bwd, fa_bwd_ext, fa_bwd_ext_workspace_size,
                  fa_bwd_noalloc, fa_bwd_varlen, fa_fwd_varlen,
                  fa_bwd_noalloc_max_workspace, fa_bwd_set_phase_events,
                  fa_bwd_workspace_size, fa_check_device_status,
@@ -23,4 +26,8 @@ __all__ = ["FAError", "fa_fwd", "fa_bwd", "fa_fwd_ext", "fa_bwd_ext",
            "fa_bwd_noalloc_max_workspace", "fa_check_device_status",
            "fa_set_wait_timeout_ns", "fa_debug_expire_wait",
            "fa_debug_expire_at", "fa_last_failure_site",
+           "fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
+           "fa_qk_norm_rope_bwd_workspace_size", "fa_cache4_page_bytes",
+           "fa_cache4_plan", "fa_cache4_append", "fa_cache4_attn",
+           "fa_cache4_attn_workspace_size",
            "fa_bwd_set_phase_events", "fa_status_string", "load_library"]

@@ -299,6 +299,15 @@ Fp8Layout fp8_layout(int B, int H, int N, int /*d*/) {
 
 }  // namespace
 
+namespace fa {
+fa_status device_info(DeviceInfo* out) {
+  DeviceCtx* ctx = nullptr;
+  const fa_status s = device_ctx(&ctx);
+  if (s == FA_OK) *out = DeviceInfo{ctx->state, ctx->sm_count, kernel_timeout()};
+  return s;
+}
+}  // namespace fa
+
 extern "C" {
 
 const char* fa_status_string(fa_status s) {

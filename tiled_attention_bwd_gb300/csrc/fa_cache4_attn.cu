@@ -1,0 +1,607 @@
+// fa_cache4_attn.cu -- attention of new tokens over the paged 4-bit cache.
+//
+//   o_r = sum_j softmax_j(scale q_r . k_j) v_j,   k_j, v_j = code * scale * g
+//
+// with one pass over the keys: running maximum m and sum l per row, the
+// values' sums rescaled when m grows.
+//
+// Work.  The query rows of one key/value head (H / Hkv heads x T tokens) are
+// taken 8, 16 or 32 at a time; such a row block of one request and head is
+// an item, its keys are cut into units of 64, and all items' units together
+// are dealt to the blocks in equal consecutive shares, whatever the lengths.
+// A block's four warps take one 16-token group of a unit each, with sums of
+// their own, and join them when the item (or the share) ends; an item that
+// lies in several blocks' shares is joined by a second kernel.
+//
+// Feeding.  Each warp copies its own groups (18 d bytes, K and V together)
+// into a ring in shared memory by bulk copies, several ahead; nothing in the
+// main loop waits for another warp.
+//
+// Products.  The scores are computed as S^T = K Q^T and the output as
+// O^T = V^T P^T by mma m16n8k16 in f16 with fp32 sums: keys and dims fill
+// the 16-high side and the few query rows the 8-wide side, so that eight
+// rows (one decode token of a group of up to 8 heads) waste nothing.  A code
+// times its scale has at most six significant bits: K and V enter exactly.
+// Q enters exactly too (bf16's 8 bits fit f16's 11, each row scaled by a
+// power of two to f16's range); P is rounded to f16 (2^-12), after a factor
+// 2^8 which keeps weights down to 2^-32 of the row's largest from vanishing.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "fa_cache4.cuh"
+#include "fa_common.cuh"
+#include "fa_launch.h"
+
+namespace fa {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kUnit = kWarps * kGroup;  // tokens of a work unit
+constexpr float kNoMax = -1e30f;        // below every score's maximum
+constexpr float kUp = 8.0f;             // P carries 2^kUp
+constexpr float kSlack = 6.0f;          // growth of m that is left standing
+
+__device__ __forceinline__ void e2m1_to_f16(uint32_t w, uint32_t* r) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
+// Two E4M3 bytes (low 16 bits) as f16.
+__device__ __forceinline__ uint32_t e4m3_to_f16(uint32_t two) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
+      : "=r"(r) : "r"(two));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// What a request has, with the values from memory brought into range.
+struct Request {
+  int len, ql;  // cached tokens, new tokens
+  int lo;       // first token of its units (a multiple of 16)
+  int units;    // of one item
+};
+__device__ __forceinline__ Request request_of(const Cache4AttnArgs& a, int b) {
+  Request r;
+  const long long cap = (long long)a.M << a.shift;
+  const int l = __ldg(a.seq_lens + b);
+  r.len = l < 0 ? 0 : (l > cap ? (int)cap : l);
+  const int n = a.q_lens ? __ldg(a.q_lens + b) : a.T;
+  r.ql = n < 0 ? 0 : (n > a.T ? a.T : n);
+  const long long first = (long long)r.len - r.ql - a.window;  // the first row's window
+  r.lo = (a.window < 0 || first < 0) ? 0 : (int)(first & ~15ll);
+  const int n_keys = r.len - r.lo;
+  // A request without keys keeps one unit, which writes its empty rows.
+  r.units = r.ql == 0 ? 0 : (n_keys > 0 ? (n_keys + kUnit - 1) / kUnit : 1);
+  return r;
+}
+
+// A block's place in the list of units.
+struct Cursor {
+  int b;     // request
+  int item;  // key/value head * row_blocks + row block
+  int unit;  // within the item
+  Request r;
+};
+
+// The next item with units, or b = B.
+__device__ __forceinline__ void next_item(const Cache4AttnArgs& a, Cursor& c) {
+  c.unit = 0;
+  if (++c.item < a.Hkv * a.row_blocks) return;
+  c.item = 0;
+  do {
+    if (++c.b >= a.B) return;
+    c.r = request_of(a, c.b);
+  } while (c.r.units == 0);
+}
+
+template <int D, int NT>
+struct Shape {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kStages = 6;
+  static constexpr int kRing = kWarps * kStages * group_bytes(D);
+  static constexpr int kPitch = D + 4;  // floats of a row in the join buffer
+  static constexpr int kJoin = kWarps * 8 * kPitch * 4;
+  static constexpr int kSmem = kRing + kJoin;
+  static constexpr int kPartRow = D + 2;  // O, m, l of a partial row
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32) cache4_attn_kernel(Cache4AttnArgs a) {
+  using S = Shape<D, NT>;
+  constexpr int kSteps = D / 16;  // 16-dim steps of Q K^T; also 16-dim tiles of O^T
+  constexpr int kWords = D / 32;  // 32-bit words of K codes per lane and token
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[kWarps][S::kStages];
+  __shared__ uint32_t cta_abort;
+  __shared__ int sh_scan[kWarps], sh_first[4];
+  __shared__ float sh_ml[kWarps][8][2];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+  uint8_t* ring = smem + warp * S::kStages * group_bytes(D);
+  float* join = reinterpret_cast<float*>(smem + S::kRing);
+  const WaitCtl ctl = {a.st, &cta_abort, a.timeout_ns};
+  if (lane < S::kStages) mbar_init(&full[warp][lane], 1);
+  if (tid == 0) cta_abort = 0;
+  fence_mbar_init();
+
+  // ---- this block's share of the units
+  const int items = a.Hkv * a.row_blocks;
+  const int per = (a.B + kWarps * 32 - 1) / (kWarps * 32);
+  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) mine += request_of(a, b).units;
+  int upto = mine;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, upto, m);
+    if (lane >= m) upto += u;
+  }
+  if (lane == 31) sh_scan[warp] = upto;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) upto += sh_scan[w];
+    total += sh_scan[w];
+  }
+  const int before = upto - mine;
+  const long long W = (long long)total * items;
+  const long long u0 = W * blockIdx.x / gridDim.x, u1 = W * (blockIdx.x + 1) / gridDim.x;
+  if (blockIdx.x == 0) {  // for the joining kernel
+    int at = before;
+    for (int b = b0; b < b1; ++b) {
+      a.unit0[b] = at;
+      at += request_of(a, b).units;
+    }
+    if (tid == 0) a.unit0[a.B] = total;
+  }
+  if (u0 >= u1) return;
+  if (u0 >= (long long)before * items && u0 < (long long)upto * items) {
+    long long left = u0 - (long long)before * items;
+    int b = b0;
+    Request r = request_of(a, b);
+    while (left >= (long long)r.units * items) {
+      left -= (long long)r.units * items;
+      r = request_of(a, ++b);
+    }
+    sh_first[0] = b;
+    sh_first[1] = (int)(left / r.units);
+    sh_first[2] = (int)(left % r.units);
+  }
+  __syncthreads();
+  Cursor use;
+  use.b = sh_first[0];
+  use.item = sh_first[1];
+  use.unit = sh_first[2];
+  use.r = request_of(a, use.b);
+  const int mine_units = (int)(u1 - u0);
+
+  // ---- the warp's own ring
+  Cursor load = use;
+  int issued = 0;        // units of the share that the loads have passed
+  int put = 0, got = 0;  // groups copied, groups used
+  bool dead = false;
+  const int gpp_shift = a.shift - 4;
+  // Page ids of the next 32 units of the loads' item, one per lane.
+  int ids = -1, ids_unit = -1;
+  auto load_ids = [&]() {
+    const int tok = load.r.lo + (load.unit + lane) * kUnit + warp * kGroup;
+    ids = -1;
+    if (tok < load.r.len) ids = __ldg(a.block_table + (size_t)load.b * a.M + (tok >> a.shift));
+    ids_unit = load.unit;
+  };
+  // Walks the loads on until the ring is full.  A group outside the request
+  // or on a page outside the cache is not copied (see `take`).
+  auto feed = [&]() {
+    while (issued < mine_units && put - got < S::kStages) {
+      if (ids_unit < 0 || load.unit - ids_unit >= 32) load_ids();
+      const int tok = load.r.lo + load.unit * kUnit + warp * kGroup;
+      const int page = __shfl_sync(0xffffffffu, ids, load.unit - ids_unit);
+      if (tok < load.r.len && page >= 0 && page < a.pages) {
+        const int slot = put % S::kStages;
+        if (lane == 0) {
+          const size_t at = ((((size_t)page * a.Hkv + load.item / a.row_blocks) << gpp_shift) +
+                             ((tok >> 4) & ((1 << gpp_shift) - 1))) * group_bytes(D);
+          mbar_arrive_expect_tx(&full[warp][slot], group_bytes(D));
+          bulk_load(ring + slot * group_bytes(D), a.cache + at, group_bytes(D), &full[warp][slot]);
+        }
+        ++put;
+      }
+      ++issued;
+      if (++load.unit == load.r.units) {
+        next_item(a, load);
+        ids_unit = -1;
+      }
+    }
+  };
+  feed();
+
+  int left = mine_units;
+  bool first_segment = true;
+  while (left > 0) {
+    // ---- one segment: units [use.unit, end) of one item
+    const int end = min(use.r.units, use.unit + left);
+    const int seg = end - use.unit;
+    const bool whole = use.unit == 0 && end == use.r.units;
+    const int hk = use.item / a.row_blocks, row0 = (use.item - hk * a.row_blocks) * S::kRows;
+    const size_t q_row = ((size_t)use.b * a.Hkv + hk) * a.rows + row0;
+
+    // Q fragments: row 8 nt + g, dims t D/4 + 0 .. D/4 - 1, scaled to f16.
+    uint32_t qf[NT][D / 8];
+    float rs[NT][2];  // rows 8 nt + 2t, + 1: power of two and scale to exponents of 2
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool live = row0 + 8 * nt + g < a.rows;
+      const __nv_bfloat16* src = a.q + (q_row + 8 * nt + g) * D + t * (D / 4);
+      uint32_t big = 0;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (live) u = __ldg(reinterpret_cast<const uint4*>(src) + i);
+        qf[nt][4 * i] = u.x, qf[nt][4 * i + 1] = u.y, qf[nt][4 * i + 2] = u.z, qf[nt][4 * i + 3] = u.w;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) big = __vmaxu2(big, qf[nt][i] & 0x7fff7fffu);
+      big = max(big & 0xffffu, big >> 16);
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      // Exponent field of the row's largest; the row is scaled to [2^8, 2^9).
+      int e = big >> 7;
+      e = e < 16 ? 16 : (e > 250 ? 250 : e);
+      const float down = __uint_as_float((uint32_t)(262 - e) << 23);
+      const float back = __uint_as_float((uint32_t)(e - 8) << 23) * a.scale_log2;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        qf[nt][i] = f16x2(__uint_as_float(qf[nt][i] << 16) * down,
+                          __uint_as_float(qf[nt][i] & 0xffff0000u) * down);
+      rs[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);
+      rs[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+    }
+
+    // Keys that a row sees: [row_lo, row_hi).
+    int row_hi[NT][2], row_lo[NT][2];
+    const int pos0 = use.r.len - use.r.ql;  // position of the first new token
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int pos = pos0 + (row0 + 8 * nt + 2 * t + i) % a.T;
+        row_hi[nt][i] = min(pos + 1, use.r.len);
+        row_lo[nt][i] = a.window < 0 ? 0 : max(0, pos - a.window);
+      }
+    // Groups within [plain_lo, plain_hi) are seen whole by every row.
+    const int plain_hi = pos0 + 1, plain_lo = a.window < 0 ? 0 : use.r.len - 1 - a.window;
+
+    float o[kSteps][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+      m[nt][0] = m[nt][1] = kNoMax;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+
+    int page_ids = -1;
+    for (int un = use.unit; un < end; ++un) {
+      const int k_in = un - use.unit;
+      const int tok = use.r.lo + un * kUnit + warp * kGroup;
+      if ((k_in & 31) == 0) {
+        const int tk = tok + lane * kUnit;
+        page_ids = tk < use.r.len ? __ldg(a.block_table + (size_t)use.b * a.M + (tk >> a.shift)) : -1;
+      }
+      const int page = __shfl_sync(0xffffffffu, page_ids, k_in & 31);
+      if (!(tok < use.r.len && page >= 0 && page < a.pages)) continue;
+      const int slot = got % S::kStages;
+      if (!dead && !wait_bar_warp(&full[warp][slot], (got / S::kStages) & 1, ctl, 0x511)) dead = true;
+      if (dead) break;
+      const uint8_t* grp = ring + slot * group_bytes(D);
+
+      // ---- S^T = K Q^T: tokens g and g + 8 of the group, rows 2t and 2t + 1
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+      uint32_t kc[2][kWords], ks[2][D / 64];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t* kp = grp + k_code_at(D, g + 8 * h, t * (D / 8));
+        const uint8_t* sp = grp + k_scale_at(D, g + 8 * h, t * (D / 64));
+        if constexpr (D == 128) {
+          const uint4 u = *reinterpret_cast<const uint4*>(kp);
+          kc[h][0] = u.x, kc[h][1] = u.y, kc[h][2] = u.z, kc[h][3] = u.w;
+          const uint32_t two = e4m3_to_f16(*reinterpret_cast<const uint16_t*>(sp));
+          ks[h][0] = __byte_perm(two, 0, 0x1010);
+          ks[h][1] = __byte_perm(two, 0, 0x3232);
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(kp);
+          kc[h][0] = u.x, kc[h][1] = u.y;
+          ks[h][0] = __byte_perm(e4m3_to_f16(*sp), 0, 0x1010);
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) {
+        uint32_t x[4], y[4];
+        e2m1_to_f16(kc[0][w], x);
+        e2m1_to_f16(kc[1][w], y);
+        const uint32_t s0 = ks[0][w / 2], s1 = ks[1][w / 2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], s0), y[i] = mul2(y[i], s1);
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const uint32_t f[4] = {x[2 * hh], y[2 * hh], x[2 * hh + 1], y[2 * hh + 1]};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma(s[nt], f, qf[nt][4 * w + 2 * hh], qf[nt][4 * w + 2 * hh + 1]);
+        }
+      }
+
+      // ---- softmax weights
+      const bool plain = tok >= plain_lo && tok + kGroup <= plain_hi;
+      bool grow = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[nt][i] *= rs[nt][i & 1];
+          if (!plain) {
+            const int j = tok + g + 8 * (i >> 1);
+            if (j >= row_hi[nt][i & 1] || j < row_lo[nt][i & 1]) s[nt][i] = -INFINITY;
+          }
+          grow |= s[nt][i] > m[nt][i & 1] + kSlack;
+        }
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float mx = fmaxf(s[nt][i], s[nt][i + 2]);
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+            mx = fmaxf(mx, m[nt][i]);
+            const float f = ex2(m[nt][i] - mx);
+            m[nt][i] = mx;
+            l[nt][i] *= f;
+#pragma unroll
+            for (int dt = 0; dt < kSteps; ++dt) o[dt][nt][i] *= f, o[dt][nt][i + 2] *= f;
+          }
+      }
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = ex2(s[nt][i] - (m[nt][i & 1] - kUp));
+        l[nt][0] += p[0] + p[2];
+        l[nt][1] += p[1] + p[3];
+        pb[nt][0] = transpose8x8(f16x2(p[0], p[1]));
+        pb[nt][1] = transpose8x8(f16x2(p[2], p[3]));
+      }
+
+      // ---- O^T += V^T P^T
+      uint32_t vs[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t two = *reinterpret_cast<const uint16_t*>(
+            grp + v_scale_at(D, 8 * h + 2 * t, D == 128 ? g : g >> 1));
+        if (!plain) {
+          // Tokens that no row sees may hold anything, NaN scales included.
+          const int j = tok + 8 * h + 2 * t, lo = a.window < 0 ? 0 : pos0 - a.window;
+          if (j < lo || j >= use.r.len) two &= 0xff00u;
+          if (j + 1 < lo || j + 1 >= use.r.len) two &= 0x00ffu;
+        }
+        vs[h] = e4m3_to_f16(two);
+      }
+      constexpr int kVWords = D / 64;  // words of one token's eighth
+      uint32_t vc[2][2][kVWords];      // [half][token parity][word]
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t* vp = grp + v_code_at(D, 8 * h + 2 * t, g);
+        if constexpr (D == 128) {
+          const uint4 u = *reinterpret_cast<const uint4*>(vp);
+          vc[h][0][0] = u.x, vc[h][0][1] = u.y, vc[h][1][0] = u.z, vc[h][1][1] = u.w;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(vp);
+          vc[h][0][0] = u.x, vc[h][1][0] = u.y;
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < kVWords; ++w) {
+        // Bytes of the two tokens' codes of one dim: even dims, odd dims.
+        uint32_t ev[2][4], od[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t x = vc[h][0][w], y = vc[h][1][w];
+          e2m1_to_f16((x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u), ev[h]);
+          e2m1_to_f16(((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), od[h]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ev[h][i] = mul2(ev[h][i], vs[h]), od[h][i] = mul2(od[h][i], vs[h]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t f[4] = {ev[0][i], od[0][i], ev[1][i], od[1][i]};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma(o[4 * w + i][nt], f, pb[nt][0], pb[nt][1]);
+        }
+      }
+      __syncwarp();  // every lane has read the slot
+      ++got;
+      feed();
+    }
+    if (dead) issued = mine_units;  // no more loads; the joins below still run
+
+    // ---- join the warps, eight rows at a time
+    const int slot = 2 * blockIdx.x + (first_segment ? 0 : 1);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], x);
+      }
+      __syncthreads();  // the buffer's last readers are done
+      if (g == 0) {
+        sh_ml[warp][2 * t][0] = m[nt][0], sh_ml[warp][2 * t][1] = l[nt][0];
+        sh_ml[warp][2 * t + 1][0] = m[nt][1], sh_ml[warp][2 * t + 1][1] = l[nt][1];
+      }
+      // Lane (g, t) holds dims g D/8 + 0 .. D/8 - 1 of rows 2t and 2t + 1.
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float* dst = join + (warp * 8 + 2 * t + i) * S::kPitch + g * (D / 8);
+#pragma unroll
+        for (int dt = 0; dt < kSteps; dt += 2)
+          *reinterpret_cast<float4*>(dst + 2 * dt) =
+              make_float4(o[dt][nt][i], o[dt][nt][i + 2], o[dt + 1][nt][i], o[dt + 1][nt][i + 2]);
+      }
+      __syncthreads();
+      const int row = tid >> 4, c = tid & 15;  // 16 threads a row
+      float mx = kNoMax, f[kWarps], sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sh_ml[w][row][0]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        f[w] = ex2(sh_ml[w][row][0] - mx);
+        sum += f[w] * sh_ml[w][row][1];
+      }
+      const int r = row0 + 8 * nt + row;
+      const bool live = r < a.rows && r % a.T < use.r.ql;
+      const float inv = sum > 0.f || sum != sum ? a.v_scale / sum : 0.f;
+      float* part = a.part + ((size_t)slot * S::kRows + 8 * nt + row) * S::kPartRow;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float4 v =
+              *reinterpret_cast<const float4*>(join + (w * 8 + row) * S::kPitch + 64 * i + 4 * c);
+          acc[0] += f[w] * v.x, acc[1] += f[w] * v.y, acc[2] += f[w] * v.z, acc[3] += f[w] * v.w;
+        }
+        if (!whole) {
+          *reinterpret_cast<float2*>(part + 64 * i + 4 * c) = make_float2(acc[0], acc[1]);
+          *reinterpret_cast<float2*>(part + 64 * i + 4 * c + 2) = make_float2(acc[2], acc[3]);
+        } else if (live) {
+          __nv_bfloat162 lo = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
+          __nv_bfloat162 hi = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
+          *reinterpret_cast<uint2*>(a.o + (q_row + 8 * nt + row) * D + 64 * i + 4 * c) =
+              make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+        }
+      }
+      if (c == 0) {
+        if (!whole) {
+          *reinterpret_cast<float2*>(part + D) = make_float2(mx, sum);
+        } else if (live) {
+          a.lse[q_row + 8 * nt + row] = sum == 0.f ? -INFINITY : (mx - kUp + log2f(sum)) * kLn2;
+        }
+      }
+    }
+    left -= seg;
+    use.unit = end;
+    if (use.unit == use.r.units && left > 0) next_item(a, use);
+    first_segment = false;
+  }
+  // A stopping block lets its copies land before it leaves.
+  if (dead)
+    for (; got < put; ++got)
+      drain_bar(&full[warp][got % S::kStages], (got / S::kStages) & 1, a.timeout_ns);
+}
+
+// Joins the partial results of an item that lies in several blocks' shares,
+// in block order.  One block per row of an item, one thread per dim.
+template <int D, int NT>
+__global__ void __launch_bounds__(D) cache4_join_kernel(Cache4AttnArgs a, int blocks) {
+  using S = Shape<D, NT>;
+  const int items = a.Hkv * a.row_blocks;
+  const int row_in = blockIdx.y;
+  const long long total = (long long)a.unit0[a.B] * items;
+  for (long long it = blockIdx.x; it < (long long)a.B * items; it += gridDim.x) {
+    const int b = (int)(it / items), item = (int)(it - (long long)b * items);
+    const int hk = item / a.row_blocks, r = (item - hk * a.row_blocks) * S::kRows + row_in;
+    const int first = a.unit0[b], units = a.unit0[b + 1] - first;
+    if (units == 0 || r >= a.rows) continue;
+    const long long i0 = (long long)first * items + (long long)item * units, i1 = i0 + units;
+    // The block of unit u is the c with c W / C <= u < (c + 1) W / C.
+    const int c0 = (int)(((i0 + 1) * blocks - 1) / total), c1 = (int)((i1 * blocks - 1) / total);
+    if (c0 == c1) continue;
+    const int n = a.q_lens ? a.q_lens[b] : a.T;
+    if (r % a.T >= (n > a.T ? a.T : n)) continue;
+    // In its first block the item is the second segment unless it starts there.
+    const int slot0 = 2 * c0 + (total * c0 / blocks < i0 ? 1 : 0);
+    auto row_of = [&](int c) {
+      return a.part + ((size_t)(c == c0 ? slot0 : 2 * c) * S::kRows + row_in) * S::kPartRow;
+    };
+    float mx = kNoMax;
+    for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, row_of(c)[D]);
+    float acc = 0.f, sum = 0.f;
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+      const float* p = row_of(c);
+      const float f = ex2(p[D] - mx);
+      sum += f * p[D + 1];
+      acc += f * p[threadIdx.x];
+    }
+    const size_t q_row = ((size_t)b * a.Hkv + hk) * a.rows + r;
+    const float inv = sum > 0.f || sum != sum ? a.v_scale / sum : 0.f;
+    a.o[q_row * D + threadIdx.x] = __float2bfloat16_rn(acc * inv);
+    if (threadIdx.x == 0)
+      a.lse[q_row] = sum == 0.f ? -INFINITY : (mx - kUp + log2f(sum)) * kLn2;
+  }
+}
+
+template <int D, int NT>
+cudaError_t run(const Cache4AttnArgs& a, int sm_count, cudaStream_t stream) {
+  using S = Shape<D, NT>;
+  auto* kernel = cache4_attn_kernel<D, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e != cudaSuccess) return e;
+  int per_sm = NT == 1 ? 3 : 2;
+  int blocks = sm_count * per_sm;
+  if (blocks > kC4MaxBlocks) blocks = kC4MaxBlocks;
+  kernel<<<blocks, kWarps * 32, S::kSmem, stream>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const long long items = (long long)a.B * a.Hkv * a.row_blocks;
+  const dim3 grid((unsigned)(items < 65536 ? items : 65536), S::kRows);
+  cache4_join_kernel<D, NT><<<grid, D, 0, stream>>>(a, blocks);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int cache4_attn_rows(int rows) { return rows <= 8 ? 8 : 16; }
+
+cudaError_t launch_cache4_attn(const Cache4AttnArgs& a, int d, int sm_count, cudaStream_t stream) {
+  const int rows = cache4_attn_rows(a.rows);
+  if (d == 128) return rows == 8 ? run<128, 1>(a, sm_count, stream) : run<128, 2>(a, sm_count, stream);
+  return rows == 8 ? run<64, 1>(a, sm_count, stream) : run<64, 2>(a, sm_count, stream);
+}
+
+}  // namespace fa

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "fa.h"
+
 namespace fa {
 
 struct DevState;
@@ -77,6 +79,97 @@ struct BwdArgs {
   DevState* st;
   uint64_t timeout_ns;
 };
+
+// Norm of query and key heads with the rotation of positions, and backward.
+constexpr int kRopeMaxBlocks = 1024;  // of the backward: rows of `partial`
+struct RopeArgs {
+  const __nv_bfloat16* qkv;  // [B, N, H + 2 Hkv, d], strides below
+  const float* table;        // [table_rows, rot]: rot/2 cosines, rot/2 sines
+  const int* positions;      // [B, N] or null (row n of an entry: n)
+  const void* q_weight;      // [d], bf16 or fp32
+  const void* k_weight;
+  int weight_bf16;
+  __nv_bfloat16 *q, *k, *v;        // forward: out, [B, H or Hkv, N, d]
+  const __nv_bfloat16 *dq, *dk, *dv;  // backward: in
+  __nv_bfloat16* dqkv;             // backward: out
+  float *dq_weight, *dk_weight;    // [d]
+  float* partial;                  // [kRopeMaxBlocks, d] (backward, with norm)
+  long long stride_b, stride_n;    // of qkv, in elements
+  long long dstride_b, dstride_n;  // of dqkv
+  int N, H, Hkv, rot, table_rows;
+  int tokens;                      // B * N
+  float eps;
+  // Set by the launcher: packs of heads per token and how blocks take them.
+  int packs, tokens_per_block, packs_per_block;
+  int split[2];
+};
+cudaError_t launch_rope_fwd(const RopeArgs& a, int d, bool interleaved,
+                            bool norm, int sm_count, cudaStream_t stream);
+cudaError_t launch_rope_bwd(const RopeArgs& a, int d, bool interleaved,
+                            bool norm, int sm_count, cudaStream_t stream);
+
+// Block tables and slot maps of the paged cache.
+struct PlanArgs {
+  const int* new_tokens;  // [R]
+  int* lens;              // [R]
+  int* block_table;       // [R, M]
+  int* free_list;         // [P]
+  int* free_count;        // [1]
+  int* slots;             // [R, T]
+  int* positions;         // [R, T]
+  int* granted;           // [R]
+  int R, M, P, T;
+  int shift;              // log2 of the page size
+  int fused;              // set by the launcher: plan_kernel writes the slots
+};
+cudaError_t launch_cache4_plan(PlanArgs a, cudaStream_t stream);
+
+// New keys and values into their slots of the 4-bit cache.
+struct AppendArgs {
+  const __nv_bfloat16 *k, *v;    // [B, Hkv, N, d]
+  __nv_bfloat16 *k_out, *v_out;  // rounded values, or null
+  uint8_t* cache;
+  const int* slots;              // [B, N]
+  int rows;                      // B * Hkv * N
+  int N, Hkv, pages, shift;
+  float k_scale, v_scale;
+};
+cudaError_t launch_cache4_append(const AppendArgs& a, int d, cudaStream_t stream);
+
+// Attention over the 4-bit cache.
+constexpr int kC4MaxBlocks = 640;
+struct Cache4AttnArgs {
+  const __nv_bfloat16* q;   // [B, H, T, d]
+  const uint8_t* cache;
+  const int* block_table;   // [B, M]
+  const int* seq_lens;      // [B]
+  const int* q_lens;        // [B] or null
+  __nv_bfloat16* o;         // [B, H, T, d]
+  float* lse;               // [B, H, T]
+  float* part;              // partial results (workspace)
+  int* unit0;               // [B + 1] first work unit of each request (workspace)
+  int B, Hkv, T, M, pages;
+  int rows;                 // H / Hkv * T: rows of one key/value head
+  int row_blocks;
+  int shift;                // log2 of the page size
+  int window;               // < 0: none
+  float scale_log2;         // scale * k_scale * log2(e)
+  float v_scale;
+  DevState* st;
+  uint64_t timeout_ns;
+};
+// Rows of one work item: 8, 16 or 32.
+int cache4_attn_rows(int rows);
+cudaError_t launch_cache4_attn(const Cache4AttnArgs& a, int d, int sm_count,
+                               cudaStream_t stream);
+
+// Status record, SM count and wait limit of the current device.
+struct DeviceInfo {
+  DevState* st;
+  int sm_count;
+  uint64_t timeout_ns;
+};
+fa_status device_info(DeviceInfo* out);
 
 // Each returns the launch error (cudaSuccess on success).  `to` maps O
 // ([BH, N, d] bf16, boxes of 32 rows x 64 columns, 128-byte swizzle) for the

@@ -1,0 +1,307 @@
+// fa_serve_api.cu -- host side of the entry points around the attention
+// kernels: norm and rotation of queries and keys, and the paged 4-bit cache.
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "fa.h"
+#include "fa_cache4.cuh"
+#include "fa_launch.h"
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) {
+  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+fa_status head_dim(int d) {
+  if (d <= 0) return FA_ERR_INVALID_ARG;
+  return d == 64 || d == 128 ? FA_OK : FA_ERR_UNSUPPORTED;
+}
+fa_status launched(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
+
+// ------------------------------------------------------ norm and rotation
+fa_status check_rope(int B, int N, int H, int Hkv, int d, int rot, int table_rows, int weight_bf16,
+                     float eps, int interleaved, const void* qw, const void* kw,
+                     const void* table, const void* qkv, const int* positions,
+                     long long stride_b, long long stride_n) {
+  if (B < 0 || N < 0 || H < 0 || Hkv < 0) return FA_ERR_INVALID_ARG;
+  fa_status s = head_dim(d);
+  if (s != FA_OK) return s;
+  if (rot <= 0 || rot > d || rot % 16 != 0 || table_rows <= 0) return FA_ERR_INVALID_ARG;
+  if (weight_bf16 != 0 && weight_bf16 != 1) return FA_ERR_INVALID_ARG;
+  if (interleaved != 0 && interleaved != 1) return FA_ERR_INVALID_ARG;
+  if ((qw == nullptr) != (kw == nullptr)) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(eps) || !(eps >= 0.0f)) return FA_ERR_INVALID_ARG;
+  if (H > 65536 || Hkv > 65536) return FA_ERR_UNSUPPORTED;
+  // Rows of one head and packs of heads are counted in 31 bits.
+  if ((long long)B * N > INT_MAX || (long long)B * N * (H + 2LL * Hkv) > INT_MAX)
+    return FA_ERR_UNSUPPORTED;
+  if (B == 0 || N == 0 || H + Hkv == 0) return FA_OK;
+  if (!qkv || !table || !aligned(qkv, 16) || !aligned(table, 16) || !aligned(positions, 4))
+    return FA_ERR_INVALID_ARG;
+  // Weights are read one by one, in their own type.
+  if (!aligned(qw, weight_bf16 ? 2 : 4) || !aligned(kw, weight_bf16 ? 2 : 4))
+    return FA_ERR_INVALID_ARG;
+  if (stride_b % 8 != 0 || stride_n % 8 != 0) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+fa::RopeArgs rope_args(const void* qkv, long long sb, long long sn, const float* table,
+                       int table_rows, int rot, const int* positions, const void* qw,
+                       const void* kw, int weight_bf16, float eps, int B, int N, int H, int Hkv) {
+  fa::RopeArgs a = {};
+  a.qkv = static_cast<const __nv_bfloat16*>(qkv);
+  a.table = table;
+  a.positions = positions;
+  a.q_weight = qw;
+  a.k_weight = kw;
+  a.weight_bf16 = weight_bf16;
+  a.stride_b = sb;
+  a.stride_n = sn;
+  a.N = N;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.rot = rot;
+  a.table_rows = table_rows;
+  a.tokens = B * N;
+  a.eps = eps;
+  return a;
+}
+
+// ------------------------------------------------------------------ cache
+// log2 of a page size, or -1.
+int page_shift(int page) {
+  for (int s = 4; s <= 8; ++s)
+    if (page == 1 << s) return s;
+  return -1;
+}
+// A finite power of two within 2^-60 .. 2^60.
+bool cache_scale(float g) {
+  int e = 0;
+  return std::isfinite(g) && g > 0.0f && std::frexp(g, &e) == 0.5f && e > -60 && e <= 61;
+}
+fa_status check_cache(int pages, int Hkv, int page, int d, int* shift) {
+  fa_status s = head_dim(d);
+  if (s != FA_OK) return s;
+  if (pages < 0 || Hkv < 0 || page <= 0) return FA_ERR_INVALID_ARG;
+  if ((*shift = page_shift(page)) < 0) return FA_ERR_UNSUPPORTED;
+  if (((long long)pages << *shift) > INT_MAX) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_qk_norm_rope(const void* qkv, long long stride_b, long long stride_n,
+                          const float* rope, int rope_rows, int rot, const int* positions,
+                          const void* q_weight, const void* k_weight, int weight_bf16, float eps,
+                          int interleaved, void* q, void* k, void* v, int B, int N, int H, int Hkv,
+                          int d, void* stream) {
+  fa_status s = check_rope(B, N, H, Hkv, d, rot, rope_rows, weight_bf16, eps, interleaved, q_weight,
+                           k_weight, rope, qkv, positions, stride_b, stride_n);
+  if (s != FA_OK) return s;
+  if (B == 0 || N == 0 || H + Hkv == 0) return FA_OK;
+  if ((H > 0 && !q) || (Hkv > 0 && (!k || !v)) || !aligned(q, 16) || !aligned(k, 16) ||
+      !aligned(v, 16))
+    return FA_ERR_INVALID_ARG;
+  fa::DeviceInfo dev;
+  if ((s = fa::device_info(&dev)) != FA_OK) return s;
+  fa::RopeArgs a = rope_args(qkv, stride_b, stride_n, rope, rope_rows, rot, positions, q_weight,
+                             k_weight, weight_bf16, eps, B, N, H, Hkv);
+  a.q = static_cast<__nv_bfloat16*>(q);
+  a.k = static_cast<__nv_bfloat16*>(k);
+  a.v = static_cast<__nv_bfloat16*>(v);
+  return launched(fa::launch_rope_fwd(a, d, interleaved != 0, q_weight != nullptr, dev.sm_count,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_qk_norm_rope_bwd_workspace_size(int d) {
+  return d == 64 || d == 128 ? (size_t)fa::kRopeMaxBlocks * d * sizeof(float) : 0;
+}
+
+fa_status fa_qk_norm_rope_bwd(const void* qkv, long long stride_b, long long stride_n,
+                              const float* rope, int rope_rows, int rot, const int* positions,
+                              const void* q_weight, const void* k_weight, int weight_bf16,
+                              float eps, int interleaved, const void* dq, const void* dk,
+                              const void* dv, void* dqkv, long long dstride_b, long long dstride_n,
+                              float* dq_weight, float* dk_weight, void* workspace,
+                              size_t workspace_bytes, int B, int N, int H, int Hkv, int d,
+                              void* stream) {
+  fa_status s = check_rope(B, N, H, Hkv, d, rot, rope_rows, weight_bf16, eps, interleaved, q_weight,
+                           k_weight, rope, qkv, positions, stride_b, stride_n);
+  if (s != FA_OK) return s;
+  const bool norm = q_weight != nullptr;
+  const bool empty = B == 0 || N == 0 || H + Hkv == 0;
+  if (norm) {
+    if (!dq_weight || !dk_weight || !aligned(dq_weight, 4) || !aligned(dk_weight, 4))
+      return FA_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 16) ||
+        workspace_bytes < fa_qk_norm_rope_bwd_workspace_size(d))
+      return FA_ERR_WORKSPACE;
+  }
+  if (!empty) {
+    if ((H > 0 && !dq) || (Hkv > 0 && (!dk || !dv)) || !dqkv || !aligned(dq, 16) ||
+        !aligned(dk, 16) || !aligned(dv, 16) || !aligned(dqkv, 16))
+      return FA_ERR_INVALID_ARG;
+    if (dstride_b % 8 != 0 || dstride_n % 8 != 0) return FA_ERR_INVALID_ARG;
+  } else if (!norm) {
+    return FA_OK;
+  }
+  fa::DeviceInfo dev;
+  if ((s = fa::device_info(&dev)) != FA_OK) return s;
+  // Without tokens the weights' gradients are zero: the kernels write that.
+  fa::RopeArgs a = rope_args(qkv, stride_b, stride_n, rope, rope_rows, rot, positions, q_weight,
+                             k_weight, weight_bf16, eps, B, N, H, Hkv);
+  a.dq = static_cast<const __nv_bfloat16*>(dq);
+  a.dk = static_cast<const __nv_bfloat16*>(dk);
+  a.dv = static_cast<const __nv_bfloat16*>(dv);
+  a.dqkv = static_cast<__nv_bfloat16*>(dqkv);
+  a.dstride_b = dstride_b;
+  a.dstride_n = dstride_n;
+  a.dq_weight = dq_weight;
+  a.dk_weight = dk_weight;
+  a.partial = static_cast<float*>(workspace);
+  return launched(fa::launch_rope_bwd(a, d, interleaved != 0, norm, dev.sm_count,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_cache4_page_bytes(int Hkv, int page_size, int d) {
+  int shift = 0;
+  if (Hkv <= 0 || check_cache(0, Hkv, page_size, d, &shift) != FA_OK) return 0;
+  return (size_t)Hkv * (page_size / fa::kGroup) * fa::group_bytes(d);
+}
+
+fa_status fa_cache4_plan(const int* new_tokens, int* lens, int* block_table, int* free_list,
+                         int* free_count, int* slots, int* positions, int* granted, int R,
+                         int max_blocks, int pages, int page_size, int T, void* stream) {
+  if (R < 0 || max_blocks < 0 || pages < 0 || T < 0 || page_size <= 0) return FA_ERR_INVALID_ARG;
+  const int shift = page_shift(page_size);
+  if (shift < 0) return FA_ERR_UNSUPPORTED;
+  if (((long long)pages << shift) > INT_MAX || ((long long)max_blocks << shift) > INT_MAX ||
+      (long long)R * max_blocks > INT_MAX || (long long)R * T > INT_MAX)
+    return FA_ERR_UNSUPPORTED;
+  if (R == 0) return FA_OK;
+  if (!new_tokens || !lens || !free_count || !granted || (max_blocks > 0 && !block_table) ||
+      (pages > 0 && !free_list) || (T > 0 && (!slots || !positions)))
+    return FA_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)new_tokens, (const void*)lens, (const void*)block_table,
+                        (const void*)free_list, (const void*)free_count, (const void*)slots,
+                        (const void*)positions, (const void*)granted})
+    if (!aligned(p, 4)) return FA_ERR_INVALID_ARG;
+  fa::PlanArgs a = {};
+  a.new_tokens = new_tokens;
+  a.lens = lens;
+  a.block_table = block_table;
+  a.free_list = free_list;
+  a.free_count = free_count;
+  a.slots = slots;
+  a.positions = positions;
+  a.granted = granted;
+  a.R = R;
+  a.M = max_blocks;
+  a.P = pages;
+  a.T = T;
+  a.shift = shift;
+  return launched(fa::launch_cache4_plan(a, static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_cache4_append(const void* k, const void* v, void* cache, const int* slots,
+                           float k_scale, float v_scale, void* k_out, void* v_out, int B, int Hkv,
+                           int N, int d, int pages, int page_size, void* stream) {
+  int shift = 0;
+  fa_status s = check_cache(pages, Hkv, page_size, d, &shift);
+  if (s != FA_OK) return s;
+  if (B < 0 || N < 0) return FA_ERR_INVALID_ARG;
+  if (!cache_scale(k_scale) || !cache_scale(v_scale)) return FA_ERR_INVALID_ARG;
+  if ((k_out == nullptr) != (v_out == nullptr)) return FA_ERR_INVALID_ARG;
+  if ((long long)B * Hkv > INT_MAX || (long long)B * Hkv * N > INT_MAX) return FA_ERR_UNSUPPORTED;
+  if (B == 0 || Hkv == 0 || N == 0 || pages == 0) return FA_OK;
+  if (!k || !v || !cache || !slots) return FA_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cache, 16) || !aligned(slots, 4) ||
+      !aligned(k_out, 16) || !aligned(v_out, 16))
+    return FA_ERR_INVALID_ARG;
+  fa::AppendArgs a = {};
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.k_out = static_cast<__nv_bfloat16*>(k_out);
+  a.v_out = static_cast<__nv_bfloat16*>(v_out);
+  a.cache = static_cast<uint8_t*>(cache);
+  a.slots = slots;
+  a.rows = B * Hkv * N;
+  a.N = N;
+  a.Hkv = Hkv;
+  a.pages = pages;
+  a.shift = shift;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  return launched(fa::launch_cache4_append(a, d, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_cache4_attn_workspace_size(int B, int H, int Hkv, int T, int d) {
+  if (head_dim(d) != FA_OK || B <= 0 || H <= 0 || T <= 0 || Hkv <= 0 || H % Hkv != 0) return 0;
+  if ((long long)B * H * T > INT_MAX) return 0;
+  const int rows = fa::cache4_attn_rows(H / Hkv * T);
+  return align_up(((size_t)B + 1) * sizeof(int)) +
+         align_up((size_t)fa::kC4MaxBlocks * 2 * rows * (d + 2) * sizeof(float));
+}
+
+fa_status fa_cache4_attn(const void* q, const void* cache, const int* block_table,
+                         const int* seq_lens, const int* q_lens, void* o, float* lse,
+                         void* workspace, size_t workspace_bytes, int B, int H, int Hkv, int T,
+                         int d, int max_blocks, int pages, int page_size, int window, float scale,
+                         float k_scale, float v_scale, void* stream) {
+  int shift = 0;
+  fa_status s = check_cache(pages, Hkv, page_size, d, &shift);
+  if (s != FA_OK) return s;
+  if (B < 0 || H < 0 || T < 0 || max_blocks < 0) return FA_ERR_INVALID_ARG;
+  if (H > 0 && (Hkv == 0 || Hkv > H || H % Hkv != 0)) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.0f)) return FA_ERR_INVALID_ARG;
+  if (!cache_scale(k_scale) || !cache_scale(v_scale)) return FA_ERR_INVALID_ARG;
+  if (((long long)max_blocks << shift) > INT_MAX || (long long)B * H > INT_MAX ||
+      (long long)B * H * T > INT_MAX || (long long)B * max_blocks > INT_MAX)
+    return FA_ERR_UNSUPPORTED;
+  if (B == 0 || H == 0 || T == 0) return FA_OK;
+  if (!q || !seq_lens || !o || !lse || (pages > 0 && !cache) || (max_blocks > 0 && !block_table))
+    return FA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(cache, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
+      !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(q_lens, 4))
+    return FA_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < fa_cache4_attn_workspace_size(B, H, Hkv, T, d))
+    return FA_ERR_WORKSPACE;
+  fa::DeviceInfo dev;
+  if ((s = fa::device_info(&dev)) != FA_OK) return s;
+  fa::Cache4AttnArgs a = {};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.q_lens = q_lens;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.unit0 = static_cast<int*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                    align_up(((size_t)B + 1) * sizeof(int)));
+  a.B = B;
+  a.Hkv = Hkv;
+  a.T = T;
+  a.M = max_blocks;
+  a.pages = pages;
+  a.rows = H / Hkv * T;
+  const int rows = fa::cache4_attn_rows(a.rows);
+  a.row_blocks = (a.rows + rows - 1) / rows;
+  a.shift = shift;
+  a.window = window < 0 ? -1 : window;
+  a.scale_log2 = scale * k_scale * 1.4426950408889634f;
+  a.v_scale = v_scale;
+  a.st = dev.st;
+  a.timeout_ns = dev.timeout_ns;
+  return launched(fa::launch_cache4_attn(a, d, dev.sm_count, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -104,6 +104,29 @@ def open_library(path: str):
     lib.fa_bwd_noalloc.restype = i
     lib.fa_bwd_noalloc_max_workspace.argtypes = []
     lib.fa_bwd_noalloc_max_workspace.restype = ctypes.c_size_t
+    ll, sz = ctypes.c_longlong, ctypes.c_size_t
+    lib.fa_qk_norm_rope.argtypes = [vp, ll, ll, vp, i, i, vp, vp, vp, i, f, i,
+                                    vp, vp, vp, i, i, i, i, i, vp]
+    lib.fa_qk_norm_rope.restype = i
+    lib.fa_qk_norm_rope_bwd_workspace_size.argtypes = [i]
+    lib.fa_qk_norm_rope_bwd_workspace_size.restype = sz
+    lib.fa_qk_norm_rope_bwd.argtypes = [vp, ll, ll, vp, i, i, vp, vp, vp, i, f,
+                                        i, vp, vp, vp, vp, ll, ll, vp, vp, vp,
+                                        sz, i, i, i, i, i, vp]
+    lib.fa_qk_norm_rope_bwd.restype = i
+    lib.fa_cache4_page_bytes.argtypes = [i, i, i]
+    lib.fa_cache4_page_bytes.restype = sz
+    lib.fa_cache4_plan.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i,
+                                   i, vp]
+    lib.fa_cache4_plan.restype = i
+    lib.fa_cache4_append.argtypes = [vp, vp, vp, vp, f, f, vp, vp, i, i, i, i,
+                                     i, i, vp]
+    lib.fa_cache4_append.restype = i
+    lib.fa_cache4_attn_workspace_size.argtypes = [i, i, i, i, i]
+    lib.fa_cache4_attn_workspace_size.restype = sz
+    lib.fa_cache4_attn.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, sz, i, i, i,
+                                   i, i, i, i, i, i, f, f, f, vp]
+    lib.fa_cache4_attn.restype = i
     lib.fa_status_string.argtypes = [i]
     lib.fa_status_string.restype = ctypes.c_char_p
     return lib
@@ -489,3 +512,273 @@ def fa_bwd_noalloc(q, k, v, o, lse, dout, causal: bool, scale: float, dq,
             _ptr(dq), _ptr(dk), _ptr(dv), B, H, N, d, int(bool(causal)),
             float(scale), _stream_handle(q.device)))
     return dq, dk, dv
+
+
+def _check_same(device, dtype, **tensors):
+    """Contiguous tensors of one type on one device (None passes)."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch.Tensor" % name)
+        if t.dtype != dtype or t.device != device or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous %s tensor on %s"
+                             % (name, dtype, device))
+
+
+def _check_shape(name, t, shape):
+    if t is not None and t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s"
+                         % (name, tuple(t.shape), tuple(shape)))
+
+
+def _rope_checks(qkv, H, Hkv, rope, positions, q_weight, k_weight):
+    """Checks of the arguments that the norm with rotation and its backward
+    share; returns the C arguments from qkv to the weights' type, and the
+    sizes."""
+    H, Hkv = int(H), int(Hkv)
+    if not isinstance(qkv, torch.Tensor):
+        raise TypeError("qkv must be a torch.Tensor")
+    if qkv.dtype != torch.bfloat16 or not qkv.is_cuda or qkv.dim() != 4 \
+            or H < 0 or Hkv < 0 or qkv.shape[2] != H + 2 * Hkv:
+        raise ValueError("qkv must be a bf16 CUDA tensor [B,N,H+2*Hkv,d]")
+    B, N, heads, d = qkv.shape
+    sb, sn = _token_strides("qkv", qkv)
+    dev = qkv.device
+    if not isinstance(rope, torch.Tensor) or rope.dim() != 2:
+        raise ValueError("rope must be an fp32 tensor [positions, rot]")
+    _check_same(dev, torch.float32, rope=rope)
+    _check_same(dev, torch.int32, positions=positions)
+    _check_shape("positions", positions, (B, N))
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight come together")
+    bf16 = 0
+    if q_weight is not None:
+        bf16 = int(q_weight.dtype == torch.bfloat16)
+        _check_same(dev, torch.bfloat16 if bf16 else torch.float32,
+                    q_weight=q_weight, k_weight=k_weight)
+        _check_shape("q_weight", q_weight, (d,))
+        _check_shape("k_weight", k_weight, (d,))
+    args = (_ptr(qkv), sb, sn, _ptr(rope), rope.shape[0], rope.shape[1],
+            _ptr(positions), _ptr(q_weight), _ptr(k_weight), bf16)
+    return args, (B, N, H, Hkv, d)
+
+
+def _token_strides(name, t):
+    """Strides of the batch and token axes of a [B,N,heads,d] tensor whose
+    tokens are contiguous rows (axes of length one may have any)."""
+    B, N, heads, d = t.shape
+    if t.numel() and ((d > 1 and t.stride(3) != 1)
+                      or (heads > 1 and t.stride(2) != d)):
+        raise ValueError("%s must have contiguous tokens [heads, d]" % name)
+    return (t.stride(0) if B > 1 else 0), (t.stride(1) if N > 1 else 0)
+
+
+def fa_qk_norm_rope(qkv, H: int, Hkv: int, rope, positions=None, q_weight=None,
+                    k_weight=None, eps: float = 1e-6,
+                    interleaved: bool = False, q=None, k=None, v=None):
+    """Norms of the query and key heads of a projection's output with the
+    rotation of their positions.
+
+    qkv: bf16 [B,N,H+2*Hkv,d] (query, key, value heads; tokens contiguous,
+    batch and token strides free); rope: fp32 [positions, rot], rot/2 cosines
+    then rot/2 sines a row; positions: int32 [B,N] or None (0 .. N-1);
+    q_weight, k_weight: [d], bf16 or fp32, or None for no norm.
+    Returns (q [B,H,N,d], k [B,Hkv,N,d], v [B,Hkv,N,d])."""
+    lib = load_library()
+    args, (B, N, H, Hkv, d) = _rope_checks(qkv, H, Hkv, rope, positions,
+                                           q_weight, k_weight)
+    dev = qkv.device
+    q = _output("q", q, (B, H, N, d), torch.bfloat16, dev)
+    k = _output("k", k, (B, Hkv, N, d), torch.bfloat16, dev)
+    v = _output("v", v, (B, Hkv, N, d), torch.bfloat16, dev)
+    with torch.cuda.device(dev):
+        _check("fa_qk_norm_rope", lib.fa_qk_norm_rope(
+            *args, float(eps), int(bool(interleaved)), _ptr(q), _ptr(k),
+            _ptr(v), B, N, H, Hkv, d, _stream_handle(dev)))
+    return q, k, v
+
+
+def _output(name, t, shape, dtype, device):
+    """The caller's output tensor (checked) or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check_same(device, dtype, **{name: t})
+    _check_shape(name, t, shape)
+    return t
+
+
+def fa_qk_norm_rope_bwd_workspace_size(d: int) -> int:
+    return int(load_library().fa_qk_norm_rope_bwd_workspace_size(d))
+
+
+def fa_qk_norm_rope_bwd(qkv, H: int, Hkv: int, rope, dq, dk, dv,
+                        positions=None, q_weight=None, k_weight=None,
+                        eps: float = 1e-6, interleaved: bool = False,
+                        dqkv=None, workspace=None):
+    """Backward of fa_qk_norm_rope.  Returns (dqkv [B,N,H+2*Hkv,d] bf16,
+    dq_weight, dk_weight fp32 [d]; None without weights)."""
+    lib = load_library()
+    args, (B, N, H, Hkv, d) = _rope_checks(qkv, H, Hkv, rope, positions,
+                                           q_weight, k_weight)
+    dev = qkv.device
+    for name, t, h in (("dq", dq, H), ("dk", dk, Hkv), ("dv", dv, Hkv)):
+        if t is None:
+            raise TypeError("%s must be a torch.Tensor" % name)
+        _check_same(dev, torch.bfloat16, **{name: t})
+        _check_shape(name, t, (B, h, N, d))
+    if dqkv is None:
+        dqkv = torch.empty((B, N, H + 2 * Hkv, d), dtype=torch.bfloat16,
+                           device=dev)
+    elif not isinstance(dqkv, torch.Tensor) or dqkv.dtype != torch.bfloat16 \
+            or dqkv.device != dev or dqkv.shape != qkv.shape:
+        raise ValueError("dqkv must be a bf16 tensor of qkv's shape on %s"
+                         % dev)
+    dsb, dsn = _token_strides("dqkv", dqkv)
+    dqw = dkw = None
+    size = 0
+    if q_weight is not None:
+        both = torch.empty((2, d), dtype=torch.float32, device=dev)
+        dqw, dkw = both[0], both[1]
+        if workspace is None:
+            workspace = torch.empty(
+                max(fa_qk_norm_rope_bwd_workspace_size(d), 16),
+                dtype=torch.uint8, device=dev)
+        size = workspace.numel() * workspace.element_size()
+    with torch.cuda.device(dev):
+        _check("fa_qk_norm_rope_bwd", lib.fa_qk_norm_rope_bwd(
+            *args, float(eps), int(bool(interleaved)), _ptr(dq), _ptr(dk),
+            _ptr(dv), _ptr(dqkv), dsb, dsn, _ptr(dqw), _ptr(dkw),
+            _ptr(workspace), size, B, N, H, Hkv, d, _stream_handle(dev)))
+    return dqkv, dqw, dkw
+
+
+def fa_cache4_page_bytes(Hkv: int, page_size: int, d: int) -> int:
+    return int(load_library().fa_cache4_page_bytes(Hkv, page_size, d))
+
+
+def _cache_sizes(cache):
+    """(pages, Hkv, page_size, d) of a 4-bit cache tensor, uint8
+    [pages, Hkv, page_size / 16, 18 * d]."""
+    if not isinstance(cache, torch.Tensor) or cache.dtype != torch.uint8 \
+            or not cache.is_cuda or cache.dim() != 4 \
+            or cache.shape[3] % 18 or not cache.is_contiguous():
+        raise ValueError("cache must be a contiguous uint8 CUDA tensor "
+                         "[pages, Hkv, page_size / 16, 18 * d]")
+    pages, Hkv, groups, width = cache.shape
+    return pages, Hkv, 16 * groups, width // 18
+
+
+def fa_cache4_plan(new_tokens, lens, block_table, free_list, free_count,
+                   page_size: int, T: int, slots=None, positions=None,
+                   granted=None):
+    """Block tables and slot maps of a step, built on the GPU.  new_tokens,
+    lens: int32 [R]; block_table: int32 [R, max_blocks]; free_list: int32
+    [pages]; free_count: int32 [1].  lens, block_table, free_list and
+    free_count are updated in place.  Returns (slots [R,T], positions [R,T],
+    granted [R]), int32."""
+    lib = load_library()
+    if not isinstance(new_tokens, torch.Tensor) or not new_tokens.is_cuda:
+        raise ValueError("new_tokens must be an int32 CUDA tensor [R]")
+    dev, R, T = new_tokens.device, new_tokens.numel(), int(T)
+    _check_same(dev, torch.int32, new_tokens=new_tokens, lens=lens,
+                block_table=block_table, free_list=free_list,
+                free_count=free_count)
+    if lens is None or block_table is None or free_list is None \
+            or free_count is None:
+        raise TypeError("lens, block_table, free_list and free_count must be "
+                        "tensors")
+    if block_table.dim() != 2 or free_list.dim() != 1:
+        raise ValueError("block_table must be [R, max_blocks], free_list "
+                         "[pages]")
+    M = block_table.shape[1]
+    for name, t, shape in (("new_tokens", new_tokens, (R,)),
+                           ("lens", lens, (R,)),
+                           ("block_table", block_table, (R, M)),
+                           ("free_count", free_count, (1,))):
+        _check_shape(name, t, shape)
+    if T < 0:
+        raise ValueError("T must not be negative")
+    slots = _output("slots", slots, (R, T), torch.int32, dev)
+    positions = _output("positions", positions, (R, T), torch.int32, dev)
+    granted = _output("granted", granted, (R,), torch.int32, dev)
+    with torch.cuda.device(dev):
+        _check("fa_cache4_plan", lib.fa_cache4_plan(
+            _ptr(new_tokens), _ptr(lens), _ptr(block_table), _ptr(free_list),
+            _ptr(free_count), _ptr(slots), _ptr(positions), _ptr(granted), R,
+            M, free_list.numel(), int(page_size), T, _stream_handle(dev)))
+    return slots, positions, granted
+
+
+def fa_cache4_append(k, v, cache, slots, k_scale: float = 1.0,
+                     v_scale: float = 1.0, k_out=None, v_out=None):
+    """Writes keys and values, bf16 [B,Hkv,N,d], to their slots (int32
+    [B,N]) of the 4-bit cache.  k_out and v_out, if given, receive the values
+    that the cache then holds.  Returns the cache."""
+    lib = load_library()
+    pages, Hkv, page, d = _cache_sizes(cache)
+    dev = cache.device
+    _check_qkv("k", k)
+    B, _, N, _ = k.shape
+    _check_same(dev, torch.bfloat16, k=k, v=v, k_out=k_out, v_out=v_out)
+    if v is None:
+        raise TypeError("v must be a torch.Tensor")
+    if (k_out is None) != (v_out is None):
+        raise ValueError("k_out and v_out come together")
+    for name, t in (("k", k), ("v", v), ("k_out", k_out), ("v_out", v_out)):
+        _check_shape(name, t, (B, Hkv, N, d))
+    if slots is None:
+        raise TypeError("slots must be a torch.Tensor")
+    _check_same(dev, torch.int32, slots=slots)
+    _check_shape("slots", slots, (B, N))
+    with torch.cuda.device(dev):
+        _check("fa_cache4_append", lib.fa_cache4_append(
+            _ptr(k), _ptr(v), _ptr(cache), _ptr(slots), float(k_scale),
+            float(v_scale), _ptr(k_out), _ptr(v_out), B, Hkv, N, d, pages,
+            page, _stream_handle(dev)))
+    return cache
+
+
+def fa_cache4_attn_workspace_size(B: int, H: int, Hkv: int, T: int,
+                                  d: int) -> int:
+    return int(load_library().fa_cache4_attn_workspace_size(B, H, Hkv, T, d))
+
+
+def fa_cache4_attn(q, cache, block_table, seq_lens, scale: float, q_lens=None,
+                   window: int = -1, k_scale: float = 1.0,
+                   v_scale: float = 1.0, out=None, lse=None, workspace=None):
+    """Causal attention of the newest tokens of each request, q bf16
+    [B,H,T,d], over its pages of the 4-bit cache.  block_table: int32
+    [B, max_blocks]; seq_lens: int32 [B], the new tokens included; q_lens:
+    int32 [B] new tokens of each request, or None for T.  Rows past a
+    request's new tokens are left as they were.  Returns (O, LSE)."""
+    lib = load_library()
+    pages, Hkv, page, d = _cache_sizes(cache)
+    _check_qkv("q", q)
+    B, H, T, _ = q.shape
+    dev = q.device
+    if cache.device != dev:
+        raise ValueError("cache is on %s, q on %s" % (cache.device, dev))
+    _check_shape("q", q, (B, H, T, d))
+    _check_seq_lens(seq_lens, B, dev)
+    if q_lens is not None:
+        _check_seq_lens(q_lens, B, dev)
+    if block_table is None or block_table.dim() != 2:
+        raise ValueError("block_table must be an int32 tensor [B, max_blocks]")
+    _check_same(dev, torch.int32, block_table=block_table)
+    M = block_table.shape[1]
+    _check_shape("block_table", block_table, (B, M))
+    out = _output("out", out, (B, H, T, d), torch.bfloat16, dev)
+    lse = _output("lse", lse, (B, H, T), torch.float32, dev)
+    if workspace is None:
+        workspace = torch.empty(
+            max(fa_cache4_attn_workspace_size(B, H, Hkv, T, d), 256),
+            dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        _check("fa_cache4_attn", lib.fa_cache4_attn(
+            _ptr(q), _ptr(cache), _ptr(block_table), _ptr(seq_lens),
+            _ptr(q_lens), _ptr(out), _ptr(lse), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), B, H, Hkv, T, d, M,
+            pages, page, int(window), float(scale), float(k_scale),
+            float(v_scale), _stream_handle(dev)))
+    return out, lse
