@@ -357,7 +357,7 @@ def check_attn(c, o, lse, rows_left=7.0):
     es = (d + 8) * 2.0 ** -24 * c["scale"] * (np.abs(q) * kmax).sum(-1)
     assert np.isfinite(o[live]).all() and np.isfinite(lse[live]).all()
     room = es + 2.0 ** -20 * (1 + np.abs(np.where(live, rl, 0)))
-    assert (np.abs(lse - rl)[live] <= room[live]).all()
+    assert (np.abs(lse[live] - rl[live]) <= room[live]).all()
     w = 2.0 ** -11 + 2 * es + 2.0 ** -20 + int(max(c["lens"])) * 2.0 ** -32
     room = 2.0 ** -8 * np.abs(np.where(live[..., None], ro, 0)) + w[..., None] * vmax
     err = np.abs(o - ro)

@@ -177,7 +177,8 @@ __global__ void __launch_bounds__(kWarps * 32) cache4_attn_kernel(Cache4AttnArgs
   }
   const int before = upto - mine;
   const long long W = (long long)total * items;
-  const long long u0 = W * blockIdx.x / gridDim.x, u1 = W * (blockIdx.x + 1) / gridDim.x;
+  // No more blocks than units: every one that works has at least one unit.
+  const int blocks = (int)min((long long)gridDim.x, W);
   if (blockIdx.x == 0) {  // for the joining kernel
     int at = before;
     for (int b = b0; b < b1; ++b) {
@@ -186,7 +187,8 @@ __global__ void __launch_bounds__(kWarps * 32) cache4_attn_kernel(Cache4AttnArgs
     }
     if (tid == 0) a.unit0[a.B] = total;
   }
-  if (u0 >= u1) return;
+  if ((int)blockIdx.x >= blocks) return;
+  const long long u0 = W * blockIdx.x / blocks, u1 = W * (blockIdx.x + 1) / blocks;
   if (u0 >= (long long)before * items && u0 < (long long)upto * items) {
     long long left = u0 - (long long)before * items;
     int b = b0;
@@ -538,11 +540,12 @@ __global__ void __launch_bounds__(kWarps * 32) cache4_attn_kernel(Cache4AttnArgs
 // Joins the partial results of an item that lies in several blocks' shares,
 // in block order.  One block per row of an item, one thread per dim.
 template <int D, int NT>
-__global__ void __launch_bounds__(D) cache4_join_kernel(Cache4AttnArgs a, int blocks) {
+__global__ void __launch_bounds__(D) cache4_join_kernel(Cache4AttnArgs a, int grid) {
   using S = Shape<D, NT>;
   const int items = a.Hkv * a.row_blocks;
   const int row_in = blockIdx.y;
   const long long total = (long long)a.unit0[a.B] * items;
+  const int blocks = (int)min((long long)grid, total);
   for (long long it = blockIdx.x; it < (long long)a.B * items; it += gridDim.x) {
     const int b = (int)(it / items), item = (int)(it - (long long)b * items);
     const int hk = item / a.row_blocks, r = (item - hk * a.row_blocks) * S::kRows + row_in;
