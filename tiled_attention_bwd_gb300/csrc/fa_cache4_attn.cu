@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kUnit = kWarps * kGroup;  // tokens of a work unit
-constexpr float kNoMax = -1e30f;        // below every score's maximum
+constexpr float kNoMax = -1e30f;        // m of a row that has seen no key
 constexpr float kUp = 8.0f;             // P carries 2^kUp
 constexpr float kSlack = 6.0f;          // growth of m that is left standing
 
@@ -107,17 +107,19 @@ __device__ __forceinline__ Request request_of(const Cache4AttnArgs& a, int b) {
 
 // A block's place in the list of units.
 struct Cursor {
-  int b;     // request
-  int item;  // key/value head * row_blocks + row block
-  int unit;  // within the item
+  int b;         // request
+  int hk, rb;    // the item's key/value head and row block
+  int unit;      // within the item
   Request r;
 };
 
 // The next item with units, or b = B.
 __device__ __forceinline__ void next_item(const Cache4AttnArgs& a, Cursor& c) {
   c.unit = 0;
-  if (++c.item < a.Hkv * a.row_blocks) return;
-  c.item = 0;
+  if (++c.rb < a.row_blocks) return;
+  c.rb = 0;
+  if (++c.hk < a.Hkv) return;
+  c.hk = 0;
   do {
     if (++c.b >= a.B) return;
     c.r = request_of(a, c.b);
@@ -127,7 +129,8 @@ __device__ __forceinline__ void next_item(const Cache4AttnArgs& a, Cursor& c) {
 template <int D, int NT>
 struct Shape {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kStages = 6;
+  static constexpr int kStages = 4;  // a power of two
+  static constexpr int kBlocksPerSm = NT == 1 ? 4 : 3;
   static constexpr int kRing = kWarps * kStages * group_bytes(D);
   static constexpr int kPitch = D + 4;  // floats of a row in the join buffer
   static constexpr int kJoin = kWarps * 8 * kPitch * 4;
@@ -136,12 +139,13 @@ struct Shape {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32) cache4_attn_kernel(Cache4AttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm) cache4_attn_kernel(Cache4AttnArgs a) {
   using S = Shape<D, NT>;
   constexpr int kSteps = D / 16;  // 16-dim steps of Q K^T; also 16-dim tiles of O^T
   constexpr int kWords = D / 32;  // 32-bit words of K codes per lane and token
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kWarps][S::kStages];
+  __shared__ int there[kWarps][S::kStages];  // 0: the slot's group was not copied
   __shared__ uint32_t cta_abort;
   __shared__ int sh_scan[kWarps], sh_first[4];
   __shared__ float sh_ml[kWarps][8][2];
@@ -204,50 +208,54 @@ __global__ void __launch_bounds__(kWarps * 32) cache4_attn_kernel(Cache4AttnArgs
   __syncthreads();
   Cursor use;
   use.b = sh_first[0];
-  use.item = sh_first[1];
+  use.hk = sh_first[1] / a.row_blocks;
+  use.rb = sh_first[1] - use.hk * a.row_blocks;
   use.unit = sh_first[2];
   use.r = request_of(a, use.b);
   const int mine_units = (int)(u1 - u0);
 
-  // ---- the warp's own ring
+  // ---- the warp's own ring: slot n % kStages for the share's n-th unit.
+  // Each lane works out where one of the next 32 units' groups lies and
+  // issues that copy when its turn comes.
   Cursor load = use;
-  int issued = 0;        // units of the share that the loads have passed
-  int put = 0, got = 0;  // groups copied, groups used
+  int put = 0, got = 0;                  // units passed by the loads and by the products
+  int turn = 0, turns = 0;               // place in the lanes' units
+  const uint8_t* src = nullptr;
   bool dead = false;
-  const int gpp_shift = a.shift - 4;
-  // Page ids of the next 32 units of the loads' item, one per lane.
-  int ids = -1, ids_unit = -1;
-  auto load_ids = [&]() {
+  auto look_ahead = [&]() {
+    turn = 0;
+    turns = min(32, load.r.units - load.unit);
     const int tok = load.r.lo + (load.unit + lane) * kUnit + warp * kGroup;
-    ids = -1;
-    if (tok < load.r.len) ids = __ldg(a.block_table + (size_t)load.b * a.M + (tok >> a.shift));
-    ids_unit = load.unit;
-  };
-  // Walks the loads on until the ring is full.  A group outside the request
-  // or on a page outside the cache is not copied (see `take`).
-  auto feed = [&]() {
-    while (issued < mine_units && put - got < S::kStages) {
-      if (ids_unit < 0 || load.unit - ids_unit >= 32) load_ids();
-      const int tok = load.r.lo + load.unit * kUnit + warp * kGroup;
-      const int page = __shfl_sync(0xffffffffu, ids, load.unit - ids_unit);
-      if (tok < load.r.len && page >= 0 && page < a.pages) {
-        const int slot = put % S::kStages;
-        if (lane == 0) {
-          const size_t at = ((((size_t)page * a.Hkv + load.item / a.row_blocks) << gpp_shift) +
-                             ((tok >> 4) & ((1 << gpp_shift) - 1))) * group_bytes(D);
-          mbar_arrive_expect_tx(&full[warp][slot], group_bytes(D));
-          bulk_load(ring + slot * group_bytes(D), a.cache + at, group_bytes(D), &full[warp][slot]);
-        }
-        ++put;
-      }
-      ++issued;
-      if (++load.unit == load.r.units) {
-        next_item(a, load);
-        ids_unit = -1;
-      }
+    src = nullptr;
+    if (lane < turns && tok < load.r.len) {
+      const int page = __ldg(a.block_table + (size_t)load.b * a.M + (tok >> a.shift));
+      const int gpp_shift = a.shift - 4;
+      if (page >= 0 && page < a.pages)
+        src = a.cache + ((((size_t)page * a.Hkv + load.hk) << gpp_shift) +
+                         ((tok >> 4) & ((1 << gpp_shift) - 1))) * group_bytes(D);
     }
   };
-  feed();
+  auto feed = [&]() {
+    if (turn == turns) {
+      load.unit += turns;
+      if (load.unit == load.r.units) next_item(a, load);
+      look_ahead();
+    }
+    if (lane == turn) {
+      const int slot = put & (S::kStages - 1);
+      there[warp][slot] = src != nullptr;
+      if (src) {
+        mbar_arrive_expect_tx(&full[warp][slot], group_bytes(D));
+        bulk_load(ring + slot * group_bytes(D), src, group_bytes(D), &full[warp][slot]);
+      } else {
+        mbar_arrive(&full[warp][slot]);
+      }
+    }
+    ++turn;
+    ++put;
+  };
+  look_ahead();
+  while (put < mine_units && put < S::kStages) feed();
 
   int left = mine_units;
   bool first_segment = true;
@@ -256,8 +264,8 @@ __global__ void __launch_bounds__(kWarps * 32) cache4_attn_kernel(Cache4AttnArgs
     const int end = min(use.r.units, use.unit + left);
     const int seg = end - use.unit;
     const bool whole = use.unit == 0 && end == use.r.units;
-    const int hk = use.item / a.row_blocks, row0 = (use.item - hk * a.row_blocks) * S::kRows;
-    const size_t q_row = ((size_t)use.b * a.Hkv + hk) * a.rows + row0;
+    const int row0 = use.rb * S::kRows;
+    const size_t q_row = ((size_t)use.b * a.Hkv + use.hk) * a.rows + row0;
 
     // Q fragments: row 8 nt + g, dims t D/4 + 0 .. D/4 - 1, scaled to f16.
     uint32_t qf[NT][D / 8];
@@ -287,8 +295,9 @@ __global__ void __launch_bounds__(kWarps * 32) cache4_attn_kernel(Cache4AttnArgs
       for (int i = 0; i < D / 8; ++i)
         qf[nt][i] = f16x2(__uint_as_float(qf[nt][i] << 16) * down,
                           __uint_as_float(qf[nt][i] & 0xffff0000u) * down);
-      rs[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);
-      rs[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+      // (Not zero: a masked score, minus infinity, is multiplied with it.)
+      rs[nt][0] = fmaxf(__shfl_sync(0xffffffffu, back, 8 * t), 1.2e-38f);
+      rs[nt][1] = fmaxf(__shfl_sync(0xffffffffu, back, 8 * t + 4), 1.2e-38f);
     }
 
     // Keys that a row sees: [row_lo, row_hi).
@@ -305,6 +314,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache4_attn_kernel(Cache4AttnArgs
     // Groups within [plain_lo, plain_hi) are seen whole by every row.
     const int plain_hi = pos0 + 1, plain_lo = a.window < 0 ? 0 : use.r.len - 1 - a.window;
 
+    // m: the row's maximum less kUp, in powers of two: weights are 2^(s - m).
     float o[kSteps][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -314,153 +324,149 @@ __global__ void __launch_bounds__(kWarps * 32) cache4_attn_kernel(Cache4AttnArgs
       l[nt][0] = l[nt][1] = 0.f;
     }
 
-    int page_ids = -1;
-    for (int un = use.unit; un < end; ++un) {
-      const int k_in = un - use.unit;
-      const int tok = use.r.lo + un * kUnit + warp * kGroup;
-      if ((k_in & 31) == 0) {
-        const int tk = tok + lane * kUnit;
-        page_ids = tk < use.r.len ? __ldg(a.block_table + (size_t)use.b * a.M + (tk >> a.shift)) : -1;
+    for (int un = dead ? end : use.unit; un < end; ++un) {
+      const int slot = got & (S::kStages - 1), tok = use.r.lo + un * kUnit + warp * kGroup;
+      if (!wait_bar_warp(&full[warp][slot], (got / S::kStages) & 1, ctl, 0x511)) {
+        dead = true;
+        break;
       }
-      const int page = __shfl_sync(0xffffffffu, page_ids, k_in & 31);
-      if (!(tok < use.r.len && page >= 0 && page < a.pages)) continue;
-      const int slot = got % S::kStages;
-      if (!dead && !wait_bar_warp(&full[warp][slot], (got / S::kStages) & 1, ctl, 0x511)) dead = true;
-      if (dead) break;
       const uint8_t* grp = ring + slot * group_bytes(D);
-
-      // ---- S^T = K Q^T: tokens g and g + 8 of the group, rows 2t and 2t + 1
-      float s[NT][4];
+      if (there[warp][slot]) {
+        // ---- S^T = K Q^T: tokens g and g + 8 of the group, rows 2t and 2t + 1
+        float s[NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-      uint32_t kc[2][kWords], ks[2][D / 64];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint8_t* kp = grp + k_code_at(D, g + 8 * h, t * (D / 8));
-        const uint8_t* sp = grp + k_scale_at(D, g + 8 * h, t * (D / 64));
-        if constexpr (D == 128) {
-          const uint4 u = *reinterpret_cast<const uint4*>(kp);
-          kc[h][0] = u.x, kc[h][1] = u.y, kc[h][2] = u.z, kc[h][3] = u.w;
-          const uint32_t two = e4m3_to_f16(*reinterpret_cast<const uint16_t*>(sp));
-          ks[h][0] = __byte_perm(two, 0, 0x1010);
-          ks[h][1] = __byte_perm(two, 0, 0x3232);
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(kp);
-          kc[h][0] = u.x, kc[h][1] = u.y;
-          ks[h][0] = __byte_perm(e4m3_to_f16(*sp), 0, 0x1010);
-        }
-      }
-#pragma unroll
-      for (int w = 0; w < kWords; ++w) {
-        uint32_t x[4], y[4];
-        e2m1_to_f16(kc[0][w], x);
-        e2m1_to_f16(kc[1][w], y);
-        const uint32_t s0 = ks[0][w / 2], s1 = ks[1][w / 2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], s0), y[i] = mul2(y[i], s1);
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const uint32_t f[4] = {x[2 * hh], y[2 * hh], x[2 * hh + 1], y[2 * hh + 1]};
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma(s[nt], f, qf[nt][4 * w + 2 * hh], qf[nt][4 * w + 2 * hh + 1]);
-        }
-      }
-
-      // ---- softmax weights
-      const bool plain = tok >= plain_lo && tok + kGroup <= plain_hi;
-      bool grow = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[nt][i] *= rs[nt][i & 1];
-          if (!plain) {
-            const int j = tok + g + 8 * (i >> 1);
-            if (j >= row_hi[nt][i & 1] || j < row_lo[nt][i & 1]) s[nt][i] = -INFINITY;
-          }
-          grow |= s[nt][i] > m[nt][i & 1] + kSlack;
-        }
-      }
-      if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float mx = fmaxf(s[nt][i], s[nt][i + 2]);
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-            mx = fmaxf(mx, m[nt][i]);
-            const float f = ex2(m[nt][i] - mx);
-            m[nt][i] = mx;
-            l[nt][i] *= f;
-#pragma unroll
-            for (int dt = 0; dt < kSteps; ++dt) o[dt][nt][i] *= f, o[dt][nt][i + 2] *= f;
-          }
-      }
-      uint32_t pb[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float p[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = ex2(s[nt][i] - (m[nt][i & 1] - kUp));
-        l[nt][0] += p[0] + p[2];
-        l[nt][1] += p[1] + p[3];
-        pb[nt][0] = transpose8x8(f16x2(p[0], p[1]));
-        pb[nt][1] = transpose8x8(f16x2(p[2], p[3]));
-      }
-
-      // ---- O^T += V^T P^T
-      uint32_t vs[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t two = *reinterpret_cast<const uint16_t*>(
-            grp + v_scale_at(D, 8 * h + 2 * t, D == 128 ? g : g >> 1));
-        if (!plain) {
-          // Tokens that no row sees may hold anything, NaN scales included.
-          const int j = tok + 8 * h + 2 * t, lo = a.window < 0 ? 0 : pos0 - a.window;
-          if (j < lo || j >= use.r.len) two &= 0xff00u;
-          if (j + 1 < lo || j + 1 >= use.r.len) two &= 0x00ffu;
-        }
-        vs[h] = e4m3_to_f16(two);
-      }
-      constexpr int kVWords = D / 64;  // words of one token's eighth
-      uint32_t vc[2][2][kVWords];      // [half][token parity][word]
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint8_t* vp = grp + v_code_at(D, 8 * h + 2 * t, g);
-        if constexpr (D == 128) {
-          const uint4 u = *reinterpret_cast<const uint4*>(vp);
-          vc[h][0][0] = u.x, vc[h][0][1] = u.y, vc[h][1][0] = u.z, vc[h][1][1] = u.w;
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(vp);
-          vc[h][0][0] = u.x, vc[h][1][0] = u.y;
-        }
-      }
-#pragma unroll
-      for (int w = 0; w < kVWords; ++w) {
-        // Bytes of the two tokens' codes of one dim: even dims, odd dims.
-        uint32_t ev[2][4], od[2][4];
+        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+        uint32_t kc[2][kWords], ks[2][D / 64];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t x = vc[h][0][w], y = vc[h][1][w];
-          e2m1_to_f16((x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u), ev[h]);
-          e2m1_to_f16(((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), od[h]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ev[h][i] = mul2(ev[h][i], vs[h]), od[h][i] = mul2(od[h][i], vs[h]);
+          const uint8_t* kp = grp + k_code_at(D, g + 8 * h, t * (D / 8));
+          const uint8_t* sp = grp + k_scale_at(D, g + 8 * h, t * (D / 64));
+          if constexpr (D == 128) {
+            const uint4 u = *reinterpret_cast<const uint4*>(kp);
+            kc[h][0] = u.x, kc[h][1] = u.y, kc[h][2] = u.z, kc[h][3] = u.w;
+            const uint32_t two = e4m3_to_f16(*reinterpret_cast<const uint16_t*>(sp));
+            ks[h][0] = __byte_perm(two, 0, 0x1010);
+            ks[h][1] = __byte_perm(two, 0, 0x3232);
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(kp);
+            kc[h][0] = u.x, kc[h][1] = u.y;
+            ks[h][0] = __byte_perm(e4m3_to_f16(*sp), 0, 0x1010);
+          }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t f[4] = {ev[0][i], od[0][i], ev[1][i], od[1][i]};
+        for (int w = 0; w < kWords; ++w) {
+          uint32_t x[4], y[4];
+          e2m1_to_f16(kc[0][w], x);
+          e2m1_to_f16(kc[1][w], y);
+          const uint32_t s0 = ks[0][w / 2], s1 = ks[1][w / 2];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma(o[4 * w + i][nt], f, pb[nt][0], pb[nt][1]);
+          for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], s0), y[i] = mul2(y[i], s1);
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const uint32_t f[4] = {x[2 * hh], y[2 * hh], x[2 * hh + 1], y[2 * hh + 1]};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma(s[nt], f, qf[nt][4 * w + 2 * hh], qf[nt][4 * w + 2 * hh + 1]);
+          }
+        }
+
+        // ---- softmax weights
+        const bool plain = tok >= plain_lo && tok + kGroup <= plain_hi;
+        float p[NT][4], top = -INFINITY;  // exponents, then weights
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            p[nt][i] = fmaf(s[nt][i], rs[nt][i & 1], -m[nt][i & 1]);
+            if (!plain) {
+              const int j = tok + g + 8 * (i >> 1);
+              if (j >= row_hi[nt][i & 1] || j < row_lo[nt][i & 1]) p[nt][i] = s[nt][i] = -INFINITY;
+            }
+            top = fmaxf(top, p[nt][i]);
+          }
+        }
+        if (__any_sync(0xffffffffu, top > kUp + kSlack)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              // (rs > 0: a score of minus infinity stays one.)
+              float mx = fmaxf(s[nt][i], s[nt][i + 2]) * rs[nt][i];
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+              mx = fmaxf(mx - kUp, m[nt][i]);
+              const float f = ex2(m[nt][i] - mx);
+              m[nt][i] = mx;
+              l[nt][i] *= f;
+#pragma unroll
+              for (int dt = 0; dt < kSteps; ++dt) o[dt][nt][i] *= f, o[dt][nt][i + 2] *= f;
+              p[nt][i] = fmaf(s[nt][i], rs[nt][i], -mx);
+              p[nt][i + 2] = fmaf(s[nt][i + 2], rs[nt][i], -mx);
+            }
+        }
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[nt][i] = ex2(p[nt][i]);
+          l[nt][0] += p[nt][0] + p[nt][2];
+          l[nt][1] += p[nt][1] + p[nt][3];
+          pb[nt][0] = transpose8x8(f16x2(p[nt][0], p[nt][1]));
+          pb[nt][1] = transpose8x8(f16x2(p[nt][2], p[nt][3]));
+        }
+
+        // ---- O^T += V^T P^T
+        uint32_t vs[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t two = *reinterpret_cast<const uint16_t*>(
+              grp + v_scale_at(D, 8 * h + 2 * t, D == 128 ? g : g >> 1));
+          if (!plain) {
+            // Tokens that no row sees may hold anything, NaN scales included.
+            const int j = tok + 8 * h + 2 * t, lo = a.window < 0 ? 0 : pos0 - a.window;
+            if (j < lo || j >= use.r.len) two &= 0xff00u;
+            if (j + 1 < lo || j + 1 >= use.r.len) two &= 0x00ffu;
+          }
+          vs[h] = e4m3_to_f16(two);
+        }
+        constexpr int kVWords = D / 64;  // words of one token's eighth
+        uint32_t vc[2][2][kVWords];      // [half][token parity][word]
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint8_t* vp = grp + v_code_at(D, 8 * h + 2 * t, g);
+          if constexpr (D == 128) {
+            const uint4 u = *reinterpret_cast<const uint4*>(vp);
+            vc[h][0][0] = u.x, vc[h][0][1] = u.y, vc[h][1][0] = u.z, vc[h][1][1] = u.w;
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(vp);
+            vc[h][0][0] = u.x, vc[h][1][0] = u.y;
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < kVWords; ++w) {
+          // Bytes of the two tokens' codes of one dim: even dims, odd dims.
+          uint32_t ev[2][4], od[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t x = vc[h][0][w], y = vc[h][1][w];
+            constexpr uint32_t kLow = 0x0f0f0f0fu;
+            e2m1_to_f16((x & kLow) | ((y << 4) & ~kLow), ev[h]);
+            e2m1_to_f16(((x >> 4) & kLow) | (y & ~kLow), od[h]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ev[h][i] = mul2(ev[h][i], vs[h]), od[h][i] = mul2(od[h][i], vs[h]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t f[4] = {ev[0][i], od[0][i], ev[1][i], od[1][i]};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma(o[4 * w + i][nt], f, pb[nt][0], pb[nt][1]);
+          }
         }
       }
       __syncwarp();  // every lane has read the slot
       ++got;
-      feed();
+      if (put < mine_units) feed();
     }
-    if (dead) issued = mine_units;  // no more loads; the joins below still run
 
     // ---- join the warps, eight rows at a time
     const int slot = 2 * blockIdx.x + (first_segment ? 0 : 1);
@@ -522,7 +528,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache4_attn_kernel(Cache4AttnArgs
         if (!whole) {
           *reinterpret_cast<float2*>(part + D) = make_float2(mx, sum);
         } else if (live) {
-          a.lse[q_row + 8 * nt + row] = sum == 0.f ? -INFINITY : (mx - kUp + log2f(sum)) * kLn2;
+          a.lse[q_row + 8 * nt + row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
         }
       }
     }
@@ -532,9 +538,8 @@ __global__ void __launch_bounds__(kWarps * 32) cache4_attn_kernel(Cache4AttnArgs
     first_segment = false;
   }
   // A stopping block lets its copies land before it leaves.
-  if (dead)
-    for (; got < put; ++got)
-      drain_bar(&full[warp][got % S::kStages], (got / S::kStages) & 1, a.timeout_ns);
+  for (; got < put; ++got)
+    drain_bar(&full[warp][got & (S::kStages - 1)], (got / S::kStages) & 1, a.timeout_ns);
 }
 
 // Joins the partial results of an item that lies in several blocks' shares,
@@ -576,7 +581,7 @@ __global__ void __launch_bounds__(D) cache4_join_kernel(Cache4AttnArgs a, int gr
     const float inv = sum > 0.f || sum != sum ? a.v_scale / sum : 0.f;
     a.o[q_row * D + threadIdx.x] = __float2bfloat16_rn(acc * inv);
     if (threadIdx.x == 0)
-      a.lse[q_row] = sum == 0.f ? -INFINITY : (mx - kUp + log2f(sum)) * kLn2;
+      a.lse[q_row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
   }
 }
 
@@ -586,8 +591,7 @@ cudaError_t run(const Cache4AttnArgs& a, int sm_count, cudaStream_t stream) {
   auto* kernel = cache4_attn_kernel<D, NT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
-  int per_sm = NT == 1 ? 3 : 2;
-  int blocks = sm_count * per_sm;
+  int blocks = sm_count * S::kBlocksPerSm;
   if (blocks > kC4MaxBlocks) blocks = kC4MaxBlocks;
   kernel<<<blocks, kWarps * 32, S::kSmem, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
