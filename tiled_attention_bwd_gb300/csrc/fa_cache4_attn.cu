@@ -37,10 +37,11 @@ namespace fa {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kUnit = kWarps * kGroup;  // tokens of a work unit
-constexpr float kNoMax = -1e30f;        // m of a row that has seen no key
-constexpr float kUp = 8.0f;             // P carries 2^kUp
-constexpr float kSlack = 6.0f;          // growth of m that is left standing
+constexpr int kGroups = 2;                        // of a warp in a unit
+constexpr int kUnit = kWarps * kGroups * kGroup;  // tokens of a work unit
+constexpr float kNoMax = -1e30f;                  // m of a row that has seen no key
+constexpr float kUp = 8.0f;                       // P carries 2^kUp
+constexpr float kSlack = 6.0f;                    // growth of m that is left standing
 
 __device__ __forceinline__ void e2m1_to_f16(uint32_t w, uint32_t* r) {
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
@@ -84,10 +85,17 @@ __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, ui
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_primary() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // What a request has, with the values from memory brought into range.
 struct Request {
   int len, ql;  // cached tokens, new tokens
-  int lo;       // first token of its units (a multiple of 16)
+  int lo;       // first token of its units (a multiple of 32)
   int units;    // of one item
 };
 __device__ __forceinline__ Request request_of(const Cache4AttnArgs& a, int b) {
@@ -98,18 +106,18 @@ __device__ __forceinline__ Request request_of(const Cache4AttnArgs& a, int b) {
   const int n = a.q_lens ? __ldg(a.q_lens + b) : a.T;
   r.ql = n < 0 ? 0 : (n > a.T ? a.T : n);
   const long long first = (long long)r.len - r.ql - a.window;  // the first row's window
-  r.lo = (a.window < 0 || first < 0) ? 0 : (int)(first & ~15ll);
+  r.lo = (a.window < 0 || first < 0) ? 0 : (int)(first & ~(long long)(kGroups * kGroup - 1));
   const int n_keys = r.len - r.lo;
   // A request without keys keeps one unit, which writes its empty rows.
-  r.units = r.ql == 0 ? 0 : (n_keys > 0 ? (n_keys + kUnit - 1) / kUnit : 1);
+  r.units = r.ql == 0 ? 0 : (n_keys > 0 ? (n_keys - 1) / kUnit + 1 : 1);
   return r;
 }
 
 // A block's place in the list of units.
 struct Cursor {
-  int b;         // request
-  int hk, rb;    // the item's key/value head and row block
-  int unit;      // within the item
+  int b;       // request
+  int hk, rb;  // the item's key/value head and row block
+  int unit;    // within the item
   Request r;
 };
 
@@ -126,33 +134,256 @@ __device__ __forceinline__ void next_item(const Cache4AttnArgs& a, Cursor& c) {
   } while (c.r.units == 0);
 }
 
-template <int D, int NT>
-struct Shape {
-  static constexpr int kRows = 8 * NT;
-  static constexpr int kStages = 4;  // a power of two
-  static constexpr int kBlocksPerSm = NT == 1 ? 4 : 3;
-  static constexpr int kRing = kWarps * kStages * group_bytes(D);
-  static constexpr int kPitch = D + 4;  // floats of a row in the join buffer
-  static constexpr int kJoin = kWarps * 8 * kPitch * 4;
-  static constexpr int kSmem = kRing + kJoin;
-  static constexpr int kPartRow = D + 2;  // O, m, l of a partial row
+// Equal shares: `units` dealt to blocks 0 .. blocks-1 in order, the first
+// `more` blocks one more than the others' `least`.
+struct Shares {
+  long long least;
+  int more, blocks;
+  __device__ __forceinline__ Shares(long long units, int grid) {
+    // No more blocks than units: every one that works has at least one.
+    blocks = (int)min((long long)grid, units);
+    if (blocks == 0) {
+      least = more = 0;
+    } else if ((units >> 32) == 0) {
+      least = (uint32_t)units / (uint32_t)blocks;
+      more = (int)((uint32_t)units - (uint32_t)least * (uint32_t)blocks);
+    } else {
+      least = units / blocks;
+      more = (int)(units - least * blocks);
+    }
+  }
+  __device__ __forceinline__ long long first(int c) const { return least * c + min(c, more); }
+  __device__ __forceinline__ int block_of(long long u) const {
+    const long long big = (least + 1) * more;
+    return (int)(u < big ? u / (least + 1) : more + (u - big) / least);
+  }
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm) cache4_attn_kernel(Cache4AttnArgs a) {
+struct Shape {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kSlot = kGroups * group_bytes(D);
+  static constexpr int kStages = 2;
+  static constexpr int kBlocksPerSm = NT == 1 ? 4 : (D == 64 ? 3 : 2);
+  static constexpr int kRing = kWarps * kStages * kSlot;
+  static constexpr int kPitch = D + 4;  // floats of a row in the join buffer
+  static constexpr int kJoin = kWarps * 8 * kPitch * 4;
+  static constexpr int kSmem = kRing + kJoin;
+};
+
+// Where the partial results of a block's first (2 c) and last (2 c + 1)
+// segment lie in the workspace.
+struct Partial {
+  float* o;    // [D]
+  float2* ml;  // m, l
+};
+template <int D, int NT>
+__device__ __forceinline__ Partial partial_of(const Cache4AttnArgs& a, int slot, int row) {
+  const size_t at = (size_t)slot * Shape<D, NT>::kRows + row;
+  return Partial{a.part + at * D, a.part_ml + at};
+}
+
+// One group's scores, S^T = K Q^T: tokens g and g + 8, rows 2t and 2t + 1.
+template <int D, int NT>
+__device__ __forceinline__ void scores(const uint8_t* grp, int g, int t,
+                                       const uint32_t (&qf)[NT][D / 8], float (&s)[NT][4]) {
+  uint32_t kc[2][D / 32], ks[2][D / 64];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint8_t* kp = grp + k_code_at(D, g + 8 * h, t * (D / 8));
+    const uint8_t* sp = grp + k_scale_at(D, g + 8 * h, t * (D / 64));
+    if constexpr (D == 128) {
+      const uint4 u = *reinterpret_cast<const uint4*>(kp);
+      kc[h][0] = u.x, kc[h][1] = u.y, kc[h][2] = u.z, kc[h][3] = u.w;
+      const uint32_t two = e4m3_to_f16(*reinterpret_cast<const uint16_t*>(sp));
+      ks[h][0] = __byte_perm(two, 0, 0x1010);
+      ks[h][1] = __byte_perm(two, 0, 0x3232);
+    } else {
+      const uint2 u = *reinterpret_cast<const uint2*>(kp);
+      kc[h][0] = u.x, kc[h][1] = u.y;
+      ks[h][0] = __byte_perm(e4m3_to_f16(*sp), 0, 0x1010);
+    }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+  for (int w = 0; w < D / 32; ++w) {
+    uint32_t x[4], y[4];
+    e2m1_to_f16(kc[0][w], x);
+    e2m1_to_f16(kc[1][w], y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], ks[0][w / 2]), y[i] = mul2(y[i], ks[1][w / 2]);
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      const uint32_t f[4] = {x[2 * hh], y[2 * hh], x[2 * hh + 1], y[2 * hh + 1]};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        mma(s[nt], f, qf[nt][4 * w + 2 * hh], qf[nt][4 * w + 2 * hh + 1]);
+    }
+  }
+}
+
+// One group's part of O^T += V^T P^T.  vs: the scales of the lane's tokens
+// 2t, 2t + 1 (low half of the group) and 2t + 8, 2t + 9.
+template <int D, int NT>
+__device__ __forceinline__ void values(const uint8_t* grp, int g, int t, const uint32_t (&vs)[2],
+                                       const uint32_t (&pb)[NT][2], float (&o)[D / 16][NT][4]) {
+  constexpr int kWords = D / 64;  // words of one token's eighth of the dims
+  uint32_t vc[2][2][kWords];      // [half][token parity][word]
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint8_t* vp = grp + v_code_at(D, 8 * h + 2 * t, g);
+    if constexpr (D == 128) {
+      const uint4 u = *reinterpret_cast<const uint4*>(vp);
+      vc[h][0][0] = u.x, vc[h][0][1] = u.y, vc[h][1][0] = u.z, vc[h][1][1] = u.w;
+    } else {
+      const uint2 u = *reinterpret_cast<const uint2*>(vp);
+      vc[h][0][0] = u.x, vc[h][1][0] = u.y;
+    }
+  }
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) {
+    // Bytes of the two tokens' codes of one dim: even dims, odd dims.
+    uint32_t ev[2][4], od[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      constexpr uint32_t kLow = 0x0f0f0f0fu;
+      const uint32_t x = vc[h][0][w], y = vc[h][1][w];
+      e2m1_to_f16((x & kLow) | ((y << 4) & ~kLow), ev[h]);
+      e2m1_to_f16(((x >> 4) & kLow) | (y & ~kLow), od[h]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ev[h][i] = mul2(ev[h][i], vs[h]), od[h][i] = mul2(od[h][i], vs[h]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t f[4] = {ev[0][i], od[0][i], ev[1][i], od[1][i]};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mma(o[4 * w + i][nt], f, pb[nt][0], pb[nt][1]);
+    }
+  }
+}
+
+// The running state of a segment's rows in one warp, and what they may see.
+template <int D, int NT>
+struct Rows {
+  uint32_t qf[NT][D / 8];  // row 8 nt + g, dims t D/4 + 0 .. D/4 - 1, scaled to f16
+  float rs[NT][2];         // rows 8 nt + 2t, + 1: score to power of two
+  // m: the row's maximum less kUp, in powers of two; weights are 2^(s - m).
+  float m[NT][2], l[NT][2];
+  float o[D / 16][NT][4];
+};
+
+// What bounds the keys that a segment's rows see.
+struct Bounds {
+  int row0, T;  // first row, rows of a head
+  int pos0;     // position of the first new token
+  int len, window;
+};
+
+// One slot of the ring: both groups' products.  kPlain: every row sees every
+// token; else masks apply and `there` says which groups were copied.
+template <int D, int NT, bool kPlain>
+__device__ __forceinline__ void use_slot(Rows<D, NT>& r, const uint8_t* slot, int tok, int there,
+                                         const Bounds& bd, int g, int t) {
+  float s[kGroups][NT][4], p[kGroups][NT][4], top = -INFINITY;
+#pragma unroll
+  for (int u = 0; u < kGroups; ++u) scores<D, NT>(slot + u * group_bytes(D), g, t, r.qf, s[u]);
+  if constexpr (!kPlain) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int pos = bd.pos0 + (bd.row0 + 8 * nt + 2 * t + i) % bd.T;
+        const int hi = min(pos + 1, bd.len), lo = bd.window < 0 ? 0 : pos - bd.window;
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int j = tok + u * kGroup + g + 8 * h;
+            if (j >= hi || j < lo || !((there >> u) & 1)) s[u][nt][i + 2 * h] = -INFINITY;
+          }
+      }
+  }
+#pragma unroll
+  for (int u = 0; u < kGroups; ++u)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[u][nt][i] = fmaf(s[u][nt][i], r.rs[nt][i & 1], -r.m[nt][i & 1]);
+        top = fmaxf(top, p[u][nt][i]);
+      }
+  if (__any_sync(0xffffffffu, top > kUp + kSlack)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) mx = fmaxf(mx, fmaxf(s[u][nt][i], s[u][nt][i + 2]));
+        mx *= r.rs[nt][i];  // (positive: minus infinity stays)
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+        mx = fmaxf(mx - kUp, r.m[nt][i]);
+        const float f = ex2(r.m[nt][i] - mx);
+        r.m[nt][i] = mx;
+        r.l[nt][i] *= f;
+#pragma unroll
+        for (int dt = 0; dt < D / 16; ++dt) r.o[dt][nt][i] *= f, r.o[dt][nt][i + 2] *= f;
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) {
+          p[u][nt][i] = fmaf(s[u][nt][i], r.rs[nt][i], -mx);
+          p[u][nt][i + 2] = fmaf(s[u][nt][i + 2], r.rs[nt][i], -mx);
+        }
+      }
+  }
+#pragma unroll
+  for (int u = 0; u < kGroups; ++u) {
+    uint32_t pb[NT][2], vs[2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[u][nt][i] = ex2(p[u][nt][i]);
+      r.l[nt][0] += p[u][nt][0] + p[u][nt][2];
+      r.l[nt][1] += p[u][nt][1] + p[u][nt][3];
+      pb[nt][0] = transpose8x8(f16x2(p[u][nt][0], p[u][nt][1]));
+      pb[nt][1] = transpose8x8(f16x2(p[u][nt][2], p[u][nt][3]));
+    }
+    const uint8_t* grp = slot + u * group_bytes(D);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t two = *reinterpret_cast<const uint16_t*>(
+          grp + v_scale_at(D, 8 * h + 2 * t, D == 128 ? g : g >> 1));
+      if constexpr (!kPlain) {
+        // Tokens that no row sees may hold anything, NaN scales included.
+        const int j = tok + u * kGroup + 8 * h + 2 * t;
+        if (!((there >> u) & 1)) two = 0;
+        const int lo = bd.window < 0 ? 0 : bd.pos0 - bd.window;
+        if (j < lo || j >= bd.len) two &= 0xff00u;
+        if (j + 1 < lo || j + 1 >= bd.len) two &= 0x00ffu;
+      }
+      vs[h] = e4m3_to_f16(two);
+    }
+    values<D, NT>(grp, g, t, vs, pb, r.o);
+  }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
+    cache4_attn_kernel(Cache4AttnArgs a) {
   using S = Shape<D, NT>;
-  constexpr int kSteps = D / 16;  // 16-dim steps of Q K^T; also 16-dim tiles of O^T
-  constexpr int kWords = D / 32;  // 32-bit words of K codes per lane and token
+  constexpr int kSteps = D / 16;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kWarps][S::kStages];
-  __shared__ int there[kWarps][S::kStages];  // 0: the slot's group was not copied
+  __shared__ int copied[kWarps][S::kStages];  // bit u: group u of the slot
   __shared__ uint32_t cta_abort;
   __shared__ int sh_scan[kWarps], sh_first[4];
   __shared__ float sh_ml[kWarps][8][2];
 
+  launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
-  uint8_t* ring = smem + warp * S::kStages * group_bytes(D);
+  uint8_t* ring = smem + warp * S::kStages * S::kSlot;
   float* join = reinterpret_cast<float*>(smem + S::kRing);
   const WaitCtl ctl = {a.st, &cta_abort, a.timeout_ns};
   if (lane < S::kStages) mbar_init(&full[warp][lane], 1);
@@ -180,19 +411,13 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm) cache
     total += sh_scan[w];
   }
   const int before = upto - mine;
-  const long long W = (long long)total * items;
-  // No more blocks than units: every one that works has at least one unit.
-  const int blocks = (int)min((long long)gridDim.x, W);
-  if (blockIdx.x == 0) {  // for the joining kernel
-    int at = before;
-    for (int b = b0; b < b1; ++b) {
-      a.unit0[b] = at;
-      at += request_of(a, b).units;
-    }
-    if (tid == 0) a.unit0[a.B] = total;
+  const Shares shares((long long)total * items, gridDim.x);
+  if ((int)blockIdx.x >= shares.blocks) {
+    if (tid == 0) a.joins[blockIdx.x].x = -1;
+    return;
   }
-  if ((int)blockIdx.x >= blocks) return;
-  const long long u0 = W * blockIdx.x / blocks, u1 = W * (blockIdx.x + 1) / blocks;
+  const long long u0 = shares.first(blockIdx.x);
+  const int mine_units = (int)(shares.first(blockIdx.x + 1) - u0);
   if (u0 >= (long long)before * items && u0 < (long long)upto * items) {
     long long left = u0 - (long long)before * items;
     int b = b0;
@@ -212,27 +437,28 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm) cache
   use.rb = sh_first[1] - use.hk * a.row_blocks;
   use.unit = sh_first[2];
   use.r = request_of(a, use.b);
-  const int mine_units = (int)(u1 - u0);
 
-  // ---- the warp's own ring: slot n % kStages for the share's n-th unit.
-  // Each lane works out where one of the next 32 units' groups lies and
-  // issues that copy when its turn comes.
+  // ---- the warp's own ring, one slot per unit.  Each lane works out where
+  // one of the next 32 units' groups lie and issues those copies when its
+  // turn comes.
   Cursor load = use;
-  int put = 0, got = 0;                  // units passed by the loads and by the products
-  int turn = 0, turns = 0;               // place in the lanes' units
-  const uint8_t* src = nullptr;
-  bool dead = false;
+  int put = 0, put_slot = 0;  // units passed by the loads, and their slot
+  int turn = 0, turns = 0;    // place in the lanes' units
+  const uint8_t* src[kGroups];
   auto look_ahead = [&]() {
     turn = 0;
     turns = min(32, load.r.units - load.unit);
-    const int tok = load.r.lo + (load.unit + lane) * kUnit + warp * kGroup;
-    src = nullptr;
-    if (lane < turns && tok < load.r.len) {
-      const int page = __ldg(a.block_table + (size_t)load.b * a.M + (tok >> a.shift));
-      const int gpp_shift = a.shift - 4;
-      if (page >= 0 && page < a.pages)
-        src = a.cache + ((((size_t)page * a.Hkv + load.hk) << gpp_shift) +
-                         ((tok >> 4) & ((1 << gpp_shift) - 1))) * group_bytes(D);
+#pragma unroll
+    for (int u = 0; u < kGroups; ++u) {
+      const int tok = load.r.lo + (load.unit + lane) * kUnit + (warp * kGroups + u) * kGroup;
+      src[u] = nullptr;
+      if (lane < turns && tok < load.r.len) {
+        const int page = __ldg(a.block_table + (size_t)load.b * a.M + (tok >> a.shift));
+        const int gpp_shift = a.shift - 4;
+        if (page >= 0 && page < a.pages)
+          src[u] = a.cache + ((((size_t)page * a.Hkv + load.hk) << gpp_shift) +
+                              ((tok >> 4) & ((1 << gpp_shift) - 1))) * group_bytes(D);
+      }
     }
   };
   auto feed = [&]() {
@@ -242,23 +468,43 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm) cache
       look_ahead();
     }
     if (lane == turn) {
-      const int slot = put & (S::kStages - 1);
-      there[warp][slot] = src != nullptr;
-      if (src) {
-        mbar_arrive_expect_tx(&full[warp][slot], group_bytes(D));
-        bulk_load(ring + slot * group_bytes(D), src, group_bytes(D), &full[warp][slot]);
+      uint64_t* bar = &full[warp][put_slot];
+      uint8_t* dst = ring + put_slot * S::kSlot;
+      const int n = (src[0] ? 1 : 0) + (src[1] ? 1 : 0);
+      copied[warp][put_slot] = (src[0] ? 1 : 0) | (src[1] ? 2 : 0);
+      if (n) mbar_arrive_expect_tx(bar, n * group_bytes(D));
+      else mbar_arrive(bar);
+      if (n == 2 && src[1] == src[0] + group_bytes(D)) {
+        bulk_load(dst, src[0], S::kSlot, bar);
       } else {
-        mbar_arrive(&full[warp][slot]);
+        if (src[0]) bulk_load(dst, src[0], group_bytes(D), bar);
+        if (src[1]) bulk_load(dst + group_bytes(D), src[1], group_bytes(D), bar);
       }
     }
     ++turn;
     ++put;
+    if (++put_slot == S::kStages) put_slot = 0;
   };
   look_ahead();
   while (put < mine_units && put < S::kStages) feed();
 
-  int left = mine_units;
-  bool first_segment = true;
+  // What the joining kernel does for this block's first item, if that began
+  // in the block before: the request, item, last block, and first partial.
+  if (tid == 0) {
+    int4 j = make_int4(-1, 0, 0, 0);
+    if (use.unit > 0) {
+      const long long i0 = u0 - use.unit, before_us = shares.first(blockIdx.x - 1);
+      if (before_us <= i0)
+        j = make_int4(use.b, use.hk * a.row_blocks + use.rb,
+                      shares.block_of(i0 + use.r.units - 1),
+                      2 * (blockIdx.x - 1) + (before_us < i0 ? 1 : 0));
+    }
+    a.joins[blockIdx.x] = j;
+  }
+
+  int got = 0, got_slot = 0, left = mine_units;
+  uint32_t parity = 0;
+  bool first_segment = true, dead = false;
   while (left > 0) {
     // ---- one segment: units [use.unit, end) of one item
     const int end = min(use.r.units, use.unit + left);
@@ -266,23 +512,23 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm) cache
     const bool whole = use.unit == 0 && end == use.r.units;
     const int row0 = use.rb * S::kRows;
     const size_t q_row = ((size_t)use.b * a.Hkv + use.hk) * a.rows + row0;
+    const int pos0 = use.r.len - use.r.ql;  // position of the first new token
 
-    // Q fragments: row 8 nt + g, dims t D/4 + 0 .. D/4 - 1, scaled to f16.
-    uint32_t qf[NT][D / 8];
-    float rs[NT][2];  // rows 8 nt + 2t, + 1: power of two and scale to exponents of 2
+    Rows<D, NT> r;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const bool live = row0 + 8 * nt + g < a.rows;
-      const __nv_bfloat16* src = a.q + (q_row + 8 * nt + g) * D + t * (D / 4);
+      const __nv_bfloat16* q = a.q + (q_row + 8 * nt + g) * D + t * (D / 4);
       uint32_t big = 0;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         uint4 u = make_uint4(0, 0, 0, 0);
-        if (live) u = __ldg(reinterpret_cast<const uint4*>(src) + i);
-        qf[nt][4 * i] = u.x, qf[nt][4 * i + 1] = u.y, qf[nt][4 * i + 2] = u.z, qf[nt][4 * i + 3] = u.w;
+        if (live) u = __ldg(reinterpret_cast<const uint4*>(q) + i);
+        r.qf[nt][4 * i] = u.x, r.qf[nt][4 * i + 1] = u.y;
+        r.qf[nt][4 * i + 2] = u.z, r.qf[nt][4 * i + 3] = u.w;
       }
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) big = __vmaxu2(big, qf[nt][i] & 0x7fff7fffu);
+      for (int i = 0; i < D / 8; ++i) big = __vmaxu2(big, r.qf[nt][i] & 0x7fff7fffu);
       big = max(big & 0xffffu, big >> 16);
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
@@ -293,194 +539,54 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm) cache
       const float back = __uint_as_float((uint32_t)(e - 8) << 23) * a.scale_log2;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
-        qf[nt][i] = f16x2(__uint_as_float(qf[nt][i] << 16) * down,
-                          __uint_as_float(qf[nt][i] & 0xffff0000u) * down);
-      // (Not zero: a masked score, minus infinity, is multiplied with it.)
-      rs[nt][0] = fmaxf(__shfl_sync(0xffffffffu, back, 8 * t), 1.2e-38f);
-      rs[nt][1] = fmaxf(__shfl_sync(0xffffffffu, back, 8 * t + 4), 1.2e-38f);
-    }
-
-    // Keys that a row sees: [row_lo, row_hi).
-    int row_hi[NT][2], row_lo[NT][2];
-    const int pos0 = use.r.len - use.r.ql;  // position of the first new token
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+        r.qf[nt][i] = f16x2(__uint_as_float(r.qf[nt][i] << 16) * down,
+                            __uint_as_float(r.qf[nt][i] & 0xffff0000u) * down);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int pos = pos0 + (row0 + 8 * nt + 2 * t + i) % a.T;
-        row_hi[nt][i] = min(pos + 1, use.r.len);
-        row_lo[nt][i] = a.window < 0 ? 0 : max(0, pos - a.window);
+        // (Not zero: a masked score, minus infinity, is multiplied with it.)
+        r.rs[nt][i] = fmaxf(__shfl_sync(0xffffffffu, back, 8 * t + 4 * i), 1.2e-38f);
+        r.m[nt][i] = kNoMax;
+        r.l[nt][i] = 0.f;
       }
-    // Groups within [plain_lo, plain_hi) are seen whole by every row.
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+        r.o[i][nt][0] = r.o[i][nt][1] = r.o[i][nt][2] = r.o[i][nt][3] = 0.f;
+    }
+    const Bounds bd = {row0, a.T, pos0, use.r.len, a.window};
+    // Tokens within [plain_lo, plain_hi) are seen by every row.
     const int plain_hi = pos0 + 1, plain_lo = a.window < 0 ? 0 : use.r.len - 1 - a.window;
 
-    // m: the row's maximum less kUp, in powers of two: weights are 2^(s - m).
-    float o[kSteps][NT][4], m[NT][2], l[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
-      m[nt][0] = m[nt][1] = kNoMax;
-      l[nt][0] = l[nt][1] = 0.f;
-    }
-
     for (int un = dead ? end : use.unit; un < end; ++un) {
-      const int slot = got & (S::kStages - 1), tok = use.r.lo + un * kUnit + warp * kGroup;
-      if (!wait_bar_warp(&full[warp][slot], (got / S::kStages) & 1, ctl, 0x511)) {
+      if (!wait_bar_warp(&full[warp][got_slot], parity, ctl, 0x511)) {
         dead = true;
         break;
       }
-      const uint8_t* grp = ring + slot * group_bytes(D);
-      if (there[warp][slot]) {
-        // ---- S^T = K Q^T: tokens g and g + 8 of the group, rows 2t and 2t + 1
-        float s[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-        uint32_t kc[2][kWords], ks[2][D / 64];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint8_t* kp = grp + k_code_at(D, g + 8 * h, t * (D / 8));
-          const uint8_t* sp = grp + k_scale_at(D, g + 8 * h, t * (D / 64));
-          if constexpr (D == 128) {
-            const uint4 u = *reinterpret_cast<const uint4*>(kp);
-            kc[h][0] = u.x, kc[h][1] = u.y, kc[h][2] = u.z, kc[h][3] = u.w;
-            const uint32_t two = e4m3_to_f16(*reinterpret_cast<const uint16_t*>(sp));
-            ks[h][0] = __byte_perm(two, 0, 0x1010);
-            ks[h][1] = __byte_perm(two, 0, 0x3232);
-          } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(kp);
-            kc[h][0] = u.x, kc[h][1] = u.y;
-            ks[h][0] = __byte_perm(e4m3_to_f16(*sp), 0, 0x1010);
-          }
-        }
-#pragma unroll
-        for (int w = 0; w < kWords; ++w) {
-          uint32_t x[4], y[4];
-          e2m1_to_f16(kc[0][w], x);
-          e2m1_to_f16(kc[1][w], y);
-          const uint32_t s0 = ks[0][w / 2], s1 = ks[1][w / 2];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], s0), y[i] = mul2(y[i], s1);
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const uint32_t f[4] = {x[2 * hh], y[2 * hh], x[2 * hh + 1], y[2 * hh + 1]};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma(s[nt], f, qf[nt][4 * w + 2 * hh], qf[nt][4 * w + 2 * hh + 1]);
-          }
-        }
-
-        // ---- softmax weights
-        const bool plain = tok >= plain_lo && tok + kGroup <= plain_hi;
-        float p[NT][4], top = -INFINITY;  // exponents, then weights
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            p[nt][i] = fmaf(s[nt][i], rs[nt][i & 1], -m[nt][i & 1]);
-            if (!plain) {
-              const int j = tok + g + 8 * (i >> 1);
-              if (j >= row_hi[nt][i & 1] || j < row_lo[nt][i & 1]) p[nt][i] = s[nt][i] = -INFINITY;
-            }
-            top = fmaxf(top, p[nt][i]);
-          }
-        }
-        if (__any_sync(0xffffffffu, top > kUp + kSlack)) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              // (rs > 0: a score of minus infinity stays one.)
-              float mx = fmaxf(s[nt][i], s[nt][i + 2]) * rs[nt][i];
-#pragma unroll
-              for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-              mx = fmaxf(mx - kUp, m[nt][i]);
-              const float f = ex2(m[nt][i] - mx);
-              m[nt][i] = mx;
-              l[nt][i] *= f;
-#pragma unroll
-              for (int dt = 0; dt < kSteps; ++dt) o[dt][nt][i] *= f, o[dt][nt][i + 2] *= f;
-              p[nt][i] = fmaf(s[nt][i], rs[nt][i], -mx);
-              p[nt][i + 2] = fmaf(s[nt][i + 2], rs[nt][i], -mx);
-            }
-        }
-        uint32_t pb[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) p[nt][i] = ex2(p[nt][i]);
-          l[nt][0] += p[nt][0] + p[nt][2];
-          l[nt][1] += p[nt][1] + p[nt][3];
-          pb[nt][0] = transpose8x8(f16x2(p[nt][0], p[nt][1]));
-          pb[nt][1] = transpose8x8(f16x2(p[nt][2], p[nt][3]));
-        }
-
-        // ---- O^T += V^T P^T
-        uint32_t vs[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t two = *reinterpret_cast<const uint16_t*>(
-              grp + v_scale_at(D, 8 * h + 2 * t, D == 128 ? g : g >> 1));
-          if (!plain) {
-            // Tokens that no row sees may hold anything, NaN scales included.
-            const int j = tok + 8 * h + 2 * t, lo = a.window < 0 ? 0 : pos0 - a.window;
-            if (j < lo || j >= use.r.len) two &= 0xff00u;
-            if (j + 1 < lo || j + 1 >= use.r.len) two &= 0x00ffu;
-          }
-          vs[h] = e4m3_to_f16(two);
-        }
-        constexpr int kVWords = D / 64;  // words of one token's eighth
-        uint32_t vc[2][2][kVWords];      // [half][token parity][word]
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint8_t* vp = grp + v_code_at(D, 8 * h + 2 * t, g);
-          if constexpr (D == 128) {
-            const uint4 u = *reinterpret_cast<const uint4*>(vp);
-            vc[h][0][0] = u.x, vc[h][0][1] = u.y, vc[h][1][0] = u.z, vc[h][1][1] = u.w;
-          } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(vp);
-            vc[h][0][0] = u.x, vc[h][1][0] = u.y;
-          }
-        }
-#pragma unroll
-        for (int w = 0; w < kVWords; ++w) {
-          // Bytes of the two tokens' codes of one dim: even dims, odd dims.
-          uint32_t ev[2][4], od[2][4];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t x = vc[h][0][w], y = vc[h][1][w];
-            constexpr uint32_t kLow = 0x0f0f0f0fu;
-            e2m1_to_f16((x & kLow) | ((y << 4) & ~kLow), ev[h]);
-            e2m1_to_f16(((x >> 4) & kLow) | (y & ~kLow), od[h]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) ev[h][i] = mul2(ev[h][i], vs[h]), od[h][i] = mul2(od[h][i], vs[h]);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t f[4] = {ev[0][i], od[0][i], ev[1][i], od[1][i]};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma(o[4 * w + i][nt], f, pb[nt][0], pb[nt][1]);
-          }
-        }
-      }
+      const uint8_t* slot = ring + got_slot * S::kSlot;
+      const int tok = use.r.lo + un * kUnit + warp * kGroups * kGroup;
+      const int there = copied[warp][got_slot];
+      if (there == 3 && tok >= plain_lo && tok + kGroups * kGroup <= plain_hi)
+        use_slot<D, NT, true>(r, slot, tok, there, bd, g, t);
+      else if (there)
+        use_slot<D, NT, false>(r, slot, tok, there, bd, g, t);
       __syncwarp();  // every lane has read the slot
       ++got;
+      if (++got_slot == S::kStages) got_slot = 0, parity ^= 1;
       if (put < mine_units) feed();
     }
 
     // ---- join the warps, eight rows at a time
-    const int slot = 2 * blockIdx.x + (first_segment ? 0 : 1);
+    const int part_slot = 2 * blockIdx.x + (first_segment ? 0 : 1);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], x);
+        for (int x = 4; x < 32; x <<= 1) r.l[nt][i] += __shfl_xor_sync(0xffffffffu, r.l[nt][i], x);
       }
       __syncthreads();  // the buffer's last readers are done
       if (g == 0) {
-        sh_ml[warp][2 * t][0] = m[nt][0], sh_ml[warp][2 * t][1] = l[nt][0];
-        sh_ml[warp][2 * t + 1][0] = m[nt][1], sh_ml[warp][2 * t + 1][1] = l[nt][1];
+        sh_ml[warp][2 * t][0] = r.m[nt][0], sh_ml[warp][2 * t][1] = r.l[nt][0];
+        sh_ml[warp][2 * t + 1][0] = r.m[nt][1], sh_ml[warp][2 * t + 1][1] = r.l[nt][1];
       }
       // Lane (g, t) holds dims g D/8 + 0 .. D/8 - 1 of rows 2t and 2t + 1.
 #pragma unroll
@@ -489,7 +595,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm) cache
 #pragma unroll
         for (int dt = 0; dt < kSteps; dt += 2)
           *reinterpret_cast<float4*>(dst + 2 * dt) =
-              make_float4(o[dt][nt][i], o[dt][nt][i + 2], o[dt + 1][nt][i], o[dt + 1][nt][i + 2]);
+              make_float4(r.o[dt][nt][i], r.o[dt][nt][i + 2], r.o[dt + 1][nt][i], r.o[dt + 1][nt][i + 2]);
       }
       __syncthreads();
       const int row = tid >> 4, c = tid & 15;  // 16 threads a row
@@ -501,10 +607,10 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm) cache
         f[w] = ex2(sh_ml[w][row][0] - mx);
         sum += f[w] * sh_ml[w][row][1];
       }
-      const int r = row0 + 8 * nt + row;
-      const bool live = r < a.rows && r % a.T < use.r.ql;
+      const int rr = row0 + 8 * nt + row;
+      const bool live = rr < a.rows && rr % a.T < use.r.ql;
       const float inv = sum > 0.f || sum != sum ? a.v_scale / sum : 0.f;
-      float* part = a.part + ((size_t)slot * S::kRows + 8 * nt + row) * S::kPartRow;
+      const Partial part = partial_of<D, NT>(a, part_slot, 8 * nt + row);
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -515,8 +621,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm) cache
           acc[0] += f[w] * v.x, acc[1] += f[w] * v.y, acc[2] += f[w] * v.z, acc[3] += f[w] * v.w;
         }
         if (!whole) {
-          *reinterpret_cast<float2*>(part + 64 * i + 4 * c) = make_float2(acc[0], acc[1]);
-          *reinterpret_cast<float2*>(part + 64 * i + 4 * c + 2) = make_float2(acc[2], acc[3]);
+          *reinterpret_cast<float4*>(part.o + 64 * i + 4 * c) =
+              make_float4(acc[0], acc[1], acc[2], acc[3]);
         } else if (live) {
           __nv_bfloat162 lo = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
           __nv_bfloat162 hi = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
@@ -525,11 +631,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm) cache
         }
       }
       if (c == 0) {
-        if (!whole) {
-          *reinterpret_cast<float2*>(part + D) = make_float2(mx, sum);
-        } else if (live) {
-          a.lse[q_row + 8 * nt + row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
-        }
+        if (!whole) *part.ml = make_float2(mx, sum);
+        else if (live) a.lse[q_row + 8 * nt + row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
       }
     }
     left -= seg;
@@ -538,51 +641,73 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm) cache
     first_segment = false;
   }
   // A stopping block lets its copies land before it leaves.
-  for (; got < put; ++got)
-    drain_bar(&full[warp][got & (S::kStages - 1)], (got / S::kStages) & 1, a.timeout_ns);
+  for (; got < put; ++got) {
+    drain_bar(&full[warp][got_slot], parity, a.timeout_ns);
+    if (++got_slot == S::kStages) got_slot = 0, parity ^= 1;
+  }
 }
 
 // Joins the partial results of an item that lies in several blocks' shares,
-// in block order.  One block per row of an item, one thread per dim.
+// in block order.  One block per row; the item's parts are dealt to its
+// warps, and a lane takes D / 32 dims.
 template <int D, int NT>
-__global__ void __launch_bounds__(D) cache4_join_kernel(Cache4AttnArgs a, int grid) {
+__global__ void __launch_bounds__(kWarps * 32) cache4_join_kernel(Cache4AttnArgs a) {
   using S = Shape<D, NT>;
-  const int items = a.Hkv * a.row_blocks;
-  const int row_in = blockIdx.y;
-  const long long total = (long long)a.unit0[a.B] * items;
-  const int blocks = (int)min((long long)grid, total);
-  for (long long it = blockIdx.x; it < (long long)a.B * items; it += gridDim.x) {
-    const int b = (int)(it / items), item = (int)(it - (long long)b * items);
-    const int hk = item / a.row_blocks, r = (item - hk * a.row_blocks) * S::kRows + row_in;
-    const int first = a.unit0[b], units = a.unit0[b + 1] - first;
-    if (units == 0 || r >= a.rows) continue;
-    const long long i0 = (long long)first * items + (long long)item * units, i1 = i0 + units;
-    // The block of unit u is the c with c W / C <= u < (c + 1) W / C.
-    const int c0 = (int)(((i0 + 1) * blocks - 1) / total), c1 = (int)((i1 * blocks - 1) / total);
-    if (c0 == c1) continue;
-    const int n = a.q_lens ? a.q_lens[b] : a.T;
-    if (r % a.T >= (n > a.T ? a.T : n)) continue;
-    // In its first block the item is the second segment unless it starts there.
-    const int slot0 = 2 * c0 + (total * c0 / blocks < i0 ? 1 : 0);
-    auto row_of = [&](int c) {
-      return a.part + ((size_t)(c == c0 ? slot0 : 2 * c) * S::kRows + row_in) * S::kPartRow;
-    };
-    float mx = kNoMax;
-    for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, row_of(c)[D]);
-    float acc = 0.f, sum = 0.f;
+  constexpr int kDims = D / 32;
+  __shared__ float sh_o[kWarps][D], sh_m[kWarps], sh_l[kWarps];
+  wait_for_primary();
+  const int4 j = a.joins[blockIdx.x];
+  if (j.x < 0) return;
+  const int b = j.x, hk = j.y / a.row_blocks, row = blockIdx.y;
+  const int r = (j.y - hk * a.row_blocks) * S::kRows + row;
+  const int n = a.q_lens ? a.q_lens[b] : a.T;
+  if (r >= a.rows || r % a.T >= min(n, a.T)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int parts = j.z - (int)blockIdx.x + 2;
+  auto part = [&](int k) {
+    return partial_of<D, NT>(a, k == 0 ? j.w : 2 * ((int)blockIdx.x + k - 1), row);
+  };
+  float mx = kNoMax;
+  for (int k = threadIdx.x; k < parts; k += kWarps * 32) mx = fmaxf(mx, part(k).ml->x);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+  if (lane == 0) sh_m[warp] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sh_m[w]);
+  float acc[kDims], sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kDims; ++i) acc[i] = 0.f;
 #pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      const float* p = row_of(c);
-      const float f = ex2(p[D] - mx);
-      sum += f * p[D + 1];
-      acc += f * p[threadIdx.x];
+  for (int k = warp; k < parts; k += kWarps) {
+    const Partial p = part(k);
+    const float2 ml = *p.ml;
+    const float f = ex2(ml.x - mx);
+    sum += f * ml.y;
+    if constexpr (D == 128) {
+      const float4 v = reinterpret_cast<const float4*>(p.o)[lane];
+      acc[0] += f * v.x, acc[1] += f * v.y, acc[2] += f * v.z, acc[3] += f * v.w;
+    } else {
+      const float2 v = reinterpret_cast<const float2*>(p.o)[lane];
+      acc[0] += f * v.x, acc[1] += f * v.y;
     }
-    const size_t q_row = ((size_t)b * a.Hkv + hk) * a.rows + r;
-    const float inv = sum > 0.f || sum != sum ? a.v_scale / sum : 0.f;
-    a.o[q_row * D + threadIdx.x] = __float2bfloat16_rn(acc * inv);
-    if (threadIdx.x == 0)
-      a.lse[q_row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
   }
+#pragma unroll
+  for (int i = 0; i < kDims; ++i) sh_o[warp][lane * kDims + i] = acc[i];
+  if (lane == 0) sh_l[warp] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) sum += sh_l[w];
+  const float inv = sum > 0.f || sum != sum ? a.v_scale / sum : 0.f;
+  const size_t q_row = ((size_t)b * a.Hkv + hk) * a.rows + r;
+  if (threadIdx.x < D) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += sh_o[w][threadIdx.x];
+    a.o[q_row * D + threadIdx.x] = __float2bfloat16_rn(v * inv);
+  }
+  if (threadIdx.x == 0) a.lse[q_row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
 template <int D, int NT>
@@ -595,10 +720,17 @@ cudaError_t run(const Cache4AttnArgs& a, int sm_count, cudaStream_t stream) {
   if (blocks > kC4MaxBlocks) blocks = kC4MaxBlocks;
   kernel<<<blocks, kWarps * 32, S::kSmem, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const long long items = (long long)a.B * a.Hkv * a.row_blocks;
-  const dim3 grid((unsigned)(items < 65536 ? items : 65536), S::kRows);
-  cache4_join_kernel<D, NT><<<grid, D, 0, stream>>>(a, blocks);
-  return cudaGetLastError();
+  // The join's launch overlaps the kernel's work; it waits on the device.
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, S::kRows);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache4_join_kernel<D, NT>, a);
 }
 
 }  // namespace

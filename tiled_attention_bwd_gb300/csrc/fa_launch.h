@@ -146,8 +146,10 @@ struct Cache4AttnArgs {
   const int* q_lens;        // [B] or null
   __nv_bfloat16* o;         // [B, H, T, d]
   float* lse;               // [B, H, T]
-  float* part;              // partial results (workspace)
-  int* unit0;               // [B + 1] first work unit of each request (workspace)
+  // Workspace: what the join does per block, and partial results.
+  int4* joins;              // [kC4MaxBlocks]
+  float* part;              // [2 kC4MaxBlocks][item rows][d]
+  float2* part_ml;          // [2 kC4MaxBlocks][item rows]
   int B, Hkv, T, M, pages;
   int rows;                 // H / Hkv * T: rows of one key/value head
   int row_blocks;
@@ -158,7 +160,7 @@ struct Cache4AttnArgs {
   DevState* st;
   uint64_t timeout_ns;
 };
-// Rows of one work item: 8, 16 or 32.
+// Query rows of one work item: 8 or 16.
 int cache4_attn_rows(int rows);
 cudaError_t launch_cache4_attn(const Cache4AttnArgs& a, int d, int sm_count,
                                cudaStream_t stream);

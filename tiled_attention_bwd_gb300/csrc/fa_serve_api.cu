@@ -246,8 +246,9 @@ size_t fa_cache4_attn_workspace_size(int B, int H, int Hkv, int T, int d) {
   if (head_dim(d) != FA_OK || B <= 0 || H <= 0 || T <= 0 || Hkv <= 0 || H % Hkv != 0) return 0;
   if ((long long)B * H * T > INT_MAX) return 0;
   const int rows = fa::cache4_attn_rows(H / Hkv * T);
-  return align_up(((size_t)B + 1) * sizeof(int)) +
-         align_up((size_t)fa::kC4MaxBlocks * 2 * rows * (d + 2) * sizeof(float));
+  return align_up(fa::kC4MaxBlocks * sizeof(int4)) +
+         align_up((size_t)fa::kC4MaxBlocks * 2 * rows * d * sizeof(float)) +
+         (size_t)fa::kC4MaxBlocks * 2 * rows * sizeof(float2);
 }
 
 fa_status fa_cache4_attn(const void* q, const void* cache, const int* block_table,
@@ -284,9 +285,10 @@ fa_status fa_cache4_attn(const void* q, const void* cache, const int* block_tabl
   a.q_lens = q_lens;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
-  a.unit0 = static_cast<int*>(workspace);
-  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                    align_up(((size_t)B + 1) * sizeof(int)));
+  char* ws = static_cast<char*>(workspace);
+  a.joins = reinterpret_cast<int4*>(ws);
+  ws += align_up(fa::kC4MaxBlocks * sizeof(int4));
+  a.part = reinterpret_cast<float*>(ws);
   a.B = B;
   a.Hkv = Hkv;
   a.T = T;
@@ -294,6 +296,8 @@ fa_status fa_cache4_attn(const void* q, const void* cache, const int* block_tabl
   a.pages = pages;
   a.rows = H / Hkv * T;
   const int rows = fa::cache4_attn_rows(a.rows);
+  ws += align_up((size_t)fa::kC4MaxBlocks * 2 * rows * d * sizeof(float));
+  a.part_ml = reinterpret_cast<float2*>(ws);
   a.row_blocks = (a.rows + rows - 1) / rows;
   a.shift = shift;
   a.window = window < 0 ? -1 : window;

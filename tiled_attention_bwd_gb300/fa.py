@@ -514,64 +514,94 @@ def fa_bwd_noalloc(q, k, v, o, lse, dout, causal: bool, scale: float, dq,
     return dq, dk, dv
 
 
-def _check_same(device, dtype, **tensors):
-    """Contiguous tensors of one type on one device (None passes)."""
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("%s must be a torch.Tensor" % name)
-        if t.dtype != dtype or t.device != device or not t.is_contiguous():
-            raise ValueError("%s must be a contiguous %s tensor on %s"
-                             % (name, dtype, device))
+# ---- norm with rotation, and the 4-bit cache.  A decode step makes several
+# of these calls per layer, each a few microseconds of GPU time, so their
+# checks are one pass of comparisons per tensor and the device context is
+# entered only where it is not the current one.
 
-
-def _check_shape(name, t, shape):
-    if t is not None and t.shape != shape:
+def _want(name, t, dtype, device, shape):
+    """A contiguous tensor of this type, device and shape, or an error."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype \
+            and t.device == device and t.shape == shape and t.is_contiguous():
+        return
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s"
                          % (name, tuple(t.shape), tuple(shape)))
+    raise ValueError("%s must be a contiguous %s tensor on %s"
+                     % (name, dtype, device))
 
 
-def _rope_checks(qkv, H, Hkv, rope, positions, q_weight, k_weight):
-    """Checks of the arguments that the norm with rotation and its backward
-    share; returns the C arguments from qkv to the weights' type, and the
-    sizes."""
-    H, Hkv = int(H), int(Hkv)
-    if not isinstance(qkv, torch.Tensor):
-        raise TypeError("qkv must be a torch.Tensor")
-    if qkv.dtype != torch.bfloat16 or not qkv.is_cuda or qkv.dim() != 4 \
-            or H < 0 or Hkv < 0 or qkv.shape[2] != H + 2 * Hkv:
-        raise ValueError("qkv must be a bf16 CUDA tensor [B,N,H+2*Hkv,d]")
-    B, N, heads, d = qkv.shape
-    sb, sn = _token_strides("qkv", qkv)
-    dev = qkv.device
-    if not isinstance(rope, torch.Tensor) or rope.dim() != 2:
-        raise ValueError("rope must be an fp32 tensor [positions, rot]")
-    _check_same(dev, torch.float32, rope=rope)
-    _check_same(dev, torch.int32, positions=positions)
-    _check_shape("positions", positions, (B, N))
-    if (q_weight is None) != (k_weight is None):
-        raise ValueError("q_weight and k_weight come together")
-    bf16 = 0
-    if q_weight is not None:
-        bf16 = int(q_weight.dtype == torch.bfloat16)
-        _check_same(dev, torch.bfloat16 if bf16 else torch.float32,
-                    q_weight=q_weight, k_weight=k_weight)
-        _check_shape("q_weight", q_weight, (d,))
-        _check_shape("k_weight", k_weight, (d,))
-    args = (_ptr(qkv), sb, sn, _ptr(rope), rope.shape[0], rope.shape[1],
-            _ptr(positions), _ptr(q_weight), _ptr(k_weight), bf16)
-    return args, (B, N, H, Hkv, d)
+def _want_cuda(name, t, dtype, dims, what):
+    """A CUDA tensor of this type and number of axes (its device and sizes
+    are then the call's)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype is not dtype or not t.is_cuda or t.dim() != dims:
+        raise ValueError("%s must be a %s" % (name, what))
+
+
+def _output(name, t, shape, dtype, device):
+    """The caller's output tensor (checked) or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _want(name, t, dtype, device, shape)
+    return t
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(name, device, *args):
+    """Calls an entry point on the device's current stream."""
+    fn = getattr(load_library(), name)
+    index = device.index
+    if torch.cuda.current_device() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != FA_OK:
+        raise FAError(name, status)
 
 
 def _token_strides(name, t):
     """Strides of the batch and token axes of a [B,N,heads,d] tensor whose
     tokens are contiguous rows (axes of length one may have any)."""
     B, N, heads, d = t.shape
-    if t.numel() and ((d > 1 and t.stride(3) != 1)
-                      or (heads > 1 and t.stride(2) != d)):
+    sb, sn, sh, sd = t.stride()
+    if t.numel() and ((d > 1 and sd != 1) or (heads > 1 and sh != d)):
         raise ValueError("%s must have contiguous tokens [heads, d]" % name)
-    return (t.stride(0) if B > 1 else 0), (t.stride(1) if N > 1 else 0)
+    return (sb if B > 1 else 0), (sn if N > 1 else 0)
+
+
+def _rope_checks(qkv, H, Hkv, rope, positions, q_weight, k_weight):
+    """Checks of the arguments that the norm with rotation and its backward
+    share; returns the C arguments from qkv to the weights' type."""
+    _want_cuda("qkv", qkv, torch.bfloat16, 4, "bf16 CUDA tensor [B,N,heads,d]")
+    B, N, heads, d = qkv.shape
+    if H < 0 or Hkv < 0 or heads != H + 2 * Hkv:
+        raise ValueError("qkv has %d heads, expected H + 2 * Hkv = %d"
+                         % (heads, H + 2 * Hkv))
+    sb, sn = _token_strides("qkv", qkv)
+    dev = qkv.device
+    _want_cuda("rope", rope, torch.float32, 2, "fp32 CUDA tensor [positions, rot]")
+    rows, rot = rope.shape
+    _want("rope", rope, torch.float32, dev, (rows, rot))
+    if positions is not None:
+        _want("positions", positions, torch.int32, dev, (B, N))
+    bf16 = 0
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight come together")
+    if q_weight is not None:
+        bf16 = int(getattr(q_weight, "dtype", None) is torch.bfloat16)
+        dtype = torch.bfloat16 if bf16 else torch.float32
+        _want("q_weight", q_weight, dtype, dev, (d,))
+        _want("k_weight", k_weight, dtype, dev, (d,))
+    return (qkv.data_ptr(), sb, sn, rope.data_ptr(), rows, rot,
+            _address(positions), _address(q_weight), _address(k_weight), bf16)
 
 
 def fa_qk_norm_rope(qkv, H: int, Hkv: int, rope, positions=None, q_weight=None,
@@ -585,27 +615,15 @@ def fa_qk_norm_rope(qkv, H: int, Hkv: int, rope, positions=None, q_weight=None,
     then rot/2 sines a row; positions: int32 [B,N] or None (0 .. N-1);
     q_weight, k_weight: [d], bf16 or fp32, or None for no norm.
     Returns (q [B,H,N,d], k [B,Hkv,N,d], v [B,Hkv,N,d])."""
-    lib = load_library()
-    args, (B, N, H, Hkv, d) = _rope_checks(qkv, H, Hkv, rope, positions,
-                                           q_weight, k_weight)
+    args = _rope_checks(qkv, H, Hkv, rope, positions, q_weight, k_weight)
+    B, N, _, d = qkv.shape
     dev = qkv.device
     q = _output("q", q, (B, H, N, d), torch.bfloat16, dev)
     k = _output("k", k, (B, Hkv, N, d), torch.bfloat16, dev)
     v = _output("v", v, (B, Hkv, N, d), torch.bfloat16, dev)
-    with torch.cuda.device(dev):
-        _check("fa_qk_norm_rope", lib.fa_qk_norm_rope(
-            *args, float(eps), int(bool(interleaved)), _ptr(q), _ptr(k),
-            _ptr(v), B, N, H, Hkv, d, _stream_handle(dev)))
+    _launch("fa_qk_norm_rope", dev, *args, float(eps), 1 if interleaved else 0,
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), B, N, H, Hkv, d)
     return q, k, v
-
-
-def _output(name, t, shape, dtype, device):
-    """The caller's output tensor (checked) or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _check_same(device, dtype, **{name: t})
-    _check_shape(name, t, shape)
-    return t
 
 
 def fa_qk_norm_rope_bwd_workspace_size(d: int) -> int:
@@ -617,39 +635,36 @@ def fa_qk_norm_rope_bwd(qkv, H: int, Hkv: int, rope, dq, dk, dv,
                         eps: float = 1e-6, interleaved: bool = False,
                         dqkv=None, workspace=None):
     """Backward of fa_qk_norm_rope.  Returns (dqkv [B,N,H+2*Hkv,d] bf16,
-    dq_weight, dk_weight fp32 [d]; None without weights)."""
-    lib = load_library()
-    args, (B, N, H, Hkv, d) = _rope_checks(qkv, H, Hkv, rope, positions,
-                                           q_weight, k_weight)
+    dq_weight, dk_weight fp32 [d]; None without weights).  dqkv may be
+    qkv."""
+    args = _rope_checks(qkv, H, Hkv, rope, positions, q_weight, k_weight)
+    B, N, heads, d = qkv.shape
     dev = qkv.device
-    for name, t, h in (("dq", dq, H), ("dk", dk, Hkv), ("dv", dv, Hkv)):
-        if t is None:
-            raise TypeError("%s must be a torch.Tensor" % name)
-        _check_same(dev, torch.bfloat16, **{name: t})
-        _check_shape(name, t, (B, h, N, d))
+    _want("dq", dq, torch.bfloat16, dev, (B, H, N, d))
+    _want("dk", dk, torch.bfloat16, dev, (B, Hkv, N, d))
+    _want("dv", dv, torch.bfloat16, dev, (B, Hkv, N, d))
     if dqkv is None:
-        dqkv = torch.empty((B, N, H + 2 * Hkv, d), dtype=torch.bfloat16,
-                           device=dev)
-    elif not isinstance(dqkv, torch.Tensor) or dqkv.dtype != torch.bfloat16 \
-            or dqkv.device != dev or dqkv.shape != qkv.shape:
-        raise ValueError("dqkv must be a bf16 tensor of qkv's shape on %s"
-                         % dev)
+        dqkv = torch.empty((B, N, heads, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _want_cuda("dqkv", dqkv, torch.bfloat16, 4,
+                   "bf16 CUDA tensor [B,N,heads,d]")
+        if dqkv.shape != qkv.shape or dqkv.device != dev:
+            raise ValueError("dqkv must have qkv's shape and device")
     dsb, dsn = _token_strides("dqkv", dqkv)
     dqw = dkw = None
     size = 0
     if q_weight is not None:
-        both = torch.empty((2, d), dtype=torch.float32, device=dev)
-        dqw, dkw = both[0], both[1]
+        dqw = torch.empty(d, dtype=torch.float32, device=dev)
+        dkw = torch.empty(d, dtype=torch.float32, device=dev)
         if workspace is None:
             workspace = torch.empty(
                 max(fa_qk_norm_rope_bwd_workspace_size(d), 16),
                 dtype=torch.uint8, device=dev)
         size = workspace.numel() * workspace.element_size()
-    with torch.cuda.device(dev):
-        _check("fa_qk_norm_rope_bwd", lib.fa_qk_norm_rope_bwd(
-            *args, float(eps), int(bool(interleaved)), _ptr(dq), _ptr(dk),
-            _ptr(dv), _ptr(dqkv), dsb, dsn, _ptr(dqw), _ptr(dkw),
-            _ptr(workspace), size, B, N, H, Hkv, d, _stream_handle(dev)))
+    _launch("fa_qk_norm_rope_bwd", dev, *args, float(eps),
+            1 if interleaved else 0, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dqkv.data_ptr(), dsb,
+            dsn, _address(dqw), _address(dkw), _address(workspace), size, B, N,
+            H, Hkv, d)
     return dqkv, dqw, dkw
 
 
@@ -660,12 +675,11 @@ def fa_cache4_page_bytes(Hkv: int, page_size: int, d: int) -> int:
 def _cache_sizes(cache):
     """(pages, Hkv, page_size, d) of a 4-bit cache tensor, uint8
     [pages, Hkv, page_size / 16, 18 * d]."""
-    if not isinstance(cache, torch.Tensor) or cache.dtype != torch.uint8 \
-            or not cache.is_cuda or cache.dim() != 4 \
-            or cache.shape[3] % 18 or not cache.is_contiguous():
-        raise ValueError("cache must be a contiguous uint8 CUDA tensor "
-                         "[pages, Hkv, page_size / 16, 18 * d]")
+    _want_cuda("cache", cache, torch.uint8, 4,
+               "uint8 CUDA tensor [pages, Hkv, page_size / 16, 18 * d]")
     pages, Hkv, groups, width = cache.shape
+    if width % 18 or not cache.is_contiguous():
+        raise ValueError("cache must be contiguous, its last axis 18 * d")
     return pages, Hkv, 16 * groups, width // 18
 
 
@@ -677,36 +691,27 @@ def fa_cache4_plan(new_tokens, lens, block_table, free_list, free_count,
     [pages]; free_count: int32 [1].  lens, block_table, free_list and
     free_count are updated in place.  Returns (slots [R,T], positions [R,T],
     granted [R]), int32."""
-    lib = load_library()
-    if not isinstance(new_tokens, torch.Tensor) or not new_tokens.is_cuda:
-        raise ValueError("new_tokens must be an int32 CUDA tensor [R]")
-    dev, R, T = new_tokens.device, new_tokens.numel(), int(T)
-    _check_same(dev, torch.int32, new_tokens=new_tokens, lens=lens,
-                block_table=block_table, free_list=free_list,
-                free_count=free_count)
-    if lens is None or block_table is None or free_list is None \
-            or free_count is None:
-        raise TypeError("lens, block_table, free_list and free_count must be "
-                        "tensors")
-    if block_table.dim() != 2 or free_list.dim() != 1:
-        raise ValueError("block_table must be [R, max_blocks], free_list "
-                         "[pages]")
-    M = block_table.shape[1]
-    for name, t, shape in (("new_tokens", new_tokens, (R,)),
-                           ("lens", lens, (R,)),
-                           ("block_table", block_table, (R, M)),
-                           ("free_count", free_count, (1,))):
-        _check_shape(name, t, shape)
+    i32 = torch.int32
+    _want_cuda("new_tokens", new_tokens, i32, 1, "int32 CUDA tensor [R]")
+    _want_cuda("block_table", block_table, i32, 2,
+               "int32 CUDA tensor [R, max_blocks]")
+    _want_cuda("free_list", free_list, i32, 1, "int32 CUDA tensor [pages]")
+    dev = new_tokens.device
+    R, M, P = new_tokens.shape[0], block_table.shape[1], free_list.shape[0]
+    _want("new_tokens", new_tokens, i32, dev, (R,))
+    _want("lens", lens, i32, dev, (R,))
+    _want("block_table", block_table, i32, dev, (R, M))
+    _want("free_list", free_list, i32, dev, (P,))
+    _want("free_count", free_count, i32, dev, (1,))
     if T < 0:
         raise ValueError("T must not be negative")
-    slots = _output("slots", slots, (R, T), torch.int32, dev)
-    positions = _output("positions", positions, (R, T), torch.int32, dev)
-    granted = _output("granted", granted, (R,), torch.int32, dev)
-    with torch.cuda.device(dev):
-        _check("fa_cache4_plan", lib.fa_cache4_plan(
-            _ptr(new_tokens), _ptr(lens), _ptr(block_table), _ptr(free_list),
-            _ptr(free_count), _ptr(slots), _ptr(positions), _ptr(granted), R,
-            M, free_list.numel(), int(page_size), T, _stream_handle(dev)))
+    slots = _output("slots", slots, (R, T), i32, dev)
+    positions = _output("positions", positions, (R, T), i32, dev)
+    granted = _output("granted", granted, (R,), i32, dev)
+    _launch("fa_cache4_plan", dev, new_tokens.data_ptr(), lens.data_ptr(),
+            block_table.data_ptr(), free_list.data_ptr(),
+            free_count.data_ptr(), slots.data_ptr(), positions.data_ptr(),
+            granted.data_ptr(), R, M, P, page_size, T)
     return slots, positions, granted
 
 
@@ -714,28 +719,21 @@ def fa_cache4_append(k, v, cache, slots, k_scale: float = 1.0,
                      v_scale: float = 1.0, k_out=None, v_out=None):
     """Writes keys and values, bf16 [B,Hkv,N,d], to their slots (int32
     [B,N]) of the 4-bit cache.  k_out and v_out, if given, receive the values
-    that the cache then holds.  Returns the cache."""
-    lib = load_library()
+    that the cache then holds (they may be k and v).  Returns the cache."""
     pages, Hkv, page, d = _cache_sizes(cache)
+    _want_cuda("k", k, torch.bfloat16, 4, "bf16 CUDA tensor [B,Hkv,N,d]")
     dev = cache.device
-    _check_qkv("k", k)
     B, _, N, _ = k.shape
-    _check_same(dev, torch.bfloat16, k=k, v=v, k_out=k_out, v_out=v_out)
-    if v is None:
-        raise TypeError("v must be a torch.Tensor")
-    if (k_out is None) != (v_out is None):
-        raise ValueError("k_out and v_out come together")
-    for name, t in (("k", k), ("v", v), ("k_out", k_out), ("v_out", v_out)):
-        _check_shape(name, t, (B, Hkv, N, d))
-    if slots is None:
-        raise TypeError("slots must be a torch.Tensor")
-    _check_same(dev, torch.int32, slots=slots)
-    _check_shape("slots", slots, (B, N))
-    with torch.cuda.device(dev):
-        _check("fa_cache4_append", lib.fa_cache4_append(
-            _ptr(k), _ptr(v), _ptr(cache), _ptr(slots), float(k_scale),
-            float(v_scale), _ptr(k_out), _ptr(v_out), B, Hkv, N, d, pages,
-            page, _stream_handle(dev)))
+    shape = (B, Hkv, N, d)
+    _want("k", k, torch.bfloat16, dev, shape)
+    _want("v", v, torch.bfloat16, dev, shape)
+    _want("slots", slots, torch.int32, dev, (B, N))
+    if k_out is not None or v_out is not None:
+        _want("k_out", k_out, torch.bfloat16, dev, shape)
+        _want("v_out", v_out, torch.bfloat16, dev, shape)
+    _launch("fa_cache4_append", dev, k.data_ptr(), v.data_ptr(),
+            cache.data_ptr(), slots.data_ptr(), float(k_scale),
+            float(v_scale), _address(k_out), _address(v_out), B, Hkv, N, d, pages, page)
     return cache
 
 
@@ -752,33 +750,28 @@ def fa_cache4_attn(q, cache, block_table, seq_lens, scale: float, q_lens=None,
     [B, max_blocks]; seq_lens: int32 [B], the new tokens included; q_lens:
     int32 [B] new tokens of each request, or None for T.  Rows past a
     request's new tokens are left as they were.  Returns (O, LSE)."""
-    lib = load_library()
     pages, Hkv, page, d = _cache_sizes(cache)
-    _check_qkv("q", q)
+    _want_cuda("q", q, torch.bfloat16, 4, "bf16 CUDA tensor [B,H,T,d]")
+    _want_cuda("block_table", block_table, torch.int32, 2,
+               "int32 CUDA tensor [B, max_blocks]")
+    dev = cache.device
     B, H, T, _ = q.shape
-    dev = q.device
-    if cache.device != dev:
-        raise ValueError("cache is on %s, q on %s" % (cache.device, dev))
-    _check_shape("q", q, (B, H, T, d))
-    _check_seq_lens(seq_lens, B, dev)
-    if q_lens is not None:
-        _check_seq_lens(q_lens, B, dev)
-    if block_table is None or block_table.dim() != 2:
-        raise ValueError("block_table must be an int32 tensor [B, max_blocks]")
-    _check_same(dev, torch.int32, block_table=block_table)
     M = block_table.shape[1]
-    _check_shape("block_table", block_table, (B, M))
+    _want("q", q, torch.bfloat16, dev, (B, H, T, d))
+    _want("block_table", block_table, torch.int32, dev, (B, M))
+    _want("seq_lens", seq_lens, torch.int32, dev, (B,))
+    if q_lens is not None:
+        _want("q_lens", q_lens, torch.int32, dev, (B,))
     out = _output("out", out, (B, H, T, d), torch.bfloat16, dev)
     lse = _output("lse", lse, (B, H, T), torch.float32, dev)
     if workspace is None:
         workspace = torch.empty(
             max(fa_cache4_attn_workspace_size(B, H, Hkv, T, d), 256),
             dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
-        _check("fa_cache4_attn", lib.fa_cache4_attn(
-            _ptr(q), _ptr(cache), _ptr(block_table), _ptr(seq_lens),
-            _ptr(q_lens), _ptr(out), _ptr(lse), _ptr(workspace),
+    _launch("fa_cache4_attn", dev, q.data_ptr(), cache.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), _address(q_lens),
+            out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), B, H, Hkv, T, d, M,
             pages, page, int(window), float(scale), float(k_scale),
-            float(v_scale), _stream_handle(dev)))
+            float(v_scale))
     return out, lse
