@@ -270,7 +270,8 @@ fa_status fa_step_host(const void* q, const void* k, const void* v,
  *   q_weight, k_weight : in, [d], bf16 (weight_bf16 = 1) or fp32 (0); both
  *               NULL: no norm, only the rotation
  *   q, k, v   : out, bf16 [B,H,N,d], [B,Hkv,N,d], [B,Hkv,N,d]
- * eps >= 0.  An H of 0, or an Hkv of 0, is a call for the other heads alone.
+ * eps >= 0; H and Hkv are at most 8192, and an H of 0, or an Hkv of 0, is a
+ * call for the other heads alone.
  */
 fa_status fa_qk_norm_rope(const void* qkv, long long stride_b,
                           long long stride_n, const float* rope, int rope_rows,

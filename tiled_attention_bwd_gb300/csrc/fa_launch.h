@@ -81,7 +81,8 @@ struct BwdArgs {
 };
 
 // Norm of query and key heads with the rotation of positions, and backward.
-constexpr int kRopeMaxBlocks = 1024;  // of the backward: rows of `partial`
+constexpr int kRopeMaxHeads = 8192;   // of H and of Hkv
+constexpr int kRopeMaxBlocks = 1024;  // a token of 3 kRopeMaxHeads heads needs 768
 struct RopeArgs {
   const __nv_bfloat16* qkv;  // [B, N, H + 2 Hkv, d], strides below
   const float* table;        // [table_rows, rot]: rot/2 cosines, rot/2 sines
@@ -93,15 +94,15 @@ struct RopeArgs {
   const __nv_bfloat16 *dq, *dk, *dv;  // backward: in
   __nv_bfloat16* dqkv;             // backward: out
   float *dq_weight, *dk_weight;    // [d]
-  float* partial;                  // [kRopeMaxBlocks, d] (backward, with norm)
+  float* partial;                  // [kRopeMaxBlocks, 2 d] (backward, with norm)
   long long stride_b, stride_n;    // of qkv, in elements
   long long dstride_b, dstride_n;  // of dqkv
   int N, H, Hkv, rot, table_rows;
   int tokens;                      // B * N
   float eps;
-  // Set by the launcher: packs of heads per token and how blocks take them.
-  int packs, tokens_per_block, packs_per_block;
-  int split[2];
+  // Set by the launcher: packs of heads per token, tokens that the warps
+  // take at a time (and that step in entries and tokens), blocks.
+  int packs, step, step_b, step_n, blocks;
 };
 cudaError_t launch_rope_fwd(const RopeArgs& a, int d, bool interleaved,
                             bool norm, int sm_count, cudaStream_t stream);
@@ -120,7 +121,7 @@ struct PlanArgs {
   int* granted;           // [R]
   int R, M, P, T;
   int shift;              // log2 of the page size
-  int fused;              // set by the launcher: plan_kernel writes the slots
+  int wide;               // set by the launcher: slots, positions 16-byte aligned
 };
 cudaError_t launch_cache4_plan(PlanArgs a, cudaStream_t stream);
 

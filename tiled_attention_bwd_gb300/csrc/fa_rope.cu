@@ -127,19 +127,13 @@ __device__ __forceinline__ float sum_lanes(float v) {
   return v;
 }
 
-// A norm weight of either type.
-__device__ __forceinline__ float weight_at(const void* w, int is_bf16, int i) {
-  return is_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i])
-                 : static_cast<const float*>(w)[i];
-}
-
-__device__ __forceinline__ void load_weight(const float* w, const Lane& l, float* out) {
+// The lane's 16 norm weights, of either type (once per warp).
+__device__ __forceinline__ void load_weight(const void* w, int is_bf16, const Lane& l, float* out) {
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const float4* p = reinterpret_cast<const float4*>(w + (c ? l.c1 : l.c0));
-    const float4 u = p[0], v = p[1];
-    out[8 * c] = u.x, out[8 * c + 1] = u.y, out[8 * c + 2] = u.z, out[8 * c + 3] = u.w;
-    out[8 * c + 4] = v.x, out[8 * c + 5] = v.y, out[8 * c + 6] = v.z, out[8 * c + 7] = v.w;
+  for (int e = 0; e < 16; ++e) {
+    const int i = (e < 8 ? l.c0 : l.c1 - 8) + e;
+    out[e] = is_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i])
+                     : static_cast<const float*>(w)[i];
   }
 }
 
@@ -147,117 +141,149 @@ __device__ __forceinline__ int position_of(const RopeArgs& a, int token, int n) 
   return a.positions ? __ldg(a.positions + token) : n;
 }
 
-// Packs of one token: the query heads', then the key heads', then the value
-// heads'; a pack never mixes kinds.
-struct PackOf {
-  int kind;   // 0 query, 1 key, 2 value
-  int head;   // of this lane, within its kind
-  int heads;  // of the kind
+// A warp's work: one pack of heads (query heads' packs first, then key heads',
+// then value heads'; a pack never mixes kinds) of the tokens `first`, `first`
+// + step, ... .  With the pack fixed, its weights (and in the backward their
+// gradient's sums) stay in registers and the next token's place follows from
+// the last without a division.  Warps next to one another take one token's
+// packs, i.e. neighbouring memory.
+struct Task {
+  int kind;    // 0 query, 1 key, 2 value
+  int head;    // of this lane, within its kind
+  int heads;   // of the kind
+  int column;  // of this lane's head in a token of qkv
+  bool live;   // this lane has a head
 };
 template <int D>
-__device__ __forceinline__ PackOf pack_of(const RopeArgs& a, int p, const Lane& l) {
+__device__ __forceinline__ Task task_of(const RopeArgs& a, int pack, const Lane& l) {
   constexpr int kPack = 512 / D;
   const int nq = (a.H + kPack - 1) / kPack, nk = (a.Hkv + kPack - 1) / kPack;
-  PackOf r;
-  r.kind = p < nq ? 0 : (p < nq + nk ? 1 : 2);
-  r.head = (p - (r.kind == 0 ? 0 : (r.kind == 1 ? nq : nq + nk))) * kPack + l.sub;
-  r.heads = r.kind == 0 ? a.H : a.Hkv;
-  return r;
-}
-__device__ __forceinline__ int column_of(const RopeArgs& a, const PackOf& p) {
-  return (p.kind == 0 ? 0 : (p.kind == 1 ? a.H : a.H + a.Hkv)) + p.head;
+  Task k;
+  k.kind = pack < nq ? 0 : (pack < nq + nk ? 1 : 2);
+  k.head = (pack - (k.kind == 0 ? 0 : (k.kind == 1 ? nq : nq + nk))) * kPack + l.sub;
+  k.heads = k.kind == 0 ? a.H : a.Hkv;
+  k.column = (k.kind == 0 ? 0 : (k.kind == 1 ? a.H : a.H + a.Hkv)) + k.head;
+  k.live = k.head < k.heads;
+  return k;
 }
 
-// One block: `tokens_per_block` tokens and the packs [first, first + count)
-// of each, one (token, pack) per warp at a time.
+// A place in the batch, stepped without division.
+struct Place {
+  int token, b, n;
+  __device__ __forceinline__ Place(const RopeArgs& a, int token_) : token(token_) {
+    b = token / a.N;
+    n = token - b * a.N;
+  }
+  __device__ __forceinline__ void advance(const RopeArgs& a) {
+    token += a.step;
+    b += a.step_b;
+    n += a.step_n;
+    if (n >= a.N) n -= a.N, ++b;
+  }
+};
+
+// Forward: bound by bytes, each read and written once.  The next token's row
+// and position are loaded before the present one is computed.
 template <int D, bool kInter, bool kNorm>
 __global__ void __launch_bounds__(kWarps * 32) rope_fwd_kernel(RopeArgs a) {
-  __shared__ __align__(16) float w_sh[2][D];
-  if (kNorm) {
-    for (int i = threadIdx.x; i < 2 * D; i += kWarps * 32)
-      w_sh[i / D][i % D] = weight_at(i < D ? a.q_weight : a.k_weight, a.weight_bf16, i % D);
-    __syncthreads();
-  }
   const Lane l = lane_of<D, kInter>(a.rot);
-  const int first = blockIdx.y * a.packs_per_block;
-  const int count = min(a.packs_per_block, a.packs - first);
-  const int t0 = blockIdx.x * a.tokens_per_block;
-  const int here = min(a.tokens_per_block, a.tokens - t0) * count;
-  for (int i = threadIdx.x >> 5; i < here; i += kWarps) {
-    const int token = t0 + i / count;
-    const PackOf p = pack_of<D>(a, first + i % count, l);
-    const bool live = p.head < p.heads;
-    const int b = token / a.N, n = token - b * a.N;
-    Raw raw = {};
-    if (live)
-      raw = load_row(a.qkv + b * a.stride_b + n * a.stride_n + (size_t)column_of(a, p) * D, l);
-    if (p.kind < 2) {
-      float x[16], cs[8], sn[8];
-      load_turn(a, l, position_of(a, token, n), cs, sn);
+  const int id = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const Task k = task_of<D>(a, id % a.packs, l);
+  if (id / a.packs >= a.step) return;  // more warps than whole tokens need
+  float w[16];
+  if (kNorm && k.kind < 2) load_weight(k.kind == 0 ? a.q_weight : a.k_weight, a.weight_bf16, l, w);
+  __nv_bfloat16* out = k.kind == 0 ? a.q : (k.kind == 1 ? a.k : a.v);
+  auto row_at = [&](const Place& p) {
+    Raw r = {};
+    if (k.live)
+      r = load_row(a.qkv + p.b * a.stride_b + p.n * a.stride_n + (size_t)k.column * D, l);
+    return r;
+  };
+  Place here(a, id / a.packs);
+  if (here.token >= a.tokens) return;
+  Raw raw = row_at(here);
+  int pos = position_of(a, here.token, here.n);
+  while (true) {
+    Place next = here;
+    const bool more = a.tokens - here.token > a.step;
+    next.advance(a);
+    float x[16], cs[8], sn[8];
+    if (k.kind < 2) load_turn(a, l, pos, cs, sn);
+    Raw ahead = {};
+    if (more) {
+      ahead = row_at(next);
+      pos = position_of(a, next.token, next.n);
+    }
+    if (k.kind < 2) {
       unpack(raw, x);
       if (kNorm) {
-        float ss = 0.f, w[16];
+        float ss = 0.f;
 #pragma unroll
         for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
         const float r = rsqrtf(sum_lanes<D>(ss) * (1.0f / D) + a.eps);
-        load_weight(w_sh[p.kind], l, w);
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] = x[e] * r * w[e];
       }
       if (l.turned) turn<kInter, false>(x, cs, sn);
       raw = pack(x);
     }
-    if (live) {
-      __nv_bfloat16* out = p.kind == 0 ? a.q : (p.kind == 1 ? a.k : a.v);
-      store_row(out + (((size_t)b * p.heads + p.head) * a.N + n) * D, l, raw);
-    }
+    if (k.live)
+      store_row(out + (((size_t)here.b * k.heads + k.head) * a.N + here.n) * D, l, raw);
+    if (!more) break;
+    here = next;
+    raw = ahead;
   }
 }
 
-// Backward.  Blocks take one kind of head each (block ranges [0, split[0])
-// queries, [split[0], split[1]) keys, the rest values), so that a lane keeps
-// one set of 16 partial sums of its weight's gradient over all its rows.
-// Block sums leave in fp32 and rope_dw_kernel adds them in block order: the
-// result does not depend on which block runs first.
+// Backward.  A lane sums its 16 dims of its weight's gradient over all its
+// rows; heads of a warp, warps of a block (by kind) and blocks follow in
+// that order, the last in rope_dw_kernel: the result does not depend on
+// which block runs first.
 template <int D, bool kInter, bool kNorm>
-__global__ void __launch_bounds__(kWarps * 32) rope_bwd_kernel(RopeArgs a) {
-  constexpr int kPack = 512 / D;
-  __shared__ __align__(16) float w_sh[D];
+__global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeArgs a) {
   __shared__ float sums[kWarps][D];
-  const int kind = (int)blockIdx.x < a.split[0] ? 0 : ((int)blockIdx.x < a.split[1] ? 1 : 2);
-  const int block0 = kind == 0 ? 0 : a.split[kind - 1];
-  const int blocks = (kind == 2 ? (int)gridDim.x : a.split[kind]) - block0;
-  if (kNorm && kind < 2) {
-    for (int i = threadIdx.x; i < D; i += kWarps * 32)
-      w_sh[i] = weight_at(kind == 0 ? a.q_weight : a.k_weight, a.weight_bf16, i);
-    __syncthreads();
-  }
+  __shared__ int kinds[kWarps];
   const Lane l = lane_of<D, kInter>(a.rot);
-  const int heads = kind == 0 ? a.H : a.Hkv;
-  const int column0 = kind == 0 ? 0 : (kind == 1 ? a.H : a.H + a.Hkv);
-  const unsigned packs = (heads + kPack - 1) / kPack;
-  const __nv_bfloat16* dz = kind == 0 ? a.dq : (kind == 1 ? a.dk : a.dv);
+  const int id = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const Task k = task_of<D>(a, id % a.packs, l);
+  const __nv_bfloat16* dz = k.kind == 0 ? a.dq : (k.kind == 1 ? a.dk : a.dv);
+  const bool norm = kNorm && k.kind < 2;
   float w[16], dw[16];
+  if (norm) load_weight(k.kind == 0 ? a.q_weight : a.k_weight, a.weight_bf16, l, w);
 #pragma unroll
   for (int e = 0; e < 16; ++e) dw[e] = 0.f;
-  if (kNorm && kind < 2) load_weight(w_sh, l, w);
-
-  const unsigned total = (unsigned)a.tokens * packs;
-  const unsigned step = blocks * kWarps;
-  for (unsigned i = (blockIdx.x - block0) * kWarps + (threadIdx.x >> 5); i < total; i += step) {
-    const int token = i / packs;
-    const int head = (i - token * packs) * kPack + l.sub;
-    const bool live = head < heads;
-    const int b = token / a.N, n = token - b * a.N;
-    Raw gx = {}, rx = {};
-    if (live) {
-      gx = load_row(dz + (((size_t)b * heads + head) * a.N + n) * D, l);
-      if (kNorm && kind < 2)
-        rx = load_row(a.qkv + b * a.stride_b + n * a.stride_n + (size_t)(column0 + head) * D, l);
+  auto dz_at = [&](const Place& p) {
+    Raw r = {};
+    if (k.live) r = load_row(dz + (((size_t)p.b * k.heads + k.head) * a.N + p.n) * D, l);
+    return r;
+  };
+  auto row_at = [&](const Place& p) {
+    Raw r = {};
+    if (norm && k.live)
+      r = load_row(a.qkv + p.b * a.stride_b + p.n * a.stride_n + (size_t)k.column * D, l);
+    return r;
+  };
+  Place here(a, id / a.packs);
+  // (Without tokens, a.N may be zero and `here` is not used.)
+  bool more = id / a.packs < a.step && here.token < a.tokens;
+  Raw gx = {}, rx = {};
+  int pos = 0;
+  if (more) {
+    gx = dz_at(here), rx = row_at(here);
+    pos = position_of(a, here.token, here.n);
+  }
+  while (more) {
+    Place next = here;
+    more = a.tokens - here.token > a.step;
+    next.advance(a);
+    float g[16], cs[8], sn[8];
+    if (k.kind < 2) load_turn(a, l, pos, cs, sn);
+    Raw ahead_g = {}, ahead_x = {};
+    if (more) {
+      ahead_g = dz_at(next), ahead_x = row_at(next);
+      pos = position_of(a, next.token, next.n);
     }
-    if (kind < 2) {
-      float g[16], cs[8], sn[8];
-      load_turn(a, l, position_of(a, token, n), cs, sn);
+    if (k.kind < 2) {
       unpack(gx, g);
       if (l.turned) turn<kInter, true>(g, cs, sn);
       if (kNorm) {
@@ -280,12 +306,13 @@ __global__ void __launch_bounds__(kWarps * 32) rope_bwd_kernel(RopeArgs a) {
       }
       gx = pack(g);
     }
-    if (live)
-      store_row(a.dqkv + b * a.dstride_b + n * a.dstride_n + (size_t)(column0 + head) * D, l, gx);
+    if (k.live)
+      store_row(a.dqkv + here.b * a.dstride_b + here.n * a.dstride_n + (size_t)k.column * D, l, gx);
+    here = next;
+    gx = ahead_g, rx = ahead_x;
   }
   if constexpr (kNorm) {
-    if (kind == 2) return;  // the block has one kind: all leave
-    // Heads of a pack, then warps of the block.
+    // Heads of a pack, then the block's warps of each kind.
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
 #pragma unroll
@@ -296,73 +323,80 @@ __global__ void __launch_bounds__(kWarps * 32) rope_bwd_kernel(RopeArgs a) {
       for (int e = 0; e < 16; ++e)
         sums[threadIdx.x >> 5][(e < 8 ? l.c0 : l.c1 - 8) + e] = dw[e];
     }
+    if ((threadIdx.x & 31) == 0) kinds[threadIdx.x >> 5] = k.kind;
     __syncthreads();
-    for (int i = threadIdx.x; i < D; i += kWarps * 32) {
+    for (int i = threadIdx.x; i < 2 * D; i += kWarps * 32) {
       float s = 0.f;
 #pragma unroll
-      for (int v = 0; v < kWarps; ++v) s += sums[v][i];
-      a.partial[(size_t)blockIdx.x * D + i] = s;
+      for (int v = 0; v < kWarps; ++v)
+        if (kinds[v] == i / D) s += sums[v][i % D];
+      a.partial[(size_t)blockIdx.x * 2 * D + i] = s;
     }
   }
 }
 
-// Weight gradients from the block sums: one warp of 32 rows x 32 columns per
-// block; kind 0 (queries) and 1 (keys) in blockIdx.y.
+// Weight gradients from the blocks' sums: 32 columns of the 2 D (queries',
+// then keys') per block, 32 rows at a time.
 template <int D>
 __global__ void __launch_bounds__(1024) rope_dw_kernel(RopeArgs a) {
   __shared__ float sums[32][33];
-  const int kind = blockIdx.y;
-  const int b0 = kind == 0 ? 0 : a.split[0], b1 = a.split[kind];
   const int col = blockIdx.x * 32 + threadIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float s = 0.f;
-  for (int i = b0 + threadIdx.y; i < b1; i += 32) s += a.partial[(size_t)i * D + col];
+#pragma unroll 8
+  for (int i = threadIdx.y; i < a.blocks; i += 32) s += a.partial[(size_t)i * 2 * D + col];
   sums[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   s = sums[threadIdx.x][threadIdx.y];
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-  if (threadIdx.x == 0) (kind == 0 ? a.dq_weight : a.dk_weight)[blockIdx.x * 32 + threadIdx.y] = s;
+  const int c = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0) (c < D ? a.dq_weight : a.dk_weight)[c % D] = s;
+}
+
+// Deals packs and tokens to warps: blocks for `resident` per SM, fewer if
+// there is less than one (token, pack) for each warp.
+template <int D>
+int deal(RopeArgs& a, int sm_count, int resident) {
+  constexpr int kPack = 512 / D;
+  a.packs = (a.H + kPack - 1) / kPack + 2 * ((a.Hkv + kPack - 1) / kPack);
+  const long long all = (long long)a.tokens * a.packs;
+  long long blocks = (all + kWarps - 1) / kWarps;
+  if (blocks > (long long)resident * sm_count) blocks = (long long)resident * sm_count;
+  if (blocks > kRopeMaxBlocks) blocks = kRopeMaxBlocks;
+  // At least one warp for every pack of a token.
+  const long long least = (a.packs + kWarps - 1) / kWarps;
+  if (blocks < least) blocks = least;
+  a.step = (int)(blocks * kWarps / (a.packs > 0 ? a.packs : 1));
+  a.step_b = a.N > 0 ? a.step / a.N : 0;
+  a.step_n = a.N > 0 ? a.step % a.N : 0;
+  a.blocks = (int)blocks;
+  return a.blocks;
 }
 
 template <int D, bool kInter, bool kNorm>
 cudaError_t fwd(RopeArgs a, int sm_count, cudaStream_t stream) {
-  constexpr int kPack = 512 / D;
-  a.packs = (a.H + kPack - 1) / kPack + 2 * ((a.Hkv + kPack - 1) / kPack);
-  // Few tokens: one pack per warp, spread over blocks.  Otherwise whole
-  // tokens, about four packs per warp.
-  const long long all = (long long)a.tokens * a.packs;
-  if (all < (long long)sm_count * kWarps * 16) {
-    a.tokens_per_block = 1;
-    a.packs_per_block = kWarps;
-  } else {
-    a.packs_per_block = a.packs;
-    a.tokens_per_block = (4 * kWarps + a.packs - 1) / a.packs;
-  }
-  const dim3 grid((a.tokens + a.tokens_per_block - 1) / a.tokens_per_block,
-                  (a.packs + a.packs_per_block - 1) / a.packs_per_block);
-  rope_fwd_kernel<D, kInter, kNorm><<<grid, kWarps * 32, 0, stream>>>(a);
+  const int blocks = deal<D>(a, sm_count, 4);
+  rope_fwd_kernel<D, kInter, kNorm><<<blocks, kWarps * 32, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
 template <int D, bool kInter, bool kNorm>
 cudaError_t bwd(RopeArgs a, int sm_count, cudaStream_t stream) {
-  constexpr int kPack = 512 / D;
-  const long long pq = (a.H + kPack - 1) / kPack, pk = (a.Hkv + kPack - 1) / kPack;
-  // Blocks in proportion to the packs of each kind, at least one each.
-  const long long all = a.tokens * (pq + 2 * pk);
-  long long grid = (all + kWarps - 1) / kWarps;
-  if (grid > 4LL * sm_count) grid = 4LL * sm_count;
-  if (grid > kRopeMaxBlocks) grid = kRopeMaxBlocks;
-  if (grid < 3) grid = 3;
-  long long k = grid * pk / (pq + 2 * pk);
-  if (k < 1) k = 1;
-  a.split[0] = (int)(grid - 2 * k);
-  a.split[1] = (int)(grid - k);
-  rope_bwd_kernel<D, kInter, kNorm><<<(int)grid, kWarps * 32, 0, stream>>>(a);
+  const int blocks = deal<D>(a, sm_count, 2);
+  if (blocks > 0) rope_bwd_kernel<D, kInter, kNorm><<<blocks, kWarps * 32, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !kNorm) return e;
-  rope_dw_kernel<D><<<dim3(D / 32, 2), dim3(32, 32), 0, stream>>>(a);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * D / 32);
+  cfg.blockDim = dim3(32, 32);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rope_dw_kernel<D>, a);
 }
 
 template <bool kBwd>

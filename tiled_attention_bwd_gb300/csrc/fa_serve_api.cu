@@ -34,7 +34,7 @@ fa_status check_rope(int B, int N, int H, int Hkv, int d, int rot, int table_row
   if (interleaved != 0 && interleaved != 1) return FA_ERR_INVALID_ARG;
   if ((qw == nullptr) != (kw == nullptr)) return FA_ERR_INVALID_ARG;
   if (!std::isfinite(eps) || !(eps >= 0.0f)) return FA_ERR_INVALID_ARG;
-  if (H > 65536 || Hkv > 65536) return FA_ERR_UNSUPPORTED;
+  if (H > fa::kRopeMaxHeads || Hkv > fa::kRopeMaxHeads) return FA_ERR_UNSUPPORTED;
   // Rows of one head and packs of heads are counted in 31 bits.
   if ((long long)B * N > INT_MAX || (long long)B * N * (H + 2LL * Hkv) > INT_MAX)
     return FA_ERR_UNSUPPORTED;
@@ -121,7 +121,7 @@ fa_status fa_qk_norm_rope(const void* qkv, long long stride_b, long long stride_
 }
 
 size_t fa_qk_norm_rope_bwd_workspace_size(int d) {
-  return d == 64 || d == 128 ? (size_t)fa::kRopeMaxBlocks * d * sizeof(float) : 0;
+  return d == 64 || d == 128 ? (size_t)fa::kRopeMaxBlocks * 2 * d * sizeof(float) : 0;
 }
 
 fa_status fa_qk_norm_rope_bwd(const void* qkv, long long stride_b, long long stride_n,
