@@ -31,29 +31,54 @@ struct Raw {  // a lane's 16 bf16 values
   uint4 c[2];
 };
 
-__device__ __forceinline__ void unpack(const Raw& r, float* f) {
+// Two fp32 values in one 64-bit register: Blackwell's packed fp32
+// instructions do both at once.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 un2(F2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float sum2(F2 v) {
+  const float2 f = un2(v);
+  return f.x + f.y;
+}
+
+__device__ __forceinline__ void unpack(const Raw& r, F2 (&x)[8]) {
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const uint32_t w[4] = {r.c[c].x, r.c[c].y, r.c[c].z, r.c[c].w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[8 * c + 2 * i] = __uint_as_float(w[i] << 16);
-      f[8 * c + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i)
+      x[4 * c + i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
 }
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&p);
+__device__ __forceinline__ uint32_t pack2(F2 v) {
+  const float2 f = un2(v);
+  const __nv_bfloat162 p = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t*>(&p);
 }
-
-__device__ __forceinline__ Raw pack(const float* f) {
+__device__ __forceinline__ Raw pack(const F2 (&x)[8]) {
   Raw r;
 #pragma unroll
   for (int c = 0; c < 2; ++c)
-    r.c[c] = make_uint4(pack2(f[8 * c], f[8 * c + 1]), pack2(f[8 * c + 2], f[8 * c + 3]),
-                        pack2(f[8 * c + 4], f[8 * c + 5]), pack2(f[8 * c + 6], f[8 * c + 7]));
+    r.c[c] = make_uint4(pack2(x[4 * c]), pack2(x[4 * c + 1]), pack2(x[4 * c + 2]), pack2(x[4 * c + 3]));
   return r;
 }
 
@@ -79,44 +104,91 @@ __device__ __forceinline__ Lane lane_of(int rot) {
   return a;
 }
 
-__device__ __forceinline__ Raw load_row(const __nv_bfloat16* row, const Lane& a) {
-  // Plain loads: the backward's output may be its input.
-  Raw r;
-  r.c[0] = *reinterpret_cast<const uint4*>(row + a.c0);
-  r.c[1] = *reinterpret_cast<const uint4*>(row + a.c1);
-  return r;
-}
 __device__ __forceinline__ void store_row(__nv_bfloat16* row, const Lane& a, const Raw& r) {
   *reinterpret_cast<uint4*>(row + a.c0) = r.c[0];
   *reinterpret_cast<uint4*>(row + a.c1) = r.c[1];
 }
 
-// The lane's 8 cosines and sines of position `pos` (the table's rows hold
-// rot/2 cosines, then rot/2 sines).  Positions are clamped to the table.
-__device__ __forceinline__ void load_turn(const RopeArgs& a, const Lane& l, int pos, float* cs,
-                                          float* sn) {
-  if (!l.turned) return;
-  pos = pos < 0 ? 0 : (pos >= a.table_rows ? a.table_rows - 1 : pos);
-  const float* row = a.table + (size_t)pos * a.rot + 8 * l.j;
-  const float4* c = reinterpret_cast<const float4*>(row);
-  const float4* s = reinterpret_cast<const float4*>(row + a.rot / 2);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const float4 u = __ldg(c + h), v = __ldg(s + h);
-    cs[4 * h] = u.x, cs[4 * h + 1] = u.y, cs[4 * h + 2] = u.z, cs[4 * h + 3] = u.w;
-    sn[4 * h] = v.x, sn[4 * h + 1] = v.y, sn[4 * h + 2] = v.z, sn[4 * h + 3] = v.w;
+// ---- A warp's ring of rows on their way from memory, in shared memory: the
+// loads in flight then cost no registers.  A lane copies its own two chunks
+// of each of kRows rows and reads them back itself; the rotation's row of
+// the table, 64 bytes per lane of a head, is copied once for all the warp's
+// heads.
+template <int D, int kRows>
+struct Ring {
+  static constexpr int kLanes = D / 16;
+  static constexpr int kTurn = kLanes * 64;
+  static constexpr int kStage = kRows * 1024 + kTurn;
+  uint8_t* base;  // this warp's
+  static __device__ __forceinline__ void copy16(uint8_t* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src)
+                 : "memory");
   }
-}
+  __device__ __forceinline__ void fetch_row(int stage, int which, const __nv_bfloat16* row,
+                                            const Lane& l) const {
+    uint8_t* at = base + stage * kStage + which * 1024 + (threadIdx.x & 31) * 16;
+    copy16(at, row + l.c0);
+    copy16(at + 512, row + l.c1);
+  }
+  __device__ __forceinline__ Raw row(int stage, int which) const {
+    const uint8_t* at = base + stage * kStage + which * 1024 + (threadIdx.x & 31) * 16;
+    Raw r;
+    r.c[0] = *reinterpret_cast<const uint4*>(at);
+    r.c[1] = *reinterpret_cast<const uint4*>(at + 512);
+    return r;
+  }
+  // The table's rows hold rot/2 cosines, then rot/2 sines.  Positions are
+  // clamped to the table.  Piece q of lane j: 4 cosines (q = 0, 1) or sines.
+  __device__ __forceinline__ void fetch_turn(int stage, const RopeArgs& a, const Lane& l,
+                                             int pos) const {
+    if (!l.turned || l.sub >= 4) return;
+    pos = pos < 0 ? 0 : (pos >= a.table_rows ? a.table_rows - 1 : pos);
+    const float* src = a.table + (size_t)pos * a.rot + 8 * l.j + (l.sub & 1) * 4 +
+                       (l.sub >> 1) * (a.rot / 2);
+    // (Through L1: the block's other warps are at the same token.)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(
+                         base + stage * kStage + kRows * 1024 + (l.sub * kLanes + l.j) * 16))),
+                 "l"(src)
+                 : "memory");
+  }
+  __device__ __forceinline__ void turn_of(int stage, const Lane& l, F2 (&cs)[4], F2 (&sn)[4]) const {
+    const uint8_t* at = base + stage * kStage + kRows * 1024 + l.j * 16;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(at + q * kLanes * 16);
+      F2* d = (q < 2 ? cs : sn) + (q & 1) * 2;
+      d[0] = u.x, d[1] = u.y;
+    }
+  }
+  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  template <int kLeft>
+  static __device__ __forceinline__ void wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+  }
+};
 
 // Rotates the lane's 8 pairs by the angle (kBack: by minus the angle).
 template <bool kInter, bool kBack>
-__device__ __forceinline__ void turn(float* y, const float* cs, const float* sn) {
+__device__ __forceinline__ void turn(F2 (&y)[8], const F2 (&cs)[4], const F2 (&sn)[4]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int p = kInter ? 2 * i : i, q = kInter ? 2 * i + 1 : i + 8;
-    const float u = y[p], v = y[q], s = kBack ? -sn[i] : sn[i];
-    y[p] = u * cs[i] - v * s;
-    y[q] = v * cs[i] + u * s;
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kInter) {  // pairs 2i and 2i + 1 are y[2i] and y[2i + 1]
+      const float2 c = un2(cs[i]), s = un2(sn[i]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float2 v = un2(y[2 * i + h]);
+        const float cc = h ? c.y : c.x, ss = (h ? s.y : s.x) * (kBack ? -1.f : 1.f);
+        y[2 * i + h] = fma2(f2(v.x, v.y), f2(cc, cc), mul2(f2(v.y, v.x), f2(-ss, ss)));
+      }
+    } else {  // pairs 2i and 2i + 1 are (y[i], y[i + 4]), both halves
+      const float2 s = un2(sn[i]);
+      const F2 minus = f2(-s.x, -s.y), u = y[i], v = y[i + 4];
+      y[i] = fma2(v, kBack ? sn[i] : minus, mul2(u, cs[i]));
+      y[i + 4] = fma2(u, kBack ? minus : sn[i], mul2(v, cs[i]));
+    }
   }
 }
 
@@ -128,13 +200,16 @@ __device__ __forceinline__ float sum_lanes(float v) {
 }
 
 // The lane's 16 norm weights, of either type (once per warp).
-__device__ __forceinline__ void load_weight(const void* w, int is_bf16, const Lane& l, float* out) {
+__device__ __forceinline__ void load_weight(const void* w, int is_bf16, const Lane& l, F2 (&out)[8]) {
+  float f[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     const int i = (e < 8 ? l.c0 : l.c1 - 8) + e;
-    out[e] = is_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i])
-                     : static_cast<const float*>(w)[i];
+    f[e] = is_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i])
+                   : static_cast<const float*>(w)[i];
   }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) out[e] = f2(f[2 * e], f[2 * e + 1]);
 }
 
 __device__ __forceinline__ int position_of(const RopeArgs& a, int token, int n) {
@@ -167,71 +242,96 @@ __device__ __forceinline__ Task task_of(const RopeArgs& a, int pack, const Lane&
   return k;
 }
 
-// A place in the batch, stepped without division.
+// A token of the batch, stepped without division; true where the step moves
+// on by one more batch entry than step_b.
 struct Place {
-  int token, b, n;
-  __device__ __forceinline__ Place(const RopeArgs& a, int token_) : token(token_) {
-    b = token / a.N;
-    n = token - b * a.N;
-  }
-  __device__ __forceinline__ void advance(const RopeArgs& a) {
+  int token, n;
+  __device__ __forceinline__ bool advance(const RopeArgs& a) {
     token += a.step;
-    b += a.step_b;
     n += a.step_n;
-    if (n >= a.N) n -= a.N, ++b;
+    if (n < a.N) return false;
+    n -= a.N;
+    return true;
   }
 };
+// The row of one head at a Place, stepped along with it.
+template <typename T>
+struct Walk {
+  T* at;
+  long long step, wrap;  // elements; wrap is added where advance() says so
+  // Strides of entries and tokens, in elements.
+  __device__ __forceinline__ Walk(const RopeArgs& a, T* base, long long sb, long long sn, int b, int n)
+      : at(base + b * sb + n * sn), step(a.step_b * sb + a.step_n * sn), wrap(sb - a.N * sn) {}
+  __device__ __forceinline__ void advance(bool w) { at += w ? step + wrap : step; }
+};
 
-// Forward: bound by bytes, each read and written once.  The next token's row
-// and position are loaded before the present one is computed.
+// Stages of the rings and blocks per SM.  Forward 4x4096 tokens of 64 + 16
+// heads: 4 stages x 3 blocks, see the launcher.
+constexpr int kFwdStages = 4, kBwdStages = 4;
+template <int D>
+constexpr int fwd_smem() { return kWarps * kFwdStages * Ring<D, 1>::kStage; }
+template <int D>
+constexpr int bwd_smem() { return kWarps * kBwdStages * Ring<D, 2>::kStage; }
+
+// Forward: bound by bytes, each read and written once.
 template <int D, bool kInter, bool kNorm>
-__global__ void __launch_bounds__(kWarps * 32) rope_fwd_kernel(RopeArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
+  using R = Ring<D, 1>;
+  extern __shared__ __align__(16) uint8_t smem[];
   const Lane l = lane_of<D, kInter>(a.rot);
-  const int id = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int warp = threadIdx.x >> 5, id = blockIdx.x * kWarps + warp;
   const Task k = task_of<D>(a, id % a.packs, l);
-  if (id / a.packs >= a.step) return;  // more warps than whole tokens need
-  float w[16];
-  if (kNorm && k.kind < 2) load_weight(k.kind == 0 ? a.q_weight : a.k_weight, a.weight_bf16, l, w);
-  __nv_bfloat16* out = k.kind == 0 ? a.q : (k.kind == 1 ? a.k : a.v);
-  auto row_at = [&](const Place& p) {
-    Raw r = {};
-    if (k.live)
-      r = load_row(a.qkv + p.b * a.stride_b + p.n * a.stride_n + (size_t)k.column * D, l);
-    return r;
-  };
-  Place here(a, id / a.packs);
-  if (here.token >= a.tokens) return;
-  Raw raw = row_at(here);
-  int pos = position_of(a, here.token, here.n);
-  while (true) {
-    Place next = here;
-    const bool more = a.tokens - here.token > a.step;
-    next.advance(a);
-    float x[16], cs[8], sn[8];
-    if (k.kind < 2) load_turn(a, l, pos, cs, sn);
-    Raw ahead = {};
-    if (more) {
-      ahead = row_at(next);
-      pos = position_of(a, next.token, next.n);
+  Place here = {id / a.packs, 0};
+  // (There may be more warps than whole tokens need.)
+  if (here.token >= a.step || here.token >= a.tokens) return;
+  const int b = here.token / a.N;
+  here.n = here.token - b * a.N;
+  const R ring = {smem + warp * kFwdStages * R::kStage};
+  const bool turns = k.kind < 2;
+  F2 w[8];
+  if (kNorm && turns) load_weight(k.kind == 0 ? a.q_weight : a.k_weight, a.weight_bf16, l, w);
+  Walk<const __nv_bfloat16> in(a, a.qkv + (size_t)k.column * D, a.stride_b, a.stride_n, b, here.n);
+  Walk<__nv_bfloat16> out(a, (k.kind == 0 ? a.q : (k.kind == 1 ? a.k : a.v)) + (size_t)k.head * a.N * D,
+                          (long long)k.heads * a.N * D, D, b, here.n);
+
+  Place ahead = here;  // next to be fetched, with its position
+  bool any = true;     // there is one
+  int pos = turns ? position_of(a, ahead.token, ahead.n) : 0;
+  auto fetch = [&](int stage) {
+    if (any) {
+      if (k.live) ring.fetch_row(stage, 0, in.at, l);
+      if (turns) ring.fetch_turn(stage, a, l, pos);
+      any = a.tokens - ahead.token > a.step;
+      in.advance(ahead.advance(a));
+      if (any && turns) pos = position_of(a, ahead.token, ahead.n);
     }
-    if (k.kind < 2) {
+    R::commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kFwdStages - 1; ++s) fetch(s);
+  for (int stage = 0;; stage = stage == kFwdStages - 1 ? 0 : stage + 1) {
+    R::template wait<kFwdStages - 2>();
+    __syncwarp();  // the table's pieces of other lanes; and all have read the last stage
+    Raw raw = ring.row(stage, 0);
+    F2 x[8], cs[4], sn[4];
+    if (turns && l.turned) ring.turn_of(stage, l, cs, sn);
+    fetch(stage == 0 ? kFwdStages - 1 : stage - 1);
+    if (turns) {
       unpack(raw, x);
       if (kNorm) {
-        float ss = 0.f;
+        F2 ss = mul2(x[0], x[0]);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
-        const float r = rsqrtf(sum_lanes<D>(ss) * (1.0f / D) + a.eps);
+        for (int e = 1; e < 8; ++e) ss = fma2(x[e], x[e], ss);
+        const float r = rsqrtf(sum_lanes<D>(sum2(ss)) * (1.0f / D) + a.eps);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = x[e] * r * w[e];
+        for (int e = 0; e < 8; ++e) x[e] = mul2(mul2(x[e], f2(r, r)), w[e]);
       }
       if (l.turned) turn<kInter, false>(x, cs, sn);
       raw = pack(x);
     }
-    if (k.live)
-      store_row(out + (((size_t)here.b * k.heads + k.head) * a.N + here.n) * D, l, raw);
-    if (!more) break;
-    here = next;
-    raw = ahead;
+    if (k.live) store_row(out.at, l, raw);
+    if (a.tokens - here.token <= a.step) break;
+    out.advance(here.advance(a));
   }
 }
 
@@ -241,89 +341,97 @@ __global__ void __launch_bounds__(kWarps * 32) rope_fwd_kernel(RopeArgs a) {
 // which block runs first.
 template <int D, bool kInter, bool kNorm>
 __global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeArgs a) {
+  using R = Ring<D, 2>;
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float sums[kWarps][D];
   __shared__ int kinds[kWarps];
   const Lane l = lane_of<D, kInter>(a.rot);
-  const int id = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int warp = threadIdx.x >> 5, id = blockIdx.x * kWarps + warp;
   const Task k = task_of<D>(a, id % a.packs, l);
-  const __nv_bfloat16* dz = k.kind == 0 ? a.dq : (k.kind == 1 ? a.dk : a.dv);
-  const bool norm = kNorm && k.kind < 2;
-  float w[16], dw[16];
+  const R ring = {smem + warp * kBwdStages * R::kStage};
+  const bool turns = k.kind < 2, norm = kNorm && turns;
+  F2 w[8], dw[8];
   if (norm) load_weight(k.kind == 0 ? a.q_weight : a.k_weight, a.weight_bf16, l, w);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) dw[e] = 0.f;
-  auto dz_at = [&](const Place& p) {
-    Raw r = {};
-    if (k.live) r = load_row(dz + (((size_t)p.b * k.heads + k.head) * a.N + p.n) * D, l);
-    return r;
-  };
-  auto row_at = [&](const Place& p) {
-    Raw r = {};
-    if (norm && k.live)
-      r = load_row(a.qkv + p.b * a.stride_b + p.n * a.stride_n + (size_t)k.column * D, l);
-    return r;
-  };
-  Place here(a, id / a.packs);
-  // (Without tokens, a.N may be zero and `here` is not used.)
-  bool more = id / a.packs < a.step && here.token < a.tokens;
-  Raw gx = {}, rx = {};
-  int pos = 0;
-  if (more) {
-    gx = dz_at(here), rx = row_at(here);
-    pos = position_of(a, here.token, here.n);
-  }
-  while (more) {
-    Place next = here;
-    more = a.tokens - here.token > a.step;
-    next.advance(a);
-    float g[16], cs[8], sn[8];
-    if (k.kind < 2) load_turn(a, l, pos, cs, sn);
-    Raw ahead_g = {}, ahead_x = {};
-    if (more) {
-      ahead_g = dz_at(next), ahead_x = row_at(next);
-      pos = position_of(a, next.token, next.n);
+  for (int e = 0; e < 8; ++e) dw[e] = 0;
+  Place here = {id / a.packs, 0};
+  bool more = here.token < a.step && here.token < a.tokens;
+  const int b = more ? here.token / a.N : 0;  // (without tokens N may be zero)
+  here.n = here.token - b * a.N;
+  Walk<const __nv_bfloat16> in(a, a.qkv + (size_t)k.column * D, a.stride_b, a.stride_n, b, here.n);
+  Walk<const __nv_bfloat16> dz(a, (k.kind == 0 ? a.dq : (k.kind == 1 ? a.dk : a.dv)) + (size_t)k.head * a.N * D,
+                               (long long)k.heads * a.N * D, D, b, here.n);
+  Walk<__nv_bfloat16> out(a, a.dqkv + (size_t)k.column * D, a.dstride_b, a.dstride_n, b, here.n);
+  Place ahead = here;
+  bool any = more;
+  int pos = any && turns ? position_of(a, ahead.token, ahead.n) : 0;
+  auto fetch = [&](int stage) {
+    if (any) {
+      if (k.live) {
+        ring.fetch_row(stage, 0, dz.at, l);
+        if (norm) ring.fetch_row(stage, 1, in.at, l);
+      }
+      if (turns) ring.fetch_turn(stage, a, l, pos);
+      any = a.tokens - ahead.token > a.step;
+      const bool wrap = ahead.advance(a);
+      dz.advance(wrap);
+      in.advance(wrap);
+      if (any && turns) pos = position_of(a, ahead.token, ahead.n);
     }
-    if (k.kind < 2) {
+    R::commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kBwdStages - 1; ++s) fetch(s);
+  for (int stage = 0; more; stage = stage == kBwdStages - 1 ? 0 : stage + 1) {
+    R::template wait<kBwdStages - 2>();
+    __syncwarp();  // the table's pieces of other lanes; and all have read the last stage
+    Raw gx = ring.row(stage, 0), rx = {};
+    if (norm && k.live) rx = ring.row(stage, 1);
+    F2 g[8], cs[4], sn[4];
+    if (turns && l.turned) ring.turn_of(stage, l, cs, sn);
+    fetch(stage == 0 ? kBwdStages - 1 : stage - 1);
+    if (turns) {
+      if (!k.live) gx = Raw{};  // (its lanes' sums of dw stay zero)
       unpack(gx, g);
       if (l.turned) turn<kInter, true>(g, cs, sn);
       if (kNorm) {
-        float x[16];
+        F2 x[8];
         unpack(rx, x);
-        float ss = 0.f, dot = 0.f;
+        F2 ss = mul2(x[0], x[0]), dot = 0;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
-        const float r = rsqrtf(sum_lanes<D>(ss) * (1.0f / D) + a.eps);
+        for (int e = 1; e < 8; ++e) ss = fma2(x[e], x[e], ss);
+        const float r = rsqrtf(sum_lanes<D>(sum2(ss)) * (1.0f / D) + a.eps);
+        const F2 r2 = f2(r, r);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          x[e] *= r;  // xh
-          dw[e] = fmaf(g[e], x[e], dw[e]);
-          g[e] *= w[e];
-          dot = fmaf(g[e], x[e], dot);
+        for (int e = 0; e < 8; ++e) {
+          x[e] = mul2(x[e], r2);  // xh
+          dw[e] = fma2(g[e], x[e], dw[e]);
+          g[e] = mul2(g[e], w[e]);
+          dot = fma2(g[e], x[e], dot);
         }
-        const float mean = sum_lanes<D>(dot) * (1.0f / D);
+        const float mean = -sum_lanes<D>(sum2(dot)) * (1.0f / D);
+        const F2 m2 = f2(mean, mean);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) g[e] = r * fmaf(-x[e], mean, g[e]);
+        for (int e = 0; e < 8; ++e) g[e] = mul2(r2, fma2(x[e], m2, g[e]));
       }
       gx = pack(g);
     }
-    if (k.live)
-      store_row(a.dqkv + here.b * a.dstride_b + here.n * a.dstride_n + (size_t)k.column * D, l, gx);
-    here = next;
-    gx = ahead_g, rx = ahead_x;
+    if (k.live) store_row(out.at, l, gx);
+    more = a.tokens - here.token > a.step;
+    out.advance(here.advance(a));
   }
+  R::template wait<0>();
   if constexpr (kNorm) {
     // Heads of a pack, then the block's warps of each kind.
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
+      const float2 pair = un2(dw[e / 2]);
+      float v = e & 1 ? pair.y : pair.x;
 #pragma unroll
-      for (int m = D / 16; m < 32; m <<= 1) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], m);
+      for (int m = D / 16; m < 32; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+      if (l.sub == 0) sums[warp][(e < 8 ? l.c0 : l.c1 - 8) + e] = v;
     }
-    if (l.sub == 0) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        sums[threadIdx.x >> 5][(e < 8 ? l.c0 : l.c1 - 8) + e] = dw[e];
-    }
-    if ((threadIdx.x & 31) == 0) kinds[threadIdx.x >> 5] = k.kind;
+    if ((threadIdx.x & 31) == 0) kinds[warp] = k.kind;
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * D; i += kWarps * 32) {
       float s = 0.f;
@@ -374,18 +482,28 @@ int deal(RopeArgs& a, int sm_count, int resident) {
   return a.blocks;
 }
 
+template <typename K>
+cudaError_t allow_smem(K* kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 template <int D, bool kInter, bool kNorm>
 cudaError_t fwd(RopeArgs a, int sm_count, cudaStream_t stream) {
-  const int blocks = deal<D>(a, sm_count, 4);
-  rope_fwd_kernel<D, kInter, kNorm><<<blocks, kWarps * 32, 0, stream>>>(a);
+  const int blocks = deal<D>(a, sm_count, 3);
+  cudaError_t e = allow_smem(rope_fwd_kernel<D, kInter, kNorm>, fwd_smem<D>());
+  if (e != cudaSuccess) return e;
+  rope_fwd_kernel<D, kInter, kNorm><<<blocks, kWarps * 32, fwd_smem<D>(), stream>>>(a);
   return cudaGetLastError();
 }
 
 template <int D, bool kInter, bool kNorm>
 cudaError_t bwd(RopeArgs a, int sm_count, cudaStream_t stream) {
   const int blocks = deal<D>(a, sm_count, 2);
-  if (blocks > 0) rope_bwd_kernel<D, kInter, kNorm><<<blocks, kWarps * 32, 0, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = allow_smem(rope_bwd_kernel<D, kInter, kNorm>, bwd_smem<D>());
+  if (e != cudaSuccess) return e;
+  if (blocks > 0)
+    rope_bwd_kernel<D, kInter, kNorm><<<blocks, kWarps * 32, bwd_smem<D>(), stream>>>(a);
+  e = cudaGetLastError();
   if (e != cudaSuccess || !kNorm) return e;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
