@@ -83,6 +83,10 @@ struct BwdArgs {
 // Norm of query and key heads with the rotation of positions, and backward.
 constexpr int kRopeMaxHeads = 8192;   // of H and of Hkv
 constexpr int kRopeMaxBlocks = 1024;  // a token of 3 kRopeMaxHeads heads needs 768
+struct RopeDeal {
+  int packs;                 // packs of heads of a token
+  int step, step_b, step_n;  // tokens taken at a time = step_b entries + step_n
+};
 struct RopeArgs {
   const __nv_bfloat16* qkv;  // [B, N, H + 2 Hkv, d], strides below
   const float* table;        // [table_rows, rot]: rot/2 cosines, rot/2 sines
@@ -100,9 +104,10 @@ struct RopeArgs {
   int N, H, Hkv, rot, table_rows;
   int tokens;                      // B * N
   float eps;
-  // Set by the launcher: packs of heads per token, tokens that the warps
-  // take at a time (and that step in entries and tokens), blocks.
-  int packs, step, step_b, step_n, blocks;
+  // Set by the launcher: how warps take the packs of a token, all together
+  // (forward) or query and key heads first, then value heads (backward).
+  RopeDeal all, grad, value;
+  int blocks;
 };
 cudaError_t launch_rope_fwd(const RopeArgs& a, int d, bool interleaved,
                             bool norm, int sm_count, cudaStream_t stream);

@@ -13,12 +13,13 @@
 // A head's row of d bf16 values lies in d/16 lanes of 16 values each, so a
 // warp takes 32 / (d/16) heads of one token at a time ("pack"): 4 at d = 128,
 // 8 at d = 64.  The two 8-value chunks of a lane are chosen such that both
-// members of every rotated pair are in one lane: chunks j and j + rot/16 for
-// pairs (i, i + rot/2), chunks 2j and 2j + 1 for pairs (2i, 2i + 1).  The
-// norm's sums are the only exchange between lanes.  Everything is computed
+// members of every rotated pair are in one lane; the norm's sums are the only
+// exchange between lanes.  Everything is computed
 // in fp32 and rounded to bf16 once, at the store.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "fa_launch.h"
 
@@ -82,12 +83,13 @@ __device__ __forceinline__ Raw pack(const F2 (&x)[8]) {
   return r;
 }
 
-// Where a lane's chunks lie in its head's row.
+// Where a lane's chunks lie in its head's row.  Neighbouring lanes take
+// neighbouring chunks, so that a warp's access covers whole sectors.
 struct Lane {
-  int j;        // lane within the head
-  int sub;      // head within the pack
-  int c0, c1;   // element offsets of the two chunks
-  bool turned;  // both chunks are rotated (else neither is)
+  int j;            // lane within the head
+  int sub;          // head within the pack
+  int c0, c1;       // element offsets of the two chunks
+  bool turn0, turn1;  // rotated (paired with one another, unless interleaved)
 };
 
 template <int D, bool kInter>
@@ -97,10 +99,17 @@ __device__ __forceinline__ Lane lane_of(int rot) {
   Lane a;
   a.j = l % kLanes;
   a.sub = l / kLanes;
-  a.turned = a.j < rot / 16;
-  const bool split = !kInter && a.turned;
-  a.c0 = 8 * (split ? a.j : 2 * a.j);
-  a.c1 = 8 * (split ? a.j + rot / 16 : 2 * a.j + 1);
+  if (kInter) {
+    a.c0 = 8 * a.j;
+    a.c1 = 8 * (a.j + kLanes);
+    a.turn0 = a.c0 < rot;
+    a.turn1 = a.c1 < rot;
+  } else {
+    const int pairs = rot / 16;  // lanes with a rotated pair of chunks
+    a.turn0 = a.turn1 = a.j < pairs;
+    a.c0 = 8 * (a.turn0 ? a.j : a.j + pairs);
+    a.c1 = 8 * (a.turn0 ? a.j + pairs : a.j + kLanes);
+  }
   return a;
 }
 
@@ -140,13 +149,16 @@ struct Ring {
     return r;
   }
   // The table's rows hold rot/2 cosines, then rot/2 sines.  Positions are
-  // clamped to the table.  Piece q of lane j: 4 cosines (q = 0, 1) or sines.
+  // clamped to the table.  Piece q of lane j: 4 cosines (q = 0, 1) or sines
+  // (2, 3), of the pair's first or second four angles, or (interleaved) of
+  // its first or second chunk's.
+  template <bool kInter>
   __device__ __forceinline__ void fetch_turn(int stage, const RopeArgs& a, const Lane& l,
                                              int pos) const {
-    if (!l.turned || l.sub >= 4) return;
+    if (l.sub >= 4 || !(l.sub & 1 ? l.turn1 : l.turn0)) return;
     pos = pos < 0 ? 0 : (pos >= a.table_rows ? a.table_rows - 1 : pos);
-    const float* src = a.table + (size_t)pos * a.rot + 8 * l.j + (l.sub & 1) * 4 +
-                       (l.sub >> 1) * (a.rot / 2);
+    const int first = kInter ? 4 * (l.j + (l.sub & 1) * kLanes) : 8 * l.j + 4 * (l.sub & 1);
+    const float* src = a.table + (size_t)pos * a.rot + first + (l.sub >> 1) * (a.rot / 2);
     // (Through L1: the block's other warps are at the same token.)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(
                      static_cast<uint32_t>(__cvta_generic_to_shared(
@@ -172,9 +184,11 @@ struct Ring {
 
 // Rotates the lane's 8 pairs by the angle (kBack: by minus the angle).
 template <bool kInter, bool kBack>
-__device__ __forceinline__ void turn(F2 (&y)[8], const F2 (&cs)[4], const F2 (&sn)[4]) {
+__device__ __forceinline__ void turn(F2 (&y)[8], const F2 (&cs)[4], const F2 (&sn)[4],
+                                     const Lane& l) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    if (!(i < 2 ? l.turn0 : l.turn1)) continue;
     if constexpr (kInter) {  // pairs 2i and 2i + 1 are y[2i] and y[2i + 1]
       const float2 c = un2(cs[i]), s = un2(sn[i]);
 #pragma unroll
@@ -246,11 +260,11 @@ __device__ __forceinline__ Task task_of(const RopeArgs& a, int pack, const Lane&
 // on by one more batch entry than step_b.
 struct Place {
   int token, n;
-  __device__ __forceinline__ bool advance(const RopeArgs& a) {
-    token += a.step;
-    n += a.step_n;
-    if (n < a.N) return false;
-    n -= a.N;
+  __device__ __forceinline__ bool advance(const RopeDeal& s, int N) {
+    token += s.step;
+    n += s.step_n;
+    if (n < N) return false;
+    n -= N;
     return true;
   }
 };
@@ -260,14 +274,14 @@ struct Walk {
   T* at;
   long long step, wrap;  // elements; wrap is added where advance() says so
   // Strides of entries and tokens, in elements.
-  __device__ __forceinline__ Walk(const RopeArgs& a, T* base, long long sb, long long sn, int b, int n)
-      : at(base + b * sb + n * sn), step(a.step_b * sb + a.step_n * sn), wrap(sb - a.N * sn) {}
+  __device__ __forceinline__ Walk(const RopeDeal& s, int N, T* base, long long sb, long long sn,
+                                  int b, int n)
+      : at(base + b * sb + n * sn), step(s.step_b * sb + s.step_n * sn), wrap(sb - N * sn) {}
   __device__ __forceinline__ void advance(bool w) { at += w ? step + wrap : step; }
 };
 
-// Stages of the rings and blocks per SM.  Forward 4x4096 tokens of 64 + 16
-// heads: 4 stages x 3 blocks, see the launcher.
-constexpr int kFwdStages = 4, kBwdStages = 4;
+// Stages of the rings (3 to 6 of them measure the same within 2%).
+constexpr int kFwdStages = 3, kBwdStages = 3;
 template <int D>
 constexpr int fwd_smem() { return kWarps * kFwdStages * Ring<D, 1>::kStage; }
 template <int D>
@@ -280,18 +294,18 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   const Lane l = lane_of<D, kInter>(a.rot);
   const int warp = threadIdx.x >> 5, id = blockIdx.x * kWarps + warp;
-  const Task k = task_of<D>(a, id % a.packs, l);
-  Place here = {id / a.packs, 0};
+  const Task k = task_of<D>(a, id % a.all.packs, l);
+  Place here = {id / a.all.packs, 0};
   // (There may be more warps than whole tokens need.)
-  if (here.token >= a.step || here.token >= a.tokens) return;
+  if (here.token >= a.all.step || here.token >= a.tokens) return;
   const int b = here.token / a.N;
   here.n = here.token - b * a.N;
   const R ring = {smem + warp * kFwdStages * R::kStage};
   const bool turns = k.kind < 2;
   F2 w[8];
   if (kNorm && turns) load_weight(k.kind == 0 ? a.q_weight : a.k_weight, a.weight_bf16, l, w);
-  Walk<const __nv_bfloat16> in(a, a.qkv + (size_t)k.column * D, a.stride_b, a.stride_n, b, here.n);
-  Walk<__nv_bfloat16> out(a, (k.kind == 0 ? a.q : (k.kind == 1 ? a.k : a.v)) + (size_t)k.head * a.N * D,
+  Walk<const __nv_bfloat16> in(a.all, a.N, a.qkv + (size_t)k.column * D, a.stride_b, a.stride_n, b, here.n);
+  Walk<__nv_bfloat16> out(a.all, a.N, (k.kind == 0 ? a.q : (k.kind == 1 ? a.k : a.v)) + (size_t)k.head * a.N * D,
                           (long long)k.heads * a.N * D, D, b, here.n);
 
   Place ahead = here;  // next to be fetched, with its position
@@ -300,9 +314,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
   auto fetch = [&](int stage) {
     if (any) {
       if (k.live) ring.fetch_row(stage, 0, in.at, l);
-      if (turns) ring.fetch_turn(stage, a, l, pos);
-      any = a.tokens - ahead.token > a.step;
-      in.advance(ahead.advance(a));
+      if (turns) ring.template fetch_turn<kInter>(stage, a, l, pos);
+      any = a.tokens - ahead.token > a.all.step;
+      in.advance(ahead.advance(a.all, a.N));
       if (any && turns) pos = position_of(a, ahead.token, ahead.n);
     }
     R::commit();
@@ -314,7 +328,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
     __syncwarp();  // the table's pieces of other lanes; and all have read the last stage
     Raw raw = ring.row(stage, 0);
     F2 x[8], cs[4], sn[4];
-    if (turns && l.turned) ring.turn_of(stage, l, cs, sn);
+    if (turns) ring.turn_of(stage, l, cs, sn);
     fetch(stage == 0 ? kFwdStages - 1 : stage - 1);
     if (turns) {
       unpack(raw, x);
@@ -326,102 +340,116 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = mul2(mul2(x[e], f2(r, r)), w[e]);
       }
-      if (l.turned) turn<kInter, false>(x, cs, sn);
+      turn<kInter, false>(x, cs, sn, l);
       raw = pack(x);
     }
     if (k.live) store_row(out.at, l, raw);
-    if (a.tokens - here.token <= a.step) break;
-    out.advance(here.advance(a));
+    if (a.tokens - here.token <= a.all.step) break;
+    out.advance(here.advance(a.all, a.N));
   }
 }
 
-// Backward.  A lane sums its 16 dims of its weight's gradient over all its
-// rows; heads of a warp, warps of a block (by kind) and blocks follow in
-// that order, the last in rope_dw_kernel: the result does not depend on
-// which block runs first.
+// Backward.  The warps first take the query and key packs together, then the
+// value packs, which are only moved: all warps do the same work.  A lane sums
+// its 16 dims of its weight's gradient over all its rows; heads of a warp,
+// warps of a block (by kind) and blocks follow in that order, the last in
+// rope_dw_kernel: the result does not depend on which block runs first.
 template <int D, bool kInter, bool kNorm>
 __global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeArgs a) {
   using R = Ring<D, 2>;
+  constexpr int kPack = 512 / D;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float sums[kWarps][D];
   __shared__ int kinds[kWarps];
   const Lane l = lane_of<D, kInter>(a.rot);
   const int warp = threadIdx.x >> 5, id = blockIdx.x * kWarps + warp;
-  const Task k = task_of<D>(a, id % a.packs, l);
   const R ring = {smem + warp * kBwdStages * R::kStage};
-  const bool turns = k.kind < 2, norm = kNorm && turns;
-  F2 w[8], dw[8];
-  if (norm) load_weight(k.kind == 0 ? a.q_weight : a.k_weight, a.weight_bf16, l, w);
+  F2 dw[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) dw[e] = 0;
-  Place here = {id / a.packs, 0};
-  bool more = here.token < a.step && here.token < a.tokens;
-  const int b = more ? here.token / a.N : 0;  // (without tokens N may be zero)
-  here.n = here.token - b * a.N;
-  Walk<const __nv_bfloat16> in(a, a.qkv + (size_t)k.column * D, a.stride_b, a.stride_n, b, here.n);
-  Walk<const __nv_bfloat16> dz(a, (k.kind == 0 ? a.dq : (k.kind == 1 ? a.dk : a.dv)) + (size_t)k.head * a.N * D,
-                               (long long)k.heads * a.N * D, D, b, here.n);
-  Walk<__nv_bfloat16> out(a, a.dqkv + (size_t)k.column * D, a.dstride_b, a.dstride_n, b, here.n);
-  Place ahead = here;
-  bool any = more;
-  int pos = any && turns ? position_of(a, ahead.token, ahead.n) : 0;
-  auto fetch = [&](int stage) {
-    if (any) {
-      if (k.live) {
-        ring.fetch_row(stage, 0, dz.at, l);
-        if (norm) ring.fetch_row(stage, 1, in.at, l);
-      }
-      if (turns) ring.fetch_turn(stage, a, l, pos);
-      any = a.tokens - ahead.token > a.step;
-      const bool wrap = ahead.advance(a);
-      dz.advance(wrap);
-      in.advance(wrap);
-      if (any && turns) pos = position_of(a, ahead.token, ahead.n);
-    }
-    R::commit();
-  };
-#pragma unroll
-  for (int s = 0; s < kBwdStages - 1; ++s) fetch(s);
-  for (int stage = 0; more; stage = stage == kBwdStages - 1 ? 0 : stage + 1) {
-    R::template wait<kBwdStages - 2>();
-    __syncwarp();  // the table's pieces of other lanes; and all have read the last stage
-    Raw gx = ring.row(stage, 0), rx = {};
-    if (norm && k.live) rx = ring.row(stage, 1);
-    F2 g[8], cs[4], sn[4];
-    if (turns && l.turned) ring.turn_of(stage, l, cs, sn);
-    fetch(stage == 0 ? kBwdStages - 1 : stage - 1);
-    if (turns) {
-      if (!k.live) gx = Raw{};  // (its lanes' sums of dw stay zero)
-      unpack(gx, g);
-      if (l.turned) turn<kInter, true>(g, cs, sn);
-      if (kNorm) {
-        F2 x[8];
-        unpack(rx, x);
-        F2 ss = mul2(x[0], x[0]), dot = 0;
-#pragma unroll
-        for (int e = 1; e < 8; ++e) ss = fma2(x[e], x[e], ss);
-        const float r = rsqrtf(sum_lanes<D>(sum2(ss)) * (1.0f / D) + a.eps);
-        const F2 r2 = f2(r, r);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] = mul2(x[e], r2);  // xh
-          dw[e] = fma2(g[e], x[e], dw[e]);
-          g[e] = mul2(g[e], w[e]);
-          dot = fma2(g[e], x[e], dot);
+
+  // One of the two deals; kGrad: query and key heads.
+  auto take = [&](auto grad, const RopeDeal& s, int first_pack) {
+    constexpr bool kGrad = decltype(grad)::value, kX = kGrad && kNorm;
+    if (s.packs == 0) return;
+    const Task k = task_of<D>(a, first_pack + id % s.packs, l);
+    Place here = {id / s.packs, 0};
+    // (There may be more warps than whole tokens need.)
+    if (here.token >= s.step || here.token >= a.tokens) return;
+    const int b = here.token / a.N;
+    here.n = here.token - b * a.N;
+    F2 w[8];
+    if (kX) load_weight(k.kind == 0 ? a.q_weight : a.k_weight, a.weight_bf16, l, w);
+    Walk<const __nv_bfloat16> in(s, a.N, a.qkv + (size_t)k.column * D, a.stride_b, a.stride_n, b, here.n);
+    Walk<const __nv_bfloat16> dz(s, a.N,
+                                 (k.kind == 0 ? a.dq : (k.kind == 1 ? a.dk : a.dv)) + (size_t)k.head * a.N * D,
+                                 (long long)k.heads * a.N * D, D, b, here.n);
+    Walk<__nv_bfloat16> out(s, a.N, a.dqkv + (size_t)k.column * D, a.dstride_b, a.dstride_n, b, here.n);
+    Place ahead = here;  // next to be fetched, with its position
+    bool any = true;     // there is one
+    int pos = kGrad ? position_of(a, ahead.token, ahead.n) : 0;
+    auto fetch = [&](int stage) {
+      if (any) {
+        if (k.live) {
+          ring.fetch_row(stage, 0, dz.at, l);
+          if (kX) ring.fetch_row(stage, 1, in.at, l);
         }
-        const float mean = -sum_lanes<D>(sum2(dot)) * (1.0f / D);
-        const F2 m2 = f2(mean, mean);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = mul2(r2, fma2(x[e], m2, g[e]));
+        if (kGrad) ring.template fetch_turn<kInter>(stage, a, l, pos);
+        any = a.tokens - ahead.token > s.step;
+        const bool wrap = ahead.advance(s, a.N);
+        dz.advance(wrap);
+        if (kX) in.advance(wrap);
+        if (kGrad && any) pos = position_of(a, ahead.token, ahead.n);
       }
-      gx = pack(g);
+      R::commit();
+    };
+#pragma unroll
+    for (int st = 0; st < kBwdStages - 1; ++st) fetch(st);
+    for (int stage = 0;; stage = stage == kBwdStages - 1 ? 0 : stage + 1) {
+      R::template wait<kBwdStages - 2>();
+      __syncwarp();  // the table's pieces of other lanes; and all have read the last stage
+      Raw gx = ring.row(stage, 0), rx = {};
+      if (kX && k.live) rx = ring.row(stage, 1);
+      F2 g[8], cs[4], sn[4];
+      if (kGrad) ring.turn_of(stage, l, cs, sn);
+      fetch(stage == 0 ? kBwdStages - 1 : stage - 1);
+      if constexpr (kGrad) {
+        if (!k.live) gx = Raw{};  // (its lanes' sums of dw stay zero)
+        unpack(gx, g);
+        turn<kInter, true>(g, cs, sn, l);
+        if constexpr (kNorm) {
+          F2 x[8];
+          unpack(rx, x);
+          F2 ss = mul2(x[0], x[0]), dot = 0;
+#pragma unroll
+          for (int e = 1; e < 8; ++e) ss = fma2(x[e], x[e], ss);
+          const float r = rsqrtf(sum_lanes<D>(sum2(ss)) * (1.0f / D) + a.eps);
+          const F2 r2 = f2(r, r);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            x[e] = mul2(x[e], r2);  // xh
+            dw[e] = fma2(g[e], x[e], dw[e]);
+            g[e] = mul2(g[e], w[e]);
+            dot = fma2(g[e], x[e], dot);
+          }
+          const float mean = -sum_lanes<D>(sum2(dot)) * (1.0f / D);
+          const F2 m2 = f2(mean, mean);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) g[e] = mul2(r2, fma2(x[e], m2, g[e]));
+        }
+        gx = pack(g);
+      }
+      if (k.live) store_row(out.at, l, gx);
+      if (a.tokens - here.token <= s.step) break;
+      out.advance(here.advance(s, a.N));
     }
-    if (k.live) store_row(out.at, l, gx);
-    more = a.tokens - here.token > a.step;
-    out.advance(here.advance(a));
-  }
-  R::template wait<0>();
+    R::template wait<0>();
+    __syncwarp();  // the ring is free for the next deal
+  };
+  take(std::true_type{}, a.grad, 0);
+  take(std::false_type{}, a.value, a.grad.packs);
   if constexpr (kNorm) {
+    const int kind = id % max(a.grad.packs, 1) < (a.H + kPack - 1) / kPack ? 0 : 1;
     // Heads of a pack, then the block's warps of each kind.
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
@@ -431,7 +459,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeArgs a) {
       for (int m = D / 16; m < 32; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
       if (l.sub == 0) sums[warp][(e < 8 ? l.c0 : l.c1 - 8) + e] = v;
     }
-    if ((threadIdx.x & 31) == 0) kinds[warp] = k.kind;
+    if ((threadIdx.x & 31) == 0) kinds[warp] = kind;
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * D; i += kWarps * 32) {
       float s = 0.f;
@@ -462,25 +490,27 @@ __global__ void __launch_bounds__(1024) rope_dw_kernel(RopeArgs a) {
   if (threadIdx.x == 0) (c < D ? a.dq_weight : a.dk_weight)[c % D] = s;
 }
 
-// Deals packs and tokens to warps: blocks for `resident` per SM, fewer if
-// there is less than one (token, pack) for each warp.
-template <int D>
-int deal(RopeArgs& a, int sm_count, int resident) {
-  constexpr int kPack = 512 / D;
-  a.packs = (a.H + kPack - 1) / kPack + 2 * ((a.Hkv + kPack - 1) / kPack);
-  const long long all = (long long)a.tokens * a.packs;
-  long long blocks = (all + kWarps - 1) / kWarps;
+// Tokens that `blocks` take at a time when their warps share `packs` packs.
+RopeDeal deal(const RopeArgs& a, int blocks, int packs) {
+  RopeDeal s = {};
+  s.packs = packs;
+  if (packs == 0 || a.N == 0) return s;
+  s.step = blocks * kWarps / packs;
+  s.step_b = s.step / a.N;
+  s.step_n = s.step % a.N;
+  return s;
+}
+// `resident` blocks per SM, fewer if there is less than one of `packs` packs
+// of a token for each warp, and at least a warp for every pack of one token.
+int blocks_for(const RopeArgs& a, int packs, int sm_count, int resident) {
+  long long blocks = ((long long)a.tokens * packs + kWarps - 1) / kWarps;
   if (blocks > (long long)resident * sm_count) blocks = (long long)resident * sm_count;
   if (blocks > kRopeMaxBlocks) blocks = kRopeMaxBlocks;
-  // At least one warp for every pack of a token.
-  const long long least = (a.packs + kWarps - 1) / kWarps;
-  if (blocks < least) blocks = least;
-  a.step = (int)(blocks * kWarps / (a.packs > 0 ? a.packs : 1));
-  a.step_b = a.N > 0 ? a.step / a.N : 0;
-  a.step_n = a.N > 0 ? a.step % a.N : 0;
-  a.blocks = (int)blocks;
-  return a.blocks;
+  const int least = (packs + kWarps - 1) / kWarps;
+  return blocks < least ? least : (int)blocks;
 }
+template <int D>
+int packs_of(int heads) { return (heads + 512 / D - 1) / (512 / D); }
 
 template <typename K>
 cudaError_t allow_smem(K* kernel, int bytes) {
@@ -489,7 +519,9 @@ cudaError_t allow_smem(K* kernel, int bytes) {
 
 template <int D, bool kInter, bool kNorm>
 cudaError_t fwd(RopeArgs a, int sm_count, cudaStream_t stream) {
-  const int blocks = deal<D>(a, sm_count, 3);
+  const int packs = packs_of<D>(a.H) + 2 * packs_of<D>(a.Hkv);
+  const int blocks = blocks_for(a, packs, sm_count, 3);
+  a.all = deal(a, blocks, packs);
   cudaError_t e = allow_smem(rope_fwd_kernel<D, kInter, kNorm>, fwd_smem<D>());
   if (e != cudaSuccess) return e;
   rope_fwd_kernel<D, kInter, kNorm><<<blocks, kWarps * 32, fwd_smem<D>(), stream>>>(a);
@@ -498,7 +530,11 @@ cudaError_t fwd(RopeArgs a, int sm_count, cudaStream_t stream) {
 
 template <int D, bool kInter, bool kNorm>
 cudaError_t bwd(RopeArgs a, int sm_count, cudaStream_t stream) {
-  const int blocks = deal<D>(a, sm_count, 2);
+  const int packs = packs_of<D>(a.H) + packs_of<D>(a.Hkv);
+  const int blocks = blocks_for(a, packs, sm_count, 2);
+  a.grad = deal(a, blocks, packs);
+  a.value = deal(a, blocks, packs_of<D>(a.Hkv));
+  a.blocks = blocks;
   cudaError_t e = allow_smem(rope_bwd_kernel<D, kInter, kNorm>, bwd_smem<D>());
   if (e != cudaSuccess) return e;
   if (blocks > 0)
