@@ -113,9 +113,10 @@ __device__ __forceinline__ Lane lane_of(int rot) {
   return a;
 }
 
-__device__ __forceinline__ void store_row(__nv_bfloat16* row, const Lane& a, const Raw& r) {
-  *reinterpret_cast<uint4*>(row + a.c0) = r.c[0];
-  *reinterpret_cast<uint4*>(row + a.c1) = r.c[1];
+// `at`: the lane's first chunk of a row; the second is c1 - c0 elements on.
+__device__ __forceinline__ void store_row(__nv_bfloat16* at, const Lane& a, const Raw& r) {
+  *reinterpret_cast<uint4*>(at) = r.c[0];
+  *reinterpret_cast<uint4*>(at + (a.c1 - a.c0)) = r.c[1];
 }
 
 // ---- A warp's ring of rows on their way from memory, in shared memory: the
@@ -135,11 +136,11 @@ struct Ring {
                  "l"(src)
                  : "memory");
   }
-  __device__ __forceinline__ void fetch_row(int stage, int which, const __nv_bfloat16* row,
+  __device__ __forceinline__ void fetch_row(int stage, int which, const __nv_bfloat16* src,
                                             const Lane& l) const {
     uint8_t* at = base + stage * kStage + which * 1024 + (threadIdx.x & 31) * 16;
-    copy16(at, row + l.c0);
-    copy16(at + 512, row + l.c1);
+    copy16(at, src);
+    copy16(at + 512, src + (l.c1 - l.c0));
   }
   __device__ __forceinline__ Raw row(int stage, int which) const {
     const uint8_t* at = base + stage * kStage + which * 1024 + (threadIdx.x & 31) * 16;
@@ -186,9 +187,10 @@ struct Ring {
 template <bool kInter, bool kBack>
 __device__ __forceinline__ void turn(F2 (&y)[8], const F2 (&cs)[4], const F2 (&sn)[4],
                                      const Lane& l) {
+  if (!kInter && !l.turn0) return;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (!(i < 2 ? l.turn0 : l.turn1)) continue;
+    if (kInter && !(i < 2 ? l.turn0 : l.turn1)) continue;
     if constexpr (kInter) {  // pairs 2i and 2i + 1 are y[2i] and y[2i + 1]
       const float2 c = un2(cs[i]), s = un2(sn[i]);
 #pragma unroll
@@ -268,7 +270,7 @@ struct Place {
     return true;
   }
 };
-// The row of one head at a Place, stepped along with it.
+// The lane's first chunk of a head's row at a Place, stepped along with it.
 template <typename T>
 struct Walk {
   T* at;
@@ -281,7 +283,7 @@ struct Walk {
 };
 
 // Stages of the rings (3 to 6 of them measure the same within 2%).
-constexpr int kFwdStages = 3, kBwdStages = 3;
+constexpr int kFwdStages = 3, kBwdStages = 4;
 template <int D>
 constexpr int fwd_smem() { return kWarps * kFwdStages * Ring<D, 1>::kStage; }
 template <int D>
@@ -304,8 +306,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
   const bool turns = k.kind < 2;
   F2 w[8];
   if (kNorm && turns) load_weight(k.kind == 0 ? a.q_weight : a.k_weight, a.weight_bf16, l, w);
-  Walk<const __nv_bfloat16> in(a.all, a.N, a.qkv + (size_t)k.column * D, a.stride_b, a.stride_n, b, here.n);
-  Walk<__nv_bfloat16> out(a.all, a.N, (k.kind == 0 ? a.q : (k.kind == 1 ? a.k : a.v)) + (size_t)k.head * a.N * D,
+  Walk<const __nv_bfloat16> in(a.all, a.N, a.qkv + (size_t)k.column * D + l.c0, a.stride_b, a.stride_n, b, here.n);
+  Walk<__nv_bfloat16> out(a.all, a.N, (k.kind == 0 ? a.q : (k.kind == 1 ? a.k : a.v)) + (size_t)k.head * a.N * D + l.c0,
                           (long long)k.heads * a.N * D, D, b, here.n);
 
   Place ahead = here;  // next to be fetched, with its position
@@ -380,11 +382,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeArgs a) {
     here.n = here.token - b * a.N;
     F2 w[8];
     if (kX) load_weight(k.kind == 0 ? a.q_weight : a.k_weight, a.weight_bf16, l, w);
-    Walk<const __nv_bfloat16> in(s, a.N, a.qkv + (size_t)k.column * D, a.stride_b, a.stride_n, b, here.n);
+    Walk<const __nv_bfloat16> in(s, a.N, a.qkv + (size_t)k.column * D + l.c0, a.stride_b, a.stride_n, b, here.n);
     Walk<const __nv_bfloat16> dz(s, a.N,
-                                 (k.kind == 0 ? a.dq : (k.kind == 1 ? a.dk : a.dv)) + (size_t)k.head * a.N * D,
+                                 (k.kind == 0 ? a.dq : (k.kind == 1 ? a.dk : a.dv)) + (size_t)k.head * a.N * D + l.c0,
                                  (long long)k.heads * a.N * D, D, b, here.n);
-    Walk<__nv_bfloat16> out(s, a.N, a.dqkv + (size_t)k.column * D, a.dstride_b, a.dstride_n, b, here.n);
+    Walk<__nv_bfloat16> out(s, a.N, a.dqkv + (size_t)k.column * D + l.c0, a.dstride_b, a.dstride_n, b, here.n);
     Place ahead = here;  // next to be fetched, with its position
     bool any = true;     // there is one
     int pos = kGrad ? position_of(a, ahead.token, ahead.n) : 0;
