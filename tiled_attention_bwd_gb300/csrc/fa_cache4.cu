@@ -18,45 +18,54 @@ __device__ __forceinline__ int pages_of(int tokens, int shift) {
   return (int)(((unsigned)tokens + (1u << shift) - 1) >> shift);
 }
 
-// Inclusive sums of one int per thread over the block; `total` the last.
-__device__ __forceinline__ int block_scan(int v, int* sh, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Two counts of pages, summed together.
+struct Pages {
+  int back, need;
+};
+// Inclusive sums over the block; `total` the last.
+__device__ __forceinline__ Pages block_scan(Pages v, Pages* sh, Pages* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, v, m);
-    if (lane >= m) v += u;
+    const int b = __shfl_up_sync(0xffffffffu, v.back, m), n = __shfl_up_sync(0xffffffffu, v.need, m);
+    if (lane >= m) v.back += b, v.need += n;
   }
   __syncthreads();  // sh may still be read from the last call
   if (lane == 31) sh[warp] = v;
   __syncthreads();
-  int s = sh[lane];
+  Pages s = lane < warps ? sh[lane] : Pages{0, 0};
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, s, m);
-    if (lane >= m) s += u;
+    const int b = __shfl_up_sync(0xffffffffu, s.back, m), n = __shfl_up_sync(0xffffffffu, s.need, m);
+    if (lane >= m) s.back += b, s.need += n;
   }
-  *total = __shfl_sync(0xffffffffu, s, 31);
-  const int before = __shfl_sync(0xffffffffu, s, warp == 0 ? 0 : warp - 1);
-  return v + (warp == 0 ? 0 : before);
+  total->back = __shfl_sync(0xffffffffu, s.back, 31);
+  total->need = __shfl_sync(0xffffffffu, s.need, 31);
+  const int b = __shfl_sync(0xffffffffu, s.back, max(warp - 1, 0));
+  const int n = __shfl_sync(0xffffffffu, s.need, max(warp - 1, 0));
+  if (warp > 0) v.back += b, v.need += n;
+  return v;
 }
 
 // A request's state at the start of the call, with every value from memory
 // brought into range first.
 struct Req {
-  int len, after, have, keep, grow;
+  int after, keep, grow;  // tokens and pages left by a shrink; tokens wanted
+  Pages pages;            // given back, wanted
 };
 __device__ __forceinline__ Req request(const PlanArgs& a, int r) {
-  Req q = {0, 0, 0, 0, 0};
+  Req q = {0, 0, 0, {0, 0}};
   if (r >= a.R) return q;
   const long long cap = (long long)a.M << a.shift;
   const int n = a.new_tokens[r];
   int len = a.lens[r];
-  q.len = len < 0 ? 0 : (len > cap ? (int)cap : len);
-  const long long less = (long long)q.len + (n < 0 ? n : 0);
+  len = len < 0 ? 0 : (len > cap ? (int)cap : len);
+  const long long less = (long long)len + (n < 0 ? n : 0);
   q.after = less < 0 ? 0 : (int)less;
-  q.have = pages_of(q.len, a.shift);
   q.keep = pages_of(q.after, a.shift);
   q.grow = (n > 0 && n <= a.T && q.after + (long long)n <= cap) ? n : 0;
+  q.pages.back = pages_of(len, a.shift) - q.keep;
+  q.pages.need = q.grow > 0 ? pages_of(q.after + q.grow, a.shift) - q.keep : 0;
   return q;
 }
 
@@ -80,81 +89,88 @@ __device__ __forceinline__ int owner_of(const Chunk& c, int n, int i) {
   return lo;
 }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" :::
-                   "memory");
+// All blocks of the grid, which is one cluster.
+__device__ __forceinline__ void grid_sync() {
+  if (gridDim.x == 1) __syncthreads();
+  else
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" :::
+                     "memory");
 }
 
-// One cluster does a call.  Every block goes through the requests' sums, 1024
-// requests at a time; the copies of page ids and the slots are dealt over
-// all the cluster's threads, whichever request they belong to.  Shrinks push
-// their pages so that the last request's last page lies deepest; grows pop
-// in request order: taking back exactly what a call granted restores the
-// stack.  Bound by latency: a few rounds of dependent loads and barriers,
-// 4 to 5 us for a decode step of 256 requests.  (One block alone took 89 us
-// for 48 prompts of 4096 tokens, 12288 pages moved by the requests' own
-// threads.)
+// One cluster does a call.  Every block goes through the requests' sums, a
+// block's width of requests at a time; the copies of page ids and the slots
+// are dealt over all the cluster's threads, whichever request they belong to.
+// Shrinks push their pages so that the last request's last page lies deepest;
+// grows pop in request order: taking back exactly what a call granted
+// restores the stack.  Bound by latency: a few rounds of dependent loads and
+// barriers.  (One block, with a request's pages moved by its own warp, took
+// 89 us for 48 prompts of 4096 tokens, 12288 pages; the cluster takes 12.)
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
-  __shared__ int sh[32];
+  __shared__ Pages sh[32];
+  __shared__ int sh_taken[32];
   __shared__ Chunk ch;
-  const int tid = threadIdx.x, rank = blockIdx.x;  // the grid is one cluster
-  const int first = rank * kPlanThreads + tid, step = gridDim.x * kPlanThreads;
+  const int tid = threadIdx.x, width = blockDim.x, rank = blockIdx.x;
+  const int first = rank * width + tid, step = gridDim.x * width;
   int count = a.free_count[0];
   count = count < 0 ? 0 : (count > a.P ? a.P : count);
-  const int chunks = (a.R + kPlanThreads - 1) / kPlanThreads;
+  const int chunks = (a.R + width - 1) / width;
 
   // ---- pages given back
   int total_back = 0;
   if (chunks > 1) {
     for (int c = 0; c < chunks; ++c) {
-      const Req q = request(a, c * kPlanThreads + tid);
-      int t;
-      block_scan(q.have - q.keep, sh, &t);
-      total_back += t;
+      Pages t;
+      block_scan(request(a, c * width + tid).pages, sh, &t);
+      total_back += t.back;
     }
   }
   int before = 0;
+  Req q;
+  Pages t, incl;
   for (int c = 0; c < chunks; ++c) {
-    const int r0 = c * kPlanThreads, n = min(kPlanThreads, a.R - r0);
-    const Req q = request(a, r0 + tid);
-    int t;
-    ch.upto[tid] = block_scan(q.have - q.keep, sh, &t);
-    ch.keep[tid] = q.keep;
-    if (chunks == 1) total_back = t;
-    __syncthreads();
-    for (int i = first; i < t; i += step) {
-      const int o = owner_of(ch, n, i);
-      // The i-th page from the front is the last but i from the back.
-      const int page = ch.keep[o] + i - (o > 0 ? ch.upto[o - 1] : 0);
-      const int s = count + total_back - before - 1 - i;
-      if (s < a.P) a.free_list[s] = a.block_table[(size_t)(r0 + o) * a.M + page];
+    const int r0 = c * width, n = min(width, a.R - r0);
+    q = request(a, r0 + tid);
+    incl = block_scan(q.pages, sh, &t);
+    if (chunks == 1) total_back = t.back;
+    if (t.back > 0) {
+      ch.upto[tid] = incl.back;
+      ch.keep[tid] = q.keep;
+      __syncthreads();
+      for (int i = first; i < t.back; i += step) {
+        const int o = owner_of(ch, n, i);
+        // The i-th page from the front is the last but i from the back.
+        const int page = ch.keep[o] + i - (o > 0 ? ch.upto[o - 1] : 0);
+        const int s = count + total_back - before - 1 - i;
+        if (s < a.P) a.free_list[s] = a.block_table[(size_t)(r0 + o) * a.M + page];
+      }
+      before += t.back;
+      __syncthreads();
     }
-    before += t;
-    __syncthreads();
   }
   count = min(count + total_back, a.P);
-  cluster_sync();  // the pushed pages are read below
+  grid_sync();  // the pushed pages are read below
 
   // ---- pages taken, and the new tokens' slots
   int wanted = 0, taken = 0;
   for (int c = 0; c < chunks; ++c) {
-    const int r0 = c * kPlanThreads, n = min(kPlanThreads, a.R - r0);
-    const Req q = request(a, r0 + tid);
-    const int need = q.grow > 0 ? pages_of(q.after + q.grow, a.shift) - q.keep : 0;
-    int t;
-    const int incl = block_scan(need, sh, &t);
-    const bool ok = q.grow > 0 && (need == 0 || wanted + incl <= count);
+    const int r0 = c * width, n = min(width, a.R - r0);
+    if (chunks > 1) {
+      q = request(a, r0 + tid);
+      incl = block_scan(q.pages, sh, &t);
+    }
+    const int need = q.pages.need;
+    const bool ok = q.grow > 0 && (need == 0 || wanted + incl.need <= count);
     // Granted needs are a prefix of the requests that need pages.
-    if (ok && need > 0) taken = wanted + incl;
-    ch.upto[tid] = incl;
+    if (ok && need > 0) taken = wanted + incl.need;
+    ch.upto[tid] = incl.need;
     ch.after[tid] = q.after;
     ch.keep[tid] = q.keep;
     ch.grow[tid] = ok ? q.grow : 0;
-    ch.at[tid] = count - 1 - (wanted + incl - need);
+    ch.at[tid] = count - 1 - (wanted + incl.need - need);
     if (rank == 0 && tid < n) a.granted[r0 + tid] = ch.grow[tid];
-    wanted += t;
+    wanted += t.need;
     __syncthreads();
-    for (int i = first; i < t; i += step) {
+    for (int i = first; i < t.need; i += step) {
       const int o = owner_of(ch, n, i), j = i - (o > 0 ? ch.upto[o - 1] : 0);
       if (ch.grow[o] > 0)
         a.block_table[(size_t)(r0 + o) * a.M + ch.keep[o] + j] = a.free_list[ch.at[o] - j];
@@ -196,15 +212,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
   }
 
   // ---- lengths and the count, once every block has read them
-  cluster_sync();
+  if (gridDim.x > 1) grid_sync();
   if (rank != 0) return;
-  for (int r = tid; r < a.R; r += kPlanThreads) a.lens[r] = request(a, r).after + a.granted[r];
+  for (int r = tid; r < a.R; r += width) a.lens[r] = request(a, r).after + a.granted[r];
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) taken = max(taken, __shfl_xor_sync(0xffffffffu, taken, m));
-  if ((tid & 31) == 0) sh[tid >> 5] = taken;
+  if ((tid & 31) == 0) sh_taken[tid >> 5] = taken;
   __syncthreads();
   if (tid == 0) {
-    for (int w = 1; w < 32; ++w) taken = max(taken, sh[w]);
+    for (int w = 1; w < width / 32; ++w) taken = max(taken, sh_taken[w]);
     a.free_count[0] = count - taken;
   }
 }
@@ -290,14 +306,17 @@ __global__ void __launch_bounds__(256) append_kernel(AppendArgs a) {
 
 cudaError_t launch_cache4_plan(PlanArgs a, cudaStream_t stream) {
   a.wide = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15) == 0;
-  // One block for up to 8192 slots, else a cluster of eight.
+  // One block for up to 8192 slots, as wide as there are requests or slots
+  // (barriers of few warps are shorter), else a cluster of eight.
+  const long long work = (long long)a.R * a.T;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (long long)a.R * a.T <= 8 * kPlanThreads ? 1 : 8;
+  attr.val.clusterDim.x = work <= 8 * kPlanThreads ? 1 : 8;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(attr.val.clusterDim.x);
-  cfg.blockDim = dim3(kPlanThreads);
+  const long long width = work > a.R ? work : a.R;
+  cfg.blockDim = dim3(width <= 128 ? 128 : (width <= 256 ? 256 : (width <= 512 ? 512 : kPlanThreads)));
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;

@@ -714,7 +714,8 @@ template <int D, int NT>
 cudaError_t run(const Cache4AttnArgs& a, int sm_count, cudaStream_t stream) {
   using S = Shape<D, NT>;
   auto* kernel = cache4_attn_kernel<D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), S::kSmem, done);
   if (e != cudaSuccess) return e;
   int blocks = sm_count * S::kBlocksPerSm;
   if (blocks > kC4MaxBlocks) blocks = kC4MaxBlocks;

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 #include "fa.h"
@@ -170,6 +171,11 @@ struct Cache4AttnArgs {
 int cache4_attn_rows(int rows);
 cudaError_t launch_cache4_attn(const Cache4AttnArgs& a, int d, int sm_count,
                                cudaStream_t stream);
+
+// Lets a kernel use `bytes` of dynamic shared memory on the current device;
+// the attribute is set once per kernel (its own `done`) and device.
+cudaError_t allow_smem(const void* kernel, int bytes,
+                       std::atomic<unsigned long long>& done);
 
 // Status record, SM count and wait limit of the current device.
 struct DeviceInfo {

@@ -514,17 +514,13 @@ int blocks_for(const RopeArgs& a, int packs, int sm_count, int resident) {
 template <int D>
 int packs_of(int heads) { return (heads + 512 / D - 1) / (512 / D); }
 
-template <typename K>
-cudaError_t allow_smem(K* kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
 template <int D, bool kInter, bool kNorm>
 cudaError_t fwd(RopeArgs a, int sm_count, cudaStream_t stream) {
   const int packs = packs_of<D>(a.H) + 2 * packs_of<D>(a.Hkv);
   const int blocks = blocks_for(a, packs, sm_count, 3);
   a.all = deal(a, blocks, packs);
-  cudaError_t e = allow_smem(rope_fwd_kernel<D, kInter, kNorm>, fwd_smem<D>());
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(rope_fwd_kernel<D, kInter, kNorm>), fwd_smem<D>(), done);
   if (e != cudaSuccess) return e;
   rope_fwd_kernel<D, kInter, kNorm><<<blocks, kWarps * 32, fwd_smem<D>(), stream>>>(a);
   return cudaGetLastError();
@@ -537,7 +533,8 @@ cudaError_t bwd(RopeArgs a, int sm_count, cudaStream_t stream) {
   a.grad = deal(a, blocks, packs);
   a.value = deal(a, blocks, packs_of<D>(a.Hkv));
   a.blocks = blocks;
-  cudaError_t e = allow_smem(rope_bwd_kernel<D, kInter, kNorm>, bwd_smem<D>());
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(rope_bwd_kernel<D, kInter, kNorm>), bwd_smem<D>(), done);
   if (e != cudaSuccess) return e;
   if (blocks > 0)
     rope_bwd_kernel<D, kInter, kNorm><<<blocks, kWarps * 32, bwd_smem<D>(), stream>>>(a);
