@@ -6,12 +6,13 @@
 // values' sums rescaled when m grows.
 //
 // Work.  The query rows of one key/value head (H / Hkv heads x T tokens) are
-// taken 8, 16 or 32 at a time; such a row block of one request and head is
-// an item, its keys are cut into units of 64, and all items' units together
-// are dealt to the blocks in equal consecutive shares, whatever the lengths.
-// A block's four warps take one 16-token group of a unit each, with sums of
-// their own, and join them when the item (or the share) ends; an item that
-// lies in several blocks' shares is joined by a second kernel.
+// taken 8 to 32 at a time; such a row block of one request and head is an
+// item, its keys are cut into units of 128, and all items' units together
+// are dealt to the blocks in equal consecutive shares, whatever the lengths
+// (an item counts as kItemCost units more, for what it costs to begin and
+// end one).  A block's four warps take two 16-token groups of a unit each,
+// with sums of their own, and join them when the item (or the share) ends; an
+// item that lies in several blocks' shares is joined by a second kernel.
 //
 // Feeding.  Each warp copies its own groups (18 d bytes, K and V together)
 // into a ring in shared memory by bulk copies, several ahead; nothing in the
@@ -39,6 +40,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kGroups = 2;                        // of a warp in a unit
 constexpr int kUnit = kWarps * kGroups * kGroup;  // tokens of a work unit
+constexpr int kItemCost = 3;                      // in units
 constexpr float kNoMax = -1e30f;                  // m of a row that has seen no key
 constexpr float kUp = 8.0f;                       // P carries 2^kUp
 constexpr float kSlack = 6.0f;                    // growth of m that is left standing
@@ -85,6 +87,12 @@ __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, ui
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void copy16_async(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_done() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
 __device__ __forceinline__ void launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -97,6 +105,8 @@ struct Request {
   int len, ql;  // cached tokens, new tokens
   int lo;       // first token of its units (a multiple of 32)
   int units;    // of one item
+  // Of one item, in shares.
+  __device__ __forceinline__ int cost() const { return units == 0 ? 0 : units + kItemCost; }
 };
 __device__ __forceinline__ Request request_of(const Cache4AttnArgs& a, int b) {
   Request r;
@@ -113,29 +123,40 @@ __device__ __forceinline__ Request request_of(const Cache4AttnArgs& a, int b) {
   return r;
 }
 
-// A block's place in the list of units.
+// A block's place in the list of items: the segment of the present item that
+// is its own, units [unit, end).
 struct Cursor {
-  int b;       // request
-  int hk, rb;  // the item's key/value head and row block
-  int unit;    // within the item
+  int b;          // request
+  int hk, rb;     // the item's key/value head and row block
+  int unit, end;
+  int left;       // of the share, behind this segment
   Request r;
+
+  // The segment of the present item that begins `at` into its cost.
+  __device__ __forceinline__ void segment(int at) {
+    const int here = min(r.cost() - at, left), to = at + here;
+    left -= here;
+    unit = max(0, at - kItemCost);
+    end = max(0, to - kItemCost);
+  }
+  // The next item's; false if the share has none.
+  __device__ __forceinline__ bool next(const Cache4AttnArgs& a) {
+    if (left == 0) return false;
+    if (++rb == a.row_blocks) {
+      rb = 0;
+      if (++hk == a.Hkv) {
+        hk = 0;
+        do r = request_of(a, ++b);
+        while (r.units == 0);
+      }
+    }
+    segment(0);
+    return end > 0;  // (a share may end before an item's first unit)
+  }
 };
 
-// The next item with units, or b = B.
-__device__ __forceinline__ void next_item(const Cache4AttnArgs& a, Cursor& c) {
-  c.unit = 0;
-  if (++c.rb < a.row_blocks) return;
-  c.rb = 0;
-  if (++c.hk < a.Hkv) return;
-  c.hk = 0;
-  do {
-    if (++c.b >= a.B) return;
-    c.r = request_of(a, c.b);
-  } while (c.r.units == 0);
-}
-
-// Equal shares: `units` dealt to blocks 0 .. blocks-1 in order, the first
-// `more` blocks one more than the others' `least`.
+// Equal shares: `units` of cost dealt to blocks 0 .. blocks-1 in order, the
+// first `more` blocks one more than the others' `least`.
 struct Shares {
   long long least;
   int more, blocks;
@@ -162,13 +183,18 @@ struct Shares {
 template <int D, int NT>
 struct Shape {
   static constexpr int kRows = 8 * NT;
+  static constexpr bool kQInRegs = NT <= 2;  // else Q's fragments are in shared memory
+  static constexpr int kTogether = NT <= 2 ? kGroups : 1;  // groups per softmax step
   static constexpr int kSlot = kGroups * group_bytes(D);
   static constexpr int kStages = 2;
-  static constexpr int kBlocksPerSm = NT == 1 ? 4 : (D == 64 ? 3 : 2);
+  static constexpr int kBlocksPerSm = NT == 1 ? 4 : (NT == 2 && D == 64 ? 3 : 2);
   static constexpr int kRing = kWarps * kStages * kSlot;
   static constexpr int kPitch = D + 4;  // floats of a row in the join buffer
-  static constexpr int kJoin = kWarps * 8 * kPitch * 4;
-  static constexpr int kSmem = kRing + kJoin;
+  static constexpr int kJoin = kWarps * 4 * kPitch * 4;  // four rows of every warp
+  static constexpr int kQPitch = 2 * D + 16;             // bytes of a raw row of Q
+  static constexpr int kQRaw = kRows * kQPitch;          // twice
+  static constexpr int kQFrag = kQInRegs ? 0 : NT * (D / 32) * 512;
+  static constexpr int kSmem = kRing + kJoin + 2 * kQRaw + kQFrag;
 };
 
 // Where the partial results of a block's first (2 c) and last (2 c + 1)
@@ -183,10 +209,23 @@ __device__ __forceinline__ Partial partial_of(const Cache4AttnArgs& a, int slot,
   return Partial{a.part + at * D, a.part_ml + at};
 }
 
+// The running state of a segment's rows in one warp.
+template <int D, int NT>
+struct Rows {
+  // Q: row 8 nt + g, dims t D/4 + 0 .. D/4 - 1, scaled to f16, here or in
+  // shared memory (4 registers' worth per lane, [nt][D / 32][lane]).
+  uint32_t qf[Shape<D, NT>::kQInRegs ? NT : 1][D / 8];
+  const uint4* qs;
+  float rs[NT][2];  // rows 8 nt + 2t, + 1: score to power of two
+  // m: the row's maximum less kUp, in powers of two; weights are 2^(s - m).
+  float m[NT][2], l[NT][2];
+  float o[D / 16][NT][4];
+};
+
 // One group's scores, S^T = K Q^T: tokens g and g + 8, rows 2t and 2t + 1.
 template <int D, int NT>
-__device__ __forceinline__ void scores(const uint8_t* grp, int g, int t,
-                                       const uint32_t (&qf)[NT][D / 8], float (&s)[NT][4]) {
+__device__ __forceinline__ void scores(const uint8_t* grp, int g, int t, const Rows<D, NT>& r,
+                                       float (&s)[NT][4]) {
   uint32_t kc[2][D / 32], ks[2][D / 64];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -213,12 +252,16 @@ __device__ __forceinline__ void scores(const uint8_t* grp, int g, int t,
     e2m1_to_f16(kc[1][w], y);
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], ks[0][w / 2]), y[i] = mul2(y[i], ks[1][w / 2]);
+    const uint32_t f0[4] = {x[0], y[0], x[1], y[1]}, f1[4] = {x[2], y[2], x[3], y[3]};
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      const uint32_t f[4] = {x[2 * hh], y[2 * hh], x[2 * hh + 1], y[2 * hh + 1]};
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        mma(s[nt], f, qf[nt][4 * w + 2 * hh], qf[nt][4 * w + 2 * hh + 1]);
+    for (int nt = 0; nt < NT; ++nt) {
+      uint4 q;
+      if constexpr (Shape<D, NT>::kQInRegs)
+        q = make_uint4(r.qf[nt][4 * w], r.qf[nt][4 * w + 1], r.qf[nt][4 * w + 2], r.qf[nt][4 * w + 3]);
+      else
+        q = r.qs[(nt * (D / 32) + w) * 32];
+      mma(s[nt], f0, q.x, q.y);
+      mma(s[nt], f1, q.z, q.w);
     }
   }
 }
@@ -263,16 +306,6 @@ __device__ __forceinline__ void values(const uint8_t* grp, int g, int t, const u
   }
 }
 
-// The running state of a segment's rows in one warp, and what they may see.
-template <int D, int NT>
-struct Rows {
-  uint32_t qf[NT][D / 8];  // row 8 nt + g, dims t D/4 + 0 .. D/4 - 1, scaled to f16
-  float rs[NT][2];         // rows 8 nt + 2t, + 1: score to power of two
-  // m: the row's maximum less kUp, in powers of two; weights are 2^(s - m).
-  float m[NT][2], l[NT][2];
-  float o[D / 16][NT][4];
-};
-
 // What bounds the keys that a segment's rows see.
 struct Bounds {
   int row0, T;  // first row, rows of a head
@@ -280,14 +313,15 @@ struct Bounds {
   int len, window;
 };
 
-// One slot of the ring: both groups' products.  kPlain: every row sees every
-// token; else masks apply and `there` says which groups were copied.
-template <int D, int NT, bool kPlain>
-__device__ __forceinline__ void use_slot(Rows<D, NT>& r, const uint8_t* slot, int tok, int there,
-                                         const Bounds& bd, int g, int t) {
-  float s[kGroups][NT][4], p[kGroups][NT][4], top = -INFINITY;
+// kN groups' scores, minus infinity where a row does not see a token.
+// kPlain: every row sees every token; else bit u of `there` says whether
+// group u was copied.
+template <int D, int NT, int kN, bool kPlain>
+__device__ __forceinline__ void masked_scores(const Rows<D, NT>& r, const uint8_t* grps, int tok,
+                                              int there, const Bounds& bd, int g, int t,
+                                              float (&s)[kN][NT][4]) {
 #pragma unroll
-  for (int u = 0; u < kGroups; ++u) scores<D, NT>(slot + u * group_bytes(D), g, t, r.qf, s[u]);
+  for (int u = 0; u < kN; ++u) scores<D, NT>(grps + u * group_bytes(D), g, t, r, s[u]);
   if constexpr (!kPlain) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -296,7 +330,7 @@ __device__ __forceinline__ void use_slot(Rows<D, NT>& r, const uint8_t* slot, in
         const int pos = bd.pos0 + (bd.row0 + 8 * nt + 2 * t + i) % bd.T;
         const int hi = min(pos + 1, bd.len), lo = bd.window < 0 ? 0 : pos - bd.window;
 #pragma unroll
-        for (int u = 0; u < kGroups; ++u)
+        for (int u = 0; u < kN; ++u)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int j = tok + u * kGroup + g + 8 * h;
@@ -304,8 +338,16 @@ __device__ __forceinline__ void use_slot(Rows<D, NT>& r, const uint8_t* slot, in
           }
       }
   }
+}
+
+// kN groups' products.
+template <int D, int NT, int kN, bool kPlain>
+__device__ __forceinline__ void step(Rows<D, NT>& r, const uint8_t* grps, int tok, int there,
+                                     const Bounds& bd, int g, int t) {
+  float s[kN][NT][4], p[kN][NT][4], top = -INFINITY;
+  masked_scores<D, NT, kN, kPlain>(r, grps, tok, there, bd, g, t, s);
 #pragma unroll
-  for (int u = 0; u < kGroups; ++u)
+  for (int u = 0; u < kN; ++u)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -320,7 +362,7 @@ __device__ __forceinline__ void use_slot(Rows<D, NT>& r, const uint8_t* slot, in
       for (int i = 0; i < 2; ++i) {
         float mx = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < kGroups; ++u) mx = fmaxf(mx, fmaxf(s[u][nt][i], s[u][nt][i + 2]));
+        for (int u = 0; u < kN; ++u) mx = fmaxf(mx, fmaxf(s[u][nt][i], s[u][nt][i + 2]));
         mx *= r.rs[nt][i];  // (positive: minus infinity stays)
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
@@ -331,14 +373,14 @@ __device__ __forceinline__ void use_slot(Rows<D, NT>& r, const uint8_t* slot, in
 #pragma unroll
         for (int dt = 0; dt < D / 16; ++dt) r.o[dt][nt][i] *= f, r.o[dt][nt][i + 2] *= f;
 #pragma unroll
-        for (int u = 0; u < kGroups; ++u) {
+        for (int u = 0; u < kN; ++u) {
           p[u][nt][i] = fmaf(s[u][nt][i], r.rs[nt][i], -mx);
           p[u][nt][i + 2] = fmaf(s[u][nt][i + 2], r.rs[nt][i], -mx);
         }
       }
   }
 #pragma unroll
-  for (int u = 0; u < kGroups; ++u) {
+  for (int u = 0; u < kN; ++u) {
     uint32_t pb[NT][2], vs[2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -349,7 +391,7 @@ __device__ __forceinline__ void use_slot(Rows<D, NT>& r, const uint8_t* slot, in
       pb[nt][0] = transpose8x8(f16x2(p[u][nt][0], p[u][nt][1]));
       pb[nt][1] = transpose8x8(f16x2(p[u][nt][2], p[u][nt][3]));
     }
-    const uint8_t* grp = slot + u * group_bytes(D);
+    const uint8_t* grp = grps + u * group_bytes(D);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t two = *reinterpret_cast<const uint16_t*>(
@@ -368,6 +410,16 @@ __device__ __forceinline__ void use_slot(Rows<D, NT>& r, const uint8_t* slot, in
   }
 }
 
+// One slot of the ring.
+template <int D, int NT, bool kPlain>
+__device__ __forceinline__ void use_slot(Rows<D, NT>& r, const uint8_t* slot, int tok, int there,
+                                         const Bounds& bd, int g, int t) {
+  constexpr int kN = Shape<D, NT>::kTogether;
+#pragma unroll
+  for (int u = 0; u < kGroups; u += kN)
+    step<D, NT, kN, kPlain>(r, slot + u * group_bytes(D), tok + u * kGroup, there >> u, bd, g, t);
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
     cache4_attn_kernel(Cache4AttnArgs a) {
@@ -377,14 +429,17 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
   __shared__ uint64_t full[kWarps][S::kStages];
   __shared__ int copied[kWarps][S::kStages];  // bit u: group u of the slot
   __shared__ uint32_t cta_abort;
-  __shared__ int sh_scan[kWarps], sh_first[4];
-  __shared__ float sh_ml[kWarps][8][2];
+  __shared__ int sh_scan[kWarps], sh_first[3];
+  __shared__ float2 sh_ml[kWarps][4];
+  __shared__ float sh_rs[S::kRows];
 
   launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * S::kStages * S::kSlot;
   float* join = reinterpret_cast<float*>(smem + S::kRing);
+  uint8_t* q_raw = smem + S::kRing + S::kJoin;
+  uint4* q_frag = reinterpret_cast<uint4*>(q_raw + 2 * S::kQRaw);
   const WaitCtl ctl = {a.st, &cta_abort, a.timeout_ns};
   if (lane < S::kStages) mbar_init(&full[warp][lane], 1);
   if (tid == 0) cta_abort = 0;
@@ -395,7 +450,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
   const int per = (a.B + kWarps * 32 - 1) / (kWarps * 32);
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += request_of(a, b).units;
+  for (int b = b0; b < b1; ++b) mine += request_of(a, b).cost();
   int upto = mine;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
@@ -417,37 +472,52 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
     return;
   }
   const long long u0 = shares.first(blockIdx.x);
-  const int mine_units = (int)(shares.first(blockIdx.x + 1) - u0);
   if (u0 >= (long long)before * items && u0 < (long long)upto * items) {
     long long left = u0 - (long long)before * items;
     int b = b0;
     Request r = request_of(a, b);
-    while (left >= (long long)r.units * items) {
-      left -= (long long)r.units * items;
+    while (left >= (long long)r.cost() * items) {
+      left -= (long long)r.cost() * items;
       r = request_of(a, ++b);
     }
     sh_first[0] = b;
-    sh_first[1] = (int)(left / r.units);
-    sh_first[2] = (int)(left % r.units);
+    sh_first[1] = (int)(left / r.cost());
+    sh_first[2] = (int)(left % r.cost());
   }
   __syncthreads();
   Cursor use;
   use.b = sh_first[0];
   use.hk = sh_first[1] / a.row_blocks;
   use.rb = sh_first[1] - use.hk * a.row_blocks;
-  use.unit = sh_first[2];
+  use.left = (int)(shares.first(blockIdx.x + 1) - u0);
   use.r = request_of(a, use.b);
+  use.segment(sh_first[2]);
+
+  // What the joining kernel does for this block's first item, if that began
+  // in the block before: the request, item, last block, and first partial.
+  if (tid == 0) {
+    int4 j = make_int4(-1, 0, 0, 0);
+    if (use.unit > 0) {
+      const long long i0 = u0 - sh_first[2], before_us = shares.first(blockIdx.x - 1);
+      if (before_us <= i0 + kItemCost)
+        j = make_int4(use.b, use.hk * a.row_blocks + use.rb, shares.block_of(i0 + use.r.cost() - 1),
+                      2 * (blockIdx.x - 1) + (before_us < i0 ? 1 : 0));
+    }
+    a.joins[blockIdx.x] = j;
+  }
+  if (use.end == use.unit) return;  // a share of nothing but an item's cost
 
   // ---- the warp's own ring, one slot per unit.  Each lane works out where
   // one of the next 32 units' groups lie and issues those copies when its
   // turn comes.
   Cursor load = use;
+  bool more = true;         // there are units left to load
   int put = 0, put_slot = 0;  // units passed by the loads, and their slot
   int turn = 0, turns = 0;    // place in the lanes' units
   const uint8_t* src[kGroups];
   auto look_ahead = [&]() {
     turn = 0;
-    turns = min(32, load.r.units - load.unit);
+    turns = min(32, load.end - load.unit);
 #pragma unroll
     for (int u = 0; u < kGroups; ++u) {
       const int tok = load.r.lo + (load.unit + lane) * kUnit + (warp * kGroups + u) * kGroup;
@@ -462,11 +532,6 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
     }
   };
   auto feed = [&]() {
-    if (turn == turns) {
-      load.unit += turns;
-      if (load.unit == load.r.units) next_item(a, load);
-      look_ahead();
-    }
     if (lane == turn) {
       uint64_t* bar = &full[warp][put_slot];
       uint8_t* dst = ring + put_slot * S::kSlot;
@@ -481,54 +546,62 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
         if (src[1]) bulk_load(dst + group_bytes(D), src[1], group_bytes(D), bar);
       }
     }
-    ++turn;
     ++put;
     if (++put_slot == S::kStages) put_slot = 0;
+    if (++turn == turns) {
+      load.unit += turns;
+      if (load.unit == load.end) more = load.next(a);
+      if (more) look_ahead();
+    }
   };
   look_ahead();
-  while (put < mine_units && put < S::kStages) feed();
+  for (int i = 0; i < S::kStages && more; ++i) feed();
 
-  // What the joining kernel does for this block's first item, if that began
-  // in the block before: the request, item, last block, and first partial.
-  if (tid == 0) {
-    int4 j = make_int4(-1, 0, 0, 0);
-    if (use.unit > 0) {
-      const long long i0 = u0 - use.unit, before_us = shares.first(blockIdx.x - 1);
-      if (before_us <= i0)
-        j = make_int4(use.b, use.hk * a.row_blocks + use.rb,
-                      shares.block_of(i0 + use.r.units - 1),
-                      2 * (blockIdx.x - 1) + (before_us < i0 ? 1 : 0));
-    }
-    a.joins[blockIdx.x] = j;
-  }
+  // ---- Q: the next segment's raw rows are on their way while one is worked on
+  auto first_row = [&](const Cursor& c) {
+    return ((size_t)c.b * a.Hkv + c.hk) * a.rows + c.rb * S::kRows;
+  };
+  auto fetch_q = [&](const Cursor& c, int buffer) {
+    constexpr int kChunks = 2 * D / 16;
+    uint8_t* dst = q_raw + buffer * S::kQRaw;
+    const int rows = min(S::kRows, a.rows - c.rb * S::kRows);
+    const uint8_t* q = reinterpret_cast<const uint8_t*>(a.q + first_row(c) * D);
+    for (int i = tid; i < rows * kChunks; i += kWarps * 32)
+      copy16_async(dst + i / kChunks * S::kQPitch + i % kChunks * 16, q + i * 16);
+  };
+  fetch_q(use, 0);
 
-  int got = 0, got_slot = 0, left = mine_units;
+  int got = 0, got_slot = 0;
   uint32_t parity = 0;
-  bool first_segment = true, dead = false;
-  while (left > 0) {
-    // ---- one segment: units [use.unit, end) of one item
-    const int end = min(use.r.units, use.unit + left);
-    const int seg = end - use.unit;
-    const bool whole = use.unit == 0 && end == use.r.units;
+  bool dead = false;
+  for (int seg = 0;; ++seg) {
+    // ---- one segment
+    const bool whole = use.unit == 0 && use.end == use.r.units;
     const int row0 = use.rb * S::kRows;
-    const size_t q_row = ((size_t)use.b * a.Hkv + use.hk) * a.rows + row0;
+    const size_t q_row = first_row(use);
     const int pos0 = use.r.len - use.r.ql;  // position of the first new token
+    copies_done();
+    __syncthreads();  // Q is there, and the other buffer's readers are done
+    {
+      Cursor then = use;
+      if (then.next(a)) fetch_q(then, (seg + 1) & 1);
+    }
 
     Rows<D, NT> r;
+    const uint8_t* raw = q_raw + (seg & 1) * S::kQRaw;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      if (!S::kQInRegs && nt % kWarps != warp) continue;
+      uint32_t qf[D / 8], big = 0;
       const bool live = row0 + 8 * nt + g < a.rows;
-      const __nv_bfloat16* q = a.q + (q_row + 8 * nt + g) * D + t * (D / 4);
-      uint32_t big = 0;
+      const uint4* q = reinterpret_cast<const uint4*>(raw + (8 * nt + g) * S::kQPitch + t * (D / 2));
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (live) u = __ldg(reinterpret_cast<const uint4*>(q) + i);
-        r.qf[nt][4 * i] = u.x, r.qf[nt][4 * i + 1] = u.y;
-        r.qf[nt][4 * i + 2] = u.z, r.qf[nt][4 * i + 3] = u.w;
+        const uint4 u = live ? q[i] : make_uint4(0, 0, 0, 0);
+        qf[4 * i] = u.x, qf[4 * i + 1] = u.y, qf[4 * i + 2] = u.z, qf[4 * i + 3] = u.w;
       }
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) big = __vmaxu2(big, r.qf[nt][i] & 0x7fff7fffu);
+      for (int i = 0; i < D / 8; ++i) big = __vmaxu2(big, qf[i] & 0x7fff7fffu);
       big = max(big & 0xffffu, big >> 16);
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
@@ -536,18 +609,35 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
       int e = big >> 7;
       e = e < 16 ? 16 : (e > 250 ? 250 : e);
       const float down = __uint_as_float((uint32_t)(262 - e) << 23);
-      const float back = __uint_as_float((uint32_t)(e - 8) << 23) * a.scale_log2;
+      // (Not zero: a masked score, minus infinity, is multiplied with it.)
+      const float back = fmaxf(__uint_as_float((uint32_t)(e - 8) << 23) * a.scale_log2, 1.2e-38f);
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
-        r.qf[nt][i] = f16x2(__uint_as_float(r.qf[nt][i] << 16) * down,
-                            __uint_as_float(r.qf[nt][i] & 0xffff0000u) * down);
+        qf[i] = f16x2(__uint_as_float(qf[i] << 16) * down, __uint_as_float(qf[i] & 0xffff0000u) * down);
+      if constexpr (S::kQInRegs) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        // (Not zero: a masked score, minus infinity, is multiplied with it.)
-        r.rs[nt][i] = fmaxf(__shfl_sync(0xffffffffu, back, 8 * t + 4 * i), 1.2e-38f);
-        r.m[nt][i] = kNoMax;
-        r.l[nt][i] = 0.f;
+        for (int i = 0; i < D / 8; ++i) r.qf[nt][i] = qf[i];
+        r.rs[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);
+        r.rs[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+          q_frag[(nt * (D / 32) + i) * 32 + lane] =
+              make_uint4(qf[4 * i], qf[4 * i + 1], qf[4 * i + 2], qf[4 * i + 3]);
+        if (t == 0) sh_rs[8 * nt + g] = back;
       }
+    }
+    if constexpr (!S::kQInRegs) {
+      __syncthreads();
+      r.qs = q_frag + lane;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        r.rs[nt][0] = sh_rs[8 * nt + 2 * t], r.rs[nt][1] = sh_rs[8 * nt + 2 * t + 1];
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      r.m[nt][0] = r.m[nt][1] = kNoMax;
+      r.l[nt][0] = r.l[nt][1] = 0.f;
 #pragma unroll
       for (int i = 0; i < kSteps; ++i)
         r.o[i][nt][0] = r.o[i][nt][1] = r.o[i][nt][2] = r.o[i][nt][3] = 0.f;
@@ -556,7 +646,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
     // Tokens within [plain_lo, plain_hi) are seen by every row.
     const int plain_hi = pos0 + 1, plain_lo = a.window < 0 ? 0 : use.r.len - 1 - a.window;
 
-    for (int un = dead ? end : use.unit; un < end; ++un) {
+    for (int un = dead ? use.end : use.unit; un < use.end; ++un) {
       if (!wait_bar_warp(&full[warp][got_slot], parity, ctl, 0x511)) {
         dead = true;
         break;
@@ -571,11 +661,11 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
       __syncwarp();  // every lane has read the slot
       ++got;
       if (++got_slot == S::kStages) got_slot = 0, parity ^= 1;
-      if (put < mine_units) feed();
+      if (more) feed();
     }
 
-    // ---- join the warps, eight rows at a time
-    const int part_slot = 2 * blockIdx.x + (first_segment ? 0 : 1);
+    // ---- join the warps, four rows at a time: a warp writes one row
+    const int part_slot = 2 * blockIdx.x + (seg == 0 ? 0 : 1);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -583,62 +673,58 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) r.l[nt][i] += __shfl_xor_sync(0xffffffffu, r.l[nt][i], x);
       }
-      __syncthreads();  // the buffer's last readers are done
-      if (g == 0) {
-        sh_ml[warp][2 * t][0] = r.m[nt][0], sh_ml[warp][2 * t][1] = r.l[nt][0];
-        sh_ml[warp][2 * t + 1][0] = r.m[nt][1], sh_ml[warp][2 * t + 1][1] = r.l[nt][1];
-      }
-      // Lane (g, t) holds dims g D/8 + 0 .. D/8 - 1 of rows 2t and 2t + 1.
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float* dst = join + (warp * 8 + 2 * t + i) * S::kPitch + g * (D / 8);
+      for (int half = 0; half < 2; ++half) {
+        __syncthreads();  // the buffer's last readers are done
+        // Lane (g, t) holds dims g D/8 + 0 .. D/8 - 1 of rows 2t and 2t + 1.
+        if (t >> 1 == half) {
 #pragma unroll
-        for (int dt = 0; dt < kSteps; dt += 2)
-          *reinterpret_cast<float4*>(dst + 2 * dt) =
-              make_float4(r.o[dt][nt][i], r.o[dt][nt][i + 2], r.o[dt + 1][nt][i], r.o[dt + 1][nt][i + 2]);
-      }
-      __syncthreads();
-      const int row = tid >> 4, c = tid & 15;  // 16 threads a row
-      float mx = kNoMax, f[kWarps], sum = 0.f;
+          for (int i = 0; i < 2; ++i) {
+            const int row = (2 * t + i) & 3;
+            if (g == 0) sh_ml[warp][row] = make_float2(r.m[nt][i], r.l[nt][i]);
+            float* dst = join + (warp * 4 + row) * S::kPitch + g * (D / 8);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sh_ml[w][row][0]);
+            for (int dt = 0; dt < kSteps; dt += 2)
+              *reinterpret_cast<float4*>(dst + 2 * dt) = make_float4(
+                  r.o[dt][nt][i], r.o[dt][nt][i + 2], r.o[dt + 1][nt][i], r.o[dt + 1][nt][i + 2]);
+          }
+        }
+        __syncthreads();
+        const int row = 8 * nt + 4 * half + warp, rr = row0 + row;
+        float mx = kNoMax, f[kWarps], sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        f[w] = ex2(sh_ml[w][row][0] - mx);
-        sum += f[w] * sh_ml[w][row][1];
-      }
-      const int rr = row0 + 8 * nt + row;
-      const bool live = rr < a.rows && rr % a.T < use.r.ql;
-      const float inv = sum > 0.f || sum != sum ? a.v_scale / sum : 0.f;
-      const Partial part = partial_of<D, NT>(a, part_slot, 8 * nt + row);
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sh_ml[w][warp].x);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float4 v =
-              *reinterpret_cast<const float4*>(join + (w * 8 + row) * S::kPitch + 64 * i + 4 * c);
-          acc[0] += f[w] * v.x, acc[1] += f[w] * v.y, acc[2] += f[w] * v.z, acc[3] += f[w] * v.w;
+          f[w] = ex2(sh_ml[w][warp].x - mx);
+          sum += f[w] * sh_ml[w][warp].y;
         }
-        if (!whole) {
-          *reinterpret_cast<float4*>(part.o + 64 * i + 4 * c) =
-              make_float4(acc[0], acc[1], acc[2], acc[3]);
-        } else if (live) {
-          __nv_bfloat162 lo = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
-          __nv_bfloat162 hi = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
-          *reinterpret_cast<uint2*>(a.o + (q_row + 8 * nt + row) * D + 64 * i + 4 * c) =
-              make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+        const bool live = rr < a.rows && rr % a.T < use.r.ql;
+        const float inv = sum > 0.f || sum != sum ? a.v_scale / sum : 0.f;
+        const Partial part = partial_of<D, NT>(a, part_slot, row);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {  // two dims a lane
+          float2 acc = make_float2(0.f, 0.f);
+          const int dim = 64 * i + 2 * lane;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float2 v = *reinterpret_cast<const float2*>(join + (w * 4 + warp) * S::kPitch + dim);
+            acc.x += f[w] * v.x, acc.y += f[w] * v.y;
+          }
+          if (!whole) {
+            *reinterpret_cast<float2*>(part.o + dim) = acc;
+          } else if (live) {
+            *reinterpret_cast<__nv_bfloat162*>(a.o + (q_row + row) * D + dim) =
+                __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+          }
         }
-      }
-      if (c == 0) {
-        if (!whole) *part.ml = make_float2(mx, sum);
-        else if (live) a.lse[q_row + 8 * nt + row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+        if (lane == 0) {
+          if (!whole) *part.ml = make_float2(mx, sum);
+          else if (live) a.lse[q_row + row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+        }
       }
     }
-    left -= seg;
-    use.unit = end;
-    if (use.unit == use.r.units && left > 0) next_item(a, use);
-    first_segment = false;
+    if (!use.next(a)) break;
   }
   // A stopping block lets its copies land before it leaves.
   for (; got < put; ++got) {
@@ -736,12 +822,29 @@ cudaError_t run(const Cache4AttnArgs& a, int sm_count, cudaStream_t stream) {
 
 }  // namespace
 
-int cache4_attn_rows(int rows) { return rows <= 8 ? 8 : 16; }
+// Rows of an item.  Wider items share the work of making K and V of codes (as
+// long as about six tiles of eight rows take) but fill whole tiles.
+int cache4_attn_rows(int rows) {
+  int best = 8;
+  long long least = 0;
+  for (int nt = 1; nt <= 4; ++nt) {
+    const long long cost = (rows + 8LL * nt - 1) / (8 * nt) * (6 + nt);
+    if (nt == 1 || cost < least) least = cost, best = 8 * nt;
+  }
+  return best;
+}
 
 cudaError_t launch_cache4_attn(const Cache4AttnArgs& a, int d, int sm_count, cudaStream_t stream) {
-  const int rows = cache4_attn_rows(a.rows);
-  if (d == 128) return rows == 8 ? run<128, 1>(a, sm_count, stream) : run<128, 2>(a, sm_count, stream);
-  return rows == 8 ? run<64, 1>(a, sm_count, stream) : run<64, 2>(a, sm_count, stream);
+  const int nt = cache4_attn_rows(a.rows) / 8;
+  if (d == 128)
+    return nt == 1   ? run<128, 1>(a, sm_count, stream)
+           : nt == 2 ? run<128, 2>(a, sm_count, stream)
+           : nt == 3 ? run<128, 3>(a, sm_count, stream)
+                     : run<128, 4>(a, sm_count, stream);
+  return nt == 1   ? run<64, 1>(a, sm_count, stream)
+         : nt == 2 ? run<64, 2>(a, sm_count, stream)
+         : nt == 3 ? run<64, 3>(a, sm_count, stream)
+                   : run<64, 4>(a, sm_count, stream);
 }
 
 }  // namespace fa

@@ -279,6 +279,8 @@ fa_status fa_cache4_attn(const void* q, const void* cache, const int* block_tabl
   if (((long long)max_blocks << shift) > INT_MAX || (long long)B * H > INT_MAX ||
       (long long)B * H * T > INT_MAX || (long long)B * max_blocks > INT_MAX)
     return FA_ERR_UNSUPPORTED;
+  // A block's share of the work is counted in 31 bits.
+  if ((double)B * max_blocks * page_size * H * T > 0x1p45) return FA_ERR_UNSUPPORTED;
   if (B == 0 || H == 0 || T == 0) return FA_OK;
   if (!q || !seq_lens || !o || !lse || (pages > 0 && !cache) || (max_blocks > 0 && !block_table))
     return FA_ERR_INVALID_ARG;
