@@ -187,7 +187,7 @@ struct Shape {
   static constexpr int kTogether = NT <= 2 ? kGroups : 1;  // groups per softmax step
   static constexpr int kSlot = kGroups * group_bytes(D);
   static constexpr int kStages = 2;
-  static constexpr int kBlocksPerSm = NT == 1 ? 4 : (NT == 2 && D == 64 ? 3 : 2);
+  static constexpr int kBlocksPerSm = NT == 1 || (NT == 2 && D == 64) ? 3 : 2;
   static constexpr int kRing = kWarps * kStages * kSlot;
   static constexpr int kPitch = D + 4;  // floats of a row in the join buffer
   static constexpr int kJoin = kWarps * 4 * kPitch * 4;  // four rows of every warp
@@ -216,7 +216,13 @@ struct Rows {
   // shared memory (4 registers' worth per lane, [nt][D / 32][lane]).
   uint32_t qf[Shape<D, NT>::kQInRegs ? NT : 1][D / 8];
   const uint4* qs;
-  float rs[NT][2];  // rows 8 nt + 2t, + 1: score to power of two
+  // Score to power of two, of rows 8 nt + 2t and + 1, likewise.
+  float rs[Shape<D, NT>::kQInRegs ? NT : 1][2];
+  const float2* rss;
+  __device__ __forceinline__ float2 scale(int nt) const {
+    if constexpr (Shape<D, NT>::kQInRegs) return make_float2(rs[nt][0], rs[nt][1]);
+    else return rss[4 * nt];
+  }
   // m: the row's maximum less kUp, in powers of two; weights are 2^(s - m).
   float m[NT][2], l[NT][2];
   float o[D / 16][NT][4];
@@ -344,17 +350,17 @@ __device__ __forceinline__ void masked_scores(const Rows<D, NT>& r, const uint8_
 template <int D, int NT, int kN, bool kPlain>
 __device__ __forceinline__ void step(Rows<D, NT>& r, const uint8_t* grps, int tok, int there,
                                      const Bounds& bd, int g, int t) {
-  float s[kN][NT][4], p[kN][NT][4], top = -INFINITY;
+  float s[kN][NT][4], top = -INFINITY;
   masked_scores<D, NT, kN, kPlain>(r, grps, tok, there, bd, g, t, s);
 #pragma unroll
-  for (int u = 0; u < kN; ++u)
+  for (int nt = 0; nt < NT; ++nt) {
+    const float2 rs = r.scale(nt);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int u = 0; u < kN; ++u)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        p[u][nt][i] = fmaf(s[u][nt][i], r.rs[nt][i & 1], -r.m[nt][i & 1]);
-        top = fmaxf(top, p[u][nt][i]);
-      }
+      for (int i = 0; i < 4; ++i)
+        top = fmaxf(top, fmaf(s[u][nt][i], i & 1 ? rs.y : rs.x, -r.m[nt][i & 1]));
+  }
   if (__any_sync(0xffffffffu, top > kUp + kSlack)) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -363,7 +369,7 @@ __device__ __forceinline__ void step(Rows<D, NT>& r, const uint8_t* grps, int to
         float mx = -INFINITY;
 #pragma unroll
         for (int u = 0; u < kN; ++u) mx = fmaxf(mx, fmaxf(s[u][nt][i], s[u][nt][i + 2]));
-        mx *= r.rs[nt][i];  // (positive: minus infinity stays)
+        mx *= i ? r.scale(nt).y : r.scale(nt).x;  // (positive: minus infinity stays)
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
         mx = fmaxf(mx - kUp, r.m[nt][i]);
@@ -372,11 +378,6 @@ __device__ __forceinline__ void step(Rows<D, NT>& r, const uint8_t* grps, int to
         r.l[nt][i] *= f;
 #pragma unroll
         for (int dt = 0; dt < D / 16; ++dt) r.o[dt][nt][i] *= f, r.o[dt][nt][i + 2] *= f;
-#pragma unroll
-        for (int u = 0; u < kN; ++u) {
-          p[u][nt][i] = fmaf(s[u][nt][i], r.rs[nt][i], -mx);
-          p[u][nt][i + 2] = fmaf(s[u][nt][i + 2], r.rs[nt][i], -mx);
-        }
       }
   }
 #pragma unroll
@@ -384,12 +385,15 @@ __device__ __forceinline__ void step(Rows<D, NT>& r, const uint8_t* grps, int to
     uint32_t pb[NT][2], vs[2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      float p[4];
+      const float2 rs = r.scale(nt);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[u][nt][i] = ex2(p[u][nt][i]);
-      r.l[nt][0] += p[u][nt][0] + p[u][nt][2];
-      r.l[nt][1] += p[u][nt][1] + p[u][nt][3];
-      pb[nt][0] = transpose8x8(f16x2(p[u][nt][0], p[u][nt][1]));
-      pb[nt][1] = transpose8x8(f16x2(p[u][nt][2], p[u][nt][3]));
+      for (int i = 0; i < 4; ++i)  // (made again: fewer registers than kept from above)
+        p[i] = ex2(fmaf(s[u][nt][i], i & 1 ? rs.y : rs.x, -r.m[nt][i & 1]));
+      r.l[nt][0] += p[0] + p[2];
+      r.l[nt][1] += p[1] + p[3];
+      pb[nt][0] = transpose8x8(f16x2(p[0], p[1]));
+      pb[nt][1] = transpose8x8(f16x2(p[2], p[3]));
     }
     const uint8_t* grp = grps + u * group_bytes(D);
 #pragma unroll
@@ -431,7 +435,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
   __shared__ uint32_t cta_abort;
   __shared__ int sh_scan[kWarps], sh_first[3];
   __shared__ float2 sh_ml[kWarps][4];
-  __shared__ float sh_rs[S::kRows];
+  __shared__ __align__(8) float sh_rs[S::kRows];
 
   launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -630,9 +634,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
     if constexpr (!S::kQInRegs) {
       __syncthreads();
       r.qs = q_frag + lane;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        r.rs[nt][0] = sh_rs[8 * nt + 2 * t], r.rs[nt][1] = sh_rs[8 * nt + 2 * t + 1];
+      r.rss = reinterpret_cast<const float2*>(sh_rs) + t;
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
