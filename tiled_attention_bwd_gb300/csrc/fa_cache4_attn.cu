@@ -437,7 +437,6 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
   __shared__ float2 sh_ml[kWarps][4];
   __shared__ __align__(8) float sh_rs[S::kRows];
 
-  launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * S::kStages * S::kSlot;
@@ -448,6 +447,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
   if (lane < S::kStages) mbar_init(&full[warp][lane], 1);
   if (tid == 0) cta_abort = 0;
   fence_mbar_init();
+  wait_for_primary();
+  launch_dependents();
 
   // ---- this block's share of the units
   const int items = a.Hkv * a.row_blocks;
@@ -736,8 +737,9 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
 }
 
 // Joins the partial results of an item that lies in several blocks' shares,
-// in block order.  One block per row; the item's parts are dealt to its
-// warps, and a lane takes D / 32 dims.
+// in block order; a lane takes D / 32 dims.  Few parts (an item across one
+// border or two, as in a batch): a warp per row.  More (a long history): a
+// block per row, the parts dealt to its warps.
 template <int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32) cache4_join_kernel(Cache4AttnArgs a) {
   using S = Shape<D, NT>;
@@ -746,28 +748,34 @@ __global__ void __launch_bounds__(kWarps * 32) cache4_join_kernel(Cache4AttnArgs
   wait_for_primary();
   const int4 j = a.joins[blockIdx.x];
   if (j.x < 0) return;
-  const int b = j.x, hk = j.y / a.row_blocks, row = blockIdx.y;
-  const int r = (j.y - hk * a.row_blocks) * S::kRows + row;
-  const int n = a.q_lens ? a.q_lens[b] : a.T;
-  if (r >= a.rows || r % a.T >= min(n, a.T)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int parts = j.z - (int)blockIdx.x + 2;
+  const bool few = parts <= 4;
+  const int row = few ? blockIdx.y * kWarps + warp : blockIdx.y;
+  const int b = j.x, hk = j.y / a.row_blocks;
+  const int r = (j.y - hk * a.row_blocks) * S::kRows + row;
+  // (Uniform in the block where the block shares a row.)
+  if (row >= S::kRows || r >= a.rows || r % a.T >= min(a.q_lens ? a.q_lens[b] : a.T, a.T)) return;
   auto part = [&](int k) {
     return partial_of<D, NT>(a, k == 0 ? j.w : 2 * ((int)blockIdx.x + k - 1), row);
   };
+  const int first = few ? 0 : warp, step = few ? 1 : kWarps;
   float mx = kNoMax;
-  for (int k = threadIdx.x; k < parts; k += kWarps * 32) mx = fmaxf(mx, part(k).ml->x);
+  for (int k = few ? lane : threadIdx.x; k < parts; k += few ? 32 : kWarps * 32)
+    mx = fmaxf(mx, part(k).ml->x);
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-  if (lane == 0) sh_m[warp] = mx;
-  __syncthreads();
+  if (!few) {
+    if (lane == 0) sh_m[warp] = mx;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sh_m[w]);
+    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sh_m[w]);
+  }
   float acc[kDims], sum = 0.f;
 #pragma unroll
   for (int i = 0; i < kDims; ++i) acc[i] = 0.f;
 #pragma unroll 4
-  for (int k = warp; k < parts; k += kWarps) {
+  for (int k = first; k < parts; k += step) {
     const Partial p = part(k);
     const float2 ml = *p.ml;
     const float f = ex2(ml.x - mx);
@@ -780,22 +788,25 @@ __global__ void __launch_bounds__(kWarps * 32) cache4_join_kernel(Cache4AttnArgs
       acc[0] += f * v.x, acc[1] += f * v.y;
     }
   }
+  if (!few) {
 #pragma unroll
-  for (int i = 0; i < kDims; ++i) sh_o[warp][lane * kDims + i] = acc[i];
-  if (lane == 0) sh_l[warp] = sum;
-  __syncthreads();
-  sum = 0.f;
+    for (int i = 0; i < kDims; ++i) sh_o[warp][lane * kDims + i] = acc[i];
+    if (lane == 0) sh_l[warp] = sum;
+    __syncthreads();
+    if (warp > 0) return;
+    for (int w = 1; w < kWarps; ++w) {
+      sum += sh_l[w];
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) sum += sh_l[w];
+      for (int i = 0; i < kDims; ++i) acc[i] += sh_o[w][lane * kDims + i];
+    }
+  }
   const float inv = sum > 0.f || sum != sum ? a.v_scale / sum : 0.f;
   const size_t q_row = ((size_t)b * a.Hkv + hk) * a.rows + r;
-  if (threadIdx.x < D) {
-    float v = 0.f;
+  __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(a.o + q_row * D) + lane * (kDims / 2);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += sh_o[w][threadIdx.x];
-    a.o[q_row * D + threadIdx.x] = __float2bfloat16_rn(v * inv);
-  }
-  if (threadIdx.x == 0) a.lse[q_row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+  for (int i = 0; i < kDims; i += 2)
+    out[i / 2] = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
+  if (lane == 0) a.lse[q_row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
 template <int D, int NT>
@@ -807,18 +818,21 @@ cudaError_t run(const Cache4AttnArgs& a, int sm_count, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   int blocks = sm_count * S::kBlocksPerSm;
   if (blocks > kC4MaxBlocks) blocks = kC4MaxBlocks;
-  kernel<<<blocks, kWarps * 32, S::kSmem, stream>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  // The join's launch overlaps the kernel's work; it waits on the device.
+  // Either launch overlaps the work before it; the kernels wait for that on
+  // the device, before their first access to global memory.
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, S::kRows);
+  cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, kernel, a)) != cudaSuccess) return e;
+  cfg.gridDim = dim3(blocks, S::kRows);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, cache4_join_kernel<D, NT>, a);
 }
 
