@@ -147,6 +147,7 @@ def _attn(lib, q=16, cache=16, table=16, lens=16, ql=16, o=16, lse=16, ws=256,
     (INVALID, dict(H=1, Hkv=2)), (INVALID, dict(T=-1)),
     (INVALID, dict(scale=0.0)), (INVALID, dict(scale=float("nan"))),
     (INVALID, dict(gk=1.5)), (INVALID, dict(gv=0.3)), (INVALID, dict(q=0)),
+    (INVALID, dict(scale=1e30, gk=2.0 ** 60)),
     (INVALID, dict(q=8)), (INVALID, dict(cache=0)), (INVALID, dict(table=0)),
     (INVALID, dict(lens=0)), (INVALID, dict(ql=2)), (INVALID, dict(o=0)),
     (INVALID, dict(o=8)), (INVALID, dict(lse=0)), (INVALID, dict(lse=2)),
@@ -155,6 +156,7 @@ def _attn(lib, q=16, cache=16, table=16, lens=16, ql=16, o=16, lse=16, ws=256,
     (UNSUPPORTED, dict(pages=1 << 28)),
     (UNSUPPORTED, dict(B=1 << 20, H=1 << 12)),
     (UNSUPPORTED, dict(B=1 << 15, T=1 << 16)),
+    (UNSUPPORTED, dict(B=1 << 10, T=1 << 18, M=1 << 20, page=256)),
 ])
 def test_attention_refusals(lib, want, bad):
     assert _attn(lib, **bad) == want
@@ -377,6 +379,10 @@ ATTN = [  # B, H, Hkv, T, d, page, lens, q_lens, window
     (2, 10, 2, 5, 128, 64, [300, 70], [3, 5], -1),       # 25 rows: more row blocks
     (2, 4, 1, 33, 64, 16, [33, 129], [33, 20], 40),
     (1, 8, 8, 70, 128, 32, [70], None, -1),              # a prompt through the cache
+    (2, 8, 1, 3, 64, 64, [500, 129], [3, 1], -1),        # 24 rows
+    (2, 8, 1, 4, 64, 64, [500, 128], None, 33),          # 32 rows
+    (1, 12, 2, 4, 128, 32, [700], None, -1),             # 24 rows
+    (2, 7, 1, 7, 128, 16, [90, 640], [2, 7], -1),        # 49 rows
     (150, 2, 1, 1, 64, 16, [(7 * i) % 90 for i in range(150)], None, -1),
     (700, 1, 1, 2, 64, 16, [(5 * i) % 40 for i in range(700)], [i % 3 for i in range(700)], 9),
 ]
@@ -486,6 +492,32 @@ def test_attention_is_repeatable_and_shares_a_workspace_in_order():
     for a, b in zip(first, gpu_attn(c, workspace=ws)):
         assert torch.equal(a, b)
     check_attn(c, *first)
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """Pages beyond 4 GiB of a cache: the same as a small cache's."""
+    Hkv, d, page = 8, 128, 256
+    small = attn_case(2, 8, Hkv, 1, d, page, [600, 257], None, -1, seed=11)
+    want = gpu_attn(small)
+    per = fa.fa_cache4_page_bytes(Hkv, page, d)
+    n = small["cache"].shape[0]
+    pages = (5 << 30) // per
+    big = torch.empty((pages, Hkv, page // 16, 18 * d), dtype=torch.uint8, device="cuda:0")
+    big[pages - n:] = torch.from_numpy(small["cache"]).cuda()
+    table = torch.where(i32(small["table"]) >= 0, i32(small["table"]) + (pages - n), -1)
+    args = (small["q"].cuda(), big, table.contiguous(), i32(small["lens"]), small["scale"])
+    got = fa.fa_cache4_attn(*args, k_scale=small["gk"], v_scale=small["gv"])
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    # And written there: the last slots of the cache.
+    k = torch.randn((1, Hkv, 3, d), generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    slots = i32([[pages * page - 1, pages * page - 18, (pages - 1) * page]])
+    fa.fa_cache4_append(k, k, big, slots)
+    tiny = torch.zeros((1, Hkv, page // 16, 18 * d), dtype=torch.uint8, device="cuda:0")
+    tiny[0] = torch.from_numpy(small["cache"][n - 1]).cuda()
+    fa.fa_cache4_append(k, k, tiny, slots - (pages - 1) * page)
+    assert torch.equal(big[-1], tiny[0])
 
 
 @pytest.mark.gpu

@@ -271,6 +271,29 @@ def test_strided_output_leaves_the_rest():
 
 
 @pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last tokens as in a call of their own."""
+    N, H, Hkv, d, tail = 150000, 96, 16, 128, 40
+    dev = torch.device("cuda:0")
+    assert N * (H + 2 * Hkv) * d > 1 << 31
+    qkv = torch.empty((1, N, H + 2 * Hkv, d), dtype=torch.bfloat16, device=dev).normal_()
+    rope = torch.from_numpy(serve.rope_table(64, d)).to(dev)
+    pos = (torch.arange(N, dtype=torch.int32, device=dev) % 64)[None].contiguous()
+    w = torch.linspace(0.5, 1.5, d, device=dev)
+    full = fa.fa_qk_norm_rope(qkv, H, Hkv, rope, pos, w, w)
+    part = fa.fa_qk_norm_rope(qkv[:, -tail:], H, Hkv, rope, pos[:, -tail:].contiguous(), w, w)
+    for a, b in zip(full, part):
+        assert torch.equal(a[:, :, -tail:], b)
+    dqkv, dqw, dkw = fa.fa_qk_norm_rope_bwd(qkv, H, Hkv, rope, *full, pos, w, w)
+    last = fa.fa_qk_norm_rope_bwd(qkv[:, -tail:], H, Hkv, rope, *part,
+                                  pos[:, -tail:].contiguous(), w, w)
+    assert torch.equal(dqkv[:, -tail:], last[0])
+    # dw = sum of xh^2 w over all rows of about unit mean square.
+    for g, heads in ((dqw, H), (dkw, Hkv)):
+        assert torch.allclose(g / (N * heads), w, rtol=1e-2)
+
+
+@pytest.mark.gpu
 def test_captured_training_step_on_another_stream():
     """Norm and rotation, attention, its backward and theirs, captured once
     and replayed on other inputs, equal the eager calls."""

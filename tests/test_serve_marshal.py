@@ -141,3 +141,38 @@ def test_cache_refusals(rec):
         with pytest.raises(TypeError):
             bad()
     assert rec == []
+
+
+def test_the_call_is_made_on_its_own_device(monkeypatch):
+    """Tensors of another device than the current one: the entry point runs
+    with that device current and on its stream; errors carry the status."""
+    class Guard:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            log.append("enter %d" % self.device.index)
+
+        def __exit__(self, *a):
+            log.append("exit")
+
+    class Lib:
+        @staticmethod
+        def fa_x(*args):
+            log.append(args)
+            return status
+
+    log = []
+    monkeypatch.setattr(fa, "load_library", lambda: Lib)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i,
+                        raising=False)
+    status = 0
+    fa._launch("fa_x", torch.device("cuda:0"), 1, 2)
+    fa._launch("fa_x", torch.device("cuda:3"), 1, 2)
+    assert log == [(1, 2, 100), "enter 3", (1, 2, 103), "exit"]
+    status = 5
+    with pytest.raises(fa.FAError) as e:
+        fa._launch("fa_x", torch.device("cuda:0"))
+    assert e.value.status == 5 and "FA_ERR_WORKSPACE" in str(e.value)

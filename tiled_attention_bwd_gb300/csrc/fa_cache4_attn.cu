@@ -838,25 +838,30 @@ cudaError_t run(const Cache4AttnArgs& a, int sm_count, cudaStream_t stream) {
 
 }  // namespace
 
-// Rows of an item.  Wider items share the work of making K and V of codes (as
-// long as about six tiles of eight rows take) but fill whole tiles.
-int cache4_attn_rows(int rows) {
+// Rows of an item: what makes the least of the passes over the keys, each of
+// a cost by its width.  Measured, 16 requests of 8192 tokens x 8 heads (us):
+//   d = 128, 16 rows: 64 as 8 + 8, 51 as 16;  24: 88 as 8s, 64 at once;
+//            32: 84 as 16s, 106 at once (registers spill: not built);
+//            40: 119 as 16s, 109 as 24s;  512: 302 as 16s, 279 as 24s
+//   d = 64,  32 rows: 54 as 16s, 51 at once;  40: 75 as 16s, 72 as 24s;
+//            64: 97 as 16s, 86 as 32s;  512: 187 as 16s, 167 as 32s
+int cache4_attn_rows(int rows, int d) {
+  const int cost[2][4] = {{22, 26, 36, 43}, {32, 42, 54, 0}};
   int best = 8;
   long long least = 0;
-  for (int nt = 1; nt <= 4; ++nt) {
-    const long long cost = (rows + 8LL * nt - 1) / (8 * nt) * (6 + nt);
-    if (nt == 1 || cost < least) least = cost, best = 8 * nt;
+  for (int nt = 1; nt <= (d == 128 ? 3 : 4); ++nt) {
+    const long long c = (rows + 8LL * nt - 1) / (8 * nt) * cost[d == 128][nt - 1];
+    if (nt == 1 || c < least) least = c, best = 8 * nt;
   }
   return best;
 }
 
 cudaError_t launch_cache4_attn(const Cache4AttnArgs& a, int d, int sm_count, cudaStream_t stream) {
-  const int nt = cache4_attn_rows(a.rows) / 8;
+  const int nt = cache4_attn_rows(a.rows, d) / 8;
   if (d == 128)
     return nt == 1   ? run<128, 1>(a, sm_count, stream)
            : nt == 2 ? run<128, 2>(a, sm_count, stream)
-           : nt == 3 ? run<128, 3>(a, sm_count, stream)
-                     : run<128, 4>(a, sm_count, stream);
+                     : run<128, 3>(a, sm_count, stream);
   return nt == 1   ? run<64, 1>(a, sm_count, stream)
          : nt == 2 ? run<64, 2>(a, sm_count, stream)
          : nt == 3 ? run<64, 3>(a, sm_count, stream)

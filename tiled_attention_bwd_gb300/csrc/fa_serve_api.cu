@@ -258,7 +258,7 @@ fa_status fa_cache4_append(const void* k, const void* v, void* cache, const int*
 size_t fa_cache4_attn_workspace_size(int B, int H, int Hkv, int T, int d) {
   if (head_dim(d) != FA_OK || B <= 0 || H <= 0 || T <= 0 || Hkv <= 0 || H % Hkv != 0) return 0;
   if ((long long)B * H * T > INT_MAX) return 0;
-  const int rows = fa::cache4_attn_rows(H / Hkv * T);
+  const int rows = fa::cache4_attn_rows(H / Hkv * T, d);
   return align_up(fa::kC4MaxBlocks * sizeof(int4)) +
          align_up((size_t)fa::kC4MaxBlocks * 2 * rows * d * sizeof(float)) +
          (size_t)fa::kC4MaxBlocks * 2 * rows * sizeof(float2);
@@ -276,6 +276,8 @@ fa_status fa_cache4_attn(const void* q, const void* cache, const int* block_tabl
   if (H > 0 && (Hkv == 0 || Hkv > H || H % Hkv != 0)) return FA_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.0f)) return FA_ERR_INVALID_ARG;
   if (!cache_scale(k_scale) || !cache_scale(v_scale)) return FA_ERR_INVALID_ARG;
+  const float scale_log2 = scale * k_scale * 1.4426950408889634f;
+  if (!std::isfinite(scale_log2)) return FA_ERR_INVALID_ARG;
   if (((long long)max_blocks << shift) > INT_MAX || (long long)B * H > INT_MAX ||
       (long long)B * H * T > INT_MAX || (long long)B * max_blocks > INT_MAX)
     return FA_ERR_UNSUPPORTED;
@@ -310,13 +312,13 @@ fa_status fa_cache4_attn(const void* q, const void* cache, const int* block_tabl
   a.M = max_blocks;
   a.pages = pages;
   a.rows = H / Hkv * T;
-  const int rows = fa::cache4_attn_rows(a.rows);
+  const int rows = fa::cache4_attn_rows(a.rows, d);
   ws += align_up((size_t)fa::kC4MaxBlocks * 2 * rows * d * sizeof(float));
   a.part_ml = reinterpret_cast<float2*>(ws);
   a.row_blocks = (a.rows + rows - 1) / rows;
   a.shift = shift;
   a.window = window < 0 ? -1 : window;
-  a.scale_log2 = scale * k_scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.v_scale = v_scale;
   a.st = dev.st;
   a.timeout_ns = dev.timeout_ns;
