@@ -156,6 +156,7 @@ def _attn(lib, q=16, cache=16, table=16, lens=16, ql=16, o=16, lse=16, ws=256,
     (UNSUPPORTED, dict(pages=1 << 28)),
     (UNSUPPORTED, dict(B=1 << 20, H=1 << 12)),
     (UNSUPPORTED, dict(B=1 << 15, T=1 << 16)),
+    (UNSUPPORTED, dict(T=1 << 30, H=1, M=1 << 23, page=256)),
     (UNSUPPORTED, dict(B=1 << 10, T=1 << 18, M=1 << 20, page=256)),
 ])
 def test_attention_refusals(lib, want, bad):
@@ -383,6 +384,7 @@ ATTN = [  # B, H, Hkv, T, d, page, lens, q_lens, window
     (2, 8, 1, 4, 64, 64, [500, 128], None, 33),          # 32 rows
     (1, 12, 2, 4, 128, 32, [700], None, -1),             # 24 rows
     (2, 7, 1, 7, 128, 16, [90, 640], [2, 7], -1),        # 49 rows
+    (1, 16, 2, 5, 64, 32, [301], None, -1),              # 40 rows
     (150, 2, 1, 1, 64, 16, [(7 * i) % 90 for i in range(150)], None, -1),
     (700, 1, 1, 2, 64, 16, [(5 * i) % 40 for i in range(700)], [i % 3 for i in range(700)], 9),
 ]
@@ -435,6 +437,15 @@ def test_pages_outside_the_cache_hide_their_tokens():
     c["table"][0, 2], c["table"][0, 5] = -3, 10 ** 9
     c["table"][1, :4] = [-1, 10 ** 6, -2 ** 31, 2 ** 31 - 1]   # nothing left
     check_attn(c, *gpu_attn(c))
+
+
+@pytest.mark.gpu
+def test_a_window_of_everything_hides_nothing():
+    c = attn_case(2, 4, 2, 3, 64, 16, [100, 2], None, -1, seed=12)
+    want = gpu_attn(c)
+    for c["window"] in (2 ** 31 - 1, 1000, 100, 99):
+        for a, b in zip(want, gpu_attn(c)):
+            assert torch.equal(a, b)
 
 
 @pytest.mark.gpu

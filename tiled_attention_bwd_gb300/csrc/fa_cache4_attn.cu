@@ -6,7 +6,7 @@
 // values' sums rescaled when m grows.
 //
 // Work.  The query rows of one key/value head (H / Hkv heads x T tokens) are
-// taken 8 to 32 at a time; such a row block of one request and head is an
+// taken 8 to 40 at a time; such a row block of one request and head is an
 // item, its keys are cut into units of 128, and all items' units together
 // are dealt to the blocks in equal consecutive shares, whatever the lengths
 // (an item counts as kItemCost units more, for what it costs to begin and
@@ -41,7 +41,7 @@ constexpr int kWarps = 4;
 constexpr int kGroups = 2;                        // of a warp in a unit
 constexpr int kUnit = kWarps * kGroups * kGroup;  // tokens of a work unit
 constexpr int kItemCost = 3;                      // in units
-constexpr float kNoMax = -1e30f;                  // m of a row that has seen no key
+constexpr float kGroupsoMax = -1e30f;                  // m of a row that has seen no key
 constexpr float kUp = 8.0f;                       // P carries 2^kUp
 constexpr float kSlack = 6.0f;                    // growth of m that is left standing
 
@@ -184,7 +184,7 @@ template <int D, int NT>
 struct Shape {
   static constexpr int kRows = 8 * NT;
   static constexpr bool kQInRegs = NT <= 2;  // else Q's fragments are in shared memory
-  static constexpr int kTogether = NT <= 2 ? kGroups : 1;  // groups per softmax step
+  static constexpr int kTiles = D / 16;                    // 16-dim tiles of O^T
   static constexpr int kSlot = kGroups * group_bytes(D);
   static constexpr int kStages = 2;
   static constexpr int kBlocksPerSm = NT == 1 || (NT == 2 && D == 64) ? 3 : 2;
@@ -192,9 +192,10 @@ struct Shape {
   static constexpr int kPitch = D + 4;  // floats of a row in the join buffer
   static constexpr int kJoin = kWarps * 4 * kPitch * 4;  // four rows of every warp
   static constexpr int kQPitch = 2 * D + 16;             // bytes of a raw row of Q
-  static constexpr int kQRaw = kRows * kQPitch;          // twice
+  static constexpr int kQRaw = kRows * kQPitch;
+  static constexpr int kQBuffers = kQInRegs ? 2 : 1;
   static constexpr int kQFrag = kQInRegs ? 0 : NT * (D / 32) * 512;
-  static constexpr int kSmem = kRing + kJoin + 2 * kQRaw + kQFrag;
+  static constexpr int kSmem = kRing + kJoin + kQBuffers * kQRaw + kQFrag;
 };
 
 // Where the partial results of a block's first (2 c) and last (2 c + 1)
@@ -225,7 +226,7 @@ struct Rows {
   }
   // m: the row's maximum less kUp, in powers of two; weights are 2^(s - m).
   float m[NT][2], l[NT][2];
-  float o[D / 16][NT][4];
+  float o[Shape<D, NT>::kTiles][NT][4];
 };
 
 // One group's scores, S^T = K Q^T: tokens g and g + 8, rows 2t and 2t + 1.
@@ -276,9 +277,10 @@ __device__ __forceinline__ void scores(const uint8_t* grp, int g, int t, const R
 // 2t, 2t + 1 (low half of the group) and 2t + 8, 2t + 9.
 template <int D, int NT>
 __device__ __forceinline__ void values(const uint8_t* grp, int g, int t, const uint32_t (&vs)[2],
-                                       const uint32_t (&pb)[NT][2], float (&o)[D / 16][NT][4]) {
+                                       const uint32_t (&pb)[NT][2],
+                                       float (&o)[Shape<D, NT>::kTiles][NT][4]) {
   constexpr int kWords = D / 64;  // words of one token's eighth of the dims
-  uint32_t vc[2][2][kWords];      // [half][token parity][word]
+  uint32_t vc[2][2][kWords];      // [half of the group][token parity][word]
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint8_t* vp = grp + v_code_at(D, 8 * h + 2 * t, g);
@@ -319,15 +321,15 @@ struct Bounds {
   int len, window;
 };
 
-// kN groups' scores, minus infinity where a row does not see a token.
+// Both groups' scores, minus infinity where a row does not see a token.
 // kPlain: every row sees every token; else bit u of `there` says whether
 // group u was copied.
-template <int D, int NT, int kN, bool kPlain>
+template <int D, int NT, bool kPlain>
 __device__ __forceinline__ void masked_scores(const Rows<D, NT>& r, const uint8_t* grps, int tok,
                                               int there, const Bounds& bd, int g, int t,
-                                              float (&s)[kN][NT][4]) {
+                                              float (&s)[kGroups][NT][4]) {
 #pragma unroll
-  for (int u = 0; u < kN; ++u) scores<D, NT>(grps + u * group_bytes(D), g, t, r, s[u]);
+  for (int u = 0; u < kGroups; ++u) scores<D, NT>(grps + u * group_bytes(D), g, t, r, s[u]);
   if constexpr (!kPlain) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -336,7 +338,7 @@ __device__ __forceinline__ void masked_scores(const Rows<D, NT>& r, const uint8_
         const int pos = bd.pos0 + (bd.row0 + 8 * nt + 2 * t + i) % bd.T;
         const int hi = min(pos + 1, bd.len), lo = bd.window < 0 ? 0 : pos - bd.window;
 #pragma unroll
-        for (int u = 0; u < kN; ++u)
+        for (int u = 0; u < kGroups; ++u)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int j = tok + u * kGroup + g + 8 * h;
@@ -346,17 +348,17 @@ __device__ __forceinline__ void masked_scores(const Rows<D, NT>& r, const uint8_
   }
 }
 
-// kN groups' products.
-template <int D, int NT, int kN, bool kPlain>
-__device__ __forceinline__ void step(Rows<D, NT>& r, const uint8_t* grps, int tok, int there,
-                                     const Bounds& bd, int g, int t) {
-  float s[kN][NT][4], top = -INFINITY;
-  masked_scores<D, NT, kN, kPlain>(r, grps, tok, there, bd, g, t, s);
+// One slot of the ring: both groups' products.
+template <int D, int NT, bool kPlain>
+__device__ __forceinline__ void use_slot(Rows<D, NT>& r, const uint8_t* grps, int tok, int there,
+                                         const Bounds& bd, int g, int t) {
+  float s[kGroups][NT][4], top = -INFINITY;
+  masked_scores<D, NT, kPlain>(r, grps, tok, there, bd, g, t, s);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const float2 rs = r.scale(nt);
 #pragma unroll
-    for (int u = 0; u < kN; ++u)
+    for (int u = 0; u < kGroups; ++u)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         top = fmaxf(top, fmaf(s[u][nt][i], i & 1 ? rs.y : rs.x, -r.m[nt][i & 1]));
@@ -368,7 +370,7 @@ __device__ __forceinline__ void step(Rows<D, NT>& r, const uint8_t* grps, int to
       for (int i = 0; i < 2; ++i) {
         float mx = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < kN; ++u) mx = fmaxf(mx, fmaxf(s[u][nt][i], s[u][nt][i + 2]));
+        for (int u = 0; u < kGroups; ++u) mx = fmaxf(mx, fmaxf(s[u][nt][i], s[u][nt][i + 2]));
         mx *= i ? r.scale(nt).y : r.scale(nt).x;  // (positive: minus infinity stays)
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
@@ -377,11 +379,11 @@ __device__ __forceinline__ void step(Rows<D, NT>& r, const uint8_t* grps, int to
         r.m[nt][i] = mx;
         r.l[nt][i] *= f;
 #pragma unroll
-        for (int dt = 0; dt < D / 16; ++dt) r.o[dt][nt][i] *= f, r.o[dt][nt][i + 2] *= f;
+        for (int dt = 0; dt < Shape<D, NT>::kTiles; ++dt) r.o[dt][nt][i] *= f, r.o[dt][nt][i + 2] *= f;
       }
   }
 #pragma unroll
-  for (int u = 0; u < kN; ++u) {
+  for (int u = 0; u < kGroups; ++u) {
     uint32_t pb[NT][2], vs[2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -414,25 +416,16 @@ __device__ __forceinline__ void step(Rows<D, NT>& r, const uint8_t* grps, int to
   }
 }
 
-// One slot of the ring.
-template <int D, int NT, bool kPlain>
-__device__ __forceinline__ void use_slot(Rows<D, NT>& r, const uint8_t* slot, int tok, int there,
-                                         const Bounds& bd, int g, int t) {
-  constexpr int kN = Shape<D, NT>::kTogether;
-#pragma unroll
-  for (int u = 0; u < kGroups; u += kN)
-    step<D, NT, kN, kPlain>(r, slot + u * group_bytes(D), tok + u * kGroup, there >> u, bd, g, t);
-}
-
 template <int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
     cache4_attn_kernel(Cache4AttnArgs a) {
   using S = Shape<D, NT>;
-  constexpr int kSteps = D / 16;
+  constexpr int kTiles = S::kTiles;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kWarps][S::kStages];
   __shared__ int copied[kWarps][S::kStages];  // bit u: group u of the slot
   __shared__ uint32_t cta_abort;
+  __shared__ Cursor sh_load[kWarps], sh_use[kWarps];
   __shared__ int sh_scan[kWarps], sh_first[3];
   __shared__ float2 sh_ml[kWarps][4];
   __shared__ __align__(8) float sh_rs[S::kRows];
@@ -442,7 +435,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
   uint8_t* ring = smem + warp * S::kStages * S::kSlot;
   float* join = reinterpret_cast<float*>(smem + S::kRing);
   uint8_t* q_raw = smem + S::kRing + S::kJoin;
-  uint4* q_frag = reinterpret_cast<uint4*>(q_raw + 2 * S::kQRaw);
+  uint4* q_frag = reinterpret_cast<uint4*>(q_raw + S::kQBuffers * S::kQRaw);
   const WaitCtl ctl = {a.st, &cta_abort, a.timeout_ns};
   if (lane < S::kStages) mbar_init(&full[warp][lane], 1);
   if (tid == 0) cta_abort = 0;
@@ -515,12 +508,15 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
   // ---- the warp's own ring, one slot per unit.  Each lane works out where
   // one of the next 32 units' groups lie and issues those copies when its
   // turn comes.
-  Cursor load = use;
+  // (The loads' and the products' places are kept in shared memory, by warp:
+  // they are needed once per 32 units and once per segment.)
+  if (lane == 0) sh_load[warp] = sh_use[warp] = use;
+  __syncwarp();
   bool more = true;         // there are units left to load
   int put = 0, put_slot = 0;  // units passed by the loads, and their slot
   int turn = 0, turns = 0;    // place in the lanes' units
   const uint8_t* src[kGroups];
-  auto look_ahead = [&]() {
+  auto look_ahead = [&](const Cursor& load) {
     turn = 0;
     turns = min(32, load.end - load.unit);
 #pragma unroll
@@ -554,12 +550,16 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
     ++put;
     if (++put_slot == S::kStages) put_slot = 0;
     if (++turn == turns) {
+      Cursor load = sh_load[warp];
       load.unit += turns;
       if (load.unit == load.end) more = load.next(a);
-      if (more) look_ahead();
+      if (more) look_ahead(load);
+      __syncwarp();  // every lane has read the old place
+      if (lane == 0) sh_load[warp] = load;
+      __syncwarp();
     }
   };
-  look_ahead();
+  look_ahead(use);
   for (int i = 0; i < S::kStages && more; ++i) feed();
 
   // ---- Q: the next segment's raw rows are on their way while one is worked on
@@ -581,19 +581,18 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
   bool dead = false;
   for (int seg = 0;; ++seg) {
     // ---- one segment
-    const bool whole = use.unit == 0 && use.end == use.r.units;
-    const int row0 = use.rb * S::kRows;
-    const size_t q_row = first_row(use);
-    const int pos0 = use.r.len - use.r.ql;  // position of the first new token
+    const int row0 = sh_use[warp].rb * S::kRows;
+    const Bounds bd = {row0, a.T, sh_use[warp].r.len - sh_use[warp].r.ql, sh_use[warp].r.len, a.window};
     copies_done();
     __syncthreads();  // Q is there, and the other buffer's readers are done
-    {
-      Cursor then = use;
-      if (then.next(a)) fetch_q(then, (seg + 1) & 1);
-    }
+    auto fetch_next = [&]() {
+      Cursor then = sh_use[warp];
+      if (then.next(a)) fetch_q(then, (seg + 1) % S::kQBuffers);
+    };
+    if constexpr (S::kQBuffers == 2) fetch_next();
 
     Rows<D, NT> r;
-    const uint8_t* raw = q_raw + (seg & 1) * S::kQRaw;
+    const uint8_t* raw = q_raw + seg % S::kQBuffers * S::kQRaw;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       if (!S::kQInRegs && nt % kWarps != warp) continue;
@@ -634,28 +633,28 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
     }
     if constexpr (!S::kQInRegs) {
       __syncthreads();
+      fetch_next();  // the one buffer is free
       r.qs = q_frag + lane;
       r.rss = reinterpret_cast<const float2*>(sh_rs) + t;
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      r.m[nt][0] = r.m[nt][1] = kNoMax;
+      r.m[nt][0] = r.m[nt][1] = kGroupsoMax;
       r.l[nt][0] = r.l[nt][1] = 0.f;
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i)
+      for (int i = 0; i < kTiles; ++i)
         r.o[i][nt][0] = r.o[i][nt][1] = r.o[i][nt][2] = r.o[i][nt][3] = 0.f;
     }
-    const Bounds bd = {row0, a.T, pos0, use.r.len, a.window};
     // Tokens within [plain_lo, plain_hi) are seen by every row.
-    const int plain_hi = pos0 + 1, plain_lo = a.window < 0 ? 0 : use.r.len - 1 - a.window;
+    const int plain_hi = bd.pos0 + 1, plain_lo = a.window < 0 ? 0 : bd.len - 1 - a.window;
 
-    for (int un = dead ? use.end : use.unit; un < use.end; ++un) {
+    int tok = sh_use[warp].r.lo + sh_use[warp].unit * kUnit + warp * kGroups * kGroup;
+    for (int left = dead ? 0 : sh_use[warp].end - sh_use[warp].unit; left > 0; --left, tok += kUnit) {
       if (!wait_bar_warp(&full[warp][got_slot], parity, ctl, 0x511)) {
         dead = true;
         break;
       }
       const uint8_t* slot = ring + got_slot * S::kSlot;
-      const int tok = use.r.lo + un * kUnit + warp * kGroups * kGroup;
       const int there = copied[warp][got_slot];
       if (there == 3 && tok >= plain_lo && tok + kGroups * kGroup <= plain_hi)
         use_slot<D, NT, true>(r, slot, tok, there, bd, g, t);
@@ -668,6 +667,9 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
     }
 
     // ---- join the warps, four rows at a time: a warp writes one row
+    Cursor at = sh_use[warp];
+    const bool whole = at.unit == 0 && at.end == at.r.units;
+    const size_t q_row = first_row(at);
     const int part_slot = 2 * blockIdx.x + (seg == 0 ? 0 : 1);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -677,24 +679,24 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
         for (int x = 4; x < 32; x <<= 1) r.l[nt][i] += __shfl_xor_sync(0xffffffffu, r.l[nt][i], x);
       }
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      for (int four = 0; four < 2; ++four) {
         __syncthreads();  // the buffer's last readers are done
-        // Lane (g, t) holds dims g D/8 + 0 .. D/8 - 1 of rows 2t and 2t + 1.
-        if (t >> 1 == half) {
+        // Lane (g, t) holds dims g D/8 + 0 .. D/8 - 1 of rows 2t, 2t + 1.
+        if (t >> 1 == four) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int row = (2 * t + i) & 3;
             if (g == 0) sh_ml[warp][row] = make_float2(r.m[nt][i], r.l[nt][i]);
             float* dst = join + (warp * 4 + row) * S::kPitch + g * (D / 8);
 #pragma unroll
-            for (int dt = 0; dt < kSteps; dt += 2)
+            for (int dt = 0; dt < kTiles; dt += 2)
               *reinterpret_cast<float4*>(dst + 2 * dt) = make_float4(
                   r.o[dt][nt][i], r.o[dt][nt][i + 2], r.o[dt + 1][nt][i], r.o[dt + 1][nt][i + 2]);
           }
         }
         __syncthreads();
-        const int row = 8 * nt + 4 * half + warp, rr = row0 + row;
-        float mx = kNoMax, f[kWarps], sum = 0.f;
+        const int row = 8 * nt + 4 * four + warp, rr = row0 + row;
+        float mx = kGroupsoMax, f[kWarps], sum = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sh_ml[w][warp].x);
 #pragma unroll
@@ -702,7 +704,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
           f[w] = ex2(sh_ml[w][warp].x - mx);
           sum += f[w] * sh_ml[w][warp].y;
         }
-        const bool live = rr < a.rows && rr % a.T < use.r.ql;
+        const bool live = rr < a.rows && rr % a.T < at.r.ql;
         const float inv = sum > 0.f || sum != sum ? a.v_scale / sum : 0.f;
         const Partial part = partial_of<D, NT>(a, part_slot, row);
 #pragma unroll
@@ -727,7 +729,11 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
         }
       }
     }
-    if (!use.next(a)) break;
+    const bool again = at.next(a);
+    __syncwarp();  // every lane has read the old place
+    if (lane == 0) sh_use[warp] = at;
+    __syncwarp();
+    if (!again) break;
   }
   // A stopping block lets its copies land before it leaves.
   for (; got < put; ++got) {
@@ -760,7 +766,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache4_join_kernel(Cache4AttnArgs
     return partial_of<D, NT>(a, k == 0 ? j.w : 2 * ((int)blockIdx.x + k - 1), row);
   };
   const int first = few ? 0 : warp, step = few ? 1 : kWarps;
-  float mx = kNoMax;
+  float mx = kGroupsoMax;
   for (int k = few ? lane : threadIdx.x; k < parts; k += few ? 32 : kWarps * 32)
     mx = fmaxf(mx, part(k).ml->x);
 #pragma unroll
@@ -840,16 +846,16 @@ cudaError_t run(const Cache4AttnArgs& a, int sm_count, cudaStream_t stream) {
 
 // Rows of an item: what makes the least of the passes over the keys, each of
 // a cost by its width.  Measured, 16 requests of 8192 tokens x 8 heads (us):
-//   d = 128, 16 rows: 64 as 8 + 8, 51 as 16;  24: 88 as 8s, 64 at once;
-//            32: 84 as 16s, 106 at once (registers spill: not built);
-//            40: 119 as 16s, 109 as 24s;  512: 302 as 16s, 279 as 24s
-//   d = 64,  32 rows: 54 as 16s, 51 at once;  40: 75 as 16s, 72 as 24s;
-//            64: 97 as 16s, 86 as 32s;  512: 187 as 16s, 167 as 32s
+//   d = 128, 16 rows: 64 as 8 + 8, 51 as 16;  24: 88 as 8s, 62 at once;
+//            32: 84 as 16s, 84 at once (spilling: not built);
+//            40: 119 as 16s, 105 as 24s;  512: 301 as 16s, 265 as 24s
+//   d = 64,  32 rows: 54 as 16s, 51 at once;  40: 72 as 24s, 62 at once;
+//            64: 97 as 16s, 86 as 32s;  512: 167 as 32s, 165 as 40s
 int cache4_attn_rows(int rows, int d) {
-  const int cost[2][4] = {{22, 26, 36, 43}, {32, 42, 54, 0}};
+  const int cost[2][5] = {{22, 26, 36, 43, 52}, {32, 41, 52, 0, 0}};
   int best = 8;
   long long least = 0;
-  for (int nt = 1; nt <= (d == 128 ? 3 : 4); ++nt) {
+  for (int nt = 1; nt <= (d == 128 ? 3 : 5); ++nt) {
     const long long c = (rows + 8LL * nt - 1) / (8 * nt) * cost[d == 128][nt - 1];
     if (nt == 1 || c < least) least = c, best = 8 * nt;
   }
@@ -865,7 +871,8 @@ cudaError_t launch_cache4_attn(const Cache4AttnArgs& a, int d, int sm_count, cud
   return nt == 1   ? run<64, 1>(a, sm_count, stream)
          : nt == 2 ? run<64, 2>(a, sm_count, stream)
          : nt == 3 ? run<64, 3>(a, sm_count, stream)
-                   : run<64, 4>(a, sm_count, stream);
+         : nt == 4 ? run<64, 4>(a, sm_count, stream)
+                   : run<64, 5>(a, sm_count, stream);
 }
 
 }  // namespace fa

@@ -167,7 +167,7 @@ struct Cache4AttnArgs {
   DevState* st;
   uint64_t timeout_ns;
 };
-// Query rows of one work item: 8, 16, 24 or 32.
+// Query rows of one work item: a multiple of 8 up to 40.
 int cache4_attn_rows(int rows, int d);
 cudaError_t launch_cache4_attn(const Cache4AttnArgs& a, int d, int sm_count,
                                cudaStream_t stream);

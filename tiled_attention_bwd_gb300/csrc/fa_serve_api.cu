@@ -278,7 +278,8 @@ fa_status fa_cache4_attn(const void* q, const void* cache, const int* block_tabl
   if (!cache_scale(k_scale) || !cache_scale(v_scale)) return FA_ERR_INVALID_ARG;
   const float scale_log2 = scale * k_scale * 1.4426950408889634f;
   if (!std::isfinite(scale_log2)) return FA_ERR_INVALID_ARG;
-  if (((long long)max_blocks << shift) > INT_MAX || (long long)B * H > INT_MAX ||
+  // Positions, which begin at -T, less a window stay within an int.
+  if (((long long)max_blocks << shift) + T > INT_MAX || (long long)B * H > INT_MAX ||
       (long long)B * H * T > INT_MAX || (long long)B * max_blocks > INT_MAX)
     return FA_ERR_UNSUPPORTED;
   // A block's share of the work is counted in 31 bits.
@@ -317,7 +318,8 @@ fa_status fa_cache4_attn(const void* q, const void* cache, const int* block_tabl
   a.part_ml = reinterpret_cast<float2*>(ws);
   a.row_blocks = (a.rows + rows - 1) / rows;
   a.shift = shift;
-  a.window = window < 0 ? -1 : window;
+  // A window of the whole table hides nothing.
+  a.window = window < 0 || (long long)window >= ((long long)max_blocks << shift) ? -1 : window;
   a.scale_log2 = scale_log2;
   a.v_scale = v_scale;
   a.st = dev.st;
