@@ -10,7 +10,10 @@
  *
  * which is the interface of "RTX Flash Attention Implementation COMPLETE",
  * section "Usage Examples" (basic forward pass; training with backward pass),
- * with tensors laid out as [batch, heads, seq_len, head_dim].  The operation
+ * with tensors laid out as [batch, heads, seq_len, head_dim].  Before and
+ * behind it stand the norm of query and key heads with the rotation of
+ * positions, and a paged key/value cache held in 4 bits with the attention
+ * of new tokens over it (last section).  The operation
  * itself is O = softmax(scale * Q K^T [+ causal mask]) V with the online
  * softmax of the same page's "Online Softmax Algorithm" section (running max
  * m, running sum l); the backward recomputes P from the saved LSE, as in

@@ -35,6 +35,10 @@ What each function follows:
                  with one float32 scale each, and the forward on the
                  dequantised values ("GPU Performance Optimization Batch 1 --
                  Design Spec", Item 3, "Optional FP8 path").
+  serve       -- (submodule) norm of query and key heads with the rotation of
+                 positions and its gradient, the 4-bit cache's format and
+                 bookkeeping, and attention over such a cache, from their
+                 formulas.
   bwd         -- gradients dQ, dK, dV of L with dL/dO = dout, P recomputed
                  from the row's LSE ("GPU Performance Optimization Batch 1 --
                  Design Spec", Item 3, backward paragraph).  The formulas come

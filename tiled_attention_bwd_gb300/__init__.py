@@ -1,4 +1,5 @@
-"""Exact tiled attention (forward + backward) for GB300 / sm_103a.
+"""Exact tiled attention (forward + backward) for GB300 / sm_103a, with the
+norm and rotation before it and a 4-bit key/value cache behind it.
 
 The compute path is libfa.so (hand-written tcgen05/TMA kernels behind the C
 ABI of include/fa.h); this package only builds it, marshals arguments to it,
