@@ -111,6 +111,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
   __shared__ Chunk ch;
   const int tid = threadIdx.x, width = blockDim.x, rank = blockIdx.x;
   const int first = rank * width + tid, step = gridDim.x * width;
+  wait_for_stream();
   int count = a.free_count[0];
   count = count < 0 ? 0 : (count > a.P ? a.P : count);
   const int chunks = (a.R + width - 1) / width;
@@ -240,6 +241,7 @@ __global__ void __launch_bounds__(256) append_kernel(AppendArgs a) {
   const unsigned row = blockIdx.x * (256 / kBlk) + threadIdx.x / kBlk;
   if (row >= (unsigned)a.rows) return;
   const int blk = threadIdx.x % kBlk;
+  wait_for_stream();
   const unsigned bh = row / (unsigned)a.N, n = row - bh * a.N;
   const unsigned b = bh / (unsigned)a.Hkv, h = bh - b * a.Hkv;
   const int slot = __ldg(a.slots + (size_t)b * a.N + n);
@@ -309,26 +311,27 @@ cudaError_t launch_cache4_plan(PlanArgs a, cudaStream_t stream) {
   // One block for up to 8192 slots, as wide as there are requests or slots
   // (barriers of few warps are shorter), else a cluster of eight.
   const long long work = (long long)a.R * a.T;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = work <= 8 * kPlanThreads ? 1 : 8;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = work <= 8 * kPlanThreads ? 1 : 8;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(attr.val.clusterDim.x);
+  cfg.gridDim = dim3(attr[0].val.clusterDim.x);
   const long long width = work > a.R ? work : a.R;
   cfg.blockDim = dim3(width <= 128 ? 128 : (width <= 256 ? 256 : (width <= 512 ? 512 : kPlanThreads)));
   cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, plan_kernel, a);
 }
 
 cudaError_t launch_cache4_append(const AppendArgs& a, int d, cudaStream_t stream) {
   const int per = 256 / (d / 16);
   const dim3 grid((a.rows + per - 1) / per, 2);
-  if (d == 128) append_kernel<128><<<grid, 256, 0, stream>>>(a);
-  else append_kernel<64><<<grid, 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(d == 128 ? append_kernel<128> : append_kernel<64>, grid, dim3(256), 0,
+                           stream, a);
 }
 
 }  // namespace fa

@@ -96,10 +96,6 @@ __device__ __forceinline__ void copies_done() {
 __device__ __forceinline__ void launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
-__device__ __forceinline__ void wait_for_primary() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // What a request has, with the values from memory brought into range.
 struct Request {
   int len, ql;  // cached tokens, new tokens
@@ -440,7 +436,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
   if (lane < S::kStages) mbar_init(&full[warp][lane], 1);
   if (tid == 0) cta_abort = 0;
   fence_mbar_init();
-  wait_for_primary();
+  wait_for_stream();
   launch_dependents();
 
   // ---- this block's share of the units
@@ -751,7 +747,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache4_join_kernel(Cache4AttnArgs
   using S = Shape<D, NT>;
   constexpr int kDims = D / 32;
   __shared__ float sh_o[kWarps][D], sh_m[kWarps], sh_l[kWarps];
-  wait_for_primary();
+  wait_for_stream();
   const int4 j = a.joins[blockIdx.x];
   if (j.x < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -824,22 +820,10 @@ cudaError_t run(const Cache4AttnArgs& a, int sm_count, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   int blocks = sm_count * S::kBlocksPerSm;
   if (blocks > kC4MaxBlocks) blocks = kC4MaxBlocks;
-  // Either launch overlaps the work before it; the kernels wait for that on
-  // the device, before their first access to global memory.
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.dynamicSmemBytes = S::kSmem;
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, kernel, a)) != cudaSuccess) return e;
-  cfg.gridDim = dim3(blocks, S::kRows);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, cache4_join_kernel<D, NT>, a);
+  e = launch_overlapped(kernel, dim3(blocks), dim3(kWarps * 32), S::kSmem, stream, a);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(cache4_join_kernel<D, NT>, dim3(blocks, S::kRows), dim3(kWarps * 32), 0,
+                           stream, a);
 }
 
 }  // namespace

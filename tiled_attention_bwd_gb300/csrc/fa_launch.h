@@ -172,6 +172,30 @@ int cache4_attn_rows(int rows, int d);
 cudaError_t launch_cache4_attn(const Cache4AttnArgs& a, int d, int sm_count,
                                cudaStream_t stream);
 
+// Launches a kernel whose launch overlaps the end of the work before it in
+// the stream.  The kernel waits for that work on the device, by
+// wait_for_stream(), before its first access to global memory.
+template <typename... Params, typename... Args>
+cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, dim3 block,
+                              size_t smem, cudaStream_t stream, Args... args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void wait_for_stream() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+#endif
+
 // Lets a kernel use `bytes` of dynamic shared memory on the current device;
 // the attribute is set once per kernel (its own `done`) and device.
 cudaError_t allow_smem(const void* kernel, int bytes,

@@ -303,6 +303,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
   const int b = here.token / a.N;
   here.n = here.token - b * a.N;
   const R ring = {smem + warp * kFwdStages * R::kStage};
+  wait_for_stream();
   const bool turns = k.kind < 2;
   F2 w[8];
   if (kNorm && turns) load_weight(k.kind == 0 ? a.q_weight : a.k_weight, a.weight_bf16, l, w);
@@ -366,6 +367,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeArgs a) {
   const Lane l = lane_of<D, kInter>(a.rot);
   const int warp = threadIdx.x >> 5, id = blockIdx.x * kWarps + warp;
   const R ring = {smem + warp * kBwdStages * R::kStage};
+  wait_for_stream();
   F2 dw[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) dw[e] = 0;
@@ -479,7 +481,7 @@ template <int D>
 __global__ void __launch_bounds__(1024) rope_dw_kernel(RopeArgs a) {
   __shared__ float sums[32][33];
   const int col = blockIdx.x * 32 + threadIdx.x;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_stream();
   float s = 0.f;
 #pragma unroll 8
   for (int i = threadIdx.y; i < a.blocks; i += 32) s += a.partial[(size_t)i * 2 * D + col];
@@ -522,8 +524,8 @@ cudaError_t fwd(RopeArgs a, int sm_count, cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(rope_fwd_kernel<D, kInter, kNorm>), fwd_smem<D>(), done);
   if (e != cudaSuccess) return e;
-  rope_fwd_kernel<D, kInter, kNorm><<<blocks, kWarps * 32, fwd_smem<D>(), stream>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(rope_fwd_kernel<D, kInter, kNorm>, dim3(blocks), dim3(kWarps * 32),
+                           fwd_smem<D>(), stream, a);
 }
 
 template <int D, bool kInter, bool kNorm>
@@ -537,19 +539,10 @@ cudaError_t bwd(RopeArgs a, int sm_count, cudaStream_t stream) {
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(rope_bwd_kernel<D, kInter, kNorm>), bwd_smem<D>(), done);
   if (e != cudaSuccess) return e;
   if (blocks > 0)
-    rope_bwd_kernel<D, kInter, kNorm><<<blocks, kWarps * 32, bwd_smem<D>(), stream>>>(a);
-  e = cudaGetLastError();
+    e = launch_overlapped(rope_bwd_kernel<D, kInter, kNorm>, dim3(blocks), dim3(kWarps * 32),
+                          bwd_smem<D>(), stream, a);
   if (e != cudaSuccess || !kNorm) return e;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * D / 32);
-  cfg.blockDim = dim3(32, 32);
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rope_dw_kernel<D>, a);
+  return launch_overlapped(rope_dw_kernel<D>, dim3(2 * D / 32), dim3(32, 32), 0, stream, a);
 }
 
 template <bool kBwd>
