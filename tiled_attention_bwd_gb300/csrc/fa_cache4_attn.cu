@@ -96,6 +96,7 @@ __device__ __forceinline__ void copies_done() {
 __device__ __forceinline__ void launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+
 // What a request has, with the values from memory brought into range.
 struct Request {
   int len, ql;  // cached tokens, new tokens

@@ -191,6 +191,9 @@ cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, dim3 block,
   return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
 }
 #ifdef __CUDACC__
+// Every thread that touches global memory calls it first, and at least one
+// thread of a grid always does: a grid that ended without waiting would let
+// the one after it start before the one before it is done.
 __device__ __forceinline__ void wait_for_stream() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
