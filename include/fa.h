@@ -273,7 +273,7 @@ fa_status fa_step_host(const void* q, const void* k, const void* v,
  *   q_weight, k_weight : in, [d], bf16 (weight_bf16 = 1) or fp32 (0); both
  *               NULL: no norm, only the rotation
  *   q, k, v   : out, bf16 [B,H,N,d], [B,Hkv,N,d], [B,Hkv,N,d]
- * eps >= 0; H and Hkv are at most 8192, and an H of 0, or an Hkv of 0, is a
+ * The outputs overlap no input.  eps >= 0; H and Hkv are at most 8192, and an H of 0, or an Hkv of 0, is a
  * call for the other heads alone.
  */
 fa_status fa_qk_norm_rope(const void* qkv, long long stride_b,
@@ -288,7 +288,7 @@ fa_status fa_qk_norm_rope(const void* qkv, long long stride_b,
  * them) and the forward's qkv to dqkv (bf16, laid out like qkv, with strides
  * of its own) and, with weights, dq_weight and dk_weight (fp32 [d], summed
  * over all tokens and heads in an order that does not change from call to
- * call; zero without tokens).  dqkv may be qkv itself.  With weights it needs
+ * call; zero without tokens).  dqkv may be qkv itself, with its strides.  With weights it needs
  * fa_qk_norm_rope_bwd_workspace_size(d) bytes of device workspace, 16-byte
  * aligned, whose contents do not matter.
  */

@@ -156,6 +156,7 @@ def _attn(lib, q=16, cache=16, table=16, lens=16, ql=16, o=16, lse=16, ws=256,
     (UNSUPPORTED, dict(pages=1 << 28)),
     (UNSUPPORTED, dict(B=1 << 20, H=1 << 12)),
     (UNSUPPORTED, dict(B=1 << 15, T=1 << 16)),
+    (UNSUPPORTED, dict(B=1 << 20, M=1 << 10, page=256)),
     (UNSUPPORTED, dict(T=1 << 30, H=1, M=1 << 23, page=256)),
     (UNSUPPORTED, dict(B=1 << 10, T=1 << 18, M=1 << 20, page=256)),
 ])

@@ -79,8 +79,14 @@ def test_rope_strides_and_refusals(rec):
             lambda: fa.fa_qk_norm_rope_bwd(part, 4, 2, rope, q, k, k, dqkv=wide)):
         with pytest.raises(ValueError):
             bad()
-    with pytest.raises(TypeError):
-        fa.fa_qk_norm_rope_bwd(part, 4, 2, rope, q, None, k)
+    for bad in (lambda: fa.fa_qk_norm_rope_bwd(part, 4, 2, rope, q, None, k),
+                lambda: fa.fa_qk_norm_rope_bwd(part, 4, 2, rope, q, k, k, None,
+                                               w, w, workspace=1024)):
+        with pytest.raises(TypeError):
+            bad()
+    with pytest.raises(ValueError):        # a workspace on another device
+        fa.fa_qk_norm_rope_bwd(part, 4, 2, rope, q, k, k, None, w, w,
+                               workspace=torch.empty(1 << 20, device="meta"))
     assert len(rec) == n
 
 
@@ -132,6 +138,8 @@ def test_cache_refusals(rec):
             lambda: fa.fa_cache4_attn(q, cache, table[:2], new, 0.1),
             lambda: fa.fa_cache4_attn(q, cache, table, new[:2], 0.1),
             lambda: fa.fa_cache4_attn(q, cache, table, new, 0.1, new.long()),
+            lambda: fa.fa_cache4_attn(q, cache, table, new, 0.1,
+                                      workspace=torch.empty(9, device="meta")),
             lambda: fa.fa_cache4_attn(q, cache, table, new, 0.1, out=q.float())):
         with pytest.raises(ValueError):
             bad()

@@ -242,8 +242,8 @@ __global__ void __launch_bounds__(256) append_kernel(AppendArgs a) {
   if (row >= (unsigned)a.rows) return;
   const int blk = threadIdx.x % kBlk;
   wait_for_stream();
-  const unsigned bh = row / (unsigned)a.N, n = row - bh * a.N;
-  const unsigned b = bh / (unsigned)a.Hkv, h = bh - b * a.Hkv;
+  const unsigned bh = a.by_N.div(row), n = row - bh * a.N;
+  const unsigned b = a.by_Hkv.div(bh), h = bh - b * a.Hkv;
   const int slot = __ldg(a.slots + (size_t)b * a.N + n);
   if (slot < 0 || slot >= (int)(a.pages << a.shift)) return;
   const bool is_v = blockIdx.y != 0;

@@ -131,6 +131,24 @@ struct PlanArgs {
 };
 cudaError_t launch_cache4_plan(PlanArgs a, cudaStream_t stream);
 
+// Division of 0 <= x < 2^31 by a number fixed at launch: three instructions
+// instead of about twenty (Granlund and Montgomery, "Division by invariant
+// integers using multiplication", 1994).
+struct FastDiv {
+  uint32_t by, mul, shift;
+  static FastDiv of(uint32_t by) {
+    FastDiv f = {by, 0, 0};
+    while (f.shift < 31 && (1u << f.shift) < by) ++f.shift;
+    f.mul = (uint32_t)(((1ull << 32) * ((1ull << f.shift) - by)) / by + 1);
+    return f;
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ uint32_t div(uint32_t x) const {
+    return (__umulhi(mul, x) + x) >> shift;
+  }
+#endif
+};
+
 // New keys and values into their slots of the 4-bit cache.
 struct AppendArgs {
   const __nv_bfloat16 *k, *v;    // [B, Hkv, N, d]
@@ -139,6 +157,7 @@ struct AppendArgs {
   const int* slots;              // [B, N]
   int rows;                      // B * Hkv * N
   int N, Hkv, pages, shift;
+  FastDiv by_N, by_Hkv;
   float k_scale, v_scale;
 };
 cudaError_t launch_cache4_append(const AppendArgs& a, int d, cudaStream_t stream);

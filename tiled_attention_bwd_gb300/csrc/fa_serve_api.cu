@@ -248,6 +248,8 @@ fa_status fa_cache4_append(const void* k, const void* v, void* cache, const int*
   a.rows = B * Hkv * N;
   a.N = N;
   a.Hkv = Hkv;
+  a.by_N = fa::FastDiv::of(N);
+  a.by_Hkv = fa::FastDiv::of(Hkv);
   a.pages = pages;
   a.shift = shift;
   a.k_scale = k_scale;
@@ -282,7 +284,9 @@ fa_status fa_cache4_attn(const void* q, const void* cache, const int* block_tabl
   if (((long long)max_blocks << shift) + T > INT_MAX || (long long)B * H > INT_MAX ||
       (long long)B * H * T > INT_MAX || (long long)B * max_blocks > INT_MAX)
     return FA_ERR_UNSUPPORTED;
-  // A block's share of the work is counted in 31 bits.
+  // All requests' units of 128 keys together, and a block's share of the
+  // work, are counted in 31 bits.
+  if ((double)B * ((double)max_blocks * page_size / 128 + 4) > INT_MAX) return FA_ERR_UNSUPPORTED;
   if ((double)B * max_blocks * page_size * H * T > 0x1p45) return FA_ERR_UNSUPPORTED;
   if (B == 0 || H == 0 || T == 0) return FA_OK;
   if (!q || !seq_lens || !o || !lse || (pages > 0 && !cache) || (max_blocks > 0 && !block_table))

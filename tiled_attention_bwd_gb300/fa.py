@@ -550,6 +550,18 @@ def _output(name, t, shape, dtype, device):
     return t
 
 
+def _workspace(t, size, device):
+    """The caller's workspace (its size is checked by the library) or a new
+    one of `size` bytes; returns the tensor and its bytes."""
+    if t is None:
+        return torch.empty(size, dtype=torch.uint8, device=device), size
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % device)
+    return t, t.numel() * t.element_size()
+
+
 def _address(t):
     return None if t is None else t.data_ptr()
 
@@ -656,15 +668,14 @@ def fa_qk_norm_rope_bwd(qkv, H: int, Hkv: int, rope, dq, dk, dv,
     if q_weight is not None:
         dqw = torch.empty(d, dtype=torch.float32, device=dev)
         dkw = torch.empty(d, dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = torch.empty(
-                max(fa_qk_norm_rope_bwd_workspace_size(d), 16),
-                dtype=torch.uint8, device=dev)
-        size = workspace.numel() * workspace.element_size()
+        workspace, size = _workspace(
+            workspace, max(fa_qk_norm_rope_bwd_workspace_size(d), 16), dev)
+    else:
+        workspace = None
     _launch("fa_qk_norm_rope_bwd", dev, *args, float(eps),
-            1 if interleaved else 0, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dqkv.data_ptr(), dsb,
-            dsn, _address(dqw), _address(dkw), _address(workspace), size, B, N,
-            H, Hkv, d)
+            1 if interleaved else 0, dq.data_ptr(), dk.data_ptr(),
+            dv.data_ptr(), dqkv.data_ptr(), dsb, dsn, _address(dqw),
+            _address(dkw), _address(workspace), size, B, N, H, Hkv, d)
     return dqkv, dqw, dkw
 
 
@@ -764,14 +775,12 @@ def fa_cache4_attn(q, cache, block_table, seq_lens, scale: float, q_lens=None,
         _want("q_lens", q_lens, torch.int32, dev, (B,))
     out = _output("out", out, (B, H, T, d), torch.bfloat16, dev)
     lse = _output("lse", lse, (B, H, T), torch.float32, dev)
-    if workspace is None:
-        workspace = torch.empty(
-            max(fa_cache4_attn_workspace_size(B, H, Hkv, T, d), 256),
-            dtype=torch.uint8, device=dev)
+    workspace, size = _workspace(
+        workspace, max(fa_cache4_attn_workspace_size(B, H, Hkv, T, d), 256),
+        dev)
     _launch("fa_cache4_attn", dev, q.data_ptr(), cache.data_ptr(),
             block_table.data_ptr(), seq_lens.data_ptr(), _address(q_lens),
-            out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), B, H, Hkv, T, d, M,
-            pages, page, int(window), float(scale), float(k_scale),
+            out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size, B, H,
+            Hkv, T, d, M, pages, page, int(window), float(scale), float(k_scale),
             float(v_scale))
     return out, lse
