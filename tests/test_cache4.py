@@ -293,6 +293,17 @@ def test_append_matches_oracle(B, Hkv, N, d, page, gk, gv):
     assert np.array_equal(g_cache.cpu().numpy(), cache)
     for g, w in zip(out, want):
         assert np.array_equal(f64(g), w, equal_nan=True)
+    # Rows that are 16-byte aligned only.
+    odd = [torch.zeros(B * Hkv * N * d + 8, dtype=torch.bfloat16, device=dev)[8:].view_as(k)
+           for _ in range(4)]
+    odd[0].copy_(k), odd[1].copy_(v)
+    odd[2].fill_(7.0), odd[3].fill_(7.0)
+    assert odd[0].data_ptr() % 32 == 16
+    again = torch.from_numpy(cache.copy()).to(dev)
+    fa.fa_cache4_append(odd[0], odd[1], again, i32(slots), gk, gv, odd[2], odd[3])
+    assert torch.equal(again, g_cache)
+    for x, g in zip(odd[2:], out):
+        assert np.array_equal(f64(x), f64(g), equal_nan=True)
     # In place: the values may replace the keys and values themselves.
     k2, v2 = k.to(dev), v.to(dev)
     fa.fa_cache4_append(k2, v2, plain, i32(slots), gk, gv, k2, v2)
