@@ -14,8 +14,15 @@
 // warp takes 32 / (d/16) heads of one token at a time ("pack"): 4 at d = 128,
 // 8 at d = 64.  The two 8-value chunks of a lane are chosen such that both
 // members of every rotated pair are in one lane; the norm's sums are the only
-// exchange between lanes.  Everything is computed
-// in fp32 and rounded to bf16 once, at the store.
+// exchange between lanes.  Everything is computed in fp32 and rounded to
+// bf16 once, at the store.
+//
+// Bound by bytes, once the instructions are few enough: packed fp32
+// arithmetic, no division in the loop, loads that cost no registers.  On a
+// GB300 (copy bandwidth 6.71 TB/s): forward, 4 x 4096 tokens of 64 + 16 heads
+// of 128, 110 us or 6.2 TB/s; backward, 4 x 1024 tokens of 32 + 64 heads,
+// 49 us or 5.5 TB/s, and 7 x 3001 tokens of 24 + 16 heads of 64, half of each
+// rotated, 57 us or 5.4 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -282,7 +289,8 @@ struct Walk {
   __device__ __forceinline__ void advance(bool w) { at += w ? step + wrap : step; }
 };
 
-// Stages of the rings (3 to 6 of them measure the same within 2%).
+// Stages of the rings: 3 to 6 of them measure the same within 2%.  Three blocks
+// of the forward per SM (80 registers): 111 us at 4 x 4096 tokens, two 125.
 constexpr int kFwdStages = 3, kBwdStages = 4;
 template <int D>
 constexpr int fwd_smem() { return kWarps * kFwdStages * Ring<D, 1>::kStage; }
@@ -353,7 +361,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
 }
 
 // Backward.  The warps first take the query and key packs together, then the
-// value packs, which are only moved: all warps do the same work.  A lane sums
+// value packs, which are only moved: all warps do the same work (51 us at
+// 4 x 1024 tokens; 57 us with warps of value packs beside the others).  A lane sums
 // its 16 dims of its weight's gradient over all its rows; heads of a warp,
 // warps of a block (by kind) and blocks follow in that order, the last in
 // rope_dw_kernel: the result does not depend on which block runs first.
