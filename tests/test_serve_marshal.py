@@ -1,31 +1,71 @@
-"""The Python binding of the norm with rotation and of the 4-bit cache: the
-arguments that reach the C ABI, and what the binding refuses (CPU only: CUDA
-tensors are stood in for, and the library by a recorder)."""
+"""The binding of the norm with rotation and of the 4-bit cache: the arguments
+that reach the C ABI, and what the binding refuses (CPU only: the compiled
+binding is connected to entry points that record their arguments, and then
+takes CPU tensors)."""
+import ctypes
+
+import numpy as np
 import pytest
 import torch
 
+from tiled_attention_bwd_gb300 import build as fa_build
 from tiled_attention_bwd_gb300 import fa
 
 I32, BF16, F32 = torch.int32, torch.bfloat16, torch.float32
 
 
-class OnGpu(torch.Tensor):
-    """A CPU tensor that says it is on a GPU."""
-    is_cuda = True
-
-
 def z(*shape, dtype=BF16):
-    return torch.zeros(shape, dtype=dtype).as_subclass(OnGpu)
+    return torch.zeros(shape, dtype=dtype)
+
+
+class Recorder:
+    """Stands in for libfa.so: every entry point notes its arguments."""
+
+    def __init__(self, lib):
+        self.calls, self.streams, self.status = [], [], 0
+        sizes = {"fa_qk_norm_rope_bwd_workspace_size": 1024,
+                 "fa_cache4_attn_workspace_size": 512}
+        for name in fa._NATIVE:
+            real = getattr(lib, name)
+            kind = ctypes.CFUNCTYPE(real.restype, *real.argtypes)
+            if name in sizes:
+                f = kind(lambda *a, n=sizes[name]: n)
+            else:
+                f = kind(lambda *a, n=name: self.note(n, a))
+            setattr(self, name, f)
+
+    def note(self, name, args):
+        self.calls.append((name, args[:-1]))
+        self.streams.append(args[-1])
+        return self.status
+
+
+@pytest.fixture(scope="module")
+def lib():
+    fa_build.build()
+    return fa.load_library()
 
 
 @pytest.fixture
-def rec(monkeypatch):
-    calls = []
-    monkeypatch.setattr(fa, "_launch", lambda name, dev, *a: calls.append((name, a)))
-    for n, size in (("fa_cache4_attn_workspace_size", 512),
-                    ("fa_qk_norm_rope_bwd_workspace_size", 1024)):
-        monkeypatch.setattr(fa, n, lambda *a, size=size: size)
-    return calls
+def recorder(lib):
+    native = fa._native()
+    r = Recorder(lib)
+    fa._connect(native, r, host=True)
+    yield r
+    fa._connect(native, lib)
+    assert not any(r.streams)              # CPU tensors have none
+
+
+@pytest.fixture
+def rec(recorder):
+    return recorder.calls
+
+
+def same(got, want):
+    """Equal arguments, floats as the C side's fp32 rounds them."""
+    assert len(got) == len(want)
+    for a, b in zip(got, want):
+        assert a == (float(np.float32(b)) if isinstance(b, float) else b)
 
 
 def p(t):
@@ -38,7 +78,8 @@ def test_rope_calls(rec):
     pos, w = z(B, N, dtype=I32), z(d, dtype=F32)
     q, k, v = fa.fa_qk_norm_rope(qkv, H, Hkv, rope, pos, w, w, eps=0.5,
                                  interleaved=True)
-    assert rec[-1] == ("fa_qk_norm_rope", (
+    assert rec[-1][0] == "fa_qk_norm_rope"
+    same(rec[-1][1], (
         p(qkv), N * 8 * d, 8 * d, p(rope), 10, 32, p(pos), p(w), p(w), 0, 0.5,
         1, p(q), p(k), p(v), B, N, H, Hkv, d))
     assert q.shape == (B, H, N, d) and v.shape == (B, Hkv, N, d)
@@ -46,8 +87,8 @@ def test_rope_calls(rec):
                                             w.bfloat16(), w.bfloat16())
     name, a = rec[-1]
     assert name == "fa_qk_norm_rope_bwd" and a[6] is None and a[9] == 1
-    assert a[10:] == (1e-6, 0, p(q), p(k), p(v), p(dqkv), N * 8 * d, 8 * d,
-                      p(dqw), p(dkw), a[20], 1024, B, N, H, Hkv, d)
+    same(a[10:], (1e-6, 0, p(q), p(k), p(v), p(dqkv), N * 8 * d, 8 * d,
+                  p(dqw), p(dkw), a[20], 1024, B, N, H, Hkv, d))
     assert fa.fa_qk_norm_rope_bwd(qkv, H, Hkv, rope, q, k, v)[1:] == (None, None)
 
 
@@ -110,8 +151,8 @@ def test_cache_calls(rec):
     q = z(R, 8, T, 64)
     o, lse = fa.fa_cache4_attn(q, cache, table, lens, 0.25, new, 7, 2.0, 0.5)
     a = rec[-1][1]
-    assert a == (p(q), p(cache), p(table), p(lens), p(new), p(o), p(lse), a[7],
-                 512, R, 8, 4, T, 64, M, P, 32, 7, 0.25, 2.0, 0.5)
+    same(a, (p(q), p(cache), p(table), p(lens), p(new), p(o), p(lse), a[7],
+             512, R, 8, 4, T, 64, M, P, 32, 7, 0.25, 2.0, 0.5))
     assert lse.shape == (R, 8, T) and lse.dtype == F32
 
 
@@ -143,44 +184,50 @@ def test_cache_refusals(rec):
             lambda: fa.fa_cache4_attn(q, cache, table, new, 0.1, out=q.float())):
         with pytest.raises(ValueError):
             bad()
-    for bad in (lambda: fa.fa_cache4_append(k, k, cache, slots, k_out=k),
-                lambda: fa.fa_cache4_append(k, None, cache, slots),
+    with pytest.raises(ValueError):
+        fa.fa_cache4_append(k, k, cache, slots, k_out=k)
+    for bad in (lambda: fa.fa_cache4_append(k, None, cache, slots),
+                lambda: fa.fa_cache4_append(k, [1.0], cache, slots),
+                lambda: fa.fa_cache4_attn(q, cache, table, new, "0.1"),
                 lambda: fa.fa_cache4_plan(new, None, table, free, one, 16, 1)):
         with pytest.raises(TypeError):
             bad()
     assert rec == []
 
 
-def test_the_call_is_made_on_its_own_device(monkeypatch):
-    """Tensors of another device than the current one: the entry point runs
-    with that device current and on its stream; errors carry the status."""
-    class Guard:
-        def __init__(self, device):
-            self.device = device
+def test_errors_carry_the_status(recorder):
+    recorder.status = 5
+    new, table = z(3, dtype=I32), z(3, 5, dtype=I32)
+    cache = z(9, 4, 2, 18 * 64, dtype=torch.uint8)
+    k, slots, q = z(3, 4, 2, 64), z(3, 2, dtype=I32), z(3, 8, 2, 64)
+    rope, qkv = z(10, 32, dtype=F32), z(2, 3, 8, 64)
+    for call in (
+            lambda: fa.fa_cache4_plan(new, new, table, new, z(1, dtype=I32), 16, 1),
+            lambda: fa.fa_cache4_append(k, k, cache, slots),
+            lambda: fa.fa_cache4_attn(q, cache, table, new, 0.1),
+            lambda: fa.fa_qk_norm_rope(qkv, 4, 2, rope),
+            lambda: fa.fa_qk_norm_rope_bwd(qkv, 4, 2, rope, z(2, 4, 3, 64),
+                                           z(2, 2, 3, 64), z(2, 2, 3, 64))):
+        with pytest.raises(fa.FAError) as e:
+            call()
+        assert e.value.status == 5 and "FA_ERR_WORKSPACE" in str(e.value)
 
-        def __enter__(self):
-            log.append("enter %d" % self.device.index)
 
-        def __exit__(self, *a):
-            log.append("exit")
+def test_values_out_of_an_int_are_refused(rec):
+    new, table = z(3, dtype=I32), z(3, 5, dtype=I32)
+    cache, q = z(9, 4, 2, 18 * 64, dtype=torch.uint8), z(3, 8, 2, 64)
+    for bad in (
+            lambda: fa.fa_cache4_plan(new, new, table, new, z(1, dtype=I32), 1 << 40, 1),
+            lambda: fa.fa_cache4_plan(new, new, table, new, z(1, dtype=I32), 16, 1 << 40),
+            lambda: fa.fa_cache4_attn(q, cache, table, new, 0.1, window=1 << 31)):
+        with pytest.raises(ValueError):
+            bad()
+    assert rec == []
 
-    class Lib:
-        @staticmethod
-        def fa_x(*args):
-            log.append(args)
-            return status
 
-    log = []
-    monkeypatch.setattr(fa, "load_library", lambda: Lib)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    monkeypatch.setattr(torch.cuda, "device", Guard)
-    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i,
-                        raising=False)
-    status = 0
-    fa._launch("fa_x", torch.device("cuda:0"), 1, 2)
-    fa._launch("fa_x", torch.device("cuda:3"), 1, 2)
-    assert log == [(1, 2, 100), "enter 3", (1, 2, 103), "exit"]
-    status = 5
-    with pytest.raises(fa.FAError) as e:
-        fa._launch("fa_x", torch.device("cuda:0"))
-    assert e.value.status == 5 and "FA_ERR_WORKSPACE" in str(e.value)
+def test_cpu_tensors_are_refused(lib):
+    new, table = z(3, dtype=I32), z(3, 5, dtype=I32)
+    with pytest.raises(ValueError):
+        fa.fa_cache4_plan(new, new, table, new, z(1, dtype=I32), 16, 1)
+    with pytest.raises(ValueError):
+        fa.fa_qk_norm_rope(z(1, 1, 3, 64), 1, 1, z(4, 64, dtype=F32))

@@ -11,6 +11,7 @@ Names mirror the C ABI: ``fa_fwd``, ``fa_bwd``, ``fa_bwd_workspace_size``,
 ``fa_bwd_set_phase_events``, ``fa_status_string``.
 """
 import ctypes
+import importlib.util
 import os
 import re
 
@@ -18,6 +19,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libfa.so")
+BINDING_PATH = os.path.join(_PKG, "_lib", "_fa_binding.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "fa.h")
 
 FA_OK = 0
@@ -516,104 +518,38 @@ def fa_bwd_noalloc(q, k, v, o, lse, dout, causal: bool, scale: float, dq,
 
 # ---- norm with rotation, and the 4-bit cache.  A decode step makes several
 # of these calls per layer, each a few microseconds of GPU time, so their
-# checks are one pass of comparisons per tensor and the device context is
-# entered only where it is not the current one.
+# checks, outputs and stream are marshalled by compiled code
+# (csrc/fa_binding.cpp); the arguments are the same as in Python.
 
-def _want(name, t, dtype, device, shape):
-    """A contiguous tensor of this type, device and shape, or an error."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype \
-            and t.device == device and t.shape == shape and t.is_contiguous():
-        return
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s"
-                         % (name, tuple(t.shape), tuple(shape)))
-    raise ValueError("%s must be a contiguous %s tensor on %s"
-                     % (name, dtype, device))
+_native_module = None
+_NATIVE = ("fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
+           "fa_qk_norm_rope_bwd_workspace_size", "fa_cache4_plan",
+           "fa_cache4_append", "fa_cache4_attn",
+           "fa_cache4_attn_workspace_size")
 
 
-def _want_cuda(name, t, dtype, dims, what):
-    """A CUDA tensor of this type and number of axes (its device and sizes
-    are then the call's)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.dtype is not dtype or not t.is_cuda or t.dim() != dims:
-        raise ValueError("%s must be a %s" % (name, what))
+def _connect(module, lib, host=False):
+    """Hands the entry points' addresses to the compiled binding."""
+    module.connect({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
+                    for n in _NATIVE}, host)
 
 
-def _output(name, t, shape, dtype, device):
-    """The caller's output tensor (checked) or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _want(name, t, dtype, device, shape)
-    return t
-
-
-def _workspace(t, size, device):
-    """The caller's workspace (its size is checked by the library) or a new
-    one of `size` bytes; returns the tensor and its bytes."""
-    if t is None:
-        return torch.empty(size, dtype=torch.uint8, device=device), size
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("workspace must be a torch.Tensor")
-    if t.device != device or not t.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on %s" % device)
-    return t, t.numel() * t.element_size()
-
-
-def _address(t):
-    return None if t is None else t.data_ptr()
-
-
-def _launch(name, device, *args):
-    """Calls an entry point on the device's current stream."""
-    fn = getattr(load_library(), name)
-    index = device.index
-    if torch.cuda.current_device() == index:
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    if status != FA_OK:
-        raise FAError(name, status)
-
-
-def _token_strides(name, t):
-    """Strides of the batch and token axes of a [B,N,heads,d] tensor whose
-    tokens are contiguous rows (axes of length one may have any)."""
-    B, N, heads, d = t.shape
-    sb, sn, sh, sd = t.stride()
-    if t.numel() and ((d > 1 and sd != 1) or (heads > 1 and sh != d)):
-        raise ValueError("%s must have contiguous tokens [heads, d]" % name)
-    return (sb if B > 1 else 0), (sn if N > 1 else 0)
-
-
-def _rope_checks(qkv, H, Hkv, rope, positions, q_weight, k_weight):
-    """Checks of the arguments that the norm with rotation and its backward
-    share; returns the C arguments from qkv to the weights' type."""
-    _want_cuda("qkv", qkv, torch.bfloat16, 4, "bf16 CUDA tensor [B,N,heads,d]")
-    B, N, heads, d = qkv.shape
-    if H < 0 or Hkv < 0 or heads != H + 2 * Hkv:
-        raise ValueError("qkv has %d heads, expected H + 2 * Hkv = %d"
-                         % (heads, H + 2 * Hkv))
-    sb, sn = _token_strides("qkv", qkv)
-    dev = qkv.device
-    _want_cuda("rope", rope, torch.float32, 2, "fp32 CUDA tensor [positions, rot]")
-    rows, rot = rope.shape
-    _want("rope", rope, torch.float32, dev, (rows, rot))
-    if positions is not None:
-        _want("positions", positions, torch.int32, dev, (B, N))
-    bf16 = 0
-    if (q_weight is None) != (k_weight is None):
-        raise ValueError("q_weight and k_weight come together")
-    if q_weight is not None:
-        bf16 = int(getattr(q_weight, "dtype", None) is torch.bfloat16)
-        dtype = torch.bfloat16 if bf16 else torch.float32
-        _want("q_weight", q_weight, dtype, dev, (d,))
-        _want("k_weight", k_weight, dtype, dev, (d,))
-    return (qkv.data_ptr(), sb, sn, rope.data_ptr(), rows, rot,
-            _address(positions), _address(q_weight), _address(k_weight), bf16)
+def _native():
+    """The compiled binding, loaded and connected to libfa.so once.  Raises if
+    it is missing: there is no other path."""
+    global _native_module
+    if _native_module is None:
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(
+                "_fa_binding.so not found at %s; build it with "
+                "`python -m tiled_attention_bwd_gb300.build`" % BINDING_PATH)
+        spec = importlib.util.spec_from_file_location("_fa_binding",
+                                                      BINDING_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _connect(module, load_library())
+        _native_module = module
+    return _native_module
 
 
 def fa_qk_norm_rope(qkv, H: int, Hkv: int, rope, positions=None, q_weight=None,
@@ -627,14 +563,11 @@ def fa_qk_norm_rope(qkv, H: int, Hkv: int, rope, positions=None, q_weight=None,
     then rot/2 sines a row; positions: int32 [B,N] or None (0 .. N-1);
     q_weight, k_weight: [d], bf16 or fp32, or None for no norm.
     Returns (q [B,H,N,d], k [B,Hkv,N,d], v [B,Hkv,N,d])."""
-    args = _rope_checks(qkv, H, Hkv, rope, positions, q_weight, k_weight)
-    B, N, _, d = qkv.shape
-    dev = qkv.device
-    q = _output("q", q, (B, H, N, d), torch.bfloat16, dev)
-    k = _output("k", k, (B, Hkv, N, d), torch.bfloat16, dev)
-    v = _output("v", v, (B, Hkv, N, d), torch.bfloat16, dev)
-    _launch("fa_qk_norm_rope", dev, *args, float(eps), 1 if interleaved else 0,
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), B, N, H, Hkv, d)
+    status, q, k, v = _native().qk_norm_rope(
+        qkv, H, Hkv, rope, positions, q_weight, k_weight, eps,
+        bool(interleaved), q, k, v)
+    if status:
+        raise FAError("fa_qk_norm_rope", status)
     return q, k, v
 
 
@@ -649,49 +582,16 @@ def fa_qk_norm_rope_bwd(qkv, H: int, Hkv: int, rope, dq, dk, dv,
     """Backward of fa_qk_norm_rope.  Returns (dqkv [B,N,H+2*Hkv,d] bf16,
     dq_weight, dk_weight fp32 [d]; None without weights).  dqkv may be
     qkv."""
-    args = _rope_checks(qkv, H, Hkv, rope, positions, q_weight, k_weight)
-    B, N, heads, d = qkv.shape
-    dev = qkv.device
-    _want("dq", dq, torch.bfloat16, dev, (B, H, N, d))
-    _want("dk", dk, torch.bfloat16, dev, (B, Hkv, N, d))
-    _want("dv", dv, torch.bfloat16, dev, (B, Hkv, N, d))
-    if dqkv is None:
-        dqkv = torch.empty((B, N, heads, d), dtype=torch.bfloat16, device=dev)
-    else:
-        _want_cuda("dqkv", dqkv, torch.bfloat16, 4,
-                   "bf16 CUDA tensor [B,N,heads,d]")
-        if dqkv.shape != qkv.shape or dqkv.device != dev:
-            raise ValueError("dqkv must have qkv's shape and device")
-    dsb, dsn = _token_strides("dqkv", dqkv)
-    dqw = dkw = None
-    size = 0
-    if q_weight is not None:
-        dqw = torch.empty(d, dtype=torch.float32, device=dev)
-        dkw = torch.empty(d, dtype=torch.float32, device=dev)
-        workspace, size = _workspace(
-            workspace, max(fa_qk_norm_rope_bwd_workspace_size(d), 16), dev)
-    else:
-        workspace = None
-    _launch("fa_qk_norm_rope_bwd", dev, *args, float(eps),
-            1 if interleaved else 0, dq.data_ptr(), dk.data_ptr(),
-            dv.data_ptr(), dqkv.data_ptr(), dsb, dsn, _address(dqw),
-            _address(dkw), _address(workspace), size, B, N, H, Hkv, d)
+    status, dqkv, dqw, dkw = _native().qk_norm_rope_bwd(
+        qkv, H, Hkv, rope, dq, dk, dv, positions, q_weight, k_weight, eps,
+        bool(interleaved), dqkv, workspace)
+    if status:
+        raise FAError("fa_qk_norm_rope_bwd", status)
     return dqkv, dqw, dkw
 
 
 def fa_cache4_page_bytes(Hkv: int, page_size: int, d: int) -> int:
     return int(load_library().fa_cache4_page_bytes(Hkv, page_size, d))
-
-
-def _cache_sizes(cache):
-    """(pages, Hkv, page_size, d) of a 4-bit cache tensor, uint8
-    [pages, Hkv, page_size / 16, 18 * d]."""
-    _want_cuda("cache", cache, torch.uint8, 4,
-               "uint8 CUDA tensor [pages, Hkv, page_size / 16, 18 * d]")
-    pages, Hkv, groups, width = cache.shape
-    if width % 18 or not cache.is_contiguous():
-        raise ValueError("cache must be contiguous, its last axis 18 * d")
-    return pages, Hkv, 16 * groups, width // 18
 
 
 def fa_cache4_plan(new_tokens, lens, block_table, free_list, free_count,
@@ -702,49 +602,24 @@ def fa_cache4_plan(new_tokens, lens, block_table, free_list, free_count,
     [pages]; free_count: int32 [1].  lens, block_table, free_list and
     free_count are updated in place.  Returns (slots [R,T], positions [R,T],
     granted [R]), int32."""
-    i32 = torch.int32
-    _want_cuda("new_tokens", new_tokens, i32, 1, "int32 CUDA tensor [R]")
-    _want_cuda("block_table", block_table, i32, 2,
-               "int32 CUDA tensor [R, max_blocks]")
-    _want_cuda("free_list", free_list, i32, 1, "int32 CUDA tensor [pages]")
-    dev = new_tokens.device
-    R, M, P = new_tokens.shape[0], block_table.shape[1], free_list.shape[0]
-    _want("new_tokens", new_tokens, i32, dev, (R,))
-    _want("lens", lens, i32, dev, (R,))
-    _want("block_table", block_table, i32, dev, (R, M))
-    _want("free_list", free_list, i32, dev, (P,))
-    _want("free_count", free_count, i32, dev, (1,))
-    if T < 0:
-        raise ValueError("T must not be negative")
-    slots = _output("slots", slots, (R, T), i32, dev)
-    positions = _output("positions", positions, (R, T), i32, dev)
-    granted = _output("granted", granted, (R,), i32, dev)
-    _launch("fa_cache4_plan", dev, new_tokens.data_ptr(), lens.data_ptr(),
-            block_table.data_ptr(), free_list.data_ptr(),
-            free_count.data_ptr(), slots.data_ptr(), positions.data_ptr(),
-            granted.data_ptr(), R, M, P, page_size, T)
+    status, slots, positions, granted = _native().cache4_plan(
+        new_tokens, lens, block_table, free_list, free_count, page_size, T,
+        slots, positions, granted)
+    if status:
+        raise FAError("fa_cache4_plan", status)
     return slots, positions, granted
 
 
 def fa_cache4_append(k, v, cache, slots, k_scale: float = 1.0,
                      v_scale: float = 1.0, k_out=None, v_out=None):
     """Writes keys and values, bf16 [B,Hkv,N,d], to their slots (int32
-    [B,N]) of the 4-bit cache.  k_out and v_out, if given, receive the values
-    that the cache then holds (they may be k and v).  Returns the cache."""
-    pages, Hkv, page, d = _cache_sizes(cache)
-    _want_cuda("k", k, torch.bfloat16, 4, "bf16 CUDA tensor [B,Hkv,N,d]")
-    dev = cache.device
-    B, _, N, _ = k.shape
-    shape = (B, Hkv, N, d)
-    _want("k", k, torch.bfloat16, dev, shape)
-    _want("v", v, torch.bfloat16, dev, shape)
-    _want("slots", slots, torch.int32, dev, (B, N))
-    if k_out is not None or v_out is not None:
-        _want("k_out", k_out, torch.bfloat16, dev, shape)
-        _want("v_out", v_out, torch.bfloat16, dev, shape)
-    _launch("fa_cache4_append", dev, k.data_ptr(), v.data_ptr(),
-            cache.data_ptr(), slots.data_ptr(), float(k_scale),
-            float(v_scale), _address(k_out), _address(v_out), B, Hkv, N, d, pages, page)
+    [B,N]) of the 4-bit cache, uint8 [pages, Hkv, page_size / 16, 18 * d].
+    k_out and v_out, if given, receive the values that the cache then holds
+    (they may be k and v).  Returns the cache."""
+    status = _native().cache4_append(k, v, cache, slots, k_scale, v_scale,
+                                     k_out, v_out)
+    if status:
+        raise FAError("fa_cache4_append", status)
     return cache
 
 
@@ -761,26 +636,9 @@ def fa_cache4_attn(q, cache, block_table, seq_lens, scale: float, q_lens=None,
     [B, max_blocks]; seq_lens: int32 [B], the new tokens included; q_lens:
     int32 [B] new tokens of each request, or None for T.  Rows past a
     request's new tokens are left as they were.  Returns (O, LSE)."""
-    pages, Hkv, page, d = _cache_sizes(cache)
-    _want_cuda("q", q, torch.bfloat16, 4, "bf16 CUDA tensor [B,H,T,d]")
-    _want_cuda("block_table", block_table, torch.int32, 2,
-               "int32 CUDA tensor [B, max_blocks]")
-    dev = cache.device
-    B, H, T, _ = q.shape
-    M = block_table.shape[1]
-    _want("q", q, torch.bfloat16, dev, (B, H, T, d))
-    _want("block_table", block_table, torch.int32, dev, (B, M))
-    _want("seq_lens", seq_lens, torch.int32, dev, (B,))
-    if q_lens is not None:
-        _want("q_lens", q_lens, torch.int32, dev, (B,))
-    out = _output("out", out, (B, H, T, d), torch.bfloat16, dev)
-    lse = _output("lse", lse, (B, H, T), torch.float32, dev)
-    workspace, size = _workspace(
-        workspace, max(fa_cache4_attn_workspace_size(B, H, Hkv, T, d), 256),
-        dev)
-    _launch("fa_cache4_attn", dev, q.data_ptr(), cache.data_ptr(),
-            block_table.data_ptr(), seq_lens.data_ptr(), _address(q_lens),
-            out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size, B, H,
-            Hkv, T, d, M, pages, page, int(window), float(scale), float(k_scale),
-            float(v_scale))
+    status, out, lse = _native().cache4_attn(
+        q, cache, block_table, seq_lens, scale, q_lens, window, k_scale,
+        v_scale, out, lse, workspace)
+    if status:
+        raise FAError("fa_cache4_attn", status)
     return out, lse
