@@ -15,6 +15,7 @@
 #include "fa.h"
 #include "fa_common.cuh"
 #include "fa_launch.h"
+#include "fa_serve.h"
 
 namespace {
 

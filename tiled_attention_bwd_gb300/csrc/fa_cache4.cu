@@ -6,7 +6,7 @@
 #include <cuda_runtime.h>
 
 #include "fa_cache4.cuh"
-#include "fa_launch.h"
+#include "fa_serve.h"
 
 namespace fa {
 namespace {

@@ -43,7 +43,7 @@
 
 #include "fa_cache4.cuh"
 #include "fa_common.cuh"
-#include "fa_launch.h"
+#include "fa_serve.h"
 
 namespace fa {
 namespace {

@@ -28,7 +28,7 @@
 
 #include <type_traits>
 
-#include "fa_launch.h"
+#include "fa_serve.h"
 
 namespace fa {
 namespace {

@@ -8,7 +8,7 @@
 
 #include "fa.h"
 #include "fa_cache4.cuh"
-#include "fa_launch.h"
+#include "fa_serve.h"
 
 namespace {
 
