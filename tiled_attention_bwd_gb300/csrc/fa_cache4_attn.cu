@@ -184,6 +184,8 @@ struct Shares {
   __device__ __forceinline__ long long first(int c) const { return least * c + min(c, more); }
   __device__ __forceinline__ int block_of(long long u) const {
     const long long big = (least + 1) * more;
+    if ((u >> 31) == 0)
+      return u < big ? (int)u / (int)(least + 1) : more + (int)(u - big) / (int)least;
     return (int)(u < big ? u / (least + 1) : more + (u - big) / least);
   }
 };
@@ -487,8 +489,9 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
       r = request_of(a, ++b);
     }
     sh_first[0] = b;
-    sh_first[1] = (int)(left / r.cost());
-    sh_first[2] = (int)(left % r.cost());
+    // (left < cost * items fits 31 bits but for absurd sizes.)
+    sh_first[1] = left >> 31 ? (int)(left / r.cost()) : (int)left / r.cost();
+    sh_first[2] = (int)(left - (long long)sh_first[1] * r.cost());
   }
   __syncthreads();
   Cursor use;
@@ -499,19 +502,10 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
   use.r = request_of(a, use.b);
   use.segment(sh_first[2]);
 
-  // What the joining kernel does for this block's first item, if that began
-  // in the block before: the request, item, last block, and first partial.
-  if (tid == 0) {
-    int4 j = make_int4(-1, 0, 0, 0);
-    if (use.unit > 0) {
-      const long long i0 = u0 - sh_first[2], before_us = shares.first(blockIdx.x - 1);
-      if (before_us <= i0 + kItemCost)
-        j = make_int4(use.b, use.hk * a.row_blocks + use.rb, shares.block_of(i0 + use.r.cost() - 1),
-                      2 * (blockIdx.x - 1) + (before_us < i0 ? 1 : 0));
-    }
-    a.joins[blockIdx.x] = j;
+  if (use.end == use.unit) {  // a share of nothing but an item's cost
+    if (tid == 0) a.joins[blockIdx.x].x = -1;
+    return;
   }
-  if (use.end == use.unit) return;  // a share of nothing but an item's cost
 
   // ---- the warp's own ring, one slot per unit.  Each lane works out where
   // one of the next 32 units' groups lie and issues those copies when its
@@ -583,6 +577,21 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
       copy16_async(dst + i / kChunks * S::kQPitch + i % kChunks * 16, q + i * 16);
   };
   fetch_q(use, 0);
+
+  // What the joining kernel does for this block's first item, if that began
+  // in the block before: the request, item, last block, and first partial.
+  // (Here, the loads being on their way; by the last warp's first thread, the
+  // first group's warp being the one that is waited for.)
+  if (tid == (kWarps - 1) * 32) {
+    int4 j = make_int4(-1, 0, 0, 0);
+    if (use.unit > 0) {
+      const long long i0 = u0 - sh_first[2], before_us = shares.first(blockIdx.x - 1);
+      if (before_us <= i0 + kItemCost)
+        j = make_int4(use.b, use.hk * a.row_blocks + use.rb, shares.block_of(i0 + use.r.cost() - 1),
+                      2 * (blockIdx.x - 1) + (before_us < i0 ? 1 : 0));
+    }
+    a.joins[blockIdx.x] = j;
+  }
 
   int got = 0, got_slot = 0;
   uint32_t parity = 0;
