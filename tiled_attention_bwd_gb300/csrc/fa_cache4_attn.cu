@@ -52,7 +52,7 @@ constexpr int kWarps = 4;
 constexpr int kGroups = 2;                        // of a warp in a unit
 constexpr int kUnit = kWarps * kGroups * kGroup;  // tokens of a work unit
 constexpr int kItemCost = 3;                      // in units
-constexpr float kGroupsoMax = -1e30f;                  // m of a row that has seen no key
+constexpr float kNoMax = -1e30f;                  // m of a row that has seen no key
 constexpr float kUp = 8.0f;                       // P carries 2^kUp
 constexpr float kSlack = 6.0f;                    // growth of m that is left standing
 
@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      r.m[nt][0] = r.m[nt][1] = kGroupsoMax;
+      r.m[nt][0] = r.m[nt][1] = kNoMax;
       r.l[nt][0] = r.l[nt][1] = 0.f;
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)
@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
         }
         __syncthreads();
         const int row = 8 * nt + 4 * four + warp, rr = row0 + row;
-        float mx = kGroupsoMax, f[kWarps], sum = 0.f;
+        float mx = kNoMax, f[kWarps], sum = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sh_ml[w][warp].x);
 #pragma unroll
@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache4_join_kernel(Cache4AttnArgs
     return partial_of<D, NT>(a, k == 0 ? j.w : 2 * ((int)blockIdx.x + k - 1), row);
   };
   const int first = few ? 0 : warp, step = few ? 1 : kWarps;
-  float mx = kGroupsoMax;
+  float mx = kNoMax;
   for (int k = few ? lane : threadIdx.x; k < parts; k += few ? 32 : kWarps * 32)
     mx = fmaxf(mx, part(k).ml->x);
 #pragma unroll
