@@ -86,7 +86,8 @@ __device__ __forceinline__ Raw pack(const F2 (&x)[8]) {
   Raw r;
 #pragma unroll
   for (int c = 0; c < 2; ++c)
-    r.c[c] = make_uint4(pack2(x[4 * c]), pack2(x[4 * c + 1]), pack2(x[4 * c + 2]), pack2(x[4 * c + 3]));
+    r.c[c] = make_uint4(pack2(x[4 * c]), pack2(x[4 * c + 1]), pack2(x[4 * c + 2]),
+                        pack2(x[4 * c + 3]));
   return r;
 }
 
@@ -174,7 +175,8 @@ struct Ring {
                  "l"(src)
                  : "memory");
   }
-  __device__ __forceinline__ void turn_of(int stage, const Lane& l, F2 (&cs)[4], F2 (&sn)[4]) const {
+  __device__ __forceinline__ void turn_of(int stage, const Lane& l, F2 (&cs)[4],
+                                          F2 (&sn)[4]) const {
     const uint8_t* at = base + stage * kStage + kRows * 1024 + l.j * 16;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -183,7 +185,9 @@ struct Ring {
       d[0] = u.x, d[1] = u.y;
     }
   }
-  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  static __device__ __forceinline__ void commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
   template <int kLeft>
   static __device__ __forceinline__ void wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
@@ -223,7 +227,8 @@ __device__ __forceinline__ float sum_lanes(float v) {
 }
 
 // The lane's 16 norm weights, of either type (once per warp).
-__device__ __forceinline__ void load_weight(const void* w, int is_bf16, const Lane& l, F2 (&out)[8]) {
+__device__ __forceinline__ void load_weight(const void* w, int is_bf16, const Lane& l,
+                                            F2 (&out)[8]) {
   float f[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
@@ -315,8 +320,10 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
   const bool turns = k.kind < 2;
   F2 w[8];
   if (kNorm && turns) load_weight(k.kind == 0 ? a.q_weight : a.k_weight, a.weight_bf16, l, w);
-  Walk<const __nv_bfloat16> in(a.all, a.N, a.qkv + (size_t)k.column * D + l.c0, a.stride_b, a.stride_n, b, here.n);
-  Walk<__nv_bfloat16> out(a.all, a.N, (k.kind == 0 ? a.q : (k.kind == 1 ? a.k : a.v)) + (size_t)k.head * a.N * D + l.c0,
+  Walk<const __nv_bfloat16> in(a.all, a.N, a.qkv + (size_t)k.column * D + l.c0, a.stride_b,
+                               a.stride_n, b, here.n);
+  __nv_bfloat16* to = k.kind == 0 ? a.q : (k.kind == 1 ? a.k : a.v);
+  Walk<__nv_bfloat16> out(a.all, a.N, to + (size_t)k.head * a.N * D + l.c0,
                           (long long)k.heads * a.N * D, D, b, here.n);
 
   Place ahead = here;  // next to be fetched, with its position
@@ -393,11 +400,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeArgs a) {
     here.n = here.token - b * a.N;
     F2 w[8];
     if (kX) load_weight(k.kind == 0 ? a.q_weight : a.k_weight, a.weight_bf16, l, w);
-    Walk<const __nv_bfloat16> in(s, a.N, a.qkv + (size_t)k.column * D + l.c0, a.stride_b, a.stride_n, b, here.n);
-    Walk<const __nv_bfloat16> dz(s, a.N,
-                                 (k.kind == 0 ? a.dq : (k.kind == 1 ? a.dk : a.dv)) + (size_t)k.head * a.N * D + l.c0,
+    Walk<const __nv_bfloat16> in(s, a.N, a.qkv + (size_t)k.column * D + l.c0, a.stride_b,
+                                 a.stride_n, b, here.n);
+    const __nv_bfloat16* from = k.kind == 0 ? a.dq : (k.kind == 1 ? a.dk : a.dv);
+    Walk<const __nv_bfloat16> dz(s, a.N, from + (size_t)k.head * a.N * D + l.c0,
                                  (long long)k.heads * a.N * D, D, b, here.n);
-    Walk<__nv_bfloat16> out(s, a.N, a.dqkv + (size_t)k.column * D + l.c0, a.dstride_b, a.dstride_n, b, here.n);
+    Walk<__nv_bfloat16> out(s, a.N, a.dqkv + (size_t)k.column * D + l.c0, a.dstride_b, a.dstride_n,
+                            b, here.n);
     Place ahead = here;  // next to be fetched, with its position
     bool any = true;     // there is one
     int pos = kGrad ? position_of(a, ahead.token, ahead.n) : 0;
