@@ -19,10 +19,10 @@
 //
 // Bound by bytes, once the instructions are few enough: packed fp32
 // arithmetic, no division in the loop, loads that cost no registers.  On a
-// GB300 (copy bandwidth 6.71 TB/s): forward, 4 x 4096 tokens of 64 + 16 heads
-// of 128, 110 us or 6.2 TB/s; backward, 4 x 1024 tokens of 32 + 64 heads,
-// 49 us or 5.5 TB/s, and 7 x 3001 tokens of 24 + 16 heads of 64, half of each
-// rotated, 57 us or 5.4 TB/s.
+// GB300 (copy bandwidth 6.71 TB/s), in a stream of calls: forward, 4 x 4096
+// tokens of 64 + 16 heads of 128, 107 us or 6.3 TB/s; backward, 4 x 1024
+// tokens of 32 + 64 heads, 47 us or 5.8 TB/s, and 7 x 3001 tokens of 24 + 16
+// heads of 64, half of each rotated, 54 us or 5.6 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -8,7 +8,9 @@ the library has not been built, loading it raises immediately.
 Names mirror the C ABI: ``fa_fwd``, ``fa_bwd``, ``fa_bwd_workspace_size``,
 ``fa_check_device_status``, ``fa_set_wait_timeout_ns``,
 ``fa_debug_expire_wait``, ``fa_debug_expire_at``, ``fa_last_failure_site``,
-``fa_bwd_set_phase_events``, ``fa_status_string``.
+``fa_bwd_set_phase_events``, ``fa_status_string``; ``fa_qk_norm_rope``,
+``fa_qk_norm_rope_bwd``, ``fa_cache4_plan``, ``fa_cache4_append``,
+``fa_cache4_attn``.
 """
 import ctypes
 import importlib.util
