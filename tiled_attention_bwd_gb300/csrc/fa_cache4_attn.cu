@@ -200,7 +200,7 @@ struct Shape {
   static constexpr int kBlocksPerSm = NT == 1 || (NT == 2 && D == 64) ? 3 : 2;
   static constexpr int kRing = kWarps * kStages * kSlot;
   static constexpr int kPitch = D + 4;  // floats of a row in the join buffer
-  static constexpr int kJoin = kWarps * 4 * kPitch * 4;  // four rows of every warp
+  static constexpr int kJoin = kWarps * 8 * kPitch * 4;  // eight rows of every warp
   static constexpr int kQPitch = 2 * D + 16;             // bytes of a raw row of Q
   static constexpr int kQRaw = kRows * kQPitch;
   static constexpr int kQBuffers = kQInRegs ? 2 : 1;
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
   __shared__ uint32_t cta_abort;
   __shared__ Cursor sh_load[kWarps], sh_use[kWarps];
   __shared__ int sh_scan[kWarps], sh_first[3];
-  __shared__ float2 sh_ml[kWarps][4];
+  __shared__ float2 sh_ml[kWarps][8];
   __shared__ __align__(8) float sh_rs[S::kRows];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -683,45 +683,43 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
       if (more) feed();
     }
 
-    // ---- join the warps, four rows at a time: a warp writes one row
+    // ---- join the warps, eight rows at a time: a warp writes two
     Cursor at = sh_use[warp];
     const bool whole = at.unit == 0 && at.end == at.r.units;
     const size_t q_row = first_row(at);
     const int part_slot = 2 * blockIdx.x + (seg == 0 ? 0 : 1);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      // (The buffer's last readers are done: the segment began with a barrier.)
+      if (nt > 0) __syncthreads();
+      // Lane (g, t) holds dims g D/8 + 0 .. D/8 - 1 of rows 2t, 2t + 1.
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
+        float l = r.l[nt][i];
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) r.l[nt][i] += __shfl_xor_sync(0xffffffffu, r.l[nt][i], x);
+        for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+        const int row = 2 * t + i;
+        if (row0 + 8 * nt + row >= a.rows) continue;
+        if (g == 0) sh_ml[warp][row] = make_float2(r.m[nt][i], l);
+        float* dst = join + (warp * 8 + row) * S::kPitch + g * (D / 8);
+#pragma unroll
+        for (int dt = 0; dt < kTiles; dt += 2)
+          *reinterpret_cast<float4*>(dst + 2 * dt) = make_float4(
+              r.o[dt][nt][i], r.o[dt][nt][i + 2], r.o[dt + 1][nt][i], r.o[dt + 1][nt][i + 2]);
       }
+      __syncthreads();
 #pragma unroll
-      for (int four = 0; four < 2; ++four) {
-        __syncthreads();  // the buffer's last readers are done
-        // Lane (g, t) holds dims g D/8 + 0 .. D/8 - 1 of rows 2t, 2t + 1.
-        if (t >> 1 == four) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int row = (2 * t + i) & 3;
-            if (g == 0) sh_ml[warp][row] = make_float2(r.m[nt][i], r.l[nt][i]);
-            float* dst = join + (warp * 4 + row) * S::kPitch + g * (D / 8);
-#pragma unroll
-            for (int dt = 0; dt < kTiles; dt += 2)
-              *reinterpret_cast<float4*>(dst + 2 * dt) = make_float4(
-                  r.o[dt][nt][i], r.o[dt][nt][i + 2], r.o[dt + 1][nt][i], r.o[dt + 1][nt][i + 2]);
-          }
-        }
-        __syncthreads();
-        const int row = 8 * nt + 4 * four + warp, rr = row0 + row;
+      for (int k = 0; k < 2; ++k) {
+        const int in = warp + k * kWarps, row = 8 * nt + in, rr = row0 + row;
+        if (rr >= a.rows || rr % a.T >= at.r.ql) continue;
         float mx = kNoMax, f[kWarps], sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sh_ml[w][warp].x);
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sh_ml[w][in].x);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          f[w] = ex2(sh_ml[w][warp].x - mx);
-          sum += f[w] * sh_ml[w][warp].y;
+          f[w] = ex2(sh_ml[w][in].x - mx);
+          sum += f[w] * sh_ml[w][in].y;
         }
-        const bool live = rr < a.rows && rr % a.T < at.r.ql;
         const float inv = sum > 0.f || sum != sum ? a.v_scale / sum : 0.f;
         const Partial part = partial_of<D, NT>(a, part_slot, row);
 #pragma unroll
@@ -730,19 +728,19 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
           const int dim = 64 * i + 2 * lane;
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
-            const float2 v = *reinterpret_cast<const float2*>(join + (w * 4 + warp) * S::kPitch + dim);
+            const float2 v =
+                *reinterpret_cast<const float2*>(join + (w * 8 + in) * S::kPitch + dim);
             acc.x += f[w] * v.x, acc.y += f[w] * v.y;
           }
-          if (!whole) {
-            *reinterpret_cast<float2*>(part.o + dim) = acc;
-          } else if (live) {
+          if (whole)
             *reinterpret_cast<__nv_bfloat162*>(a.o + (q_row + row) * D + dim) =
                 __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-          }
+          else
+            *reinterpret_cast<float2*>(part.o + dim) = acc;
         }
         if (lane == 0) {
-          if (!whole) *part.ml = make_float2(mx, sum);
-          else if (live) a.lse[q_row + row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+          if (whole) a.lse[q_row + row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+          else *part.ml = make_float2(mx, sum);
         }
       }
     }
