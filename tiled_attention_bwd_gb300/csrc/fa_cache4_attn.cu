@@ -841,7 +841,8 @@ cudaError_t run(const Cache4AttnArgs& a, int sm_count, cudaStream_t stream) {
   if (blocks > kC4MaxBlocks) blocks = kC4MaxBlocks;
   e = launch_overlapped(kernel, dim3(blocks), dim3(kWarps * 32), S::kSmem, stream, a);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(cache4_join_kernel<D, NT>, dim3(blocks, S::kRows), dim3(kWarps * 32), 0,
+  const int rows = a.rows < S::kRows ? a.rows : S::kRows;
+  return launch_overlapped(cache4_join_kernel<D, NT>, dim3(blocks, rows), dim3(kWarps * 32), 0,
                            stream, a);
 }
 
