@@ -75,6 +75,12 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+// The same by a half of a pair: as __half2 the compiler takes the half in the
+// multiplication itself.
+__device__ __forceinline__ uint32_t mul2(uint32_t a, __half2 b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), b);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
@@ -243,7 +249,8 @@ struct Rows {
 template <int D, int NT>
 __device__ __forceinline__ void scores(const uint8_t* grp, int g, int t, const Rows<D, NT>& r,
                                        float (&s)[NT][4]) {
-  uint32_t kc[2][D / 32], ks[2][D / 64];
+  uint32_t kc[2][D / 32];
+  __half2 ks[2][D / 64];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint8_t* kp = grp + k_code_at(D, g + 8 * h, t * (D / 8));
@@ -252,12 +259,14 @@ __device__ __forceinline__ void scores(const uint8_t* grp, int g, int t, const R
       const uint4 u = *reinterpret_cast<const uint4*>(kp);
       kc[h][0] = u.x, kc[h][1] = u.y, kc[h][2] = u.z, kc[h][3] = u.w;
       const uint32_t two = e4m3_to_f16(*reinterpret_cast<const uint16_t*>(sp));
-      ks[h][0] = __byte_perm(two, 0, 0x1010);
-      ks[h][1] = __byte_perm(two, 0, 0x3232);
+      const __half2 th = *reinterpret_cast<const __half2*>(&two);
+      ks[h][0] = __low2half2(th);
+      ks[h][1] = __high2half2(th);
     } else {
       const uint2 u = *reinterpret_cast<const uint2*>(kp);
       kc[h][0] = u.x, kc[h][1] = u.y;
-      ks[h][0] = __byte_perm(e4m3_to_f16(*sp), 0, 0x1010);
+      const uint32_t two = e4m3_to_f16(*sp);
+      ks[h][0] = __low2half2(*reinterpret_cast<const __half2*>(&two));
     }
   }
 #pragma unroll
