@@ -176,37 +176,49 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
       if (ch.grow[o] > 0)
         a.block_table[(size_t)(r0 + o) * a.M + ch.keep[o] + j] = a.free_list[ch.at[o] - j];
     }
-    // Slots of four neighbouring tokens at a time where rows allow it.
-    const int w = a.T % 4 == 0 ? 4 : 1, per = a.T / w;
-    const unsigned all = (unsigned)n * per;
-    for (unsigned i = first; i < all; i += step) {
-      const int o = i / per, t0 = (i - o * per) * w, grow = ch.grow[o];
+    // Slots, for rows of four and more four neighbours at a time, which may
+    // lie across the end of a row.
+    const unsigned all = (unsigned)n * a.T, w = a.T >= 4 ? 4 : 1;
+    // Page p of request o; pages taken now come from the stack, as the table
+    // may not have them yet.
+    auto page_of = [&](int o, int p) {
+      const int j = p - ch.keep[o];
+      return j >= 0 ? a.free_list[ch.at[o] - j] : a.block_table[(size_t)(r0 + o) * a.M + p];
+    };
+    for (unsigned i = w * first; i < all; i += w * step) {
+      int o = a.by_T.div(i), tok = i - o * a.T;
       int slot[4] = {-1, -1, -1, -1}, pos[4] = {0, 0, 0, 0};
-      if (t0 < grow) {
-        int had = -1, page = 0;
+      const int in_page = (1 << a.shift) - 1;
+      if (tok + (int)w <= a.T) {  // of one request, on two pages at most
+        const int left = min(ch.grow[o] - tok, (int)w), at = ch.after[o] + tok;
+        if (left > 0) {
+          const int p0 = at >> a.shift, p1 = (at + left - 1) >> a.shift;
+          const int page0 = page_of(o, p0), page1 = p1 == p0 ? page0 : page_of(o, p1);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < left) {
+              pos[k] = at + k;
+              slot[k] = (pos[k] >> a.shift == p0 ? page0 : page1) * (in_page + 1) + (pos[k] & in_page);
+            }
+        }
+      } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          if (k < w && t0 + k < grow) {
-            pos[k] = ch.after[o] + t0 + k;
-            const int p = pos[k] >> a.shift, j = p - ch.keep[o];
-            // Pages taken now come from the stack: the table may not have
-            // them yet.
-            if (p != had) {
-              page = j >= 0 ? a.free_list[ch.at[o] - j] : a.block_table[(size_t)(r0 + o) * a.M + p];
-              had = p;
-            }
-            slot[k] = page * (1 << a.shift) + (pos[k] & ((1 << a.shift) - 1));
+          if (o < n && tok < ch.grow[o]) {
+            pos[k] = ch.after[o] + tok;
+            slot[k] = page_of(o, pos[k] >> a.shift) * (in_page + 1) + (pos[k] & in_page);
           }
+          if (++tok == a.T) tok = 0, ++o;
         }
       }
-      const size_t at = (size_t)(r0 + o) * a.T + t0;
-      if (w == 4 && a.wide) {
+      const size_t at = (size_t)r0 * a.T + i;
+      if (w == 4 && a.wide && i + 4 <= all) {
         *reinterpret_cast<int4*>(a.slots + at) = make_int4(slot[0], slot[1], slot[2], slot[3]);
         *reinterpret_cast<int4*>(a.positions + at) = make_int4(pos[0], pos[1], pos[2], pos[3]);
       } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (k < w) a.slots[at + k] = slot[k], a.positions[at + k] = pos[k];
+          if (k < w && i + k < all) a.slots[at + k] = slot[k], a.positions[at + k] = pos[k];
       }
     }
     __syncthreads();

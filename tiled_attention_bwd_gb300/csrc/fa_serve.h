@@ -48,22 +48,6 @@ cudaError_t launch_rope_fwd(const RopeArgs& a, int d, bool interleaved,
 cudaError_t launch_rope_bwd(const RopeArgs& a, int d, bool interleaved,
                             bool norm, int sm_count, cudaStream_t stream);
 
-// Block tables and slot maps of the paged cache.
-struct PlanArgs {
-  const int* new_tokens;  // [R]
-  int* lens;              // [R]
-  int* block_table;       // [R, M]
-  int* free_list;         // [P]
-  int* free_count;        // [1]
-  int* slots;             // [R, T]
-  int* positions;         // [R, T]
-  int* granted;           // [R]
-  int R, M, P, T;
-  int shift;              // log2 of the page size
-  int wide;               // set by the launcher: slots, positions 16-byte aligned
-};
-cudaError_t launch_cache4_plan(PlanArgs a, cudaStream_t stream);
-
 // Division of 0 <= x < 2^31 by a number fixed at launch: three instructions
 // instead of about twenty (Granlund and Montgomery, "Division by invariant
 // integers using multiplication", 1994).
@@ -81,6 +65,23 @@ struct FastDiv {
   }
 #endif
 };
+
+// Block tables and slot maps of the paged cache.
+struct PlanArgs {
+  const int* new_tokens;  // [R]
+  int* lens;              // [R]
+  int* block_table;       // [R, M]
+  int* free_list;         // [P]
+  int* free_count;        // [1]
+  int* slots;             // [R, T]
+  int* positions;         // [R, T]
+  int* granted;           // [R]
+  int R, M, P, T;
+  FastDiv by_T;
+  int shift;              // log2 of the page size
+  int wide;               // set by the launcher: slots, positions 16-byte aligned
+};
+cudaError_t launch_cache4_plan(PlanArgs a, cudaStream_t stream);
 
 // New keys and values into their slots of the 4-bit cache.
 struct AppendArgs {

@@ -219,6 +219,7 @@ fa_status fa_cache4_plan(const int* new_tokens, int* lens, int* block_table, int
   a.M = max_blocks;
   a.P = pages;
   a.T = T;
+  a.by_T = fa::FastDiv::of(T > 0 ? T : 1);
   a.shift = shift;
   return launched(fa::launch_cache4_plan(a, static_cast<cudaStream_t>(stream)));
 }
