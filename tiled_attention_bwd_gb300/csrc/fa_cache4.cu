@@ -104,7 +104,7 @@ __device__ __forceinline__ void grid_sync() {
 // grows pop in request order: taking back exactly what a call granted
 // restores the stack.  Bound by latency: a few rounds of dependent loads and
 // barriers.  (One block, with a request's pages moved by its own warp, took
-// 89 us for 48 prompts of 4096 tokens, 12288 pages; the cluster takes 12.)
+// 89 us for 48 prompts of 4096 tokens, 12288 pages; a cluster of 16 takes 7.)
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
   __shared__ Pages sh[32];
   __shared__ int sh_taken[32];
@@ -321,20 +321,50 @@ __global__ void __launch_bounds__(256) append_kernel(AppendArgs a) {
 
 }  // namespace
 
+// Blocks of the plan's large cluster on the current device: 16 where such a
+// cluster fits one of its GPCs (found out once per device), else the 8 that
+// always do.
+static unsigned plan_cluster() {
+  static std::atomic<unsigned> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 8;
+  std::atomic<unsigned>& blocks = known[dev & 63];
+  if (blocks.load() == 0) {
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 16;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int fit = 0;
+    const bool ok =
+        cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+            cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&fit, plan_kernel, &cfg) == cudaSuccess && fit > 0;
+    if (!ok) (void)cudaGetLastError();
+    blocks.store(ok ? 16 : 8);
+  }
+  return blocks.load();
+}
+
 cudaError_t launch_cache4_plan(PlanArgs a, cudaStream_t stream) {
-  a.wide = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15) == 0;
+  a.wide = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) &
+            15) == 0;
   // One block for up to 8192 slots, as wide as there are requests or slots
-  // (barriers of few warps are shorter), else a cluster of eight.
-  const long long work = (long long)a.R * a.T;
+  // (barriers of few warps are shorter), else a cluster: the slots are bound
+  // by how many SMs write them (48 prompts of 4096: 9.5 us by 8, 7.3 by 16).
+  const long long work = (long long)a.R * a.T, width = work > a.R ? work : a.R;
   cudaLaunchAttribute attr[2] = {};
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = work <= 8 * kPlanThreads ? 1 : 8;
+  attr[0].val.clusterDim.x = work <= 8 * kPlanThreads ? 1 : plan_cluster();
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(attr[0].val.clusterDim.x);
-  const long long width = work > a.R ? work : a.R;
   cfg.blockDim = dim3(width <= 128 ? 128 : (width <= 256 ? 256 : (width <= 512 ? 512 : kPlanThreads)));
   cfg.stream = stream;
   cfg.attrs = attr;
