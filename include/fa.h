@@ -394,9 +394,9 @@ fa_status fa_cache4_append(const void* k, const void* v, void* cache,
  *   workspace   : fa_cache4_attn_workspace_size(B, H, Hkv, T, d) bytes,
  *                 256-byte aligned; contents do not matter.  Calls that
  *                 share a workspace must not overlap in time.
- * Table entries outside [0, pages) hide their tokens.  Cached values that no
- * row of the request sees are never used, whatever they hold; a NaN that
- * some row sees may reach every row of the request and key/value head.
+ * Table entries outside [0, pages) hide their tokens.  A row uses nothing of
+ * tokens that it does not see, whatever they hold: a NaN scale reaches the
+ * rows that see its token (of a value, in its 16 dims) and no others.
  * The result does not depend on the order in which blocks run.  The kernel's
  * waits have the time limit of fa_set_wait_timeout_ns, where-code 0x511.
  */

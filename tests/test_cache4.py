@@ -444,6 +444,43 @@ def test_unseen_places_may_hold_anything(T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d,H,T,window,lens", [
+    (128, 4, 4, -1, [100, 36]),     # 8 rows
+    (128, 8, 5, 7, [40, 300]),      # 24 rows
+    (64, 4, 4, 9, [100, 31]),
+    (64, 16, 5, -1, [33, 129]),     # 40 rows
+])
+def test_a_nan_reaches_the_rows_that_see_it(d, H, T, window, lens):
+    """A NaN scale of a key or of a value, at tokens that the first rows, the
+    last rows, or (with a window) both do not see."""
+    page = 16
+    for of_key in (False, True):
+        for back in (0, 1, T - 1, T, T + 6):
+            c = attn_case(2, H, H // 4, T, d, page, lens, None, window, seed=back)
+            clean, cache = gpu_attn(c), c["cache"]
+            c["cache"] = cache.copy()
+            for b, n in enumerate(lens):
+                j = n - 1 - back
+                grp = c["cache"][c["table"][b, j // page], 0, j % page // 16]
+                _, ksa, _, vsa = serve._places(d, j % 16)
+                grp[(ksa if of_key else vsa)[back % (d // 16)]] = 0xff if back & 1 else 0x7f
+            ro, rl = serve.cache_attention(
+                f64(c["q"]), c["cache"], c["table"], c["lens"], None, c["scale"],
+                window, c["gk"], c["gv"])
+            o, lse = gpu_attn(c)
+            assert np.array_equal(np.isnan(f64(o)), np.isnan(ro))
+            assert np.array_equal(np.isnan(f64(lse)), np.isnan(rl))
+            # What is left is as without the NaN: with a value's to the bit,
+            # with a key's within the tolerance, as rows that share a tile
+            # grow their maxima together.
+            o, lse = (torch.where(torch.isnan(x), y, x) for x, y in zip((o, lse), clean))
+            if not of_key:
+                assert torch.equal(o, clean[0]) and torch.equal(lse, clean[1])
+            c["cache"] = cache
+            check_attn(c, o, lse)
+
+
+@pytest.mark.gpu
 def test_pages_outside_the_cache_hide_their_tokens():
     c = attn_case(2, 4, 1, 1, 64, 16, [130, 60], None, -1, seed=5)
     c["table"][0, 2], c["table"][0, 5] = -3, 10 ** 9

@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
       int o = a.by_T.div(i), tok = i - o * a.T;
       int slot[4] = {-1, -1, -1, -1}, pos[4] = {0, 0, 0, 0};
       const int in_page = (1 << a.shift) - 1;
-      if (tok + (int)w <= a.T) {  // of one request, on two pages at most
+      if (tok <= a.T - (int)w) {  // of one request, on two pages at most
         const int left = min(ch.grow[o] - tok, (int)w), at = ch.after[o] + tok;
         if (left > 0) {
           const int p0 = at >> a.shift, p1 = (at + left - 1) >> a.shift;

@@ -417,6 +417,7 @@ __device__ __forceinline__ void use_slot(Rows<D, NT>& r, const uint8_t* grps, in
       pb[nt][1] = transpose8x8(f16x2(p[2], p[3]));
     }
     const uint8_t* grp = grps + u * group_bytes(D);
+    uint32_t nans = 0;  // by token of the group: a scale of the lane's dims is NaN
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t two = *reinterpret_cast<const uint16_t*>(
@@ -428,10 +429,32 @@ __device__ __forceinline__ void use_slot(Rows<D, NT>& r, const uint8_t* grps, in
         const int lo = bd.window < 0 ? 0 : bd.pos0 - bd.window;
         if (j < lo || j >= bd.len) two &= 0xff00u;
         if (j + 1 < lo || j + 1 >= bd.len) two &= 0x00ffu;
+        const uint32_t nan = __vcmpeq4(two & 0x7f7fu, 0x7f7f7f7fu);
+        nans |= ((nan & 1) | (nan >> 7 & 2)) << (8 * h + 2 * t);
+        two &= ~nan;
       }
       vs[h] = e4m3_to_f16(two);
     }
     values<D, NT>(grp, g, t, vs, pb, r.o);
+    // A NaN goes to the rows that see its token, and not, by a weight of zero,
+    // to the others.
+    if (!kPlain && __any_sync(0xffffffffu, nans != 0)) {
+      nans |= __shfl_xor_sync(0xffffffffu, nans, 1);
+      nans |= __shfl_xor_sync(0xffffffffu, nans, 2);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int pos = bd.pos0 + (bd.row0 + 8 * nt + 2 * t + i) % bd.T, at = tok + u * kGroup;
+          const int hi = min(max(min(pos + 1, bd.len) - at, 0), kGroup);
+          const int lo = bd.window < 0 ? 0 : min(max(pos - bd.window - at, 0), kGroup);
+          if (nans & ((1u << hi) - 1) & ~((1u << lo) - 1)) {
+#pragma unroll
+            for (int dt = 0; dt < Shape<D, NT>::kTiles; ++dt)
+              r.o[dt][nt][i] = r.o[dt][nt][i + 2] = __uint_as_float(0x7fffffffu);
+          }
+        }
+    }
   }
 }
 
