@@ -245,6 +245,18 @@ def test_backward_in_place_and_repeatable():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H,Hkv,d", [(3, 1, 128), (5, 2, 64)])
+def test_weight_gradients_without_eps(H, Hkv, d):
+    """Heads that do not fill a warp, eps = 0: as with an eps far below the
+    rows' squares, whose effect is below fp32's rounding."""
+    x, gpu, args, kw, ref = setup((2, 9, H, Hkv, d, d, False, "f32", True, False))
+    grads = gpu["dq"], gpu["dk"], gpu["dv"]
+    want = fa.fa_qk_norm_rope_bwd(*args, *grads, eps=1e-30, **kw)
+    for a, b in zip(fa.fa_qk_norm_rope_bwd(*args, *grads, eps=0.0, **kw), want):
+        assert torch.isfinite(b).all() and torch.equal(a, b)
+
+
+@pytest.mark.gpu
 def test_no_tokens_give_zero_weight_gradients():
     dev = torch.device("cuda:0")
     z = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device=dev)  # noqa: E731

@@ -436,7 +436,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeArgs a) {
       if (kGrad) ring.turn_of(stage, l, cs, sn);
       fetch(stage == 0 ? kBwdStages - 1 : stage - 1);
       if constexpr (kGrad) {
-        if (!k.live) gx = Raw{};  // (its lanes' sums of dw stay zero)
+        if (!k.live) {  // no head: its lanes' sums of dw stay zero
+          gx = Raw{};
+          const uint32_t one = 0x3f803f80u;  // (a row of zeros without eps has no norm)
+          rx.c[0] = rx.c[1] = make_uint4(one, one, one, one);
+        }
         unpack(gx, g);
         turn<kInter, true>(g, cs, sn, l);
         if constexpr (kNorm) {
