@@ -273,8 +273,8 @@ fa_status fa_step_host(const void* q, const void* k, const void* v,
  *   q_weight, k_weight : in, [d], bf16 (weight_bf16 = 1) or fp32 (0); both
  *               NULL: no norm, only the rotation
  *   q, k, v   : out, bf16 [B,H,N,d], [B,Hkv,N,d], [B,Hkv,N,d]
- * The outputs overlap no input.  eps >= 0; H and Hkv are at most 8192, and an H of 0, or an Hkv of 0, is a
- * call for the other heads alone.
+ * The outputs overlap no input.  eps >= 0; H and Hkv are at most 8192, and
+ * an H of 0, or an Hkv of 0, is a call for the other heads alone.
  */
 fa_status fa_qk_norm_rope(const void* qkv, long long stride_b,
                           long long stride_n, const float* rope, int rope_rows,
@@ -288,7 +288,8 @@ fa_status fa_qk_norm_rope(const void* qkv, long long stride_b,
  * them) and the forward's qkv to dqkv (bf16, laid out like qkv, with strides
  * of its own) and, with weights, dq_weight and dk_weight (fp32 [d], summed
  * over all tokens and heads in an order that does not change from call to
- * call; zero without tokens).  dqkv may be qkv itself, with its strides.  With weights it needs
+ * call; zero without tokens).  dqkv may be qkv itself, with its strides; its
+ * tokens do not overlap.  With weights it needs
  * fa_qk_norm_rope_bwd_workspace_size(d) bytes of device workspace, 16-byte
  * aligned, whose contents do not matter.
  */
@@ -352,7 +353,7 @@ size_t fa_cache4_page_bytes(int Hkv, int page_size, int d);
  * including it are there (or it needs none), if n <= T, and if it fits
  * max_blocks pages; otherwise it is left as it was, granted 0.  Dropping what
  * one call granted restores the stack.  Values out of range in lens and
- * free_count are clamped.  The results feed fa_qk_norm_rope (positions),
+ * free_count are clamped.  No two of the arrays overlap.  The results feed fa_qk_norm_rope (positions),
  * fa_cache4_append (slots) and fa_cache4_attn (lens, granted, block_table).
  */
 fa_status fa_cache4_plan(const int* new_tokens, int* lens, int* block_table,
@@ -368,8 +369,9 @@ fa_status fa_cache4_plan(const int* new_tokens, int* lens, int* block_table,
  *   k_out, v_out : out, bf16 [B,Hkv,N,d], or both NULL: the values that the
  *                  cache now holds for these tokens, so that a prompt's
  *                  attention (fa_fwd_varlen) can use what later steps will
- *                  read.  They may be k and v themselves.  Rows of skipped
- *                  tokens are left as they were.
+ *                  read.  They may be k and v themselves, and overlap them
+ *                  in no other way.  Rows of skipped tokens are left as
+ *                  they were.
  * A slot that occurs twice in a call holds an unspecified mix of the two.
  */
 fa_status fa_cache4_append(const void* k, const void* v, void* cache,
@@ -391,6 +393,7 @@ fa_status fa_cache4_append(const void* k, const void* v, void* cache,
  *   o, lse      : out, bf16 [B,H,T,d], fp32 [B,H,T]; rows t >= q_lens[b] are
  *                 left as they were.  A row that sees no key gets o = 0 and
  *                 lse = -infinity.
+ *                 They overlap no input.
  *   workspace   : fa_cache4_attn_workspace_size(B, H, Hkv, T, d) bytes,
  *                 256-byte aligned; contents do not matter.  Calls that
  *                 share a workspace must not overlap in time.

@@ -88,8 +88,8 @@ def p(x):
     return ctypes.c_void_p(x) if x else None
 
 
-def _plan(lib, new=16, lens=16, table=16, free=16, count=16, slots=16, pos=16,
-          granted=16, R=1, M=1, P=1, page=16, T=1):
+def _plan(lib, new=256, lens=512, table=768, free=1024, count=1280, slots=1536,
+          pos=1792, granted=2048, R=1, M=1, P=1, page=16, T=1):
     return lib.fa_cache4_plan(p(new), p(lens), p(table), p(free), p(count),
                               p(slots), p(pos), p(granted), R, M, P, page, T,
                               None)
@@ -105,7 +105,9 @@ def _plan(lib, new=16, lens=16, table=16, free=16, count=16, slots=16, pos=16,
     (INVALID, dict(lens=0)), (INVALID, dict(table=0)), (INVALID, dict(free=0)),
     (INVALID, dict(count=0)), (INVALID, dict(slots=0)),
     (INVALID, dict(pos=0)), (INVALID, dict(granted=0)),
-    (INVALID, dict(lens=18)), (INVALID, dict(slots=17)),
+    (INVALID, dict(lens=514)), (INVALID, dict(slots=1537)),
+    (INVALID, dict(granted=256)), (INVALID, dict(slots=1792)),
+    (INVALID, dict(new=508, R=2)), (INVALID, dict(T=65)),
 ])
 def test_plan_refusals(lib, want, bad):
     assert _plan(lib, **bad) == want
@@ -126,7 +128,10 @@ def _append(lib, k=16, v=16, cache=16, slots=16, gk=1.0, gv=1.0, ko=0, vo=0,
     (INVALID, dict(gk=2.0 ** 61)), (INVALID, dict(gv=2.0 ** -61)),
     (INVALID, dict(ko=16)), (INVALID, dict(vo=16)), (INVALID, dict(k=0)),
     (INVALID, dict(v=8)), (INVALID, dict(cache=0)), (INVALID, dict(slots=2)),
-    (INVALID, dict(ko=8, vo=16)), (INVALID, dict(B=-1)),
+    (INVALID, dict(ko=1032, vo=2048)), (INVALID, dict(B=-1)),
+    (INVALID, dict(k=256, v=512, ko=512, vo=1024)),
+    (INVALID, dict(k=256, v=512, ko=1024, vo=1264)),
+    (INVALID, dict(k=256, v=512, ko=256, vo=528)),
     (UNSUPPORTED, dict(B=1 << 20, N=1 << 12)),
 ])
 def test_append_refusals(lib, want, bad):

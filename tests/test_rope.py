@@ -82,11 +82,11 @@ def _fwd(lib, qkv=16, rope=16, pos=16, qw=16, kw=16, q=16, k=16, v=16, B=1,
 
 
 def _bwd(lib, ptr=16, qkv=16, ws=16, ws_bytes=1 << 30, dw=16, qw=16, kw=16, B=1, N=1,
-         H=2, Hkv=1, d=128, rot=128, dsn=512):
+         H=2, Hkv=1, d=128, rot=128, dsn=512, dsb=512):
     p = lambda x: ctypes.c_void_p(x) if x else None  # noqa: E731
     return lib.fa_qk_norm_rope_bwd(p(qkv), 512, 512, p(16), 8, rot, p(16),
                                    p(qw), p(kw), 0, 1e-6, 0, p(ptr), p(ptr),
-                                   p(ptr), p(ptr), 512, dsn, p(dw), p(dw),
+                                   p(ptr), p(ptr), dsb, dsn, p(dw), p(dw),
                                    p(ws), ws_bytes, B, N, H, Hkv, d, None)
 
 
@@ -111,7 +111,9 @@ def test_forward_refusals(lib, want, bad):
 
 @pytest.mark.parametrize("want,bad", [
     (INVALID, dict(ptr=0)), (INVALID, dict(ptr=8)), (INVALID, dict(dw=0)),
-    (INVALID, dict(dsn=4)), (WORKSPACE, dict(ws=0)), (WORKSPACE, dict(ws=8)),
+    (INVALID, dict(dsn=4)), (INVALID, dict(N=2, dsn=0)),
+    (INVALID, dict(N=2, dsn=504)), (INVALID, dict(N=2, dsn=-504)),
+    (INVALID, dict(B=2, dsb=0)), (WORKSPACE, dict(ws=0)), (WORKSPACE, dict(ws=8)),
     (WORKSPACE, dict(ws_bytes=1000)), (UNSUPPORTED, dict(d=80)),
     (INVALID, dict(qkv=0)), (INVALID, dict(kw=0)),
 ])

@@ -19,6 +19,16 @@ fa_status head_dim(int d) {
   if (d <= 0) return FA_ERR_INVALID_ARG;
   return d == 64 || d == 128 ? FA_OK : FA_ERR_UNSUPPORTED;
 }
+// A piece of memory that a call reads or writes, and whether two share a byte.
+struct Span {
+  const void* p;
+  long long bytes;
+  bool meets(const Span& o) const {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
+    const uintptr_t apart = a <= b ? b - a : a - b;
+    return bytes > 0 && o.bytes > 0 && apart < (uintptr_t)(a <= b ? bytes : o.bytes);
+  }
+};
 fa_status launched(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
 
 // ------------------------------------------------------ norm and rotation
@@ -162,6 +172,11 @@ fa_status fa_qk_norm_rope_bwd(const void* qkv, long long stride_b, long long str
         !aligned(dk, 16) || !aligned(dv, 16) || !aligned(dqkv, 16))
       return FA_ERR_INVALID_ARG;
     if (dstride_b % 8 != 0 || dstride_n % 8 != 0) return FA_ERR_INVALID_ARG;
+    // (Tokens of the output may not lie on one another.)
+    const long long width = (H + 2LL * Hkv) * d;
+    if ((B > 1 && dstride_b < width && -dstride_b < width) ||
+        (N > 1 && dstride_n < width && -dstride_n < width))
+      return FA_ERR_INVALID_ARG;
   } else if (!norm) {
     return FA_OK;
   }
@@ -206,6 +221,13 @@ fa_status fa_cache4_plan(const int* new_tokens, int* lens, int* block_table, int
                         (const void*)free_list, (const void*)free_count, (const void*)slots,
                         (const void*)positions, (const void*)granted})
     if (!aligned(p, 4)) return FA_ERR_INVALID_ARG;
+  const Span spans[] = {{new_tokens, 4LL * R},      {lens, 4LL * R},
+                        {free_count, 4},            {granted, 4LL * R},
+                        {block_table, 4LL * R * max_blocks}, {free_list, 4LL * pages},
+                        {slots, 4LL * R * T},       {positions, 4LL * R * T}};
+  for (const Span& x : spans)
+    for (const Span* y = spans; y != &x; ++y)
+      if (x.meets(*y)) return FA_ERR_INVALID_ARG;
   fa::PlanArgs a = {};
   a.new_tokens = new_tokens;
   a.lens = lens;
@@ -239,6 +261,13 @@ fa_status fa_cache4_append(const void* k, const void* v, void* cache, const int*
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cache, 16) || !aligned(slots, 4) ||
       !aligned(k_out, 16) || !aligned(v_out, 16))
     return FA_ERR_INVALID_ARG;
+  if (k_out) {  // an output is its own input or neither
+    const long long bytes = 2LL * B * Hkv * N * d;
+    const Span ki = {k, bytes}, vi = {v, bytes}, ko = {k_out, bytes}, vo = {v_out, bytes};
+    if (ko.meets(vo) || ko.meets(vi) || vo.meets(ki) || (k_out != k && ko.meets(ki)) ||
+        (v_out != v && vo.meets(vi)))
+      return FA_ERR_INVALID_ARG;
+  }
   fa::AppendArgs a = {};
   a.k = static_cast<const __nv_bfloat16*>(k);
   a.v = static_cast<const __nv_bfloat16*>(v);
