@@ -431,16 +431,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeArgs a) {
       R::template wait<kBwdStages - 2>();
       __syncwarp();  // the table's pieces of other lanes; and all have read the last stage
       Raw gx = ring.row(stage, 0), rx = {};
-      if (kX && k.live) rx = ring.row(stage, 1);
+      if (kX) rx = ring.row(stage, 1);
       F2 g[8], cs[4], sn[4];
       if (kGrad) ring.turn_of(stage, l, cs, sn);
       fetch(stage == 0 ? kBwdStages - 1 : stage - 1);
       if constexpr (kGrad) {
-        if (!k.live) {  // no head: its lanes' sums of dw stay zero
-          gx = Raw{};
-          const uint32_t one = 0x3f803f80u;  // (a row of zeros without eps has no norm)
-          rx.c[0] = rx.c[1] = make_uint4(one, one, one, one);
-        }
         unpack(gx, g);
         turn<kInter, true>(g, cs, sn, l);
         if constexpr (kNorm) {
@@ -469,6 +464,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeArgs a) {
       if (a.tokens - here.token <= s.step) break;
       out.advance(here.advance(s, a.N));
     }
+    if (kX && !k.live)  // no head: whatever the ring held
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dw[e] = 0;
     R::template wait<0>();
     __syncwarp();  // the ring is free for the next deal
   };
