@@ -400,6 +400,8 @@ ATTN = [  # B, H, Hkv, T, d, page, lens, q_lens, window
     (2, 8, 1, 3, 64, 64, [500, 129], [3, 1], -1),        # 24 rows
     (2, 8, 1, 4, 64, 64, [500, 128], None, 33),          # 32 rows
     (1, 12, 2, 4, 128, 32, [700], None, -1),             # 24 rows
+    (2, 16, 2, 4, 128, 64, [300, 77], [4, 2], -1),       # 32 rows
+    (2, 8, 1, 8, 128, 16, [411, 66], [8, 3], 50),        # 64 rows
     (2, 7, 1, 7, 128, 16, [90, 640], [2, 7], -1),        # 49 rows
     (1, 16, 2, 5, 64, 32, [301], None, -1),              # 40 rows
     (150, 2, 1, 1, 64, 16, [(7 * i) % 90 for i in range(150)], None, -1),
@@ -451,7 +453,8 @@ def test_unseen_places_may_hold_anything(T):
 @pytest.mark.gpu
 @pytest.mark.parametrize("d,H,T,window,lens", [
     (128, 4, 4, -1, [100, 36]),     # 8 rows
-    (128, 8, 5, 7, [40, 300]),      # 24 rows
+    (128, 8, 5, 7, [40, 300]),      # 16 rows
+    (128, 16, 8, 7, [40, 300]),     # 32 rows
     (64, 4, 4, 9, [100, 31]),
     (64, 16, 5, -1, [33, 129]),     # 40 rows
 ])

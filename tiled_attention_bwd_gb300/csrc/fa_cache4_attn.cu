@@ -203,6 +203,8 @@ struct Shape {
   static constexpr int kTiles = D / 16;                    // 16-dim tiles of O^T
   static constexpr int kSlot = kGroups * group_bytes(D);
   static constexpr int kStages = 2;
+  // Groups of a step: both, but where the registers are full with sums.
+  static constexpr int kTogether = D == 128 && NT > 3 ? 1 : kGroups;
   static constexpr int kBlocksPerSm = NT == 1 || (NT == 2 && D == 64) ? 3 : 2;
   static constexpr int kRing = kWarps * kStages * kSlot;
   static constexpr int kPitch = D + 4;  // floats of a row in the join buffer
@@ -340,15 +342,15 @@ struct Bounds {
   int len, window;
 };
 
-// Both groups' scores, minus infinity where a row does not see a token.
+// kU groups' scores, minus infinity where a row does not see a token.
 // kPlain: every row sees every token; else bit u of `there` says whether
 // group u was copied.
-template <int D, int NT, bool kPlain>
+template <int D, int NT, int kU, bool kPlain>
 __device__ __forceinline__ void masked_scores(const Rows<D, NT>& r, const uint8_t* grps, int tok,
                                               int there, const Bounds& bd, int g, int t,
-                                              float (&s)[kGroups][NT][4]) {
+                                              float (&s)[kU][NT][4]) {
 #pragma unroll
-  for (int u = 0; u < kGroups; ++u) scores<D, NT>(grps + u * group_bytes(D), g, t, r, s[u]);
+  for (int u = 0; u < kU; ++u) scores<D, NT>(grps + u * group_bytes(D), g, t, r, s[u]);
   if constexpr (!kPlain) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -357,7 +359,7 @@ __device__ __forceinline__ void masked_scores(const Rows<D, NT>& r, const uint8_
         const int pos = bd.pos0 + (bd.row0 + 8 * nt + 2 * t + i) % bd.T;
         const int hi = min(pos + 1, bd.len), lo = bd.window < 0 ? 0 : pos - bd.window;
 #pragma unroll
-        for (int u = 0; u < kGroups; ++u)
+        for (int u = 0; u < kU; ++u)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int j = tok + u * kGroup + g + 8 * h;
@@ -367,17 +369,17 @@ __device__ __forceinline__ void masked_scores(const Rows<D, NT>& r, const uint8_
   }
 }
 
-// One slot of the ring: both groups' products.
-template <int D, int NT, bool kPlain>
-__device__ __forceinline__ void use_slot(Rows<D, NT>& r, const uint8_t* grps, int tok, int there,
-                                         const Bounds& bd, int g, int t) {
-  float s[kGroups][NT][4], top = -INFINITY;
-  masked_scores<D, NT, kPlain>(r, grps, tok, there, bd, g, t, s);
+// kU groups' products.
+template <int D, int NT, int kU, bool kPlain>
+__device__ __forceinline__ void use_groups(Rows<D, NT>& r, const uint8_t* grps, int tok, int there,
+                                           const Bounds& bd, int g, int t) {
+  float s[kU][NT][4], top = -INFINITY;
+  masked_scores<D, NT, kU, kPlain>(r, grps, tok, there, bd, g, t, s);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const float2 rs = r.scale(nt);
 #pragma unroll
-    for (int u = 0; u < kGroups; ++u)
+    for (int u = 0; u < kU; ++u)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         top = fmaxf(top, fmaf(s[u][nt][i], i & 1 ? rs.y : rs.x, -r.m[nt][i & 1]));
@@ -389,7 +391,7 @@ __device__ __forceinline__ void use_slot(Rows<D, NT>& r, const uint8_t* grps, in
       for (int i = 0; i < 2; ++i) {
         float mx = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < kGroups; ++u) mx = fmaxf(mx, fmaxf(s[u][nt][i], s[u][nt][i + 2]));
+        for (int u = 0; u < kU; ++u) mx = fmaxf(mx, fmaxf(s[u][nt][i], s[u][nt][i + 2]));
         mx *= i ? r.scale(nt).y : r.scale(nt).x;  // (positive: minus infinity stays)
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
@@ -402,7 +404,7 @@ __device__ __forceinline__ void use_slot(Rows<D, NT>& r, const uint8_t* grps, in
       }
   }
 #pragma unroll
-  for (int u = 0; u < kGroups; ++u) {
+  for (int u = 0; u < kU; ++u) {
     uint32_t pb[NT][2], vs[2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -456,6 +458,16 @@ __device__ __forceinline__ void use_slot(Rows<D, NT>& r, const uint8_t* grps, in
         }
     }
   }
+}
+
+// One slot of the ring.
+template <int D, int NT, bool kPlain>
+__device__ __forceinline__ void use_slot(Rows<D, NT>& r, const uint8_t* grps, int tok, int there,
+                                         const Bounds& bd, int g, int t) {
+  constexpr int kU = Shape<D, NT>::kTogether;
+#pragma unroll 1
+  for (int u = 0; u < kGroups; u += kU)
+    use_groups<D, NT, kU, kPlain>(r, grps + u * group_bytes(D), tok + u * kGroup, there >> u, bd, g, t);
 }
 
 template <int D, int NT>
@@ -883,15 +895,16 @@ cudaError_t run(const Cache4AttnArgs& a, int sm_count, cudaStream_t stream) {
 // Rows of an item: what makes the least of the passes over the keys, each of
 // a cost by its width.  Measured, 16 requests of 8192 tokens x 8 heads (us):
 //   d = 128, 16 rows: 64 as 8 + 8, 51 as 16;  24: 88 as 8s, 62 at once;
-//            32: 84 as 16s, 84 at once (spilling: not built);
-//            40: 119 as 16s, 105 as 24s;  512: 301 as 16s, 265 as 24s
+//            32: 83 as 16s, 76 at once;  40: 116 as 16s, 101 as 24s, 127 as
+//            32s, 105 at once (spilling: not built);  64: 146 as 24s, 131 as
+//            32s;  512 (x 4096 tokens): 261 as 24s, 250 as 32s
 //   d = 64,  32 rows: 54 as 16s, 51 at once;  40: 72 as 24s, 62 at once;
 //            64: 97 as 16s, 86 as 32s;  512: 167 as 32s, 165 as 40s
 int cache4_attn_rows(int rows, int d) {
-  const int cost[2][5] = {{22, 26, 36, 43, 52}, {32, 41, 52, 0, 0}};
+  const int cost[2][5] = {{22, 26, 36, 43, 52}, {32, 41, 52, 65, 0}};
   int best = 8;
   long long least = 0;
-  for (int nt = 1; nt <= (d == 128 ? 3 : 5); ++nt) {
+  for (int nt = 1; nt <= (d == 128 ? 4 : 5); ++nt) {
     const long long c = (rows + 8LL * nt - 1) / (8 * nt) * cost[d == 128][nt - 1];
     if (nt == 1 || c < least) least = c, best = 8 * nt;
   }
@@ -903,7 +916,8 @@ cudaError_t launch_cache4_attn(const Cache4AttnArgs& a, int d, int sm_count, cud
   if (d == 128)
     return nt == 1   ? run<128, 1>(a, sm_count, stream)
            : nt == 2 ? run<128, 2>(a, sm_count, stream)
-                     : run<128, 3>(a, sm_count, stream);
+           : nt == 3 ? run<128, 3>(a, sm_count, stream)
+                     : run<128, 4>(a, sm_count, stream);
   return nt == 1   ? run<64, 1>(a, sm_count, stream)
          : nt == 2 ? run<64, 2>(a, sm_count, stream)
          : nt == 3 ? run<64, 3>(a, sm_count, stream)
