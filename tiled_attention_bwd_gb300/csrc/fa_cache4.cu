@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
 // f16 (within 2^-11, which returns the half-way points exactly), then to the
 // code: the codes are those of the exact quotient.  (49 us at 8 x 4000 tokens
 // of 8 heads of 128 with a residual correction per quotient instead of the
-// two roundings; 36 us so in a stream of calls: 6.3 TB/s, and three quarters of
+// two roundings; 36 us so in a stream of calls: 6.3 TB/s, and seven tenths of
 // the issue slots.)
 template <int D>
 __global__ void __launch_bounds__(256) append_kernel(AppendArgs a) {

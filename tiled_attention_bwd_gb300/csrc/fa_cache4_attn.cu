@@ -28,12 +28,12 @@
 // 2^8 which keeps weights down to 2^-32 of the row's largest from vanishing.
 //
 // What bounds it is making f16 of 4-bit codes: a 16-token group of one head
-// costs 293 warp instructions (64 conversions, 64 products with scales, 24 to
+// costs 269 warp instructions (64 conversions, 64 products with scales, 24 to
 // put two tokens' value codes side by side, 16 matrix products, the softmax
 // and the loop), and twelve warps per SM find issue slots for 58% of the time.
 // Measured (d = 128, 8 query heads to a key/value head): 64 requests of 100 to
-// 8192 tokens x 8 heads 64 us, 4.8 TB/s of codes and scales; 3 requests of
-// 100000 to 131072 tokens x 8 heads 75 us, 5.3 TB/s; with all pages in L2
+// 8192 tokens x 8 heads 62 us, 4.9 TB/s of codes and scales; 3 requests of
+// 100000 to 131072 tokens x 8 heads 73 us, 5.5 TB/s; with all pages in L2
 // 2 us less.  Tiles: two groups per step (one: 98 us at the batch, two: 79),
 // blocks per SM three (four, at 128 registers: 72 us, three: 70), kItemCost
 // three units (one: 79 us, three: 72, five: 74).
