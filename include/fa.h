@@ -353,7 +353,9 @@ size_t fa_cache4_page_bytes(int Hkv, int page_size, int d);
  * including it are there (or it needs none), if n <= T, and if it fits
  * max_blocks pages; otherwise it is left as it was, granted 0.  Dropping what
  * one call granted restores the stack.  Values out of range in lens and
- * free_count are clamped.  No two of the arrays overlap.  The results feed fa_qk_norm_rope (positions),
+ * free_count are clamped; a token on a page outside [0, pages), which only a
+ * block_table or free_list that no call wrote can hold, gets the slot -1.  No
+ * two of the arrays overlap.  The results feed fa_qk_norm_rope (positions),
  * fa_cache4_append (slots) and fa_cache4_attn (lens, granted, block_table).
  */
 fa_status fa_cache4_plan(const int* new_tokens, int* lens, int* block_table,

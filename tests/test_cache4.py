@@ -226,6 +226,28 @@ def test_plan_matches_oracle(R, M, page, P, T, seed):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("bad", [-1, -2 ** 31, 40, 2 ** 28, 2 ** 31 - 1])
+@pytest.mark.parametrize("T", [3, 9])
+def test_plan_gives_no_slots_on_pages_outside_the_cache(bad, T):
+    """A bad id in the table (request 0) and in the stack (request 1)."""
+    page, n = 16, T - 1
+    table, lens = i32([[bad, -1], [3, -1]]), i32([10, 14])
+    free, count = i32([7, bad] + [0] * 38), i32([2])
+    slots, pos, granted = fa.fa_cache4_plan(i32([n, n]), lens, table, free,
+                                            count, page, T)
+    assert granted.tolist() == [n, n] and lens.tolist() == [10 + n, 14 + n]
+    ids = [[bad, bad if n > 6 else -1], [3, 7 if n > 6 else bad if n > 2 else -1]]
+    assert table.tolist() == ids
+    for r, at in ((0, 10), (1, 14)):
+        for t in range(T):
+            p = at + t
+            held = ids[r][p // page]
+            ok = t < n and 0 <= held < 40
+            assert slots[r, t].item() == (held * page + p % page if ok else -1)
+            assert pos[r, t].item() == (p if t < n else 0)
+
+
+@pytest.mark.gpu
 def test_plan_brings_values_into_range():
     """Lengths, counts and page ids that no call writes are clamped."""
     lens, table = i32([-7, 1 << 30, 5]), i32([[0, 1], [9, -4], [2, 3]])

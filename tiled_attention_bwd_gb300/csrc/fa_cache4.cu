@@ -185,10 +185,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
       const int j = p - ch.keep[o];
       return j >= 0 ? a.free_list[ch.at[o] - j] : a.block_table[(size_t)(r0 + o) * a.M + p];
     };
+    auto slot_of = [&](int page, int pos) {
+      return (unsigned)page < (unsigned)a.P ? (page << a.shift) + (pos & ((1 << a.shift) - 1)) : -1;
+    };
     for (unsigned i = w * first; i < all; i += w * step) {
       int o = a.by_T.div(i), tok = i - o * a.T;
       int slot[4] = {-1, -1, -1, -1}, pos[4] = {0, 0, 0, 0};
-      const int in_page = (1 << a.shift) - 1;
       if (tok <= a.T - (int)w) {  // of one request, on two pages at most
         const int left = min(ch.grow[o] - tok, (int)w), at = ch.after[o] + tok;
         if (left > 0) {
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
           for (int k = 0; k < 4; ++k)
             if (k < left) {
               pos[k] = at + k;
-              slot[k] = (pos[k] >> a.shift == p0 ? page0 : page1) * (in_page + 1) + (pos[k] & in_page);
+              slot[k] = slot_of(pos[k] >> a.shift == p0 ? page0 : page1, pos[k]);
             }
         }
       } else {
@@ -206,7 +208,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
         for (int k = 0; k < 4; ++k) {
           if (o < n && tok < ch.grow[o]) {
             pos[k] = ch.after[o] + tok;
-            slot[k] = page_of(o, pos[k] >> a.shift) * (in_page + 1) + (pos[k] & in_page);
+            slot[k] = slot_of(page_of(o, pos[k] >> a.shift), pos[k]);
           }
           if (++tok == a.T) tok = 0, ++o;
         }
