@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(256) append_kernel(AppendArgs a) {
   wait_for_stream();
   const unsigned bh = a.by_N.div(row), n = row - bh * a.N;
   const unsigned b = a.by_Hkv.div(bh), h = bh - b * a.Hkv;
-  const int slot = __ldg(a.slots + (size_t)b * a.N + n);
+  const int slot = a.slots[(size_t)b * a.N + n];
   if (slot < 0 || slot >= (int)(a.pages << a.shift)) return;
   const bool is_v = blockIdx.y != 0;
   const size_t at = (size_t)row * D + blk * 16;

@@ -125,9 +125,9 @@ struct Request {
 __device__ __forceinline__ Request request_of(const Cache4AttnArgs& a, int b) {
   Request r;
   const long long cap = (long long)a.M << a.shift;
-  const int l = __ldg(a.seq_lens + b);
+  const int l = a.seq_lens[b];
   r.len = l < 0 ? 0 : (l > cap ? (int)cap : l);
-  const int n = a.q_lens ? __ldg(a.q_lens + b) : a.T;
+  const int n = a.q_lens ? a.q_lens[b] : a.T;
   r.ql = n < 0 ? 0 : (n > a.T ? a.T : n);
   const long long first = (long long)r.len - r.ql - a.window;  // the first row's window
   r.lo = (a.window < 0 || first < 0) ? 0 : (int)(first & ~(long long)(kGroups * kGroup - 1));
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
       const int tok = load.r.lo + (load.unit + lane) * kUnit + (warp * kGroups + u) * kGroup;
       src[u] = nullptr;
       if (lane < turns && tok < load.r.len) {
-        const int page = __ldg(a.block_table + (size_t)load.b * a.M + (tok >> a.shift));
+        const int page = a.block_table[(size_t)load.b * a.M + (tok >> a.shift)];
         const int gpp_shift = a.shift - 4;
         if (page >= 0 && page < a.pages)
           src[u] = a.cache + ((((size_t)page * a.Hkv + load.hk) << gpp_shift) +

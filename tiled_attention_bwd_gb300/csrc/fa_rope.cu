@@ -241,7 +241,7 @@ __device__ __forceinline__ void load_weight(const void* w, int is_bf16, const La
 }
 
 __device__ __forceinline__ int position_of(const RopeArgs& a, int token, int n) {
-  return a.positions ? __ldg(a.positions + token) : n;
+  return a.positions ? a.positions[token] : n;
 }
 
 // A warp's work: one pack of heads (query heads' packs first, then key heads',

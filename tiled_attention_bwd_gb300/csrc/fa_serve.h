@@ -147,6 +147,11 @@ cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, dim3 block,
 // Every thread that touches global memory calls it first, and at least one
 // thread of a grid always does: a grid that ended without waiting would let
 // the one after it start before the one before it is done.
+//
+// What the work before wrote (lengths, tables, slots, positions, weights) is
+// read by plain loads only.  A read-only load (__ldg, a const __restrict__
+// pointer) says that the data does not change while the kernel lives, which
+// is not so before the wait, and the clobber here does not hold it back.
 __device__ __forceinline__ void wait_for_stream() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
