@@ -288,8 +288,8 @@ fa_status fa_qk_norm_rope(const void* qkv, long long stride_b,
  * them) and the forward's qkv to dqkv (bf16, laid out like qkv, with strides
  * of its own) and, with weights, dq_weight and dk_weight (fp32 [d], summed
  * over all tokens and heads in an order that does not change from call to
- * call; zero without tokens).  dqkv may be qkv itself, with its strides; its
- * tokens do not overlap.  With weights it needs
+ * call; zero without tokens).  dqkv may be qkv itself, with its strides; no two
+ * of its tokens share memory, whatever its strides (refused).  With weights it needs
  * fa_qk_norm_rope_bwd_workspace_size(d) bytes of device workspace, 16-byte
  * aligned, whose contents do not matter.
  */

@@ -1,0 +1,85 @@
+"""Calls whose outputs lie on one another or on an input (CPU only: the C ABI
+refuses them before it touches a GPU).
+
+Where a call is in order, it gets past the checks to the device, which is not
+there: FA_ERR_CUDA then, and on a machine with a GPU these tests do not run.
+"""
+import ctypes
+import itertools
+
+import pytest
+import torch
+
+from tiled_attention_bwd_gb300 import build as fa_build
+from tiled_attention_bwd_gb300 import fa
+
+INVALID, CUDA = 1, 3
+
+pytestmark = pytest.mark.skipif(torch.cuda.is_available(),
+                                reason="made-up addresses: no GPU may read them")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    fa_build.build()
+    return fa.load_library()
+
+
+def p(x):
+    return ctypes.c_void_p(x) if x else None
+
+
+M = 1 << 20
+
+
+def bwd(lib, B=2, N=3, H=3, Hkv=1, d=128, rot=128, rows=8, sb=None, sn=None,
+        dsb=None, dsn=None, norm=True, **at):
+    """fa_qk_norm_rope_bwd on addresses a megabyte apart, but for `at`."""
+    width = (H + 2 * Hkv) * d
+    sn = width if sn is None else sn
+    sb = N * sn if sb is None else sb
+    dsn = width if dsn is None else dsn
+    dsb = N * dsn if dsb is None else dsb
+    names = ["qkv", "rope", "pos", "qw", "kw", "dq", "dk", "dv", "dqkv", "dqw",
+             "dkw", "ws"]
+    a = {n: (16 + i) * 16 * M for i, n in enumerate(names)}
+    if not norm:
+        a.update(qw=0, kw=0, dqw=0, dkw=0, ws=0)
+    a.update(at)
+    return lib.fa_qk_norm_rope_bwd(
+        p(a["qkv"]), sb, sn, p(a["rope"]), rows, rot, p(a["pos"]), p(a["qw"]),
+        p(a["kw"]), 0, 1e-6, 0, p(a["dq"]), p(a["dk"]), p(a["dv"]), p(a["dqkv"]),
+        dsb, dsn, p(a["dqw"]), p(a["dkw"]), p(a["ws"]), 1 << 24, B, N, H, Hkv,
+        d, None)
+
+
+W = 5 * 128                                # elements of a token above
+
+
+def tokens_meet(B, N, sb, sn, width):
+    at = sorted(b * sb + n * sn for b in range(B) for n in range(N))
+    return any(y - x < width for x, y in zip(at, at[1:]))
+
+
+@pytest.mark.parametrize("B,N", [(1, 1), (1, 4), (4, 1), (2, 2), (2, 3), (3, 2), (3, 5), (6, 4)])
+def test_tokens_of_the_gradient_that_lie_on_one_another(lib, B, N):
+    """Every pair of strides of up to a few rows, in half rows, both signs."""
+    seen = set()
+    steps = [s * W // 2 for s in range(-9, 10)] + [W - 8, W + 8, 1 << 40]
+    for sb, sn in itertools.product(steps, steps):
+        meet = tokens_meet(B, N, sb, sn, W)
+        got = bwd(lib, B, N, dsb=sb, dsn=sn, dqkv=1 << 50, norm=False)
+        assert got == (INVALID if meet else CUDA), (sb, sn)
+        seen.add(meet)
+    assert B * N == 1 or seen == {False, True}
+
+
+def test_tokens_on_one_another_in_many_entries(lib):
+    """Strides of the same size: entry 0's second token is entry 1's first."""
+    for B, N in ((2, 2), (64, 4096), (4096, 64)):
+        assert bwd(lib, B, N, dsb=W, dsn=W, dqkv=1 << 50, norm=False) == INVALID
+        assert bwd(lib, B, N, dsb=W, dsn=-W, dqkv=1 << 50, norm=False) == INVALID
+        assert bwd(lib, B, N, dsb=N * W, dsn=W, dqkv=1 << 50, norm=False) == CUDA
+        assert bwd(lib, B, N, dsb=W, dsn=B * W, dqkv=1 << 50, norm=False) == CUDA
+        # (The last token on the next entry's first.)
+        assert bwd(lib, B, N, dsb=(N - 1) * W, dsn=W, dqkv=1 << 50, norm=False) == INVALID

@@ -29,6 +29,39 @@ struct Span {
     return bytes > 0 && o.bytes > 0 && apart < (uintptr_t)(a <= b ? bytes : o.bytes);
   }
 };
+// Rows of `width` bytes, one at p + b sb + n sn for each b < B, n < N (strides
+// in bytes, of any sign).
+using Wide = __int128;
+struct Rows {
+  const void* p;
+  Wide sb, sn;
+  long long B, N, width;
+  // Whether a row begins at an offset between lo and hi, both left out.
+  // (Walks the shorter axis and solves for the other.)
+  bool begins_within(Wide lo, Wide hi) const {
+    if (B > N) return Rows{p, sn, sb, N, B, width}.begins_within(lo, hi);
+    const Wide step = sn < 0 ? -sn : sn;
+    for (long long b = 0; b < B; ++b) {
+      const Wide first = b * sb + (sn < 0 ? (N - 1) * sn : 0);  // then by `step` upwards
+      const Wide n = first > lo ? 0 : (step > 0 ? (lo - first) / step + 1 : N);
+      if (n < N && first + n * step < hi) return true;
+    }
+    return false;
+  }
+  // Two of these rows share a byte.
+  bool meet() const {
+    if (B > 1 && N > 1) {
+      const Wide b = sb < 0 ? -sb : sb, n = sn < 0 ? -sn : sn;
+      if (n >= width && b >= (N - 1) * n + width) return false;  // entries apart
+      if (b >= width && n >= (B - 1) * b + width) return false;  // tokens apart
+    }
+    if (N > 1 && sn < width && -sn < width) return true;
+    if (B <= 1) return false;
+    // Row (b, n) less row (0, n'), b > 0: sb, 2 sb, ... and -(N-1) sn, ... on.
+    const Wide from = sb - (N - 1) * sn;
+    return Rows{p, sb, sn, B - 1, 2 * N - 1, width}.begins_within(-width - from, width - from);
+  }
+};
 fa_status launched(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
 
 // ------------------------------------------------------ norm and rotation
@@ -173,10 +206,8 @@ fa_status fa_qk_norm_rope_bwd(const void* qkv, long long stride_b, long long str
       return FA_ERR_INVALID_ARG;
     if (dstride_b % 8 != 0 || dstride_n % 8 != 0) return FA_ERR_INVALID_ARG;
     // (Tokens of the output may not lie on one another.)
-    const long long width = (H + 2LL * Hkv) * d;
-    if ((B > 1 && dstride_b < width && -dstride_b < width) ||
-        (N > 1 && dstride_n < width && -dstride_n < width))
-      return FA_ERR_INVALID_ARG;
+    const Rows out = {dqkv, 2 * (Wide)dstride_b, 2 * (Wide)dstride_n, B, N, 2 * (H + 2LL * Hkv) * d};
+    if (out.meet()) return FA_ERR_INVALID_ARG;
   } else if (!norm) {
     return FA_OK;
   }
