@@ -273,7 +273,8 @@ fa_status fa_step_host(const void* q, const void* k, const void* v,
  *   q_weight, k_weight : in, [d], bf16 (weight_bf16 = 1) or fp32 (0); both
  *               NULL: no norm, only the rotation
  *   q, k, v   : out, bf16 [B,H,N,d], [B,Hkv,N,d], [B,Hkv,N,d]
- * The outputs overlap no input.  eps >= 0; H and Hkv are at most 8192, and
+ * The outputs overlap neither an input nor one another (refused; they may lie
+ * between the tokens of a wider qkv).  eps >= 0; H and Hkv are at most 8192, and
  * an H of 0, or an Hkv of 0, is a call for the other heads alone.
  */
 fa_status fa_qk_norm_rope(const void* qkv, long long stride_b,

@@ -83,3 +83,70 @@ def test_tokens_on_one_another_in_many_entries(lib):
         assert bwd(lib, B, N, dsb=W, dsn=B * W, dqkv=1 << 50, norm=False) == CUDA
         # (The last token on the next entry's first.)
         assert bwd(lib, B, N, dsb=(N - 1) * W, dsn=W, dqkv=1 << 50, norm=False) == INVALID
+
+
+def fwd(lib, B=2, N=3, H=3, Hkv=1, d=128, rot=128, rows=8, sb=None, sn=None,
+        bf16=0, **at):
+    """fa_qk_norm_rope on addresses 16 megabytes apart, but for `at`."""
+    width = (H + 2 * Hkv) * d
+    sn = width if sn is None else sn
+    sb = N * sn if sb is None else sb
+    a = {n: (16 + i) * 16 * M for i, n in enumerate(
+        ["qkv", "rope", "pos", "qw", "kw", "q", "k", "v"])}
+    a.update(at)
+    return lib.fa_qk_norm_rope(
+        p(a["qkv"]), sb, sn, p(a["rope"]), rows, rot, p(a["pos"]), p(a["qw"]),
+        p(a["kw"]), bf16, 1e-6, 0, p(a["q"]), p(a["k"]), p(a["v"]), B, N, H,
+        Hkv, d, None)
+
+
+def touching(x, size, y, other):
+    """Addresses of a piece of `size` bytes at x: just before, over either
+    end of, within and just behind a piece of `other` bytes at y."""
+    return [(y - size, False), (y - size + 16, True), (y, True),
+            (y + other - 16, True), (y + other, False)]
+
+
+def test_forward_outputs_on_one_another_and_on_inputs(lib):
+    at = {n: (16 + i) * 16 * M for i, n in enumerate(
+        ["qkv", "rope", "pos", "qw", "kw", "q", "k", "v"])}
+    # B, N, H, Hkv, d = 2, 3, 3, 1, 128: six tokens
+    size = {"qkv": 6 * 2 * W, "rope": 8 * 128 * 4, "pos": 32, "qw": 512,
+            "kw": 512, "q": 6 * 768, "k": 6 * 256, "v": 6 * 256}
+    assert fwd(lib) == CUDA
+    for out in ("q", "k", "v"):
+        for other in at:
+            if other == out:
+                continue
+            for x, bad in touching(at[out], size[out], at[other], size[other]):
+                assert fwd(lib, **{out: x}) == (INVALID if bad else CUDA), (out, other, x)
+    # Weights of two bytes, no positions, no weights: nothing to meet.
+    assert fwd(lib, bf16=1, q=at["qw"] + 256) == CUDA
+    assert fwd(lib, bf16=1, q=at["qw"] + 240) == INVALID
+    assert fwd(lib, pos=0, q=at["pos"]) == CUDA
+    assert fwd(lib, qw=0, kw=0, q=at["qw"]) == CUDA
+    assert fwd(lib, H=0, q=0) == CUDA
+    assert fwd(lib, H=0, k=at["v"]) == INVALID
+
+
+def test_forward_outputs_between_the_tokens_of_a_wide_input(lib):
+    """qkv as columns of wider rows: outputs may lie in the gaps."""
+    qkv, row = 1 << 30, 2 * 4096           # bytes from token to token
+    ok = dict(qkv=qkv, sn=4096, sb=3 * 4096)
+    tok, q, k = 2 * W, 6 * 768, 6 * 256    # bytes of a token, of q, of k or v
+    # One request of one token: nothing behind it.
+    assert fwd(lib, B=1, N=1, qkv=qkv, q=qkv + tok, sn=0, sb=0) == CUDA
+    assert fwd(lib, q=qkv + tok, k=qkv + row + tok, v=qkv + row + tok + k, **ok) == CUDA
+    assert fwd(lib, q=qkv + tok - 16, **ok) == INVALID
+    assert fwd(lib, q=qkv + row - q, **ok) == CUDA
+    assert fwd(lib, q=qkv + row - q + 16, **ok) == INVALID
+    assert fwd(lib, k=qkv + 5 * row + tok, **ok) == CUDA
+    assert fwd(lib, k=qkv + 5 * row + tok - 16, **ok) == INVALID
+    assert fwd(lib, k=qkv - k, **ok) == CUDA
+    assert fwd(lib, k=qkv - k + 16, **ok) == INVALID
+    # Negative strides: tokens lie before the address.
+    back = dict(qkv=qkv, sn=-4096, sb=-3 * 4096)
+    assert fwd(lib, k=qkv - row - k, **back) == CUDA
+    assert fwd(lib, k=qkv - row - k + 16, **back) == INVALID
+    assert fwd(lib, k=qkv - 5 * row + tok, **back) == CUDA
+    assert fwd(lib, k=qkv - 5 * row, **back) == INVALID

@@ -5,6 +5,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "fa.h"
 #include "fa_cache4.cuh"
@@ -61,7 +62,24 @@ struct Rows {
     const Wide from = sb - (N - 1) * sn;
     return Rows{p, sb, sn, B - 1, 2 * N - 1, width}.begins_within(-width - from, width - from);
   }
+  bool meet(const Span& o) const {
+    if (o.bytes <= 0 || width <= 0) return false;
+    const Wide at = (Wide)reinterpret_cast<uintptr_t>(o.p) - (Wide)reinterpret_cast<uintptr_t>(p);
+    return begins_within(at - width, at + o.bytes);
+  }
 };
+// Memory of a tensor, none where it is not given.
+Span span(const void* p, long long bytes) { return {p, p ? bytes : 0}; }
+// Whether an output meets an input, or another output.
+bool meet(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& i : ins)
+      if (o->meets(i)) return true;
+    for (const Span* x = outs.begin(); x != o; ++x)
+      if (o->meets(*x)) return true;
+  }
+  return false;
+}
 fa_status launched(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
 
 // ------------------------------------------------------ norm and rotation
@@ -89,6 +107,12 @@ fa_status check_rope(int B, int N, int H, int Hkv, int d, int rot, int table_row
     return FA_ERR_INVALID_ARG;
   if (stride_b % 8 != 0 || stride_n % 8 != 0) return FA_ERR_INVALID_ARG;
   return FA_OK;
+}
+
+// The tokens of a [B,N,H+2Hkv,d] tensor.
+Rows tokens(const void* p, long long stride_b, long long stride_n, int B, int N, int H, int Hkv,
+            int d) {
+  return {p, 2 * (Wide)stride_b, 2 * (Wide)stride_n, B, N, 2 * (H + 2LL * Hkv) * d};
 }
 
 fa::RopeArgs rope_args(const void* qkv, long long sb, long long sn, const float* table,
@@ -165,6 +189,13 @@ fa_status fa_qk_norm_rope(const void* qkv, long long stride_b, long long stride_
   if ((H > 0 && !q) || (Hkv > 0 && (!k || !v)) || !aligned(q, 16) || !aligned(k, 16) ||
       !aligned(v, 16))
     return FA_ERR_INVALID_ARG;
+  const long long head = 2LL * B * N * d, weight = (weight_bf16 ? 2LL : 4LL) * d;
+  const Span qs = span(q, H * head), ks = span(k, Hkv * head), vs = span(v, Hkv * head);
+  if (meet({qs, ks, vs}, {span(rope, 4LL * rope_rows * rot), span(positions, 4LL * B * N),
+                          span(q_weight, weight), span(k_weight, weight)}))
+    return FA_ERR_INVALID_ARG;
+  const Rows in = tokens(qkv, stride_b, stride_n, B, N, H, Hkv, d);
+  if (in.meet(qs) || in.meet(ks) || in.meet(vs)) return FA_ERR_INVALID_ARG;
   fa::DeviceInfo dev;
   if ((s = fa::device_info(&dev)) != FA_OK) return s;
   fa::RopeArgs a = rope_args(qkv, stride_b, stride_n, rope, rope_rows, rot, positions, q_weight,
@@ -206,8 +237,7 @@ fa_status fa_qk_norm_rope_bwd(const void* qkv, long long stride_b, long long str
       return FA_ERR_INVALID_ARG;
     if (dstride_b % 8 != 0 || dstride_n % 8 != 0) return FA_ERR_INVALID_ARG;
     // (Tokens of the output may not lie on one another.)
-    const Rows out = {dqkv, 2 * (Wide)dstride_b, 2 * (Wide)dstride_n, B, N, 2 * (H + 2LL * Hkv) * d};
-    if (out.meet()) return FA_ERR_INVALID_ARG;
+    if (tokens(dqkv, dstride_b, dstride_n, B, N, H, Hkv, d).meet()) return FA_ERR_INVALID_ARG;
   } else if (!norm) {
     return FA_OK;
   }
