@@ -289,8 +289,11 @@ fa_status fa_qk_norm_rope(const void* qkv, long long stride_b,
  * them) and the forward's qkv to dqkv (bf16, laid out like qkv, with strides
  * of its own) and, with weights, dq_weight and dk_weight (fp32 [d], summed
  * over all tokens and heads in an order that does not change from call to
- * call; zero without tokens).  dqkv may be qkv itself, with its strides; no two
- * of its tokens share memory, whatever its strides (refused).  With weights it needs
+ * call; zero without tokens).  dqkv may be qkv itself, with its strides, or
+ * other columns of the same rows.  Otherwise no output shares memory with an
+ * input or another output, and no two tokens of dqkv with one another, whatever
+ * the strides (refused; a dqkv of other strides than qkv's counts as all of its
+ * extent).  With weights it needs
  * fa_qk_norm_rope_bwd_workspace_size(d) bytes of device workspace, 16-byte
  * aligned, whose contents do not matter.
  */

@@ -150,3 +150,60 @@ def test_forward_outputs_between_the_tokens_of_a_wide_input(lib):
     assert fwd(lib, k=qkv - row - k + 16, **back) == INVALID
     assert fwd(lib, k=qkv - 5 * row + tok, **back) == CUDA
     assert fwd(lib, k=qkv - 5 * row, **back) == INVALID
+
+
+NAMES = ["qkv", "rope", "pos", "qw", "kw", "dq", "dk", "dv", "dqkv", "dqw",
+         "dkw", "ws"]
+
+
+def test_backward_outputs_on_one_another_and_on_inputs(lib):
+    at = {n: (16 + i) * 16 * M for i, n in enumerate(NAMES)}
+    size = {"qkv": 6 * 2 * W, "rope": 8 * 128 * 4, "pos": 32, "qw": 512,
+            "kw": 512, "dq": 6 * 768, "dk": 6 * 256, "dv": 6 * 256,
+            "dqkv": 6 * 2 * W, "dqw": 512, "dkw": 512,
+            "ws": lib.fa_qk_norm_rope_bwd_workspace_size(128)}
+    assert bwd(lib) == CUDA
+    for out in ("dqkv", "dqw", "dkw", "ws"):
+        for other in at:
+            if other == out:
+                continue
+            for x, bad in touching(at[out], size[out], at[other], size[other]):
+                if (out, other) == ("dqkv", "qkv") and x == at[other]:
+                    bad = False            # the one input that it may be
+                assert bwd(lib, **{out: x}) == (INVALID if bad else CUDA), (out, other, x)
+    # Without weights there is no sum, and qkv is not read.
+    assert bwd(lib, norm=False, dqkv=at["qkv"] + 16) == CUDA
+    assert bwd(lib, norm=False, dqkv=at["dq"]) == INVALID
+    assert bwd(lib, norm=False, dqkv=at["rope"]) == INVALID
+    # Without tokens only the weights' gradients are written.
+    empty = dict(N=0, qkv=0, dq=0, dk=0, dv=0, dqkv=0, rope=0, pos=0)
+    assert bwd(lib, **empty) == CUDA
+    assert bwd(lib, dqw=at["dkw"], **empty) == INVALID
+    assert bwd(lib, dkw=at["qw"] + 256, **empty) == INVALID
+
+
+def test_gradient_in_place_and_beside_its_input(lib):
+    """dqkv as qkv itself needs qkv's strides; as other columns of the same
+    wide rows it shares nothing."""
+    x, row, tok = 1 << 30, 2 * 4096, 2 * W
+    wide = dict(qkv=x, sn=4096, sb=3 * 4096, dsn=4096, dsb=3 * 4096)
+    assert bwd(lib, dqkv=x, **wide) == CUDA
+    assert bwd(lib, dqkv=x + tok, **wide) == CUDA
+    assert bwd(lib, dqkv=x + row - tok, **wide) == CUDA
+    for off in (16, tok - 16, row, row - tok + 16, 3 * row, 5 * row, -row + 16,
+                -5 * row, 2 * row + tok - 16):
+        assert bwd(lib, dqkv=x + off, **wide) == INVALID, off
+    for off in (6 * row, 5 * row + tok, -5 * row - tok, -6 * row, 3 * row + tok):
+        assert bwd(lib, dqkv=x + off, **wide) == CUDA, off
+    # Other strides on the same memory: refused, whatever lies between.
+    other = dict(wide, dsn=4096 + 8)
+    assert bwd(lib, dqkv=x, **other) == INVALID
+    assert bwd(lib, dqkv=x + 6 * row, **other) == CUDA
+    # A single entry or token has no stride.
+    assert bwd(lib, B=1, qkv=x, dqkv=x, sb=0, dsb=77 * 8) == CUDA
+    assert bwd(lib, B=1, N=1, qkv=x, dqkv=x, sn=0, dsn=8) == CUDA
+    # Entries within the tokens' gaps of one another.
+    loose = dict(B=2, N=3, qkv=x, sb=1024, sn=4096, dsb=1024, dsn=4096)
+    assert bwd(lib, dqkv=x, **loose) == CUDA
+    assert bwd(lib, dqkv=x + 2 * 2048, **loose) == CUDA
+    assert bwd(lib, dqkv=x + 2048, **loose) == INVALID

@@ -68,17 +68,39 @@ struct Rows {
     return begins_within(at - width, at + o.bytes);
   }
 };
+// Two tensors of such rows share a byte; `may_be` lets the second be the
+// first itself.  (Of different strides, each is taken as all of its extent.)
+bool meet(const Rows& a, const Rows& b, bool may_be) {
+  auto extent = [](const Rows& r, Wide* lo, Wide* hi) {
+    *lo = (Wide)reinterpret_cast<uintptr_t>(r.p);
+    *hi = *lo + r.width;
+    for (Wide x : {(r.B - 1) * r.sb, (r.N - 1) * r.sn}) (x < 0 ? *lo : *hi) += x;
+  };
+  Wide al, ah, bl, bh;
+  extent(a, &al, &ah), extent(b, &bl, &bh);
+  if (al >= bh || bl >= ah) return false;
+  if ((a.B > 1 && a.sb != b.sb) || (a.N > 1 && a.sn != b.sn)) return true;
+  if (may_be && a.p == b.p) return false;
+  // Differences of two rows' offsets: from this one up, by sb and sn.
+  const Wide from = -((a.B - 1) * a.sb + (a.N - 1) * a.sn);
+  const Wide at = (Wide)reinterpret_cast<uintptr_t>(b.p) - (Wide)reinterpret_cast<uintptr_t>(a.p);
+  return Rows{a.p, a.sb, a.sn, 2 * a.B - 1, 2 * a.N - 1, a.width}.begins_within(
+      at - a.width - from, at + a.width - from);
+}
 // Memory of a tensor, none where it is not given.
 Span span(const void* p, long long bytes) { return {p, p ? bytes : 0}; }
 // Whether an output meets an input, or another output.
-bool meet(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
-  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
-    for (const Span& i : ins)
-      if (o->meets(i)) return true;
-    for (const Span* x = outs.begin(); x != o; ++x)
+bool meet(const Span* outs, const Span* outs_end, const Span* ins, const Span* ins_end) {
+  for (const Span* o = outs; o != outs_end; ++o) {
+    for (const Span* i = ins; i != ins_end; ++i)
+      if (o->meets(*i)) return true;
+    for (const Span* x = outs; x != o; ++x)
       if (o->meets(*x)) return true;
   }
   return false;
+}
+bool meet(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  return meet(outs.begin(), outs.end(), ins.begin(), ins.end());
 }
 fa_status launched(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
 
@@ -236,10 +258,30 @@ fa_status fa_qk_norm_rope_bwd(const void* qkv, long long stride_b, long long str
         !aligned(dk, 16) || !aligned(dv, 16) || !aligned(dqkv, 16))
       return FA_ERR_INVALID_ARG;
     if (dstride_b % 8 != 0 || dstride_n % 8 != 0) return FA_ERR_INVALID_ARG;
-    // (Tokens of the output may not lie on one another.)
-    if (tokens(dqkv, dstride_b, dstride_n, B, N, H, Hkv, d).meet()) return FA_ERR_INVALID_ARG;
   } else if (!norm) {
     return FA_OK;
+  }
+  const long long head = 2LL * B * N * d, weight = (weight_bf16 ? 2LL : 4LL) * d;
+  const Span ins[] = {span(dq, H * head),
+                      span(dk, Hkv * head),
+                      span(dv, Hkv * head),
+                      span(empty ? nullptr : rope, 4LL * rope_rows * rot),
+                      span(empty ? nullptr : positions, 4LL * B * N),
+                      span(q_weight, weight),
+                      span(k_weight, weight)};
+  const Span sums[] = {span(norm ? dq_weight : nullptr, 4LL * d),
+                       span(norm ? dk_weight : nullptr, 4LL * d),
+                       span(norm ? workspace : nullptr, fa_qk_norm_rope_bwd_workspace_size(d))};
+  if (meet(sums, sums + 3, ins, ins + 7)) return FA_ERR_INVALID_ARG;
+  if (!empty) {
+    const Rows x = tokens(qkv, stride_b, stride_n, B, N, H, Hkv, d);
+    const Rows out = tokens(dqkv, dstride_b, dstride_n, B, N, H, Hkv, d);
+    // (Without weights qkv is not read.)
+    if (out.meet() || (norm && meet(out, x, true))) return FA_ERR_INVALID_ARG;
+    for (const Span& i : ins)
+      if (out.meet(i)) return FA_ERR_INVALID_ARG;
+    for (const Span& i : sums)
+      if (out.meet(i) || x.meet(i)) return FA_ERR_INVALID_ARG;
   }
   fa::DeviceInfo dev;
   if ((s = fa::device_info(&dev)) != FA_OK) return s;
