@@ -399,7 +399,8 @@ fa_status fa_cache4_append(const void* k, const void* v, void* cache,
  *   o, lse      : out, bf16 [B,H,T,d], fp32 [B,H,T]; rows t >= q_lens[b] are
  *                 left as they were.  A row that sees no key gets o = 0 and
  *                 lse = -infinity.
- *                 They overlap no input.
+ *                 They and the workspace overlap neither an input nor one
+ *                 another (refused).
  *   workspace   : fa_cache4_attn_workspace_size(B, H, Hkv, T, d) bytes,
  *                 256-byte aligned; contents do not matter.  Calls that
  *                 share a workspace must not overlap in time.

@@ -207,3 +207,41 @@ def test_gradient_in_place_and_beside_its_input(lib):
     assert bwd(lib, dqkv=x, **loose) == CUDA
     assert bwd(lib, dqkv=x + 2 * 2048, **loose) == CUDA
     assert bwd(lib, dqkv=x + 2048, **loose) == INVALID
+
+
+ATTN = ["q", "cache", "table", "lens", "ql", "o", "lse", "ws"]
+
+
+def attn(lib, B=2, H=4, Hkv=2, T=3, d=64, blocks=2, pages=3, page=32, **at):
+    """fa_cache4_attn on addresses 64 megabytes apart, but for `at`."""
+    a = {n: (16 + i) * 64 * M for i, n in enumerate(ATTN)}
+    a.update(at)
+    return lib.fa_cache4_attn(
+        p(a["q"]), p(a["cache"]), p(a["table"]), p(a["lens"]), p(a["ql"]),
+        p(a["o"]), p(a["lse"]), p(a["ws"]), 1 << 40, B, H, Hkv, T, d, blocks,
+        pages, page, -1, 0.1, 1.0, 1.0, None)
+
+
+def test_attention_outputs_on_one_another_and_on_inputs(lib):
+    at = {n: (16 + i) * 64 * M for i, n in enumerate(ATTN)}
+    B, H, T, d = 4, 4, 3, 64
+    rows = B * H * T
+    size = {"q": rows * d * 2, "cache": 3 * 2 * 2 * 18 * d, "table": B * 2 * 4,
+            "lens": B * 4, "ql": B * 4, "o": rows * d * 2, "lse": rows * 4,
+            "ws": lib.fa_cache4_attn_workspace_size(B, H, 2, T, d)}
+    assert attn(lib, B) == CUDA
+    for out in ("o", "lse", "ws"):
+        for other in at:
+            if other == out:
+                continue
+            if out == "ws":                # 256-byte aligned
+                up = lambda n: -(-n // 256) * 256  # noqa: E731
+                places = [(at[other] - up(size["ws"]), False),
+                          (at[other] + 256 - up(size["ws"]), True),
+                          (at[other], True), (at[other] + up(size[other]), False)]
+            else:
+                places = touching(at[out], size[out], at[other], size[other])
+            for x, bad in places:
+                assert attn(lib, B, **{out: x}) == (INVALID if bad else CUDA), (out, other, x)
+    assert attn(lib, B, ql=0, lse=at["ql"]) == CUDA
+    assert attn(lib, B, ql=at["lens"]) == CUDA  # inputs may share what they read

@@ -180,6 +180,10 @@ fa_status check_cache(int pages, int Hkv, int page, int d, int* shift) {
   return FA_OK;
 }
 
+long long cache_bytes(int pages, int Hkv, int page, int d) {
+  return (long long)pages * Hkv * (page / fa::kGroup) * fa::group_bytes(d);
+}
+
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
@@ -430,6 +434,13 @@ fa_status fa_cache4_attn(const void* q, const void* cache, const int* block_tabl
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < fa_cache4_attn_workspace_size(B, H, Hkv, T, d))
     return FA_ERR_WORKSPACE;
+  const long long q_rows = (long long)B * H * T;
+  if (meet({span(o, 2 * q_rows * d), span(lse, 4 * q_rows),
+            span(workspace, fa_cache4_attn_workspace_size(B, H, Hkv, T, d))},
+           {span(q, 2 * q_rows * d), span(cache, cache_bytes(pages, Hkv, page_size, d)),
+            span(block_table, 4LL * B * max_blocks), span(seq_lens, 4LL * B),
+            span(q_lens, 4LL * B)}))
+    return FA_ERR_INVALID_ARG;
   fa::DeviceInfo dev;
   if ((s = fa::device_info(&dev)) != FA_OK) return s;
   fa::Cache4AttnArgs a = {};
