@@ -378,6 +378,8 @@ fa_status fa_cache4_plan(const int* new_tokens, int* lens, int* block_table,
  *                  read.  They may be k and v themselves, and overlap them
  *                  in no other way.  Rows of skipped tokens are left as
  *                  they were.
+ * Neither the cache nor these outputs overlap an input or one another in any
+ * other way (refused).
  * A slot that occurs twice in a call holds an unspecified mix of the two.
  */
 fa_status fa_cache4_append(const void* k, const void* v, void* cache,

@@ -245,3 +245,40 @@ def test_attention_outputs_on_one_another_and_on_inputs(lib):
                 assert attn(lib, B, **{out: x}) == (INVALID if bad else CUDA), (out, other, x)
     assert attn(lib, B, ql=0, lse=at["ql"]) == CUDA
     assert attn(lib, B, ql=at["lens"]) == CUDA  # inputs may share what they read
+
+
+APPEND = ["k", "v", "cache", "slots", "ko", "vo"]
+
+
+def append(lib, B=2, Hkv=2, N=4, d=64, pages=3, page=32, **at):
+    """fa_cache4_append on addresses 16 megabytes apart, but for `at`."""
+    a = {n: (16 + i) * 16 * M for i, n in enumerate(APPEND)}
+    a.update(at)
+    return lib.fa_cache4_append(
+        p(a["k"]), p(a["v"]), p(a["cache"]), p(a["slots"]), 1.0, 1.0,
+        p(a["ko"]), p(a["vo"]), B, Hkv, N, d, pages, page, None)
+
+
+def test_append_outputs_on_one_another_and_on_inputs(lib):
+    at = {n: (16 + i) * 16 * M for i, n in enumerate(APPEND)}
+    rows = 2 * 2 * 4 * 64 * 2
+    size = {"k": rows, "v": rows, "cache": 3 * 2 * 2 * 18 * 64, "slots": 32,
+            "ko": rows, "vo": rows}
+    assert append(lib) == CUDA
+    for out in ("cache", "ko", "vo"):
+        for other in at:
+            if other == out:
+                continue
+            for x, bad in touching(at[out], size[out], at[other], size[other]):
+                if out[1:] == "o" and other == out[0] and x == at[other]:
+                    bad = False            # values may replace their own input
+                assert append(lib, **{out: x}) == (INVALID if bad else CUDA), (out, other, x)
+    both = dict(ko=at["k"], vo=at["v"])
+    assert append(lib, **both) == CUDA
+    for other in ("k", "v"):
+        assert append(lib, cache=at[other], **both) == INVALID
+        assert append(lib, cache=at[other], ko=0, vo=0) == INVALID
+        assert append(lib, slots=at[other], **both) == INVALID
+    assert append(lib, cache=at["slots"], ko=0, vo=0) == INVALID
+    assert append(lib, v=at["k"], ko=0, vo=0) == CUDA
+    assert append(lib, v=at["k"], **dict(both, vo=at["vo"])) == INVALID

@@ -368,13 +368,14 @@ fa_status fa_cache4_append(const void* k, const void* v, void* cache, const int*
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cache, 16) || !aligned(slots, 4) ||
       !aligned(k_out, 16) || !aligned(v_out, 16))
     return FA_ERR_INVALID_ARG;
-  if (k_out) {  // an output is its own input or neither
-    const long long bytes = 2LL * B * Hkv * N * d;
-    const Span ki = {k, bytes}, vi = {v, bytes}, ko = {k_out, bytes}, vo = {v_out, bytes};
-    if (ko.meets(vo) || ko.meets(vi) || vo.meets(ki) || (k_out != k && ko.meets(ki)) ||
-        (v_out != v && vo.meets(vi)))
-      return FA_ERR_INVALID_ARG;
-  }
+  const long long bytes = 2LL * B * Hkv * N * d;
+  const Span ko = span(k_out, bytes), vo = span(v_out, bytes);
+  if (meet({span(cache, cache_bytes(pages, Hkv, page_size, d)), ko, vo},
+           {span(slots, 4LL * B * N), span(k_out == k ? nullptr : k, bytes),
+            span(v_out == v ? nullptr : v, bytes)}))
+    return FA_ERR_INVALID_ARG;
+  // (Values that replace their own keys or values still meet nothing else.)
+  if (ko.meets(span(v, bytes)) || vo.meets(span(k, bytes))) return FA_ERR_INVALID_ARG;
   fa::AppendArgs a = {};
   a.k = static_cast<const __nv_bfloat16*>(k);
   a.v = static_cast<const __nv_bfloat16*>(v);
