@@ -445,8 +445,8 @@ void fa_set_wait_timeout_ns(uint64_t ns);
 
 /*
  * Test hook of the failure path, for the current device.  Until called
- * again with 0, every pipeline wait at `site` inside the forward and
- * backward kernels launched after this call that finds its barrier not yet
+ * again with 0, every pipeline wait at `site` inside the kernels
+ * launched after this call that finds its barrier not yet
  * complete (a real wait) behaves as if its time limit had passed: it
  * records FA_ERR_DEVICE_TIMEOUT with that
  * site, and its block and the rest of the grid stop exactly as after a real
@@ -465,9 +465,12 @@ void fa_set_wait_timeout_ns(uint64_t ns);
  *             waiting for Q, 0x312 S, 0x313 dP, 0x314 the dS buffer, 0x315
  *             the finished dK, 0x316 the next item; 0x411 dQ drain waiting
  *             for dQ, 0x412 the finished dV, 0x413 the next item.
+ *   cache attention: 0x511 a warp waiting for its copies (the hook takes the
+ *             first warp of every block, whether its wait is complete or not).
  * While a site is set, forward and backward calls with d = 128 and no
- * window, lengths or FP8 run kernel instantiations compiled with the hook
- * (the same source; the ones used otherwise carry no trace of it, since
+ * window, lengths or FP8, and cache attention calls with d = 128 and at most
+ * 8 query rows per key/value head, run kernel instantiations compiled with
+ * the hook (the same source; the ones used otherwise carry no trace of it, since
  * even a test on the slow path of each wait cost about 1%); other calls
  * ignore it.  The call is synchronous (it writes a constant in device
  * memory): make it only while no kernel of this library is running on the

@@ -304,7 +304,8 @@ namespace fa {
 fa_status device_info(DeviceInfo* out) {
   DeviceCtx* ctx = nullptr;
   const fa_status s = device_ctx(&ctx);
-  if (s == FA_OK) *out = DeviceInfo{ctx->state, ctx->sm_count, kernel_timeout()};
+  if (s == FA_OK) *out = DeviceInfo{ctx->state, ctx->sm_count, kernel_timeout(),
+                                        g_hook_on.load() ? 1 : 0};
   return s;
 }
 }  // namespace fa
@@ -326,6 +327,7 @@ const char* fa_status_string(fa_status s) {
 void fa_debug_expire_at(uint32_t site) {
   (void)fa::set_expire_site_fwd(site);
   (void)fa::set_expire_site_bwd(site);
+  (void)fa::set_expire_site_cache4(site);
   g_hook_on.store(site != 0);
 }
 

@@ -55,6 +55,7 @@ constexpr int kItemCost = 3;                      // in units
 constexpr float kNoMax = -1e30f;                  // m of a row that has seen no key
 constexpr float kUp = 8.0f;                       // P carries 2^kUp
 constexpr float kSlack = 6.0f;                    // growth of m that is left standing
+constexpr uint32_t kWCopy = 0x511;                // where-code of the waits for copies
 
 __device__ __forceinline__ void e2m1_to_f16(uint32_t w, uint32_t* r) {
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
@@ -470,7 +471,8 @@ __device__ __forceinline__ void use_slot(Rows<D, NT>& r, const uint8_t* grps, in
     use_groups<D, NT, kU, kPlain>(r, grps + u * group_bytes(D), tok + u * kGroup, there >> u, bd, g, t);
 }
 
-template <int D, int NT>
+// kHook: the instantiation with the failure-path test hook.
+template <int D, int NT, bool kHook>
 __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
     cache4_attn_kernel(Cache4AttnArgs a) {
   using S = Shape<D, NT>;
@@ -711,7 +713,11 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
 
     int tok = sh_use[warp].r.lo + sh_use[warp].unit * kUnit + warp * kGroups * kGroup;
     for (int left = dead ? 0 : sh_use[warp].end - sh_use[warp].unit; left > 0; --left, tok += kUnit) {
-      if (!wait_bar_warp(&full[warp][got_slot], parity, ctl, 0x511)) {
+      // (The hook stops a block's first warp whether its copy has landed or
+      // not: a warp's first look at a barrier may sleep until it has.)
+      const bool expire = kHook && warp == 0 && c_expire_site == kWCopy;
+      if (expire && lane == 0) raise_abort(ctl, kWCopy);
+      if (expire || !wait_bar_warp(&full[warp][got_slot], parity, ctl, kWCopy)) {
         dead = true;
         break;
       }
@@ -874,10 +880,14 @@ __global__ void __launch_bounds__(kWarps * 32) cache4_join_kernel(Cache4AttnArgs
   if (lane == 0) a.lse[q_row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kHook = false>
 cudaError_t run(const Cache4AttnArgs& a, int sm_count, cudaStream_t stream) {
   using S = Shape<D, NT>;
-  auto* kernel = cache4_attn_kernel<D, NT>;
+  // The hook has its own instantiation, for d = 128 and items of 8 rows only.
+  if constexpr (D == 128 && NT == 1 && !kHook) {
+    if (a.hook) return run<D, NT, true>(a, sm_count, stream);
+  }
+  auto* kernel = cache4_attn_kernel<D, NT, kHook>;
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), S::kSmem, done);
   if (e != cudaSuccess) return e;
@@ -923,6 +933,10 @@ cudaError_t launch_cache4_attn(const Cache4AttnArgs& a, int d, int sm_count, cud
          : nt == 3 ? run<64, 3>(a, sm_count, stream)
          : nt == 4 ? run<64, 4>(a, sm_count, stream)
                    : run<64, 5>(a, sm_count, stream);
+}
+
+cudaError_t set_expire_site_cache4(uint32_t site) {
+  return cudaMemcpyToSymbol(c_expire_site, &site, sizeof(site));
 }
 
 }  // namespace fa

@@ -119,11 +119,15 @@ struct Cache4AttnArgs {
   float v_scale;
   DevState* st;
   uint64_t timeout_ns;
+  int hook;                 // 1: run the failure-path test hook instantiation
 };
 // Query rows of one work item: a multiple of 8 up to 40.
 int cache4_attn_rows(int rows, int d);
 cudaError_t launch_cache4_attn(const Cache4AttnArgs& a, int d, int sm_count,
                                cudaStream_t stream);
+// The site whose waits expire (0: none), on the current device.  Synchronous;
+// call only while no kernel of the library runs.
+cudaError_t set_expire_site_cache4(uint32_t site);
 
 // Launches a kernel whose launch overlaps the end of the work before it in
 // the stream.  The kernel waits for that work on the device, by
@@ -162,11 +166,13 @@ __device__ __forceinline__ void wait_for_stream() {
 cudaError_t allow_smem(const void* kernel, int bytes,
                        std::atomic<unsigned long long>& done);
 
-// Status record, SM count and wait limit of the current device.
+// Status record, SM count and wait limit of the current device, and whether
+// the failure-path test hook has a site.
 struct DeviceInfo {
   DevState* st;
   int sm_count;
   uint64_t timeout_ns;
+  int hook;
 };
 fa_status device_info(DeviceInfo* out);
 

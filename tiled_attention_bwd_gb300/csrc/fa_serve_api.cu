@@ -473,6 +473,7 @@ fa_status fa_cache4_attn(const void* q, const void* cache, const int* block_tabl
   a.v_scale = v_scale;
   a.st = dev.st;
   a.timeout_ns = dev.timeout_ns;
+  a.hook = dev.hook;
   return launched(fa::launch_cache4_attn(a, d, dev.sm_count, static_cast<cudaStream_t>(stream)));
 }
 
