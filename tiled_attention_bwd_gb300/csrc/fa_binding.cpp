@@ -13,8 +13,9 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
 
-#include <initializer_list>
+#include <memory>
 #include <optional>
+#include <stdexcept>
 #include <string>
 
 #include "fa.h"
@@ -34,8 +35,15 @@ struct Entries {
   decltype(&fa_cache4_append) append = nullptr;
   decltype(&fa_cache4_attn) attn = nullptr;
   decltype(&fa_cache4_attn_workspace_size) attn_size = nullptr;
-} g;
-bool g_host = false;  // CPU tensors pass (with entry points that only record)
+  bool host = false;  // CPU tensors pass (to entry points that only record)
+};
+// The table in use.  It is not changed but replaced, under the GIL; a call
+// takes it once, before it lets go of the GIL, and keeps it to its end.
+std::shared_ptr<const Entries> g_entries;
+std::shared_ptr<const Entries> entries() {
+  if (!g_entries) throw std::runtime_error("_fa_binding is not connected to libfa.so");
+  return g_entries;
+}
 
 template <typename F>
 void entry(const py::dict& from, const char* name, F& to) {
@@ -61,9 +69,9 @@ void want(const char* name, const Tensor& t, at::ScalarType type, const at::Devi
 }
 // A CUDA tensor of this type and number of axes (its device and sizes are
 // then the call's).
-void want_cuda(const char* name, const Tensor& t, at::ScalarType type, int64_t axes,
-               const char* what) {
-  if (t.scalar_type() != type || !(t.is_cuda() || (g_host && t.is_cpu())) || t.dim() != axes)
+void want_cuda(const Entries& g, const char* name, const Tensor& t, at::ScalarType type,
+               int64_t axes, const char* what) {
+  if (t.scalar_type() != type || !(t.is_cuda() || (g.host && t.is_cpu())) || t.dim() != axes)
     throw py::value_error(std::string(name) + " must be a " + what);
 }
 void want(const char* name, const Maybe& t, at::ScalarType type, const at::Device& device,
@@ -122,15 +130,15 @@ struct RopeCall {
   at::Device device;
   int B, N, H, Hkv, d, rows, rot, weight_bf16 = 0;
   TokenStrides s;
-  RopeCall(const Tensor& qkv, int64_t h, int64_t hkv, const Tensor& rope, const Maybe& positions,
-           const Maybe& qw, const Maybe& kw)
-      : device(qkv.device()), s(check("qkv", qkv), qkv) {
+  RopeCall(const Entries& g, const Tensor& qkv, int64_t h, int64_t hkv, const Tensor& rope,
+           const Maybe& positions, const Maybe& qw, const Maybe& kw)
+      : device(qkv.device()), s(check(g, "qkv", qkv), qkv) {
     if (h < 0 || hkv < 0 || qkv.size(2) != h + 2 * hkv)
       throw py::value_error("qkv has " + std::to_string(qkv.size(2)) +
                             " heads, expected H + 2 * Hkv = " + std::to_string(h + 2 * hkv));
     B = to_int(qkv.size(0), "B"), N = to_int(qkv.size(1), "N");
     H = to_int(h, "H"), Hkv = to_int(hkv, "Hkv"), d = to_int(qkv.size(3), "d");
-    want_cuda("rope", rope, at::kFloat, 2, "fp32 CUDA tensor [positions, rot]");
+    want_cuda(g, "rope", rope, at::kFloat, 2, "fp32 CUDA tensor [positions, rot]");
     want("rope", rope, at::kFloat, device, rope.sizes());
     rows = to_int(rope.size(0), "positions"), rot = to_int(rope.size(1), "rot");
     want("positions", positions, at::kInt, device, {B, N});
@@ -143,8 +151,8 @@ struct RopeCall {
       want("k_weight", *kw, type, device, {d});
     }
   }
-  static const char* check(const char* name, const Tensor& t) {
-    want_cuda(name, t, at::kBFloat16, 4, "bf16 CUDA tensor [B,N,heads,d]");
+  static const char* check(const Entries& g, const char* name, const Tensor& t) {
+    want_cuda(g, name, t, at::kBFloat16, 4, "bf16 CUDA tensor [B,N,heads,d]");
     return name;
   }
 };
@@ -152,7 +160,9 @@ struct RopeCall {
 py::tuple qk_norm_rope(const Tensor& qkv, int64_t H, int64_t Hkv, const Tensor& rope,
                        const Maybe& positions, const Maybe& qw, const Maybe& kw, double eps,
                        bool interleaved, const Maybe& q_, const Maybe& k_, const Maybe& v_) {
-  const RopeCall c(qkv, H, Hkv, rope, positions, qw, kw);
+  const auto held = entries();
+  const Entries& g = *held;
+  const RopeCall c(g, qkv, H, Hkv, rope, positions, qw, kw);
   const Tensor q = output("q", q_, at::kBFloat16, c.device, {c.B, c.H, c.N, c.d});
   const Tensor k = output("k", k_, at::kBFloat16, c.device, {c.B, c.Hkv, c.N, c.d});
   const Tensor v = output("v", v_, at::kBFloat16, c.device, {c.B, c.Hkv, c.N, c.d});
@@ -168,12 +178,14 @@ py::tuple qk_norm_rope_bwd(const Tensor& qkv, int64_t H, int64_t Hkv, const Tens
                            const Tensor& dq, const Tensor& dk, const Tensor& dv,
                            const Maybe& positions, const Maybe& qw, const Maybe& kw, double eps,
                            bool interleaved, const Maybe& dqkv_, const Maybe& workspace_) {
-  const RopeCall c(qkv, H, Hkv, rope, positions, qw, kw);
+  const auto held = entries();
+  const Entries& g = *held;
+  const RopeCall c(g, qkv, H, Hkv, rope, positions, qw, kw);
   want("dq", dq, at::kBFloat16, c.device, {c.B, c.H, c.N, c.d});
   want("dk", dk, at::kBFloat16, c.device, {c.B, c.Hkv, c.N, c.d});
   want("dv", dv, at::kBFloat16, c.device, {c.B, c.Hkv, c.N, c.d});
   if (dqkv_) {
-    RopeCall::check("dqkv", *dqkv_);
+    RopeCall::check(g, "dqkv", *dqkv_);
     if (dqkv_->sizes() != qkv.sizes() || dqkv_->device() != c.device)
       throw py::value_error("dqkv must have qkv's shape and device");
   }
@@ -202,8 +214,8 @@ py::tuple qk_norm_rope_bwd(const Tensor& qkv, int64_t H, int64_t Hkv, const Tens
 // A 4-bit cache, uint8 [pages, Hkv, page_size / 16, 18 d].
 struct Cache {
   int pages, Hkv, page, d;
-  explicit Cache(const Tensor& t) {
-    want_cuda("cache", t, at::kByte, 4, "uint8 CUDA tensor [pages, Hkv, page_size / 16, 18 * d]");
+  Cache(const Entries& g, const Tensor& t) {
+    want_cuda(g, "cache", t, at::kByte, 4, "uint8 CUDA tensor [pages, Hkv, page_size / 16, 18 * d]");
     if (t.size(3) % 18 || !t.is_contiguous())
       throw py::value_error("cache must be contiguous, its last axis 18 * d");
     pages = to_int(t.size(0), "pages"), Hkv = to_int(t.size(1), "Hkv");
@@ -215,9 +227,11 @@ py::tuple cache4_plan(const Tensor& fresh, const Tensor& lens, const Tensor& tab
                       const Tensor& free_list, const Tensor& free_count, int64_t page_size,
                       int64_t T_, const Maybe& slots_, const Maybe& positions_,
                       const Maybe& granted_) {
-  want_cuda("new_tokens", fresh, at::kInt, 1, "int32 CUDA tensor [R]");
-  want_cuda("block_table", table, at::kInt, 2, "int32 CUDA tensor [R, max_blocks]");
-  want_cuda("free_list", free_list, at::kInt, 1, "int32 CUDA tensor [pages]");
+  const auto held = entries();
+  const Entries& g = *held;
+  want_cuda(g, "new_tokens", fresh, at::kInt, 1, "int32 CUDA tensor [R]");
+  want_cuda(g, "block_table", table, at::kInt, 2, "int32 CUDA tensor [R, max_blocks]");
+  want_cuda(g, "free_list", free_list, at::kInt, 1, "int32 CUDA tensor [pages]");
   const at::Device device = fresh.device();
   const int R = to_int(fresh.size(0), "R"), M = to_int(table.size(1), "max_blocks");
   const int P = to_int(free_list.size(0), "pages"), T = to_int(T_, "T");
@@ -241,8 +255,10 @@ py::tuple cache4_plan(const Tensor& fresh, const Tensor& lens, const Tensor& tab
 
 int cache4_append(const Tensor& k, const Tensor& v, const Tensor& cache, const Tensor& slots,
                   double k_scale, double v_scale, const Maybe& k_out, const Maybe& v_out) {
-  const Cache c(cache);
-  want_cuda("k", k, at::kBFloat16, 4, "bf16 CUDA tensor [B,Hkv,N,d]");
+  const auto held = entries();
+  const Entries& g = *held;
+  const Cache c(g, cache);
+  want_cuda(g, "k", k, at::kBFloat16, 4, "bf16 CUDA tensor [B,Hkv,N,d]");
   const at::Device device = cache.device();
   const int B = to_int(k.size(0), "B"), N = to_int(k.size(2), "N");
   const int64_t shape[4] = {B, c.Hkv, N, c.d};
@@ -263,9 +279,11 @@ py::tuple cache4_attn(const Tensor& q, const Tensor& cache, const Tensor& table,
                       const Tensor& seq_lens, double scale, const Maybe& q_lens, int64_t window,
                       double k_scale, double v_scale, const Maybe& out_, const Maybe& lse_,
                       const Maybe& workspace_) {
-  const Cache c(cache);
-  want_cuda("q", q, at::kBFloat16, 4, "bf16 CUDA tensor [B,H,T,d]");
-  want_cuda("block_table", table, at::kInt, 2, "int32 CUDA tensor [B, max_blocks]");
+  const auto held = entries();
+  const Entries& g = *held;
+  const Cache c(g, cache);
+  want_cuda(g, "q", q, at::kBFloat16, 4, "bf16 CUDA tensor [B,H,T,d]");
+  want_cuda(g, "block_table", table, at::kInt, 2, "int32 CUDA tensor [B, max_blocks]");
   const at::Device device = cache.device();
   const int B = to_int(q.size(0), "B"), H = to_int(q.size(1), "H"), T = to_int(q.size(2), "T");
   const int M = to_int(table.size(1), "max_blocks"), w = to_int(window, "window");
@@ -289,15 +307,17 @@ py::tuple cache4_attn(const Tensor& q, const Tensor& cache, const Tensor& table,
 }  // namespace
 
 PYBIND11_MODULE(_fa_binding, m) {
-  m.def("connect", [](const py::dict& at, bool host) {
-    entry(at, "fa_qk_norm_rope", g.norm_rope);
-    entry(at, "fa_qk_norm_rope_bwd", g.norm_rope_bwd);
-    entry(at, "fa_qk_norm_rope_bwd_workspace_size", g.norm_rope_bwd_size);
-    entry(at, "fa_cache4_plan", g.plan);
-    entry(at, "fa_cache4_append", g.append);
-    entry(at, "fa_cache4_attn", g.attn);
-    entry(at, "fa_cache4_attn_workspace_size", g.attn_size);
-    g_host = host;
+  m.def("connect", [](const py::dict& from, bool host) {
+    Entries e;
+    entry(from, "fa_qk_norm_rope", e.norm_rope);
+    entry(from, "fa_qk_norm_rope_bwd", e.norm_rope_bwd);
+    entry(from, "fa_qk_norm_rope_bwd_workspace_size", e.norm_rope_bwd_size);
+    entry(from, "fa_cache4_plan", e.plan);
+    entry(from, "fa_cache4_append", e.append);
+    entry(from, "fa_cache4_attn", e.attn);
+    entry(from, "fa_cache4_attn_workspace_size", e.attn_size);
+    e.host = host;
+    g_entries = std::make_shared<const Entries>(e);
   });
   m.def("qk_norm_rope", &qk_norm_rope);
   m.def("qk_norm_rope_bwd", &qk_norm_rope_bwd);
