@@ -5,14 +5,16 @@
 // with one pass over the keys: running maximum m and sum l per row, the
 // values' sums rescaled when m grows.
 //
-// Work.  The query rows of one key/value head (H / Hkv heads x T tokens) are
-// taken 8 to 40 at a time; such a row block of one request and head is an
-// item, its keys are cut into units of 128, and all items' units together
-// are dealt to the blocks in equal consecutive shares, whatever the lengths
-// (an item counts as kItemCost units more, for what it costs to begin and
-// end one).  A block's four warps take two 16-token groups of a unit each,
-// with sums of their own, and join them when the item (or the share) ends; an
-// item that lies in several blocks' shares is joined by a second kernel.
+// Work.  The query rows of one request and key/value head (H / Hkv heads x
+// its new tokens, by token first) are taken 8 to 40 at a time; such a row block
+// is an item, the keys that it sees are cut into units of 128, and all items'
+// units together are dealt to the blocks in equal consecutive shares, whatever
+// the lengths (fa_cache4_work.h).  A block's four warps take two 16-token
+// groups of a unit each, with sums of their own, and join them when the item
+// (or the share) ends; an item that lies in several blocks' shares is joined
+// by a second kernel.  (Rows by head first, every item with all of its
+// request's keys, took 13.6 ms where one of 64 requests has 512 new tokens and
+// the others one each, of 64 heads over 8; so it takes 0.35 ms.)
 //
 // Feeding.  Each warp copies its own groups (18 d bytes, K and V together)
 // into a ring in shared memory by bulk copies, several ahead; nothing in the
@@ -35,13 +37,14 @@
 // 8192 tokens x 8 heads 62 us, 4.9 TB/s of codes and scales; 3 requests of
 // 100000 to 131072 tokens x 8 heads 73 us, 5.5 TB/s; with all pages in L2
 // 2 us less.  Tiles: two groups per step (one: 98 us at the batch, two: 79),
-// blocks per SM three (four, at 128 registers: 72 us, three: 70), kItemCost
+// blocks per SM three (four, at 128 registers: 72 us, three: 70), kC4ItemCost
 // three units (one: 79 us, three: 72, five: 74).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "fa_cache4.cuh"
+#include "fa_cache4_work.h"
 #include "fa_common.cuh"
 #include "fa_serve.h"
 
@@ -50,8 +53,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kGroups = 2;                        // of a warp in a unit
-constexpr int kUnit = kWarps * kGroups * kGroup;  // tokens of a work unit
-constexpr int kItemCost = 3;                      // in units
+static_assert(kC4Unit == kWarps * kGroups * kGroup && kC4Align == kGroups * kGroup);
 constexpr float kNoMax = -1e30f;                  // m of a row that has seen no key
 constexpr float kUp = 8.0f;                       // P carries 2^kUp
 constexpr float kSlack = 6.0f;                    // growth of m that is left standing
@@ -115,87 +117,17 @@ __device__ __forceinline__ void launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// What a request has, with the values from memory brought into range.
-struct Request {
-  int len, ql;  // cached tokens, new tokens
-  int lo;       // first token of its units (a multiple of 32)
-  int units;    // of one item
-  // Of one item, in shares.
-  __device__ __forceinline__ int cost() const { return units == 0 ? 0 : units + kItemCost; }
-};
-__device__ __forceinline__ Request request_of(const Cache4AttnArgs& a, int b) {
-  Request r;
-  const long long cap = (long long)a.M << a.shift;
-  const int l = a.seq_lens[b];
-  r.len = l < 0 ? 0 : (l > cap ? (int)cap : l);
-  const int n = a.q_lens ? a.q_lens[b] : a.T;
-  r.ql = n < 0 ? 0 : (n > a.T ? a.T : n);
-  const long long first = (long long)r.len - r.ql - a.window;  // the first row's window
-  r.lo = (a.window < 0 || first < 0) ? 0 : (int)(first & ~(long long)(kGroups * kGroup - 1));
-  const int n_keys = r.len - r.lo;
-  // A request without keys keeps one unit, which writes its empty rows.
-  r.units = r.ql == 0 ? 0 : (n_keys > 0 ? (n_keys - 1) / kUnit + 1 : 1);
-  return r;
+// The call as the division of work sees it, for items of kRows rows, and its
+// requests (read by plain loads: the kernel before may have written them).
+template <int kRows>
+__device__ __forceinline__ c4::Call call_of(const Cache4AttnArgs& a) {
+  return {a.B, a.Hkv, a.T, a.window, a.heads, kRows, a.row_blocks, a.M << a.shift, a.by_heads};
 }
-
-// A block's place in the list of items: the segment of the present item that
-// is its own, units [unit, end).
-struct Cursor {
-  int b;          // request
-  int hk, rb;     // the item's key/value head and row block
-  int unit, end;
-  int left;       // of the share, behind this segment
-  Request r;
-
-  // The segment of the present item that begins `at` into its cost.
-  __device__ __forceinline__ void segment(int at) {
-    const int here = min(r.cost() - at, left), to = at + here;
-    left -= here;
-    unit = max(0, at - kItemCost);
-    end = max(0, to - kItemCost);
-  }
-  // The next item's; false if the share has none.
-  __device__ __forceinline__ bool next(const Cache4AttnArgs& a) {
-    if (left == 0) return false;
-    if (++rb == a.row_blocks) {
-      rb = 0;
-      if (++hk == a.Hkv) {
-        hk = 0;
-        do r = request_of(a, ++b);
-        while (r.units == 0);
-      }
-    }
-    segment(0);
-    return end > 0;  // (a share may end before an item's first unit)
-  }
-};
-
-// Equal shares: `units` of cost dealt to blocks 0 .. blocks-1 in order, the
-// first `more` blocks one more than the others' `least`.
-struct Shares {
-  long long least;
-  int more, blocks;
-  __device__ __forceinline__ Shares(long long units, int grid) {
-    // No more blocks than units: every one that works has at least one.
-    blocks = (int)min((long long)grid, units);
-    if (blocks == 0) {
-      least = more = 0;
-    } else if ((units >> 32) == 0) {
-      least = (uint32_t)units / (uint32_t)blocks;
-      more = (int)((uint32_t)units - (uint32_t)least * (uint32_t)blocks);
-    } else {
-      least = units / blocks;
-      more = (int)(units - least * blocks);
-    }
-  }
-  __device__ __forceinline__ long long first(int c) const { return least * c + min(c, more); }
-  __device__ __forceinline__ int block_of(long long u) const {
-    const long long big = (least + 1) * more;
-    if ((u >> 31) == 0)
-      return u < big ? (int)u / (int)(least + 1) : more + (int)(u - big) / (int)least;
-    return (int)(u < big ? u / (least + 1) : more + (u - big) / least);
-  }
-};
+// Row `row` of a request and key/value head in q, o and lse.
+__device__ __forceinline__ size_t row_at(const Cache4AttnArgs& a, int b, int hk, int row) {
+  const int t = (int)a.by_heads.div(row), h = row - t * a.heads;
+  return (((size_t)b * a.Hkv + hk) * a.heads + h) * a.T + t;
+}
 
 template <int D, int NT>
 struct Shape {
@@ -336,11 +268,19 @@ __device__ __forceinline__ void values(const uint8_t* grp, int g, int t, const u
   }
 }
 
-// What bounds the keys that a segment's rows see.
+// What bounds the keys that a segment's rows see: its place, in shared memory
+// (it is needed for masks only, where registers are scarce).
 struct Bounds {
-  int row0, T;  // first row, rows of a head
-  int pos0;     // position of the first new token
-  int len, window;
+  const Cache4AttnArgs& a;
+  const c4::Cursor& at;
+  int rows;  // of an item
+  // Position of a row of the segment.
+  __device__ __forceinline__ int pos(int row) const {
+    return at.r.len - at.r.ql + (int)a.by_heads.div(at.rb * rows + row);
+  }
+  // A live row sees the keys low(pos) to pos, all of them in the cache.  Rows
+  // behind the live ones have Q = 0 and are not written.
+  __device__ __forceinline__ int low(int pos) const { return a.window < 0 ? 0 : pos - a.window; }
 };
 
 // kU groups' scores, minus infinity where a row does not see a token.
@@ -357,8 +297,8 @@ __device__ __forceinline__ void masked_scores(const Rows<D, NT>& r, const uint8_
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int pos = bd.pos0 + (bd.row0 + 8 * nt + 2 * t + i) % bd.T;
-        const int hi = min(pos + 1, bd.len), lo = bd.window < 0 ? 0 : pos - bd.window;
+        const int pos = bd.pos(8 * nt + 2 * t + i);
+        const int hi = pos + 1, lo = bd.low(pos);
 #pragma unroll
         for (int u = 0; u < kU; ++u)
 #pragma unroll
@@ -426,12 +366,7 @@ __device__ __forceinline__ void use_groups(Rows<D, NT>& r, const uint8_t* grps, 
       uint32_t two = *reinterpret_cast<const uint16_t*>(
           grp + v_scale_at(D, 8 * h + 2 * t, D == 128 ? g : g >> 1));
       if constexpr (!kPlain) {
-        // Tokens that no row sees may hold anything, NaN scales included.
-        const int j = tok + u * kGroup + 8 * h + 2 * t;
         if (!((there >> u) & 1)) two = 0;
-        const int lo = bd.window < 0 ? 0 : bd.pos0 - bd.window;
-        if (j < lo || j >= bd.len) two &= 0xff00u;
-        if (j + 1 < lo || j + 1 >= bd.len) two &= 0x00ffu;
         const uint32_t nan = __vcmpeq4(two & 0x7f7fu, 0x7f7f7f7fu);
         nans |= ((nan & 1) | (nan >> 7 & 2)) << (8 * h + 2 * t);
         two &= ~nan;
@@ -440,7 +375,7 @@ __device__ __forceinline__ void use_groups(Rows<D, NT>& r, const uint8_t* grps, 
     }
     values<D, NT>(grp, g, t, vs, pb, r.o);
     // A NaN goes to the rows that see its token, and not, by a weight of zero,
-    // to the others.
+    // to the others (a token that no row sees may hold anything).
     if (!kPlain && __any_sync(0xffffffffu, nans != 0)) {
       nans |= __shfl_xor_sync(0xffffffffu, nans, 1);
       nans |= __shfl_xor_sync(0xffffffffu, nans, 2);
@@ -448,9 +383,9 @@ __device__ __forceinline__ void use_groups(Rows<D, NT>& r, const uint8_t* grps, 
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int pos = bd.pos0 + (bd.row0 + 8 * nt + 2 * t + i) % bd.T, at = tok + u * kGroup;
-          const int hi = min(max(min(pos + 1, bd.len) - at, 0), kGroup);
-          const int lo = bd.window < 0 ? 0 : min(max(pos - bd.window - at, 0), kGroup);
+          const int pos = bd.pos(8 * nt + 2 * t + i), at = tok + u * kGroup;
+          const int hi = min(max(pos + 1 - at, 0), kGroup);
+          const int lo = min(max(bd.low(pos) - at, 0), kGroup);
           if (nans & ((1u << hi) - 1) & ~((1u << lo) - 1)) {
 #pragma unroll
             for (int dt = 0; dt < Shape<D, NT>::kTiles; ++dt)
@@ -481,8 +416,9 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
   __shared__ uint64_t full[kWarps][S::kStages];
   __shared__ int copied[kWarps][S::kStages];  // bit u: group u of the slot
   __shared__ uint32_t cta_abort;
-  __shared__ Cursor sh_load[kWarps], sh_use[kWarps];
-  __shared__ int sh_scan[kWarps], sh_first[3];
+  __shared__ c4::Cursor sh_load[kWarps], sh_use[kWarps], sh_first;
+  __shared__ int sh_into;
+  __shared__ long long sh_scan[kWarps];
   __shared__ float2 sh_ml[kWarps][8];
   __shared__ __align__(8) float sh_rs[S::kRows];
 
@@ -500,54 +436,39 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
   launch_dependents();
 
   // ---- this block's share of the units
-  const int items = a.Hkv * a.row_blocks;
-  const int per = (a.B + kWarps * 32 - 1) / (kWarps * 32);
-  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-  int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += request_of(a, b).cost();
-  int upto = mine;
+  const c4::Call call = call_of<S::kRows>(a);
+  auto read = [&](int b) {
+    return c4::request_of(call, a.seq_lens[b], a.q_lens ? a.q_lens[b] : a.T);
+  };
+  const int pairs = a.B * a.row_blocks, per = (pairs - 1) / (kWarps * 32) + 1;
+  const int p0 = (int)min((long long)pairs, (long long)tid * per), p1 = p0 + min(pairs - p0, per);
+  const long long mine = c4::cost_of(call, read, p0, p1);
+  long long upto = mine;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, upto, m);
+    const long long u = __shfl_up_sync(0xffffffffu, upto, m);
     if (lane >= m) upto += u;
   }
   if (lane == 31) sh_scan[warp] = upto;
   __syncthreads();
-  int total = 0;
+  long long total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) upto += sh_scan[w];
     total += sh_scan[w];
   }
-  const int before = upto - mine;
-  const Shares shares((long long)total * items, gridDim.x);
+  const long long before = upto - mine;
+  const c4::Shares shares(total * a.Hkv, gridDim.x);
   if ((int)blockIdx.x >= shares.blocks) {
     if (tid == 0) a.joins[blockIdx.x].x = -1;
     return;
   }
   const long long u0 = shares.first(blockIdx.x);
-  if (u0 >= (long long)before * items && u0 < (long long)upto * items) {
-    long long left = u0 - (long long)before * items;
-    int b = b0;
-    Request r = request_of(a, b);
-    while (left >= (long long)r.cost() * items) {
-      left -= (long long)r.cost() * items;
-      r = request_of(a, ++b);
-    }
-    sh_first[0] = b;
-    // (left < cost * items fits 31 bits but for absurd sizes.)
-    sh_first[1] = left >> 31 ? (int)(left / r.cost()) : (int)left / r.cost();
-    sh_first[2] = (int)(left - (long long)sh_first[1] * r.cost());
-  }
+  if (u0 >= before * a.Hkv && u0 < upto * a.Hkv)
+    sh_into = sh_first.seek(call, read, p0, u0 - before * a.Hkv,
+                            (int)(shares.first(blockIdx.x + 1) - u0));
   __syncthreads();
-  Cursor use;
-  use.b = sh_first[0];
-  use.hk = sh_first[1] / a.row_blocks;
-  use.rb = sh_first[1] - use.hk * a.row_blocks;
-  use.left = (int)(shares.first(blockIdx.x + 1) - u0);
-  use.r = request_of(a, use.b);
-  use.segment(sh_first[2]);
-
+  const c4::Cursor use = sh_first;
   if (use.end == use.unit) {  // a share of nothing but an item's cost
     if (tid == 0) a.joins[blockIdx.x].x = -1;
     return;
@@ -564,14 +485,14 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
   int put = 0, put_slot = 0;  // units passed by the loads, and their slot
   int turn = 0, turns = 0;    // place in the lanes' units
   const uint8_t* src[kGroups];
-  auto look_ahead = [&](const Cursor& load) {
+  auto look_ahead = [&](const c4::Cursor& load) {
     turn = 0;
     turns = min(32, load.end - load.unit);
 #pragma unroll
     for (int u = 0; u < kGroups; ++u) {
-      const int tok = load.r.lo + (load.unit + lane) * kUnit + (warp * kGroups + u) * kGroup;
+      const int tok = load.k.lo + (load.unit + lane) * kC4Unit + (warp * kGroups + u) * kGroup;
       src[u] = nullptr;
-      if (lane < turns && tok < load.r.len) {
+      if (lane < turns && tok < load.k.hi) {
         const int page = a.block_table[(size_t)load.b * a.M + (tok >> a.shift)];
         const int gpp_shift = a.shift - 4;
         if (page >= 0 && page < a.pages)
@@ -598,9 +519,9 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
     ++put;
     if (++put_slot == S::kStages) put_slot = 0;
     if (++turn == turns) {
-      Cursor load = sh_load[warp];
+      c4::Cursor load = sh_load[warp];
       load.unit += turns;
-      if (load.unit == load.end) more = load.next(a);
+      if (load.unit == load.end) more = load.next(call, read);
       if (more) look_ahead(load);
       __syncwarp();  // every lane has read the old place
       if (lane == 0) sh_load[warp] = load;
@@ -611,16 +532,13 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
   for (int i = 0; i < S::kStages && more; ++i) feed();
 
   // ---- Q: the next segment's raw rows are on their way while one is worked on
-  auto first_row = [&](const Cursor& c) {
-    return ((size_t)c.b * a.Hkv + c.hk) * a.rows + c.rb * S::kRows;
-  };
-  auto fetch_q = [&](const Cursor& c, int buffer) {
+  auto fetch_q = [&](const c4::Cursor& c, int buffer) {
     constexpr int kChunks = 2 * D / 16;
     uint8_t* dst = q_raw + buffer * S::kQRaw;
-    const int rows = min(S::kRows, a.rows - c.rb * S::kRows);
-    const uint8_t* q = reinterpret_cast<const uint8_t*>(a.q + first_row(c) * D);
+    const int row0 = c.rb * S::kRows, rows = min(S::kRows, c.r.ql * a.heads - row0);
     for (int i = tid; i < rows * kChunks; i += kWarps * 32)
-      copy16_async(dst + i / kChunks * S::kQPitch + i % kChunks * 16, q + i * 16);
+      copy16_async(dst + i / kChunks * S::kQPitch + i % kChunks * 16,
+                   a.q + row_at(a, c.b, c.hk, row0 + i / kChunks) * D + i % kChunks * 8);
   };
   fetch_q(use, 0);
 
@@ -630,12 +548,9 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
   // first group's warp being the one that is waited for.)
   if (tid == (kWarps - 1) * 32) {
     int4 j = make_int4(-1, 0, 0, 0);
-    if (use.unit > 0) {
-      const long long i0 = u0 - sh_first[2], before_us = shares.first(blockIdx.x - 1);
-      if (before_us <= i0 + kItemCost)
-        j = make_int4(use.b, use.hk * a.row_blocks + use.rb, shares.block_of(i0 + use.r.cost() - 1),
-                      2 * (blockIdx.x - 1) + (before_us < i0 ? 1 : 0));
-    }
+    int last, first_part;
+    if (c4::join_of(shares, use, blockIdx.x, u0, sh_into, &last, &first_part))
+      j = make_int4(use.b, use.hk * a.row_blocks + use.rb, last, first_part);
     a.joins[blockIdx.x] = j;
   }
 
@@ -644,13 +559,15 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
   bool dead = false;
   for (int seg = 0;; ++seg) {
     // ---- one segment
-    const int row0 = sh_use[warp].rb * S::kRows;
-    const Bounds bd = {row0, a.T, sh_use[warp].r.len - sh_use[warp].r.ql, sh_use[warp].r.len, a.window};
+    // The item's live rows, if they are fewer than all.
+    auto live_rows = [&] { return sh_use[warp].r.ql * a.heads - sh_use[warp].rb * S::kRows; };
+    const int live_q = live_rows();
+    const Bounds bd = {a, sh_use[warp], S::kRows};
     copies_done();
     __syncthreads();  // Q is there, and the other buffer's readers are done
     auto fetch_next = [&]() {
-      Cursor then = sh_use[warp];
-      if (then.next(a)) fetch_q(then, (seg + 1) % S::kQBuffers);
+      c4::Cursor then = sh_use[warp];
+      if (then.next(call, read)) fetch_q(then, (seg + 1) % S::kQBuffers);
     };
     if constexpr (S::kQBuffers == 2) fetch_next();
 
@@ -660,11 +577,10 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
     for (int nt = 0; nt < NT; ++nt) {
       if (!S::kQInRegs && nt % kWarps != warp) continue;
       uint32_t qf[D / 8], big = 0;
-      const bool live = row0 + 8 * nt + g < a.rows;
       const uint4* q = reinterpret_cast<const uint4*>(raw + (8 * nt + g) * S::kQPitch + t * (D / 2));
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const uint4 u = live ? q[i] : make_uint4(0, 0, 0, 0);
+        const uint4 u = 8 * nt + g < live_q ? q[i] : make_uint4(0, 0, 0, 0);
         qf[4 * i] = u.x, qf[4 * i + 1] = u.y, qf[4 * i + 2] = u.z, qf[4 * i + 3] = u.w;
       }
 #pragma unroll
@@ -708,11 +624,11 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
       for (int i = 0; i < kTiles; ++i)
         r.o[i][nt][0] = r.o[i][nt][1] = r.o[i][nt][2] = r.o[i][nt][3] = 0.f;
     }
-    // Tokens within [plain_lo, plain_hi) are seen by every row.
-    const int plain_hi = bd.pos0 + 1, plain_lo = a.window < 0 ? 0 : bd.len - 1 - a.window;
+    // Tokens within [plain_lo, plain_hi) are seen by every live row.
+    const int plain_hi = sh_use[warp].k.first + 1, plain_lo = bd.low(sh_use[warp].k.hi - 1);
 
-    int tok = sh_use[warp].r.lo + sh_use[warp].unit * kUnit + warp * kGroups * kGroup;
-    for (int left = dead ? 0 : sh_use[warp].end - sh_use[warp].unit; left > 0; --left, tok += kUnit) {
+    int tok = sh_use[warp].k.lo + sh_use[warp].unit * kC4Unit + warp * kGroups * kGroup;
+    for (int left = dead ? 0 : sh_use[warp].end - sh_use[warp].unit; left > 0; --left, tok += kC4Unit) {
       // (The hook stops a block's first warp whether its copy has landed or
       // not: a warp's first look at a barrier may sleep until it has.)
       const bool expire = kHook && warp == 0 && c_expire_site == kWCopy;
@@ -734,9 +650,9 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
     }
 
     // ---- join the warps, eight rows at a time: a warp writes two
-    Cursor at = sh_use[warp];
-    const bool whole = at.unit == 0 && at.end == at.r.units;
-    const size_t q_row = first_row(at);
+    c4::Cursor at = sh_use[warp];
+    const bool whole = at.unit == 0 && at.end == at.k.units;
+    const int live = live_rows();
     const int part_slot = 2 * blockIdx.x + (seg == 0 ? 0 : 1);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -749,7 +665,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
         const int row = 2 * t + i;
-        if (row0 + 8 * nt + row >= a.rows) continue;
+        if (8 * nt + row >= live) continue;
         if (g == 0) sh_ml[warp][row] = make_float2(r.m[nt][i], l);
         float* dst = join + (warp * 8 + row) * S::kPitch + g * (D / 8);
 #pragma unroll
@@ -760,8 +676,9 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int in = warp + k * kWarps, row = 8 * nt + in, rr = row0 + row;
-        if (rr >= a.rows || rr % a.T >= at.r.ql) continue;
+        const int in = warp + k * kWarps, row = 8 * nt + in;
+        if (row >= live) continue;
+        const size_t out = row_at(a, at.b, at.hk, at.rb * S::kRows + row);
         float mx = kNoMax, f[kWarps], sum = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sh_ml[w][in].x);
@@ -783,18 +700,18 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, NT>::kBlocksPerSm)
             acc.x += f[w] * v.x, acc.y += f[w] * v.y;
           }
           if (whole)
-            *reinterpret_cast<__nv_bfloat162*>(a.o + (q_row + row) * D + dim) =
+            *reinterpret_cast<__nv_bfloat162*>(a.o + out * D + dim) =
                 __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
           else
             *reinterpret_cast<float2*>(part.o + dim) = acc;
         }
         if (lane == 0) {
-          if (whole) a.lse[q_row + row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+          if (whole) a.lse[out] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
           else *part.ml = make_float2(mx, sum);
         }
       }
     }
-    const bool again = at.next(a);
+    const bool again = at.next(call, read);
     __syncwarp();  // every lane has read the old place
     if (lane == 0) sh_use[warp] = at;
     __syncwarp();
@@ -826,7 +743,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache4_join_kernel(Cache4AttnArgs
   const int b = j.x, hk = j.y / a.row_blocks;
   const int r = (j.y - hk * a.row_blocks) * S::kRows + row;
   // (Uniform in the block where the block shares a row.)
-  if (row >= S::kRows || r >= a.rows || r % a.T >= min(a.q_lens ? a.q_lens[b] : a.T, a.T)) return;
+  if (row >= S::kRows || r >= min(a.q_lens ? a.q_lens[b] : a.T, a.T) * a.heads) return;
   auto part = [&](int k) {
     return partial_of<D, NT>(a, k == 0 ? j.w : 2 * ((int)blockIdx.x + k - 1), row);
   };
@@ -872,7 +789,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache4_join_kernel(Cache4AttnArgs
     }
   }
   const float inv = sum > 0.f || sum != sum ? a.v_scale / sum : 0.f;
-  const size_t q_row = ((size_t)b * a.Hkv + hk) * a.rows + r;
+  const size_t q_row = row_at(a, b, hk, r);
   __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(a.o + q_row * D) + lane * (kDims / 2);
 #pragma unroll
   for (int i = 0; i < kDims; i += 2)

@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "fa.h"
+#include "fa_cache4_work.h"
 
 namespace fa {
 
@@ -47,24 +48,6 @@ cudaError_t launch_rope_fwd(const RopeArgs& a, int d, bool interleaved,
                             bool norm, int sm_count, cudaStream_t stream);
 cudaError_t launch_rope_bwd(const RopeArgs& a, int d, bool interleaved,
                             bool norm, int sm_count, cudaStream_t stream);
-
-// Division of 0 <= x < 2^31 by a number fixed at launch: three instructions
-// instead of about twenty (Granlund and Montgomery, "Division by invariant
-// integers using multiplication", 1994).
-struct FastDiv {
-  uint32_t by, mul, shift;
-  static FastDiv of(uint32_t by) {
-    FastDiv f = {by, 0, 0};
-    while (f.shift < 31 && (1u << f.shift) < by) ++f.shift;
-    f.mul = (uint32_t)(((1ull << 32) * ((1ull << f.shift) - by)) / by + 1);
-    return f;
-  }
-#ifdef __CUDACC__
-  __device__ __forceinline__ uint32_t div(uint32_t x) const {
-    return (__umulhi(mul, x) + x) >> shift;
-  }
-#endif
-};
 
 // Block tables and slot maps of the paged cache.
 struct PlanArgs {
@@ -111,7 +94,9 @@ struct Cache4AttnArgs {
   float* part;              // [2 kC4MaxBlocks][item rows][d]
   float2* part_ml;          // [2 kC4MaxBlocks][item rows]
   int B, Hkv, T, M, pages;
-  int rows;                 // H / Hkv * T: rows of one key/value head
+  int heads;                // H / Hkv, of one key/value head
+  FastDiv by_heads;
+  int rows;                 // heads * T: a request's most
   int row_blocks;
   int shift;                // log2 of the page size
   int window;               // < 0: none

@@ -461,7 +461,9 @@ fa_status fa_cache4_attn(const void* q, const void* cache, const int* block_tabl
   a.T = T;
   a.M = max_blocks;
   a.pages = pages;
-  a.rows = H / Hkv * T;
+  a.heads = H / Hkv;
+  a.by_heads = fa::FastDiv::of(a.heads);
+  a.rows = a.heads * T;
   const int rows = fa::cache4_attn_rows(a.rows, d);
   ws += align_up((size_t)fa::kC4MaxBlocks * 2 * rows * d * sizeof(float));
   a.part_ml = reinterpret_cast<float2*>(ws);
