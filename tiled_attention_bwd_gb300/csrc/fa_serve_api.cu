@@ -40,6 +40,10 @@ struct Rows {
   // Whether a row begins at an offset between lo and hi, both left out.
   // (Walks the shorter axis and solves for the other.)
   bool begins_within(Wide lo, Wide hi) const {
+    const Wide last_b = (B - 1) * sb, last_n = (N - 1) * sn;
+    if ((last_b < 0 ? last_b : 0) + (last_n < 0 ? last_n : 0) >= hi ||
+        (last_b > 0 ? last_b : 0) + (last_n > 0 ? last_n : 0) <= lo)
+      return false;
     if (B > N) return Rows{p, sn, sb, N, B, width}.begins_within(lo, hi);
     const Wide step = sn < 0 ? -sn : sn;
     for (long long b = 0; b < B; ++b) {
