@@ -257,7 +257,10 @@ fa_status fa_step_host(const void* q, const void* k, const void* v,
  * of qkv, p the token's position, w the norm's weight and R(p) the rotation:
  *   y = x * (mean(x^2) + eps)^(-1/2) * w,   out = R(p) y
  * for query heads (q_weight) and key heads (k_weight); value heads are only
- * moved.  Computed in fp32 and rounded once.
+ * moved.  Computed in fp32, the squares too, and rounded once: a row whose
+ * sum of squares overflows (entries of 1e18 and more) comes out as zeros, and
+ * with eps = 0 a row whose squares all vanish (entries below 1e-23) is not
+ * finite.
  *   qkv       : in, bf16 [B, N, H + 2 Hkv, d]: the H query heads of a token,
  *               then its Hkv key heads, then its Hkv value heads, contiguous;
  *               stride_b, stride_n: elements from one batch entry and from
@@ -409,6 +412,14 @@ fa_status fa_cache4_append(const void* k, const void* v, void* cache,
  * Table entries outside [0, pages) hide their tokens.  A row uses nothing of
  * tokens that it does not see, whatever they hold: a NaN scale reaches the
  * rows that see its token (of a value, in its 16 dims) and no others.
+ * Scores and the softmax's maxima and sums are fp32.  The weights are rounded
+ * to f16 for their product with the values, which is summed in fp32: within
+ * 2^-11 of a weight, down to 2^-22 of its row's largest; weights below about
+ * 2^-32 of it count in lse only.  Elements of q below 2^-25 of their row's
+ * largest are off by up to 2^-33 of that.
+ * Rows t >= q_lens[b] cost no pass over the keys, and a chunk's tokens none
+ * over keys far behind their positions: requests with one new token and with
+ * a chunk of a prompt can share a call.
  * The result does not depend on the order in which blocks run.  The kernel's
  * waits have the time limit of fa_set_wait_timeout_ns, where-code 0x511.
  */

@@ -25,9 +25,11 @@
 // the 16-high side and the few query rows the 8-wide side, so that eight
 // rows (one decode token of a group of up to 8 heads) waste nothing.  A code
 // times its scale has at most six significant bits: K and V enter exactly.
-// Q enters exactly too (bf16's 8 bits fit f16's 11, each row scaled by a
-// power of two to f16's range); P is rounded to f16 (2^-12), after a factor
-// 2^8 which keeps weights down to 2^-32 of the row's largest from vanishing.
+// Q's rows are scaled by a power of two, the largest to [2^8, 2^9): bf16's 8
+// bits fit f16's 11, and elements down to 2^-25 of their row's largest enter
+// exactly; below, f16's spacing is off by at most 2^-33 of the largest.  P is
+// rounded to f16 (half a step: 2^-11), after a factor 2^8: weights below 2^-22
+// of the row's largest lose low bits, those below about 2^-32 vanish.
 //
 // What bounds it is making f16 of 4-bit codes: a 16-token group of one head
 // costs 269 warp instructions (64 conversions, 64 products with scales, 24 to
