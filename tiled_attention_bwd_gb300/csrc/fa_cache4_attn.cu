@@ -33,11 +33,12 @@
 //
 // What bounds it is making f16 of 4-bit codes: a 16-token group of one head
 // costs 269 warp instructions (64 conversions, 64 products with scales, 24 to
-// put two tokens' value codes side by side, 16 matrix products, the softmax
-// and the loop), and twelve warps per SM find issue slots for 58% of the time.
+// put two tokens' value codes side by side, which the layout asks for, 16
+// matrix products, the softmax and the loop), and twelve warps per SM find
+// issue slots for 58% of the time.
 // Measured (d = 128, 8 query heads to a key/value head): 64 requests of 100 to
-// 8192 tokens x 8 heads 62 us, 4.9 TB/s of codes and scales; 3 requests of
-// 100000 to 131072 tokens x 8 heads 73 us, 5.5 TB/s; with all pages in L2
+// 8192 tokens x 8 heads 61 us, 5.0 TB/s of codes and scales; 3 requests of
+// 100000 to 131072 tokens x 8 heads 72 us, 5.5 TB/s; with all pages in L2
 // 2 us less.  Tiles: two groups per step (one: 98 us at the batch, two: 79),
 // blocks per SM three (four, at 128 registers: 72 us, three: 70), kC4ItemCost
 // three units (one: 79 us, three: 72, five: 74).
@@ -823,12 +824,12 @@ cudaError_t run(const Cache4AttnArgs& a, int sm_count, cudaStream_t stream) {
 
 // Rows of an item: what makes the least of the passes over the keys, each of
 // a cost by its width.  Measured, 16 requests of 8192 tokens x 8 heads (us):
-//   d = 128, 16 rows: 64 as 8 + 8, 51 as 16;  24: 88 as 8s, 62 at once;
-//            32: 83 as 16s, 76 at once;  40: 116 as 16s, 101 as 24s, 127 as
-//            32s, 105 at once (spilling: not built);  64: 146 as 24s, 131 as
-//            32s;  512 (x 4096 tokens): 261 as 24s, 250 as 32s
-//   d = 64,  32 rows: 54 as 16s, 51 at once;  40: 72 as 24s, 62 at once;
-//            64: 97 as 16s, 86 as 32s;  512: 167 as 32s, 165 as 40s
+//   d = 128, 16 rows: 62 as 8 + 8, 50 as 16;  24: 84 as 8s, 60 at once;
+//            32: 84 as 16s, 74 at once;  40: 118 as 16s, 103 as 24s, 129 as
+//            32s (at once it spills: not built);  64: 144 as 24s, 130 as 32s;
+//            512 (x 4096 tokens): 258 as 24s, 245 as 32s
+//   d = 64,  32 rows: 53 as 16s, 49 at once;  40: 70 as 24s, 58 at once;
+//            64: 94 as 16s, 82 as 32s;  512: 158 as 32s, 153 as 40s
 int cache4_attn_rows(int rows, int d) {
   const int cost[2][5] = {{22, 26, 36, 43, 52}, {32, 41, 52, 65, 0}};
   int best = 8;

@@ -19,9 +19,9 @@
 //
 // Bound by bytes, once the instructions are few enough: packed fp32
 // arithmetic, no division in the loop, loads that cost no registers.  On a
-// GB300 (copy bandwidth 6.71 TB/s), in a stream of calls: forward, 4 x 4096
+// GB300 (copy bandwidth 6.79 TB/s), in a stream of calls: forward, 4 x 4096
 // tokens of 64 + 16 heads of 128, 107 us or 6.3 TB/s; backward, 4 x 1024
-// tokens of 32 + 64 heads, 47 us or 5.8 TB/s, and 7 x 3001 tokens of 24 + 16
+// tokens of 32 + 64 heads, 48 us or 5.7 TB/s, and 7 x 3001 tokens of 24 + 16
 // heads of 64, half of each rotated, 54 us or 5.6 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
