@@ -12,8 +12,8 @@
  * section "Usage Examples" (basic forward pass; training with backward pass),
  * with tensors laid out as [batch, heads, seq_len, head_dim].  Before and
  * behind it stand the norm of query and key heads with the rotation of
- * positions, and a paged key/value cache held in 4 bits with the attention
- * of new tokens over it (last section).  The operation
+ * positions, and paged key/value caches held in 4 or 8 bits with the attention
+ * of new tokens over them (last section).  The operation
  * itself is O = softmax(scale * Q K^T [+ causal mask]) V with the online
  * softmax of the same page's "Online Softmax Algorithm" section (running max
  * m, running sum l); the backward recomputes P from the saved LSE, as in
@@ -433,6 +433,89 @@ fa_status fa_cache4_attn(const void* q, const void* cache,
                          float v_scale, void* stream);
 
 /*
+ * A paged key/value cache held in 8 bits, twice the 4-bit one's codes and most
+ * of bf16's accuracy.  `cache` is pages * fa_cache8_page_bytes(Hkv, page_size,
+ * d) bytes of device memory, 16-byte aligned, owned by the caller; pages, slots
+ * and block tables are as above, and fa_cache4_plan keeps them for either
+ * cache.
+ *
+ * The 16 tokens of a group (page_size / 16 of them in a page) share an exponent
+ * e for one head's keys and one for its values, within -60 .. 60:
+ *   code = E4M3(x / 2^e), to nearest, ties to even, saturating at +-448;
+ * the value held is code * 2^e, which bf16 represents exactly.  A call that
+ * writes tokens of a group takes the smallest e with |x| <= 448 * 2^e for all
+ * finite elements x of these tokens, or the group's present e if that is
+ * larger.  Where e grows, the codes of the group's other tokens are rounded,
+ * likewise, to the new one (those of 2^-6 * 2^e and more stay exact).  Writing
+ * a group's first token begins it: e then comes from this call's tokens alone,
+ * and tokens that the group held before are no longer there.  An infinity
+ * saturates and a NaN reads as NaN; neither counts for e.
+ *
+ * Layout: [pages][Hkv][page_size / 16] groups of 16 tokens, 32 d + 16 bytes:
+ *   K codes  [2][d/64][8][4][2][8]  axes: token / 8, dim / 64, token % 8,
+ *                                   dim % 32 / 8, dim % 64 / 32, dim % 8
+ *   V codes  [d/64][2][8][4][8][2]  axes: dim / 64, token / 8, dim % 64 / 8,
+ *                                   token % 8 / 2, dim % 8, token % 2
+ *   K's e, V's e                    one signed byte each, then 14 unused bytes
+ * A cache of zeros holds zeros.  fa_cache8_page_bytes returns 0 for sizes that
+ * are not supported.
+ */
+size_t fa_cache8_page_bytes(int Hkv, int page_size, int d);
+
+/*
+ * Writes keys and values to their slots of the 8-bit cache; arguments as
+ * fa_cache4_append's, without scales.  The values that k_out and v_out receive
+ * are those held at the end of this call (a later call that grows the group's
+ * exponent may round them again).
+ * The tokens of a call that share a group stand within 16 neighbouring tokens
+ * of one batch entry, in any order, as fa_cache4_plan places them; a group
+ * whose tokens stand elsewhere, or a slot that occurs twice, holds an
+ * unspecified mix of them.
+ */
+fa_status fa_cache8_append(const void* k, const void* v, void* cache,
+                           const int* slots, void* k_out, void* v_out, int B,
+                           int Hkv, int N, int d, int pages, int page_size,
+                           void* stream);
+
+/*
+ * Reads tokens back: row n of batch entry b receives the keys and values of the
+ * request's token starts[b] + n.
+ *   block_table  : in,  int32 [B, max_blocks]
+ *   seq_lens     : in,  int32 [B]  tokens in the cache, clamped to
+ *                  [0, max_blocks * page_size]
+ *   starts       : in,  int32 [B], or NULL for 0; clamped likewise
+ *   k_out, v_out : out, bf16 [B,Hkv,N,d]; rows of tokens at or past
+ *                  seq_lens[b], or on pages outside [0, pages), are left as
+ *                  they were
+ * The outputs overlap neither an input nor one another (refused).
+ */
+fa_status fa_cache8_read(const void* cache, const int* block_table,
+                         const int* seq_lens, const int* starts, void* k_out,
+                         void* v_out, int B, int Hkv, int N, int d,
+                         int max_blocks, int pages, int page_size,
+                         void* stream);
+
+/*
+ * Causal attention of each request's newest tokens over the 8-bit cache:
+ * arguments, masks, workspace rules and waits (where-code 0x521) as
+ * fa_cache4_attn's, without scales; the workspace is
+ * fa_cache8_attn_workspace_size(B, H, Hkv, T, d) bytes.  A NaN that the cache
+ * holds reaches the rows that see its token (of a value, in its dim) and no
+ * others.
+ * Scores and the softmax's maxima and sums are fp32.  The weights, each times
+ * its group's 2^e of the values, are rounded to f16 for their product with the
+ * codes, which is summed in fp32: within 2^-11 of such a product, down to 2^-22
+ * of its row's largest; products below about 2^-32 of it count in lse only.
+ */
+size_t fa_cache8_attn_workspace_size(int B, int H, int Hkv, int T, int d);
+fa_status fa_cache8_attn(const void* q, const void* cache,
+                         const int* block_table, const int* seq_lens,
+                         const int* q_lens, void* o, float* lse,
+                         void* workspace, size_t workspace_bytes, int B, int H,
+                         int Hkv, int T, int d, int max_blocks, int pages,
+                         int page_size, int window, float scale, void* stream);
+
+/*
  * Synchronises `stream`, then reports (and clears) the device status record
  * of the current GPU: FA_ERR_DEVICE_TIMEOUT if any kernel of this library
  * gave up on a pipeline wait since the last check, FA_ERR_CUDA if the stream
@@ -478,6 +561,7 @@ void fa_set_wait_timeout_ns(uint64_t ns);
  *             for dQ, 0x412 the finished dV, 0x413 the next item.
  *   cache attention: 0x511 a warp waiting for its copies (the hook takes the
  *             first warp of every block, whether its wait is complete or not).
+ *             0x521 the same over the 8-bit cache.
  * While a site is set, forward and backward calls with d = 128 and no
  * window, lengths or FP8, and cache attention calls with d = 128 and at most
  * 8 query rows per key/value head, run kernel instantiations compiled with

@@ -35,6 +35,10 @@ struct Entries {
   decltype(&fa_cache4_append) append = nullptr;
   decltype(&fa_cache4_attn) attn = nullptr;
   decltype(&fa_cache4_attn_workspace_size) attn_size = nullptr;
+  decltype(&fa_cache8_append) append8 = nullptr;
+  decltype(&fa_cache8_read) read8 = nullptr;
+  decltype(&fa_cache8_attn) attn8 = nullptr;
+  decltype(&fa_cache8_attn_workspace_size) attn8_size = nullptr;
   bool host = false;  // CPU tensors pass (to entry points that only record)
 };
 // The table in use.  It is not changed but replaced, under the GIL; a call
@@ -211,15 +215,20 @@ py::tuple qk_norm_rope_bwd(const Tensor& qkv, int64_t H, int64_t Hkv, const Tens
 }
 
 // ------------------------------------------------------------------ cache
-// A 4-bit cache, uint8 [pages, Hkv, page_size / 16, 18 d].
+// A cache, uint8 [pages, Hkv, page_size / 16, 18 d] in 4 bits, or [pages, Hkv,
+// page_size / 16, 32 d + 16] in 8.
 struct Cache {
   int pages, Hkv, page, d;
-  Cache(const Entries& g, const Tensor& t) {
-    want_cuda(g, "cache", t, at::kByte, 4, "uint8 CUDA tensor [pages, Hkv, page_size / 16, 18 * d]");
-    if (t.size(3) % 18 || !t.is_contiguous())
-      throw py::value_error("cache must be contiguous, its last axis 18 * d");
+  Cache(const Entries& g, const Tensor& t, int bits = 4) {
+    want_cuda(g, "cache", t, at::kByte, 4,
+              bits == 4 ? "uint8 CUDA tensor [pages, Hkv, page_size / 16, 18 * d]"
+                        : "uint8 CUDA tensor [pages, Hkv, page_size / 16, 32 * d + 16]");
+    const int64_t codes = t.size(3) - (bits == 4 ? 0 : 16), per = bits == 4 ? 18 : 32;
+    if (codes < 0 || codes % per || !t.is_contiguous())
+      throw py::value_error(std::string("cache must be contiguous, its last axis ") +
+                            (bits == 4 ? "18 * d" : "32 * d + 16"));
     pages = to_int(t.size(0), "pages"), Hkv = to_int(t.size(1), "Hkv");
-    page = to_int(16 * t.size(2), "page_size"), d = to_int(t.size(3) / 18, "d");
+    page = to_int(16 * t.size(2), "page_size"), d = to_int(codes / per, "d");
   }
 };
 
@@ -275,33 +284,104 @@ int cache4_append(const Tensor& k, const Tensor& v, const Tensor& cache, const T
   });
 }
 
+// What the attention's calls over either cache have in common.
+struct AttnCall {
+  at::Device device;
+  int B, H, T, M, window;
+  Tensor out, lse, ws;
+  AttnCall(const Entries& g, const Cache& c, const Tensor& q, const Tensor& cache,
+           const Tensor& table, const Tensor& seq_lens, const Maybe& q_lens, int64_t window_,
+           const Maybe& out_, const Maybe& lse_, const Maybe& workspace_,
+           decltype(&fa_cache4_attn_workspace_size) size)
+      : device(cache.device()) {
+    want_cuda(g, "q", q, at::kBFloat16, 4, "bf16 CUDA tensor [B,H,T,d]");
+    want_cuda(g, "block_table", table, at::kInt, 2, "int32 CUDA tensor [B, max_blocks]");
+    B = to_int(q.size(0), "B"), H = to_int(q.size(1), "H"), T = to_int(q.size(2), "T");
+    M = to_int(table.size(1), "max_blocks"), window = to_int(window_, "window");
+    want("q", q, at::kBFloat16, device, {B, H, T, c.d});
+    want("block_table", table, at::kInt, device, {B, M});
+    want("seq_lens", seq_lens, at::kInt, device, {B});
+    want("q_lens", q_lens, at::kInt, device, {B});
+    out = output("out", out_, at::kBFloat16, device, {B, H, T, c.d});
+    lse = output("lse", lse_, at::kFloat, device, {B, H, T});
+    ws = workspace_of(workspace_, std::max<size_t>(size(B, H, c.Hkv, T, c.d), 256), device);
+  }
+};
+
 py::tuple cache4_attn(const Tensor& q, const Tensor& cache, const Tensor& table,
                       const Tensor& seq_lens, double scale, const Maybe& q_lens, int64_t window,
-                      double k_scale, double v_scale, const Maybe& out_, const Maybe& lse_,
-                      const Maybe& workspace_) {
+                      double k_scale, double v_scale, const Maybe& out, const Maybe& lse,
+                      const Maybe& workspace) {
   const auto held = entries();
   const Entries& g = *held;
   const Cache c(g, cache);
-  want_cuda(g, "q", q, at::kBFloat16, 4, "bf16 CUDA tensor [B,H,T,d]");
+  const AttnCall x(g, c, q, cache, table, seq_lens, q_lens, window, out, lse, workspace, g.attn_size);
+  const int status = launch(x.device, [&](void* stream) {
+    return g.attn(at_of(q), at_of(cache), at_of<int>(table), at_of<int>(seq_lens),
+                  at_of<int>(q_lens), at_of(x.out), at_of<float>(x.lse), at_of(x.ws),
+                  x.ws.nbytes(), x.B, x.H, c.Hkv, x.T, c.d, x.M, c.pages, c.page, x.window,
+                  (float)scale, (float)k_scale, (float)v_scale, stream);
+  });
+  return py::make_tuple(status, x.out, x.lse);
+}
+
+int cache8_append(const Tensor& k, const Tensor& v, const Tensor& cache, const Tensor& slots,
+                  const Maybe& k_out, const Maybe& v_out) {
+  const auto held = entries();
+  const Entries& g = *held;
+  const Cache c(g, cache, 8);
+  want_cuda(g, "k", k, at::kBFloat16, 4, "bf16 CUDA tensor [B,Hkv,N,d]");
+  const at::Device device = cache.device();
+  const int B = to_int(k.size(0), "B"), N = to_int(k.size(2), "N");
+  const int64_t shape[4] = {B, c.Hkv, N, c.d};
+  want("k", k, at::kBFloat16, device, shape);
+  want("v", v, at::kBFloat16, device, shape);
+  want("slots", slots, at::kInt, device, {B, N});
+  if (k_out.has_value() != v_out.has_value()) throw py::value_error("k_out and v_out come together");
+  want("k_out", k_out, at::kBFloat16, device, shape);
+  want("v_out", v_out, at::kBFloat16, device, shape);
+  return launch(device, [&](void* stream) {
+    return g.append8(at_of(k), at_of(v), at_of(cache), at_of<int>(slots), at_of(k_out),
+                     at_of(v_out), B, c.Hkv, N, c.d, c.pages, c.page, stream);
+  });
+}
+
+py::tuple cache8_read(const Tensor& cache, const Tensor& table, const Tensor& seq_lens, int64_t N_,
+                      const Maybe& starts, const Maybe& k_out, const Maybe& v_out) {
+  const auto held = entries();
+  const Entries& g = *held;
+  const Cache c(g, cache, 8);
   want_cuda(g, "block_table", table, at::kInt, 2, "int32 CUDA tensor [B, max_blocks]");
   const at::Device device = cache.device();
-  const int B = to_int(q.size(0), "B"), H = to_int(q.size(1), "H"), T = to_int(q.size(2), "T");
-  const int M = to_int(table.size(1), "max_blocks"), w = to_int(window, "window");
-  want("q", q, at::kBFloat16, device, {B, H, T, c.d});
+  const int B = to_int(table.size(0), "B"), M = to_int(table.size(1), "max_blocks");
+  const int N = to_int(N_, "N");
+  if (N < 0) throw py::value_error("N must not be negative");
   want("block_table", table, at::kInt, device, {B, M});
   want("seq_lens", seq_lens, at::kInt, device, {B});
-  want("q_lens", q_lens, at::kInt, device, {B});
-  const Tensor out = output("out", out_, at::kBFloat16, device, {B, H, T, c.d});
-  const Tensor lse = output("lse", lse_, at::kFloat, device, {B, H, T});
-  const Tensor ws =
-      workspace_of(workspace_, std::max<size_t>(g.attn_size(B, H, c.Hkv, T, c.d), 256), device);
+  want("starts", starts, at::kInt, device, {B});
+  const Tensor k = output("k_out", k_out, at::kBFloat16, device, {B, c.Hkv, N, c.d});
+  const Tensor v = output("v_out", v_out, at::kBFloat16, device, {B, c.Hkv, N, c.d});
   const int status = launch(device, [&](void* stream) {
-    return g.attn(at_of(q), at_of(cache), at_of<int>(table), at_of<int>(seq_lens),
-                  at_of<int>(q_lens), at_of(out), at_of<float>(lse), at_of(ws), ws.nbytes(), B, H,
-                  c.Hkv, T, c.d, M, c.pages, c.page, w, (float)scale, (float)k_scale, (float)v_scale,
-                  stream);
+    return g.read8(at_of(cache), at_of<int>(table), at_of<int>(seq_lens), at_of<int>(starts),
+                   at_of(k), at_of(v), B, c.Hkv, N, c.d, M, c.pages, c.page, stream);
   });
-  return py::make_tuple(status, out, lse);
+  return py::make_tuple(status, k, v);
+}
+
+py::tuple cache8_attn(const Tensor& q, const Tensor& cache, const Tensor& table,
+                      const Tensor& seq_lens, double scale, const Maybe& q_lens, int64_t window,
+                      const Maybe& out, const Maybe& lse, const Maybe& workspace) {
+  const auto held = entries();
+  const Entries& g = *held;
+  const Cache c(g, cache, 8);
+  const AttnCall x(g, c, q, cache, table, seq_lens, q_lens, window, out, lse, workspace, g.attn8_size);
+  const int status = launch(x.device, [&](void* stream) {
+    return g.attn8(at_of(q), at_of(cache), at_of<int>(table), at_of<int>(seq_lens),
+                   at_of<int>(q_lens), at_of(x.out), at_of<float>(x.lse), at_of(x.ws),
+                   x.ws.nbytes(), x.B, x.H, c.Hkv, x.T, c.d, x.M, c.pages, c.page, x.window,
+                   (float)scale, stream);
+  });
+  return py::make_tuple(status, x.out, x.lse);
 }
 
 }  // namespace
@@ -316,6 +396,10 @@ PYBIND11_MODULE(_fa_binding, m) {
     entry(from, "fa_cache4_append", e.append);
     entry(from, "fa_cache4_attn", e.attn);
     entry(from, "fa_cache4_attn_workspace_size", e.attn_size);
+    entry(from, "fa_cache8_append", e.append8);
+    entry(from, "fa_cache8_read", e.read8);
+    entry(from, "fa_cache8_attn", e.attn8);
+    entry(from, "fa_cache8_attn_workspace_size", e.attn8_size);
     e.host = host;
     g_entries = std::make_shared<const Entries>(e);
   });
@@ -324,4 +408,7 @@ PYBIND11_MODULE(_fa_binding, m) {
   m.def("cache4_plan", &cache4_plan);
   m.def("cache4_append", &cache4_append);
   m.def("cache4_attn", &cache4_attn);
+  m.def("cache8_append", &cache8_append);
+  m.def("cache8_read", &cache8_read);
+  m.def("cache8_attn", &cache8_attn);
 }

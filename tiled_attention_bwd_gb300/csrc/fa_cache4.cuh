@@ -18,9 +18,10 @@
 #pragma once
 #include <cstdint>
 
+#include "fa_cache4_work.h"
+
 namespace fa {
 
-constexpr int kGroup = 16;  // tokens of a group
 __host__ __device__ constexpr int group_bytes(int d) { return 18 * d; }
 
 __device__ __forceinline__ int k_code_at(int d, int tok, int byte) { return tok * (d / 2) + byte; }

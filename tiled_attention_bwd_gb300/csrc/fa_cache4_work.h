@@ -22,6 +22,7 @@
 
 namespace fa {
 
+constexpr int kGroup = 16;      // tokens of a group of the cache
 constexpr int kC4Unit = 128;    // keys of a unit
 constexpr int kC4Align = 32;    // an item's first key is a multiple of it
 constexpr int kC4ItemCost = 3;  // in units

@@ -1,6 +1,6 @@
 // fa_serve.h -- internal interface between the host layer (fa_serve_api.cu)
 // and the kernels of the norm with rotation and of the 4-bit cache (fa_rope.cu,
-// fa_cache4.cu, fa_cache4_attn.cu).  Not part of the ABI.
+// fa_cache4.cu, fa_cache4_attn.cu, fa_cache8*.cu).  Not part of the ABI.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -79,9 +79,34 @@ struct AppendArgs {
 };
 cudaError_t launch_cache4_append(const AppendArgs& a, int d, cudaStream_t stream);
 
-// Attention over the 4-bit cache.
+// New keys and values into their slots of the 8-bit cache.
+struct Append8Args {
+  const __nv_bfloat16 *k, *v;    // [B, Hkv, N, d]
+  __nv_bfloat16 *k_out, *v_out;  // rounded values, or null
+  uint8_t* cache;
+  const int* slots;              // [B, N]
+  int warps;                     // B * Hkv * chunks
+  int N, Hkv, chunks, slots_end, shift;
+  FastDiv by_chunks, by_Hkv;
+};
+cudaError_t launch_cache8_append(const Append8Args& a, int d, cudaStream_t stream);
+
+// Tokens of the 8-bit cache back into rows.
+struct Read8Args {
+  const uint8_t* cache;
+  const int* block_table;        // [B, M]
+  const int* seq_lens;           // [B]
+  const int* starts;             // [B] or null (0)
+  __nv_bfloat16 *k_out, *v_out;  // [B, Hkv, N, d]
+  int warps;                     // B * Hkv * chunks
+  int N, Hkv, M, pages, chunks, shift;
+  FastDiv by_chunks, by_Hkv;
+};
+cudaError_t launch_cache8_read(const Read8Args& a, int d, cudaStream_t stream);
+
+// Attention over a cache, in either format.
 constexpr int kC4MaxBlocks = 640;
-struct Cache4AttnArgs {
+struct CacheAttnArgs {
   const __nv_bfloat16* q;   // [B, H, T, d]
   const uint8_t* cache;
   const int* block_table;   // [B, M]
@@ -108,11 +133,15 @@ struct Cache4AttnArgs {
 };
 // Query rows of one work item: a multiple of 8 up to 40.
 int cache4_attn_rows(int rows, int d);
-cudaError_t launch_cache4_attn(const Cache4AttnArgs& a, int d, int sm_count,
+cudaError_t launch_cache4_attn(const CacheAttnArgs& a, int d, int sm_count,
+                               cudaStream_t stream);
+int cache8_attn_rows(int rows, int d);
+cudaError_t launch_cache8_attn(const CacheAttnArgs& a, int d, int sm_count,
                                cudaStream_t stream);
 // The site whose waits expire (0: none), on the current device.  Synchronous;
 // call only while no kernel of the library runs.
 cudaError_t set_expire_site_cache4(uint32_t site);
+cudaError_t set_expire_site_cache8(uint32_t site);
 
 // Launches a kernel whose launch overlaps the end of the work before it in
 // the stream.  The kernel waits for that work on the device, by

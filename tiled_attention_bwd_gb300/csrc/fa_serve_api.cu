@@ -9,6 +9,7 @@
 
 #include "fa.h"
 #include "fa_cache4.cuh"
+#include "fa_cache8.cuh"
 #include "fa_serve.h"
 
 namespace {
@@ -184,11 +185,110 @@ fa_status check_cache(int pages, int Hkv, int page, int d, int* shift) {
   return FA_OK;
 }
 
-long long cache_bytes(int pages, int Hkv, int page, int d) {
-  return (long long)pages * Hkv * (page / fa::kGroup) * fa::group_bytes(d);
+// A format's bytes of a group, and its attention's rows of an item and launch.
+struct Format {
+  int (*group)(int d);
+  int (*rows)(int rows, int d);
+  cudaError_t (*attn)(const fa::CacheAttnArgs& a, int d, int sm_count, cudaStream_t stream);
+};
+constexpr Format kCache4 = {fa::group_bytes, fa::cache4_attn_rows, fa::launch_cache4_attn};
+constexpr Format kCache8 = {fa::group8_bytes, fa::cache8_attn_rows, fa::launch_cache8_attn};
+
+long long cache_bytes(const Format& f, int pages, int Hkv, int page, int d) {
+  return (long long)pages * Hkv * (page / fa::kGroup) * f.group(d);
+}
+size_t page_bytes(const Format& f, int Hkv, int page_size, int d) {
+  int shift = 0;
+  if (Hkv <= 0 || check_cache(0, Hkv, page_size, d, &shift) != FA_OK) return 0;
+  return (size_t)cache_bytes(f, 1, Hkv, page_size, d);
 }
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+
+// Attention over a cache in either format.
+size_t attn_workspace_size(const Format& f, int B, int H, int Hkv, int T, int d) {
+  if (head_dim(d) != FA_OK || B <= 0 || H <= 0 || T <= 0 || Hkv <= 0 || H % Hkv != 0) return 0;
+  if ((long long)B * H * T > INT_MAX) return 0;
+  const int rows = f.rows(H / Hkv * T, d);
+  return align_up(fa::kC4MaxBlocks * sizeof(int4)) +
+         align_up((size_t)fa::kC4MaxBlocks * 2 * rows * d * sizeof(float)) +
+         (size_t)fa::kC4MaxBlocks * 2 * rows * sizeof(float2);
+}
+
+fa_status cache_attn(const Format& f, const void* q, const void* cache, const int* block_table,
+                     const int* seq_lens, const int* q_lens, void* o, float* lse, void* workspace,
+                     size_t workspace_bytes, int B, int H, int Hkv, int T, int d, int max_blocks,
+                     int pages, int page_size, int window, float scale, float k_scale,
+                     float v_scale, void* stream) {
+  int shift = 0;
+  fa_status s = check_cache(pages, Hkv, page_size, d, &shift);
+  if (s != FA_OK) return s;
+  if (B < 0 || H < 0 || T < 0 || max_blocks < 0) return FA_ERR_INVALID_ARG;
+  if (H > 0 && (Hkv == 0 || Hkv > H || H % Hkv != 0)) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.0f)) return FA_ERR_INVALID_ARG;
+  if (!cache_scale(k_scale) || !cache_scale(v_scale)) return FA_ERR_INVALID_ARG;
+  const float scale_log2 = scale * k_scale * 1.4426950408889634f;
+  if (!std::isfinite(scale_log2)) return FA_ERR_INVALID_ARG;
+  // Positions, which begin at -T, less a window stay within an int.
+  if (((long long)max_blocks << shift) + T > INT_MAX || (long long)B * H > INT_MAX ||
+      (long long)B * H * T > INT_MAX || (long long)B * max_blocks > INT_MAX)
+    return FA_ERR_UNSUPPORTED;
+  // All requests' units of 128 keys together, and a block's share of the
+  // work, are counted in 31 bits.
+  if ((double)B * ((double)max_blocks * page_size / 128 + 4) > INT_MAX) return FA_ERR_UNSUPPORTED;
+  if ((double)B * max_blocks * page_size * H * T > 0x1p45) return FA_ERR_UNSUPPORTED;
+  if (B == 0 || H == 0 || T == 0) return FA_OK;
+  if (!q || !seq_lens || !o || !lse || (pages > 0 && !cache) || (max_blocks > 0 && !block_table))
+    return FA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(cache, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
+      !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(q_lens, 4))
+    return FA_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < attn_workspace_size(f, B, H, Hkv, T, d))
+    return FA_ERR_WORKSPACE;
+  const long long q_rows = (long long)B * H * T;
+  if (meet({span(o, 2 * q_rows * d), span(lse, 4 * q_rows),
+            span(workspace, attn_workspace_size(f, B, H, Hkv, T, d))},
+           {span(q, 2 * q_rows * d), span(cache, cache_bytes(f, pages, Hkv, page_size, d)),
+            span(block_table, 4LL * B * max_blocks), span(seq_lens, 4LL * B),
+            span(q_lens, 4LL * B)}))
+    return FA_ERR_INVALID_ARG;
+  fa::DeviceInfo dev;
+  if ((s = fa::device_info(&dev)) != FA_OK) return s;
+  fa::CacheAttnArgs a = {};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.q_lens = q_lens;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  char* ws = static_cast<char*>(workspace);
+  a.joins = reinterpret_cast<int4*>(ws);
+  ws += align_up(fa::kC4MaxBlocks * sizeof(int4));
+  a.part = reinterpret_cast<float*>(ws);
+  a.B = B;
+  a.Hkv = Hkv;
+  a.T = T;
+  a.M = max_blocks;
+  a.pages = pages;
+  a.heads = H / Hkv;
+  a.by_heads = fa::FastDiv::of(a.heads);
+  a.rows = a.heads * T;
+  const int rows = f.rows(a.rows, d);
+  ws += align_up((size_t)fa::kC4MaxBlocks * 2 * rows * d * sizeof(float));
+  a.part_ml = reinterpret_cast<float2*>(ws);
+  a.row_blocks = (a.rows + rows - 1) / rows;
+  a.shift = shift;
+  // A window of the whole table hides nothing.
+  a.window = window < 0 || (long long)window >= ((long long)max_blocks << shift) ? -1 : window;
+  a.scale_log2 = scale_log2;
+  a.v_scale = v_scale;
+  a.st = dev.st;
+  a.timeout_ns = dev.timeout_ns;
+  a.hook = dev.hook;
+  return launched(f.attn(a, d, dev.sm_count, static_cast<cudaStream_t>(stream)));
+}
 
 }  // namespace
 
@@ -310,9 +410,7 @@ fa_status fa_qk_norm_rope_bwd(const void* qkv, long long stride_b, long long str
 }
 
 size_t fa_cache4_page_bytes(int Hkv, int page_size, int d) {
-  int shift = 0;
-  if (Hkv <= 0 || check_cache(0, Hkv, page_size, d, &shift) != FA_OK) return 0;
-  return (size_t)Hkv * (page_size / fa::kGroup) * fa::group_bytes(d);
+  return page_bytes(kCache4, Hkv, page_size, d);
 }
 
 fa_status fa_cache4_plan(const int* new_tokens, int* lens, int* block_table, int* free_list,
@@ -374,7 +472,7 @@ fa_status fa_cache4_append(const void* k, const void* v, void* cache, const int*
     return FA_ERR_INVALID_ARG;
   const long long bytes = 2LL * B * Hkv * N * d;
   const Span ko = span(k_out, bytes), vo = span(v_out, bytes);
-  if (meet({span(cache, cache_bytes(pages, Hkv, page_size, d)), ko, vo},
+  if (meet({span(cache, cache_bytes(kCache4, pages, Hkv, page_size, d)), ko, vo},
            {span(slots, 4LL * B * N), span(k_out == k ? nullptr : k, bytes),
             span(v_out == v ? nullptr : v, bytes)}))
     return FA_ERR_INVALID_ARG;
@@ -400,12 +498,7 @@ fa_status fa_cache4_append(const void* k, const void* v, void* cache, const int*
 }
 
 size_t fa_cache4_attn_workspace_size(int B, int H, int Hkv, int T, int d) {
-  if (head_dim(d) != FA_OK || B <= 0 || H <= 0 || T <= 0 || Hkv <= 0 || H % Hkv != 0) return 0;
-  if ((long long)B * H * T > INT_MAX) return 0;
-  const int rows = fa::cache4_attn_rows(H / Hkv * T, d);
-  return align_up(fa::kC4MaxBlocks * sizeof(int4)) +
-         align_up((size_t)fa::kC4MaxBlocks * 2 * rows * d * sizeof(float)) +
-         (size_t)fa::kC4MaxBlocks * 2 * rows * sizeof(float2);
+  return attn_workspace_size(kCache4, B, H, Hkv, T, d);
 }
 
 fa_status fa_cache4_attn(const void* q, const void* cache, const int* block_table,
@@ -413,74 +506,111 @@ fa_status fa_cache4_attn(const void* q, const void* cache, const int* block_tabl
                          void* workspace, size_t workspace_bytes, int B, int H, int Hkv, int T,
                          int d, int max_blocks, int pages, int page_size, int window, float scale,
                          float k_scale, float v_scale, void* stream) {
+  return cache_attn(kCache4, q, cache, block_table, seq_lens, q_lens, o, lse, workspace,
+                    workspace_bytes, B, H, Hkv, T, d, max_blocks, pages, page_size, window, scale,
+                    k_scale, v_scale, stream);
+}
+
+size_t fa_cache8_page_bytes(int Hkv, int page_size, int d) {
+  return page_bytes(kCache8, Hkv, page_size, d);
+}
+
+fa_status fa_cache8_append(const void* k, const void* v, void* cache, const int* slots, void* k_out,
+                           void* v_out, int B, int Hkv, int N, int d, int pages, int page_size,
+                           void* stream) {
   int shift = 0;
   fa_status s = check_cache(pages, Hkv, page_size, d, &shift);
   if (s != FA_OK) return s;
-  if (B < 0 || H < 0 || T < 0 || max_blocks < 0) return FA_ERR_INVALID_ARG;
-  if (H > 0 && (Hkv == 0 || Hkv > H || H % Hkv != 0)) return FA_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || !(scale > 0.0f)) return FA_ERR_INVALID_ARG;
-  if (!cache_scale(k_scale) || !cache_scale(v_scale)) return FA_ERR_INVALID_ARG;
-  const float scale_log2 = scale * k_scale * 1.4426950408889634f;
-  if (!std::isfinite(scale_log2)) return FA_ERR_INVALID_ARG;
-  // Positions, which begin at -T, less a window stay within an int.
-  if (((long long)max_blocks << shift) + T > INT_MAX || (long long)B * H > INT_MAX ||
-      (long long)B * H * T > INT_MAX || (long long)B * max_blocks > INT_MAX)
+  if (B < 0 || N < 0) return FA_ERR_INVALID_ARG;
+  if ((k_out == nullptr) != (v_out == nullptr)) return FA_ERR_INVALID_ARG;
+  // (A warp's work ends up to 31 tokens behind the last one.)
+  if ((long long)B * Hkv > INT_MAX || (long long)B * Hkv * N > INT_MAX || N > INT_MAX - 64)
     return FA_ERR_UNSUPPORTED;
-  // All requests' units of 128 keys together, and a block's share of the
-  // work, are counted in 31 bits.
-  if ((double)B * ((double)max_blocks * page_size / 128 + 4) > INT_MAX) return FA_ERR_UNSUPPORTED;
-  if ((double)B * max_blocks * page_size * H * T > 0x1p45) return FA_ERR_UNSUPPORTED;
-  if (B == 0 || H == 0 || T == 0) return FA_OK;
-  if (!q || !seq_lens || !o || !lse || (pages > 0 && !cache) || (max_blocks > 0 && !block_table))
+  if (B == 0 || Hkv == 0 || N == 0 || pages == 0) return FA_OK;
+  if (!k || !v || !cache || !slots) return FA_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cache, 16) || !aligned(slots, 4) ||
+      !aligned(k_out, 16) || !aligned(v_out, 16))
     return FA_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(cache, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
-      !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(q_lens, 4))
+  const long long bytes = 2LL * B * Hkv * N * d;
+  const Span ko = span(k_out, bytes), vo = span(v_out, bytes);
+  if (meet({span(cache, cache_bytes(kCache8, pages, Hkv, page_size, d)), ko, vo},
+           {span(slots, 4LL * B * N), span(k_out == k ? nullptr : k, bytes),
+            span(v_out == v ? nullptr : v, bytes)}))
     return FA_ERR_INVALID_ARG;
-  if (!workspace || !aligned(workspace, 256) ||
-      workspace_bytes < fa_cache4_attn_workspace_size(B, H, Hkv, T, d))
-    return FA_ERR_WORKSPACE;
-  const long long q_rows = (long long)B * H * T;
-  if (meet({span(o, 2 * q_rows * d), span(lse, 4 * q_rows),
-            span(workspace, fa_cache4_attn_workspace_size(B, H, Hkv, T, d))},
-           {span(q, 2 * q_rows * d), span(cache, cache_bytes(pages, Hkv, page_size, d)),
-            span(block_table, 4LL * B * max_blocks), span(seq_lens, 4LL * B),
-            span(q_lens, 4LL * B)}))
+  // (The cache meets no input; values that replace their own keys or values
+  // still meet nothing else.)
+  if (ko.meets(span(v, bytes)) || vo.meets(span(k, bytes))) return FA_ERR_INVALID_ARG;
+  fa::Append8Args a = {};
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.k_out = static_cast<__nv_bfloat16*>(k_out);
+  a.v_out = static_cast<__nv_bfloat16*>(v_out);
+  a.cache = static_cast<uint8_t*>(cache);
+  a.slots = slots;
+  a.N = N;
+  a.Hkv = Hkv;
+  a.chunks = (N - 1) / 16 + 1;
+  a.warps = B * Hkv * a.chunks;
+  a.by_chunks = fa::FastDiv::of(a.chunks);
+  a.by_Hkv = fa::FastDiv::of(Hkv);
+  a.slots_end = pages << shift;
+  a.shift = shift;
+  return launched(fa::launch_cache8_append(a, d, static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_cache8_read(const void* cache, const int* block_table, const int* seq_lens,
+                         const int* starts, void* k_out, void* v_out, int B, int Hkv, int N, int d,
+                         int max_blocks, int pages, int page_size, void* stream) {
+  int shift = 0;
+  fa_status s = check_cache(pages, Hkv, page_size, d, &shift);
+  if (s != FA_OK) return s;
+  if (B < 0 || N < 0 || max_blocks < 0) return FA_ERR_INVALID_ARG;
+  // Positions and a row block's end are counted in 31 bits.
+  if ((long long)B * Hkv > INT_MAX || (long long)B * Hkv * ((N + 15LL) / 16 + 1) > INT_MAX ||
+      N > INT_MAX - 64 || (((long long)max_blocks << shift) + 64) > INT_MAX ||
+      (long long)B * max_blocks > INT_MAX)
+    return FA_ERR_UNSUPPORTED;
+  if (B == 0 || Hkv == 0 || N == 0 || max_blocks == 0 || pages == 0) return FA_OK;
+  if (!cache || !block_table || !seq_lens || !k_out || !v_out) return FA_ERR_INVALID_ARG;
+  if (!aligned(cache, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(starts, 4) || !aligned(k_out, 16) || !aligned(v_out, 16))
     return FA_ERR_INVALID_ARG;
-  fa::DeviceInfo dev;
-  if ((s = fa::device_info(&dev)) != FA_OK) return s;
-  fa::Cache4AttnArgs a = {};
-  a.q = static_cast<const __nv_bfloat16*>(q);
+  const long long bytes = 2LL * B * Hkv * N * d;
+  if (meet({span(k_out, bytes), span(v_out, bytes)},
+           {span(cache, cache_bytes(kCache8, pages, Hkv, page_size, d)),
+            span(block_table, 4LL * B * max_blocks), span(seq_lens, 4LL * B), span(starts, 4LL * B)}))
+    return FA_ERR_INVALID_ARG;
+  fa::Read8Args a = {};
   a.cache = static_cast<const uint8_t*>(cache);
   a.block_table = block_table;
   a.seq_lens = seq_lens;
-  a.q_lens = q_lens;
-  a.o = static_cast<__nv_bfloat16*>(o);
-  a.lse = lse;
-  char* ws = static_cast<char*>(workspace);
-  a.joins = reinterpret_cast<int4*>(ws);
-  ws += align_up(fa::kC4MaxBlocks * sizeof(int4));
-  a.part = reinterpret_cast<float*>(ws);
-  a.B = B;
+  a.starts = starts;
+  a.k_out = static_cast<__nv_bfloat16*>(k_out);
+  a.v_out = static_cast<__nv_bfloat16*>(v_out);
+  a.N = N;
   a.Hkv = Hkv;
-  a.T = T;
   a.M = max_blocks;
   a.pages = pages;
-  a.heads = H / Hkv;
-  a.by_heads = fa::FastDiv::of(a.heads);
-  a.rows = a.heads * T;
-  const int rows = fa::cache4_attn_rows(a.rows, d);
-  ws += align_up((size_t)fa::kC4MaxBlocks * 2 * rows * d * sizeof(float));
-  a.part_ml = reinterpret_cast<float2*>(ws);
-  a.row_blocks = (a.rows + rows - 1) / rows;
+  a.chunks = (N - 1) / 16 + 2;  // groups that N tokens may lie in
+  a.warps = B * Hkv * a.chunks;
+  a.by_chunks = fa::FastDiv::of(a.chunks);
+  a.by_Hkv = fa::FastDiv::of(Hkv);
   a.shift = shift;
-  // A window of the whole table hides nothing.
-  a.window = window < 0 || (long long)window >= ((long long)max_blocks << shift) ? -1 : window;
-  a.scale_log2 = scale_log2;
-  a.v_scale = v_scale;
-  a.st = dev.st;
-  a.timeout_ns = dev.timeout_ns;
-  a.hook = dev.hook;
-  return launched(fa::launch_cache4_attn(a, d, dev.sm_count, static_cast<cudaStream_t>(stream)));
+  return launched(fa::launch_cache8_read(a, d, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_cache8_attn_workspace_size(int B, int H, int Hkv, int T, int d) {
+  return attn_workspace_size(kCache8, B, H, Hkv, T, d);
+}
+
+fa_status fa_cache8_attn(const void* q, const void* cache, const int* block_table,
+                         const int* seq_lens, const int* q_lens, void* o, float* lse,
+                         void* workspace, size_t workspace_bytes, int B, int H, int Hkv, int T,
+                         int d, int max_blocks, int pages, int page_size, int window, float scale,
+                         void* stream) {
+  return cache_attn(kCache8, q, cache, block_table, seq_lens, q_lens, o, lse, workspace,
+                    workspace_bytes, B, H, Hkv, T, d, max_blocks, pages, page_size, window, scale,
+                    1.0f, 1.0f, stream);
 }
 
 }  // extern "C"

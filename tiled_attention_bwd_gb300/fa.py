@@ -10,7 +10,8 @@ Names mirror the C ABI: ``fa_fwd``, ``fa_bwd``, ``fa_bwd_workspace_size``,
 ``fa_debug_expire_wait``, ``fa_debug_expire_at``, ``fa_last_failure_site``,
 ``fa_bwd_set_phase_events``, ``fa_status_string``; ``fa_qk_norm_rope``,
 ``fa_qk_norm_rope_bwd``, ``fa_cache4_plan``, ``fa_cache4_append``,
-``fa_cache4_attn``.
+``fa_cache4_attn``; ``fa_cache8_append``, ``fa_cache8_read``,
+``fa_cache8_attn``.
 """
 import ctypes
 import importlib.util
@@ -131,6 +132,19 @@ def open_library(path: str):
     lib.fa_cache4_attn.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, sz, i, i, i,
                                    i, i, i, i, i, i, f, f, f, vp]
     lib.fa_cache4_attn.restype = i
+    lib.fa_cache8_page_bytes.argtypes = [i, i, i]
+    lib.fa_cache8_page_bytes.restype = sz
+    lib.fa_cache8_append.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i,
+                                     vp]
+    lib.fa_cache8_append.restype = i
+    lib.fa_cache8_read.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i,
+                                   vp]
+    lib.fa_cache8_read.restype = i
+    lib.fa_cache8_attn_workspace_size.argtypes = [i, i, i, i, i]
+    lib.fa_cache8_attn_workspace_size.restype = sz
+    lib.fa_cache8_attn.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, sz, i, i, i,
+                                   i, i, i, i, i, i, f, vp]
+    lib.fa_cache8_attn.restype = i
     lib.fa_status_string.argtypes = [i]
     lib.fa_status_string.restype = ctypes.c_char_p
     return lib
@@ -518,7 +532,7 @@ def fa_bwd_noalloc(q, k, v, o, lse, dout, causal: bool, scale: float, dq,
     return dq, dk, dv
 
 
-# ---- norm with rotation, and the 4-bit cache.  A decode step makes several
+# ---- norm with rotation, and the caches in 4 and 8 bits.  A decode step makes several
 # of these calls per layer, each a few microseconds of GPU time, so their
 # checks, outputs and stream are marshalled by compiled code
 # (csrc/fa_binding.cpp); the arguments are the same as in Python.
@@ -527,7 +541,9 @@ _native_module = None
 _NATIVE = ("fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
            "fa_qk_norm_rope_bwd_workspace_size", "fa_cache4_plan",
            "fa_cache4_append", "fa_cache4_attn",
-           "fa_cache4_attn_workspace_size")
+           "fa_cache4_attn_workspace_size", "fa_cache8_append",
+           "fa_cache8_read", "fa_cache8_attn",
+           "fa_cache8_attn_workspace_size")
 
 
 def _connect(module, lib, host=False):
@@ -643,4 +659,51 @@ def fa_cache4_attn(q, cache, block_table, seq_lens, scale: float, q_lens=None,
         v_scale, out, lse, workspace)
     if status:
         raise FAError("fa_cache4_attn", status)
+    return out, lse
+
+
+def fa_cache8_page_bytes(Hkv: int, page_size: int, d: int) -> int:
+    return int(load_library().fa_cache8_page_bytes(Hkv, page_size, d))
+
+
+def fa_cache8_append(k, v, cache, slots, k_out=None, v_out=None):
+    """Writes keys and values, bf16 [B,Hkv,N,d], to their slots (int32
+    [B,N]) of the 8-bit cache, uint8 [pages, Hkv, page_size / 16,
+    32 * d + 16].  Tokens that share a group of 16 slots stand within 16
+    neighbouring tokens of one batch entry.  k_out and v_out, if given,
+    receive the values that the cache then holds (they may be k and v).
+    Returns the cache."""
+    status = _native().cache8_append(k, v, cache, slots, k_out, v_out)
+    if status:
+        raise FAError("fa_cache8_append", status)
+    return cache
+
+
+def fa_cache8_read(cache, block_table, seq_lens, N: int, starts=None,
+                   k_out=None, v_out=None):
+    """Tokens starts[b] .. starts[b] + N - 1 (starts: int32 [B], or None for
+    0) of each request, as the 8-bit cache holds them.  block_table: int32
+    [B, max_blocks]; seq_lens: int32 [B].  Rows past a request's tokens are
+    left as they were.  Returns (k, v), bf16 [B,Hkv,N,d]."""
+    status, k, v = _native().cache8_read(cache, block_table, seq_lens, N,
+                                         starts, k_out, v_out)
+    if status:
+        raise FAError("fa_cache8_read", status)
+    return k, v
+
+
+def fa_cache8_attn_workspace_size(B: int, H: int, Hkv: int, T: int,
+                                  d: int) -> int:
+    return int(load_library().fa_cache8_attn_workspace_size(B, H, Hkv, T, d))
+
+
+def fa_cache8_attn(q, cache, block_table, seq_lens, scale: float, q_lens=None,
+                   window: int = -1, out=None, lse=None, workspace=None):
+    """fa_cache4_attn over the 8-bit cache: causal attention of the newest
+    tokens of each request, q bf16 [B,H,T,d].  Returns (O, LSE)."""
+    status, out, lse = _native().cache8_attn(
+        q, cache, block_table, seq_lens, scale, q_lens, window, out, lse,
+        workspace)
+    if status:
+        raise FAError("fa_cache8_attn", status)
     return out, lse
