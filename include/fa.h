@@ -314,6 +314,39 @@ fa_status fa_qk_norm_rope_bwd(const void* qkv, long long stride_b,
                               int Hkv, int d, void* stream);
 
 /*
+ * The same with positions of several axes, e.g. time, height and width of
+ * images and video: every pair of dims turns by its own axis's position.
+ *   positions : in, int32 [n_axes, B, N]; clamped to [0, rope_rows); 1 to 4 axes
+ *   axes      : in, HOST memory, [rot/2] bytes below n_axes: the axis of each
+ *               pair, in any order (sections, or axes in turn); read during the
+ *               call
+ * Pair i of a token turns by angle i of row positions[axes[i]][b][n] of `rope`,
+ * (cos, sin) = (rope[row][i], rope[row][rot/2 + i]).  Everything else, and the
+ * workspace of the backward, is as without axes.
+ */
+fa_status fa_qk_norm_rope_axes(const void* qkv, long long stride_b,
+                               long long stride_n, const float* rope,
+                               int rope_rows, int rot, const int* positions,
+                               int n_axes, const uint8_t* axes,
+                               const void* q_weight, const void* k_weight,
+                               int weight_bf16, float eps, int interleaved,
+                               void* q, void* k, void* v, int B, int N, int H,
+                               int Hkv, int d, void* stream);
+fa_status fa_qk_norm_rope_axes_bwd(const void* qkv, long long stride_b,
+                                   long long stride_n, const float* rope,
+                                   int rope_rows, int rot, const int* positions,
+                                   int n_axes, const uint8_t* axes,
+                                   const void* q_weight, const void* k_weight,
+                                   int weight_bf16, float eps, int interleaved,
+                                   const void* dq, const void* dk,
+                                   const void* dv, void* dqkv,
+                                   long long dstride_b, long long dstride_n,
+                                   float* dq_weight, float* dk_weight,
+                                   void* workspace, size_t workspace_bytes,
+                                   int B, int N, int H, int Hkv, int d,
+                                   void* stream);
+
+/*
  * A paged key/value cache held in 4 bits.  `cache` is pages *
  * fa_cache4_page_bytes(Hkv, page_size, d) bytes of device memory, 16-byte
  * aligned, owned by the caller; page_size is 16, 32, 64, 128 or 256 tokens.

@@ -69,6 +69,19 @@ def norm_rope_bwd(qkv, H, Hkv, table, positions, qw, kw, eps, interleaved,
     return np.concatenate(parts, 2), dws[0], dws[1]
 
 
+def axes_table(table, positions, axes):
+    """Positions of several axes [A,B,N] as plain ones [B,N] into a table of
+    one row per token: pair i of a token with the angle of its axis axes[i]."""
+    pos = np.clip(np.asarray(positions, np.int64), 0, table.shape[0] - 1)
+    half = table.shape[1] // 2
+    _, B, N = pos.shape
+    rows = np.empty((B * N, 2 * half), np.float32)
+    for i in range(half):
+        at = pos[axes[i]].reshape(-1)
+        rows[:, i], rows[:, half + i] = table[at, i], table[at, half + i]
+    return rows, np.arange(B * N).reshape(B, N)
+
+
 # ------------------------------------------------------------ 4-bit format
 def _e4m3_grid():
     """The 127 non-negative finite E4M3 values by code."""

@@ -10,6 +10,7 @@ from .fa import (FAError, fa_cache4_append, fa_cache4_attn,
                  fa_cache4_plan, fa_cache8_append, fa_cache8_attn,
                  fa_cache8_attn_workspace_size, fa_cache8_page_bytes,
                  fa_cache8_read, fa_qk_norm_rope, fa_qk_norm_rope_bwd,
+                 fa_qk_norm_rope_axes, fa_qk_norm_rope_axes_bwd,
                  fa_qk_norm_rope_bwd_workspace_size, fa_bwd, fa_bwd_ext, fa_bwd_ext_workspace_size,
                  fa_bwd_noalloc, fa_bwd_varlen, fa_fwd_varlen,
                  fa_bwd_noalloc_max_workspace, fa_bwd_set_phase_events,
@@ -30,6 +31,7 @@ __all__ = ["FAError", "fa_fwd", "fa_bwd", "fa_fwd_ext", "fa_bwd_ext",
            "fa_set_wait_timeout_ns", "fa_debug_expire_wait",
            "fa_debug_expire_at", "fa_last_failure_site",
            "fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
+           "fa_qk_norm_rope_axes", "fa_qk_norm_rope_axes_bwd",
            "fa_qk_norm_rope_bwd_workspace_size", "fa_cache4_page_bytes",
            "fa_cache4_plan", "fa_cache4_append", "fa_cache4_attn",
            "fa_cache4_attn_workspace_size", "fa_cache8_page_bytes",

@@ -31,6 +31,8 @@ struct Entries {
   decltype(&fa_qk_norm_rope) norm_rope = nullptr;
   decltype(&fa_qk_norm_rope_bwd) norm_rope_bwd = nullptr;
   decltype(&fa_qk_norm_rope_bwd_workspace_size) norm_rope_bwd_size = nullptr;
+  decltype(&fa_qk_norm_rope_axes) norm_rope_axes = nullptr;
+  decltype(&fa_qk_norm_rope_axes_bwd) norm_rope_axes_bwd = nullptr;
   decltype(&fa_cache4_plan) plan = nullptr;
   decltype(&fa_cache4_append) append = nullptr;
   decltype(&fa_cache4_attn) attn = nullptr;
@@ -130,12 +132,18 @@ struct TokenStrides {
   }
 };
 
+// The axis of each rotated pair, one byte each, if positions have axes.
+using Axes = std::optional<std::string>;
+const uint8_t* bytes_of(const Axes& axes) {
+  return reinterpret_cast<const uint8_t*>(axes->data());
+}
+
 struct RopeCall {
   at::Device device;
-  int B, N, H, Hkv, d, rows, rot, weight_bf16 = 0;
+  int B, N, H, Hkv, d, rows, rot, weight_bf16 = 0, n_axes = 0;
   TokenStrides s;
   RopeCall(const Entries& g, const Tensor& qkv, int64_t h, int64_t hkv, const Tensor& rope,
-           const Maybe& positions, const Maybe& qw, const Maybe& kw)
+           const Maybe& positions, const Axes& axes, const Maybe& qw, const Maybe& kw)
       : device(qkv.device()), s(check(g, "qkv", qkv), qkv) {
     if (h < 0 || hkv < 0 || qkv.size(2) != h + 2 * hkv)
       throw py::value_error("qkv has " + std::to_string(qkv.size(2)) +
@@ -145,7 +153,17 @@ struct RopeCall {
     want_cuda(g, "rope", rope, at::kFloat, 2, "fp32 CUDA tensor [positions, rot]");
     want("rope", rope, at::kFloat, device, rope.sizes());
     rows = to_int(rope.size(0), "positions"), rot = to_int(rope.size(1), "rot");
-    want("positions", positions, at::kInt, device, {B, N});
+    if (axes) {
+      if (!positions || positions->dim() != 3)
+        throw py::value_error("positions must be an int32 tensor [axes, B, N]");
+      n_axes = to_int(positions->size(0), "axes");
+      want("positions", positions, at::kInt, device, {n_axes, B, N});
+      if ((int64_t)axes->size() != rot / 2)
+        throw py::value_error("axes has " + std::to_string(axes->size()) + " pairs, expected " +
+                              std::to_string(rot / 2));
+    } else {
+      want("positions", positions, at::kInt, device, {B, N});
+    }
     if (qw.has_value() != kw.has_value())
       throw py::value_error("q_weight and k_weight come together");
     if (qw) {
@@ -162,15 +180,21 @@ struct RopeCall {
 };
 
 py::tuple qk_norm_rope(const Tensor& qkv, int64_t H, int64_t Hkv, const Tensor& rope,
-                       const Maybe& positions, const Maybe& qw, const Maybe& kw, double eps,
-                       bool interleaved, const Maybe& q_, const Maybe& k_, const Maybe& v_) {
+                       const Maybe& positions, const Axes& axes, const Maybe& qw, const Maybe& kw,
+                       double eps, bool interleaved, const Maybe& q_, const Maybe& k_,
+                       const Maybe& v_) {
   const auto held = entries();
   const Entries& g = *held;
-  const RopeCall c(g, qkv, H, Hkv, rope, positions, qw, kw);
+  const RopeCall c(g, qkv, H, Hkv, rope, positions, axes, qw, kw);
   const Tensor q = output("q", q_, at::kBFloat16, c.device, {c.B, c.H, c.N, c.d});
   const Tensor k = output("k", k_, at::kBFloat16, c.device, {c.B, c.Hkv, c.N, c.d});
   const Tensor v = output("v", v_, at::kBFloat16, c.device, {c.B, c.Hkv, c.N, c.d});
   const int status = launch(c.device, [&](void* stream) {
+    if (axes)
+      return g.norm_rope_axes(at_of(qkv), c.s.b, c.s.n, at_of<float>(rope), c.rows, c.rot,
+                              at_of<int>(positions), c.n_axes, bytes_of(axes), at_of(qw),
+                              at_of(kw), c.weight_bf16, (float)eps, interleaved, at_of(q), at_of(k),
+                              at_of(v), c.B, c.N, c.H, c.Hkv, c.d, stream);
     return g.norm_rope(at_of(qkv), c.s.b, c.s.n, at_of<float>(rope), c.rows, c.rot,
                        at_of<int>(positions), at_of(qw), at_of(kw), c.weight_bf16, (float)eps,
                        interleaved, at_of(q), at_of(k), at_of(v), c.B, c.N, c.H, c.Hkv, c.d, stream);
@@ -180,11 +204,12 @@ py::tuple qk_norm_rope(const Tensor& qkv, int64_t H, int64_t Hkv, const Tensor& 
 
 py::tuple qk_norm_rope_bwd(const Tensor& qkv, int64_t H, int64_t Hkv, const Tensor& rope,
                            const Tensor& dq, const Tensor& dk, const Tensor& dv,
-                           const Maybe& positions, const Maybe& qw, const Maybe& kw, double eps,
-                           bool interleaved, const Maybe& dqkv_, const Maybe& workspace_) {
+                           const Maybe& positions, const Axes& axes, const Maybe& qw,
+                           const Maybe& kw, double eps, bool interleaved, const Maybe& dqkv_,
+                           const Maybe& workspace_) {
   const auto held = entries();
   const Entries& g = *held;
-  const RopeCall c(g, qkv, H, Hkv, rope, positions, qw, kw);
+  const RopeCall c(g, qkv, H, Hkv, rope, positions, axes, qw, kw);
   want("dq", dq, at::kBFloat16, c.device, {c.B, c.H, c.N, c.d});
   want("dk", dk, at::kBFloat16, c.device, {c.B, c.Hkv, c.N, c.d});
   want("dv", dv, at::kBFloat16, c.device, {c.B, c.Hkv, c.N, c.d});
@@ -205,6 +230,13 @@ py::tuple qk_norm_rope_bwd(const Tensor& qkv, int64_t H, int64_t Hkv, const Tens
     size = workspace->nbytes();
   }
   const int status = launch(c.device, [&](void* stream) {
+    if (axes)
+      return g.norm_rope_axes_bwd(at_of(qkv), c.s.b, c.s.n, at_of<float>(rope), c.rows, c.rot,
+                                  at_of<int>(positions), c.n_axes, bytes_of(axes), at_of(qw),
+                                  at_of(kw), c.weight_bf16, (float)eps, interleaved, at_of(dq),
+                                  at_of(dk), at_of(dv), at_of(dqkv), s.b, s.n, at_of<float>(dqw),
+                                  at_of<float>(dkw), at_of(workspace), size, c.B, c.N, c.H, c.Hkv,
+                                  c.d, stream);
     return g.norm_rope_bwd(at_of(qkv), c.s.b, c.s.n, at_of<float>(rope), c.rows, c.rot,
                            at_of<int>(positions), at_of(qw), at_of(kw), c.weight_bf16, (float)eps,
                            interleaved, at_of(dq), at_of(dk), at_of(dv), at_of(dqkv), s.b, s.n,
@@ -392,6 +424,8 @@ PYBIND11_MODULE(_fa_binding, m) {
     entry(from, "fa_qk_norm_rope", e.norm_rope);
     entry(from, "fa_qk_norm_rope_bwd", e.norm_rope_bwd);
     entry(from, "fa_qk_norm_rope_bwd_workspace_size", e.norm_rope_bwd_size);
+    entry(from, "fa_qk_norm_rope_axes", e.norm_rope_axes);
+    entry(from, "fa_qk_norm_rope_axes_bwd", e.norm_rope_axes_bwd);
     entry(from, "fa_cache4_plan", e.plan);
     entry(from, "fa_cache4_append", e.append);
     entry(from, "fa_cache4_attn", e.attn);

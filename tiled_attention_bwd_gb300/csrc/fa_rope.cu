@@ -10,6 +10,10 @@
 //   dw = sum over rows of dy * xh
 //   dx = r * (dy w - xh * mean(dy w xh)).
 //
+// Positions may have several axes (time, height, width, ...): each pair then
+// turns by its own axis's position, and its cosine and sine come from that
+// position's row of the table.
+//
 // A head's row of d bf16 values lies in d/16 lanes of 16 values each, so a
 // warp takes 32 / (d/16) heads of one token at a time ("pack"): 4 at d = 128,
 // 8 at d = 64.  The two 8-value chunks of a lane are chosen such that both
@@ -162,18 +166,48 @@ struct Ring {
   // (2, 3), of the pair's first or second four angles, or (interleaved) of
   // its first or second chunk's.
   template <bool kInter>
+  static __device__ __forceinline__ int first_angle(const Lane& l) {
+    return kInter ? 4 * (l.j + (l.sub & 1) * kLanes) : 8 * l.j + 4 * (l.sub & 1);
+  }
+  template <bool kInter>
   __device__ __forceinline__ void fetch_turn(int stage, const RopeArgs& a, const Lane& l,
                                              int pos) const {
     if (l.sub >= 4 || !(l.sub & 1 ? l.turn1 : l.turn0)) return;
     pos = pos < 0 ? 0 : (pos >= a.table_rows ? a.table_rows - 1 : pos);
-    const int first = kInter ? 4 * (l.j + (l.sub & 1) * kLanes) : 8 * l.j + 4 * (l.sub & 1);
-    const float* src = a.table + (size_t)pos * a.rot + first + (l.sub >> 1) * (a.rot / 2);
-    // (Through L1: the block's other warps are at the same token.)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(
-                     static_cast<uint32_t>(__cvta_generic_to_shared(
-                         base + stage * kStage + kRows * 1024 + (l.sub * kLanes + l.j) * 16))),
-                 "l"(src)
+    const float* src =
+        a.table + (size_t)pos * a.rot + first_angle<kInter>(l) + (l.sub >> 1) * (a.rot / 2);
+    copy_turn<16>(piece(stage, l), src);
+  }
+  // With axes: `pos` is that of axis (lane % 4), `axes` the axes of the lane's
+  // four angles, two bits each.  A piece of one axis is a copy of 16 bytes,
+  // else each angle one of 4 (`mixed`, of the warp: some piece is).
+  template <bool kInter>
+  __device__ __forceinline__ void fetch_turn(int stage, const RopeArgs& a, const Lane& l, int pos,
+                                             uint32_t axes, bool mixed) const {
+    pos = pos < 0 ? 0 : (pos >= a.table_rows ? a.table_rows - 1 : pos);
+    const bool turns = l.sub < 4 && (l.sub & 1 ? l.turn1 : l.turn0);
+    const float* src = a.table + first_angle<kInter>(l) + (l.sub >> 1) * (a.rot / 2);
+    if (mixed) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = __shfl_sync(0xffffffffu, pos, (axes >> (2 * i)) & 3);
+        if (turns) copy_turn<4>(piece(stage, l) + 4 * i, src + (size_t)at * a.rot + i);
+      }
+    } else {
+      const int at = __shfl_sync(0xffffffffu, pos, axes & 3);
+      if (turns) copy_turn<16>(piece(stage, l), src + (size_t)at * a.rot);
+    }
+  }
+  // (Through L1: the block's other warps are at the same token.)
+  template <int kBytes>
+  static __device__ __forceinline__ void copy_turn(uint8_t* dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "n"(kBytes)
                  : "memory");
+  }
+  __device__ __forceinline__ uint8_t* piece(int stage, const Lane& l) const {
+    return base + stage * kStage + kRows * 1024 + (l.sub * kLanes + l.j) * 16;
   }
   __device__ __forceinline__ void turn_of(int stage, const Lane& l, F2 (&cs)[4],
                                           F2 (&sn)[4]) const {
@@ -240,8 +274,21 @@ __device__ __forceinline__ void load_weight(const void* w, int is_bf16, const La
   for (int e = 0; e < 8; ++e) out[e] = f2(f[2 * e], f[2 * e + 1]);
 }
 
+// Of the lane's axis, with axes.
+template <bool kAxes>
 __device__ __forceinline__ int position_of(const RopeArgs& a, int token, int n) {
-  return a.positions ? a.positions[token] : n;
+  if constexpr (kAxes) {
+    const int axis = threadIdx.x & 3;
+    return a.positions[(size_t)(axis < a.n_axes ? axis : 0) * a.tokens + token];
+  } else {
+    return a.positions ? a.positions[token] : n;
+  }
+}
+// The axes of four angles, two bits each.
+__device__ __forceinline__ uint32_t axes_of(const RopeArgs& a, int first) {
+  const int w = first >> 4;
+  const uint32_t bits = w == 0 ? a.axes[0] : (w == 1 ? a.axes[1] : (w == 2 ? a.axes[2] : a.axes[3]));
+  return (bits >> (2 * (first & 15))) & 0xff;
 }
 
 // A warp's work: one pack of heads (query heads' packs first, then key heads',
@@ -303,7 +350,7 @@ template <int D>
 constexpr int bwd_smem() { return kWarps * kBwdStages * Ring<D, 2>::kStage; }
 
 // Forward: bound by bytes, each read and written once.
-template <int D, bool kInter, bool kNorm>
+template <int D, bool kInter, bool kNorm, bool kAxes>
 __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
   using R = Ring<D, 1>;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -318,6 +365,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
   const R ring = {smem + warp * kFwdStages * R::kStage};
   wait_for_stream();
   const bool turns = k.kind < 2;
+  const uint32_t axes = kAxes ? axes_of(a, R::template first_angle<kInter>(l)) : 0;
+  const bool mixed = kAxes && __any_sync(0xffffffffu, axes != (axes & 3) * 0x55);
   F2 w[8];
   if (kNorm && turns) load_weight(k.kind == 0 ? a.q_weight : a.k_weight, a.weight_bf16, l, w);
   Walk<const __nv_bfloat16> in(a.all, a.N, a.qkv + (size_t)k.column * D + l.c0, a.stride_b,
@@ -328,14 +377,17 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
 
   Place ahead = here;  // next to be fetched, with its position
   bool any = true;     // there is one
-  int pos = turns ? position_of(a, ahead.token, ahead.n) : 0;
+  int pos = turns ? position_of<kAxes>(a, ahead.token, ahead.n) : 0;
   auto fetch = [&](int stage) {
     if (any) {
       if (k.live) ring.fetch_row(stage, 0, in.at, l);
-      if (turns) ring.template fetch_turn<kInter>(stage, a, l, pos);
+      if (turns) {
+        if constexpr (kAxes) ring.template fetch_turn<kInter>(stage, a, l, pos, axes, mixed);
+        else ring.template fetch_turn<kInter>(stage, a, l, pos);
+      }
       any = a.tokens - ahead.token > a.all.step;
       in.advance(ahead.advance(a.all, a.N));
-      if (any && turns) pos = position_of(a, ahead.token, ahead.n);
+      if (any && turns) pos = position_of<kAxes>(a, ahead.token, ahead.n);
     }
     R::commit();
   };
@@ -373,7 +425,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
 // its 16 dims of its weight's gradient over all its rows; heads of a warp,
 // warps of a block (by kind) and blocks follow in that order, the last in
 // rope_dw_kernel: the result does not depend on which block runs first.
-template <int D, bool kInter, bool kNorm>
+template <int D, bool kInter, bool kNorm, bool kAxes>
 __global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeArgs a) {
   using R = Ring<D, 2>;
   constexpr int kPack = 512 / D;
@@ -384,6 +436,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeArgs a) {
   const int warp = threadIdx.x >> 5, id = blockIdx.x * kWarps + warp;
   const R ring = {smem + warp * kBwdStages * R::kStage};
   wait_for_stream();
+  const uint32_t axes = kAxes ? axes_of(a, R::template first_angle<kInter>(l)) : 0;
+  const bool mixed = kAxes && __any_sync(0xffffffffu, axes != (axes & 3) * 0x55);
   F2 dw[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) dw[e] = 0;
@@ -409,19 +463,22 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeArgs a) {
                             b, here.n);
     Place ahead = here;  // next to be fetched, with its position
     bool any = true;     // there is one
-    int pos = kGrad ? position_of(a, ahead.token, ahead.n) : 0;
+    int pos = kGrad ? position_of<kAxes>(a, ahead.token, ahead.n) : 0;
     auto fetch = [&](int stage) {
       if (any) {
         if (k.live) {
           ring.fetch_row(stage, 0, dz.at, l);
           if (kX) ring.fetch_row(stage, 1, in.at, l);
         }
-        if (kGrad) ring.template fetch_turn<kInter>(stage, a, l, pos);
+        if constexpr (kGrad && kAxes)
+          ring.template fetch_turn<kInter>(stage, a, l, pos, axes, mixed);
+        else if constexpr (kGrad)
+          ring.template fetch_turn<kInter>(stage, a, l, pos);
         any = a.tokens - ahead.token > s.step;
         const bool wrap = ahead.advance(s, a.N);
         dz.advance(wrap);
         if (kX) in.advance(wrap);
-        if (kGrad && any) pos = position_of(a, ahead.token, ahead.n);
+        if (kGrad && any) pos = position_of<kAxes>(a, ahead.token, ahead.n);
       }
       R::commit();
     };
@@ -536,19 +593,19 @@ int blocks_for(const RopeArgs& a, int packs, int sm_count, int resident) {
 template <int D>
 int packs_of(int heads) { return (heads + 512 / D - 1) / (512 / D); }
 
-template <int D, bool kInter, bool kNorm>
+template <int D, bool kInter, bool kNorm, bool kAxes>
 cudaError_t fwd(RopeArgs a, int sm_count, cudaStream_t stream) {
   const int packs = packs_of<D>(a.H) + 2 * packs_of<D>(a.Hkv);
   const int blocks = blocks_for(a, packs, sm_count, 3);
   a.all = deal(a, blocks, packs);
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(rope_fwd_kernel<D, kInter, kNorm>), fwd_smem<D>(), done);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(rope_fwd_kernel<D, kInter, kNorm, kAxes>), fwd_smem<D>(), done);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(rope_fwd_kernel<D, kInter, kNorm>, dim3(blocks), dim3(kWarps * 32),
+  return launch_overlapped(rope_fwd_kernel<D, kInter, kNorm, kAxes>, dim3(blocks), dim3(kWarps * 32),
                            fwd_smem<D>(), stream, a);
 }
 
-template <int D, bool kInter, bool kNorm>
+template <int D, bool kInter, bool kNorm, bool kAxes>
 cudaError_t bwd(RopeArgs a, int sm_count, cudaStream_t stream) {
   const int packs = packs_of<D>(a.H) + packs_of<D>(a.Hkv);
   const int blocks = blocks_for(a, packs, sm_count, 2);
@@ -556,20 +613,20 @@ cudaError_t bwd(RopeArgs a, int sm_count, cudaStream_t stream) {
   a.value = deal(a, blocks, packs_of<D>(a.Hkv));
   a.blocks = blocks;
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(rope_bwd_kernel<D, kInter, kNorm>), bwd_smem<D>(), done);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(rope_bwd_kernel<D, kInter, kNorm, kAxes>), bwd_smem<D>(), done);
   if (e != cudaSuccess) return e;
   if (blocks > 0)
-    e = launch_overlapped(rope_bwd_kernel<D, kInter, kNorm>, dim3(blocks), dim3(kWarps * 32),
+    e = launch_overlapped(rope_bwd_kernel<D, kInter, kNorm, kAxes>, dim3(blocks), dim3(kWarps * 32),
                           bwd_smem<D>(), stream, a);
   if (e != cudaSuccess || !kNorm) return e;
   return launch_overlapped(rope_dw_kernel<D>, dim3(2 * D / 32), dim3(32, 32), 0, stream, a);
 }
 
-template <bool kBwd>
+template <bool kBwd, bool kAxes>
 cudaError_t pick(const RopeArgs& a, int d, bool inter, bool norm, int sm_count,
                  cudaStream_t s) {
 #define FA_ROPE(DD, II, NN) \
-  return kBwd ? bwd<DD, II, NN>(a, sm_count, s) : fwd<DD, II, NN>(a, sm_count, s)
+  return kBwd ? bwd<DD, II, NN, kAxes>(a, sm_count, s) : fwd<DD, II, NN, kAxes>(a, sm_count, s)
   if (d == 128) {
     if (inter) { if (norm) FA_ROPE(128, true, true); else FA_ROPE(128, true, false); }
     else       { if (norm) FA_ROPE(128, false, true); else FA_ROPE(128, false, false); }
@@ -583,11 +640,13 @@ cudaError_t pick(const RopeArgs& a, int d, bool inter, bool norm, int sm_count,
 
 cudaError_t launch_rope_fwd(const RopeArgs& a, int d, bool interleaved, bool norm, int sm_count,
                             cudaStream_t stream) {
-  return pick<false>(a, d, interleaved, norm, sm_count, stream);
+  return a.n_axes ? pick<false, true>(a, d, interleaved, norm, sm_count, stream)
+                  : pick<false, false>(a, d, interleaved, norm, sm_count, stream);
 }
 cudaError_t launch_rope_bwd(const RopeArgs& a, int d, bool interleaved, bool norm, int sm_count,
                             cudaStream_t stream) {
-  return pick<true>(a, d, interleaved, norm, sm_count, stream);
+  return a.n_axes ? pick<true, true>(a, d, interleaved, norm, sm_count, stream)
+                  : pick<true, false>(a, d, interleaved, norm, sm_count, stream);
 }
 
 }  // namespace fa

@@ -25,7 +25,10 @@ struct RopeDeal {
 struct RopeArgs {
   const __nv_bfloat16* qkv;  // [B, N, H + 2 Hkv, d], strides below
   const float* table;        // [table_rows, rot]: rot/2 cosines, rot/2 sines
-  const int* positions;      // [B, N] or null (row n of an entry: n)
+  const int* positions;      // [B, N] or null (row n of an entry: n); with
+                             // axes [n_axes, B, N]
+  int n_axes;                // 0: positions have no axes
+  uint32_t axes[4];          // axis of each pair, two bits each
   const void* q_weight;      // [d], bf16 or fp32
   const void* k_weight;
   int weight_bf16;

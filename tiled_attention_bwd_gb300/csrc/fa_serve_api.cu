@@ -136,6 +136,24 @@ fa_status check_rope(int B, int N, int H, int Hkv, int d, int rot, int table_row
   return FA_OK;
 }
 
+// The axes of positions: none, or n of them with the axis of every pair.
+struct Axes {
+  int n = 0;
+  const uint8_t* of_pair = nullptr;
+  // Positions' memory.
+  long long bytes(int B, int N) const { return 4LL * B * N * (n > 0 ? n : 1); }
+};
+constexpr int kMaxAxes = 4;  // two bits a pair
+// (Behind check_rope: rot is in range.)
+fa_status check_axes(const Axes& x, int rot, const int* positions, bool empty) {
+  if (x.n < 1) return FA_ERR_INVALID_ARG;
+  if (x.n > kMaxAxes) return FA_ERR_UNSUPPORTED;
+  if (!x.of_pair || (!empty && !positions)) return FA_ERR_INVALID_ARG;
+  for (int i = 0; i < rot / 2; ++i)
+    if (x.of_pair[i] >= x.n) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
 // The tokens of a [B,N,H+2Hkv,d] tensor.
 Rows tokens(const void* p, long long stride_b, long long stride_n, int B, int N, int H, int Hkv,
             int d) {
@@ -144,8 +162,12 @@ Rows tokens(const void* p, long long stride_b, long long stride_n, int B, int N,
 
 fa::RopeArgs rope_args(const void* qkv, long long sb, long long sn, const float* table,
                        int table_rows, int rot, const int* positions, const void* qw,
-                       const void* kw, int weight_bf16, float eps, int B, int N, int H, int Hkv) {
+                       const void* kw, int weight_bf16, float eps, int B, int N, int H, int Hkv,
+                       const Axes& axes) {
   fa::RopeArgs a = {};
+  a.n_axes = axes.n;
+  for (int i = 0; axes.n > 0 && i < rot / 2; ++i)
+    a.axes[i / 16] |= (uint32_t)axes.of_pair[i] << (2 * (i % 16));
   a.qkv = static_cast<const __nv_bfloat16*>(qkv);
   a.table = table;
   a.positions = positions;
@@ -204,6 +226,113 @@ size_t page_bytes(const Format& f, int Hkv, int page_size, int d) {
 }
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+
+// Norm and rotation, with or without axes of positions.
+fa_status norm_rope(const void* qkv, long long stride_b, long long stride_n, const float* rope,
+                    int rope_rows, int rot, const int* positions, const Axes* axes,
+                    const void* q_weight, const void* k_weight, int weight_bf16, float eps,
+                    int interleaved, void* q, void* k, void* v, int B, int N, int H, int Hkv,
+                    int d, void* stream) {
+  fa_status s = check_rope(B, N, H, Hkv, d, rot, rope_rows, weight_bf16, eps, interleaved, q_weight,
+                           k_weight, rope, qkv, positions, stride_b, stride_n);
+  if (s != FA_OK) return s;
+  const bool empty = B == 0 || N == 0 || H + Hkv == 0;
+  if (axes && (s = check_axes(*axes, rot, positions, empty)) != FA_OK) return s;
+  if (empty) return FA_OK;
+  if ((H > 0 && !q) || (Hkv > 0 && (!k || !v)) || !aligned(q, 16) || !aligned(k, 16) ||
+      !aligned(v, 16))
+    return FA_ERR_INVALID_ARG;
+  const long long head = 2LL * B * N * d, weight = (weight_bf16 ? 2LL : 4LL) * d;
+  const Span qs = span(q, H * head), ks = span(k, Hkv * head), vs = span(v, Hkv * head);
+  if (meet({qs, ks, vs}, {span(rope, 4LL * rope_rows * rot), span(positions, (axes ? *axes : Axes()).bytes(B, N)),
+                          span(q_weight, weight), span(k_weight, weight)}))
+    return FA_ERR_INVALID_ARG;
+  const Rows in = tokens(qkv, stride_b, stride_n, B, N, H, Hkv, d);
+  if (in.meet(qs) || in.meet(ks) || in.meet(vs)) return FA_ERR_INVALID_ARG;
+  fa::DeviceInfo dev;
+  if ((s = fa::device_info(&dev)) != FA_OK) return s;
+  fa::RopeArgs a = rope_args(qkv, stride_b, stride_n, rope, rope_rows, rot, positions, q_weight,
+                             k_weight, weight_bf16, eps, B, N, H, Hkv,
+                             axes ? *axes : Axes());
+  a.q = static_cast<__nv_bfloat16*>(q);
+  a.k = static_cast<__nv_bfloat16*>(k);
+  a.v = static_cast<__nv_bfloat16*>(v);
+  return launched(fa::launch_rope_fwd(a, d, interleaved != 0, q_weight != nullptr, dev.sm_count,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+size_t rope_bwd_workspace(int d) {
+  return d == 64 || d == 128 ? (size_t)fa::kRopeMaxBlocks * 2 * d * sizeof(float) : 0;
+}
+
+fa_status norm_rope_bwd(const void* qkv, long long stride_b, long long stride_n, const float* rope,
+                        int rope_rows, int rot, const int* positions, const Axes* axes,
+                        const void* q_weight, const void* k_weight, int weight_bf16, float eps,
+                        int interleaved, const void* dq, const void* dk, const void* dv,
+                        void* dqkv, long long dstride_b, long long dstride_n, float* dq_weight,
+                        float* dk_weight, void* workspace, size_t workspace_bytes, int B, int N,
+                        int H, int Hkv, int d, void* stream) {
+  fa_status s = check_rope(B, N, H, Hkv, d, rot, rope_rows, weight_bf16, eps, interleaved, q_weight,
+                           k_weight, rope, qkv, positions, stride_b, stride_n);
+  if (s != FA_OK) return s;
+  const bool norm = q_weight != nullptr;
+  const bool empty = B == 0 || N == 0 || H + Hkv == 0;
+  if (axes && (s = check_axes(*axes, rot, positions, empty)) != FA_OK) return s;
+  if (norm) {
+    if (!dq_weight || !dk_weight || !aligned(dq_weight, 4) || !aligned(dk_weight, 4))
+      return FA_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 16) ||
+        workspace_bytes < rope_bwd_workspace(d))
+      return FA_ERR_WORKSPACE;
+  }
+  if (!empty) {
+    if ((H > 0 && !dq) || (Hkv > 0 && (!dk || !dv)) || !dqkv || !aligned(dq, 16) ||
+        !aligned(dk, 16) || !aligned(dv, 16) || !aligned(dqkv, 16))
+      return FA_ERR_INVALID_ARG;
+    if (dstride_b % 8 != 0 || dstride_n % 8 != 0) return FA_ERR_INVALID_ARG;
+  } else if (!norm) {
+    return FA_OK;
+  }
+  const long long head = 2LL * B * N * d, weight = (weight_bf16 ? 2LL : 4LL) * d;
+  const Span ins[] = {span(dq, H * head),
+                      span(dk, Hkv * head),
+                      span(dv, Hkv * head),
+                      span(empty ? nullptr : rope, 4LL * rope_rows * rot),
+                      span(empty ? nullptr : positions, (axes ? *axes : Axes()).bytes(B, N)),
+                      span(q_weight, weight),
+                      span(k_weight, weight)};
+  const Span sums[] = {span(norm ? dq_weight : nullptr, 4LL * d),
+                       span(norm ? dk_weight : nullptr, 4LL * d),
+                       span(norm ? workspace : nullptr, rope_bwd_workspace(d))};
+  if (meet(sums, sums + 3, ins, ins + 7)) return FA_ERR_INVALID_ARG;
+  if (!empty) {
+    const Rows x = tokens(qkv, stride_b, stride_n, B, N, H, Hkv, d);
+    const Rows out = tokens(dqkv, dstride_b, dstride_n, B, N, H, Hkv, d);
+    // (Without weights qkv is not read.)
+    if (out.meet() || (norm && meet(out, x, true))) return FA_ERR_INVALID_ARG;
+    for (const Span& i : ins)
+      if (out.meet(i)) return FA_ERR_INVALID_ARG;
+    for (const Span& i : sums)
+      if (out.meet(i) || x.meet(i)) return FA_ERR_INVALID_ARG;
+  }
+  fa::DeviceInfo dev;
+  if ((s = fa::device_info(&dev)) != FA_OK) return s;
+  // Without tokens the weights' gradients are zero: the kernels write that.
+  fa::RopeArgs a = rope_args(qkv, stride_b, stride_n, rope, rope_rows, rot, positions, q_weight,
+                             k_weight, weight_bf16, eps, B, N, H, Hkv,
+                             axes ? *axes : Axes());
+  a.dq = static_cast<const __nv_bfloat16*>(dq);
+  a.dk = static_cast<const __nv_bfloat16*>(dk);
+  a.dv = static_cast<const __nv_bfloat16*>(dv);
+  a.dqkv = static_cast<__nv_bfloat16*>(dqkv);
+  a.dstride_b = dstride_b;
+  a.dstride_n = dstride_n;
+  a.dq_weight = dq_weight;
+  a.dk_weight = dk_weight;
+  a.partial = static_cast<float*>(workspace);
+  return launched(fa::launch_rope_bwd(a, d, interleaved != 0, norm, dev.sm_count,
+                                      static_cast<cudaStream_t>(stream)));
+}
 
 // Attention over a cache in either format.
 size_t attn_workspace_size(const Format& f, int B, int H, int Hkv, int T, int d) {
@@ -312,34 +441,22 @@ fa_status fa_qk_norm_rope(const void* qkv, long long stride_b, long long stride_
                           const void* q_weight, const void* k_weight, int weight_bf16, float eps,
                           int interleaved, void* q, void* k, void* v, int B, int N, int H, int Hkv,
                           int d, void* stream) {
-  fa_status s = check_rope(B, N, H, Hkv, d, rot, rope_rows, weight_bf16, eps, interleaved, q_weight,
-                           k_weight, rope, qkv, positions, stride_b, stride_n);
-  if (s != FA_OK) return s;
-  if (B == 0 || N == 0 || H + Hkv == 0) return FA_OK;
-  if ((H > 0 && !q) || (Hkv > 0 && (!k || !v)) || !aligned(q, 16) || !aligned(k, 16) ||
-      !aligned(v, 16))
-    return FA_ERR_INVALID_ARG;
-  const long long head = 2LL * B * N * d, weight = (weight_bf16 ? 2LL : 4LL) * d;
-  const Span qs = span(q, H * head), ks = span(k, Hkv * head), vs = span(v, Hkv * head);
-  if (meet({qs, ks, vs}, {span(rope, 4LL * rope_rows * rot), span(positions, 4LL * B * N),
-                          span(q_weight, weight), span(k_weight, weight)}))
-    return FA_ERR_INVALID_ARG;
-  const Rows in = tokens(qkv, stride_b, stride_n, B, N, H, Hkv, d);
-  if (in.meet(qs) || in.meet(ks) || in.meet(vs)) return FA_ERR_INVALID_ARG;
-  fa::DeviceInfo dev;
-  if ((s = fa::device_info(&dev)) != FA_OK) return s;
-  fa::RopeArgs a = rope_args(qkv, stride_b, stride_n, rope, rope_rows, rot, positions, q_weight,
-                             k_weight, weight_bf16, eps, B, N, H, Hkv);
-  a.q = static_cast<__nv_bfloat16*>(q);
-  a.k = static_cast<__nv_bfloat16*>(k);
-  a.v = static_cast<__nv_bfloat16*>(v);
-  return launched(fa::launch_rope_fwd(a, d, interleaved != 0, q_weight != nullptr, dev.sm_count,
-                                      static_cast<cudaStream_t>(stream)));
+  return norm_rope(qkv, stride_b, stride_n, rope, rope_rows, rot, positions, nullptr, q_weight,
+                   k_weight, weight_bf16, eps, interleaved, q, k, v, B, N, H, Hkv, d, stream);
 }
 
-size_t fa_qk_norm_rope_bwd_workspace_size(int d) {
-  return d == 64 || d == 128 ? (size_t)fa::kRopeMaxBlocks * 2 * d * sizeof(float) : 0;
+fa_status fa_qk_norm_rope_axes(const void* qkv, long long stride_b, long long stride_n,
+                               const float* rope, int rope_rows, int rot, const int* positions,
+                               int n_axes, const uint8_t* axes, const void* q_weight,
+                               const void* k_weight, int weight_bf16, float eps, int interleaved,
+                               void* q, void* k, void* v, int B, int N, int H, int Hkv, int d,
+                               void* stream) {
+  const Axes x = {n_axes, axes};
+  return norm_rope(qkv, stride_b, stride_n, rope, rope_rows, rot, positions, &x, q_weight, k_weight,
+                   weight_bf16, eps, interleaved, q, k, v, B, N, H, Hkv, d, stream);
 }
+
+size_t fa_qk_norm_rope_bwd_workspace_size(int d) { return rope_bwd_workspace(d); }
 
 fa_status fa_qk_norm_rope_bwd(const void* qkv, long long stride_b, long long stride_n,
                               const float* rope, int rope_rows, int rot, const int* positions,
@@ -349,64 +466,26 @@ fa_status fa_qk_norm_rope_bwd(const void* qkv, long long stride_b, long long str
                               float* dq_weight, float* dk_weight, void* workspace,
                               size_t workspace_bytes, int B, int N, int H, int Hkv, int d,
                               void* stream) {
-  fa_status s = check_rope(B, N, H, Hkv, d, rot, rope_rows, weight_bf16, eps, interleaved, q_weight,
-                           k_weight, rope, qkv, positions, stride_b, stride_n);
-  if (s != FA_OK) return s;
-  const bool norm = q_weight != nullptr;
-  const bool empty = B == 0 || N == 0 || H + Hkv == 0;
-  if (norm) {
-    if (!dq_weight || !dk_weight || !aligned(dq_weight, 4) || !aligned(dk_weight, 4))
-      return FA_ERR_INVALID_ARG;
-    if (!workspace || !aligned(workspace, 16) ||
-        workspace_bytes < fa_qk_norm_rope_bwd_workspace_size(d))
-      return FA_ERR_WORKSPACE;
-  }
-  if (!empty) {
-    if ((H > 0 && !dq) || (Hkv > 0 && (!dk || !dv)) || !dqkv || !aligned(dq, 16) ||
-        !aligned(dk, 16) || !aligned(dv, 16) || !aligned(dqkv, 16))
-      return FA_ERR_INVALID_ARG;
-    if (dstride_b % 8 != 0 || dstride_n % 8 != 0) return FA_ERR_INVALID_ARG;
-  } else if (!norm) {
-    return FA_OK;
-  }
-  const long long head = 2LL * B * N * d, weight = (weight_bf16 ? 2LL : 4LL) * d;
-  const Span ins[] = {span(dq, H * head),
-                      span(dk, Hkv * head),
-                      span(dv, Hkv * head),
-                      span(empty ? nullptr : rope, 4LL * rope_rows * rot),
-                      span(empty ? nullptr : positions, 4LL * B * N),
-                      span(q_weight, weight),
-                      span(k_weight, weight)};
-  const Span sums[] = {span(norm ? dq_weight : nullptr, 4LL * d),
-                       span(norm ? dk_weight : nullptr, 4LL * d),
-                       span(norm ? workspace : nullptr, fa_qk_norm_rope_bwd_workspace_size(d))};
-  if (meet(sums, sums + 3, ins, ins + 7)) return FA_ERR_INVALID_ARG;
-  if (!empty) {
-    const Rows x = tokens(qkv, stride_b, stride_n, B, N, H, Hkv, d);
-    const Rows out = tokens(dqkv, dstride_b, dstride_n, B, N, H, Hkv, d);
-    // (Without weights qkv is not read.)
-    if (out.meet() || (norm && meet(out, x, true))) return FA_ERR_INVALID_ARG;
-    for (const Span& i : ins)
-      if (out.meet(i)) return FA_ERR_INVALID_ARG;
-    for (const Span& i : sums)
-      if (out.meet(i) || x.meet(i)) return FA_ERR_INVALID_ARG;
-  }
-  fa::DeviceInfo dev;
-  if ((s = fa::device_info(&dev)) != FA_OK) return s;
-  // Without tokens the weights' gradients are zero: the kernels write that.
-  fa::RopeArgs a = rope_args(qkv, stride_b, stride_n, rope, rope_rows, rot, positions, q_weight,
-                             k_weight, weight_bf16, eps, B, N, H, Hkv);
-  a.dq = static_cast<const __nv_bfloat16*>(dq);
-  a.dk = static_cast<const __nv_bfloat16*>(dk);
-  a.dv = static_cast<const __nv_bfloat16*>(dv);
-  a.dqkv = static_cast<__nv_bfloat16*>(dqkv);
-  a.dstride_b = dstride_b;
-  a.dstride_n = dstride_n;
-  a.dq_weight = dq_weight;
-  a.dk_weight = dk_weight;
-  a.partial = static_cast<float*>(workspace);
-  return launched(fa::launch_rope_bwd(a, d, interleaved != 0, norm, dev.sm_count,
-                                      static_cast<cudaStream_t>(stream)));
+  return norm_rope_bwd(qkv, stride_b, stride_n, rope, rope_rows, rot, positions, nullptr, q_weight,
+                       k_weight, weight_bf16, eps, interleaved, dq, dk, dv, dqkv, dstride_b,
+                       dstride_n, dq_weight, dk_weight, workspace, workspace_bytes, B, N, H, Hkv, d,
+                       stream);
+}
+
+fa_status fa_qk_norm_rope_axes_bwd(const void* qkv, long long stride_b, long long stride_n,
+                                   const float* rope, int rope_rows, int rot, const int* positions,
+                                   int n_axes, const uint8_t* axes, const void* q_weight,
+                                   const void* k_weight, int weight_bf16, float eps,
+                                   int interleaved, const void* dq, const void* dk, const void* dv,
+                                   void* dqkv, long long dstride_b, long long dstride_n,
+                                   float* dq_weight, float* dk_weight, void* workspace,
+                                   size_t workspace_bytes, int B, int N, int H, int Hkv, int d,
+                                   void* stream) {
+  const Axes x = {n_axes, axes};
+  return norm_rope_bwd(qkv, stride_b, stride_n, rope, rope_rows, rot, positions, &x, q_weight,
+                       k_weight, weight_bf16, eps, interleaved, dq, dk, dv, dqkv, dstride_b,
+                       dstride_n, dq_weight, dk_weight, workspace, workspace_bytes, B, N, H, Hkv, d,
+                       stream);
 }
 
 size_t fa_cache4_page_bytes(int Hkv, int page_size, int d) {

@@ -9,7 +9,8 @@ Names mirror the C ABI: ``fa_fwd``, ``fa_bwd``, ``fa_bwd_workspace_size``,
 ``fa_check_device_status``, ``fa_set_wait_timeout_ns``,
 ``fa_debug_expire_wait``, ``fa_debug_expire_at``, ``fa_last_failure_site``,
 ``fa_bwd_set_phase_events``, ``fa_status_string``; ``fa_qk_norm_rope``,
-``fa_qk_norm_rope_bwd``, ``fa_cache4_plan``, ``fa_cache4_append``,
+``fa_qk_norm_rope_bwd``, ``fa_qk_norm_rope_axes``,
+``fa_qk_norm_rope_axes_bwd``, ``fa_cache4_plan``, ``fa_cache4_append``,
 ``fa_cache4_attn``; ``fa_cache8_append``, ``fa_cache8_read``,
 ``fa_cache8_attn``.
 """
@@ -119,6 +120,15 @@ def open_library(path: str):
                                         i, vp, vp, vp, vp, ll, ll, vp, vp, vp,
                                         sz, i, i, i, i, i, vp]
     lib.fa_qk_norm_rope_bwd.restype = i
+    lib.fa_qk_norm_rope_axes.argtypes = [vp, ll, ll, vp, i, i, vp, i, vp, vp,
+                                         vp, i, f, i, vp, vp, vp, i, i, i, i,
+                                         i, vp]
+    lib.fa_qk_norm_rope_axes.restype = i
+    lib.fa_qk_norm_rope_axes_bwd.argtypes = [vp, ll, ll, vp, i, i, vp, i, vp,
+                                             vp, vp, i, f, i, vp, vp, vp, vp,
+                                             ll, ll, vp, vp, vp, sz, i, i, i,
+                                             i, i, vp]
+    lib.fa_qk_norm_rope_axes_bwd.restype = i
     lib.fa_cache4_page_bytes.argtypes = [i, i, i]
     lib.fa_cache4_page_bytes.restype = sz
     lib.fa_cache4_plan.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i,
@@ -539,6 +549,7 @@ def fa_bwd_noalloc(q, k, v, o, lse, dout, causal: bool, scale: float, dq,
 
 _native_module = None
 _NATIVE = ("fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
+           "fa_qk_norm_rope_axes", "fa_qk_norm_rope_axes_bwd",
            "fa_qk_norm_rope_bwd_workspace_size", "fa_cache4_plan",
            "fa_cache4_append", "fa_cache4_attn",
            "fa_cache4_attn_workspace_size", "fa_cache8_append",
@@ -582,7 +593,7 @@ def fa_qk_norm_rope(qkv, H: int, Hkv: int, rope, positions=None, q_weight=None,
     q_weight, k_weight: [d], bf16 or fp32, or None for no norm.
     Returns (q [B,H,N,d], k [B,Hkv,N,d], v [B,Hkv,N,d])."""
     status, q, k, v = _native().qk_norm_rope(
-        qkv, H, Hkv, rope, positions, q_weight, k_weight, eps,
+        qkv, H, Hkv, rope, positions, None, q_weight, k_weight, eps,
         bool(interleaved), q, k, v)
     if status:
         raise FAError("fa_qk_norm_rope", status)
@@ -601,10 +612,42 @@ def fa_qk_norm_rope_bwd(qkv, H: int, Hkv: int, rope, dq, dk, dv,
     dq_weight, dk_weight fp32 [d]; None without weights).  dqkv may be
     qkv."""
     status, dqkv, dqw, dkw = _native().qk_norm_rope_bwd(
-        qkv, H, Hkv, rope, dq, dk, dv, positions, q_weight, k_weight, eps,
-        bool(interleaved), dqkv, workspace)
+        qkv, H, Hkv, rope, dq, dk, dv, positions, None, q_weight, k_weight,
+        eps, bool(interleaved), dqkv, workspace)
     if status:
         raise FAError("fa_qk_norm_rope_bwd", status)
+    return dqkv, dqw, dkw
+
+
+def fa_qk_norm_rope_axes(qkv, H: int, Hkv: int, rope, positions, axes,
+                         q_weight=None, k_weight=None, eps: float = 1e-6,
+                         interleaved: bool = False, q=None, k=None, v=None):
+    """fa_qk_norm_rope with positions of several axes (time, height, width).
+
+    positions: int32 [A,B,N], A of 1 to 4; axes: the axis of each of the
+    rot/2 rotated pairs, as bytes or any sequence of whole numbers (bytes cost
+    the call nothing).  Pair i of a token turns by angle i of the rope's row
+    positions[axes[i], b, n].  Returns (q, k, v)."""
+    status, q, k, v = _native().qk_norm_rope(
+        qkv, H, Hkv, rope, positions, bytes(axes), q_weight, k_weight, eps,
+        bool(interleaved), q, k, v)
+    if status:
+        raise FAError("fa_qk_norm_rope_axes", status)
+    return q, k, v
+
+
+def fa_qk_norm_rope_axes_bwd(qkv, H: int, Hkv: int, rope, dq, dk, dv,
+                             positions, axes, q_weight=None, k_weight=None,
+                             eps: float = 1e-6, interleaved: bool = False,
+                             dqkv=None, workspace=None):
+    """Backward of fa_qk_norm_rope_axes.  Returns (dqkv [B,N,H+2*Hkv,d] bf16,
+    dq_weight, dk_weight fp32 [d]; None without weights).  dqkv may be
+    qkv."""
+    status, dqkv, dqw, dkw = _native().qk_norm_rope_bwd(
+        qkv, H, Hkv, rope, dq, dk, dv, positions, bytes(axes), q_weight,
+        k_weight, eps, bool(interleaved), dqkv, workspace)
+    if status:
+        raise FAError("fa_qk_norm_rope_axes_bwd", status)
     return dqkv, dqw, dkw
 
 
