@@ -131,6 +131,32 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* at, const Lane& a, cons
   *reinterpret_cast<uint4*>(at + (a.c1 - a.c0)) = r.c[1];
 }
 
+// How positions and their axes are taken: none; a lane's four angles are of
+// one axis, whose position it holds; or of several, and the lanes hold the
+// positions of axis (lane % 4) for one another.  (One kernel for the last two,
+// with a branch, spills: 106 us for 102 at 3 x 5001 tokens, the backward of
+// 4 x 1024 56 for 52.)
+enum Turning { kPlain, kSections, kMixed };
+template <Turning kTurn>
+struct LaneAxes {
+  int axis;       // whose position the lane holds
+  uint32_t four;  // axes of its angles, two bits each
+  __device__ __forceinline__ LaneAxes(const RopeArgs& a, int first) {
+    if constexpr (kTurn != kPlain) {
+      const int w = first >> 4;
+      const uint32_t bits =
+          w == 0 ? a.axes[0] : (w == 1 ? a.axes[1] : (w == 2 ? a.axes[2] : a.axes[3]));
+      four = (bits >> (2 * (first & 15))) & 0xff;
+      axis = kTurn == kMixed ? threadIdx.x & 3 : four & 3;
+      if (axis >= a.n_axes) axis = 0;
+    }
+  }
+  __device__ __forceinline__ int position(const RopeArgs& a, int token, int n) const {
+    if constexpr (kTurn != kPlain) return a.positions[(size_t)axis * a.tokens + token];
+    else return a.positions ? a.positions[token] : n;
+  }
+};
+
 // ---- A warp's ring of rows on their way from memory, in shared memory: the
 // loads in flight then cost no registers.  A lane copies its own two chunks
 // of each of kRows rows and reads them back itself; the rotation's row of
@@ -169,33 +195,24 @@ struct Ring {
   static __device__ __forceinline__ int first_angle(const Lane& l) {
     return kInter ? 4 * (l.j + (l.sub & 1) * kLanes) : 8 * l.j + 4 * (l.sub & 1);
   }
-  template <bool kInter>
+  template <bool kInter, Turning kTurn>
   __device__ __forceinline__ void fetch_turn(int stage, const RopeArgs& a, const Lane& l,
-                                             int pos) const {
-    if (l.sub >= 4 || !(l.sub & 1 ? l.turn1 : l.turn0)) return;
-    pos = pos < 0 ? 0 : (pos >= a.table_rows ? a.table_rows - 1 : pos);
-    const float* src =
-        a.table + (size_t)pos * a.rot + first_angle<kInter>(l) + (l.sub >> 1) * (a.rot / 2);
-    copy_turn<16>(piece(stage, l), src);
-  }
-  // With axes: `pos` is that of axis (lane % 4), `axes` the axes of the lane's
-  // four angles, two bits each.  A piece of one axis is a copy of 16 bytes,
-  // else each angle one of 4 (`mixed`, of the warp: some piece is).
-  template <bool kInter>
-  __device__ __forceinline__ void fetch_turn(int stage, const RopeArgs& a, const Lane& l, int pos,
-                                             uint32_t axes, bool mixed) const {
-    pos = pos < 0 ? 0 : (pos >= a.table_rows ? a.table_rows - 1 : pos);
-    const bool turns = l.sub < 4 && (l.sub & 1 ? l.turn1 : l.turn0);
-    const float* src = a.table + first_angle<kInter>(l) + (l.sub >> 1) * (a.rot / 2);
-    if (mixed) {
+                                             const LaneAxes<kTurn>& axes, int pos) const {
+    if constexpr (kTurn != kMixed) {
+      if (l.sub >= 4 || !(l.sub & 1 ? l.turn1 : l.turn0)) return;
+      pos = pos < 0 ? 0 : (pos >= a.table_rows ? a.table_rows - 1 : pos);
+      const int first = first_angle<kInter>(l);
+      const float* src = a.table + (size_t)pos * a.rot + first + (l.sub >> 1) * (a.rot / 2);
+      copy_turn<16>(piece(stage, l), src);
+    } else {
+      const bool turns = l.sub < 4 && (l.sub & 1 ? l.turn1 : l.turn0);
+      pos = pos < 0 ? 0 : (pos >= a.table_rows ? a.table_rows - 1 : pos);
+      const int first = first_angle<kInter>(l) + (l.sub >> 1) * (a.rot / 2);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int at = __shfl_sync(0xffffffffu, pos, (axes >> (2 * i)) & 3);
-        if (turns) copy_turn<4>(piece(stage, l) + 4 * i, src + (size_t)at * a.rot + i);
+        const int at = __shfl_sync(0xffffffffu, pos, (axes.four >> (2 * i)) & 3);
+        if (turns) copy_turn<4>(piece(stage, l) + 4 * i, a.table + (size_t)at * a.rot + first + i);
       }
-    } else {
-      const int at = __shfl_sync(0xffffffffu, pos, axes & 3);
-      if (turns) copy_turn<16>(piece(stage, l), src + (size_t)at * a.rot);
     }
   }
   // (Through L1: the block's other warps are at the same token.)
@@ -274,23 +291,6 @@ __device__ __forceinline__ void load_weight(const void* w, int is_bf16, const La
   for (int e = 0; e < 8; ++e) out[e] = f2(f[2 * e], f[2 * e + 1]);
 }
 
-// Of the lane's axis, with axes.
-template <bool kAxes>
-__device__ __forceinline__ int position_of(const RopeArgs& a, int token, int n) {
-  if constexpr (kAxes) {
-    const int axis = threadIdx.x & 3;
-    return a.positions[(size_t)(axis < a.n_axes ? axis : 0) * a.tokens + token];
-  } else {
-    return a.positions ? a.positions[token] : n;
-  }
-}
-// The axes of four angles, two bits each.
-__device__ __forceinline__ uint32_t axes_of(const RopeArgs& a, int first) {
-  const int w = first >> 4;
-  const uint32_t bits = w == 0 ? a.axes[0] : (w == 1 ? a.axes[1] : (w == 2 ? a.axes[2] : a.axes[3]));
-  return (bits >> (2 * (first & 15))) & 0xff;
-}
-
 // A warp's work: one pack of heads (query heads' packs first, then key heads',
 // then value heads'; a pack never mixes kinds) of the tokens `first`, `first`
 // + step, ... .  With the pack fixed, its weights (and in the backward their
@@ -350,7 +350,7 @@ template <int D>
 constexpr int bwd_smem() { return kWarps * kBwdStages * Ring<D, 2>::kStage; }
 
 // Forward: bound by bytes, each read and written once.
-template <int D, bool kInter, bool kNorm, bool kAxes>
+template <int D, bool kInter, bool kNorm, Turning kTurn>
 __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
   using R = Ring<D, 1>;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -365,8 +365,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
   const R ring = {smem + warp * kFwdStages * R::kStage};
   wait_for_stream();
   const bool turns = k.kind < 2;
-  const uint32_t axes = kAxes ? axes_of(a, R::template first_angle<kInter>(l)) : 0;
-  const bool mixed = kAxes && __any_sync(0xffffffffu, axes != (axes & 3) * 0x55);
+  const LaneAxes<kTurn> axes(a, R::template first_angle<kInter>(l));
   F2 w[8];
   if (kNorm && turns) load_weight(k.kind == 0 ? a.q_weight : a.k_weight, a.weight_bf16, l, w);
   Walk<const __nv_bfloat16> in(a.all, a.N, a.qkv + (size_t)k.column * D + l.c0, a.stride_b,
@@ -377,17 +376,14 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
 
   Place ahead = here;  // next to be fetched, with its position
   bool any = true;     // there is one
-  int pos = turns ? position_of<kAxes>(a, ahead.token, ahead.n) : 0;
+  int pos = turns ? axes.position(a, ahead.token, ahead.n) : 0;
   auto fetch = [&](int stage) {
     if (any) {
       if (k.live) ring.fetch_row(stage, 0, in.at, l);
-      if (turns) {
-        if constexpr (kAxes) ring.template fetch_turn<kInter>(stage, a, l, pos, axes, mixed);
-        else ring.template fetch_turn<kInter>(stage, a, l, pos);
-      }
+      if (turns) ring.template fetch_turn<kInter>(stage, a, l, axes, pos);
       any = a.tokens - ahead.token > a.all.step;
       in.advance(ahead.advance(a.all, a.N));
-      if (any && turns) pos = position_of<kAxes>(a, ahead.token, ahead.n);
+      if (any && turns) pos = axes.position(a, ahead.token, ahead.n);
     }
     R::commit();
   };
@@ -425,7 +421,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
 // its 16 dims of its weight's gradient over all its rows; heads of a warp,
 // warps of a block (by kind) and blocks follow in that order, the last in
 // rope_dw_kernel: the result does not depend on which block runs first.
-template <int D, bool kInter, bool kNorm, bool kAxes>
+template <int D, bool kInter, bool kNorm, Turning kTurn>
 __global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeArgs a) {
   using R = Ring<D, 2>;
   constexpr int kPack = 512 / D;
@@ -436,8 +432,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeArgs a) {
   const int warp = threadIdx.x >> 5, id = blockIdx.x * kWarps + warp;
   const R ring = {smem + warp * kBwdStages * R::kStage};
   wait_for_stream();
-  const uint32_t axes = kAxes ? axes_of(a, R::template first_angle<kInter>(l)) : 0;
-  const bool mixed = kAxes && __any_sync(0xffffffffu, axes != (axes & 3) * 0x55);
+  const LaneAxes<kTurn> axes(a, R::template first_angle<kInter>(l));
   F2 dw[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) dw[e] = 0;
@@ -463,22 +458,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeArgs a) {
                             b, here.n);
     Place ahead = here;  // next to be fetched, with its position
     bool any = true;     // there is one
-    int pos = kGrad ? position_of<kAxes>(a, ahead.token, ahead.n) : 0;
+    int pos = kGrad ? axes.position(a, ahead.token, ahead.n) : 0;
     auto fetch = [&](int stage) {
       if (any) {
         if (k.live) {
           ring.fetch_row(stage, 0, dz.at, l);
           if (kX) ring.fetch_row(stage, 1, in.at, l);
         }
-        if constexpr (kGrad && kAxes)
-          ring.template fetch_turn<kInter>(stage, a, l, pos, axes, mixed);
-        else if constexpr (kGrad)
-          ring.template fetch_turn<kInter>(stage, a, l, pos);
+        if (kGrad) ring.template fetch_turn<kInter>(stage, a, l, axes, pos);
         any = a.tokens - ahead.token > s.step;
         const bool wrap = ahead.advance(s, a.N);
         dz.advance(wrap);
         if (kX) in.advance(wrap);
-        if (kGrad && any) pos = position_of<kAxes>(a, ahead.token, ahead.n);
+        if (kGrad && any) pos = axes.position(a, ahead.token, ahead.n);
       }
       R::commit();
     };
@@ -593,19 +585,19 @@ int blocks_for(const RopeArgs& a, int packs, int sm_count, int resident) {
 template <int D>
 int packs_of(int heads) { return (heads + 512 / D - 1) / (512 / D); }
 
-template <int D, bool kInter, bool kNorm, bool kAxes>
+template <int D, bool kInter, bool kNorm, Turning kTurn>
 cudaError_t fwd(RopeArgs a, int sm_count, cudaStream_t stream) {
   const int packs = packs_of<D>(a.H) + 2 * packs_of<D>(a.Hkv);
   const int blocks = blocks_for(a, packs, sm_count, 3);
   a.all = deal(a, blocks, packs);
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(rope_fwd_kernel<D, kInter, kNorm, kAxes>), fwd_smem<D>(), done);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(rope_fwd_kernel<D, kInter, kNorm, kTurn>), fwd_smem<D>(), done);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(rope_fwd_kernel<D, kInter, kNorm, kAxes>, dim3(blocks), dim3(kWarps * 32),
+  return launch_overlapped(rope_fwd_kernel<D, kInter, kNorm, kTurn>, dim3(blocks), dim3(kWarps * 32),
                            fwd_smem<D>(), stream, a);
 }
 
-template <int D, bool kInter, bool kNorm, bool kAxes>
+template <int D, bool kInter, bool kNorm, Turning kTurn>
 cudaError_t bwd(RopeArgs a, int sm_count, cudaStream_t stream) {
   const int packs = packs_of<D>(a.H) + packs_of<D>(a.Hkv);
   const int blocks = blocks_for(a, packs, sm_count, 2);
@@ -613,20 +605,20 @@ cudaError_t bwd(RopeArgs a, int sm_count, cudaStream_t stream) {
   a.value = deal(a, blocks, packs_of<D>(a.Hkv));
   a.blocks = blocks;
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(rope_bwd_kernel<D, kInter, kNorm, kAxes>), bwd_smem<D>(), done);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(rope_bwd_kernel<D, kInter, kNorm, kTurn>), bwd_smem<D>(), done);
   if (e != cudaSuccess) return e;
   if (blocks > 0)
-    e = launch_overlapped(rope_bwd_kernel<D, kInter, kNorm, kAxes>, dim3(blocks), dim3(kWarps * 32),
+    e = launch_overlapped(rope_bwd_kernel<D, kInter, kNorm, kTurn>, dim3(blocks), dim3(kWarps * 32),
                           bwd_smem<D>(), stream, a);
   if (e != cudaSuccess || !kNorm) return e;
   return launch_overlapped(rope_dw_kernel<D>, dim3(2 * D / 32), dim3(32, 32), 0, stream, a);
 }
 
-template <bool kBwd, bool kAxes>
+template <bool kBwd, Turning kTurn>
 cudaError_t pick(const RopeArgs& a, int d, bool inter, bool norm, int sm_count,
                  cudaStream_t s) {
 #define FA_ROPE(DD, II, NN) \
-  return kBwd ? bwd<DD, II, NN, kAxes>(a, sm_count, s) : fwd<DD, II, NN, kAxes>(a, sm_count, s)
+  return kBwd ? bwd<DD, II, NN, kTurn>(a, sm_count, s) : fwd<DD, II, NN, kTurn>(a, sm_count, s)
   if (d == 128) {
     if (inter) { if (norm) FA_ROPE(128, true, true); else FA_ROPE(128, true, false); }
     else       { if (norm) FA_ROPE(128, false, true); else FA_ROPE(128, false, false); }
@@ -636,17 +628,26 @@ cudaError_t pick(const RopeArgs& a, int d, bool inter, bool norm, int sm_count,
 #undef FA_ROPE
 }
 
+template <bool kBwd>
+cudaError_t pick(const RopeArgs& a, int d, bool inter, bool norm, int sm_count, cudaStream_t s) {
+  if (a.n_axes == 0) return pick<kBwd, kPlain>(a, d, inter, norm, sm_count, s);
+  // A lane's four angles are neighbours from a multiple of four on.
+  bool mixed = false;
+  for (int i = 0; i < a.rot / 2; ++i)
+    mixed |= ((a.axes[i / 16] >> (2 * (i % 16))) & 3) != ((a.axes[i / 16] >> (2 * (i % 16 & ~3))) & 3);
+  return mixed ? pick<kBwd, kMixed>(a, d, inter, norm, sm_count, s)
+               : pick<kBwd, kSections>(a, d, inter, norm, sm_count, s);
+}
+
 }  // namespace
 
 cudaError_t launch_rope_fwd(const RopeArgs& a, int d, bool interleaved, bool norm, int sm_count,
                             cudaStream_t stream) {
-  return a.n_axes ? pick<false, true>(a, d, interleaved, norm, sm_count, stream)
-                  : pick<false, false>(a, d, interleaved, norm, sm_count, stream);
+  return pick<false>(a, d, interleaved, norm, sm_count, stream);
 }
 cudaError_t launch_rope_bwd(const RopeArgs& a, int d, bool interleaved, bool norm, int sm_count,
                             cudaStream_t stream) {
-  return a.n_axes ? pick<true, true>(a, d, interleaved, norm, sm_count, stream)
-                  : pick<true, false>(a, d, interleaved, norm, sm_count, stream);
+  return pick<true>(a, d, interleaved, norm, sm_count, stream);
 }
 
 }  // namespace fa
