@@ -95,16 +95,136 @@ __device__ __forceinline__ int exponent_for(uint32_t amax) {
   return min(max(e, -kExp8), kExp8);
 }
 
+// A group's exponent: `big` is the lane's largest magnitude among the new
+// tokens, `old` the exponent's byte, `fresh` whether the group begins.
+struct Exponent {
+  int e;
+  bool grown;     // the other tokens' codes are of a smaller one,
+  uint32_t down;  // by this factor (an f16 pair)
+  float unit, inv;  // 2^e, 2^-e
+  __device__ __forceinline__ Exponent(uint32_t big, uint32_t old, bool fresh) {
+    e = exponent_for(__reduce_max_sync(0xffffffffu, big));
+    const int was = exp8(old);
+    if (!fresh) e = max(e, was);
+    grown = !fresh && e > was;
+    down = factor_of(e - was);
+    unit = pow2(e), inv = pow2(-e);
+  }
+};
+
 // ----------------------------------------------------------------- append
-// A warp takes 16 neighbouring tokens of one batch entry and head and, one
-// after the other, the groups whose first token (in the call's order) is among
-// them, with all their tokens up to 15 places on: a group is written by one
-// warp, which knows all that the call brings to it.
+// Which tokens of the call come to the places of a group.
+struct Places {
+  signed char at[16];  // relative to the warp's first token; -1: none
+};
+
+// One group's keys: a lane has the tokens g and g + 8.
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) append8_kernel(Append8Args a) {
-  __shared__ signed char places[kWarps][16];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__device__ __forceinline__ void append_keys(const Append8Args& a, const Places& p, uint8_t* grp,
+                                            size_t row0, bool fresh, int lane) {
   const int g = lane >> 2, t = lane & 3;
+  const uint32_t head = grp[32 * D];
+  uint4 x[2][D / 32];
+  int n[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    n[h] = p.at[8 * h + g];
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j)
+      x[h][j] = n[h] >= 0 ? *reinterpret_cast<const uint4*>(a.k + (row0 + n[h]) * D + 32 * j + 8 * t)
+                          : make_uint4(0, 0, 0, 0);
+  }
+  uint32_t big = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) big = larger(big, x[h][j]);
+  const Exponent e(big, head, fresh);
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      uint4* at = reinterpret_cast<uint4*>(grp + k8_piece(D, h, c, lane));
+      if (n[h] >= 0) {
+        const uint2 u = quantise(x[h][2 * c], e.inv), v = quantise(x[h][2 * c + 1], e.inv);
+        *at = make_uint4(u.x, u.y, v.x, v.y);
+        if (a.k_out) {
+          __nv_bfloat16* out = a.k_out + (row0 + n[h]) * D + 64 * c + 8 * t;
+          *reinterpret_cast<uint4*>(out) = values8(u, e.unit);
+          *reinterpret_cast<uint4*>(out + 32) = values8(v, e.unit);
+        }
+      } else if (e.grown) {
+        *at = rescale(*at, e.down);
+      }
+    }
+  __syncwarp();  // every lane has the old exponent
+  if (lane == 0) grp[32 * D] = (uint8_t)e.e;
+}
+
+// Its values: a lane has the tokens 2t, 2t + 1, 2t + 8 and 2t + 9.
+template <int D>
+__device__ __forceinline__ void append_values(const Append8Args& a, const Places& p, uint8_t* grp,
+                                              size_t row0, bool fresh, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t head = grp[32 * D + 1];
+  uint4 x[2][2][D / 64];
+  int n[2][2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      n[h][s] = p.at[8 * h + 2 * t + s];
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j)
+        x[h][s][j] = n[h][s] >= 0 ? *reinterpret_cast<const uint4*>(a.v + (row0 + n[h][s]) * D + 64 * j + 8 * g)
+                                  : make_uint4(0, 0, 0, 0);
+    }
+  uint32_t big = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) big = larger(big, x[h][s][j]);
+  const Exponent e(big, head, fresh);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const bool has0 = n[h][0] >= 0, has1 = n[h][1] >= 0;
+    if (!has0 && !has1 && !e.grown) continue;
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+      uint4* at = reinterpret_cast<uint4*>(grp + v8_piece(D, j, h, lane));
+      const uint2 u = quantise(x[h][0][j], e.inv), v = quantise(x[h][1][j], e.inv);
+      // The two tokens' codes side by side.
+      uint4 c = make_uint4(__byte_perm(u.x, v.x, 0x5140), __byte_perm(u.x, v.x, 0x7362),
+                           __byte_perm(u.y, v.y, 0x5140), __byte_perm(u.y, v.y, 0x7362));
+      if (!(has0 && has1)) {
+        uint4 old = *at;
+        if (e.grown) old = rescale(old, e.down);
+        const uint32_t m = (has0 ? 0x00ff00ffu : 0) | (has1 ? 0xff00ff00u : 0);
+        c = make_uint4((c.x & m) | (old.x & ~m), (c.y & m) | (old.y & ~m), (c.z & m) | (old.z & ~m),
+                       (c.w & m) | (old.w & ~m));
+      }
+      *at = c;
+      if (a.v_out) {
+        __nv_bfloat16* out = a.v_out + row0 * D + 64 * j + 8 * g;
+        if (has0) *reinterpret_cast<uint4*>(out + (ptrdiff_t)n[h][0] * D) = values8(u, e.unit);
+        if (has1) *reinterpret_cast<uint4*>(out + (ptrdiff_t)n[h][1] * D) = values8(v, e.unit);
+      }
+    }
+  }
+  __syncwarp();  // every lane has the old exponent
+  if (lane == 0) grp[32 * D + 1] = (uint8_t)e.e;
+}
+
+// A warp takes 16 neighbouring tokens of one batch entry and head, their keys
+// or their values, and, one after the other, the groups whose first token (in
+// the call's order) is among them, with all their tokens up to 15 places on: a
+// group is written by one warp, which knows all that the call brings to it.
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32, 4) append8_kernel(Append8Args a) {
+  __shared__ Places places[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   wait_for_stream();
   const unsigned id = blockIdx.x * kWarps + warp;
   if (id >= (unsigned)a.warps) return;
@@ -124,109 +244,23 @@ __global__ void __launch_bounds__(kWarps * 32) append8_kernel(Append8Args a) {
   const uint32_t earlier = same & ((1u << lane) - 1) & ~((1u << (lane - 15 > 0 ? lane - 15 : 0)) - 1);
   uint32_t leaders = __ballot_sync(0xffffffffu, lane >= 16 && sa >= 0 && earlier == 0);
   for (; leaders; leaders &= leaders - 1) {
-    const int first = __ffs(leaders) - 1, grp_id = __shfl_sync(0xffffffffu, sa, first) >> 4;
-    // Which token comes to each of the group's places.
-    if (lane < 16) places[warp][lane] = -1;
+    const int first = __ffs(leaders) - 1, id16 = __shfl_sync(0xffffffffu, sa, first) >> 4;
+    Places& p = places[warp];
+    if (lane < 16) p.at[lane] = -1;
     __syncwarp();
-    if (lane >= first && sa >= 0 && sa >> 4 == grp_id) places[warp][sa & 15] = lane - 16;
+    if (lane >= first && sa >= 0 && sa >> 4 == id16) p.at[sa & 15] = lane - 16;
     __syncwarp();
-    if (lane <= first - 17 && sb >= 0 && sb >> 4 == grp_id) places[warp][sb & 15] = 16 + lane;
+    if (lane <= first - 17 && sb >= 0 && sb >> 4 == id16) p.at[sb & 15] = 16 + lane;
     __syncwarp();
-    const int mine = places[warp][lane & 15];
-    const uint32_t here = __ballot_sync(0xffffffffu, mine >= 0) & 0xffffu;
-    int kn[2], vn[2][2];  // tokens of the lane's places
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      kn[h] = places[warp][8 * h + g];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) vn[h][e] = places[warp][8 * h + 2 * t + e];
-    }
-    __syncwarp();  // read before the next group's
-    const int gpp = a.shift - 4, page = grp_id >> gpp;
-    uint8_t* grp = a.cache + ((((size_t)page * a.Hkv + hk) << gpp) + (grp_id & ((1 << gpp) - 1))) *
-                                 group8_bytes(D);
-    const uint32_t head = *reinterpret_cast<const uint16_t*>(grp + 32 * D);
-    const size_t row0 = (size_t)bh * a.N + n0;
-    uint4 k[2][D / 32], v[2][2][D / 64];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int j = 0; j < D / 32; ++j)
-        k[h][j] = kn[h] >= 0 ? *reinterpret_cast<const uint4*>(a.k + (row0 + kn[h]) * D + 32 * j + 8 * t)
-                             : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j)
-          v[h][e][j] = vn[h][e] >= 0
-                           ? *reinterpret_cast<const uint4*>(a.v + (row0 + vn[h][e]) * D + 64 * j + 8 * g)
-                           : make_uint4(0, 0, 0, 0);
-    }
-    uint32_t kbig = 0, vbig = 0;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int j = 0; j < D / 32; ++j) kbig = larger(kbig, k[h][j]);
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j) vbig = larger(vbig, v[h][e][j]);
-    }
-    kbig = __reduce_max_sync(0xffffffffu, kbig);
-    vbig = __reduce_max_sync(0xffffffffu, vbig);
     // The group's first token begins it; what it held before is not there.
-    const bool fresh = here & 1;
-    const int kold = exp8(head & 0xff), vold = exp8(head >> 8);
-    int ke = exponent_for(kbig), ve = exponent_for(vbig);
-    if (!fresh) ke = max(ke, kold), ve = max(ve, vold);
-    const bool kgrow = !fresh && ke > kold, vgrow = !fresh && ve > vold;
-    const float kinv = pow2(-ke), vinv = pow2(-ve), ks = pow2(ke), vs = pow2(ve);
-    const uint32_t kf = factor_of(ke - kold), vf = factor_of(ve - vold);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint4* at = reinterpret_cast<uint4*>(grp + k8_piece(D, h, c, lane));
-        if (kn[h] >= 0) {
-          const uint2 x = quantise(k[h][2 * c], kinv), y = quantise(k[h][2 * c + 1], kinv);
-          *at = make_uint4(x.x, x.y, y.x, y.y);
-          if (a.k_out) {
-            __nv_bfloat16* out = a.k_out + (row0 + kn[h]) * D + 64 * c + 8 * t;
-            *reinterpret_cast<uint4*>(out) = values8(x, ks);
-            *reinterpret_cast<uint4*>(out + 32) = values8(y, ks);
-          }
-        } else if (kgrow) {
-          *at = rescale(*at, kf);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < D / 64; ++j) {
-        const bool has0 = vn[h][0] >= 0, has1 = vn[h][1] >= 0;
-        if (!has0 && !has1 && !vgrow) continue;
-        uint4* at = reinterpret_cast<uint4*>(grp + v8_piece(D, j, h, lane));
-        const uint2 x = quantise(v[h][0][j], vinv), y = quantise(v[h][1][j], vinv);
-        // The two tokens' codes side by side.
-        uint4 u = make_uint4(__byte_perm(x.x, y.x, 0x5140), __byte_perm(x.x, y.x, 0x7362),
-                             __byte_perm(x.y, y.y, 0x5140), __byte_perm(x.y, y.y, 0x7362));
-        if (!(has0 && has1)) {
-          uint4 old = *at;
-          if (vgrow) old = rescale(old, vf);
-          const uint32_t m = (has0 ? 0x00ff00ffu : 0) | (has1 ? 0xff00ff00u : 0);
-          u = make_uint4((u.x & m) | (old.x & ~m), (u.y & m) | (old.y & ~m), (u.z & m) | (old.z & ~m),
-                         (u.w & m) | (old.w & ~m));
-        }
-        *at = u;
-        if (a.v_out) {
-          if (has0)
-            *reinterpret_cast<uint4*>(a.v_out + (row0 + vn[h][0]) * D + 64 * j + 8 * g) = values8(x, vs);
-          if (has1)
-            *reinterpret_cast<uint4*>(a.v_out + (row0 + vn[h][1]) * D + 64 * j + 8 * g) = values8(y, vs);
-        }
-      }
-    }
-    __syncwarp();  // every lane has the old exponents
-    if (lane == 0)
-      *reinterpret_cast<uint16_t*>(grp + 32 * D) = (uint16_t)((ke & 0xff) | (ve & 0xff) << 8);
+    const bool fresh = p.at[0] >= 0;
+    const int gpp = a.shift - 4, page = id16 >> gpp;
+    uint8_t* grp = a.cache + ((((size_t)page * a.Hkv + hk) << gpp) + (id16 & ((1 << gpp) - 1))) *
+                                 group8_bytes(D);
+    const size_t row0 = (size_t)bh * a.N + n0;
+    if (blockIdx.y == 0) append_keys<D>(a, p, grp, row0, fresh, lane);
+    else append_values<D>(a, p, grp, row0, fresh, lane);
+    __syncwarp();  // the places are read
   }
 }
 
@@ -294,7 +328,7 @@ __global__ void __launch_bounds__(kWarps * 32) read8_kernel(Read8Args a) {
 
 cudaError_t launch_cache8_append(const Append8Args& a, int d, cudaStream_t stream) {
   return launch_overlapped(d == 128 ? append8_kernel<128> : append8_kernel<64>,
-                           dim3((a.warps + kWarps - 1) / kWarps), dim3(kWarps * 32), 0, stream, a);
+                           dim3((a.warps + kWarps - 1) / kWarps, 2), dim3(kWarps * 32), 0, stream, a);
 }
 cudaError_t launch_cache8_read(const Read8Args& a, int d, cudaStream_t stream) {
   return launch_overlapped(d == 128 ? read8_kernel<128> : read8_kernel<64>,
