@@ -30,7 +30,7 @@ BINDING = os.path.join(OUT_DIR, "_fa_binding.so")
 FLAGS = os.path.join(OUT_DIR, "build_flags.json")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_serve_api.cu",
            "fa_rope.cu", "fa_cache4.cu", "fa_cache4_attn.cu",
-           "fa_cache8.cu", "fa_cache8_attn.cu"]
+           "fa_cache8.cu", "fa_cache8_attn.cu", "fa_cache8_wide.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -246,7 +246,7 @@ int cache4_attn_rows(int rows, int d) {
 }
 
 cudaError_t launch_cache4_attn(const CacheAttnArgs& a, int d, int sm_count, cudaStream_t stream) {
-  const int nt = cache4_attn_rows(a.rows, d) / 8;
+  const int nt = a.item_rows / 8;
   if (d == 128)
     return nt == 1   ? run<128, 1>(a, sm_count, stream)
            : nt == 2 ? run<128, 2>(a, sm_count, stream)

@@ -59,6 +59,8 @@ struct Call {
   int row_blocks;         // of T tokens: a request's most
   int max_len;            // tokens of a block table
   FastDiv by_heads;
+  // Requests with fewer or more live rows have no items here.
+  int least_rows = 0, most_rows = 0x7fffffff;
   // (Most calls have one row block; a division costs 0.1 us of a short one.)
   FA_BOTH int request_of_pair(int at) const { return row_blocks == 1 ? at : at / row_blocks; }
 };
@@ -72,7 +74,8 @@ FA_BOTH Request request_of(const Call& c, int len, int n) {
   Request r;
   r.len = len < 0 ? 0 : lesser(len, c.max_len);
   r.ql = n < 0 ? 0 : lesser(n, c.T);
-  r.row_blocks = r.ql == 0 ? 0 : (r.ql * c.heads - 1) / c.rows + 1;
+  const int live = r.ql * c.heads;
+  r.row_blocks = live == 0 || live < c.least_rows || live > c.most_rows ? 0 : (live - 1) / c.rows + 1;
   return r;
 }
 

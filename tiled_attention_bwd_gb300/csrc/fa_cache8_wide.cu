@@ -1,0 +1,753 @@
+// fa_cache8_wide.cu -- the attention over the 8-bit cache for requests with
+// many query rows (chunks of a prompt, many drafts): codes are made f16 once
+// for up to 256 rows, and the products run on tcgen05.
+//
+// The division of work is that of fa_cache4_work.h with 256 rows to an item:
+// two tiles of 128 rows (a token's heads next to one another), units of 128
+// keys.  One block per SM, sixteen warps:
+//   warps 0-7    softmax, tile 0 and tile 1; thread = row.  They also bring
+//                the rows of Q, scaled by a power of two to f16 as in
+//                fa_cache_attn.cuh, and write the results.
+//   warps 8-11   make f16 tiles of K and V (128-byte swizzle) of a unit's
+//                groups, 32 of its keys each
+//   warp 12      deals out the segments and copies the groups of the next
+//                units into shared memory
+//   warp 13      issues S_t = Q_t K^T and O_t += P_t V, P_t f16 in TMEM
+// While one tile's softmax runs, the tensor core works for the other.
+//
+// Products.  Codes are f16 values, so K and V enter exactly.  A group's power
+// of two for K multiplies its 16 columns of S; the row's maximum is taken of
+// s + e_v, and P = 2^(s + e_v - m + 8) in f16: as in fa_cache8_attn.cu, whose
+// accuracy this kernel shares.
+//
+// NaN.  A hidden key is masked by selection.  A hidden value would reach a row
+// as 0 * NaN: in units that some row does not see all of, NaN codes of V are
+// taken as zero, and rows that do see them note their dims (in the workspace;
+// rare) and write NaN at the end.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "fa_cache4_work.h"
+#include "fa_cache8.cuh"
+#include "fa_common.cuh"
+#include "fa_serve.h"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kMakeWarp = 8, kLoadWarp = 12, kMmaWarp = 13;
+// Registers: launched at 128 a thread; the four warpgroups' shares add up to
+// 512 * 128.
+constexpr int kSoftmaxRegs = 192, kMakeRegs = 80, kCtrlRegs = 48;
+static_assert(2 * 128 * kSoftmaxRegs + 128 * kMakeRegs + 128 * kCtrlRegs <= kThreads * 128);
+constexpr float kNoMax = -1e30f;  // m of a row that has seen no key
+constexpr float kUp = 8.0f;       // P carries 2^kUp
+constexpr float kSlack = 6.0f;    // growth of m that is left standing
+constexpr int kUnitGroups = kC4Unit / kGroup;
+constexpr int kSegs = 4, kInfos = 4;
+
+// Where-codes of the waits.
+constexpr uint32_t kWLoadSeg = 0x531, kWLoadRaw = 0x532, kWMakeSeg = 0x533, kWMakeRaw = 0x534,
+                   kWMakeTile = 0x535, kWMmaSeg = 0x536, kWMmaQ = 0x537, kWMmaTile = 0x538,
+                   kWMmaP = 0x539, kWSmSeg = 0x53a, kWSmInfo = 0x53b, kWSmS = 0x53c,
+                   kWSmO = 0x53d;
+
+// A segment: some units of an item.
+struct Seg {
+  int b, hk, row0, live;   // live: rows of the item, from row0 on
+  int pos0;                // position of the request's first new token
+  int tok0, units;         // units < 0: no more segments
+  int plain_lo, plain_hi;  // tokens within are seen by every live row
+  int whole, part;         // part: place of the partial results
+};
+// What the softmax needs of a group: factor of the keys, exponent of the
+// values, 2^-that, and whether some value is NaN (not 0).
+struct alignas(16) Info {
+  float k, log_v, inv_v;
+  int nan;
+};
+
+template <int D>
+struct Wide {
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kStages = D == 128 ? 3 : 6;     // of the ring of K and V tiles
+  static constexpr int kRawStages = D == 128 ? 2 : 4;  // units on their way
+  static constexpr int kRawBytes = kUnitGroups * group8_bytes(D);
+  static constexpr int kRingOff = 2 * kTileBytes;  // (behind the Q tiles)
+  static constexpr int kRawOff = kRingOff + kStages * kTileBytes;
+  static constexpr int kCtrlOff = kRawOff + kRawStages * kRawBytes;
+  struct Ctrl {
+    uint64_t raw_full[kRawStages], raw_empty[kRawStages];
+    uint64_t kv_full[kStages], kv_empty[kStages];
+    uint64_t q_full[2], s_full[2], p_full[2], o_done[2], mma_done;
+    uint64_t seg_full[kSegs], seg_empty[kSegs], info_full[kInfos];
+    Info info[kInfos][kUnitGroups];
+    int there[kInfos];               // bit g: group g of the unit is there
+    int raw_there[kRawStages];
+    Seg seg[kSegs];
+    uint32_t abort, tmem;
+  };
+  static constexpr int kSmem = kCtrlOff + (int)sizeof(Ctrl) + 1024;  // + alignment
+};
+static_assert(Wide<128>::kSmem <= 232448 && Wide<64>::kSmem <= 232448);
+
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
+  return idesc_bf16(M, N, false, b_mn) & ~((1u << 7) | (1u << 10));  // A and B: f16
+}
+template <int D>
+__device__ __forceinline__ void issue_qk(uint32_t s, uint64_t q, uint64_t k) {
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    const uint32_t off = (i >> 2) * kSubTileBytes + (i & 3) * 32;
+    mma_ss(s, sdesc_adv(q, off), sdesc_adv(k, off), idesc_f16(128, 128, false), i > 0);
+  }
+}
+template <int D>
+__device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint64_t v, bool accumulate) {
+#pragma unroll
+  for (int i = 0; i < kC4Unit / 16; ++i)
+    mma_ts(o, p + i * 8, sdesc_adv(v, i * 2048), idesc_f16(128, D, true), accumulate || i > 0);
+}
+
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint4 make8(uint32_t a, uint32_t b) {
+  uint4 r;
+  e4m3_to_f16(a, r.x, r.y);
+  e4m3_to_f16(b, r.z, r.w);
+  return r;
+}
+// 16 bytes, dims `dim` .. + 7 of row `row` of a tile.
+__device__ __forceinline__ uint4* chunk_of(uint8_t* tile, int row, int dim) {
+  return reinterpret_cast<uint4*>(tile + (dim >> 6) * kSubTileBytes + row * 128 +
+                                  ((((dim >> 3) & 7) ^ (row & 7)) << 4));
+}
+
+// One group's keys into rows row0 .. + 15 of a K tile.
+template <int D>
+__device__ __forceinline__ void make_keys(uint8_t* tile, const uint8_t* grp, int row0, bool there,
+                                          int lane) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (there) u = *reinterpret_cast<const uint4*>(grp + k8_piece(D, h, c, lane));
+      // Odd rows write their halves in the other order: eight lanes then
+      // write eight different chunks.
+      const bool odd = g & 1;
+      const int at = 64 * c + 8 * t, row = row0 + 8 * h + g;
+      *chunk_of(tile, row, at + (odd ? 32 : 0)) = make8(odd ? u.z : u.x, odd ? u.w : u.y);
+      *chunk_of(tile, row, at + (odd ? 0 : 32)) = make8(odd ? u.x : u.z, odd ? u.y : u.w);
+    }
+}
+// One group's values.  kEdge: NaN as zero.
+template <int D, bool kEdge>
+__device__ __forceinline__ void make_values(uint8_t* tile, const uint8_t* grp, int row0, bool there,
+                                            int lane) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (there) u = *reinterpret_cast<const uint4*>(grp + v8_piece(D, j, h, lane));
+      if (kEdge) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] &= ~__vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t sel = e ? 0x7531 : 0x6420;  // one token's codes of a pair
+        *chunk_of(tile, row0 + 8 * h + 2 * t + e, 64 * j + 8 * g) =
+            make8(__byte_perm(u.x, u.y, sel), __byte_perm(u.z, u.w, sel));
+      }
+    }
+}
+// Whether a group has a NaN value (the same on every lane).
+template <int D>
+__device__ __forceinline__ bool has_nan(const uint8_t* grp, int lane) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const uint4 u = *reinterpret_cast<const uint4*>(grp + 16 * D + (i * 32 + lane) * 16);
+    for (uint32_t w : {u.x, u.y, u.z, u.w}) any |= __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+  }
+  return __any_sync(0xffffffffu, any != 0);
+}
+
+__device__ __forceinline__ c4::Call wide_call(const CacheAttnArgs& a) {
+  c4::Call c = {a.B, a.Hkv, a.T, a.window, a.heads, kC8WideRows, a.row_blocks, a.M << a.shift, a.by_heads};
+  c.least_rows = a.least_rows;
+  c.most_rows = a.most_rows;
+  return c;
+}
+__device__ __forceinline__ size_t row_at(const CacheAttnArgs& a, int b, int hk, int row) {
+  const int t = (int)a.by_heads.div(row), h = row - t * a.heads;
+  return (((size_t)b * a.Hkv + hk) * a.heads + h) * a.T + t;
+}
+// A request's group that holds token `tok`, or null.
+__device__ __forceinline__ const uint8_t* group_at(const CacheAttnArgs& a, int b, int hk, int tok,
+                                                   int bytes) {
+  const int page = a.block_table[(size_t)b * a.M + (tok >> a.shift)], gpp = a.shift - 4;
+  if (page < 0 || page >= a.pages) return nullptr;
+  return a.cache + ((((size_t)page * a.Hkv + hk) << gpp) + ((tok >> 4) & ((1 << gpp) - 1))) * bytes;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs a) {
+  using L = Wide<D>;
+  using Ctrl = typename L::Ctrl;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  Ctrl* c = reinterpret_cast<Ctrl*>(smem + L::kCtrlOff);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < L::kRawStages; ++i) mbar_init(&c->raw_full[i], 1), mbar_init(&c->raw_empty[i], 4);
+    for (int i = 0; i < L::kStages; ++i) mbar_init(&c->kv_full[i], 4), mbar_init(&c->kv_empty[i], 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&c->q_full[t], 4), mbar_init(&c->s_full[t], 1);
+      mbar_init(&c->p_full[t], 4), mbar_init(&c->o_done[t], 1);
+    }
+    mbar_init(&c->mma_done, 1);
+    // A segment is let go of by the making warps, the MMA thread and the
+    // softmax warps.
+    for (int i = 0; i < kSegs; ++i) mbar_init(&c->seg_full[i], 1), mbar_init(&c->seg_empty[i], 4 + 1 + 8);
+    for (int i = 0; i < kInfos; ++i) mbar_init(&c->info_full[i], 4);
+    c->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&c->tmem, 512);
+    tmem_relinquish();
+  }
+  wait_for_stream();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // ---- this block's share of the units
+  const c4::Call call = wide_call(a);
+  auto read = [&](int b) {
+    return c4::request_of(call, a.seq_lens[b], a.q_lens ? a.q_lens[b] : a.T);
+  };
+  long long* scan = reinterpret_cast<long long*>(smem);  // (before the tiles are in use)
+  c4::Cursor* start = reinterpret_cast<c4::Cursor*>(smem + 256);
+  int* into = reinterpret_cast<int*>(smem + 512);
+  const int pairs = a.B * a.row_blocks, per = (pairs - 1) / kThreads + 1;
+  const int p0 = (int)min((long long)pairs, (long long)tid * per), p1 = p0 + min(pairs - p0, per);
+  const long long mine = c4::cost_of(call, read, p0, p1);
+  long long upto = mine;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, upto, m);
+    if (lane >= m) upto += u;
+  }
+  if (lane == 31) scan[warp] = upto;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  long long total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) upto += scan[w];
+    total += scan[w];
+  }
+  const long long before = upto - mine;
+  const c4::Shares shares(total * a.Hkv, gridDim.x);
+  bool work = (int)blockIdx.x < shares.blocks;  // of the block
+  const long long u0 = work ? shares.first(blockIdx.x) : 0;
+  if (work && u0 >= before * a.Hkv && u0 < upto * a.Hkv)
+    *into = start->seek(call, read, p0, u0 - before * a.Hkv, (int)(shares.first(blockIdx.x + 1) - u0));
+  __syncthreads();
+  c4::Cursor at;
+  if (work) at = *start;
+  if (work && at.end == at.unit) work = false;  // a share of nothing but an item's cost
+  if (tid == 0) {
+    int4 j = make_int4(-1, 0, 0, 0);
+    int last, first_part;
+    if (work && c4::join_of(shares, at, blockIdx.x, u0, *into, &last, &first_part))
+      j = make_int4(at.b, at.hk * a.row_blocks + at.rb, last, first_part);
+    a.joins[blockIdx.x] = j;
+  }
+  const uint32_t tmem = c->tmem;
+  const WaitCtl wc = {a.st, &c->abort, a.timeout_ns};
+  __syncthreads();  // the start is read: Q's tiles may be written
+
+  if (warp >= kLoadWarp) {
+    reg_dealloc<kCtrlRegs>();
+    if (warp == kLoadWarp && work) {
+      // ------------------------------------------------- segments and copies
+      bool ok = true;
+      int stage = 0, last_par[L::kRawStages];
+      uint32_t phase = 0;
+#pragma unroll
+      for (int i = 0; i < L::kRawStages; ++i) last_par[i] = -1;
+      for (int s = 0; ok; ++s) {
+        const bool more = s == 0 || at.next(call, read);
+        ok = __all_sync(0xffffffffu, wait_bar<true>(&c->seg_empty[s % kSegs], ((s / kSegs) & 1) ^ 1, wc, kWLoadSeg));
+        if (!ok) break;
+        const int units = more ? at.end - at.unit : -1;
+        const int tok0 = more ? at.k.lo + at.unit * kC4Unit : 0;
+        if (lane == 0) {
+          Seg g = {};
+          g.units = units;
+          if (more) {
+            g.b = at.b, g.hk = at.hk, g.row0 = at.rb * kC8WideRows;
+            g.live = min(kC8WideRows, at.r.ql * a.heads - g.row0);
+            g.pos0 = at.r.len - at.r.ql;
+            g.tok0 = tok0;
+            g.plain_hi = at.k.first + 1;
+            g.plain_lo = a.window < 0 ? 0 : at.k.hi - 1 - a.window;
+            g.whole = at.unit == 0 && at.end == at.k.units;
+            g.part = 2 * blockIdx.x + (s == 0 ? 0 : 1);
+          }
+          c->seg[s % kSegs] = g;
+          mbar_arrive(&c->seg_full[s % kSegs]);
+        }
+        if (!more) break;
+        // Each lane looks up one group of the next four units.
+        for (int base = 0; base < units && ok; base += 4) {
+          const int u = base + lane / kUnitGroups, tok = tok0 + u * kC4Unit + lane % kUnitGroups * kGroup;
+          const uint8_t* src = nullptr;
+          if (u < units && tok < at.k.hi) src = group_at(a, at.b, at.hk, tok, group8_bytes(D));
+          const uint32_t have = __ballot_sync(0xffffffffu, src != nullptr);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (base + q >= units || !ok) break;
+            ok = __all_sync(0xffffffffu, wait_bar<true>(&c->raw_empty[stage], phase ^ 1, wc, kWLoadRaw));
+            if (!ok) break;
+            const int mask = (have >> (q * kUnitGroups)) & 0xff;
+            if (lane == 0) {
+              c->raw_there[stage] = mask;
+              if (mask) mbar_arrive_expect_tx(&c->raw_full[stage], __popc(mask) * group8_bytes(D));
+              else mbar_arrive(&c->raw_full[stage]);
+            }
+            __syncwarp();
+            if (lane / kUnitGroups == q && src)
+              bulk_load(smem + L::kRawOff + stage * L::kRawBytes + lane % kUnitGroups * group8_bytes(D), src,
+                        group8_bytes(D), &c->raw_full[stage]);
+#pragma unroll
+            for (int i = 0; i < L::kRawStages; ++i)
+              if (i == stage) last_par[i] = (int)phase;
+            if (++stage == L::kRawStages) stage = 0, phase ^= 1;
+          }
+        }
+      }
+      // The copies land before the block leaves, whether it stops or not.
+#pragma unroll
+      for (int i = 0; i < L::kRawStages; ++i)
+        if (last_par[i] >= 0) drain_bar<true>(&c->raw_full[i], (uint32_t)last_par[i], a.timeout_ns);
+      __syncwarp();
+    } else if (warp == kMmaWarp && lane == 0 && work) {
+      // --------------------------------------------------------- MMA issuer
+      const uint64_t q_desc = sdesc_sw128(smem_addr(smem), 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_addr(smem + L::kRingOff), 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(smem_addr(smem + L::kRingOff), kSubTileBytes, 1024);
+      int stage = 0;
+      uint32_t phase = 0, q_cnt[2] = {0, 0}, p_cnt[2] = {0, 0};
+      bool ok = true;
+      auto next_tile = [&](int& st) {
+        st = stage;
+        const bool r = wait_bar<true>(&c->kv_full[stage], phase, wc, kWMmaTile);
+        if (++stage == L::kStages) stage = 0, phase ^= 1;
+        tc_fence_after();
+        return r;
+      };
+      auto qk = [&](int t, int st) {
+        issue_qk<D>(tmem + t * 128, sdesc_adv(q_desc, t * L::kTileBytes), sdesc_adv(k_desc, st * L::kTileBytes));
+        mma_commit(&c->s_full[t]);
+      };
+      for (int s = 0; ok; ++s) {
+        ok = wait_bar<true>(&c->seg_full[s % kSegs], (s / kSegs) & 1, wc, kWMmaSeg);
+        if (!ok) break;
+        const int units = c->seg[s % kSegs].units;
+        const bool two = c->seg[s % kSegs].live > 128;
+        mbar_arrive(&c->seg_empty[s % kSegs]);
+        if (units < 0) break;
+        int kst = 0, vst = 0;
+        ok = wait_bar<true>(&c->q_full[0], q_cnt[0]++ & 1, wc, kWMmaQ) && next_tile(kst);
+        if (!ok) break;
+        qk(0, kst);
+        if (two) {
+          ok = wait_bar<true>(&c->q_full[1], q_cnt[1]++ & 1, wc, kWMmaQ);
+          if (!ok) break;
+          tc_fence_after();
+          qk(1, kst);
+        }
+        mma_commit(&c->kv_empty[kst]);
+        for (int j = 0; j < units && ok; ++j) {
+          const bool last = j == units - 1;
+          ok = next_tile(vst) && wait_bar<true>(&c->p_full[0], p_cnt[0]++ & 1, wc, kWMmaP);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vd = sdesc_adv(v_desc, vst * L::kTileBytes);
+          issue_pv<D>(tmem + 256, tmem, vd, j > 0);
+          if (!last) {
+            ok = next_tile(kst);
+            if (!ok) break;
+            qk(0, kst);
+          } else {
+            mma_commit(&c->o_done[0]);
+          }
+          if (two) {
+            ok = wait_bar<true>(&c->p_full[1], p_cnt[1]++ & 1, wc, kWMmaP);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv<D>(tmem + 256 + D, tmem + 128, vd, j > 0);
+          }
+          mma_commit(&c->kv_empty[vst]);
+          if (two && !last) qk(1, kst);
+          else if (two) mma_commit(&c->o_done[1]);
+          if (!last) mma_commit(&c->kv_empty[kst]);
+        }
+      }
+      // Every MMA issued above must finish before TMEM is released.
+      mma_commit(&c->mma_done);
+      drain_bar<true>(&c->mma_done, 0, a.timeout_ns);
+    }
+  } else if (warp >= kMakeWarp) {
+    reg_dealloc<kMakeRegs>();
+    // ------------------------------------------------------- f16 of the codes
+    const int w = warp - kMakeWarp;
+    int stage = 0, raw = 0, u = 0;
+    uint32_t phase = 0, raw_phase = 0;
+    bool ok = work;
+    auto tile_free = [&]() {
+      return wait_bar_warp<true>(&c->kv_empty[stage], phase ^ 1, wc, kWMakeTile);
+    };
+    auto tile_done = [&]() {
+      fence_proxy_async_smem();
+      warp_arrive(&c->kv_full[stage]);
+      if (++stage == L::kStages) stage = 0, phase ^= 1;
+    };
+    for (int s = 0; ok; ++s) {
+      ok = wait_bar_warp<true>(&c->seg_full[s % kSegs], (s / kSegs) & 1, wc, kWMakeSeg);
+      if (!ok) break;
+      const int units = c->seg[s % kSegs].units, tok0 = c->seg[s % kSegs].tok0;
+      const int lo = c->seg[s % kSegs].plain_lo, hi = c->seg[s % kSegs].plain_hi;
+      warp_arrive(&c->seg_empty[s % kSegs]);
+      if (units < 0) break;
+      for (int j = 0; j < units; ++j, ++u) {
+        ok = wait_bar_warp<true>(&c->raw_full[raw], raw_phase, wc, kWMakeRaw) && tile_free();
+        if (!ok) break;
+        const int there = c->raw_there[raw], tok = tok0 + j * kC4Unit;
+        const bool edge = there != 0xff || tok < lo || tok + kC4Unit > hi;
+        const uint8_t* base = smem + L::kRawOff + raw * L::kRawBytes;
+        uint8_t* tile = smem + L::kRingOff + stage * L::kTileBytes;
+        Info* info = c->info[u % kInfos];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int g = 2 * w + i;
+          const uint8_t* grp = base + g * group8_bytes(D);
+          const bool have = (there >> g) & 1;
+          make_keys<D>(tile, grp, g * kGroup, have, lane);
+          const int nan = edge && have && has_nan<D>(grp, lane);
+          if (lane == 0) {
+            const uint32_t two = *reinterpret_cast<const uint16_t*>(grp + 32 * D);
+            const int ve = exp8(two >> 8);
+            info[g] = {pow2(exp8(two & 0xff)), (float)ve, pow2(-ve), nan};
+          }
+        }
+        if (w == 0 && lane == 0) c->there[u % kInfos] = there;
+        warp_arrive(&c->info_full[u % kInfos]);
+        tile_done();
+        ok = tile_free();
+        if (!ok) break;
+        tile = smem + L::kRingOff + stage * L::kTileBytes;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int g = 2 * w + i;
+          const uint8_t* grp = base + g * group8_bytes(D);
+          const bool have = (there >> g) & 1;
+          if (edge) make_values<D, true>(tile, grp, g * kGroup, have, lane);
+          else make_values<D, false>(tile, grp, g * kGroup, have, lane);
+        }
+        tile_done();
+        warp_arrive(&c->raw_empty[raw]);
+        if (++raw == L::kRawStages) raw = 0, raw_phase ^= 1;
+      }
+    }
+  } else {
+    reg_alloc<kSoftmaxRegs>();
+    // ------------------------------------------------- softmax (thread = row)
+    const int t = warp >> 2, quarter = warp & 3;
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t tS = tl + t * 128, tO = tl + 256 + t * D;
+    const int in_tile = quarter * 32 + lane;
+    uint32_t s_cnt = 0, o_cnt = 0;
+    int u_seg = 0;  // units of the segments before
+    bool ok = work;
+    for (int s = 0; ok; ++s) {
+      ok = wait_bar_warp<true>(&c->seg_full[s % kSegs], (s / kSegs) & 1, wc, kWSmSeg);
+      if (!ok) break;
+      const Seg& seg = c->seg[s % kSegs];  // (kept until the segment's end)
+      const int units = seg.units;
+      if (units < 0) break;
+      if (seg.live <= t * 128) {
+        u_seg += units;
+        warp_arrive(&c->seg_empty[s % kSegs]);
+        continue;
+      }
+      const bool valid = t * 128 + in_tile < seg.live;
+      const int row = seg.row0 + (valid ? t * 128 + in_tile : 0);
+      const int pos = seg.pos0 + (int)a.by_heads.div(row);
+
+      // ---- the row of Q, scaled by a power of two: largest in [2^8, 2^9)
+      float cr;
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + row_at(a, seg.b, seg.hk, row) * D);
+        uint4 q[D / 8];
+        uint32_t big = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          q[i] = valid ? src[i] : make_uint4(0, 0, 0, 0);
+          big = __vmaxu2(__vmaxu2(big, q[i].x & 0x7fff7fffu), q[i].y & 0x7fff7fffu);
+          big = __vmaxu2(__vmaxu2(big, q[i].z & 0x7fff7fffu), q[i].w & 0x7fff7fffu);
+        }
+        big = max(big & 0xffffu, big >> 16);
+        int e = big >> 7;
+        e = e < 16 ? 16 : (e > 250 ? 250 : e);
+        const float down = __uint_as_float((uint32_t)(262 - e) << 23);
+        cr = __uint_as_float((uint32_t)(e - 8) << 23) * a.scale_log2;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+          uint32_t f[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) f[x] = f16x2(bf16_lo(w[x]) * down, bf16_hi(w[x]) * down);
+          *chunk_of(smem + t * L::kTileBytes, in_tile, 8 * i) = make_uint4(f[0], f[1], f[2], f[3]);
+        }
+        fence_proxy_async_smem();
+        warp_arrive(&c->q_full[t]);
+      }
+
+      float m = kNoMax, l = 0.f;
+      bool had_nan = false;
+      for (int j = 0; j < units; ++j) {
+        const int u = u_seg + j;
+        ok = wait_bar_warp<true>(&c->info_full[u % kInfos], (u / kInfos) & 1, wc, kWSmInfo) &&
+             wait_bar_warp<true>(&c->s_full[t], s_cnt & 1, wc, kWSmS);
+        ++s_cnt;
+        if (!ok) break;
+        tc_fence_after();
+        const float4* info = reinterpret_cast<const float4*>(c->info[u % kInfos]);
+        uint32_t x[128];
+        tmem_ld32(tS, x);
+        tmem_ld32(tS + 32, x + 32);
+        tmem_ld32(tS + 64, x + 64);
+        tmem_ld32(tS + 96, x + 96);
+        tmem_wait_ld();
+        reg_fence32(x);
+        reg_fence32(x + 32);
+        reg_fence32(x + 64);
+        reg_fence32(x + 96);
+        const int tok = seg.tok0 + j * kC4Unit, there = c->there[u % kInfos];
+        if (there != 0xff || tok < seg.plain_lo || tok + kC4Unit > seg.plain_hi) {
+          const int hi = pos - tok, lo = a.window < 0 ? -1 : pos - a.window - tok;
+#pragma unroll
+          for (int e = 0; e < 128; ++e)
+            if (e > hi || e < lo || !((there >> (e / kGroup)) & 1)) x[e] = __float_as_uint(-INFINITY);
+          // Dims of NaN values that the row sees, into the workspace.
+          bool nan = false;
+#pragma unroll
+          for (int g = 0; g < kUnitGroups; ++g) nan |= __float_as_int(info[g].w) != 0;
+          if (nan) {
+            uint32_t* note = a.nan_rows + ((size_t)blockIdx.x * kC8WideRows + t * 128 + in_tile) * 4;
+#pragma unroll 1
+            for (int d0 = 0; d0 < D; d0 += 32) {
+              uint32_t dims = had_nan ? note[d0 / 32] : 0;
+#pragma unroll 1
+              for (int e = max(lo, 0); e <= min(hi, 127); ++e) {
+                const uint8_t* grp = nullptr;
+                if (__float_as_int(info[e / kGroup].w))
+                  grp = group_at(a, seg.b, seg.hk, tok + e, group8_bytes(D));
+                if (!grp) continue;
+#pragma unroll 1
+                for (int d = 0; d < 32; ++d)
+                  if ((grp[v8_at(D, e % kGroup, d0 + d)] & 0x7f) == 0x7f) dims |= 1u << d;
+              }
+              note[d0 / 32] = dims;
+            }
+            had_nan = true;
+            __syncwarp();
+          }
+        }
+        // Largest s + e_v, in powers of two.
+        float top = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < kUnitGroups; ++g) {
+          const float4 f = info[g];
+          float mg = fmaxf(__uint_as_float(x[16 * g]), __uint_as_float(x[16 * g + 1]));
+#pragma unroll
+          for (int e = 16 * g + 2; e < 16 * g + 16; e += 2)
+            mg = max3(mg, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+          top = fmaxf(top, fmaf(mg, fmaxf(cr * f.x, 1.2e-38f), f.y));
+        }
+        const bool bump = top > m + kUp + kSlack;
+        float alpha = 1.f;
+        if (bump) {
+          alpha = ex2(m - (top - kUp));
+          m = top - kUp;
+          l *= alpha;
+        }
+#pragma unroll
+        for (int g = 0; g < kUnitGroups; ++g) {
+          const float4 f = info[g];
+          const uint64_t w2 = bcast2(fmaxf(cr * f.x, 1.2e-38f)), c2 = bcast2(f.y - m);
+          float la[2] = {0.f, 0.f}, lb[2] = {0.f, 0.f};
+#pragma unroll
+          for (int e = 16 * g; e < 16 * g + 16; e += 2) {
+            float y0, y1;
+            fma2_bcast(y0, y1, __uint_as_float(x[e]), __uint_as_float(x[e + 1]), w2, c2);
+            const float p0 = ex2(y0), p1 = ex2(y1);
+            add2_acc(la[(e >> 1) & 1], lb[(e >> 1) & 1], p0, p1);
+            x[e / 2] = f16x2(p0, p1);
+          }
+          l = fmaf((la[0] + lb[0]) + (la[1] + lb[1]), f.z, l);
+        }
+        tmem_st32(tS, x);
+        tmem_st32(tS + 32, x + 32);
+        if (j > 0 && __any_sync(0xffffffffu, bump)) {
+#pragma unroll 1
+          for (int ch = 0; ch < D / 32; ++ch) {
+            uint32_t o[32];
+            tmem_ld32(tO + ch * 32, o);
+            tmem_wait_ld();
+            reg_fence32(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(tO + ch * 32, o);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(&c->p_full[t]);
+      }
+      if (!ok) break;
+      u_seg += units;
+      ok = wait_bar_warp<true>(&c->o_done[t], o_cnt & 1, wc, kWSmO);
+      ++o_cnt;
+      if (!ok) break;
+      tc_fence_after();
+
+      // ---- the results
+      const bool whole = seg.whole;
+      const float mul = !whole ? 1.f : (l > 0.f || l != l ? 1.f / l : 0.f);
+      const size_t out = row_at(a, seg.b, seg.hk, row);
+      const size_t part = (size_t)seg.part * kC8WideRows + t * 128 + in_tile;
+      const uint32_t* note = a.nan_rows + ((size_t)blockIdx.x * kC8WideRows + t * 128 + in_tile) * 4;
+#pragma unroll 1
+      for (int ch = 0; ch < D / 32; ++ch) {
+        uint32_t o[32];
+        tmem_ld32(tO + ch * 32, o);
+        tmem_wait_ld();
+        reg_fence32(o);
+        const uint32_t dims = had_nan ? note[ch] : 0;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          o[e] = (dims >> e) & 1 ? 0x7fffffffu : __float_as_uint(__uint_as_float(o[e]) * mul);
+        if (valid && whole) {
+          uint4* dst = reinterpret_cast<uint4*>(a.o + out * D + ch * 32);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              pk[k] = pack_bf16(__uint_as_float(o[8 * i + 2 * k]), __uint_as_float(o[8 * i + 2 * k + 1]));
+            dst[i] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
+        } else if (valid) {
+          float* dst = a.part + part * D + ch * 32;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st_global_v8(dst + 8 * i, o + 8 * i);
+        }
+        __syncwarp();
+      }
+      if (valid) {
+        if (whole) a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        else a.part_ml[part] = make_float2(m, l);
+      }
+      tc_fence_before();
+      warp_arrive(&c->seg_empty[s % kSegs]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the partial results of an item that lies in several blocks' shares,
+// in block order: a warp per row, D / 32 dims a lane.
+template <int D>
+__global__ void __launch_bounds__(256) cache8_wide_join_kernel(CacheAttnArgs a, int blocks) {
+  constexpr int kDims = D / 32;
+  wait_for_stream();
+  const int lane = threadIdx.x & 31, warps = gridDim.x * 8;
+  for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < blocks * kC8WideRows; i += warps) {
+    const int block = i / kC8WideRows, in = i % kC8WideRows;
+    const int4 j = a.joins[block];
+    if (j.x < 0) continue;
+    const int hk = j.y / a.row_blocks, row = (j.y - hk * a.row_blocks) * kC8WideRows + in;
+    const int ql = min(a.q_lens ? a.q_lens[j.x] : a.T, a.T);
+    if (row >= ql * a.heads) continue;
+    const int parts = j.z - block + 2;
+    auto at = [&](int k) {
+      return (size_t)(k == 0 ? j.w : 2 * (block + k - 1)) * kC8WideRows + in;
+    };
+    float mx = kNoMax;
+    for (int k = lane; k < parts; k += 32) mx = fmaxf(mx, a.part_ml[at(k)].x);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+    float acc[kDims], sum = 0.f;
+#pragma unroll
+    for (int d = 0; d < kDims; ++d) acc[d] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+      const float2 ml = a.part_ml[at(k)];
+      const float f = ex2(ml.x - mx);
+      sum += f * ml.y;
+      const float* o = a.part + at(k) * D + lane * kDims;
+      if constexpr (kDims == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(o);
+        acc[0] += f * v.x, acc[1] += f * v.y, acc[2] += f * v.z, acc[3] += f * v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(o);
+        acc[0] += f * v.x, acc[1] += f * v.y;
+      }
+    }
+    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+    const size_t out = row_at(a, j.x, hk, row);
+    __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.o + out * D) + lane * (kDims / 2);
+#pragma unroll
+    for (int d = 0; d < kDims; d += 2) dst[d / 2] = __floats2bfloat162_rn(acc[d] * inv, acc[d + 1] * inv);
+    if (lane == 0) a.lse[out] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+  }
+}
+
+template <int D>
+cudaError_t run(const CacheAttnArgs& a, int sm_count, cudaStream_t stream) {
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(cache8_wide_kernel<D>), Wide<D>::kSmem, done);
+  if (e != cudaSuccess) return e;
+  const int blocks = sm_count < kC8WideBlocks ? sm_count : kC8WideBlocks;
+  e = launch_overlapped(cache8_wide_kernel<D>, dim3(blocks), dim3(kThreads), Wide<D>::kSmem, stream, a);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(cache8_wide_join_kernel<D>, dim3(4 * blocks), dim3(256), 0, stream, a, blocks);
+}
+
+}  // namespace
+
+cudaError_t launch_cache8_wide(const CacheAttnArgs& a, int d, int sm_count, cudaStream_t stream) {
+  return d == 128 ? run<128>(a, sm_count, stream) : run<64>(a, sm_count, stream);
+}
+
+}  // namespace fa

@@ -101,7 +101,9 @@ __device__ __forceinline__ void launch_dependents() {
 // requests (read by plain loads: the kernel before may have written them).
 template <int kRows>
 __device__ __forceinline__ c4::Call call_of(const CacheAttnArgs& a) {
-  return {a.B, a.Hkv, a.T, a.window, a.heads, kRows, a.row_blocks, a.M << a.shift, a.by_heads};
+  c4::Call c = {a.B, a.Hkv, a.T, a.window, a.heads, kRows, a.row_blocks, a.M << a.shift, a.by_heads};
+  c.most_rows = a.most_rows;
+  return c;
 }
 // Row `row` of a request and key/value head in q, o and lse.
 __device__ __forceinline__ size_t row_at(const CacheAttnArgs& a, int b, int hk, int row) {

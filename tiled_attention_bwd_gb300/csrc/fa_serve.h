@@ -121,11 +121,14 @@ struct CacheAttnArgs {
   int4* joins;              // [kC4MaxBlocks]
   float* part;              // [2 kC4MaxBlocks][item rows][d]
   float2* part_ml;          // [2 kC4MaxBlocks][item rows]
+  uint32_t* nan_rows;       // [kC8WideBlocks][kC8WideRows][4] (wide kernel)
   int B, Hkv, T, M, pages;
   int heads;                // H / Hkv, of one key/value head
   FastDiv by_heads;
   int rows;                 // heads * T: a request's most
+  int item_rows;            // of an item
   int row_blocks;
+  int least_rows, most_rows;  // live rows of the requests that the kernel takes
   int shift;                // log2 of the page size
   int window;               // < 0: none
   float scale_log2;         // scale * k_scale * log2(e)
@@ -134,12 +137,18 @@ struct CacheAttnArgs {
   uint64_t timeout_ns;
   int hook;                 // 1: run the failure-path test hook instantiation
 };
-// Query rows of one work item: a multiple of 8 up to 40.
+// Query rows of one work item for requests of `rows`: a multiple of 8 up to 40.
 int cache4_attn_rows(int rows, int d);
 cudaError_t launch_cache4_attn(const CacheAttnArgs& a, int d, int sm_count,
                                cudaStream_t stream);
 int cache8_attn_rows(int rows, int d);
 cudaError_t launch_cache8_attn(const CacheAttnArgs& a, int d, int sm_count,
+                               cudaStream_t stream);
+// The same for requests with many rows, more than kC8NarrowRows.
+constexpr int kC8NarrowRows = 32;
+constexpr int kC8WideRows = 256;    // of an item
+constexpr int kC8WideBlocks = 160;
+cudaError_t launch_cache8_wide(const CacheAttnArgs& a, int d, int sm_count,
                                cudaStream_t stream);
 // The site whose waits expire (0: none), on the current device.  Synchronous;
 // call only while no kernel of the library runs.

@@ -207,14 +207,21 @@ fa_status check_cache(int pages, int Hkv, int page, int d, int* shift) {
   return FA_OK;
 }
 
-// A format's bytes of a group, and its attention's rows of an item and launch.
+// A format's bytes of a group, and its attention's rows of an item and launch;
+// for requests of more than narrow_rows rows, another kernel of wide_rows.
+using AttnLaunch = cudaError_t (*)(const fa::CacheAttnArgs& a, int d, int sm_count,
+                                   cudaStream_t stream);
 struct Format {
   int (*group)(int d);
   int (*rows)(int rows, int d);
-  cudaError_t (*attn)(const fa::CacheAttnArgs& a, int d, int sm_count, cudaStream_t stream);
+  AttnLaunch attn;
+  int narrow_rows = INT_MAX, wide_rows = 0, wide_blocks = 0;
+  AttnLaunch wide = nullptr;
 };
 constexpr Format kCache4 = {fa::group_bytes, fa::cache4_attn_rows, fa::launch_cache4_attn};
-constexpr Format kCache8 = {fa::group8_bytes, fa::cache8_attn_rows, fa::launch_cache8_attn};
+constexpr Format kCache8 = {fa::group8_bytes,      fa::cache8_attn_rows, fa::launch_cache8_attn,
+                            fa::kC8NarrowRows,     fa::kC8WideRows,      fa::kC8WideBlocks,
+                            fa::launch_cache8_wide};
 
 long long cache_bytes(const Format& f, int pages, int Hkv, int page, int d) {
   return (long long)pages * Hkv * (page / fa::kGroup) * f.group(d);
@@ -335,13 +342,44 @@ fa_status norm_rope_bwd(const void* qkv, long long stride_b, long long stride_n,
 }
 
 // Attention over a cache in either format.
+// The workspace of a kernel with items of `rows` rows, `blocks` blocks at
+// most, from `ws` on; returns its end.
+uintptr_t lay_out(fa::CacheAttnArgs& a, uintptr_t ws, int blocks, int rows, int d, bool notes) {
+  a.joins = reinterpret_cast<int4*>(ws);
+  ws += align_up(blocks * sizeof(int4));
+  a.part = reinterpret_cast<float*>(ws);
+  ws += align_up((size_t)blocks * 2 * rows * d * sizeof(float));
+  a.part_ml = reinterpret_cast<float2*>(ws);
+  ws += align_up((size_t)blocks * 2 * rows * sizeof(float2));
+  a.nan_rows = reinterpret_cast<uint32_t*>(ws);
+  if (notes) ws += (size_t)blocks * rows * 4 * sizeof(uint32_t);
+  a.row_blocks = (int)((a.rows + (long long)rows - 1) / rows);
+  return ws;
+}
+// The kernels of a call of requests with up to `rows` rows, with their places
+// in the workspace; returns its end.  (Requests of many rows have items of one
+// token's heads in the first kernel: most of what it gets is single tokens.)
+uintptr_t lay_out(const Format& f, int rows, int heads, int d, uintptr_t ws,
+                  fa::CacheAttnArgs& narrow, fa::CacheAttnArgs& wide, bool* is_wide) {
+  *is_wide = rows > f.narrow_rows;
+  narrow.rows = *is_wide ? f.narrow_rows : rows;
+  narrow.least_rows = 0;
+  narrow.most_rows = f.narrow_rows;
+  narrow.item_rows = f.rows(*is_wide && heads < f.narrow_rows ? heads : narrow.rows, d);
+  ws = lay_out(narrow, ws, fa::kC4MaxBlocks, narrow.item_rows, d, false);
+  if (!*is_wide) return ws;
+  wide.rows = rows;
+  wide.least_rows = f.narrow_rows + 1;
+  wide.most_rows = INT_MAX;
+  return lay_out(wide, ws, f.wide_blocks, f.wide_rows, d, true);
+}
+
 size_t attn_workspace_size(const Format& f, int B, int H, int Hkv, int T, int d) {
   if (head_dim(d) != FA_OK || B <= 0 || H <= 0 || T <= 0 || Hkv <= 0 || H % Hkv != 0) return 0;
   if ((long long)B * H * T > INT_MAX) return 0;
-  const int rows = f.rows(H / Hkv * T, d);
-  return align_up(fa::kC4MaxBlocks * sizeof(int4)) +
-         align_up((size_t)fa::kC4MaxBlocks * 2 * rows * d * sizeof(float)) +
-         (size_t)fa::kC4MaxBlocks * 2 * rows * sizeof(float2);
+  fa::CacheAttnArgs narrow = {}, wide = {};
+  bool is_wide;
+  return lay_out(f, H / Hkv * T, H / Hkv, d, 0, narrow, wide, &is_wide);
 }
 
 fa_status cache_attn(const Format& f, const void* q, const void* cache, const int* block_table,
@@ -392,10 +430,6 @@ fa_status cache_attn(const Format& f, const void* q, const void* cache, const in
   a.q_lens = q_lens;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
-  char* ws = static_cast<char*>(workspace);
-  a.joins = reinterpret_cast<int4*>(ws);
-  ws += align_up(fa::kC4MaxBlocks * sizeof(int4));
-  a.part = reinterpret_cast<float*>(ws);
   a.B = B;
   a.Hkv = Hkv;
   a.T = T;
@@ -403,11 +437,6 @@ fa_status cache_attn(const Format& f, const void* q, const void* cache, const in
   a.pages = pages;
   a.heads = H / Hkv;
   a.by_heads = fa::FastDiv::of(a.heads);
-  a.rows = a.heads * T;
-  const int rows = f.rows(a.rows, d);
-  ws += align_up((size_t)fa::kC4MaxBlocks * 2 * rows * d * sizeof(float));
-  a.part_ml = reinterpret_cast<float2*>(ws);
-  a.row_blocks = (a.rows + rows - 1) / rows;
   a.shift = shift;
   // A window of the whole table hides nothing.
   a.window = window < 0 || (long long)window >= ((long long)max_blocks << shift) ? -1 : window;
@@ -416,7 +445,16 @@ fa_status cache_attn(const Format& f, const void* q, const void* cache, const in
   a.st = dev.st;
   a.timeout_ns = dev.timeout_ns;
   a.hook = dev.hook;
-  return launched(f.attn(a, d, dev.sm_count, static_cast<cudaStream_t>(stream)));
+  fa::CacheAttnArgs wide = a;
+  bool is_wide;
+  lay_out(f, a.heads * T, a.heads, d, reinterpret_cast<uintptr_t>(workspace), a, wide,
+          &is_wide);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // (Without lengths every request has as many rows.)
+  cudaError_t e = cudaSuccess;
+  if (!is_wide || q_lens) e = f.attn(a, d, dev.sm_count, st);
+  if (is_wide && e == cudaSuccess) e = f.wide(wide, d, dev.sm_count, st);
+  return launched(e);
 }
 
 }  // namespace
