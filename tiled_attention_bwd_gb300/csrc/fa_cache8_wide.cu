@@ -40,11 +40,11 @@ constexpr int kThreads = 512;
 constexpr int kMakeWarp = 8, kLoadWarp = 12, kMmaWarp = 13;
 // Registers: launched at 128 a thread; the four warpgroups' shares add up to
 // 512 * 128.
-constexpr int kSoftmaxRegs = 192, kMakeRegs = 80, kCtrlRegs = 48;
+constexpr int kSoftmaxRegs = 200, kMakeRegs = 64, kCtrlRegs = 48;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kMakeRegs + 128 * kCtrlRegs <= kThreads * 128);
 constexpr float kNoMax = -1e30f;  // m of a row that has seen no key
 constexpr float kUp = 8.0f;       // P carries 2^kUp
-constexpr float kSlack = 6.0f;    // growth of m that is left standing
+constexpr float kSlack = 7.0f;    // growth of m that is left standing (f16 ends at 2^16)
 constexpr int kUnitGroups = kC4Unit / kGroup;
 constexpr int kSegs = 4, kInfos = 4;
 
@@ -59,14 +59,14 @@ struct Seg {
   int b, hk, row0, live;   // live: rows of the item, from row0 on
   int pos0;                // position of the request's first new token
   int tok0, units;         // units < 0: no more segments
+  int key_end;             // behind the last key that the item needs
   int plain_lo, plain_hi;  // tokens within are seen by every live row
   int whole, part;         // part: place of the partial results
 };
-// What the softmax needs of a group: factor of the keys, exponent of the
-// values, 2^-that, and whether some value is NaN (not 0).
+// What the softmax needs of a group: factor of the keys and exponent of the
+// values (read together), the exponent again and 2^-that.
 struct alignas(16) Info {
-  float k, log_v, inv_v;
-  int nan;
+  float2 key, value;
 };
 
 template <int D>
@@ -84,9 +84,13 @@ struct Wide {
     uint64_t q_full[2], s_full[2], p_full[2], o_done[2], mma_done;
     uint64_t seg_full[kSegs], seg_empty[kSegs], info_full[kInfos];
     Info info[kInfos][kUnitGroups];
-    int there[kInfos];               // bit g: group g of the unit is there
+    uint8_t nan[kInfos][kUnitGroups];  // 1: some value is NaN (in edge units)
+    int edge[kInfos];                // 0: every live row sees all of the unit; else
+                                     // 256 + (bit g: group g is there)
     int raw_there[kRawStages];
     Seg seg[kSegs];
+    c4::Cursor at;  // of the loading warp
+    int into;
     uint32_t abort, tmem;
   };
   static constexpr int kSmem = kCtrlOff + (int)sizeof(Ctrl) + 1024;  // + alignment
@@ -96,19 +100,36 @@ static_assert(Wide<128>::kSmem <= 232448 && Wide<64>::kSmem <= 232448);
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
   return idesc_bf16(M, N, false, b_mn) & ~((1u << 7) | (1u << 10));  // A and B: f16
 }
+// The operands' descriptors are kept as their low halves, where the address
+// and one stride stand, and put together at each instruction: whole ones of
+// every step, which the compiler would keep, take more registers than the
+// issuing warp has.  (Stride and swizzle in the high half are the same for all.)
+__device__ __forceinline__ uint32_t desc_low(const void* tile, uint32_t lbo) {
+  return (uint32_t)sdesc_sw128(smem_addr(tile), lbo, 1024);
+}
+__device__ __forceinline__ uint64_t desc_of(uint32_t low) {
+  return sdesc_sw128(0, 0, 1024) | low;
+}
+// `low` as a value that the compiler does not compute ahead with.
+__device__ __forceinline__ uint32_t opaque(uint32_t low) {
+  asm volatile("" : "+r"(low));
+  return low;
+}
 template <int D>
-__device__ __forceinline__ void issue_qk(uint32_t s, uint64_t q, uint64_t k) {
+__device__ __forceinline__ void issue_qk(uint32_t s, uint32_t q, uint32_t k) {
+  q = opaque(q), k = opaque(k);
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) {
-    const uint32_t off = (i >> 2) * kSubTileBytes + (i & 3) * 32;
-    mma_ss(s, sdesc_adv(q, off), sdesc_adv(k, off), idesc_f16(128, 128, false), i > 0);
+    const uint32_t off = ((i >> 2) * kSubTileBytes + (i & 3) * 32) >> 4;
+    mma_ss(s, desc_of(q + off), desc_of(k + off), idesc_f16(128, 128, false), i > 0);
   }
 }
 template <int D>
-__device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint64_t v, bool accumulate) {
+__device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint32_t v, bool accumulate) {
+  v = opaque(v), p = opaque(p);
 #pragma unroll
   for (int i = 0; i < kC4Unit / 16; ++i)
-    mma_ts(o, p + i * 8, sdesc_adv(v, i * 2048), idesc_f16(128, D, true), accumulate || i > 0);
+    mma_ts(o, p + i * 8, desc_of(v + (i * 2048 >> 4)), idesc_f16(128, D, true), accumulate || i > 0);
 }
 
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
@@ -147,29 +168,32 @@ __device__ __forceinline__ void make_keys(uint8_t* tile, const uint8_t* grp, int
       *chunk_of(tile, row, at + (odd ? 0 : 32)) = make8(odd ? u.x : u.z, odd ? u.y : u.w);
     }
 }
-// One group's values.  kEdge: NaN as zero.
-template <int D, bool kEdge>
+// One group's values; in an edge unit NaN as zero.
+template <int D>
 __device__ __forceinline__ void make_values(uint8_t* tile, const uint8_t* grp, int row0, bool there,
-                                            int lane) {
+                                            bool edge, int lane) {
   const int g = lane >> 2, t = lane & 3;
+  uint4 u[D / 64][2];
 #pragma unroll
   for (int j = 0; j < D / 64; ++j)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (there) u = *reinterpret_cast<const uint4*>(grp + v8_piece(D, j, h, lane));
-      if (kEdge) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+    for (int h = 0; h < 2; ++h)
+      u[j][h] = there ? *reinterpret_cast<const uint4*>(grp + v8_piece(D, j, h, lane)) : make_uint4(0, 0, 0, 0);
+  if (__builtin_expect(edge, 0)) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(u);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] &= ~__vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-      }
+    for (int i = 0; i < D / 8; ++i) w[i] &= ~__vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+  }
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const uint32_t sel = e ? 0x7531 : 0x6420;  // one token's codes of a pair
         *chunk_of(tile, row0 + 8 * h + 2 * t + e, 64 * j + 8 * g) =
-            make8(__byte_perm(u.x, u.y, sel), __byte_perm(u.z, u.w, sel));
+            make8(__byte_perm(u[j][h].x, u[j][h].y, sel), __byte_perm(u[j][h].z, u[j][h].w, sel));
       }
-    }
 }
 // Whether a group has a NaN value (the same on every lane).
 template <int D>
@@ -237,8 +261,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
     return c4::request_of(call, a.seq_lens[b], a.q_lens ? a.q_lens[b] : a.T);
   };
   long long* scan = reinterpret_cast<long long*>(smem);  // (before the tiles are in use)
-  c4::Cursor* start = reinterpret_cast<c4::Cursor*>(smem + 256);
-  int* into = reinterpret_cast<int*>(smem + 512);
   const int pairs = a.B * a.row_blocks, per = (pairs - 1) / kThreads + 1;
   const int p0 = (int)min((long long)pairs, (long long)tid * per), p1 = p0 + min(pairs - p0, per);
   const long long mine = c4::cost_of(call, read, p0, p1);
@@ -262,64 +284,63 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
   bool work = (int)blockIdx.x < shares.blocks;  // of the block
   const long long u0 = work ? shares.first(blockIdx.x) : 0;
   if (work && u0 >= before * a.Hkv && u0 < upto * a.Hkv)
-    *into = start->seek(call, read, p0, u0 - before * a.Hkv, (int)(shares.first(blockIdx.x + 1) - u0));
-  __syncthreads();
-  c4::Cursor at;
-  if (work) at = *start;
-  if (work && at.end == at.unit) work = false;  // a share of nothing but an item's cost
+    c->into = c->at.seek(call, read, p0, u0 - before * a.Hkv, (int)(shares.first(blockIdx.x + 1) - u0));
+  __syncthreads();  // (the tiles are free, too)
+  if (work && c->at.end == c->at.unit) work = false;  // a share of nothing but an item's cost
   if (tid == 0) {
     int4 j = make_int4(-1, 0, 0, 0);
     int last, first_part;
-    if (work && c4::join_of(shares, at, blockIdx.x, u0, *into, &last, &first_part))
-      j = make_int4(at.b, at.hk * a.row_blocks + at.rb, last, first_part);
+    if (work && c4::join_of(shares, c->at, blockIdx.x, u0, c->into, &last, &first_part))
+      j = make_int4(c->at.b, c->at.hk * a.row_blocks + c->at.rb, last, first_part);
     a.joins[blockIdx.x] = j;
   }
   const uint32_t tmem = c->tmem;
   const WaitCtl wc = {a.st, &c->abort, a.timeout_ns};
-  __syncthreads();  // the start is read: Q's tiles may be written
+  __syncthreads();  // every thread has seen the cursor
 
   if (warp >= kLoadWarp) {
     reg_dealloc<kCtrlRegs>();
     if (warp == kLoadWarp && work) {
       // ------------------------------------------------- segments and copies
       bool ok = true;
-      int stage = 0, last_par[L::kRawStages];
+      int stage = 0, used = 0;  // used: stages that copies went into
       uint32_t phase = 0;
-#pragma unroll
-      for (int i = 0; i < L::kRawStages; ++i) last_par[i] = -1;
       for (int s = 0; ok; ++s) {
-        const bool more = s == 0 || at.next(call, read);
-        ok = __all_sync(0xffffffffu, wait_bar<true>(&c->seg_empty[s % kSegs], ((s / kSegs) & 1) ^ 1, wc, kWLoadSeg));
+        Seg& seg = c->seg[s % kSegs];
+        ok = wait_bar_warp<true>(&c->seg_empty[s % kSegs], ((s / kSegs) & 1) ^ 1, wc, kWLoadSeg);
         if (!ok) break;
-        const int units = more ? at.end - at.unit : -1;
-        const int tok0 = more ? at.k.lo + at.unit * kC4Unit : 0;
-        if (lane == 0) {
-          Seg g = {};
-          g.units = units;
-          if (more) {
-            g.b = at.b, g.hk = at.hk, g.row0 = at.rb * kC8WideRows;
-            g.live = min(kC8WideRows, at.r.ql * a.heads - g.row0);
-            g.pos0 = at.r.len - at.r.ql;
-            g.tok0 = tok0;
-            g.plain_hi = at.k.first + 1;
-            g.plain_lo = a.window < 0 ? 0 : at.k.hi - 1 - a.window;
-            g.whole = at.unit == 0 && at.end == at.k.units;
-            g.part = 2 * blockIdx.x + (s == 0 ? 0 : 1);
+        if (lane == 0) {  // (the cursor stays in shared memory: registers are scarce)
+          if (s > 0 && !c->at.next(call, read)) {
+            seg.units = -1;
+          } else {
+            const c4::Cursor& at = c->at;
+            seg.b = at.b, seg.hk = at.hk, seg.row0 = at.rb * kC8WideRows;
+            seg.live = min(kC8WideRows, at.r.ql * a.heads - seg.row0);
+            seg.pos0 = at.r.len - at.r.ql;
+            seg.tok0 = at.k.lo + at.unit * kC4Unit;
+            seg.units = at.end - at.unit;
+            seg.key_end = at.k.hi;
+            seg.plain_hi = at.k.first + 1;
+            seg.plain_lo = a.window < 0 ? 0 : at.k.hi - 1 - a.window;
+            seg.whole = at.unit == 0 && at.end == at.k.units;
+            seg.part = 2 * blockIdx.x + (s == 0 ? 0 : 1);
           }
-          c->seg[s % kSegs] = g;
           mbar_arrive(&c->seg_full[s % kSegs]);
         }
-        if (!more) break;
+        __syncwarp();
+        const int units = seg.units;
+        if (units < 0) break;
         // Each lane looks up one group of the next four units.
         for (int base = 0; base < units && ok; base += 4) {
-          const int u = base + lane / kUnitGroups, tok = tok0 + u * kC4Unit + lane % kUnitGroups * kGroup;
+          const int u = base + lane / kUnitGroups;
+          const int tok = seg.tok0 + u * kC4Unit + lane % kUnitGroups * kGroup;
           const uint8_t* src = nullptr;
-          if (u < units && tok < at.k.hi) src = group_at(a, at.b, at.hk, tok, group8_bytes(D));
+          if (u < units && tok < seg.key_end) src = group_at(a, seg.b, seg.hk, tok, group8_bytes(D));
           const uint32_t have = __ballot_sync(0xffffffffu, src != nullptr);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (base + q >= units || !ok) break;
-            ok = __all_sync(0xffffffffu, wait_bar<true>(&c->raw_empty[stage], phase ^ 1, wc, kWLoadRaw));
+          const int n = min(4, units - base);
+#pragma unroll 1
+          for (int q = 0; q < n; ++q) {
+            ok = wait_bar_warp<true>(&c->raw_empty[stage], phase ^ 1, wc, kWLoadRaw);
             if (!ok) break;
             const int mask = (have >> (q * kUnitGroups)) & 0xff;
             if (lane == 0) {
@@ -331,25 +352,25 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
             if (lane / kUnitGroups == q && src)
               bulk_load(smem + L::kRawOff + stage * L::kRawBytes + lane % kUnitGroups * group8_bytes(D), src,
                         group8_bytes(D), &c->raw_full[stage]);
-#pragma unroll
-            for (int i = 0; i < L::kRawStages; ++i)
-              if (i == stage) last_par[i] = (int)phase;
+            used |= 1 << stage;
             if (++stage == L::kRawStages) stage = 0, phase ^= 1;
           }
         }
       }
       // The copies land before the block leaves, whether it stops or not.
-#pragma unroll
+      // (A stage's last phase is this one before the ring's present stage, the
+      // one before from there on.)
+#pragma unroll 1
       for (int i = 0; i < L::kRawStages; ++i)
-        if (last_par[i] >= 0) drain_bar<true>(&c->raw_full[i], (uint32_t)last_par[i], a.timeout_ns);
+        if ((used >> i) & 1) drain_bar<true>(&c->raw_full[i], i < stage ? phase : phase ^ 1, a.timeout_ns);
       __syncwarp();
     } else if (warp == kMmaWarp && lane == 0 && work) {
       // --------------------------------------------------------- MMA issuer
-      const uint64_t q_desc = sdesc_sw128(smem_addr(smem), 16, 1024);
-      const uint64_t k_desc = sdesc_sw128(smem_addr(smem + L::kRingOff), 16, 1024);
-      const uint64_t v_desc = sdesc_sw128(smem_addr(smem + L::kRingOff), kSubTileBytes, 1024);
+      // Q and K: rows of 128 bytes along the dims; V: 64-dim columns of keys.
+      const uint32_t q_desc = desc_low(smem, 16), k_desc = desc_low(smem + L::kRingOff, 16);
+      const uint32_t v_desc = desc_low(smem + L::kRingOff, kSubTileBytes);
       int stage = 0;
-      uint32_t phase = 0, q_cnt[2] = {0, 0}, p_cnt[2] = {0, 0};
+      uint32_t phase = 0, q_par = 0, p_par = 0;  // bit t: of tile t
       bool ok = true;
       auto next_tile = [&](int& st) {
         st = stage;
@@ -359,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
         return r;
       };
       auto qk = [&](int t, int st) {
-        issue_qk<D>(tmem + t * 128, sdesc_adv(q_desc, t * L::kTileBytes), sdesc_adv(k_desc, st * L::kTileBytes));
+        issue_qk<D>(tmem + t * 128, q_desc + (t * L::kTileBytes >> 4), k_desc + (st * L::kTileBytes >> 4));
         mma_commit(&c->s_full[t]);
       };
       for (int s = 0; ok; ++s) {
@@ -370,22 +391,25 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
         mbar_arrive(&c->seg_empty[s % kSegs]);
         if (units < 0) break;
         int kst = 0, vst = 0;
-        ok = wait_bar<true>(&c->q_full[0], q_cnt[0]++ & 1, wc, kWMmaQ) && next_tile(kst);
+        ok = wait_bar<true>(&c->q_full[0], q_par & 1, wc, kWMmaQ) && next_tile(kst);
         if (!ok) break;
+        q_par ^= 1;
         qk(0, kst);
         if (two) {
-          ok = wait_bar<true>(&c->q_full[1], q_cnt[1]++ & 1, wc, kWMmaQ);
+          ok = wait_bar<true>(&c->q_full[1], q_par >> 1, wc, kWMmaQ);
           if (!ok) break;
+          q_par ^= 2;
           tc_fence_after();
           qk(1, kst);
         }
         mma_commit(&c->kv_empty[kst]);
         for (int j = 0; j < units && ok; ++j) {
           const bool last = j == units - 1;
-          ok = next_tile(vst) && wait_bar<true>(&c->p_full[0], p_cnt[0]++ & 1, wc, kWMmaP);
+          ok = next_tile(vst) && wait_bar<true>(&c->p_full[0], p_par & 1, wc, kWMmaP);
           if (!ok) break;
+          p_par ^= 1;
           tc_fence_after();
-          const uint64_t vd = sdesc_adv(v_desc, vst * L::kTileBytes);
+          const uint32_t vd = v_desc + (vst * L::kTileBytes >> 4);
           issue_pv<D>(tmem + 256, tmem, vd, j > 0);
           if (!last) {
             ok = next_tile(kst);
@@ -395,8 +419,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
             mma_commit(&c->o_done[0]);
           }
           if (two) {
-            ok = wait_bar<true>(&c->p_full[1], p_cnt[1]++ & 1, wc, kWMmaP);
+            ok = wait_bar<true>(&c->p_full[1], p_par >> 1, wc, kWMmaP);
             if (!ok) break;
+            p_par ^= 2;
             tc_fence_after();
             issue_pv<D>(tmem + 256 + D, tmem + 128, vd, j > 0);
           }
@@ -440,9 +465,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
         const uint8_t* base = smem + L::kRawOff + raw * L::kRawBytes;
         uint8_t* tile = smem + L::kRingOff + stage * L::kTileBytes;
         Info* info = c->info[u % kInfos];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int g = 2 * w + i;
+        // (Loops, not unrolled: the roles' code shares the instruction cache.)
+#pragma unroll 1
+        for (int g = 2 * w; g < 2 * w + 2; ++g) {
           const uint8_t* grp = base + g * group8_bytes(D);
           const bool have = (there >> g) & 1;
           make_keys<D>(tile, grp, g * kGroup, have, lane);
@@ -450,23 +475,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
           if (lane == 0) {
             const uint32_t two = *reinterpret_cast<const uint16_t*>(grp + 32 * D);
             const int ve = exp8(two >> 8);
-            info[g] = {pow2(exp8(two & 0xff)), (float)ve, pow2(-ve), nan};
+            info[g] = {make_float2(pow2(exp8(two & 0xff)), (float)ve), make_float2((float)ve, pow2(-ve))};
+            c->nan[u % kInfos][g] = nan;
           }
         }
-        if (w == 0 && lane == 0) c->there[u % kInfos] = there;
+        if (w == 0 && lane == 0) c->edge[u % kInfos] = edge ? 256 + there : 0;
         warp_arrive(&c->info_full[u % kInfos]);
         tile_done();
         ok = tile_free();
         if (!ok) break;
         tile = smem + L::kRingOff + stage * L::kTileBytes;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int g = 2 * w + i;
-          const uint8_t* grp = base + g * group8_bytes(D);
-          const bool have = (there >> g) & 1;
-          if (edge) make_values<D, true>(tile, grp, g * kGroup, have, lane);
-          else make_values<D, false>(tile, grp, g * kGroup, have, lane);
-        }
+#pragma unroll 1
+        for (int g = 2 * w; g < 2 * w + 2; ++g)
+          make_values<D>(tile, base + g * group8_bytes(D), g * kGroup, (there >> g) & 1, edge, lane);
         tile_done();
         warp_arrive(&c->raw_empty[raw]);
         if (++raw == L::kRawStages) raw = 0, raw_phase ^= 1;
@@ -535,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
         ++s_cnt;
         if (!ok) break;
         tc_fence_after();
-        const float4* info = reinterpret_cast<const float4*>(c->info[u % kInfos]);
+        const Info* info = c->info[u % kInfos];
         uint32_t x[128];
         tmem_ld32(tS, x);
         tmem_ld32(tS + 32, x + 32);
@@ -546,25 +567,31 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
         reg_fence32(x + 32);
         reg_fence32(x + 64);
         reg_fence32(x + 96);
-        const int tok = seg.tok0 + j * kC4Unit, there = c->there[u % kInfos];
-        if (there != 0xff || tok < seg.plain_lo || tok + kC4Unit > seg.plain_hi) {
-          const int hi = pos - tok, lo = a.window < 0 ? -1 : pos - a.window - tok;
+        const int edge = c->edge[u % kInfos];
+        if (__builtin_expect(edge != 0, 0)) {
+          const int tok = seg.tok0 + j * kC4Unit;
+          const int hi = pos - tok, lo = a.window < 0 ? 0 : max(pos - a.window - tok, 0);
 #pragma unroll
-          for (int e = 0; e < 128; ++e)
-            if (e > hi || e < lo || !((there >> (e / kGroup)) & 1)) x[e] = __float_as_uint(-INFINITY);
+          for (int w = 0; w < 4; ++w) {  // 32 keys, those that the row sees as bits
+            const int n = min(max(hi + 1 - 32 * w, 0), 32), z = min(max(lo - 32 * w, 0), 32);
+            uint32_t see = (uint32_t)((1ull << n) - 1) & ~(uint32_t)((1ull << z) - 1);
+            if (!((edge >> (2 * w)) & 1)) see &= 0xffff0000u;
+            if (!((edge >> (2 * w + 1)) & 1)) see &= 0xffffu;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((see >> e) & 1)) x[32 * w + e] = __float_as_uint(-INFINITY);
+          }
           // Dims of NaN values that the row sees, into the workspace.
-          bool nan = false;
-#pragma unroll
-          for (int g = 0; g < kUnitGroups; ++g) nan |= __float_as_int(info[g].w) != 0;
-          if (nan) {
+          const uint8_t* nan = c->nan[u % kInfos];
+          if (*reinterpret_cast<const unsigned long long*>(nan)) {
             uint32_t* note = a.nan_rows + ((size_t)blockIdx.x * kC8WideRows + t * 128 + in_tile) * 4;
 #pragma unroll 1
             for (int d0 = 0; d0 < D; d0 += 32) {
               uint32_t dims = had_nan ? note[d0 / 32] : 0;
 #pragma unroll 1
-              for (int e = max(lo, 0); e <= min(hi, 127); ++e) {
+              for (int e = lo; e <= min(hi, 127); ++e) {
                 const uint8_t* grp = nullptr;
-                if (__float_as_int(info[e / kGroup].w))
+                if (nan[e / kGroup])
                   grp = group_at(a, seg.b, seg.hk, tok + e, group8_bytes(D));
                 if (!grp) continue;
 #pragma unroll 1
@@ -574,19 +601,21 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
               note[d0 / 32] = dims;
             }
             had_nan = true;
-            __syncwarp();
           }
+          __syncwarp();
         }
         // Largest s + e_v, in powers of two.
-        float top = -INFINITY;
+        float top = -INFINITY, w[kUnitGroups];
 #pragma unroll
         for (int g = 0; g < kUnitGroups; ++g) {
-          const float4 f = info[g];
+          const float2 f = info[g].key;
+          // (Not zero: a masked score, minus infinity, is multiplied with it.)
+          w[g] = fmaxf(cr * f.x, 1.2e-38f);
           float mg = fmaxf(__uint_as_float(x[16 * g]), __uint_as_float(x[16 * g + 1]));
 #pragma unroll
           for (int e = 16 * g + 2; e < 16 * g + 16; e += 2)
             mg = max3(mg, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-          top = fmaxf(top, fmaf(mg, fmaxf(cr * f.x, 1.2e-38f), f.y));
+          top = fmaxf(top, fmaf(mg, w[g], f.y));
         }
         const bool bump = top > m + kUp + kSlack;
         float alpha = 1.f;
@@ -597,8 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
         }
 #pragma unroll
         for (int g = 0; g < kUnitGroups; ++g) {
-          const float4 f = info[g];
-          const uint64_t w2 = bcast2(fmaxf(cr * f.x, 1.2e-38f)), c2 = bcast2(f.y - m);
+          const float2 f = info[g].value;
+          const uint64_t w2 = bcast2(w[g]), c2 = bcast2(f.x - m);
           float la[2] = {0.f, 0.f}, lb[2] = {0.f, 0.f};
 #pragma unroll
           for (int e = 16 * g; e < 16 * g + 16; e += 2) {
@@ -608,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
             add2_acc(la[(e >> 1) & 1], lb[(e >> 1) & 1], p0, p1);
             x[e / 2] = f16x2(p0, p1);
           }
-          l = fmaf((la[0] + lb[0]) + (la[1] + lb[1]), f.z, l);
+          l = fmaf((la[0] + lb[0]) + (la[1] + lb[1]), f.y, l);
         }
         tmem_st32(tS, x);
         tmem_st32(tS + 32, x + 32);
