@@ -28,6 +28,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "fa_cache4_work.h"
 #include "fa_cache8.cuh"
 #include "fa_common.cuh"
@@ -714,51 +716,86 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
   }
 }
 
-// Joins the partial results of an item that lies in several blocks' shares,
-// in block order: a warp per row, D / 32 dims a lane.
-template <int D>
-__global__ void __launch_bounds__(256) cache8_wide_join_kernel(CacheAttnArgs a, int blocks) {
+// Joins the partial results of an item that lies in several blocks' shares, in
+// block order.  A warp takes kRows rows, D / 32 dims a lane, and has the loads
+// of kParts parts on their way at once.  (One row and four parts at a time: 22
+// us for 152 joins of 256 rows.)
+template <int D, int kRows, int kParts>
+__device__ __forceinline__ void join_rows(const CacheAttnArgs& a, const int4& j, int block, int in0) {
   constexpr int kDims = D / 32;
-  wait_for_stream();
-  const int lane = threadIdx.x & 31, warps = gridDim.x * 8;
-  for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < blocks * kC8WideRows; i += warps) {
-    const int block = i / kC8WideRows, in = i % kC8WideRows;
-    const int4 j = a.joins[block];
-    if (j.x < 0) continue;
-    const int hk = j.y / a.row_blocks, row = (j.y - hk * a.row_blocks) * kC8WideRows + in;
-    const int ql = min(a.q_lens ? a.q_lens[j.x] : a.T, a.T);
-    if (row >= ql * a.heads) continue;
-    const int parts = j.z - block + 2;
-    auto at = [&](int k) {
-      return (size_t)(k == 0 ? j.w : 2 * (block + k - 1)) * kC8WideRows + in;
-    };
-    float mx = kNoMax;
-    for (int k = lane; k < parts; k += 32) mx = fmaxf(mx, a.part_ml[at(k)].x);
+  using Vec = std::conditional_t<D == 128, float4, float2>;
+  const int lane = threadIdx.x & 31, hk = j.y / a.row_blocks;
+  const int row0 = (j.y - hk * a.row_blocks) * kC8WideRows + in0;
+  const int live = min(a.q_lens ? a.q_lens[j.x] : a.T, a.T) * a.heads;
+  const int parts = j.z - block + 2;
+  auto at = [&](int k, int r) {
+    return (size_t)(k == 0 ? j.w : 2 * (block + k - 1)) * kC8WideRows + in0 + r;
+  };
+  float acc[kRows][kDims], sum[kRows], mx[kRows];
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-    float acc[kDims], sum = 0.f;
+  for (int r = 0; r < kRows; ++r) {
+    mx[r] = kNoMax, sum[r] = 0.f;
 #pragma unroll
-    for (int d = 0; d < kDims; ++d) acc[d] = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < parts; ++k) {
-      const float2 ml = a.part_ml[at(k)];
-      const float f = ex2(ml.x - mx);
-      sum += f * ml.y;
-      const float* o = a.part + at(k) * D + lane * kDims;
-      if constexpr (kDims == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(o);
-        acc[0] += f * v.x, acc[1] += f * v.y, acc[2] += f * v.z, acc[3] += f * v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(o);
-        acc[0] += f * v.x, acc[1] += f * v.y;
+    for (int d = 0; d < kDims; ++d) acc[r][d] = 0.f;
+  }
+#pragma unroll 1
+  for (int k0 = 0; k0 < parts; k0 += kParts) {
+    float2 ml[kRows][kParts];
+    Vec v[kRows][kParts];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) {
+        const bool there = k0 + k < parts && row0 + r < live;
+        ml[r][k] = there ? a.part_ml[at(k0 + k, r)] : make_float2(kNoMax, 0.f);
+        v[r][k] = there ? reinterpret_cast<const Vec*>(a.part + at(k0 + k, r) * D)[lane] : Vec{};
+      }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      float top = mx[r];
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) top = fmaxf(top, ml[r][k].x);
+      const float f0 = ex2(mx[r] - top);
+      mx[r] = top;
+      sum[r] *= f0;
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) acc[r][d] *= f0;
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) {
+        const float f = ex2(ml[r][k].x - top);
+        sum[r] += f * ml[r][k].y;
+        const float* o = reinterpret_cast<const float*>(&v[r][k]);
+#pragma unroll
+        for (int d = 0; d < kDims; ++d) acc[r][d] += f * o[d];
       }
     }
-    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-    const size_t out = row_at(a, j.x, hk, row);
+  }
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    if (row0 + r >= live) break;
+    const float inv = sum[r] > 0.f || sum[r] != sum[r] ? 1.f / sum[r] : 0.f;
+    const size_t out = row_at(a, j.x, hk, row0 + r);
     __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.o + out * D) + lane * (kDims / 2);
 #pragma unroll
-    for (int d = 0; d < kDims; d += 2) dst[d / 2] = __floats2bfloat162_rn(acc[d] * inv, acc[d + 1] * inv);
-    if (lane == 0) a.lse[out] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+    for (int d = 0; d < kDims; d += 2)
+      dst[d / 2] = __floats2bfloat162_rn(acc[r][d] * inv, acc[r][d + 1] * inv);
+    if (lane == 0) a.lse[out] = sum[r] == 0.f ? -INFINITY : (mx[r] + log2f(sum[r])) * kLn2;
+  }
+}
+
+constexpr int kJoinWarps = 8, kJoinRows = 2;
+constexpr int kJoinBlocks = kC8WideRows / (kJoinWarps * kJoinRows);  // per block of the attention
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) cache8_wide_join_kernel(CacheAttnArgs a) {
+  wait_for_stream();
+  const int4 j = a.joins[blockIdx.x];
+  if (j.x < 0) return;
+  const int in0 = (blockIdx.y * kJoinWarps + (threadIdx.x >> 5)) * kJoinRows;
+  if (j.z - (int)blockIdx.x + 2 <= 4) {
+    join_rows<D, kJoinRows, 4>(a, j, blockIdx.x, in0);
+  } else {  // a long history of few rows
+#pragma unroll 1
+    for (int r = 0; r < kJoinRows; ++r) join_rows<D, 1, 16>(a, j, blockIdx.x, in0 + r);
   }
 }
 
@@ -770,7 +807,7 @@ cudaError_t run(const CacheAttnArgs& a, int sm_count, cudaStream_t stream) {
   const int blocks = sm_count < kC8WideBlocks ? sm_count : kC8WideBlocks;
   e = launch_overlapped(cache8_wide_kernel<D>, dim3(blocks), dim3(kThreads), Wide<D>::kSmem, stream, a);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(cache8_wide_join_kernel<D>, dim3(4 * blocks), dim3(256), 0, stream, a, blocks);
+  return launch_overlapped(cache8_wide_join_kernel<D>, dim3(blocks, kJoinBlocks), dim3(256), 0, stream, a);
 }
 
 }  // namespace
