@@ -44,6 +44,8 @@ constexpr int kMakeWarp = 8, kLoadWarp = 12, kMmaWarp = 13;
 // 512 * 128.
 constexpr int kSoftmaxRegs = 200, kMakeRegs = 64, kCtrlRegs = 48;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kMakeRegs + 128 * kCtrlRegs <= kThreads * 128);
+// TMEM columns, of the 512 that the block takes: S of each tile, O of each.
+constexpr uint32_t kTmemS = 0, kTmemO = 256;
 constexpr float kNoMax = -1e30f;  // m of a row that has seen no key
 constexpr float kUp = 8.0f;       // P carries 2^kUp
 constexpr float kSlack = 7.0f;    // growth of m that is left standing (f16 ends at 2^16)
@@ -102,36 +104,52 @@ static_assert(Wide<128>::kSmem <= 232448 && Wide<64>::kSmem <= 232448);
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
   return idesc_bf16(M, N, false, b_mn) & ~((1u << 7) | (1u << 10));  // A and B: f16
 }
-// The operands' descriptors are kept as their low halves, where the address
-// and one stride stand, and put together at each instruction: whole ones of
-// every step, which the compiler would keep, take more registers than the
-// issuing warp has.  (Stride and swizzle in the high half are the same for all.)
-__device__ __forceinline__ uint32_t desc_low(const void* tile, uint32_t lbo) {
-  return (uint32_t)sdesc_sw128(smem_addr(tile), lbo, 1024);
+// The issuing warp runs its loop with all lanes and only the instructions
+// themselves are predicated: addresses and descriptors then are uniform values,
+// which tcgen05.mma takes from uniform registers.  (In a branch of one lane each
+// has to be moved there.)  TMEM
+// addresses are constants, all columns being this block's.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
 }
-__device__ __forceinline__ uint64_t desc_of(uint32_t low) {
-  return sdesc_sw128(0, 0, 1024) | low;
+__device__ __forceinline__ void mma_ss_if(uint32_t who, uint32_t d, uint64_t a, uint64_t b,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b),
+      "r"(idesc), "r"(accumulate), "r"(who)
+      : "memory");
 }
-// `low` as a value that the compiler does not compute ahead with.
-__device__ __forceinline__ uint32_t opaque(uint32_t low) {
-  asm volatile("" : "+r"(low));
-  return low;
+__device__ __forceinline__ void mma_ts_if(uint32_t who, uint32_t d, uint32_t a, uint64_t b,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b),
+      "r"(idesc), "r"(accumulate), "r"(who)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t who, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_addr(bar)), "r"(who)
+      : "memory");
 }
 template <int D>
-__device__ __forceinline__ void issue_qk(uint32_t s, uint32_t q, uint32_t k) {
-  q = opaque(q), k = opaque(k);
+__device__ __forceinline__ void issue_qk(uint32_t who, uint32_t s, uint64_t q, uint64_t k) {
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) {
-    const uint32_t off = ((i >> 2) * kSubTileBytes + (i & 3) * 32) >> 4;
-    mma_ss(s, desc_of(q + off), desc_of(k + off), idesc_f16(128, 128, false), i > 0);
+    const uint32_t off = (i >> 2) * kSubTileBytes + (i & 3) * 32;
+    mma_ss_if(who, s, sdesc_adv(q, off), sdesc_adv(k, off), idesc_f16(128, 128, false), i > 0);
   }
 }
 template <int D>
-__device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint32_t v, bool accumulate) {
-  v = opaque(v), p = opaque(p);
+__device__ __forceinline__ void issue_pv(uint32_t who, uint32_t o, uint32_t p, uint64_t v, bool accumulate) {
 #pragma unroll
   for (int i = 0; i < kC4Unit / 16; ++i)
-    mma_ts(o, p + i * 8, desc_of(v + (i * 2048 >> 4)), idesc_f16(128, D, true), accumulate || i > 0);
+    mma_ts_if(who, o, p + i * 8, sdesc_adv(v, i * 2048), idesc_f16(128, D, true), accumulate || i > 0);
 }
 
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
@@ -296,7 +314,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
       j = make_int4(c->at.b, c->at.hk * a.row_blocks + c->at.rb, last, first_part);
     a.joins[blockIdx.x] = j;
   }
-  const uint32_t tmem = c->tmem;
   const WaitCtl wc = {a.st, &c->abort, a.timeout_ns};
   __syncthreads();  // every thread has seen the cursor
 
@@ -366,76 +383,63 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
       for (int i = 0; i < L::kRawStages; ++i)
         if ((used >> i) & 1) drain_bar<true>(&c->raw_full[i], i < stage ? phase : phase ^ 1, a.timeout_ns);
       __syncwarp();
-    } else if (warp == kMmaWarp && lane == 0 && work) {
+    } else if (warp == kMmaWarp && work) {
       // --------------------------------------------------------- MMA issuer
       // Q and K: rows of 128 bytes along the dims; V: 64-dim columns of keys.
-      const uint32_t q_desc = desc_low(smem, 16), k_desc = desc_low(smem + L::kRingOff, 16);
-      const uint32_t v_desc = desc_low(smem + L::kRingOff, kSubTileBytes);
+      const uint64_t q_desc = sdesc_sw128(smem_addr(smem), 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_addr(smem + L::kRingOff), 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(smem_addr(smem + L::kRingOff), kSubTileBytes, 1024);
+      const uint32_t who = elect_one();
       int stage = 0;
       uint32_t phase = 0, q_par = 0, p_par = 0;  // bit t: of tile t
       bool ok = true;
       auto next_tile = [&](int& st) {
         st = stage;
-        const bool r = wait_bar<true>(&c->kv_full[stage], phase, wc, kWMmaTile);
+        const bool r = wait_bar_warp<true>(&c->kv_full[stage], phase, wc, kWMmaTile);
         if (++stage == L::kStages) stage = 0, phase ^= 1;
         tc_fence_after();
         return r;
       };
-      auto qk = [&](int t, int st) {
-        issue_qk<D>(tmem + t * 128, q_desc + (t * L::kTileBytes >> 4), k_desc + (st * L::kTileBytes >> 4));
-        mma_commit(&c->s_full[t]);
-      };
       for (int s = 0; ok; ++s) {
-        ok = wait_bar<true>(&c->seg_full[s % kSegs], (s / kSegs) & 1, wc, kWMmaSeg);
+        ok = wait_bar_warp<true>(&c->seg_full[s % kSegs], (s / kSegs) & 1, wc, kWMmaSeg);
         if (!ok) break;
-        const int units = c->seg[s % kSegs].units;
-        const bool two = c->seg[s % kSegs].live > 128;
-        mbar_arrive(&c->seg_empty[s % kSegs]);
+        const int units = __shfl_sync(0xffffffffu, c->seg[s % kSegs].units, 0);
+        const int tiles = __shfl_sync(0xffffffffu, c->seg[s % kSegs].live > 128 ? 2 : 1, 0);
+        warp_arrive(&c->seg_empty[s % kSegs]);
         if (units < 0) break;
-        int kst = 0, vst = 0;
-        ok = wait_bar<true>(&c->q_full[0], q_par & 1, wc, kWMmaQ) && next_tile(kst);
-        if (!ok) break;
-        q_par ^= 1;
-        qk(0, kst);
-        if (two) {
-          ok = wait_bar<true>(&c->q_full[1], q_par >> 1, wc, kWMmaQ);
-          if (!ok) break;
-          q_par ^= 2;
-          tc_fence_after();
-          qk(1, kst);
-        }
-        mma_commit(&c->kv_empty[kst]);
-        for (int j = 0; j < units && ok; ++j) {
-          const bool last = j == units - 1;
-          ok = next_tile(vst) && wait_bar<true>(&c->p_full[0], p_par & 1, wc, kWMmaP);
-          if (!ok) break;
-          p_par ^= 1;
-          tc_fence_after();
-          const uint32_t vd = v_desc + (vst * L::kTileBytes >> 4);
-          issue_pv<D>(tmem + 256, tmem, vd, j > 0);
-          if (!last) {
-            ok = next_tile(kst);
-            if (!ok) break;
-            qk(0, kst);
-          } else {
-            mma_commit(&c->o_done[0]);
+        // A tile's P V of unit j - 1, then its Q K^T of unit j, which overwrites
+        // that P.
+        for (int j = 0; j <= units && ok; ++j) {
+          int kst = 0, vst = 0;
+          if (j > 0) ok = next_tile(vst);
+#pragma unroll 1
+          for (int t = 0; t < tiles && ok; ++t) {
+            if (j == 0) {
+              ok = wait_bar_warp<true>(&c->q_full[t], (q_par >> t) & 1, wc, kWMmaQ);
+              q_par ^= 1u << t;
+            } else {
+              ok = wait_bar_warp<true>(&c->p_full[t], (p_par >> t) & 1, wc, kWMmaP);
+              p_par ^= 1u << t;
+              tc_fence_after();
+              issue_pv<D>(who, kTmemO + t * D, kTmemS + t * 128, sdesc_adv(v_desc, vst * L::kTileBytes), j > 1);
+              if (t == tiles - 1) commit_if(who, &c->kv_empty[vst]);
+              if (j == units) commit_if(who, &c->o_done[t]);
+            }
+            if (j < units) {
+              if (t == 0) ok = ok && next_tile(kst);
+              tc_fence_after();
+              issue_qk<D>(who, kTmemS + t * 128, sdesc_adv(q_desc, t * L::kTileBytes),
+                          sdesc_adv(k_desc, kst * L::kTileBytes));
+              commit_if(who, &c->s_full[t]);
+              if (t == tiles - 1) commit_if(who, &c->kv_empty[kst]);
+            }
           }
-          if (two) {
-            ok = wait_bar<true>(&c->p_full[1], p_par >> 1, wc, kWMmaP);
-            if (!ok) break;
-            p_par ^= 2;
-            tc_fence_after();
-            issue_pv<D>(tmem + 256 + D, tmem + 128, vd, j > 0);
-          }
-          mma_commit(&c->kv_empty[vst]);
-          if (two && !last) qk(1, kst);
-          else if (two) mma_commit(&c->o_done[1]);
-          if (!last) mma_commit(&c->kv_empty[kst]);
         }
       }
       // Every MMA issued above must finish before TMEM is released.
-      mma_commit(&c->mma_done);
+      commit_if(who, &c->mma_done);
       drain_bar<true>(&c->mma_done, 0, a.timeout_ns);
+      __syncwarp();
     }
   } else if (warp >= kMakeWarp) {
     reg_dealloc<kMakeRegs>();
@@ -499,8 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
     reg_alloc<kSoftmaxRegs>();
     // ------------------------------------------------- softmax (thread = row)
     const int t = warp >> 2, quarter = warp & 3;
-    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t tS = tl + t * 128, tO = tl + 256 + t * D;
+    const uint32_t tl = (uint32_t)(quarter * 32) << 16;
+    const uint32_t tS = tl + kTmemS + t * 128, tO = tl + kTmemO + t * D;
     const int in_tile = quarter * 32 + lane;
     uint32_t s_cnt = 0, o_cnt = 0;
     int u_seg = 0;  // units of the segments before
@@ -712,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
   if (warp == kMmaWarp) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(c->tmem, 512);
   }
 }
 
