@@ -78,15 +78,26 @@ __device__ __forceinline__ uint32_t factor_of(int by) {
   return h | h << 16;
 }
 
-// Largest finite magnitude of two bf16 pairs' halves, by their bits.
-__device__ __forceinline__ uint32_t larger(uint32_t big, uint32_t w) {
-  const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
-  if (lo < 0x7f80u) big = max(big, lo);
-  if (hi < 0x7f80u) big = max(big, hi);
+// Largest magnitude of a warp's bf16 pairs by its bits, of the finite ones where
+// others are among them.
+template <int N>
+__device__ __forceinline__ uint32_t largest(const uint4 (&x)[N]) {
+  uint32_t big = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    for (uint32_t w : {x[i].x, x[i].y, x[i].z, x[i].w}) big = __vmaxu2(big, w & 0x7fff7fffu);
+  big = __reduce_max_sync(0xffffffffu, max(big & 0xffffu, big >> 16));
+  if (big >= 0x7f80u) {
+    big = 0;
+    for (int i = 0; i < N; ++i)
+      for (uint32_t w : {x[i].x, x[i].y, x[i].z, x[i].w}) {
+        const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
+        if (lo < 0x7f80u) big = max(big, lo);
+        if (hi < 0x7f80u) big = max(big, hi);
+      }
+    big = __reduce_max_sync(0xffffffffu, big);
+  }
   return big;
-}
-__device__ __forceinline__ uint32_t larger(uint32_t big, const uint4& u) {
-  return larger(larger(larger(larger(big, u.x), u.y), u.z), u.w);
 }
 // Smallest exponent e with amax <= 448 2^e, 448 being 1.75 2^8; amax by its
 // bf16 bits.
@@ -95,15 +106,14 @@ __device__ __forceinline__ int exponent_for(uint32_t amax) {
   return min(max(e, -kExp8), kExp8);
 }
 
-// A group's exponent: `big` is the lane's largest magnitude among the new
-// tokens, `old` the exponent's byte, `fresh` whether the group begins.
+// A group's exponent: `big` is the largest magnitude among the new tokens, `old` the exponent's byte, `fresh` whether the group begins.
 struct Exponent {
   int e;
   bool grown;     // the other tokens' codes are of a smaller one,
   uint32_t down;  // by this factor (an f16 pair)
   float unit, inv;  // 2^e, 2^-e
   __device__ __forceinline__ Exponent(uint32_t big, uint32_t old, bool fresh) {
-    e = exponent_for(__reduce_max_sync(0xffffffffu, big));
+    e = exponent_for(big);
     const int was = exp8(old);
     if (!fresh) e = max(e, was);
     grown = !fresh && e > was;
@@ -124,29 +134,25 @@ __device__ __forceinline__ void append_keys(const Append8Args& a, const Places& 
                                             size_t row0, bool fresh, int lane) {
   const int g = lane >> 2, t = lane & 3;
   const uint32_t head = grp[32 * D];
-  uint4 x[2][D / 32];
+  uint4 x[2 * (D / 32)];  // [h][j]
   int n[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     n[h] = p.at[8 * h + g];
 #pragma unroll
     for (int j = 0; j < D / 32; ++j)
-      x[h][j] = n[h] >= 0 ? *reinterpret_cast<const uint4*>(a.k + (row0 + n[h]) * D + 32 * j + 8 * t)
+      x[h * (D / 32) + j] = n[h] >= 0 ? *reinterpret_cast<const uint4*>(a.k + (row0 + n[h]) * D + 32 * j + 8 * t)
                           : make_uint4(0, 0, 0, 0);
   }
-  uint32_t big = 0;
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) big = larger(big, x[h][j]);
-  const Exponent e(big, head, fresh);
+  const Exponent e(largest(x), head, fresh);
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
       uint4* at = reinterpret_cast<uint4*>(grp + k8_piece(D, h, c, lane));
       if (n[h] >= 0) {
-        const uint2 u = quantise(x[h][2 * c], e.inv), v = quantise(x[h][2 * c + 1], e.inv);
+        const uint4* row = x + h * (D / 32) + 2 * c;
+        const uint2 u = quantise(row[0], e.inv), v = quantise(row[1], e.inv);
         *at = make_uint4(u.x, u.y, v.x, v.y);
         if (a.k_out) {
           __nv_bfloat16* out = a.k_out + (row0 + n[h]) * D + 64 * c + 8 * t;
@@ -167,7 +173,7 @@ __device__ __forceinline__ void append_values(const Append8Args& a, const Places
                                               size_t row0, bool fresh, int lane) {
   const int g = lane >> 2, t = lane & 3;
   const uint32_t head = grp[32 * D + 1];
-  uint4 x[2][2][D / 64];
+  uint4 x[4 * (D / 64)];  // [h][s][j]
   int n[2][2];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
@@ -176,17 +182,10 @@ __device__ __forceinline__ void append_values(const Append8Args& a, const Places
       n[h][s] = p.at[8 * h + 2 * t + s];
 #pragma unroll
       for (int j = 0; j < D / 64; ++j)
-        x[h][s][j] = n[h][s] >= 0 ? *reinterpret_cast<const uint4*>(a.v + (row0 + n[h][s]) * D + 64 * j + 8 * g)
+        x[(2 * h + s) * (D / 64) + j] = n[h][s] >= 0 ? *reinterpret_cast<const uint4*>(a.v + (row0 + n[h][s]) * D + 64 * j + 8 * g)
                                   : make_uint4(0, 0, 0, 0);
     }
-  uint32_t big = 0;
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int j = 0; j < D / 64; ++j) big = larger(big, x[h][s][j]);
-  const Exponent e(big, head, fresh);
+  const Exponent e(largest(x), head, fresh);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const bool has0 = n[h][0] >= 0, has1 = n[h][1] >= 0;
@@ -194,7 +193,8 @@ __device__ __forceinline__ void append_values(const Append8Args& a, const Places
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
       uint4* at = reinterpret_cast<uint4*>(grp + v8_piece(D, j, h, lane));
-      const uint2 u = quantise(x[h][0][j], e.inv), v = quantise(x[h][1][j], e.inv);
+      const uint2 u = quantise(x[2 * h * (D / 64) + j], e.inv);
+      const uint2 v = quantise(x[(2 * h + 1) * (D / 64) + j], e.inv);
       // The two tokens' codes side by side.
       uint4 c = make_uint4(__byte_perm(u.x, v.x, 0x5140), __byte_perm(u.x, v.x, 0x7362),
                            __byte_perm(u.y, v.y, 0x5140), __byte_perm(u.y, v.y, 0x7362));
