@@ -132,24 +132,42 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* at, const Lane& a, cons
 }
 
 // How positions and their axes are taken: none; a lane's four angles are of
-// one axis, whose position it holds; or of several, and the lanes hold the
-// positions of axis (lane % 4) for one another.  (One kernel for the last two,
-// with a branch, spills: 106 us for 102 at 3 x 5001 tokens, the backward of
-// 4 x 1024 56 for 52.)
+// one axis, whose position it holds; or of several: the warp then copies the
+// angles one by one, and the lanes hold the positions of axis (lane % 4) for one
+// another.  (One kernel for the last two, with a branch, spills: 106 us for 102
+// at 3 x 5001 tokens, the backward of 4 x 1024 56 for 48.)
 enum Turning { kPlain, kSections, kMixed };
-template <Turning kTurn>
+
+// The angle at place `at` of a row of angles in a ring (below): 4 for each piece
+// q and lane j.
+template <int D, bool kInter>
+__device__ __forceinline__ int angle_at(int at) {
+  constexpr int kLanes = D / 16;
+  const int q = at / (4 * kLanes), j = at / 4 % kLanes, i = at % 4;
+  return (kInter ? 4 * (j + (q & 1) * kLanes) : 8 * j + 4 * (q & 1)) + i;
+}
+template <int D, bool kInter, Turning kTurn>
 struct LaneAxes {
   int axis;       // whose position the lane holds
-  uint32_t four;  // axes of its angles, two bits each
-  __device__ __forceinline__ LaneAxes(const RopeArgs& a, int first) {
-    if constexpr (kTurn != kPlain) {
-      const int w = first >> 4;
+  uint32_t each;  // kMixed: axes of the angles that it copies, two bits each
+  __device__ __forceinline__ LaneAxes(const RopeArgs& a, const Lane& l) {
+    auto of = [&](int angle) {
+      const int w = angle >> 4;
       const uint32_t bits =
           w == 0 ? a.axes[0] : (w == 1 ? a.axes[1] : (w == 2 ? a.axes[2] : a.axes[3]));
-      four = (bits >> (2 * (first & 15))) & 0xff;
-      axis = kTurn == kMixed ? threadIdx.x & 3 : four & 3;
-      if (axis >= a.n_axes) axis = 0;
+      return (bits >> (2 * (angle & 15))) & 3;
+    };
+    if constexpr (kTurn == kSections) {
+      axis = of(angle_at<D, kInter>((l.sub & 1) * (D / 4) + 4 * l.j));
+    } else if constexpr (kTurn == kMixed) {
+      axis = threadIdx.x & 3;
+      each = 0;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+        each |= of(angle_at<D, kInter>((threadIdx.x & 31) + 32 * i)) << (2 * i);
     }
+    if constexpr (kTurn != kPlain)
+      if (axis >= a.n_axes) axis = 0;
   }
   __device__ __forceinline__ int position(const RopeArgs& a, int token, int n) const {
     if constexpr (kTurn != kPlain) return a.positions[(size_t)axis * a.tokens + token];
@@ -191,27 +209,23 @@ struct Ring {
   // clamped to the table.  Piece q of lane j: 4 cosines (q = 0, 1) or sines
   // (2, 3), of the pair's first or second four angles, or (interleaved) of
   // its first or second chunk's.
-  template <bool kInter>
-  static __device__ __forceinline__ int first_angle(const Lane& l) {
-    return kInter ? 4 * (l.j + (l.sub & 1) * kLanes) : 8 * l.j + 4 * (l.sub & 1);
-  }
   template <bool kInter, Turning kTurn>
   __device__ __forceinline__ void fetch_turn(int stage, const RopeArgs& a, const Lane& l,
-                                             const LaneAxes<kTurn>& axes, int pos) const {
+                                             const LaneAxes<D, kInter, kTurn>& axes, int pos) const {
     if constexpr (kTurn != kMixed) {
       if (l.sub >= 4 || !(l.sub & 1 ? l.turn1 : l.turn0)) return;
       pos = pos < 0 ? 0 : (pos >= a.table_rows ? a.table_rows - 1 : pos);
-      const int first = first_angle<kInter>(l);
+      const int first = kInter ? 4 * (l.j + (l.sub & 1) * kLanes) : 8 * l.j + 4 * (l.sub & 1);
       const float* src = a.table + (size_t)pos * a.rot + first + (l.sub >> 1) * (a.rot / 2);
-      copy_turn<16>(piece(stage, l), src);
+      copy_turn<16>(turns(stage) + (l.sub * kLanes + l.j) * 16, src);
     } else {
-      const bool turns = l.sub < 4 && (l.sub & 1 ? l.turn1 : l.turn0);
       pos = pos < 0 ? 0 : (pos >= a.table_rows ? a.table_rows - 1 : pos);
-      const int first = first_angle<kInter>(l) + (l.sub >> 1) * (a.rot / 2);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int at = __shfl_sync(0xffffffffu, pos, (axes.four >> (2 * i)) & 3);
-        if (turns) copy_turn<4>(piece(stage, l) + 4 * i, a.table + (size_t)at * a.rot + first + i);
+      for (int i = 0; i < D / 32; ++i) {
+        const int at = (threadIdx.x & 31) + 32 * i, angle = angle_at<D, kInter>(at);
+        const int row = __shfl_sync(0xffffffffu, pos, (axes.each >> (2 * i)) & 3);
+        const int sine = at >= 8 * kLanes ? a.rot / 2 : 0;
+        if (angle < a.rot / 2) copy_turn<4>(turns(stage) + 4 * at, a.table + (size_t)row * a.rot + angle + sine);
       }
     }
   }
@@ -223,12 +237,12 @@ struct Ring {
                  "l"(src), "n"(kBytes)
                  : "memory");
   }
-  __device__ __forceinline__ uint8_t* piece(int stage, const Lane& l) const {
-    return base + stage * kStage + kRows * 1024 + (l.sub * kLanes + l.j) * 16;
+  __device__ __forceinline__ uint8_t* turns(int stage) const {
+    return base + stage * kStage + kRows * 1024;
   }
   __device__ __forceinline__ void turn_of(int stage, const Lane& l, F2 (&cs)[4],
                                           F2 (&sn)[4]) const {
-    const uint8_t* at = base + stage * kStage + kRows * 1024 + l.j * 16;
+    const uint8_t* at = turns(stage) + l.j * 16;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(at + q * kLanes * 16);
@@ -365,7 +379,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_fwd_kernel(RopeArgs a) {
   const R ring = {smem + warp * kFwdStages * R::kStage};
   wait_for_stream();
   const bool turns = k.kind < 2;
-  const LaneAxes<kTurn> axes(a, R::template first_angle<kInter>(l));
+  const LaneAxes<D, kInter, kTurn> axes(a, l);
   F2 w[8];
   if (kNorm && turns) load_weight(k.kind == 0 ? a.q_weight : a.k_weight, a.weight_bf16, l, w);
   Walk<const __nv_bfloat16> in(a.all, a.N, a.qkv + (size_t)k.column * D + l.c0, a.stride_b,
@@ -432,7 +446,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rope_bwd_kernel(RopeArgs a) {
   const int warp = threadIdx.x >> 5, id = blockIdx.x * kWarps + warp;
   const R ring = {smem + warp * kBwdStages * R::kStage};
   wait_for_stream();
-  const LaneAxes<kTurn> axes(a, R::template first_angle<kInter>(l));
+  const LaneAxes<D, kInter, kTurn> axes(a, l);
   F2 dw[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) dw[e] = 0;
