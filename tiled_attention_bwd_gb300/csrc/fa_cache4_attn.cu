@@ -54,6 +54,7 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, __half2 b) {
 
 struct Cache4 {
   static constexpr uint32_t kWhere = 0x511;
+  static constexpr int kItemCost = kC4ItemCost;
   static constexpr __host__ __device__ int group_bytes(int d) { return fa::group_bytes(d); }
   static constexpr __host__ __device__ int blocks_per_sm(int d, int nt) {
     return nt == 1 || (nt == 2 && d == 64) ? 3 : 2;

@@ -25,7 +25,7 @@ namespace fa {
 constexpr int kGroup = 16;      // tokens of a group of the cache
 constexpr int kC4Unit = 128;    // keys of a unit
 constexpr int kC4Align = 32;    // an item's first key is a multiple of it
-constexpr int kC4ItemCost = 3;  // in units
+constexpr int kC4ItemCost = 3;  // in units, unless a call says otherwise
 
 // Division of 0 <= x < 2^31 by a number fixed at launch: three instructions
 // instead of about twenty (Granlund and Montgomery, "Division by invariant
@@ -61,6 +61,7 @@ struct Call {
   FastDiv by_heads;
   // Requests with fewer or more live rows have no items here.
   int least_rows = 0, most_rows = 0x7fffffff;
+  int item_cost = kC4ItemCost;
   // (Most calls have one row block; a division costs 0.1 us of a short one.)
   FA_BOTH int request_of_pair(int at) const { return row_blocks == 1 ? at : at / row_blocks; }
 };
@@ -84,7 +85,8 @@ struct Keys {
   int lo, hi;  // lo: a multiple of kC4Align; behind the last token's
   int first;   // position of the first token, negative before the cache
   int units;
-  FA_BOTH int cost() const { return units + kC4ItemCost; }
+  int begin;   // what the item costs besides, in units
+  FA_BOTH int cost() const { return units + begin; }
 };
 FA_BOTH Keys keys_of(const Call& c, const Request& r, int row_block) {
   const int row = row_block * c.rows, live = r.ql * c.heads - row;
@@ -97,6 +99,7 @@ FA_BOTH Keys keys_of(const Call& c, const Request& r, int row_block) {
   k.lo = c.window < 0 || k.first < c.window ? 0 : (k.first - c.window) & ~(kC4Align - 1);
   // Without keys one unit is left, which writes the empty rows.
   k.units = k.hi > k.lo ? (k.hi - k.lo - 1) / kC4Unit + 1 : 1;
+  k.begin = c.item_cost;
   return k;
 }
 
@@ -155,8 +158,8 @@ struct Cursor {
   FA_BOTH void segment(int at) {
     const int here = lesser(k.cost() - at, left), to = at + here;
     left -= here;
-    unit = at < kC4ItemCost ? 0 : at - kC4ItemCost;
-    end = to < kC4ItemCost ? 0 : to - kC4ItemCost;
+    unit = at < k.begin ? 0 : at - k.begin;
+    end = to < k.begin ? 0 : to - k.begin;
   }
   // Goes to the item that holds place `u` of the pairs from `at` on, and its
   // segment of at most `share`; returns how far into the item's cost it is.
@@ -211,7 +214,7 @@ FA_BOTH bool join_of(const Shares& s, const Cursor& at, int block, long long u0,
                      int* last, int* first_part) {
   if (at.unit == 0) return false;
   const long long i0 = u0 - into, before = s.first(block - 1);
-  if (before > i0 + kC4ItemCost) return false;
+  if (before > i0 + at.k.begin) return false;
   *last = s.block_of(i0 + at.k.cost() - 1);
   *first_part = 2 * (block - 1) + (before < i0 ? 1 : 0);
   return true;

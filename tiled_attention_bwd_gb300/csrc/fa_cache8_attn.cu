@@ -20,6 +20,7 @@ namespace {
 
 struct Cache8 {
   static constexpr uint32_t kWhere = 0x521;
+  static constexpr int kItemCost = 1;  // (three: 111 us at 3 x 131072 tokens, one: 107)
   static constexpr __host__ __device__ int group_bytes(int d) { return group8_bytes(d); }
   static constexpr __host__ __device__ int blocks_per_sm(int d, int nt) {
     return d == 64 && nt <= 2 ? 3 : 2;
@@ -164,9 +165,11 @@ cudaError_t run(const CacheAttnArgs& a, int sm_count, cudaStream_t stream) {
 
 }  // namespace
 
-// Rows of an item: what makes the least of the passes over the keys.
+// Rows of an item: what makes the least of the passes over the keys, each of a
+// cost by its width (us measured at 16 requests of 8192 tokens x 8 heads; 40
+// rows at once at d = 128 spill: not built).
 int cache8_attn_rows(int rows, int d) {
-  const int cost[2][5] = {{22, 26, 36, 43, 52}, {32, 41, 52, 65, 0}};
+  const int cost[2][5] = {{31, 36, 43, 50, 59}, {51, 54, 59, 76, 0}};
   int best = 8;
   long long least = 0;
   for (int nt = 1; nt <= (d == 128 ? 4 : 5); ++nt) {
@@ -175,6 +178,12 @@ int cache8_attn_rows(int rows, int d) {
   }
   return best;
 }
+
+// Measured against the kernel for many rows (us, this one first; 16 requests of
+// 8192 tokens x 8 heads, 64 of 1000 x 2, 1 of 4096 x 8, 2 of 60000 x 1):
+//   d = 128, 64 rows: 130/129, 38/39, 23/28, 35/47; 128: 236/136, 56/43, 27/30, 44/49
+//   d = 64,  64 rows: 83/108, 28/34, 18/25, 27/36;  128: 150/111, 42/36, 20/25, 32/38
+int cache8_narrow_rows(int d) { return d == 128 ? 64 : 80; }
 
 cudaError_t launch_cache8_attn(const CacheAttnArgs& a, int d, int sm_count, cudaStream_t stream) {
   const int nt = a.item_rows / 8;

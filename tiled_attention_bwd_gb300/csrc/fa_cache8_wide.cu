@@ -50,6 +50,7 @@ constexpr float kNoMax = -1e30f;  // m of a row that has seen no key
 constexpr float kUp = 8.0f;       // P carries 2^kUp
 constexpr float kSlack = 7.0f;    // growth of m that is left standing (f16 ends at 2^16)
 constexpr int kUnitGroups = kC4Unit / kGroup;
+constexpr int kItemCost = 4;  // what beginning and ending an item costs, in units
 constexpr int kSegs = 4, kInfos = 4;
 
 // Where-codes of the waits.
@@ -231,6 +232,7 @@ __device__ __forceinline__ c4::Call wide_call(const CacheAttnArgs& a) {
   c4::Call c = {a.B, a.Hkv, a.T, a.window, a.heads, kC8WideRows, a.row_blocks, a.M << a.shift, a.by_heads};
   c.least_rows = a.least_rows;
   c.most_rows = a.most_rows;
+  c.item_cost = kItemCost;
   return c;
 }
 __device__ __forceinline__ size_t row_at(const CacheAttnArgs& a, int b, int hk, int row) {

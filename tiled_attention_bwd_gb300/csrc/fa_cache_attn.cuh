@@ -35,7 +35,8 @@
 //
 // A format F says how a group of 16 tokens is laid out and how its codes
 // become the products' operands:
-//   group_bytes(D), blocks_per_sm(D, NT), kWhere (where-code of its waits)
+//   group_bytes(D), blocks_per_sm(D, NT), kWhere (where-code of its waits),
+//   kItemCost (c4::Call::item_cost)
 //   q_piece(D, t, i)   offset of lane t's i-th 16-byte piece of a row of Q, in
 //                      the order in which scores() takes the dims
 //   o_dim(D, g, dt)    first of the four dims that lane g holds in the tiles
@@ -100,9 +101,10 @@ __device__ __forceinline__ void launch_dependents() {
 // The call as the division of work sees it, for items of kRows rows, and its
 // requests (read by plain loads: the kernel before may have written them).
 template <int kRows>
-__device__ __forceinline__ c4::Call call_of(const CacheAttnArgs& a) {
+__device__ __forceinline__ c4::Call call_of(const CacheAttnArgs& a, int item_cost) {
   c4::Call c = {a.B, a.Hkv, a.T, a.window, a.heads, kRows, a.row_blocks, a.M << a.shift, a.by_heads};
   c.most_rows = a.most_rows;
+  c.item_cost = item_cost;
   return c;
 }
 // Row `row` of a request and key/value head in q, o and lse.
@@ -316,7 +318,7 @@ __device__ __forceinline__ void cache_attn(const CacheAttnArgs& a, Block<F, D, N
   launch_dependents();
 
   // ---- this block's share of the units
-  const c4::Call call = call_of<S::kRows>(a);
+  const c4::Call call = call_of<S::kRows>(a, F::kItemCost);
   auto read = [&](int b) {
     return c4::request_of(call, a.seq_lens[b], a.q_lens ? a.q_lens[b] : a.T);
   };

@@ -144,8 +144,9 @@ cudaError_t launch_cache4_attn(const CacheAttnArgs& a, int d, int sm_count,
 int cache8_attn_rows(int rows, int d);
 cudaError_t launch_cache8_attn(const CacheAttnArgs& a, int d, int sm_count,
                                cudaStream_t stream);
-// The same for requests with many rows, more than kC8NarrowRows.
-constexpr int kC8NarrowRows = 32;
+// The same for requests with many rows; calls of up to cache8_narrow_rows a
+// request are for the first kernel alone.
+int cache8_narrow_rows(int d);
 constexpr int kC8WideRows = 256;    // of an item
 constexpr int kC8WideBlocks = 160;
 cudaError_t launch_cache8_wide(const CacheAttnArgs& a, int d, int sm_count,

@@ -2,6 +2,7 @@
 // kernels: norm and rotation of queries and keys, and the paged 4-bit cache.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -208,19 +209,21 @@ fa_status check_cache(int pages, int Hkv, int page, int d, int* shift) {
 }
 
 // A format's bytes of a group, and its attention's rows of an item and launch;
-// for requests of more than narrow_rows rows, another kernel of wide_rows.
+// for calls of more than narrow_rows rows a request, a second kernel with items
+// of wide_rows.
 using AttnLaunch = cudaError_t (*)(const fa::CacheAttnArgs& a, int d, int sm_count,
                                    cudaStream_t stream);
 struct Format {
   int (*group)(int d);
   int (*rows)(int rows, int d);
   AttnLaunch attn;
-  int narrow_rows = INT_MAX, wide_rows = 0, wide_blocks = 0;
+  int (*narrow_rows)(int d) = nullptr;
+  int wide_rows = 0, wide_blocks = 0;
   AttnLaunch wide = nullptr;
 };
 constexpr Format kCache4 = {fa::group_bytes, fa::cache4_attn_rows, fa::launch_cache4_attn};
-constexpr Format kCache8 = {fa::group8_bytes,      fa::cache8_attn_rows, fa::launch_cache8_attn,
-                            fa::kC8NarrowRows,     fa::kC8WideRows,      fa::kC8WideBlocks,
+constexpr Format kCache8 = {fa::group8_bytes,       fa::cache8_attn_rows, fa::launch_cache8_attn,
+                            fa::cache8_narrow_rows, fa::kC8WideRows,      fa::kC8WideBlocks,
                             fa::launch_cache8_wide};
 
 long long cache_bytes(const Format& f, int pages, int Hkv, int page, int d) {
@@ -357,19 +360,21 @@ uintptr_t lay_out(fa::CacheAttnArgs& a, uintptr_t ws, int blocks, int rows, int 
   return ws;
 }
 // The kernels of a call of requests with up to `rows` rows, with their places
-// in the workspace; returns its end.  (Requests of many rows have items of one
-// token's heads in the first kernel: most of what it gets is single tokens.)
+// in the workspace; returns its end.  In a call with many rows the first kernel
+// gets the requests with one token or two: its items are of one token's heads.
+// (64 heads over 8, d = 128: a token that takes two passes over the keys that
+// way costs 104 to the second kernel's 127.)
 uintptr_t lay_out(const Format& f, int rows, int heads, int d, uintptr_t ws,
                   fa::CacheAttnArgs& narrow, fa::CacheAttnArgs& wide, bool* is_wide) {
-  *is_wide = rows > f.narrow_rows;
-  narrow.rows = *is_wide ? f.narrow_rows : rows;
+  *is_wide = f.wide && rows > f.narrow_rows(d);
+  narrow.item_rows = f.rows(*is_wide ? heads : rows, d);
   narrow.least_rows = 0;
-  narrow.most_rows = f.narrow_rows;
-  narrow.item_rows = f.rows(*is_wide && heads < f.narrow_rows ? heads : narrow.rows, d);
+  narrow.most_rows = *is_wide ? 2 * narrow.item_rows : INT_MAX;
+  narrow.rows = *is_wide ? std::min(rows, narrow.most_rows) : rows;
   ws = lay_out(narrow, ws, fa::kC4MaxBlocks, narrow.item_rows, d, false);
   if (!*is_wide) return ws;
   wide.rows = rows;
-  wide.least_rows = f.narrow_rows + 1;
+  wide.least_rows = narrow.most_rows + 1;
   wide.most_rows = INT_MAX;
   return lay_out(wide, ws, f.wide_blocks, f.wide_rows, d, true);
 }
@@ -450,7 +455,7 @@ fa_status cache_attn(const Format& f, const void* q, const void* cache, const in
   lay_out(f, a.heads * T, a.heads, d, reinterpret_cast<uintptr_t>(workspace), a, wide,
           &is_wide);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // (Without lengths every request has as many rows.)
+  // (Without lengths every request has as many rows, too many for the first.)
   cudaError_t e = cudaSuccess;
   if (!is_wide || q_lens) e = f.attn(a, d, dev.sm_count, st);
   if (is_wide && e == cudaSuccess) e = f.wide(wide, d, dev.sm_count, st);
