@@ -532,7 +532,10 @@ fa_status fa_cache8_read(const void* cache, const int* block_table,
  * Causal attention of each request's newest tokens over the 8-bit cache:
  * arguments, masks, workspace rules and waits (where-code 0x521) as
  * fa_cache4_attn's, without scales; the workspace is
- * fa_cache8_attn_workspace_size(B, H, Hkv, T, d) bytes.  A NaN that the cache
+ * fa_cache8_attn_workspace_size(B, H, Hkv, T, d) bytes, and max_blocks *
+ * page_size + T at most 2^31 - 257.  Calls of more than 64 rows T * H / Hkv (80
+ * for d = 64) may run two kernels, one for the requests with few live rows;
+ * waits of the other have the where-codes 0x531 to 0x53d.  A NaN that the cache
  * holds reaches the rows that see its token (of a value, in its dim) and no
  * others.
  * Scores and the softmax's maxima and sums are fp32.  The weights, each times
@@ -594,15 +597,22 @@ void fa_set_wait_timeout_ns(uint64_t ns);
  *             for dQ, 0x412 the finished dV, 0x413 the next item.
  *   cache attention: 0x511 a warp waiting for its copies (the hook takes the
  *             first warp of every block, whether its wait is complete or not).
- *             0x521 the same over the 8-bit cache.
+ *             0x521 the same over the 8-bit cache; its kernel for many rows
+ *             (stopped at the site whether a wait is complete or not):
+ *             0x531 the loading warp waiting for a segment's place, 0x532 for
+ *             room for codes; 0x533 the warps that make f16 tiles waiting for a
+ *             segment, 0x534 for codes, 0x535 for a free tile; 0x536 MMA warp
+ *             waiting for a segment, 0x537 Q, 0x538 a tile, 0x539 P; 0x53a
+ *             softmax waiting for a segment, 0x53b a unit's exponents, 0x53c S,
+ *             0x53d the finished O.
  * While a site is set, forward and backward calls with d = 128 and no
  * window, lengths or FP8, and cache attention calls with d = 128 and at most
- * 8 query rows per key/value head, run kernel instantiations compiled with
- * the hook (the same source; the ones used otherwise carry no trace of it, since
- * even a test on the slow path of each wait cost about 1%); other calls
- * ignore it.  The call is synchronous (it writes a constant in device
- * memory): make it only while no kernel of this library is running on the
- * device.
+ * 8 query rows per key/value head or with many over the 8-bit cache, run
+ * kernel instantiations compiled with the hook (the same source; the ones used
+ * otherwise carry no trace of it, since even a test on the slow path of each
+ * wait cost about 1%); other calls ignore it.  The call is synchronous (it
+ * writes a constant in device memory): make it only while no kernel of this
+ * library is running on the device.
  * The pages have no counterpart; this exists so that the failure handling
  * of the real kernels can be tested without harming the GPU.
  */

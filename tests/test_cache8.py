@@ -151,6 +151,7 @@ def _attn(lib, q=16, cache=1 << 20, table=16, lens=16, ql=16, o=4096, lse=16384,
     (WORKSPACE, dict(ws=0)), (WORKSPACE, dict(ws=16)),
     (WORKSPACE, dict(wsb=100)), (INVALID, dict(ws=1 << 20)),
     (UNSUPPORTED, dict(M=1 << 28)), (UNSUPPORTED, dict(pages=1 << 28)),
+    (UNSUPPORTED, dict(M=(1 << 27) - 8, page=16)),
     (UNSUPPORTED, dict(B=1 << 20, H=1 << 12)),
     (UNSUPPORTED, dict(B=1 << 20, M=1 << 10, page=256)),
 ])
@@ -582,16 +583,18 @@ def test_offsets_past_32_bits():
 
 
 @pytest.mark.gpu
-def test_a_stopped_attention_reports_and_recovers():
-    """The kernel's stopping path, by the test hook (no fault, no hang)."""
-    c = attn_case(2, 8, 1, 1, 128, 64, [3000, 700], None, -1)
+@pytest.mark.parametrize("T,site", [(1, 0x521)] + [(300, s) for s in range(
+    0x531, 0x53e)])
+def test_a_stopped_attention_reports_and_recovers(T, site):
+    """The kernels' stopping paths, by the test hook (no fault, no hang)."""
+    c = attn_case(2, 8, 1, T, 128, 64, [30000, 700], None, -1)
     o, lse = gpu_attn(c)
     torch.cuda.synchronize()
-    fa.fa_debug_expire_at(0x521)
+    fa.fa_debug_expire_at(site)
     try:
         gpu_attn(c)
         assert fa.fa_check_device_status(DEV) == 4
-        assert fa.fa_last_failure_site() == 0x521
+        assert fa.fa_last_failure_site() == site
     finally:
         torch.cuda.synchronize()
         fa.fa_debug_expire_at(0)

@@ -104,8 +104,9 @@ def test_refusals(rec):
             lambda: fa.fa_qk_norm_rope_axes(qkv, 4, 2, rope, None, [0] * 16)):
         with pytest.raises(ValueError):
             bad()
-    with pytest.raises(TypeError):
-        fa.fa_qk_norm_rope_axes(qkv, 4, 2, rope, pos, None)
+    for axes in (None, 16):
+        with pytest.raises(TypeError):
+            fa.fa_qk_norm_rope_axes(qkv, 4, 2, rope, pos, axes)
     assert rec == []
 
 

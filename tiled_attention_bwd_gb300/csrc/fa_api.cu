@@ -329,6 +329,7 @@ void fa_debug_expire_at(uint32_t site) {
   (void)fa::set_expire_site_bwd(site);
   (void)fa::set_expire_site_cache4(site);
   (void)fa::set_expire_site_cache8(site);
+  (void)fa::set_expire_site_cache8_wide(site);
   g_hook_on.store(site != 0);
 }
 

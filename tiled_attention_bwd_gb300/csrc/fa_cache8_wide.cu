@@ -228,6 +228,20 @@ __device__ __forceinline__ bool has_nan(const uint8_t* grp, int lane) {
   return __any_sync(0xffffffffu, any != 0);
 }
 
+// A wait of a whole warp.  kHook: with the failure-path test hook, which stops
+// a warp at its site whether the barrier is complete or not (the first look at
+// one may sleep until it is).
+template <bool kHook>
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const WaitCtl& wc,
+                                          uint32_t where) {
+  if (kHook && c_expire_site == where) {
+    if ((threadIdx.x & 31) == 0) raise_abort(wc, where);
+    __syncwarp();
+    return false;
+  }
+  return __all_sync(0xffffffffu, wait_bar<true>(bar, parity, wc, where));
+}
+
 __device__ __forceinline__ c4::Call wide_call(const CacheAttnArgs& a) {
   c4::Call c = {a.B, a.Hkv, a.T, a.window, a.heads, kC8WideRows, a.row_blocks, a.M << a.shift, a.by_heads};
   c.least_rows = a.least_rows;
@@ -247,7 +261,7 @@ __device__ __forceinline__ const uint8_t* group_at(const CacheAttnArgs& a, int b
   return a.cache + ((((size_t)page * a.Hkv + hk) << gpp) + ((tok >> 4) & ((1 << gpp) - 1))) * bytes;
 }
 
-template <int D>
+template <int D, bool kHook>
 __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs a) {
   using L = Wide<D>;
   using Ctrl = typename L::Ctrl;
@@ -328,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
       uint32_t phase = 0;
       for (int s = 0; ok; ++s) {
         Seg& seg = c->seg[s % kSegs];
-        ok = wait_bar_warp<true>(&c->seg_empty[s % kSegs], ((s / kSegs) & 1) ^ 1, wc, kWLoadSeg);
+        ok = wait_warp<kHook>(&c->seg_empty[s % kSegs], ((s / kSegs) & 1) ^ 1, wc, kWLoadSeg);
         if (!ok) break;
         if (lane == 0) {  // (the cursor stays in shared memory: registers are scarce)
           if (s > 0 && !c->at.next(call, read)) {
@@ -361,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
           const int n = min(4, units - base);
 #pragma unroll 1
           for (int q = 0; q < n; ++q) {
-            ok = wait_bar_warp<true>(&c->raw_empty[stage], phase ^ 1, wc, kWLoadRaw);
+            ok = wait_warp<kHook>(&c->raw_empty[stage], phase ^ 1, wc, kWLoadRaw);
             if (!ok) break;
             const int mask = (have >> (q * kUnitGroups)) & 0xff;
             if (lane == 0) {
@@ -397,13 +411,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
       bool ok = true;
       auto next_tile = [&](int& st) {
         st = stage;
-        const bool r = wait_bar_warp<true>(&c->kv_full[stage], phase, wc, kWMmaTile);
+        const bool r = wait_warp<kHook>(&c->kv_full[stage], phase, wc, kWMmaTile);
         if (++stage == L::kStages) stage = 0, phase ^= 1;
         tc_fence_after();
         return r;
       };
       for (int s = 0; ok; ++s) {
-        ok = wait_bar_warp<true>(&c->seg_full[s % kSegs], (s / kSegs) & 1, wc, kWMmaSeg);
+        ok = wait_warp<kHook>(&c->seg_full[s % kSegs], (s / kSegs) & 1, wc, kWMmaSeg);
         if (!ok) break;
         const int units = __shfl_sync(0xffffffffu, c->seg[s % kSegs].units, 0);
         const int tiles = __shfl_sync(0xffffffffu, c->seg[s % kSegs].live > 128 ? 2 : 1, 0);
@@ -417,10 +431,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
 #pragma unroll 1
           for (int t = 0; t < tiles && ok; ++t) {
             if (j == 0) {
-              ok = wait_bar_warp<true>(&c->q_full[t], (q_par >> t) & 1, wc, kWMmaQ);
+              ok = wait_warp<kHook>(&c->q_full[t], (q_par >> t) & 1, wc, kWMmaQ);
               q_par ^= 1u << t;
             } else {
-              ok = wait_bar_warp<true>(&c->p_full[t], (p_par >> t) & 1, wc, kWMmaP);
+              ok = wait_warp<kHook>(&c->p_full[t], (p_par >> t) & 1, wc, kWMmaP);
               p_par ^= 1u << t;
               tc_fence_after();
               issue_pv<D>(who, kTmemO + t * D, kTmemS + t * 128, sdesc_adv(v_desc, vst * L::kTileBytes), j > 1);
@@ -451,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
     uint32_t phase = 0, raw_phase = 0;
     bool ok = work;
     auto tile_free = [&]() {
-      return wait_bar_warp<true>(&c->kv_empty[stage], phase ^ 1, wc, kWMakeTile);
+      return wait_warp<kHook>(&c->kv_empty[stage], phase ^ 1, wc, kWMakeTile);
     };
     auto tile_done = [&]() {
       fence_proxy_async_smem();
@@ -459,14 +473,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
       if (++stage == L::kStages) stage = 0, phase ^= 1;
     };
     for (int s = 0; ok; ++s) {
-      ok = wait_bar_warp<true>(&c->seg_full[s % kSegs], (s / kSegs) & 1, wc, kWMakeSeg);
+      ok = wait_warp<kHook>(&c->seg_full[s % kSegs], (s / kSegs) & 1, wc, kWMakeSeg);
       if (!ok) break;
       const int units = c->seg[s % kSegs].units, tok0 = c->seg[s % kSegs].tok0;
       const int lo = c->seg[s % kSegs].plain_lo, hi = c->seg[s % kSegs].plain_hi;
       warp_arrive(&c->seg_empty[s % kSegs]);
       if (units < 0) break;
       for (int j = 0; j < units; ++j, ++u) {
-        ok = wait_bar_warp<true>(&c->raw_full[raw], raw_phase, wc, kWMakeRaw) && tile_free();
+        ok = wait_warp<kHook>(&c->raw_full[raw], raw_phase, wc, kWMakeRaw) && tile_free();
         if (!ok) break;
         const int there = c->raw_there[raw], tok = tok0 + j * kC4Unit;
         const bool edge = there != 0xff || tok < lo || tok + kC4Unit > hi;
@@ -512,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
     int u_seg = 0;  // units of the segments before
     bool ok = work;
     for (int s = 0; ok; ++s) {
-      ok = wait_bar_warp<true>(&c->seg_full[s % kSegs], (s / kSegs) & 1, wc, kWSmSeg);
+      ok = wait_warp<kHook>(&c->seg_full[s % kSegs], (s / kSegs) & 1, wc, kWSmSeg);
       if (!ok) break;
       const Seg& seg = c->seg[s % kSegs];  // (kept until the segment's end)
       const int units = seg.units;
@@ -559,8 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
       bool had_nan = false;
       for (int j = 0; j < units; ++j) {
         const int u = u_seg + j;
-        ok = wait_bar_warp<true>(&c->info_full[u % kInfos], (u / kInfos) & 1, wc, kWSmInfo) &&
-             wait_bar_warp<true>(&c->s_full[t], s_cnt & 1, wc, kWSmS);
+        ok = wait_warp<kHook>(&c->info_full[u % kInfos], (u / kInfos) & 1, wc, kWSmInfo) &&
+             wait_warp<kHook>(&c->s_full[t], s_cnt & 1, wc, kWSmS);
         ++s_cnt;
         if (!ok) break;
         tc_fence_after();
@@ -667,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
       }
       if (!ok) break;
       u_seg += units;
-      ok = wait_bar_warp<true>(&c->o_done[t], o_cnt & 1, wc, kWSmO);
+      ok = wait_warp<kHook>(&c->o_done[t], o_cnt & 1, wc, kWSmO);
       ++o_cnt;
       if (!ok) break;
       tc_fence_after();
@@ -805,13 +819,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache8_wide_join_kernel(Cache
   }
 }
 
-template <int D>
+template <int D, bool kHook = false>
 cudaError_t run(const CacheAttnArgs& a, int sm_count, cudaStream_t stream) {
+  // The hook has its own instantiation, for d = 128.
+  if constexpr (D == 128 && !kHook) {
+    if (a.hook) return run<D, true>(a, sm_count, stream);
+  }
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(cache8_wide_kernel<D>), Wide<D>::kSmem, done);
+  auto* kernel = cache8_wide_kernel<D, kHook>;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Wide<D>::kSmem, done);
   if (e != cudaSuccess) return e;
   const int blocks = sm_count < kC8WideBlocks ? sm_count : kC8WideBlocks;
-  e = launch_overlapped(cache8_wide_kernel<D>, dim3(blocks), dim3(kThreads), Wide<D>::kSmem, stream, a);
+  e = launch_overlapped(kernel, dim3(blocks), dim3(kThreads), Wide<D>::kSmem, stream, a);
   if (e != cudaSuccess) return e;
   return launch_overlapped(cache8_wide_join_kernel<D>, dim3(blocks, kJoinBlocks), dim3(256), 0, stream, a);
 }
@@ -820,6 +839,10 @@ cudaError_t run(const CacheAttnArgs& a, int sm_count, cudaStream_t stream) {
 
 cudaError_t launch_cache8_wide(const CacheAttnArgs& a, int d, int sm_count, cudaStream_t stream) {
   return d == 128 ? run<128>(a, sm_count, stream) : run<64>(a, sm_count, stream);
+}
+
+cudaError_t set_expire_site_cache8_wide(uint32_t site) {
+  return cudaMemcpyToSymbol(c_expire_site, &site, sizeof(site));
 }
 
 }  // namespace fa

@@ -372,9 +372,11 @@ __device__ __forceinline__ void cache_attn(const CacheAttnArgs& a, Block<F, D, N
     turns = min(32, load.end - load.unit);
 #pragma unroll
     for (int u = 0; u < kGroups; ++u) {
-      const int tok = load.k.lo + (load.unit + lane) * kC4Unit + (warp * kGroups + u) * kGroup;
+      // (Unsigned: behind the last key it may pass 31 bits.)
+      const unsigned tok =
+          load.k.lo + (unsigned)(load.unit + lane) * kC4Unit + (warp * kGroups + u) * kGroup;
       src[u] = nullptr;
-      if (lane < turns && tok < load.k.hi) {
+      if (lane < turns && tok < (unsigned)load.k.hi) {
         const int page = a.block_table[(size_t)load.b * a.M + (tok >> a.shift)];
         const int gpp_shift = a.shift - 4;
         if (page >= 0 && page < a.pages)

@@ -155,6 +155,7 @@ cudaError_t launch_cache8_wide(const CacheAttnArgs& a, int d, int sm_count,
 // call only while no kernel of the library runs.
 cudaError_t set_expire_site_cache4(uint32_t site);
 cudaError_t set_expire_site_cache8(uint32_t site);
+cudaError_t set_expire_site_cache8_wide(uint32_t site);
 
 // Launches a kernel whose launch overlaps the end of the work before it in
 // the stream.  The kernel waits for that work on the device, by

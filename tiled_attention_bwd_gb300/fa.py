@@ -619,6 +619,15 @@ def fa_qk_norm_rope_bwd(qkv, H: int, Hkv: int, rope, dq, dk, dv,
     return dqkv, dqw, dkw
 
 
+def _axis_bytes(axes):
+    """The axis of each pair, one byte each."""
+    if isinstance(axes, bytes):
+        return axes
+    if isinstance(axes, int):              # (bytes() would make that many)
+        raise TypeError("axes must be a sequence of whole numbers")
+    return bytes(axes)
+
+
 def fa_qk_norm_rope_axes(qkv, H: int, Hkv: int, rope, positions, axes,
                          q_weight=None, k_weight=None, eps: float = 1e-6,
                          interleaved: bool = False, q=None, k=None, v=None):
@@ -629,8 +638,8 @@ def fa_qk_norm_rope_axes(qkv, H: int, Hkv: int, rope, positions, axes,
     the call nothing).  Pair i of a token turns by angle i of the rope's row
     positions[axes[i], b, n].  Returns (q, k, v)."""
     status, q, k, v = _native().qk_norm_rope(
-        qkv, H, Hkv, rope, positions, bytes(axes), q_weight, k_weight, eps,
-        bool(interleaved), q, k, v)
+        qkv, H, Hkv, rope, positions, _axis_bytes(axes), q_weight, k_weight,
+        eps, bool(interleaved), q, k, v)
     if status:
         raise FAError("fa_qk_norm_rope_axes", status)
     return q, k, v
@@ -644,7 +653,7 @@ def fa_qk_norm_rope_axes_bwd(qkv, H: int, Hkv: int, rope, dq, dk, dv,
     dq_weight, dk_weight fp32 [d]; None without weights).  dqkv may be
     qkv."""
     status, dqkv, dqw, dkw = _native().qk_norm_rope_bwd(
-        qkv, H, Hkv, rope, dq, dk, dv, positions, bytes(axes), q_weight,
+        qkv, H, Hkv, rope, dq, dk, dv, positions, _axis_bytes(axes), q_weight,
         k_weight, eps, bool(interleaved), dqkv, workspace)
     if status:
         raise FAError("fa_qk_norm_rope_axes_bwd", status)
@@ -727,7 +736,8 @@ def fa_cache8_read(cache, block_table, seq_lens, N: int, starts=None,
     """Tokens starts[b] .. starts[b] + N - 1 (starts: int32 [B], or None for
     0) of each request, as the 8-bit cache holds them.  block_table: int32
     [B, max_blocks]; seq_lens: int32 [B].  Rows past a request's tokens are
-    left as they were.  Returns (k, v), bf16 [B,Hkv,N,d]."""
+    left as they were (in new outputs: hold anything).  Returns (k, v), bf16
+    [B,Hkv,N,d]."""
     status, k, v = _native().cache8_read(cache, block_table, seq_lens, N,
                                          starts, k_out, v_out)
     if status:
