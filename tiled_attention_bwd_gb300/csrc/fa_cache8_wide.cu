@@ -170,30 +170,35 @@ __device__ __forceinline__ uint4* chunk_of(uint8_t* tile, int row, int dim) {
                                   ((((dim >> 3) & 7) ^ (row & 7)) << 4));
 }
 
-// One group's keys into rows row0 .. + 15 of a K tile.
+// One group's keys into 16 rows of a K tile, `tile` being where the first stands
+// (a multiple of eight rows: a lane's places are the same in each).
 template <int D>
-__device__ __forceinline__ void make_keys(uint8_t* tile, const uint8_t* grp, int row0, bool there,
-                                          int lane) {
+__device__ __forceinline__ void make_keys(uint8_t* tile, const uint8_t* grp, bool there, int lane) {
   const int g = lane >> 2, t = lane & 3;
+  // Odd rows write their halves in the other order: eight lanes then write
+  // eight different chunks.
+  const bool odd = g & 1;
+  uint8_t* const first = reinterpret_cast<uint8_t*>(chunk_of(tile, g, 8 * t + (odd ? 32 : 0)));
+  uint8_t* const second = reinterpret_cast<uint8_t*>(chunk_of(tile, g, 8 * t + (odd ? 0 : 32)));
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
       uint4 u = make_uint4(0, 0, 0, 0);
       if (there) u = *reinterpret_cast<const uint4*>(grp + k8_piece(D, h, c, lane));
-      // Odd rows write their halves in the other order: eight lanes then
-      // write eight different chunks.
-      const bool odd = g & 1;
-      const int at = 64 * c + 8 * t, row = row0 + 8 * h + g;
-      *chunk_of(tile, row, at + (odd ? 32 : 0)) = make8(odd ? u.z : u.x, odd ? u.w : u.y);
-      *chunk_of(tile, row, at + (odd ? 0 : 32)) = make8(odd ? u.x : u.z, odd ? u.y : u.w);
+      const int off = 8 * h * 128 + c * kSubTileBytes;
+      *reinterpret_cast<uint4*>(first + off) = make8(odd ? u.z : u.x, odd ? u.w : u.y);
+      *reinterpret_cast<uint4*>(second + off) = make8(odd ? u.x : u.z, odd ? u.y : u.w);
     }
 }
 // One group's values; in an edge unit NaN as zero.
 template <int D>
-__device__ __forceinline__ void make_values(uint8_t* tile, const uint8_t* grp, int row0, bool there,
+__device__ __forceinline__ void make_values(uint8_t* tile, const uint8_t* grp, bool there,
                                             bool edge, int lane) {
   const int g = lane >> 2, t = lane & 3;
+  uint8_t* to[2];  // of the lane's two tokens
+#pragma unroll
+  for (int e = 0; e < 2; ++e) to[e] = reinterpret_cast<uint8_t*>(chunk_of(tile, 2 * t + e, 8 * g));
   uint4 u[D / 64][2];
 #pragma unroll
   for (int j = 0; j < D / 64; ++j)
@@ -212,7 +217,7 @@ __device__ __forceinline__ void make_values(uint8_t* tile, const uint8_t* grp, i
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const uint32_t sel = e ? 0x7531 : 0x6420;  // one token's codes of a pair
-        *chunk_of(tile, row0 + 8 * h + 2 * t + e, 64 * j + 8 * g) =
+        *reinterpret_cast<uint4*>(to[e] + 8 * h * 128 + j * kSubTileBytes) =
             make8(__byte_perm(u[j][h].x, u[j][h].y, sel), __byte_perm(u[j][h].z, u[j][h].w, sel));
       }
 }
@@ -492,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
         for (int g = 2 * w; g < 2 * w + 2; ++g) {
           const uint8_t* grp = base + g * group8_bytes(D);
           const bool have = (there >> g) & 1;
-          make_keys<D>(tile, grp, g * kGroup, have, lane);
+          make_keys<D>(tile + g * kGroup * 128, grp, have, lane);
           const int nan = edge && have && has_nan<D>(grp, lane);
           if (lane == 0) {
             const uint32_t two = *reinterpret_cast<const uint16_t*>(grp + 32 * D);
@@ -509,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
         tile = smem + L::kRingOff + stage * L::kTileBytes;
 #pragma unroll 1
         for (int g = 2 * w; g < 2 * w + 2; ++g)
-          make_values<D>(tile, base + g * group8_bytes(D), g * kGroup, (there >> g) & 1, edge, lane);
+          make_values<D>(tile + g * kGroup * 128, base + g * group8_bytes(D), (there >> g) & 1, edge, lane);
         tile_done();
         warp_arrive(&c->raw_empty[raw]);
         if (++raw == L::kRawStages) raw = 0, raw_phase ^= 1;
