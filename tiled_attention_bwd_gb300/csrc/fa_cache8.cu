@@ -7,6 +7,13 @@
 // taken; in a group that holds earlier tokens, the larger of that and the
 // present one, and the earlier codes are rounded to the grown scale.  Division
 // by 2^e is exact, so every code is that of the exact quotient.
+//
+// Both directions are bound by memory: rows of bf16 and pieces of a group go
+// straight between registers and memory, 16 bytes a lane and whole sectors a
+// warp, in the order of the lanes that the attention reads them in.  Measured
+// (d = 128, 8 heads): append of 8 x 4000 tokens with the values that are held
+// 39.9 us, 6.2 TB/s; read of 12 x 6000 tokens 53.5 us, 6.5 TB/s; one token of 128
+// requests 3.2 us, most of it the host's call.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -218,7 +225,8 @@ __device__ __forceinline__ void append_values(const Append8Args& a, const Places
 }
 
 // A warp takes 16 neighbouring tokens of one batch entry and head, their keys
-// or their values, and, one after the other, the groups whose first token (in
+// or their values (both: 51 us at 8 x 4000 tokens, at half the occupancy, so 43;
+// with maxima by packed comparisons 40), and, one after the other, the groups whose first token (in
 // the call's order) is among them, with all their tokens up to 15 places on: a
 // group is written by one warp, which knows all that the call brings to it.
 template <int D>

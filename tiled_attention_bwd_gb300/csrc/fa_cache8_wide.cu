@@ -20,6 +20,17 @@
 // s + e_v, and P = 2^(s + e_v - m + 8) in f16: as in fa_cache8_attn.cu, whose
 // accuracy this kernel shares.
 //
+// What bounds it is the softmax: about 1000 instructions a unit and scheduler,
+// next to 300 that make the tiles, and its chain S -> P -> P V -> next S, with
+// two tiles in turn.  2 x 512 tokens (the second with 256) over 5000 and 16384,
+// 64 heads over 8, d = 128: 223 us a call, 1.19 PFLOP/s; issue slots 46% and
+// tensor pipe 45% busy; 2048 tokens over 32768: 1.22 PFLOP/s.  The roles share an
+// instruction cache that their loops fill: the making warps' loops are not
+// unrolled (292 us otherwise, so 270), the masks are bits, the issuing warp runs
+// uniformly (below: 257, so 228).  One S for both tiles, with P apart so that
+// Q K^T need not wait for P V, was slower (271): both softmaxes then run at once
+// and share the same issue slots.
+//
 // NaN.  A hidden key is masked by selection.  A hidden value would reach a row
 // as 0 * NaN: in units that some row does not see all of, NaN codes of V are
 // taken as zero, and rows that do see them note their dims (in the workspace;

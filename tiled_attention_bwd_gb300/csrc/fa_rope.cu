@@ -26,7 +26,10 @@
 // GB300 (copy bandwidth 6.79 TB/s), in a stream of calls: forward, 4 x 4096
 // tokens of 64 + 16 heads of 128, 107 us or 6.3 TB/s; backward, 4 x 1024
 // tokens of 32 + 64 heads, 48 us or 5.7 TB/s, and 7 x 3001 tokens of 24 + 16
-// heads of 64, half of each rotated, 54 us or 5.6 TB/s.
+// heads of 64, half of each rotated, 54 us or 5.6 TB/s.  With three axes in
+// sections: forward, 3 x 5001 tokens of 64 + 16 heads of 128, 100 us or 6.2 TB/s;
+// backward of 4 x 1024 48 us; with the axes in turn, 7 x 3001 tokens of 24 + 16
+// heads of 64, all of each rotated, 56 us or 5.5 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
