@@ -140,6 +140,23 @@ def test_binding_refusals():
                                 z((3, 1, 1), dtype=torch.int32), [256] * 32)
 
 
+def test_axes_of_any_sequence():
+    """Their elements count, not the memory or the size that they stand for."""
+    want = bytes([0, 2, 1, 0])
+    for axes in ([0, 2, 1, 0], (0, 2, 1, 0), bytearray(want), np.array([0, 2, 1, 0]),
+                 np.array([0, 2, 1, 0], dtype=np.int32), torch.tensor([0, 2, 1, 0]),
+                 (x for x in (0, 2, 1, 0))):
+        assert fa._axis_bytes(axes) == want
+    assert fa._axis_bytes(np.array([3])) == b"\3"
+    assert fa._axis_bytes(torch.tensor([3])) == b"\3"
+    for axes in (4, True, np.int64(4), np.array(4), torch.tensor(4), "0210", [0.0], None):
+        with pytest.raises(TypeError):
+            fa._axis_bytes(axes)
+    for axes in ([-1], [256]):
+        with pytest.raises(ValueError):
+            fa._axis_bytes(axes)
+
+
 # ------------------------------------------------------------------- on GPU
 CASES = [  # B, N, H, Hkv, d, rot, interleaved, weights, axes, strided
     (1, 1, 1, 1, 128, 128, False, "f32", sections(64, (16, 24, 24)), False),

@@ -621,11 +621,9 @@ def fa_qk_norm_rope_bwd(qkv, H: int, Hkv: int, rope, dq, dk, dv,
 
 def _axis_bytes(axes):
     """The axis of each pair, one byte each."""
-    if isinstance(axes, bytes):
-        return axes
-    if isinstance(axes, int):              # (bytes() would make that many)
-        raise TypeError("axes must be a sequence of whole numbers")
-    return bytes(axes)
+    # (By way of a list: bytes() makes a number of zeros of what has an index,
+    # and takes an array's memory for its elements.)
+    return axes if isinstance(axes, bytes) else bytes(list(axes))
 
 
 def fa_qk_norm_rope_axes(qkv, H: int, Hkv: int, rope, positions, axes,
