@@ -533,9 +533,9 @@ fa_status fa_cache8_read(const void* cache, const int* block_table,
  * arguments, masks, workspace rules and waits (where-code 0x521) as
  * fa_cache4_attn's, without scales; the workspace is
  * fa_cache8_attn_workspace_size(B, H, Hkv, T, d) bytes, and max_blocks *
- * page_size + T at most 2^31 - 257.  Calls of more than 64 rows T * H / Hkv (80
+ * page_size + T at most 2^31 - 257.  Calls of more than 48 rows T * H / Hkv (64
  * for d = 64) may run two kernels, one for the requests with few live rows;
- * waits of the other have the where-codes 0x531 to 0x53d.  A NaN that the cache
+ * waits of the other have the where-codes 0x531 to 0x53e.  A NaN that the cache
  * holds reaches the rows that see its token (of a value, in its dim) and no
  * others.
  * Scores and the softmax's maxima and sums are fp32.  The weights, each times
@@ -604,7 +604,8 @@ void fa_set_wait_timeout_ns(uint64_t ns);
  *             segment, 0x534 for codes, 0x535 for a free tile; 0x536 MMA warp
  *             waiting for a segment, 0x537 Q, 0x538 a tile, 0x539 P; 0x53a
  *             softmax waiting for a segment, 0x53b a unit's exponents, 0x53c S,
- *             0x53d the finished O.
+ *             0x53d the finished O, 0x53e the other tile's sums (calls of up to
+ *             128 rows).
  * While a site is set, forward and backward calls with d = 128 and no
  * window, lengths or FP8, and cache attention calls with d = 128 and at most
  * 8 query rows per key/value head or with many over the 8-bit cache, run

@@ -4,6 +4,8 @@ calls against the float64 oracle (tolerances: test_cache8.py)."""
 import ctypes
 import random
 import subprocess
+import tempfile
+from pathlib import Path
 
 import numpy as np
 import pytest
@@ -83,6 +85,121 @@ def test_mixed_calls_match_the_oracle(case):
     c = attn_case(*case)
     check_attn(c, *gpu_attn(c))
     assert fa.fa_check_device_status(DEV) == OK
+
+
+# Calls whose items' units two tiles of the same rows take in turn (up to 128
+# rows a request).
+TURNS = [
+    # One unit, two, three: the second tile has none, one, fewer than the first.
+    (4, 8, 1, 16, 128, 16, [16, 129, 300, 257], None, -1),
+    (4, 8, 1, 9, 64, 32, [9, 128, 256, 385], None, -1),
+    # Fewer rows than the items have; lengths of the new tokens around the limits.
+    (6, 7, 1, 7, 128, 64, [900, 12, 640, 7, 0, 77], [7, 6, 2, 7, 5, 1], -1),
+    (5, 24, 2, 9, 64, 16, [500, 90, 9, 30, 1000], [9, 5, 8, 3, 1], -1),
+    (3, 65, 1, 1, 128, 16, [130, 1, 0], None, -1),
+    (2, 128, 1, 1, 64, 256, [1500, 255], [1, 1], -1),
+    # More new tokens than cached ones; windows that end before a unit, within
+    # one and within the item's own tokens.
+    (3, 16, 2, 15, 128, 16, [7, 15, 3], [15, 15, 15], -1),
+    (2, 8, 1, 16, 128, 32, [700, 300], None, 0),
+    (2, 8, 1, 16, 128, 32, [700, 300], [16, 13], 3),
+    (2, 12, 1, 10, 64, 16, [900, 140], None, 127),
+    (3, 16, 2, 8, 128, 64, [600, 513, 8], None, 200),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", TURNS)
+def test_units_taken_in_turn_match_the_oracle(case):
+    c = attn_case(*case)
+    check_attn(c, *gpu_attn(c))
+    assert fa.fa_check_device_status(DEV) == OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,Hkv,lens", [(128, 1, [40000]), (64, 2, [30000, 5]),
+                                        (128, 3, [9000, 129, 12000])])
+def test_turns_over_many_blocks(d, Hkv, lens):
+    """A block begins and ends inside an item: odd and even shares, and joins of
+    few and of many parts; the same twice, and each row as the oracle's."""
+    T = 14
+    c = attn_case(len(lens), 8 * Hkv, Hkv, T, d, 256, lens, None, -1)
+    c["q"] = c["q"] * 0.25
+    o, lse = gpu_attn(c)
+    o2, lse2 = gpu_attn(c)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    for t in (0, T - 1):
+        one = dict(c, q=c["q"][:, :, t:t + 1].contiguous(), lens=c["lens"] - (T - 1 - t))
+        check_attn(one, o[:, :, t:t + 1], lse[:, :, t:t + 1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tok", [0, 127, 128, 300, 511, 519, 525])
+def test_nan_values_of_either_tile(d, tok):
+    """A NaN value reaches the rows that see its token, whichever tile took its
+    unit, and no others."""
+    c = attn_case(1, 8, 1, 14, d, 16, [526], None, 300)
+    page = int(c["table"][0, tok // 16])
+    dim = 70 % d
+    at = (page, 0, 0, v_at(d, tok % 16, dim))
+    c["cache"][at] = 0
+    want = gpu_attn(c)
+    check_attn(c, *want)
+    c["cache"][at] = 0x7f
+    o, lse = gpu_attn(c)
+    pos = 526 - 14 + np.arange(14)
+    seen = torch.from_numpy((tok <= pos) & (tok >= pos - 300)).to(DEV)
+    assert torch.equal(lse, want[1])
+    assert (torch.isnan(o[0, :, :, dim]) == seen).all()
+    want[0][0, :, :, dim].masked_fill_(seen, 0)
+    o[0, :, :, dim].masked_fill_(seen, 0)
+    assert torch.equal(o, want[0])
+
+
+def v_at(d, tok, dim):
+    """Byte of a value in its group, from the documented axes."""
+    return 16 * d + ((((dim // 64 * 2 + tok // 8) * 8 + dim % 64 // 8) * 4 + tok % 8 // 2) * 8
+                     + dim % 8) * 2 + tok % 2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("site", range(0x531, 0x53f))
+def test_a_stop_between_turns_reports_and_recovers(site):
+    """By the test hook (no fault, no hang), at every wait."""
+    c = attn_case(2, 8, 1, 12, 128, 64, [30000, 700], None, -1)
+    o, lse = gpu_attn(c)
+    torch.cuda.synchronize()
+    fa.fa_debug_expire_at(site)
+    try:
+        gpu_attn(c)
+        assert fa.fa_check_device_status(DEV) == 4
+        assert fa.fa_last_failure_site() == site
+    finally:
+        torch.cuda.synchronize()
+        fa.fa_debug_expire_at(0)
+    o2, lse2 = gpu_attn(c)
+    assert fa.fa_check_device_status(DEV) == OK
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_few_rows_are_fewer_than_the_calls():
+    """The first kernel leaves the second every request with all of a call's rows:
+    a call without lengths runs the second alone."""
+    src = (Path(fa_build.CSRC) / "fa_cache8_attn.cu").read_text()
+    rows_of = src[src.index("int cache8_attn_rows("):src.index("// Measured against")]
+    few = src[src.index("int cache8_narrow_rows("):src.index("cudaError_t launch_cache8_attn(")]
+    wide = (Path(fa_build.CSRC) / "fa_cache8_wide.cu").read_text()
+    at = wide.index("int cache8_wide_rows(int rows) {")
+    code = (rows_of + wide[at:wide.index("\n", at)] + "\n" + few
+            + 'int main() { for (int d = 64; d <= 128; d += 64)\n'
+            '  for (int heads = 1; heads <= 300; ++heads) for (int T = 1; T <= 400; ++T)\n'
+            '    if (heads * T > cache8_narrow_rows(d) && cache8_few_rows(heads * T, heads, d) >= heads * T)\n'
+            '      return 1;\n  return 0; }\n')
+    with tempfile.TemporaryDirectory() as tmp:
+        (Path(tmp) / "few.cpp").write_text(code)
+        subprocess.run(["g++", "-O1", "-std=c++17", "few.cpp", "-o", "few"], cwd=tmp, check=True)
+        assert subprocess.run([str(Path(tmp) / "few")]).returncode == 0
 
 
 @pytest.mark.gpu

@@ -187,11 +187,21 @@ int cache8_attn_rows(int rows, int d) {
   return best;
 }
 
-// Measured against the kernel for many rows (us, this one first; 16 requests of
-// 8192 tokens x 8 heads, 64 of 1000 x 2, 1 of 4096 x 8, 2 of 60000 x 1):
-//   d = 128, 64 rows: 130/129, 38/39, 23/28, 35/47; 128: 236/136, 56/43, 27/30, 44/49
-//   d = 64,  64 rows: 83/108, 28/34, 18/25, 27/36;  128: 150/111, 42/36, 20/25, 32/38
-int cache8_narrow_rows(int d) { return d == 128 ? 64 : 80; }
+// Measured against the kernel for many rows (us: this one / the other without
+// lengths of the new tokens / with them, where an empty launch of this one stands
+// before it; 16 requests of 4096 to 8192 tokens x 8 heads, 64 of 500 to 1000 x 2,
+// 2 of 30000 to 60000 x 1):
+//   d = 128, 48 rows: 82/74/81, 28/25/30, 30/34/40; 64: 108/75/83, 35/27/32, 36/35/40
+//   d = 64,  64 rows: 69/65/71, 27/23/28, 28/25/30; 80: 82/66/73, 33/24/29, 32/25/30
+int cache8_narrow_rows(int d) { return d == 128 ? 48 : 64; }
+
+// A token that takes two passes over the keys this way costs 104 us to 127 in the
+// items of 256 rows of a call with many (64 heads over 8, d = 128); smaller items
+// cost less.
+int cache8_few_rows(int rows, int heads, int d) {
+  const int two = 2 * cache8_attn_rows(heads, d);
+  return cache8_wide_rows(rows) < 256 && two > cache8_narrow_rows(d) ? cache8_narrow_rows(d) : two;
+}
 
 cudaError_t launch_cache8_attn(const CacheAttnArgs& a, int d, int sm_count, cudaStream_t stream) {
   const int nt = a.item_rows / 8;

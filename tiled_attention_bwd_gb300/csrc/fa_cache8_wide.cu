@@ -13,23 +13,33 @@
 //   warp 12      deals out the segments and copies the groups of the next
 //                units into shared memory
 //   warp 13      issues S_t = Q_t K^T and O_t += P_t V, P_t f16 in TMEM
-// While one tile's softmax runs, the tensor core works for the other.
+// While one tile's softmax runs, the tensor core works for the other.  In calls
+// of up to 128 rows a request both tiles are of the same rows and take the units
+// in turn, each with a maximum, sum and O of its own, which a segment's end joins
+// (16 requests of 4096 to 8192 tokens x 8 heads, 128 rows: 102 us with one tile
+// empty, so 84; 64 rows, which then went through the first kernel twice, 108 and
+// 75).
 //
 // Products.  Codes are f16 values, so K and V enter exactly.  A group's power
 // of two for K multiplies its 16 columns of S; the row's maximum is taken of
 // s + e_v, and P = 2^(s + e_v - m + 8) in f16: as in fa_cache8_attn.cu, whose
 // accuracy this kernel shares.
 //
-// What bounds it is the softmax: about 1000 instructions a unit and scheduler,
-// next to 300 that make the tiles, and its chain S -> P -> P V -> next S, with
-// two tiles in turn.  2 x 512 tokens (the second with 256) over 5000 and 16384,
-// 64 heads over 8, d = 128: 223 us a call, 1.19 PFLOP/s; issue slots 46% and
-// tensor pipe 45% busy; 2048 tokens over 32768: 1.22 PFLOP/s.  The roles share an
+// What bounds it is shared memory.  Per unit, at 128 bytes a cycle: the codes in
+// and out again 512 cycles, their f16 tiles in 512, the products' operands 1024
+// for Q K^T (a tile's Q and K take as long to read as to multiply; all of TMEM is
+// S and O) and 512 for P V: 2560 of the 3200 that a unit takes, while the tensor
+// pipe needs 2048.  2 x 512 tokens (the second with 256) over 5000 and 16384, 64
+// heads over 8, d = 128: 222 us a call, 1.19 PFLOP/s; issue slots 46% and tensor
+// pipe 45% busy; 2048 tokens over 32768: 1.22 PFLOP/s.  The roles share an
 // instruction cache that their loops fill: the making warps' loops are not
 // unrolled (292 us otherwise, so 270), the masks are bits, the issuing warp runs
 // uniformly (below: 257, so 228).  One S for both tiles, with P apart so that
 // Q K^T need not wait for P V, was slower (271): both softmaxes then run at once
-// and share the same issue slots.
+// and share the same issue slots.  With one row block to a unit the making warps
+// and the chain of a tile share the time (2900 cycles a unit); eight making warps,
+// with the softmax's columns in two parts for their registers, gained nothing (64
+// rows 106 us, 100 with four).
 //
 // NaN.  A hidden key is masked by selection.  A hidden value would reach a row
 // as 0 * NaN: in units that some row does not see all of, NaN codes of V are
@@ -39,6 +49,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "fa_cache4_work.h"
@@ -68,7 +79,7 @@ constexpr int kSegs = 4, kInfos = 4;
 constexpr uint32_t kWLoadSeg = 0x531, kWLoadRaw = 0x532, kWMakeSeg = 0x533, kWMakeRaw = 0x534,
                    kWMakeTile = 0x535, kWMmaSeg = 0x536, kWMmaQ = 0x537, kWMmaTile = 0x538,
                    kWMmaP = 0x539, kWSmSeg = 0x53a, kWSmInfo = 0x53b, kWSmS = 0x53c,
-                   kWSmO = 0x53d;
+                   kWSmO = 0x53d, kWSmMeet = 0x53e;
 
 // A segment: some units of an item.
 struct Seg {
@@ -85,19 +96,27 @@ struct alignas(16) Info {
   float2 key, value;
 };
 
-template <int D>
+// kAlternate: items of 128 rows; the two tiles are of the same rows and take the
+// units in turn.
+template <int D, bool kAlternate>
 struct Wide {
+  static constexpr int kRows = kAlternate ? 128 : 256;
+  static constexpr int kQTiles = kAlternate ? 1 : 2;
   static constexpr int kTileBytes = 128 * D * 2;
-  static constexpr int kStages = D == 128 ? 3 : 6;     // of the ring of K and V tiles
+  // Of the ring of K and V tiles.  (A unit's notes, of which kInfos are kept, are
+  // written behind the values of the unit before, whose place the values three or
+  // four units back, or the keys two back, had: the softmax is done with the unit
+  // kInfos back.)
+  static constexpr int kStages = D == 128 ? (kAlternate ? 4 : 3) : 6;
   static constexpr int kRawStages = D == 128 ? 2 : 4;  // units on their way
   static constexpr int kRawBytes = kUnitGroups * group8_bytes(D);
-  static constexpr int kRingOff = 2 * kTileBytes;  // (behind the Q tiles)
+  static constexpr int kRingOff = kQTiles * kTileBytes;  // (behind the Q tiles)
   static constexpr int kRawOff = kRingOff + kStages * kTileBytes;
   static constexpr int kCtrlOff = kRawOff + kRawStages * kRawBytes;
   struct Ctrl {
     uint64_t raw_full[kRawStages], raw_empty[kRawStages];
     uint64_t kv_full[kStages], kv_empty[kStages];
-    uint64_t q_full[2], s_full[2], p_full[2], o_done[2], mma_done;
+    uint64_t q_full[2], s_full[2], p_full[2], o_done[2], meet, mma_done;
     uint64_t seg_full[kSegs], seg_empty[kSegs], info_full[kInfos];
     Info info[kInfos][kUnitGroups];
     uint8_t nan[kInfos][kUnitGroups];  // 1: some value is NaN (in edge units)
@@ -111,7 +130,8 @@ struct Wide {
   };
   static constexpr int kSmem = kCtrlOff + (int)sizeof(Ctrl) + 1024;  // + alignment
 };
-static_assert(Wide<128>::kSmem <= 232448 && Wide<64>::kSmem <= 232448);
+static_assert(Wide<128, false>::kSmem <= 232448 && Wide<64, false>::kSmem <= 232448);
+static_assert(Wide<128, true>::kSmem <= 232448 && Wide<64, true>::kSmem <= 232448);
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
   return idesc_bf16(M, N, false, b_mn) & ~((1u << 7) | (1u << 10));  // A and B: f16
@@ -182,8 +202,9 @@ __device__ __forceinline__ uint4* chunk_of(uint8_t* tile, int row, int dim) {
 }
 
 // One group's keys into 16 rows of a K tile, `tile` being where the first stands
-// (a multiple of eight rows: a lane's places are the same in each).
-template <int D>
+// (a multiple of eight rows: a lane's places are the same in each).  kAhead: with
+// all loads before the first use.
+template <int D, bool kAhead>
 __device__ __forceinline__ void make_keys(uint8_t* tile, const uint8_t* grp, bool there, int lane) {
   const int g = lane >> 2, t = lane & 3;
   // Odd rows write their halves in the other order: eight lanes then write
@@ -191,12 +212,20 @@ __device__ __forceinline__ void make_keys(uint8_t* tile, const uint8_t* grp, boo
   const bool odd = g & 1;
   uint8_t* const first = reinterpret_cast<uint8_t*>(chunk_of(tile, g, 8 * t + (odd ? 32 : 0)));
   uint8_t* const second = reinterpret_cast<uint8_t*>(chunk_of(tile, g, 8 * t + (odd ? 0 : 32)));
+  uint4 ahead[2][D / 64];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      if (kAhead)
+        ahead[h][c] = there ? *reinterpret_cast<const uint4*>(grp + k8_piece(D, h, c, lane)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
       uint4 u = make_uint4(0, 0, 0, 0);
-      if (there) u = *reinterpret_cast<const uint4*>(grp + k8_piece(D, h, c, lane));
+      if (kAhead) u = ahead[h][c];
+      else if (there) u = *reinterpret_cast<const uint4*>(grp + k8_piece(D, h, c, lane));
       const int off = 8 * h * 128 + c * kSubTileBytes;
       *reinterpret_cast<uint4*>(first + off) = make8(odd ? u.z : u.x, odd ? u.w : u.y);
       *reinterpret_cast<uint4*>(second + off) = make8(odd ? u.x : u.z, odd ? u.y : u.w);
@@ -258,8 +287,9 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const 
   return __all_sync(0xffffffffu, wait_bar<true>(bar, parity, wc, where));
 }
 
+template <int kRows>
 __device__ __forceinline__ c4::Call wide_call(const CacheAttnArgs& a) {
-  c4::Call c = {a.B, a.Hkv, a.T, a.window, a.heads, kC8WideRows, a.row_blocks, a.M << a.shift, a.by_heads};
+  c4::Call c = {a.B, a.Hkv, a.T, a.window, a.heads, kRows, a.row_blocks, a.M << a.shift, a.by_heads};
   c.least_rows = a.least_rows;
   c.most_rows = a.most_rows;
   c.item_cost = kItemCost;
@@ -277,9 +307,20 @@ __device__ __forceinline__ const uint8_t* group_at(const CacheAttnArgs& a, int b
   return a.cache + ((((size_t)page * a.Hkv + hk) << gpp) + ((tok >> 4) & ((1 << gpp) - 1))) * bytes;
 }
 
-template <int D, bool kHook>
+// Four words of a thread's row, at a column of TMEM.
+__device__ __forceinline__ void tmem_st4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a),
+               "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld4(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+
+template <int D, bool kAlternate, bool kHook>
 __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs a) {
-  using L = Wide<D>;
+  using L = Wide<D, kAlternate>;
   using Ctrl = typename L::Ctrl;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -289,10 +330,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
     for (int i = 0; i < L::kRawStages; ++i) mbar_init(&c->raw_full[i], 1), mbar_init(&c->raw_empty[i], 4);
     for (int i = 0; i < L::kStages; ++i) mbar_init(&c->kv_full[i], 4), mbar_init(&c->kv_empty[i], 1);
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&c->q_full[t], 4), mbar_init(&c->s_full[t], 1);
+      mbar_init(&c->q_full[t], kAlternate ? 8 : 4), mbar_init(&c->s_full[t], 1);
       mbar_init(&c->p_full[t], 4), mbar_init(&c->o_done[t], 1);
     }
-    mbar_init(&c->mma_done, 1);
+    mbar_init(&c->meet, 8), mbar_init(&c->mma_done, 1);
     // A segment is let go of by the making warps, the MMA thread and the
     // softmax warps.
     for (int i = 0; i < kSegs; ++i) mbar_init(&c->seg_full[i], 1), mbar_init(&c->seg_empty[i], 4 + 1 + 8);
@@ -308,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- this block's share of the units
-  const c4::Call call = wide_call(a);
+  const c4::Call call = wide_call<L::kRows>(a);
   auto read = [&](int b) {
     return c4::request_of(call, a.seq_lens[b], a.q_lens ? a.q_lens[b] : a.T);
   };
@@ -365,8 +406,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
             seg.units = -1;
           } else {
             const c4::Cursor& at = c->at;
-            seg.b = at.b, seg.hk = at.hk, seg.row0 = at.rb * kC8WideRows;
-            seg.live = min(kC8WideRows, at.r.ql * a.heads - seg.row0);
+            seg.b = at.b, seg.hk = at.hk, seg.row0 = at.rb * L::kRows;
+            seg.live = min(L::kRows, at.r.ql * a.heads - seg.row0);
             seg.pos0 = at.r.len - at.r.ql;
             seg.tok0 = at.k.lo + at.unit * kC4Unit;
             seg.units = at.end - at.unit;
@@ -422,9 +463,17 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
       const uint64_t k_desc = sdesc_sw128(smem_addr(smem + L::kRingOff), 16, 1024);
       const uint64_t v_desc = sdesc_sw128(smem_addr(smem + L::kRingOff), kSubTileBytes, 1024);
       const uint32_t who = elect_one();
-      int stage = 0;
+      int stage = 0, u_seg = 0;  // u_seg: units of the segments before
       uint32_t phase = 0, q_par = 0, p_par = 0;  // bit t: of tile t
       bool ok = true;
+      // A unit's K (half 0) or V tile, in the ring's order.
+      auto tile_at = [&](int u, int half, int& st) {
+        const uint32_t at = 2u * u + half;
+        st = at % L::kStages;
+        const bool r = wait_warp<kHook>(&c->kv_full[st], (at / L::kStages) & 1, wc, kWMmaTile);
+        tc_fence_after();
+        return r;
+      };
       auto next_tile = [&](int& st) {
         st = stage;
         const bool r = wait_warp<kHook>(&c->kv_full[stage], phase, wc, kWMmaTile);
@@ -439,31 +488,63 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
         const int tiles = __shfl_sync(0xffffffffu, c->seg[s % kSegs].live > 128 ? 2 : 1, 0);
         warp_arrive(&c->seg_empty[s % kSegs]);
         if (units < 0) break;
-        // A tile's P V of unit j - 1, then its Q K^T of unit j, which overwrites
-        // that P.
-        for (int j = 0; j <= units && ok; ++j) {
-          int kst = 0, vst = 0;
-          if (j > 0) ok = next_tile(vst);
+        if constexpr (kAlternate) {
+          // Of unit j's tile: P V of its last unit, then Q K^T of unit j, which
+          // overwrites that P.
 #pragma unroll 1
-          for (int t = 0; t < tiles && ok; ++t) {
-            if (j == 0) {
-              ok = wait_warp<kHook>(&c->q_full[t], (q_par >> t) & 1, wc, kWMmaQ);
-              q_par ^= 1u << t;
-            } else {
-              ok = wait_warp<kHook>(&c->p_full[t], (p_par >> t) & 1, wc, kWMmaP);
+          for (int j = 0; j < units + 2 && ok; ++j) {
+            const int t = j & 1;
+            int st = 0;
+            if (j >= 2) {
+              ok = tile_at(u_seg + j - 2, 1, st) &&
+                   wait_warp<kHook>(&c->p_full[t], (p_par >> t) & 1, wc, kWMmaP);
+              if (!ok) break;
               p_par ^= 1u << t;
               tc_fence_after();
-              issue_pv<D>(who, kTmemO + t * D, kTmemS + t * 128, sdesc_adv(v_desc, vst * L::kTileBytes), j > 1);
-              if (t == tiles - 1) commit_if(who, &c->kv_empty[vst]);
-              if (j == units) commit_if(who, &c->o_done[t]);
+              issue_pv<D>(who, kTmemO + t * D, kTmemS + t * 128, sdesc_adv(v_desc, st * L::kTileBytes), j > 3);
+              commit_if(who, &c->kv_empty[st]);
             }
             if (j < units) {
-              if (t == 0) ok = ok && next_tile(kst);
-              tc_fence_after();
-              issue_qk<D>(who, kTmemS + t * 128, sdesc_adv(q_desc, t * L::kTileBytes),
-                          sdesc_adv(k_desc, kst * L::kTileBytes));
+              if (j == 0) {
+                ok = wait_warp<kHook>(&c->q_full[0], q_par & 1, wc, kWMmaQ);
+                q_par ^= 1u;
+              }
+              ok = ok && tile_at(u_seg + j, 0, st);
+              if (!ok) break;
+              issue_qk<D>(who, kTmemS + t * 128, q_desc, sdesc_adv(k_desc, st * L::kTileBytes));
               commit_if(who, &c->s_full[t]);
-              if (t == tiles - 1) commit_if(who, &c->kv_empty[kst]);
+              commit_if(who, &c->kv_empty[st]);
+            }
+          }
+          if (ok) commit_if(who, &c->o_done[0]);
+          u_seg += units;
+        } else {
+          // A tile's P V of unit j - 1, then its Q K^T of unit j, which overwrites
+          // that P.
+          for (int j = 0; j <= units && ok; ++j) {
+            int kst = 0, vst = 0;
+            if (j > 0) ok = next_tile(vst);
+#pragma unroll 1
+            for (int t = 0; t < tiles && ok; ++t) {
+              if (j == 0) {
+                ok = wait_warp<kHook>(&c->q_full[t], (q_par >> t) & 1, wc, kWMmaQ);
+                q_par ^= 1u << t;
+              } else {
+                ok = wait_warp<kHook>(&c->p_full[t], (p_par >> t) & 1, wc, kWMmaP);
+                p_par ^= 1u << t;
+                tc_fence_after();
+                issue_pv<D>(who, kTmemO + t * D, kTmemS + t * 128, sdesc_adv(v_desc, vst * L::kTileBytes), j > 1);
+                if (t == tiles - 1) commit_if(who, &c->kv_empty[vst]);
+                if (j == units) commit_if(who, &c->o_done[t]);
+              }
+              if (j < units) {
+                if (t == 0) ok = ok && next_tile(kst);
+                tc_fence_after();
+                issue_qk<D>(who, kTmemS + t * 128, sdesc_adv(q_desc, t * L::kTileBytes),
+                            sdesc_adv(k_desc, kst * L::kTileBytes));
+                commit_if(who, &c->s_full[t]);
+                if (t == tiles - 1) commit_if(who, &c->kv_empty[kst]);
+              }
             }
           }
         }
@@ -502,20 +583,29 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
         const bool edge = there != 0xff || tok < lo || tok + kC4Unit > hi;
         const uint8_t* base = smem + L::kRawOff + raw * L::kRawBytes;
         uint8_t* tile = smem + L::kRingOff + stage * L::kTileBytes;
-        Info* info = c->info[u % kInfos];
+        auto note = [&](int g) {
+          const uint32_t two = *reinterpret_cast<const uint16_t*>(base + g * group8_bytes(D) + 32 * D);
+          const int ve = exp8(two >> 8);
+          c->info[u % kInfos][g] = {make_float2(pow2(exp8(two & 0xff)), (float)ve),
+                                    make_float2((float)ve, pow2(-ve))};
+          c->nan[u % kInfos][g] = 0;
+        };
+        // (Keys as fast as they can be made are a tenth faster where the units'
+        // tiles take turns, the making being what is waited for there, and 3%
+        // slower where it is not: 2048 tokens over 32768 1767 us, so 1715.)
+        if (kAlternate && lane < 2) note(2 * w + lane);
         // (Loops, not unrolled: the roles' code shares the instruction cache.)
 #pragma unroll 1
         for (int g = 2 * w; g < 2 * w + 2; ++g) {
-          const uint8_t* grp = base + g * group8_bytes(D);
-          const bool have = (there >> g) & 1;
-          make_keys<D>(tile + g * kGroup * 128, grp, have, lane);
-          const int nan = edge && have && has_nan<D>(grp, lane);
-          if (lane == 0) {
-            const uint32_t two = *reinterpret_cast<const uint16_t*>(grp + 32 * D);
-            const int ve = exp8(two >> 8);
-            info[g] = {make_float2(pow2(exp8(two & 0xff)), (float)ve), make_float2((float)ve, pow2(-ve))};
-            c->nan[u % kInfos][g] = nan;
-          }
+          make_keys<D, kAlternate>(tile + g * kGroup * 128, base + g * group8_bytes(D), (there >> g) & 1, lane);
+          if (!kAlternate && lane == 0) note(g);
+        }
+        if (__builtin_expect(edge, 0)) {
+          __syncwarp();
+#pragma unroll 1
+          for (int g = 2 * w; g < 2 * w + 2; ++g)
+            if (((there >> g) & 1) && has_nan<D>(base + g * group8_bytes(D), lane) && lane == 0)
+              c->nan[u % kInfos][g] = 1;
         }
         if (w == 0 && lane == 0) c->edge[u % kInfos] = edge ? 256 + there : 0;
         warp_arrive(&c->info_full[u % kInfos]);
@@ -537,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
     const int t = warp >> 2, quarter = warp & 3;
     const uint32_t tl = (uint32_t)(quarter * 32) << 16;
     const uint32_t tS = tl + kTmemS + t * 128, tO = tl + kTmemO + t * D;
-    const int in_tile = quarter * 32 + lane;
+    const int in_tile = quarter * 32 + lane, tile_row = (kAlternate ? 0 : t * 128) + in_tile;
     uint32_t s_cnt = 0, o_cnt = 0;
     int u_seg = 0;  // units of the segments before
     bool ok = work;
@@ -547,13 +637,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
       const Seg& seg = c->seg[s % kSegs];  // (kept until the segment's end)
       const int units = seg.units;
       if (units < 0) break;
-      if (seg.live <= t * 128) {
+      if (!kAlternate && seg.live <= t * 128) {
         u_seg += units;
         warp_arrive(&c->seg_empty[s % kSegs]);
         continue;
       }
-      const bool valid = t * 128 + in_tile < seg.live;
-      const int row = seg.row0 + (valid ? t * 128 + in_tile : 0);
+      const bool valid = tile_row < seg.live;
+      const int row = seg.row0 + (valid ? tile_row : 0);
       const int pos = seg.pos0 + (int)a.by_heads.div(row);
 
       // ---- the row of Q, scaled by a power of two: largest in [2^8, 2^9)
@@ -579,15 +669,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
           uint32_t f[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) f[x] = f16x2(bf16_lo(w[x]) * down, bf16_hi(w[x]) * down);
-          *chunk_of(smem + t * L::kTileBytes, in_tile, 8 * i) = make_uint4(f[0], f[1], f[2], f[3]);
+          uint8_t* tile = smem + (kAlternate ? 0 : t * L::kTileBytes);
+          if (!kAlternate || i / (D / 16) == t)  // (or half of the tile's)
+            *chunk_of(tile, in_tile, 8 * i) = make_uint4(f[0], f[1], f[2], f[3]);
         }
         fence_proxy_async_smem();
-        warp_arrive(&c->q_full[t]);
+        warp_arrive(&c->q_full[kAlternate ? 0 : t]);
       }
 
       float m = kNoMax, l = 0.f;
       bool had_nan = false;
-      for (int j = 0; j < units; ++j) {
+      const int j0 = kAlternate ? t : 0;
+      for (int j = j0; j < units; j += kAlternate ? 2 : 1) {
         const int u = u_seg + j;
         ok = wait_warp<kHook>(&c->info_full[u % kInfos], (u / kInfos) & 1, wc, kWSmInfo) &&
              wait_warp<kHook>(&c->s_full[t], s_cnt & 1, wc, kWSmS);
@@ -622,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
           // Dims of NaN values that the row sees, into the workspace.
           const uint8_t* nan = c->nan[u % kInfos];
           if (*reinterpret_cast<const unsigned long long*>(nan)) {
-            uint32_t* note = a.nan_rows + ((size_t)blockIdx.x * kC8WideRows + t * 128 + in_tile) * 4;
+            uint32_t* note = a.nan_rows + ((size_t)blockIdx.x * kC8WideThreads + t * 128 + in_tile) * 4;
 #pragma unroll 1
             for (int d0 = 0; d0 < D; d0 += 32) {
               uint32_t dims = had_nan ? note[d0 / 32] : 0;
@@ -679,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
         }
         tmem_st32(tS, x);
         tmem_st32(tS + 32, x + 32);
-        if (j > 0 && __any_sync(0xffffffffu, bump)) {
+        if (j > j0 && __any_sync(0xffffffffu, bump)) {
 #pragma unroll 1
           for (int ch = 0; ch < D / 32; ++ch) {
             uint32_t o[32];
@@ -697,29 +790,72 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
       }
       if (!ok) break;
       u_seg += units;
-      ok = wait_warp<kHook>(&c->o_done[t], o_cnt & 1, wc, kWSmO);
-      ++o_cnt;
+      ok = wait_warp<kHook>(&c->o_done[kAlternate ? 0 : t], o_cnt & 1, wc, kWSmO);
       if (!ok) break;
       tc_fence_after();
 
       // ---- the results
+      // A row's two sums, where its units went to both tiles: the tiles' threads
+      // tell each other theirs, and either brings half of the dims.  (In columns
+      // of S, whose next product waits for both.)
+      float f[2] = {1.f, 1.f};  // of the tiles' O
+      bool nan_at[2] = {had_nan, false};
+      if constexpr (kAlternate) {
+        tmem_st4(tS, __float_as_uint(m), __float_as_uint(l), had_nan, 0);
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(&c->meet);
+        ok = wait_warp<kHook>(&c->meet, o_cnt & 1, wc, kWSmMeet);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t other[4];
+        tmem_ld4(tl + kTmemS + (t ^ 1) * 128, other);
+        tmem_wait_ld();
+        asm volatile("" : "+r"(other[0]), "+r"(other[1]), "+r"(other[2]), "+r"(other[3]));
+        const float m2 = __uint_as_float(other[0]), top = fmaxf(m, m2);
+        const float mine = ex2(m - top), its = ex2(m2 - top);
+        l = mine * l + its * __uint_as_float(other[1]);
+        m = top;
+        f[t] = mine, f[t ^ 1] = its;
+        nan_at[t] = had_nan, nan_at[t ^ 1] = other[2] != 0;
+      }
+      ++o_cnt;
       const bool whole = seg.whole;
       const float mul = !whole ? 1.f : (l > 0.f || l != l ? 1.f / l : 0.f);
       const size_t out = row_at(a, seg.b, seg.hk, row);
-      const size_t part = (size_t)seg.part * kC8WideRows + t * 128 + in_tile;
-      const uint32_t* note = a.nan_rows + ((size_t)blockIdx.x * kC8WideRows + t * 128 + in_tile) * 4;
+      const size_t part = (size_t)seg.part * L::kRows + tile_row;
+      const uint32_t* note = a.nan_rows + ((size_t)blockIdx.x * kC8WideThreads + in_tile) * 4;
+      const int dim0 = kAlternate ? t * (D / 2) : 0;
 #pragma unroll 1
-      for (int ch = 0; ch < D / 32; ++ch) {
-        uint32_t o[32];
-        tmem_ld32(tO + ch * 32, o);
+      for (int ch = 0; ch < (kAlternate ? D / 64 : D / 32); ++ch) {
+        const int dim = dim0 + ch * 32;
+        uint32_t o[32], dims = 0;
+        tmem_ld32(tl + kTmemO + (kAlternate ? 0 : t * D) + dim, o);
         tmem_wait_ld();
         reg_fence32(o);
-        const uint32_t dims = had_nan ? note[ch] : 0;
+        if constexpr (kAlternate) {
+          uint32_t o1[32];
+          if (units > 1) {  // (else the second tile has nothing)
+            tmem_ld32(tl + kTmemO + D + dim, o1);
+            tmem_wait_ld();
+            reg_fence32(o1);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float v = __uint_as_float(o[e]) * f[0];
+            if (units > 1) v = fmaf(__uint_as_float(o1[e]), f[1], v);
+            o[e] = __float_as_uint(v);
+          }
+          for (int i = 0; i < 2; ++i)
+            if (nan_at[i]) dims |= note[i * 512 + dim / 32];
+        } else if (had_nan) {
+          dims = note[t * 512 + dim / 32];
+        }
 #pragma unroll
         for (int e = 0; e < 32; ++e)
           o[e] = (dims >> e) & 1 ? 0x7fffffffu : __float_as_uint(__uint_as_float(o[e]) * mul);
         if (valid && whole) {
-          uint4* dst = reinterpret_cast<uint4*>(a.o + out * D + ch * 32);
+          uint4* dst = reinterpret_cast<uint4*>(a.o + out * D + dim);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t pk[4];
@@ -729,13 +865,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
             dst[i] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
           }
         } else if (valid) {
-          float* dst = a.part + part * D + ch * 32;
+          float* dst = a.part + part * D + dim;
 #pragma unroll
           for (int i = 0; i < 4; ++i) st_global_v8(dst + 8 * i, o + 8 * i);
         }
         __syncwarp();
       }
-      if (valid) {
+      if (valid && (!kAlternate || t == 0)) {
         if (whole) a.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         else a.part_ml[part] = make_float2(m, l);
       }
@@ -756,16 +892,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
 // block order.  A warp takes kRows rows, D / 32 dims a lane, and has the loads
 // of kParts parts on their way at once.  (One row and four parts at a time: 22
 // us for 152 joins of 256 rows.)
-template <int D, int kRows, int kParts>
+template <int D, int kItem, int kRows, int kParts>
 __device__ __forceinline__ void join_rows(const CacheAttnArgs& a, const int4& j, int block, int in0) {
   constexpr int kDims = D / 32;
   using Vec = std::conditional_t<D == 128, float4, float2>;
   const int lane = threadIdx.x & 31, hk = j.y / a.row_blocks;
-  const int row0 = (j.y - hk * a.row_blocks) * kC8WideRows + in0;
+  const int row0 = (j.y - hk * a.row_blocks) * kItem + in0;
   const int live = min(a.q_lens ? a.q_lens[j.x] : a.T, a.T) * a.heads;
   const int parts = j.z - block + 2;
   auto at = [&](int k, int r) {
-    return (size_t)(k == 0 ? j.w : 2 * (block + k - 1)) * kC8WideRows + in0 + r;
+    return (size_t)(k == 0 ? j.w : 2 * (block + k - 1)) * kItem + in0 + r;
   };
   float acc[kRows][kDims], sum[kRows], mx[kRows];
 #pragma unroll
@@ -819,42 +955,50 @@ __device__ __forceinline__ void join_rows(const CacheAttnArgs& a, const int4& j,
   }
 }
 
-constexpr int kJoinWarps = 8, kJoinRows = 2;
-constexpr int kJoinBlocks = kC8WideRows / (kJoinWarps * kJoinRows);  // per block of the attention
-template <int D>
+constexpr int kJoinWarps = 8;
+constexpr int join_rows_each(int item) { return item > 128 ? 2 : 1; }
+template <int D, int kItem>
 __global__ void __launch_bounds__(kJoinWarps * 32) cache8_wide_join_kernel(CacheAttnArgs a) {
   wait_for_stream();
   const int4 j = a.joins[blockIdx.x];
   if (j.x < 0) return;
+  constexpr int kJoinRows = join_rows_each(kItem);
   const int in0 = (blockIdx.y * kJoinWarps + (threadIdx.x >> 5)) * kJoinRows;
   if (j.z - (int)blockIdx.x + 2 <= 4) {
-    join_rows<D, kJoinRows, 4>(a, j, blockIdx.x, in0);
+    join_rows<D, kItem, kJoinRows, 4>(a, j, blockIdx.x, in0);
   } else {  // a long history of few rows
 #pragma unroll 1
-    for (int r = 0; r < kJoinRows; ++r) join_rows<D, 1, 16>(a, j, blockIdx.x, in0 + r);
+    for (int r = 0; r < kJoinRows; ++r) join_rows<D, kItem, 1, 16>(a, j, blockIdx.x, in0 + r);
   }
 }
 
-template <int D, bool kHook = false>
+template <int D, bool kAlternate, bool kHook = false>
 cudaError_t run(const CacheAttnArgs& a, int sm_count, cudaStream_t stream) {
   // The hook has its own instantiation, for d = 128.
   if constexpr (D == 128 && !kHook) {
-    if (a.hook) return run<D, true>(a, sm_count, stream);
+    if (a.hook) return run<D, kAlternate, true>(a, sm_count, stream);
   }
+  using L = Wide<D, kAlternate>;
   static std::atomic<unsigned long long> done{0};
-  auto* kernel = cache8_wide_kernel<D, kHook>;
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Wide<D>::kSmem, done);
+  auto* kernel = cache8_wide_kernel<D, kAlternate, kHook>;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), L::kSmem, done);
   if (e != cudaSuccess) return e;
   const int blocks = sm_count < kC8WideBlocks ? sm_count : kC8WideBlocks;
-  e = launch_overlapped(kernel, dim3(blocks), dim3(kThreads), Wide<D>::kSmem, stream, a);
+  e = launch_overlapped(kernel, dim3(blocks), dim3(kThreads), L::kSmem, stream, a);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(cache8_wide_join_kernel<D>, dim3(blocks, kJoinBlocks), dim3(256), 0, stream, a);
+  const int rows = std::min(a.rows, L::kRows), of_a_block = kJoinWarps * join_rows_each(L::kRows);
+  return launch_overlapped(cache8_wide_join_kernel<D, L::kRows>, dim3(blocks, (rows - 1) / of_a_block + 1),
+                           dim3(32 * kJoinWarps), 0, stream, a);
 }
 
 }  // namespace
 
+int cache8_wide_rows(int rows) { return rows <= 128 ? 128 : 256; }
+
 cudaError_t launch_cache8_wide(const CacheAttnArgs& a, int d, int sm_count, cudaStream_t stream) {
-  return d == 128 ? run<128>(a, sm_count, stream) : run<64>(a, sm_count, stream);
+  if (a.item_rows == 128)
+    return d == 128 ? run<128, true>(a, sm_count, stream) : run<64, true>(a, sm_count, stream);
+  return d == 128 ? run<128, false>(a, sm_count, stream) : run<64, false>(a, sm_count, stream);
 }
 
 cudaError_t set_expire_site_cache8_wide(uint32_t site) {

@@ -109,6 +109,7 @@ cudaError_t launch_cache8_read(const Read8Args& a, int d, cudaStream_t stream);
 
 // Attention over a cache, in either format.
 constexpr int kC4MaxBlocks = 640;
+constexpr int kC8WideThreads = 256;  // of the wide kernel's softmax
 struct CacheAttnArgs {
   const __nv_bfloat16* q;   // [B, H, T, d]
   const uint8_t* cache;
@@ -121,7 +122,7 @@ struct CacheAttnArgs {
   int4* joins;              // [kC4MaxBlocks]
   float* part;              // [2 kC4MaxBlocks][item rows][d]
   float2* part_ml;          // [2 kC4MaxBlocks][item rows]
-  uint32_t* nan_rows;       // [kC8WideBlocks][kC8WideRows][4] (wide kernel)
+  uint32_t* nan_rows;       // [kC8WideBlocks][kC8WideThreads][4] (wide kernel)
   int B, Hkv, T, M, pages;
   int heads;                // H / Hkv, of one key/value head
   FastDiv by_heads;
@@ -144,10 +145,12 @@ cudaError_t launch_cache4_attn(const CacheAttnArgs& a, int d, int sm_count,
 int cache8_attn_rows(int rows, int d);
 cudaError_t launch_cache8_attn(const CacheAttnArgs& a, int d, int sm_count,
                                cudaStream_t stream);
-// The same for requests with many rows; calls of up to cache8_narrow_rows a
-// request are for the first kernel alone.
+// The same for requests with many rows.  Calls of up to cache8_narrow_rows a
+// request are for the first kernel alone; in others (of `rows` a request) it takes
+// those with up to cache8_few_rows, which is less than `rows`.
 int cache8_narrow_rows(int d);
-constexpr int kC8WideRows = 256;    // of an item
+int cache8_few_rows(int rows, int heads, int d);
+int cache8_wide_rows(int rows);  // of an item, for requests of `rows`
 constexpr int kC8WideBlocks = 160;
 cudaError_t launch_cache8_wide(const CacheAttnArgs& a, int d, int sm_count,
                                cudaStream_t stream);

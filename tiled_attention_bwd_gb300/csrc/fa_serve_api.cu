@@ -209,8 +209,8 @@ fa_status check_cache(int pages, int Hkv, int page, int d, int* shift) {
 }
 
 // A format's bytes of a group, and its attention's rows of an item and launch;
-// for calls of more than narrow_rows rows a request, a second kernel with items
-// of wide_rows.
+// for calls of more than narrow_rows rows a request, where the first kernel takes
+// requests of up to few_rows, the second kernel's.
 using AttnLaunch = cudaError_t (*)(const fa::CacheAttnArgs& a, int d, int sm_count,
                                    cudaStream_t stream);
 struct Format {
@@ -218,13 +218,15 @@ struct Format {
   int (*rows)(int rows, int d);
   AttnLaunch attn;
   int (*narrow_rows)(int d) = nullptr;
-  int wide_rows = 0, wide_blocks = 0;
+  int (*few_rows)(int rows, int heads, int d) = nullptr;
+  int (*wide_rows)(int rows) = nullptr;
+  int wide_blocks = 0;
   AttnLaunch wide = nullptr;
 };
 constexpr Format kCache4 = {fa::group_bytes, fa::cache4_attn_rows, fa::launch_cache4_attn};
 constexpr Format kCache8 = {fa::group8_bytes,       fa::cache8_attn_rows, fa::launch_cache8_attn,
-                            fa::cache8_narrow_rows, fa::kC8WideRows,      fa::kC8WideBlocks,
-                            fa::launch_cache8_wide};
+                            fa::cache8_narrow_rows, fa::cache8_few_rows,  fa::cache8_wide_rows,
+                            fa::kC8WideBlocks,      fa::launch_cache8_wide};
 
 long long cache_bytes(const Format& f, int pages, int Hkv, int page, int d) {
   return (long long)pages * Hkv * (page / fa::kGroup) * f.group(d);
@@ -355,28 +357,27 @@ uintptr_t lay_out(fa::CacheAttnArgs& a, uintptr_t ws, int blocks, int rows, int 
   a.part_ml = reinterpret_cast<float2*>(ws);
   ws += align_up((size_t)blocks * 2 * rows * sizeof(float2));
   a.nan_rows = reinterpret_cast<uint32_t*>(ws);
-  if (notes) ws += (size_t)blocks * rows * 4 * sizeof(uint32_t);
+  if (notes) ws += (size_t)blocks * fa::kC8WideThreads * 4 * sizeof(uint32_t);
   a.row_blocks = (int)((a.rows + (long long)rows - 1) / rows);
   return ws;
 }
 // The kernels of a call of requests with up to `rows` rows, with their places
 // in the workspace; returns its end.  In a call with many rows the first kernel
 // gets the requests with one token or two: its items are of one token's heads.
-// (64 heads over 8, d = 128: a token that takes two passes over the keys that
-// way costs 104 to the second kernel's 127.)
 uintptr_t lay_out(const Format& f, int rows, int heads, int d, uintptr_t ws,
                   fa::CacheAttnArgs& narrow, fa::CacheAttnArgs& wide, bool* is_wide) {
   *is_wide = f.wide && rows > f.narrow_rows(d);
   narrow.item_rows = f.rows(*is_wide ? heads : rows, d);
   narrow.least_rows = 0;
-  narrow.most_rows = *is_wide ? 2 * narrow.item_rows : INT_MAX;
+  narrow.most_rows = *is_wide ? f.few_rows(rows, heads, d) : INT_MAX;
   narrow.rows = *is_wide ? std::min(rows, narrow.most_rows) : rows;
   ws = lay_out(narrow, ws, fa::kC4MaxBlocks, narrow.item_rows, d, false);
   if (!*is_wide) return ws;
   wide.rows = rows;
   wide.least_rows = narrow.most_rows + 1;
   wide.most_rows = INT_MAX;
-  return lay_out(wide, ws, f.wide_blocks, f.wide_rows, d, true);
+  wide.item_rows = f.wide_rows(rows);
+  return lay_out(wide, ws, f.wide_blocks, wide.item_rows, d, true);
 }
 
 size_t attn_workspace_size(const Format& f, int B, int H, int Hkv, int T, int d) {
