@@ -25,21 +25,23 @@
 // s + e_v, and P = 2^(s + e_v - m + 8) in f16: as in fa_cache8_attn.cu, whose
 // accuracy this kernel shares.
 //
-// What bounds it is shared memory.  Per unit, at 128 bytes a cycle: the codes in
-// and out again 512 cycles, their f16 tiles in 512, the products' operands 1024
-// for Q K^T (a tile's Q and K take as long to read as to multiply; all of TMEM is
-// S and O) and 512 for P V: 2560 of the 3200 that a unit takes, while the tensor
-// pipe needs 2048.  2 x 512 tokens (the second with 256) over 5000 and 16384, 64
-// heads over 8, d = 128: 222 us a call, 1.19 PFLOP/s; issue slots 46% and tensor
-// pipe 45% busy; 2048 tokens over 32768: 1.22 PFLOP/s.  The roles share an
-// instruction cache that their loops fill: the making warps' loops are not
-// unrolled (292 us otherwise, so 270), the masks are bits, the issuing warp runs
-// uniformly (below: 257, so 228).  One S for both tiles, with P apart so that
-// Q K^T need not wait for P V, was slower (271): both softmaxes then run at once
-// and share the same issue slots.  With one row block to a unit the making warps
-// and the chain of a tile share the time (2900 cycles a unit); eight making warps,
-// with the softmax's columns in two parts for their registers, gained nothing (64
-// rows 106 us, 100 with four).
+// What bounds it is each tile's chain S -> P -> P V -> next S, with two tiles in
+// turn.  Of the 3500 cycles that a unit takes, a tile's softmax takes 1850 (the
+// maximum 500, the exponentials 930, the stores of P 310); the products are 2048
+// of the tensor pipe's (45 to 48% busy); the issuing warp waits for weights 15% of
+// the time and for tiles 10%.  Issue slots are 46% busy, shared memory's banks 31%.
+// 2 x 512 tokens (the second with 256) over 5000 and 16384, 64 heads over 8,
+// d = 128: 222 us a call, 1.19 PFLOP/s; 2048 tokens over 32768: 1.24 PFLOP/s.  A
+// launch begins cold: 20000 to 30000 cycles pass until the first unit's weights
+// are there, most of them instruction fetches.  The roles share an instruction
+// cache that their loops fill: the making warps' loops are not unrolled (292 us
+// otherwise, so 270), the masks are bits, the issuing warp runs uniformly (below:
+// 257, so 228).  One S for both tiles, with P apart so that Q K^T need not wait
+// for P V, was slower (271): both softmaxes then run at once and share the same
+// issue slots.  With one row block to a unit the making warps and the tiles' chains
+// share the time (2900 cycles a unit); eight making warps, with the softmax's
+// columns in two parts for their registers, gained nothing (64 rows 106 us, 100
+// with four).
 //
 // NaN.  A hidden key is masked by selection.  A hidden value would reach a row
 // as 0 * NaN: in units that some row does not see all of, NaN codes of V are
