@@ -146,3 +146,46 @@ def attention(q, cache, table, lens, q_lens, scale, window):
                 mag[b, h, t] = p @ np.abs(V[see]) / p.sum()
                 lse[b, h, t] = m + np.log(p.sum())
     return o, lse, mag
+
+
+def products(q, cache, table, lens, q_lens, scale, window):
+    """The same with what bounds its rounding, a matrix product per request and
+    head: o, lse and mag as attention()'s, top [B,H,T]: the largest
+    weight times its value's power of two, and few [B,H,T]: how many keys that
+    the row sees have less than 2^-22 of that."""
+    q = np.asarray(q, np.float64)
+    B, H, T, d = q.shape
+    pages, Hkv, per, _ = cache.shape
+    page = 16 * per
+    all_k, all_v = values(cache)
+    unit = 2.0 ** np.clip(cache[..., 32 * d + 1].astype(np.int8), -MOST, MOST).astype(np.float64)
+    unit = unit.repeat(16, -1)             # [pages, Hkv, page_size]
+    o, mag = np.full(q.shape, np.nan), np.zeros(q.shape)
+    lse, top, few = np.full((B, H, T), np.nan), np.zeros((B, H, T)), np.zeros((B, H, T))
+    for b in range(B):
+        L = min(max(int(lens[b]), 0), len(table[b]) * page)
+        n = T if q_lens is None else min(max(int(q_lens[b]), 0), T)
+        j = np.arange(L)
+        pg = np.asarray(table[b], int)[j // page] if L else j
+        ok = (pg >= 0) & (pg < pages)
+        at, pg = j[ok], pg[ok]
+        i = L - n + np.arange(n)[:, None]
+        see = at <= i
+        if window >= 0:
+            see &= at >= i - window
+        some = see.any(1)
+        for h in range(H):
+            hk = h // (H // Hkv)
+            K, V, u = (x[pg, hk, at % page] for x in (all_k, all_v, unit))
+            V = np.where(see.any(0)[:, None], V, 0)
+            s = np.where(see, q[b, h, :n] @ np.where(see.any(0)[:, None], K, 0).T * scale, -np.inf)
+            m = np.where(some, s.max(1, initial=-np.inf), 0)[:, None]
+            p = np.exp(s - m)
+            l = p.sum(1)
+            p /= np.where(some, l, 1)[:, None]
+            o[b, h, :n], mag[b, h, :n] = p @ V, p @ np.abs(V)
+            with np.errstate(divide="ignore"):
+                lse[b, h, :n] = m[:, 0] + np.log(l)
+            top[b, h, :n] = (p * u).max(1, initial=0)
+            few[b, h, :n] = (see & (p * u < top[b, h, :n, None] * 2.0 ** -22)).sum(1)
+    return o, lse, mag, top, few
