@@ -449,7 +449,9 @@ fa_status fa_cache4_append(const void* k, const void* v, void* cache,
  * to f16 for their product with the values, which is summed in fp32: within
  * 2^-11 of a weight, down to 2^-22 of its row's largest; weights below about
  * 2^-32 of it count in lse only.  Elements of q below 2^-25 of their row's
- * largest are off by up to 2^-33 of that.
+ * largest are off by up to 2^-33 of that.  Scores (scale q.k) may have up to 2^22
+ * in magnitude: beyond, where fp32 tells no differences of a half apart any more,
+ * a weight may leave f16's range and its row become infinite or NaN.
  * Rows t >= q_lens[b] cost no pass over the keys, and a chunk's tokens none
  * over keys far behind their positions: requests with one new token and with
  * a chunk of a prompt can share a call.
@@ -541,7 +543,9 @@ fa_status fa_cache8_read(const void* cache, const int* block_table,
  * Scores and the softmax's maxima and sums are fp32.  The weights, each times
  * its group's 2^e of the values, are rounded to f16 for their product with the
  * codes, which is summed in fp32: within 2^-11 of such a product, down to 2^-22
- * of its row's largest; products below about 2^-32 of it count in lse only.
+ * of its row's largest; products below about 2^-32 of it count in lse only, and
+ * those below 2^-134 nowhere (where exponents of a row's values are 100 and more
+ * apart, weights of some size may be among them).  Scores as in fa_cache4_attn.
  */
 size_t fa_cache8_attn_workspace_size(int B, int H, int Hkv, int T, int d);
 fa_status fa_cache8_attn(const void* q, const void* cache,
