@@ -103,6 +103,12 @@ FA_BOTH Keys keys_of(const Call& c, const Request& r, int row_block) {
   return k;
 }
 
+// First token of a group of unit `unit` of those from token `lo` on.  Unsigned: who
+// looks ahead comes up to 31 units behind the last key, and so past 31 bits.
+FA_BOTH unsigned group_token(int lo, int unit, int group) {
+  return (unsigned)lo + (unsigned)unit * kC4Unit + (unsigned)(group * kGroup);
+}
+
 // Equal shares: `units` of cost dealt to blocks 0 .. blocks-1 in order, the
 // first `more` blocks one more than the others' `least`.
 struct Shares {

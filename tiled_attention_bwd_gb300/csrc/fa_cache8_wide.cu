@@ -427,9 +427,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
         // Each lane looks up one group of the next four units.
         for (int base = 0; base < units && ok; base += 4) {
           const int u = base + lane / kUnitGroups;
-          const int tok = seg.tok0 + u * kC4Unit + lane % kUnitGroups * kGroup;
+          const unsigned tok = c4::group_token(seg.tok0, u, lane % kUnitGroups);
           const uint8_t* src = nullptr;
-          if (u < units && tok < seg.key_end) src = group_at(a, seg.b, seg.hk, tok, group8_bytes(D));
+          if (u < units && tok < (unsigned)seg.key_end) src = group_at(a, seg.b, seg.hk, tok, group8_bytes(D));
           const uint32_t have = __ballot_sync(0xffffffffu, src != nullptr);
           const int n = min(4, units - base);
 #pragma unroll 1

@@ -372,9 +372,7 @@ __device__ __forceinline__ void cache_attn(const CacheAttnArgs& a, Block<F, D, N
     turns = min(32, load.end - load.unit);
 #pragma unroll
     for (int u = 0; u < kGroups; ++u) {
-      // (Unsigned: behind the last key it may pass 31 bits.)
-      const unsigned tok =
-          load.k.lo + (unsigned)(load.unit + lane) * kC4Unit + (warp * kGroups + u) * kGroup;
+      const unsigned tok = c4::group_token(load.k.lo, load.unit + lane, warp * kGroups + u);
       src[u] = nullptr;
       if (lane < turns && tok < (unsigned)load.k.hi) {
         const int page = a.block_table[(size_t)load.b * a.M + (tok >> a.shift)];

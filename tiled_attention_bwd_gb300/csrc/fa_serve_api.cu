@@ -402,8 +402,8 @@ fa_status cache_attn(const Format& f, const void* q, const void* cache, const in
   if (!cache_scale(k_scale) || !cache_scale(v_scale)) return FA_ERR_INVALID_ARG;
   const float scale_log2 = scale * k_scale * 1.4426950408889634f;
   if (!std::isfinite(scale_log2)) return FA_ERR_INVALID_ARG;
-  // Positions, which begin at -T, less a window stay within an int (and those up
-  // to a unit behind the last, for the kernels that look there).
+  // Positions, which begin at -T, less a window stay within an int (and so does the
+  // end of the unit that the last key is in, for the kernels that compare with it).
   if (((long long)max_blocks << shift) + T > INT_MAX - (f.wide ? 256 : 0) ||
       (long long)B * H > INT_MAX ||
       (long long)B * H * T > INT_MAX || (long long)B * max_blocks > INT_MAX)
