@@ -621,9 +621,16 @@ def fa_qk_norm_rope_bwd(qkv, H: int, Hkv: int, rope, dq, dk, dv,
 
 def _axis_bytes(axes):
     """The axis of each pair, one byte each."""
+    if isinstance(axes, bytes):
+        return axes
+    # (Each element of a tensor on a GPU would wait for all its work, and end a
+    # capture.)
+    axes = [axes] if isinstance(axes, torch.Tensor) and axes.device.type != "cpu" else list(axes)
+    if any(isinstance(a, torch.Tensor) and a.device.type != "cpu" for a in axes):
+        raise ValueError("axes are read on the host: bytes, or a sequence in host memory")
     # (By way of a list: bytes() makes a number of zeros of what has an index,
     # and takes an array's memory for its elements.)
-    return axes if isinstance(axes, bytes) else bytes(list(axes))
+    return bytes(axes)
 
 
 def fa_qk_norm_rope_axes(qkv, H: int, Hkv: int, rope, positions, axes,
@@ -632,8 +639,8 @@ def fa_qk_norm_rope_axes(qkv, H: int, Hkv: int, rope, positions, axes,
     """fa_qk_norm_rope with positions of several axes (time, height, width).
 
     positions: int32 [A,B,N], A of 1 to 4; axes: the axis of each of the
-    rot/2 rotated pairs, as bytes or any sequence of whole numbers (bytes cost
-    the call nothing).  Pair i of a token turns by angle i of the rope's row
+    rot/2 rotated pairs, as bytes or any sequence of whole numbers in host
+    memory (bytes cost the call nothing).  Pair i of a token turns by angle i of the rope's row
     positions[axes[i], b, n].  Returns (q, k, v)."""
     status, q, k, v = _native().qk_norm_rope(
         qkv, H, Hkv, rope, positions, _axis_bytes(axes), q_weight, k_weight,
