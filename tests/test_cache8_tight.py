@@ -166,3 +166,29 @@ def test_long_histories_miss_nothing(H, Hkv, T, d, page, lens, q_lens, make):
         one = dict(c, q=c["q"][:, :, t:t + 1].contiguous(), lens=c["lens"] - n + t + 1,
                    q_lens=(n > t).astype(np.int32))
         check(one, o[:, :, t:t + 1], lse[:, :, t:t + 1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_last_pages_of_a_cache_past_32_bits(d):
+    """Each kernel on pages beyond 2^32 bytes: the bits that it has on a cache of
+    these pages alone."""
+    H, Hkv, page, lens = 16, 2, 64, [900, 333]
+    small = one_sign(attn_case(2, H, Hkv, 1, d, page, lens, None, -1))
+    n = small["cache"].shape[0]
+    pages = 2 ** 32 // small["cache"][0].size + n + 1
+    big = torch.zeros((pages, *small["cache"].shape[1:]), dtype=torch.uint8, device=DEV)
+    big[-n:] = torch.from_numpy(small["cache"]).to(DEV)
+    assert big[:-n].numel() > 2 ** 32
+    for T, q_lens in ((1, None), (4, None), (9, None), (40, None), (40, [40, 1])):
+        c = attn_case(2, H, Hkv, T, d, page, lens, q_lens, -1)
+        c.update(cache=small["cache"], table=small["table"])
+        want = gpu_attn(c)
+        check(c, *want)
+        table = np.where(c["table"] < 0, -1, c["table"] + pages - n).astype(np.int32)
+        dev = lambda x: torch.from_numpy(x).to(DEV)  # noqa: E731
+        out = torch.full_like(want[0], 7.0), torch.full_like(want[1], 7.0)
+        fa.fa_cache8_attn(c["q"].to(DEV), big, dev(table), dev(c["lens"]), c["scale"],
+                          None if q_lens is None else dev(c["q_lens"]), out=out[0], lse=out[1])
+        assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+    assert fa.fa_check_device_status(DEV) == OK
