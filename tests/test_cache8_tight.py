@@ -192,3 +192,46 @@ def test_the_last_pages_of_a_cache_past_32_bits(d):
                           None if q_lens is None else dev(c["q_lens"]), out=out[0], lse=out[1])
         assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
     assert fa.fa_check_device_status(DEV) == OK
+
+
+MANY_HEADS = [  # B, H, Hkv, T, d, page, lens, q_lens, window
+    # Items that end within a token; a token of several items.
+    (2, 300, 1, 1, 128, 16, [700, 33], None, -1), (2, 300, 1, 2, 64, 64, [300, 5], [2, 1], -1),
+    (3, 100, 2, 2, 128, 32, [260, 1, 90], None, 40), (1, 130, 1, 1, 64, 16, [400], None, -1),
+    (2, 520, 4, 3, 128, 128, [129, 400], [1, 3], -1), (2, 40, 1, 1, 128, 16, [300, 2], None, -1),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", MANY_HEADS)
+def test_many_heads_of_one_key_value_head(case):
+    c = one_sign(attn_case(*case))
+    check(c, *gpu_attn(c))
+    assert fa.fa_check_device_status(DEV) == OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("T,d", [(1, 128), (4, 64), (9, 128), (40, 64), (40, 128)])
+def test_a_query_that_is_no_number_spoils_its_row_only(T, d, value):
+    c = attn_case(2, 8, 1, T, d, 32, [700, 150], None, -1)
+    good = c["q"].clone()
+    c["q"][0, 3, T // 2, 5] = value
+    o, lse = gpu_attn(c)
+    assert torch.isnan(lse[0, 3, T // 2]) and torch.isnan(o[0, 3, T // 2]).all()
+    c["q"] = good
+    want = gpu_attn(c)
+    o[0, 3, T // 2], lse[0, 3, T // 2] = want[0][0, 3, T // 2], want[1][0, 3, T // 2]
+    check(c, o, lse)
+
+
+@pytest.mark.gpu
+def test_more_requests_than_threads():
+    """A thread sums up several requests; most have no work."""
+    B = 1500
+    rng = np.random.default_rng(4)
+    lens = np.where(rng.random(B) < 0.7, 0, rng.integers(1, 40, B)).tolist()
+    for T, q in ((1, None), (6, 1), (9, None), (33, 2)):
+        q_lens = None if q is None else [min(q, n) if i % 50 else min(T, n) for i, n in enumerate(lens)]
+        c = one_sign(attn_case(B, 8, 1, T, 64, 16, lens, q_lens, -1))
+        check(c, *gpu_attn(c))
