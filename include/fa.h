@@ -468,23 +468,25 @@ fa_status fa_cache4_attn(const void* q, const void* cache,
                          float v_scale, void* stream);
 
 /*
- * A paged key/value cache held in 8 bits, twice the 4-bit one's codes and most
- * of bf16's accuracy.  `cache` is pages * fa_cache8_page_bytes(Hkv, page_size,
- * d) bytes of device memory, 16-byte aligned, owned by the caller; pages, slots
- * and block tables are as above, and fa_cache4_plan keeps them for either
- * cache.
+ * A paged key/value cache held in 8 bits.  `cache` is pages *
+ * fa_cache8_page_bytes(Hkv, page_size, d) bytes of device memory, 16-byte
+ * aligned, owned by the caller; pages, slots and block tables are as above, and
+ * fa_cache4_plan keeps them for either cache.
  *
  * The 16 tokens of a group (page_size / 16 of them in a page) share an exponent
  * e for one head's keys and one for its values, within -60 .. 60:
  *   code = E4M3(x / 2^e), to nearest, ties to even, saturating at +-448;
- * the value held is code * 2^e, which bf16 represents exactly.  A call that
- * writes tokens of a group takes the smallest e with |x| <= 448 * 2^e for all
- * finite elements x of these tokens, or the group's present e if that is
+ * the value held is code * 2^e, which bf16 represents exactly.  Rounding is off
+ * by at most 2^-4 of x where |x| is 2^-6 * 2^e or more, and by 2^-10 * 2^e below.
+ * A call that writes tokens of a group takes the smallest e with |x| <= 448 * 2^e
+ * for all finite elements x of these tokens, or the group's present e if that is
  * larger.  Where e grows, the codes of the group's other tokens are rounded,
  * likewise, to the new one (those of 2^-6 * 2^e and more stay exact).  Writing
  * a group's first token begins it: e then comes from this call's tokens alone,
- * and tokens that the group held before are no longer there.  An infinity
- * saturates and a NaN reads as NaN; neither counts for e.
+ * and tokens that the group held before are no longer there.  Until then e never
+ * falls: tokens that are taken back (drafts that were refused) leave the exponent
+ * that they needed, and the others' codes as they were rounded to it.  An
+ * infinity saturates and a NaN reads as NaN; neither counts for e.
  *
  * Layout: [pages][Hkv][page_size / 16] groups of 16 tokens, 32 d + 16 bytes:
  *   K codes  [2][d/64][8][4][2][8]  axes: token / 8, dim / 64, token % 8,
