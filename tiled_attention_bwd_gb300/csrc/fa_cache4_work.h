@@ -1,5 +1,6 @@
-// fa_cache4_work.h -- how the cache attention's work is cut and dealt to
-// blocks.  Plain C++ for both sides, so that it can be gone through on the CPU.
+// fa_cache4_work.h -- how the attention's work over a cache of either format is
+// cut and dealt to blocks.  Plain C++ for both sides, so that it can be gone through
+// on the CPU.
 //
 // The query rows of one request and key/value head are its T tokens times the
 // G = H / Hkv heads that share it.  They are numbered by token first (row
@@ -8,9 +9,9 @@
 // of R rows with one key/value head is an item.  It needs the keys that its
 // live rows see and no others: those up to its last token's position and, with
 // a window, from its first token's window on.  They are cut into units; an
-// item counts as kC4ItemCost units more, for what it costs to begin and end
-// one.  All items' units, in the order request, row block, head, are dealt to
-// the blocks in equal consecutive shares.
+// item counts as some units more (Call::item_cost, by kernel), for what it costs
+// to begin and end one.  All items' units, in the order request, row block, head,
+// are dealt to the blocks in equal consecutive shares.
 #pragma once
 #include <cstdint>
 

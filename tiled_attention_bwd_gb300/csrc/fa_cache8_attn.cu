@@ -13,9 +13,10 @@
 // about 150 warp instructions, 64 of them conversions; the cache's layout gives
 // them whole registers in the fragments' order, without a permutation.
 // Measured (d = 128, 8 query heads to a key/value head): 64 requests of 100 to
-// 8192 tokens x 8 heads 88 us, 6.2 TB/s of codes; 3 requests of 100000 to 131072
-// tokens x 8 heads 107 us, 6.6 TB/s; issue slots 30% busy, DRAM 77 and 83% of
-// its nominal rate.  Rows of 32 and more cost as much as memory does.
+// 8192 tokens x 8 heads 89 us, 6.1 TB/s of codes; 3 requests of 100000 to 131072
+// tokens x 8 heads 109 us, 6.5 TB/s; issue slots 30% busy, DRAM 77 and 83% of
+// its nominal rate.  With more rows the warps' instructions and registers bound it:
+// 32 rows take 76 us where 8 take 51, over the same 40 us of bytes.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -28,7 +29,7 @@ namespace {
 
 struct Cache8 {
   static constexpr uint32_t kWhere = 0x521;
-  static constexpr int kItemCost = 1;  // (three: 111 us at 3 x 131072 tokens, one: 107)
+  static constexpr int kItemCost = 1;  // (three: 111.4 us at 3 x 131072 tokens, one: 108.8)
   static constexpr __host__ __device__ int group_bytes(int d) { return group8_bytes(d); }
   static constexpr __host__ __device__ int blocks_per_sm(int d, int nt) {
     return d == 64 && nt <= 2 ? 3 : 2;
@@ -195,9 +196,16 @@ int cache8_attn_rows(int rows, int d) {
 //   d = 64,  64 rows: 69/65/71, 27/23/28, 28/25/30; 80: 82/66/73, 33/24/29, 32/25/30
 int cache8_narrow_rows(int d) { return d == 128 ? 48 : 64; }
 
-// A token that takes two passes over the keys this way costs 104 us to 127 in the
-// items of 256 rows of a call with many (64 heads over 8, d = 128); smaller items
-// cost less.
+// In a call with many rows the first kernel's items are of one token's rows, and it
+// takes the requests of up to two such items, two passes over the keys.  Measured
+// beside one chunk of 512 (63 requests of 4096 tokens x 8 heads, d = 128; us, one
+// pass / two / the second kernel, whatever the rows up to 48): 8 query heads to a
+// key/value head 193 / 265 / 333, 4 heads 155 / 227 / 300, 1 head 130 / 203 / 280;
+// a pass is 73, so a third would gain nothing (d = 64, 8 heads: 128 / 166 / 268).
+// Larger items for them, with one pass for 24 or 32 rows, are not built.  In calls
+// of up to 128 rows the second kernel's items are of 128 rows and cost less: there
+// the limit is at most that of a call without many.  Where two items are less than a
+// token's heads the first kernel gets nothing.
 int cache8_few_rows(int rows, int heads, int d) {
   const int two = 2 * cache8_attn_rows(heads, d);
   return cache8_wide_rows(rows) < 256 && two > cache8_narrow_rows(d) ? cache8_narrow_rows(d) : two;

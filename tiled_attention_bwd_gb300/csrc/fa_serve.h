@@ -1,5 +1,5 @@
 // fa_serve.h -- internal interface between the host layer (fa_serve_api.cu)
-// and the kernels of the norm with rotation and of the 4-bit cache (fa_rope.cu,
+// and the kernels of the norm with rotation and of the caches (fa_rope.cu,
 // fa_cache4.cu, fa_cache4_attn.cu, fa_cache8*.cu).  Not part of the ABI.
 #pragma once
 #include <cuda_bf16.h>

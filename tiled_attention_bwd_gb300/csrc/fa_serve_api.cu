@@ -1,5 +1,6 @@
 // fa_serve_api.cu -- host side of the entry points around the attention
-// kernels: norm and rotation of queries and keys, and the paged 4-bit cache.
+// kernels: norm and rotation of queries and keys, and the paged caches in 4 and 8
+// bits.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -363,7 +364,8 @@ uintptr_t lay_out(fa::CacheAttnArgs& a, uintptr_t ws, int blocks, int rows, int 
 }
 // The kernels of a call of requests with up to `rows` rows, with their places
 // in the workspace; returns its end.  In a call with many rows the first kernel
-// gets the requests with one token or two: its items are of one token's heads.
+// gets the requests with few of them (by rows, whatever tokens these are): its items
+// are of one token's heads.
 uintptr_t lay_out(const Format& f, int rows, int heads, int d, uintptr_t ws,
                   fa::CacheAttnArgs& narrow, fa::CacheAttnArgs& wide, bool* is_wide) {
   *is_wide = f.wide && rows > f.narrow_rows(d);
