@@ -684,6 +684,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache8_wide_kernel(CacheAttnArgs 
       const int j0 = kAlternate ? t : 0;
       for (int j = j0; j < units; j += kAlternate ? 2 : 1) {
         const int u = u_seg + j;
+        // (Behind a segment that the second tile had no part in, its first wait may
+        // pass early, a barrier's phase being one bit.  The second may not, and S
+        // comes from a tile of keys that all making warps wrote behind their notes.)
         ok = wait_warp<kHook>(&c->info_full[u % kInfos], (u / kInfos) & 1, wc, kWSmInfo) &&
              wait_warp<kHook>(&c->s_full[t], s_cnt & 1, wc, kWSmS);
         ++s_cnt;
